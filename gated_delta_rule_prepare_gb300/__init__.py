@@ -10,6 +10,9 @@ Entry points (same names as the C ABI): ``kda_decode``, ``kda_decode_k``,
 ``kda_prefill``, ``kda_prefill_gated``, ``kda_prefill_o_norm``, ``kda_conv_silu_l2``,
 ``kda_conv_silu_l2_k``,
 ``kda_gate``, ``kda_o_norm_gated``, ``kda_prefill_workspace_size``, ``kda_sync_status``.
+Full attention: ``kda_attn_prefill`` over packed prompts, and the paged 4-bit cache's
+``kda_attn_kv4_append``, ``kda_attn_kv4_read`` and ``kda_attn_kv4_decode`` (``kv4_cache``
+allocates one).
 ``kda_prefill_static_ws`` is reached through ``LIB`` (its callers hold raw pointers).
 """
 
@@ -25,7 +28,9 @@ from . import build as _build
 HEAD_DIM = 128
 Q_SCALE = 0.08838834764831845
 MAX_K = 8
-F32, BF16 = 0, 1
+F32, BF16, F16 = 0, 1, 2
+KV4_TOKEN_BYTES = 144
+KV4_PAGES = (16, 32, 64, 128, 256)
 
 _c = ctypes
 _vp, _i, _u64, _i64, _f, _sz = _c.c_void_p, _c.c_int, _c.c_uint64, _c.c_int64, _c.c_float, _c.c_size_t
@@ -56,12 +61,25 @@ def _load():
         "kda_prefill_o_norm": [_vp] * 7 + [_i64, _vp, _f, _vp, _i64, _i, _i, _i, _i, _i, _i,
                                            _i64, _vp, _i, _vp, _sz, _u64],
     }
+    sig.update({
+        "kda_attn_prefill": [_vp] * 5 + [_i, _i, _vp, _vp] + [_i] * 5 + [_i64] * 4
+                            + [_i, _f, _vp, _sz, _u64],
+        "kda_attn_kv4_append": [_vp, _vp, _i64, _i64, _i, _vp, _i, _i, _i, _i, _vp, _i64, _i, _vp,
+                                _i, _vp, _u64],
+        "kda_attn_kv4_decode": [_vp, _vp, _i64, _i, _vp, _i, _vp, _vp, _vp] + [_i] * 7
+                               + [_f, _vp, _sz, _u64],
+    })
+    sig["kda_attn_kv4_read"] = sig["kda_attn_kv4_append"]
     for name, args in sig.items():
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = _i
     lib.kda_prefill_workspace_size.argtypes = [_i64, _i, _i, _i, _i, _i]
     lib.kda_prefill_workspace_size.restype = _sz
+    lib.kda_attn_prefill_workspace_size.argtypes = [_i64, _i, _i, _i]
+    lib.kda_attn_prefill_workspace_size.restype = _sz
+    lib.kda_attn_kv4_workspace_size.argtypes = [_i] * 4
+    lib.kda_attn_kv4_workspace_size.restype = _sz
     lib.kda_last_error.argtypes = []
     lib.kda_last_error.restype = _c.c_char_p
     lib.kda_version.argtypes = []
@@ -419,6 +437,217 @@ def kda_gate(g_raw, dt_bias, a_log, b_raw, g_out, beta_out, gate_lower_bound):
                         float(gate_lower_bound), _ptr(b_raw, b16, "b_raw"), int(b_raw.stride(0)),
                         _ptr(g_out), _ptr(beta_out), BF16 if g_out.dtype == b16 else F32,
                         int(rows), H, HEAD_DIM, _stream(g_out)))
+
+
+# ---------------------------------------------------------------- full attention
+
+_ATTN_TYPES = {torch.bfloat16: BF16, torch.float16: F16}
+
+
+def _rows(t, dtype, name):
+    """(pointer, token-row stride) of a [..., rows, heads, 128] tensor with its
+    heads packed; a leading sequence dimension must be consecutive row blocks."""
+    if not t.is_cuda or t.dtype != dtype:
+        raise TypeError("%s must be a CUDA %s tensor" % (name, dtype))
+    shape, stride = t.shape, t.stride()
+    if (len(shape) not in (3, 4) or shape[-1] != HEAD_DIM or stride[-1] != 1
+            or (stride[-2] != HEAD_DIM and shape[-2] > 1)):
+        raise ValueError("%s must be [rows, heads, 128] with unit channel stride and heads packed"
+                         % name)
+    packed = shape[-2] * HEAD_DIM
+    row = stride[-3] if shape[-3] > 1 else packed
+    if len(shape) == 4 and shape[0] > 1:
+        if shape[1] == 1:
+            row = stride[0]
+        elif stride[0] != shape[1] * row:
+            raise ValueError("%s: sequences must be consecutive row blocks" % name)
+    return t.data_ptr(), row
+
+
+def _int32(t, n, name):
+    if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous():
+        raise TypeError("%s must be a contiguous CUDA int32 tensor" % name)
+    if n is not None and t.numel() != n:
+        raise ValueError("%s must hold %d values" % (name, n))
+    return t.data_ptr()
+
+
+def _same_device(a, *others):
+    for t in others:
+        if t is not None and t.device != a.device:
+            raise ValueError("all tensors of one call must be on one device")
+
+
+def _scratch(workspace, need, device):
+    """(tensor, pointer, bytes) of the caller's workspace, or of one allocated
+    here (the library itself never allocates)."""
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("the workspace must be a contiguous tensor on the call's device")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def kda_attn_prefill_workspace(rows, n_seqs, heads, kv_heads, device="cuda"):
+    """Workspace for kda_attn_prefill over `rows` query rows in total."""
+    need = LIB.kda_attn_prefill_workspace_size(int(rows), n_seqs, heads, kv_heads)
+    return torch.empty(int(need), dtype=torch.uint8, device=device)
+
+
+def kda_attn_prefill(q, k, v, out, lse=None, cu_seqlens=None, cu_seqlens_k=None, window=0,
+                     scale=Q_SCALE, workspace=None):
+    """Causal attention with grouped heads.  BF16 or FP16 q, out
+    [rows, heads, 128] and k, v [key rows, kv_heads, 128], which may be strided
+    views of wider rows; lse FP32 [rows, heads] or None.  cu_seqlens and
+    cu_seqlens_k (device int32 [N+1]; the keys' default to the queries') give
+    packed sequences; without them, tensors of four dimensions
+    [N, T, heads, 128] hold N sequences and of three one.  A sequence's queries
+    are its last positions; window > 0 limits each to the last `window` keys."""
+    dt = q.dtype
+    if dt not in _ATTN_TYPES:
+        raise TypeError("kda_attn_prefill: inputs must be bfloat16 or float16")
+    q_ptr, q_row = _rows(q, dt, "q")
+    k_ptr, k_row = _rows(k, dt, "k")
+    v_ptr, v_row = _rows(v, dt, "v")
+    o_ptr, o_row = _rows(out, dt, "out")
+    heads, kv_heads = q.shape[-2], k.shape[-2]
+    if out.shape != q.shape or v.shape != k.shape or q.dim() != k.dim():
+        raise ValueError("kda_attn_prefill: out must have q's shape, v k's, and k q's dimensions")
+    _same_device(q, k, v, out, lse, cu_seqlens, cu_seqlens_k)
+    cu_q = cu_k = None
+    if cu_seqlens is not None:
+        if q.dim() != 3:
+            raise ValueError("kda_attn_prefill: packed rows have three dimensions")
+        n_seqs = cu_seqlens.numel() - 1
+        cu_q = _int32(cu_seqlens, None, "cu_seqlens")
+        cu_k = cu_q if cu_seqlens_k is None else _int32(cu_seqlens_k, n_seqs + 1, "cu_seqlens_k")
+        t_q, t_k = q.shape[0], k.shape[0]
+    elif cu_seqlens_k is not None:
+        raise ValueError("kda_attn_prefill: cu_seqlens_k needs cu_seqlens")
+    else:
+        n_seqs = q.shape[0] if q.dim() == 4 else 1
+        if q.dim() == 4 and k.shape[0] != n_seqs:
+            raise ValueError("kda_attn_prefill: q and k hold different numbers of sequences")
+        t_q, t_k = q.shape[-3], k.shape[-3]
+    lse_ptr = None
+    if lse is not None:
+        if lse.shape != q.shape[:-1]:
+            raise ValueError("kda_attn_prefill: lse must be [rows, heads]")
+        _contig(lse, "lse")
+        lse_ptr = _ptr(lse, torch.float32, "lse")
+    need = 0
+    if workspace is None:
+        rows = t_q if cu_seqlens is not None else t_q * n_seqs
+        need = LIB.kda_attn_prefill_workspace_size(rows, n_seqs, heads, kv_heads)
+    ws, ws_ptr, ws_bytes = _scratch(workspace, need, q.device)
+    _check(LIB.kda_attn_prefill(q_ptr, k_ptr, v_ptr, o_ptr, lse_ptr, t_q, t_k, cu_q, cu_k, n_seqs,
+                                heads, kv_heads, HEAD_DIM, _ATTN_TYPES[dt], q_row, k_row, v_row,
+                                o_row, window, scale, ws_ptr, ws_bytes, _stream(q)))
+
+
+def kv4_cache(n_pages, kv_heads, page=64, device="cuda"):
+    """A 4-bit cache of n_pages pages: uint8 [n_pages, kv_heads, page * 144]."""
+    if page not in KV4_PAGES:
+        raise ValueError("page must be one of %s" % (KV4_PAGES,))
+    return torch.zeros((n_pages, kv_heads, page * KV4_TOKEN_BYTES), dtype=torch.uint8,
+                       device=device)
+
+
+def _kv4(cache, page_table, lens):
+    """The cache arguments: (pointer, pages, tokens a page, table, width, lens)."""
+    if not cache.is_cuda or cache.dtype != torch.uint8 or cache.dim() != 3:
+        raise TypeError("the cache must be a CUDA uint8 [pages, kv_heads, page * 144] tensor")
+    _contig(cache, "cache")
+    page, rest = divmod(cache.shape[2], KV4_TOKEN_BYTES)
+    if rest or page not in KV4_PAGES:
+        raise ValueError("the cache's last dimension must be page * 144, page one of %s"
+                         % (KV4_PAGES,))
+    if page_table.dim() != 2 or page_table.shape[0] != lens.numel():
+        raise ValueError("page_table must be [sequences, pages], lens [sequences]")
+    _same_device(cache, page_table, lens)
+    return (cache.data_ptr(), cache.shape[0], page, _int32(page_table, None, "page_table"),
+            page_table.shape[1], _int32(lens, None, "lens"))
+
+
+def _kv4_rows(name, fn, k, v, cache, page_table, lens, cu_seqlens):
+    dt = k.dtype
+    if dt not in _ATTN_TYPES:
+        raise TypeError("%s: rows must be bfloat16 or float16" % name)
+    k_ptr, k_row = _rows(k, dt, "k")
+    v_ptr, v_row = _rows(v, dt, "v")
+    c_ptr, n_pages, page, table, width, lens_ptr = _kv4(cache, page_table, lens)
+    n_seqs, kv_heads = lens.numel(), cache.shape[1]
+    if v.shape != k.shape or k.shape[-2] != kv_heads:
+        raise ValueError("%s: k and v must be [rows, kv_heads, 128] of the cache's kv_heads" % name)
+    _same_device(cache, k, v, cu_seqlens)
+    cu = None
+    if cu_seqlens is not None:
+        cu, t = _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"), k.shape[0]
+        if k.dim() != 3:
+            raise ValueError("%s: packed rows have three dimensions" % name)
+    else:
+        rows = k.shape[0] * (k.shape[1] if k.dim() == 4 else 1)
+        if rows % n_seqs or (k.dim() == 4 and k.shape[0] != n_seqs):
+            raise ValueError("%s: the rows do not divide over the sequences" % name)
+        t = rows // n_seqs
+    _check(fn(k_ptr, v_ptr, k_row, v_row, t, cu, n_seqs, kv_heads, HEAD_DIM, _ATTN_TYPES[dt],
+              c_ptr, n_pages, page, table, width, lens_ptr, _stream(k)))
+
+
+def kda_attn_kv4_append(k, v, cache, page_table, lens, cu_seqlens=None):
+    """Writes rows into the 4-bit cache: BF16 or FP16 k, v [rows, kv_heads, 128]
+    become the last positions of their sequences, lens (device int32 [N]) counting
+    them already.  page_table: device int32 [N, pages].  cu_seqlens: offsets of
+    packed rows; without it each sequence has rows / N (also [N, k, kv_heads, 128])."""
+    _kv4_rows("kda_attn_kv4_append", LIB.kda_attn_kv4_append, k, v, cache, page_table, lens,
+              cu_seqlens)
+
+
+def kda_attn_kv4_read(k, v, cache, page_table, lens, cu_seqlens=None):
+    """The last rows of each sequence out of the 4-bit cache into k and v, which
+    are laid out as kda_attn_kv4_append's."""
+    _kv4_rows("kda_attn_kv4_read", LIB.kda_attn_kv4_read, k, v, cache, page_table, lens,
+              cu_seqlens)
+
+
+def kda_attn_kv4_workspace(n_seqs, krows, heads, kv_heads, device="cuda"):
+    """Workspace for kda_attn_kv4_decode."""
+    need = LIB.kda_attn_kv4_workspace_size(n_seqs, krows, heads, kv_heads)
+    return torch.empty(int(need), dtype=torch.uint8, device=device)
+
+
+def kda_attn_kv4_decode(q, cache, page_table, lens, out, lse=None, window=0, scale=Q_SCALE,
+                        workspace=None):
+    """k query rows of each sequence over the 4-bit cache: q, out BF16 or FP16
+    [N, k, heads, 128] (or [N, heads, 128]), the last k of lens[n] positions; lse
+    FP32 [N, k, heads] or None."""
+    dt = q.dtype
+    if dt not in _ATTN_TYPES:
+        raise TypeError("kda_attn_kv4_decode: q must be bfloat16 or float16")
+    if q.dim() not in (3, 4) or q.shape[-1] != HEAD_DIM or out.shape != q.shape:
+        raise ValueError("kda_attn_kv4_decode: q and out must be [N, k, heads, 128]")
+    _contig(q, "q")
+    _contig(out, "out")
+    c_ptr, n_pages, page, table, width, lens_ptr = _kv4(cache, page_table, lens)
+    n_seqs, heads, kv_heads = q.shape[0], q.shape[-2], cache.shape[1]
+    krows = q.shape[1] if q.dim() == 4 else 1
+    if lens.numel() != n_seqs:
+        raise ValueError("kda_attn_kv4_decode: lens must hold one length per sequence")
+    _same_device(cache, q, out, lse)
+    lse_ptr = None
+    if lse is not None:
+        if lse.shape != q.shape[:-1]:
+            raise ValueError("kda_attn_kv4_decode: lse must be [N, k, heads]")
+        _contig(lse, "lse")
+        lse_ptr = _ptr(lse, torch.float32, "lse")
+    need = 0
+    if workspace is None:
+        need = LIB.kda_attn_kv4_workspace_size(n_seqs, krows, heads, kv_heads)
+    ws, ws_ptr, ws_bytes = _scratch(workspace, need, q.device)
+    _check(LIB.kda_attn_kv4_decode(_ptr(q, dt, "q"), c_ptr, n_pages, page, table, width, lens_ptr,
+                                   _ptr(out, dt, "out"), lse_ptr, n_seqs, krows, heads, kv_heads,
+                                   HEAD_DIM, _ATTN_TYPES[dt], window, scale, ws_ptr, ws_bytes,
+                                   _stream(q)))
 
 
 def kda_sync_status(device=None):

@@ -34,17 +34,25 @@ extern "C" kda_status kda_sync_status(uint64_t stream) {
     if (e == cudaSuccess) e = kda::read_and_clear_status_conv(&b);
     if (e == cudaSuccess) e = kda::read_and_clear_status_prefill_tc(&c);
     a |= c;
+    unsigned d = 0, f = 0, g = 0;
+    if (e == cudaSuccess) e = kda::read_and_clear_status_attn(&d);
+    if (e == cudaSuccess) e = kda::read_and_clear_status_kv4(&f);
+    if (e == cudaSuccess) e = kda::read_and_clear_status_decode(&g);
+    d |= f | g;
     if (e != cudaSuccess) {
         kda::set_error("kda_sync_status: reading the status word failed: %s",
                        cudaGetErrorString(e));
         return KDA_ERR_CUDA;
     }
-    if (a | b) {
-        kda::set_error("kda_sync_status: device-side check failed (prefill 0x%x, conv 0x%x): %s",
-                       a, b,
-                       ((a | b) & kda::STATUS_TIMEOUT)      ? "a bounded wait timed out"
-                       : ((a | b) & kda::STATUS_SMEM_ALIGN) ? "shared memory misaligned"
-                                                            : "malformed cu_seqlens");
+    const unsigned all = a | b | d;
+    if (all) {
+        kda::set_error("kda_sync_status: device-side check failed (prefill 0x%x, conv 0x%x, "
+                       "attention 0x%x): %s",
+                       a, b, d,
+                       (all & kda::STATUS_TIMEOUT)      ? "a bounded wait timed out"
+                       : (all & kda::STATUS_SMEM_ALIGN) ? "shared memory misaligned"
+                       : (all & kda::STATUS_BAD_PAGES)  ? "lens or page_table outside the cache"
+                                                        : "malformed cu_seqlens");
         return KDA_ERR_DEVICE;
     }
     return KDA_OK;

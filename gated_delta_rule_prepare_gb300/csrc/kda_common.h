@@ -41,6 +41,7 @@ enum : unsigned {
     STATUS_BAD_CU_SEQLENS = 1u << 0,
     STATUS_TIMEOUT = 1u << 1,  // a bounded wait on a copy or an MMA gave up
     STATUS_SMEM_ALIGN = 1u << 2,  // dynamic shared memory not 1024-byte aligned
+    STATUS_BAD_PAGES = 1u << 3,  // lens or page_table does not fit the 4-bit cache
 };
 
 // Each checking unit exposes a reader that returns and clears its word on the
@@ -48,6 +49,9 @@ enum : unsigned {
 cudaError_t read_and_clear_status_prefill(unsigned* out);
 cudaError_t read_and_clear_status_conv(unsigned* out);
 cudaError_t read_and_clear_status_prefill_tc(unsigned* out);
+cudaError_t read_and_clear_status_attn(unsigned* out);
+cudaError_t read_and_clear_status_kv4(unsigned* out);
+cudaError_t read_and_clear_status_decode(unsigned* out);
 
 // kda_prefill's argument checks, shared with kda_prefill_static_ws (prefill.cu).
 kda_status validate_prefill(const char* fn, const float* state, const void* q, const void* k,

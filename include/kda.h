@@ -53,6 +53,9 @@ extern "C" {
 /* Depthwise conv taps: the conv kernels keep the window in 4 registers
  * (config.rs validate). */
 #define KDA_MAX_CONV_KERNEL 4
+/* Bytes one token of one KV head takes in the 4-bit cache, K and V together:
+ * for each, 64 bytes of codes and 8 of parameters. */
+#define KDA_KV4_TOKEN_BYTES 144
 
 typedef enum {
     KDA_OK = 0,
@@ -63,7 +66,8 @@ typedef enum {
     KDA_ERR_DEVICE = 5       /* device-side check failed (kda_sync_status)     */
 } kda_status;
 
-typedef enum { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype;
+/* KDA_F16 is taken by the attention calls only. */
+typedef enum { KDA_F32 = 0, KDA_BF16 = 1, KDA_F16 = 2 } kda_dtype;
 
 /*
  * kda_decode -- one token for each of n_seqs independent sequences
@@ -408,6 +412,133 @@ kda_status kda_prefill_static_ws(float* state, const void* q, const void* k, con
                                  int chunk, float pad_fill, int heads, int head_dim, int in_dtype,
                                  int64_t qkv_row_stride, const int* cu_seqlens, int n_seqs,
                                  uint64_t stream);
+
+/*
+ * Full attention.  A hybrid decoder puts full-attention layers between its KDA
+ * layers; the four calls below are such a layer's core, for the same packed
+ * prompts (kda_attn_prefill beside kda_prefill) and the same decode and verify
+ * steps (kda_attn_kv4_decode beside kda_decode and kda_decode_k).  The source
+ * pages describe the KDA layer only; these calls are the library's own.
+ *
+ * kda_attn_prefill -- causal attention with grouped heads over packed prompts.
+ * For query row i of a sequence of Lq query and Lk key rows, at position
+ * p = Lk - Lq + i (the queries are the last positions: Lk > Lq is a chunk
+ * behind its context), query head h and KV head h / (heads / kv_heads):
+ *     s_j = scale * q_i . k_j,          max(0, p - window + 1) <= j <= p
+ *     o_i = sum_j exp(s_j - lse_i) v_j, lse_i = log sum_j exp(s_j)
+ * A row that sees no key (Lk < Lq) gives o = 0 and lse = -inf.  Keys a row does
+ * not see have no influence on it, whatever they hold (infinities and NaN
+ * included).
+ *
+ *   q : in_dtype, token row r of head h at q + r*q_row_stride + h*128
+ *   k, v : in_dtype, kv_heads heads, likewise       o : in_dtype, like q
+ *   lse : FP32 [rows][heads] (natural logarithm), or NULL
+ *   cu_seqlens_q, cu_seqlens_k : DEVICE int32 [n_seqs + 1] row offsets; t_q
+ *           and t_k are then the totals.  Both NULL: n_seqs sequences of t_q
+ *           query rows and t_k key rows each.  Checked on the device: rows of a
+ *           sequence whose offsets lie outside the arrays are not written, and
+ *           kda_sync_status reports KDA_ERR_DEVICE.
+ *   heads : a multiple of kv_heads, at most 128 per KV head
+ *   in_dtype : KDA_BF16 or KDA_F16
+ *   row strides : >= heads*128 (kv_heads*128), multiples of 8 elements; q, k, v
+ *           and o 16-byte aligned; o overlaps none of the inputs
+ *   window : 0 for none      scale : finite, positive
+ *   workspace : device scratch of at least kda_attn_prefill_workspace_size
+ *           bytes, 16-byte aligned; its contents on entry do not matter; calls
+ *           that share one must be ordered on the GPU.
+ * Scores, the softmax and the sums are FP32; the weights enter the product
+ * with v rounded to in_dtype.
+ */
+kda_status kda_attn_prefill(const void* q, const void* k, const void* v, void* o, float* lse,
+                            int t_q, int t_k, const int* cu_seqlens_q, const int* cu_seqlens_k,
+                            int n_seqs, int heads, int kv_heads, int head_dim, int in_dtype,
+                            int64_t q_row_stride, int64_t k_row_stride, int64_t v_row_stride,
+                            int64_t o_row_stride, int window, float scale, void* workspace,
+                            size_t workspace_bytes, uint64_t stream);
+
+/* Bytes of workspace kda_attn_prefill needs for `rows` query rows in total.
+ * Returns 0 for invalid arguments. */
+size_t kda_attn_prefill_workspace_size(int64_t rows, int n_seqs, int heads, int kv_heads);
+
+/*
+ * The 4-bit cache.  A page holds `page` tokens (16, 32, 64, 128 or 256) of all
+ * KV heads: uint8 [n_pages][kv_heads][page * KDA_KV4_TOKEN_BYTES], caller-owned,
+ * 16-byte aligned.  Position j of sequence n is token j % page of page
+ * page_table[n][j / page] (DEVICE int32 [n_seqs][max_pages]).
+ *
+ * A block (one page of one head) is four parts: K codes (64 * page bytes), K
+ * parameters (8 * page), V codes, V parameters.  64 channels of a row share a
+ * step s and a minimum m, both BF16; a token's parameters are s, m of channels
+ * 0..63, then of 64..127.  A code c of 0..15 stands for m + s * c.  Codes lie
+ * in groups of 16 tokens x 128 channels, 1024 bytes: with
+ *     K: token = 8 i + g,        channel = 64 a + 16 b + 8 j + 2 t + e
+ *     V: token = 8 i + 2 t + e,  channel = 64 a + 16 b + 8 j + g
+ * a code is in byte 512 a + 16 (4 g + t) + 4 b + 2 e + i, in the low (j = 0) or
+ * the high (j = 1) four bits: the order in which the decode's matrix
+ * instructions take them.  Every byte belongs to one token.
+ *
+ * lens (DEVICE int32 [n_seqs]) counts each sequence's positions, the rows of
+ * the call included: append and read work on the last rows of each sequence,
+ * decode's queries are its last krows positions.  Device-side checks (lens
+ * outside 0..max_pages * page or below the rows of the call, a page number
+ * outside 0..n_pages - 1): nothing outside the cache is touched, and
+ * kda_sync_status reports KDA_ERR_DEVICE.
+ *
+ * kda_attn_kv4_append -- writes rows into the cache.  Per row, head and 64
+ * channels: m is the largest BF16 <= min x, s the smallest BF16 >=
+ * (max x - m) / 15, and the code round((x - m) / s), ties to even (0 where s is
+ * 0).  Where the 64 values hold an infinity or a NaN, all of them read as NaN.
+ *
+ *   k, v : in_dtype (KDA_BF16, KDA_F16), token row r of head h at
+ *           k + r*k_row_stride + h*128 (stride >= kv_heads*128, a multiple of 8)
+ *   cu_seqlens : DEVICE int32 [n_seqs + 1] offsets of the packed rows, t their
+ *           total; NULL: t rows for each sequence
+ * Rows of one call must not share a page (two sequences writing to one page);
+ * pages that sequences share as a common prefix are only read.
+ */
+kda_status kda_attn_kv4_append(const void* k, const void* v, int64_t k_row_stride,
+                               int64_t v_row_stride, int t, const int* cu_seqlens, int n_seqs,
+                               int kv_heads, int head_dim, int in_dtype, uint8_t* cache,
+                               int64_t n_pages, int page, const int* page_table, int max_pages,
+                               const int* lens, uint64_t stream);
+
+/*
+ * kda_attn_kv4_read -- the last rows of each sequence out of the cache, as
+ * in_dtype: m + s * code in FP32, rounded once.  Arguments as
+ * kda_attn_kv4_append, k and v written.  (With as many rows as positions: the
+ * whole context, as kda_attn_prefill takes it for the next chunk.)  Rows of a
+ * page that is not there read as NaN.
+ */
+kda_status kda_attn_kv4_read(void* k, void* v, int64_t k_row_stride, int64_t v_row_stride, int t,
+                             const int* cu_seqlens, int n_seqs, int kv_heads, int head_dim,
+                             int in_dtype, const uint8_t* cache, int64_t n_pages, int page,
+                             const int* page_table, int max_pages, const int* lens,
+                             uint64_t stream);
+
+/*
+ * kda_attn_kv4_decode -- krows query rows of each sequence (1 for decode, up to
+ * KDA_MAX_K for verification) over the cache: kda_attn_prefill's formula with
+ * Lq = krows, Lk = lens[n] and the cache's values as k and v.  Row i of
+ * sequence n sees positions up to lens[n] - krows + i; a row that sees none
+ * gives o = 0 and lse = -inf.  Positions on a page that is not there are left
+ * out.
+ *
+ *   q, o : in_dtype (KDA_BF16, KDA_F16) [n_seqs][krows][heads][128]
+ *   lse : FP32 [n_seqs][krows][heads], or NULL
+ *   workspace : device scratch of at least kda_attn_kv4_workspace_size bytes,
+ *           16-byte aligned; its contents on entry do not matter; calls that
+ *           share one must be ordered on the GPU.
+ * The result is deterministic: the same inputs give the same bits.
+ */
+kda_status kda_attn_kv4_decode(const void* q, const uint8_t* cache, int64_t n_pages, int page,
+                               const int* page_table, int max_pages, const int* lens, void* o,
+                               float* lse, int n_seqs, int krows, int heads, int kv_heads,
+                               int head_dim, int in_dtype, int window, float scale,
+                               void* workspace, size_t workspace_bytes, uint64_t stream);
+
+/* Bytes of workspace kda_attn_kv4_decode needs.  Returns 0 for invalid
+ * arguments. */
+size_t kda_attn_kv4_workspace_size(int n_seqs, int krows, int heads, int kv_heads);
 
 /* Synchronises `stream`, then reads and clears the device status words of the
  * calling thread's current device.  Returns KDA_OK, KDA_ERR_DEVICE (a
