@@ -4,14 +4,35 @@
 //     s_j = scale * q_i . k_j          for max(0, p - window + 1) <= j <= p
 //     o_i = sum_j exp(s_j - lse) v_j,  lse = log sum_j exp(s_j)
 // A row that sees no key gives o = 0 and lse = -inf.
+//
+// Bound by the tensor cores: 512 FLOP per (query row, key) against 512 bytes
+// per key and tile.  The shape of the work:
+//  - A tile is 128 rows of Q: the G = heads / kv_heads query heads of one KV
+//    head for 128 / G consecutive tokens (rows past G * (128 / G) idle).  The
+//    heads that share keys share their loads, and a tile spans few tokens, so
+//    little of its last key block is masked.
+//  - A work item is two such tiles, one after the other in the sequence, and
+//    walks their keys in blocks of 128.  S = Q K^T (FP32) sits in TMEM, one
+//    thread owns one row of it, and writes exp2(S - max) over it in 16 bits,
+//    from where the second product reads it as its A operand.  The tensor
+//    cores work for one tile while the other tile's softmax runs.
+//  - One persistent CTA per SM: a TMA warp, a thread that issues the MMAs, four
+//    softmax warps for each tile, four warps that write finished tiles, so the
+//    next item's first block overlaps the last one's end.
+//  - Items go out longest first, by a list that attn_plan_kernel sorts and a
+//    ticket counter; a call whose items fit one per SM needs neither.
 #include <cmath>
 
 #include "attn_common.h"
+#include "f32x2.h"
+#include "sm103_tc.h"
+#include "tma_map.h"
 
 namespace kda {
 namespace {
 
 using namespace attn;
+using namespace tc;
 
 __device__ unsigned g_attn_status = 0;
 
@@ -22,17 +43,20 @@ struct PrefillArgs {
     const int *cu_q, *cu_k;
     long long q_stride, k_stride, v_stride, o_stride;
     int t_q, t_k, n_seqs, heads, kv_heads, window;
+    int group, tile_tokens;  // heads per KV head; tokens per tile
     float scale;
+    int4* list;       // sorted entries; null: the slots themselves, one item per CTA
+    unsigned* count;  // entries in the list, then the ticket counter
+    int slots, bucket_shift;
 };
 
 // Sequence n's query and key rows; false for offsets outside the arrays.
 struct Span {
-    long long q0, k0;
-    int lq, lk;
+    int q0, k0, lq, lk;
 };
 __device__ __forceinline__ bool sequence_span(const PrefillArgs& a, int n, Span& s) {
     if (!a.cu_q) {
-        s = {(long long)n * a.t_q, (long long)n * a.t_k, a.t_q, a.t_k};
+        s = {n * a.t_q, n * a.t_k, a.t_q, a.t_k};
         return true;
     }
     const int q0 = __ldg(a.cu_q + n), q1 = __ldg(a.cu_q + n + 1);
@@ -41,22 +65,121 @@ __device__ __forceinline__ bool sequence_span(const PrefillArgs& a, int n, Span&
     return q0 >= 0 && q0 <= q1 && q1 <= a.t_q && k0 >= 0 && k0 <= k1 && k1 <= a.t_k;
 }
 
-// One (row, head) per warp, 4 channels a lane: one pass over the row's keys
-// with the running maximum and sum of the softmax.
+// An item's tokens, all heads: first query row, tokens (at most two tiles'),
+// first key row of the sequence, position of the first token (it may be
+// negative).  Keys of the sequence end at its last query's position.
+struct Entry {
+    int row, tokens, k0, pos;
+};
+
+// Slots number the items of all sequences: sequence n, whose queries start at
+// row c, owns slots from c / span + n (span = 2 tiles of tokens), never fewer
+// than it has items.
+__device__ __forceinline__ long long first_slot(const PrefillArgs& a, int n) {
+    const int span = 2 * a.tile_tokens;
+    const long long c = a.cu_q ? (long long)__ldg(a.cu_q + n) : (long long)n * a.t_q;
+    return c / span + n;
+}
+__device__ __forceinline__ bool slot_entry(const PrefillArgs& a, int n, long long slot, Entry& e) {
+    Span s;
+    if (!sequence_span(a, n, s)) return false;
+    const int span = 2 * a.tile_tokens;
+    const long long i = (slot - first_slot(a, n)) * span;  // first token
+    if (i < 0 || i >= s.lq) return false;
+    e = {s.q0 + (int)i, min(span, s.lq - (int)i), s.k0, s.lk - s.lq + (int)i};
+    return true;
+}
+
+// Key blocks [lo, hi) of 128 that `tokens` tokens from position `pos` see.
+__device__ __forceinline__ void key_blocks(const PrefillArgs& a, int pos, int tokens, int& lo,
+                                           int& hi) {
+    const int last = pos + tokens - 1;
+    lo = a.window ? max(0, pos - a.window + 1) >> 7 : 0;
+    hi = tokens > 0 && last >= 0 ? (last >> 7) + 1 : lo;
+    if (hi < lo) hi = lo;
+}
+
+// Writes the entries, most key blocks first (a counting sort), and zeroes the
+// ticket counter.  One CTA: at 16 prompts of 512 to 8192 tokens it sorts about
+// 1100 entries.
+constexpr int kPlanThreads = 1024;
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(PrefillArgs a) {
+    __shared__ int hist[kPlanThreads];
+    __shared__ int warp_sum[32];
+    pdl_wait();
+    pdl_release();
+    const int tid = threadIdx.x;
+    hist[tid] = 0;
+    if (tid < 32 && a.cu_q) {
+        const bool ok = warp_offsets_ok(a.cu_q, a.n_seqs, a.t_q) &&
+                        warp_offsets_ok(a.cu_k, a.n_seqs, a.t_k);
+        if (!ok && tid == 0) atomicOr(&g_attn_status, STATUS_BAD_CU_SEQLENS);
+    }
+    __syncthreads();
+    // bucket 0 holds the longest entries
+    auto entry_of = [&](int slot, Entry& e, int& bucket) {
+        int lo = 0, n = a.n_seqs;
+        while (n > 1) {
+            const int half = n / 2;
+            if (first_slot(a, lo + half) <= slot) {
+                lo += half;
+                n -= half;
+            } else {
+                n = half;
+            }
+        }
+        if (!slot_entry(a, lo, slot, e)) return false;
+        int b0, b1;
+        key_blocks(a, e.pos, e.tokens, b0, b1);
+        bucket = kPlanThreads - 1 - min((b1 - b0) >> a.bucket_shift, kPlanThreads - 1);
+        return true;
+    };
+    Entry e;
+    int bucket;
+    for (int s = tid; s < a.slots; s += kPlanThreads)
+        if (entry_of(s, e, bucket)) atomicAdd(&hist[bucket], 1);
+    __syncthreads();
+    const int mine = hist[tid];
+    int sum = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, sum, off);
+        if ((tid & 31) >= off) sum += up;
+    }
+    if ((tid & 31) == 31) warp_sum[tid >> 5] = sum;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < (tid >> 5); ++w) before += warp_sum[w];
+    hist[tid] = before + sum - mine;
+    if (tid == kPlanThreads - 1) {
+        a.count[0] = before + sum;
+        a.count[1] = 0;
+    }
+    __syncthreads();
+    for (int s = tid; s < a.slots; s += kPlanThreads)
+        if (entry_of(s, e, bucket))
+            a.list[atomicAdd(&hist[bucket], 1)] = make_int4(e.row, e.tokens, e.k0, e.pos);
+}
+
+// One row on the CUDA cores by one warp, 4 channels a lane, touching only the
+// keys that the row sees.  The tensor cores multiply a masked key's weight 0
+// with its value, which gives NaN where the value is infinite or NaN; rows that
+// come out so are done again here.  Not a path for ordinary inputs.
 template <bool F16>
-__device__ __forceinline__ void attend_row(const PrefillArgs& a, const Span& s, int i, int h) {
+__device__ __noinline__ void attend_row(const PrefillArgs& a, long long row, long long k0, int p,
+                                        int h) {
     const int lane = threadIdx.x & 31;
-    const int hk = h / (a.heads / a.kv_heads);
-    const int p = s.lk - s.lq + i;
+    const int hk = h / a.group;
     const int first = a.window ? max(0, p - a.window + 1) : 0;
-    const uint2 qb = __ldg(reinterpret_cast<const uint2*>(a.q + (s.q0 + i) * a.q_stride +
-                                                          h * D + 4 * lane));
+    const uint2 qb = __ldg(reinterpret_cast<const uint2*>(a.q + row * a.q_stride + h * D +
+                                                          4 * lane));
     const float c = a.scale * kLog2e;
     const float2 q01 = widen2<F16>(qb.x), q23 = widen2<F16>(qb.y);
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    const uint16_t* kp = a.k + s.k0 * a.k_stride + hk * D + 4 * lane;
-    const uint16_t* vp = a.v + s.k0 * a.v_stride + hk * D + 4 * lane;
+    const uint16_t* kp = a.k + k0 * a.k_stride + hk * D + 4 * lane;
+    const uint16_t* vp = a.v + k0 * a.v_stride + hk * D + 4 * lane;
+#pragma unroll 1
     for (int j = first; j <= p; ++j) {
         const uint2 kb = __ldg(reinterpret_cast<const uint2*>(kp + j * a.k_stride));
         const uint2 vb = __ldg(reinterpret_cast<const uint2*>(vp + j * a.v_stride));
@@ -81,26 +204,542 @@ __device__ __forceinline__ void attend_row(const PrefillArgs& a, const Span& s, 
     }
     const float r = l == 0.f ? 0.f : 1.f / l;
     const uint2 out = make_uint2(narrow2<F16>(o.x * r, o.y * r), narrow2<F16>(o.z * r, o.w * r));
-    *reinterpret_cast<uint2*>(a.o + (s.q0 + i) * a.o_stride + h * D + 4 * lane) = out;
+    *reinterpret_cast<uint2*>(a.o + row * a.o_stride + h * D + 4 * lane) = out;
     if (a.lse && lane == 0)
-        a.lse[(s.q0 + i) * a.heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        a.lse[row * a.heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// ---------------------------------------------------------------- the kernel
+constexpr int kThreads = 512;
+constexpr int kStages = 5;                 // of 32 KB: a block's K, then its V
+constexpr uint32_t kTileBytes = 128 * 128 * 2;
+constexpr int kRing = 4;                   // items between the TMA warp and the others
+constexpr uint32_t kTmemO = 256;           // S0, S1, O0, O1: 128 columns each
+// Registers a thread: softmax (2 x 128 threads), writers (128), the rest (128).
+// Together what the launch has: 4 * 128.
+constexpr int kRegSoftmax = 176, kRegWriter = 96, kRegOther = 64;
+static_assert(2 * kRegSoftmax + kRegWriter + kRegOther <= 512, "registers of the launch");
+// The running maximum is left behind by up to 2^kLag before O is rescaled: a
+// weight is then at most 2^kLag, the sum and O carry the same factor and the
+// final division removes it.  The exponents of FP16 weights start at
+// 2^kLift so that weights down to 2^-31 of the largest one stay above its
+// smallest number.
+constexpr float kLag = 8.f;
+template <bool F16>
+constexpr float kLift = F16 ? 7.f : 0.f;
+
+struct Item {
+    Entry e;
+    int head;  // KV head; negative: no more items
+};
+
+struct Shared {
+    uint64_t kv_full[kStages], kv_empty[kStages];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[2], p_full[2];
+    uint64_t o_full[2], o_empty[2], stat_full[2];
+    uint64_t item_full[kRing], item_empty[kRing];
+    Item item[kRing];
+    float2 stat[2][128];  // a finished row's reference maximum (raw score) and sum
+    uint32_t tmem;
+    int stop;  // a wait gave up: everybody leaves
+};
+constexpr uint32_t kSharedOff = (2 + kStages) * kTileBytes;
+constexpr uint32_t kSmemBytes = kSharedOff + sizeof(Shared);
+static_assert(kSmemBytes <= 232448, "shared memory");
+
+// Waits with an end: a phase that does not come within 2^35 clocks (some 17
+// seconds; rows done again by attend_row may keep others waiting for long), or
+// another role's giving up, ends the kernel with an error status.
+__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity) {
+    if (mbar_wait(bar, parity, 1)) return true;
+    const long long from = clock64();
+    while (!mbar_wait(bar, parity, 32)) {
+        if (*(volatile int*)&sh.stop) return false;
+        if (clock64() - from > 1LL << 35) {
+            atomicOr(&g_attn_status, STATUS_TIMEOUT);
+            *(volatile int*)&sh.stop = 1;
+            return false;
+        }
+    }
+    return true;
+}
+// For a whole warp, which leaves together.
+__device__ __forceinline__ bool wait_warp(Shared& sh, uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait(sh, bar, parity));
+}
+
+// Tile t's tokens and key blocks within an item.
+struct Tile {
+    int tokens, pos, lo, hi;
+};
+__device__ __forceinline__ Tile tile_of(const PrefillArgs& a, const Entry& e, int t) {
+    Tile r;
+    r.tokens = min(a.tile_tokens, e.tokens - t * a.tile_tokens);
+    if (r.tokens < 0) r.tokens = 0;
+    r.pos = e.pos + t * a.tile_tokens;
+    key_blocks(a, r.pos, r.tokens, r.lo, r.hi);
+    return r;
+}
+// The union of both tiles' blocks (their ranges overlap or touch).
+struct Blocks {
+    int lo, hi;
+};
+__device__ __forceinline__ Blocks blocks_of(const Tile& x, const Tile& y) {
+    if (x.hi <= x.lo) return {y.lo, y.hi};
+    if (y.hi <= y.lo) return {x.lo, x.hi};
+    return {min(x.lo, y.lo), max(x.hi, y.hi)};
+}
+
+// The TMA warp: hands out items and fills the Q tiles and the ring of K and V.
+__device__ __forceinline__ void load_role(const PrefillArgs& a, Shared& sh, unsigned char* sm,
+                                          const CUtensorMap* mq, const CUtensorMap* mk,
+                                          const CUtensorMap* mv) {
+    const int lane = threadIdx.x & 31;
+    int stage = 0;
+    uint32_t phase = 0, q_phase[2] = {0, 0}, ring_phase = 0;
+    int ring = 0;
+    const int n_list = a.list ? (int)*a.count : 0;
+    bool go = true;
+    for (int round = 0; go; ++round) {
+        Item it;
+        it.head = -1;
+        if (a.list) {
+            unsigned x = 0;
+            if (lane == 0) x = atomicAdd(a.count + 1, 1u);
+            x = __shfl_sync(0xffffffffu, x, 0);
+            const unsigned e = x / (unsigned)a.kv_heads;
+            if (e < (unsigned)n_list) {
+                const int4 v = __ldcg(a.list + e);
+                it.e = {v.x, v.y, v.z, v.w};
+                it.head = (int)(x - e * a.kv_heads);
+            }
+        } else if (round == 0) {
+            const int slot = blockIdx.x / a.kv_heads;
+            const int n = warp_find_last(a.n_seqs, slot, [&](int i) { return first_slot(a, i); });
+            if (slot_entry(a, n, slot, it.e)) it.head = blockIdx.x - slot * a.kv_heads;
+        }
+        if (lane == 0) {
+            go = wait(sh, &sh.item_empty[ring], ring_phase ^ 1);
+            if (go) {
+                sh.item[ring] = it;
+                mbar_arrive(&sh.item_full[ring]);
+            }
+        }
+        if (++ring == kRing) ring = 0, ring_phase ^= 1;
+        go = __shfl_sync(0xffffffffu, go && it.head >= 0, 0);
+        if (!go) break;
+        if (lane == 0) {
+            const Tile tile[2] = {tile_of(a, it.e, 0), tile_of(a, it.e, 1)};
+            const uint32_t q_bytes = (uint32_t)(a.group * a.tile_tokens) * 256;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (!go || tile[t].hi <= tile[t].lo) continue;
+                go = wait(sh, &sh.q_empty[t], q_phase[t] ^ 1);
+                q_phase[t] ^= 1;
+                if (!go) continue;
+                mbar_arrive_expect_tx(&sh.q_full[t], q_bytes);
+                for (int half = 0; half < 2; ++half)
+                    tma_load_3d(sm + t * kTileBytes + half * (kTileBytes / 2), mq, &sh.q_full[t],
+                                64 * half, it.head * a.group, it.e.row + t * a.tile_tokens);
+            }
+            const Blocks b = blocks_of(tile[0], tile[1]);
+            for (int j = b.lo; go && j < b.hi; ++j) {
+                for (int which = 0; which < 2; ++which) {
+                    go = go && wait(sh, &sh.kv_empty[stage], phase ^ 1);
+                    if (!go) break;
+                    mbar_arrive_expect_tx(&sh.kv_full[stage], kTileBytes);
+                    unsigned char* dst = sm + (2 + stage) * kTileBytes;
+                    for (int half = 0; half < 2; ++half)
+                        tma_load_3d(dst + half * (kTileBytes / 2), which ? mv : mk,
+                                    &sh.kv_full[stage], 64 * half, it.head, it.e.k0 + j * 128);
+                    if (++stage == kStages) stage = 0, phase ^= 1;
+                }
+            }
+        }
+        go = __shfl_sync(0xffffffffu, go, 0);
+    }
+    // copies in flight must land before the CTA's memory goes away: each stage
+    // that was filled and not waited for
+    if (lane == 0 && *(volatile int*)&sh.stop) {
+        for (int s = 0; s < kStages; ++s)
+            mbar_wait(&sh.kv_full[s], s < stage ? phase : phase ^ 1, 1 << 12);
+        for (int t = 0; t < 2; ++t) mbar_wait(&sh.q_full[t], q_phase[t] ^ 1, 1 << 12);
+    }
+}
+
+// The thread that issues the MMAs.  Per block and tile: O += P V, then S of the
+// next block, which may be the next item's first.  MMAs of one CTA execute in
+// the order of their issue, so S's write over P needs no wait of its own.
+template <bool F16>
+__device__ __forceinline__ void mma_role(const PrefillArgs& a, Shared& sh, unsigned char* sm) {
+    constexpr uint32_t kQK = idesc_16(128, 128, !F16, false);
+    constexpr uint32_t kPV = idesc_16(128, 128, !F16, true);
+    const uint32_t tmem = sh.tmem;
+    int stage = 0;  // of the next K or V to be used
+    uint32_t phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, o_phase[2] = {0, 0};
+    int ring = 0;
+    uint32_t ring_phase = 0;
+    struct Work {  // key blocks of the tiles and of both
+        Blocks t[2], b;
+        bool any;
+    };
+    // the next item that has key blocks at all
+    auto next_item = [&](Work& w) {
+        for (;;) {
+            w.any = false;
+            if (!wait(sh, &sh.item_full[ring], ring_phase)) return false;
+            const Item it = sh.item[ring];
+            mbar_arrive(&sh.item_empty[ring]);
+            if (++ring == kRing) ring = 0, ring_phase ^= 1;
+            if (it.head < 0) return true;
+            const Tile x = tile_of(a, it.e, 0), y = tile_of(a, it.e, 1);
+            w.t[0] = {x.lo, x.hi};
+            w.t[1] = {y.lo, y.hi};
+            w.b = blocks_of(x, y);
+            if (w.b.hi > w.b.lo) {
+                w.any = true;
+                return true;
+            }
+        }
+    };
+    auto active = [](const Work& w, int t, int j) { return j >= w.t[t].lo && j < w.t[t].hi; };
+    auto qk = [&](const Work& w, int t, int j, int k_stage) {
+        if (j == w.t[t].lo) {
+            if (!wait(sh, &sh.q_full[t], q_phase[t])) return false;
+            q_phase[t] ^= 1;
+        }
+        tc_fence_after();
+        const uint32_t qa = smem_u32(sm) + t * kTileBytes;
+        const uint32_t kb = smem_u32(sm) + (2 + k_stage) * kTileBytes;
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            const uint32_t off = (s >> 2) * (kTileBytes / 2) + (s & 3) * 32;
+            mma_f16(tmem + t * 128, make_desc_sw128(qa + off, 16), make_desc_sw128(kb + off, 16),
+                    kQK, s > 0);
+        }
+        mma_commit(&sh.s_full[t]);
+        if (j == w.t[t].hi - 1) mma_commit(&sh.q_empty[t]);
+        return true;
+    };
+    auto pv = [&](const Work& w, int t, int j, int v_stage) {
+        if (j == w.t[t].lo) {
+            if (!wait(sh, &sh.o_empty[t], o_phase[t] ^ 1)) return false;
+            o_phase[t] ^= 1;
+        }
+        if (!wait(sh, &sh.p_full[t], p_phase[t])) return false;
+        p_phase[t] ^= 1;
+        tc_fence_after();
+        const uint32_t vb = smem_u32(sm) + (2 + v_stage) * kTileBytes;
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            mma_f16_ta(tmem + kTmemO + t * 128, tmem + t * 128 + 8 * s,
+                       make_desc_sw128(vb + s * 2048, kTileBytes / 2), kPV,
+                       j > w.t[t].lo || s > 0);
+        if (j == w.t[t].hi - 1) mma_commit(&sh.o_full[t]);
+        return true;
+    };
+    auto take = [&](int& s) {  // the next stage of the ring, once it is filled
+        s = stage;
+        if (!wait(sh, &sh.kv_full[stage], phase)) return false;
+        if (++stage == kStages) stage = 0, phase ^= 1;
+        return true;
+    };
+    Work cur, nxt;
+    if (!next_item(cur) || !cur.any) return;
+    int ks, vs;
+    if (!take(ks)) return;
+    for (int t = 0; t < 2; ++t)
+        if (active(cur, t, cur.b.lo) && !qk(cur, t, cur.b.lo, ks)) return;
+    mma_commit(&sh.kv_empty[ks]);
+    for (;;) {
+        bool more = true;
+        for (int j = cur.b.lo; j < cur.b.hi; ++j) {
+            const bool last = j + 1 == cur.b.hi;
+            if (!take(vs)) return;
+            const Work* n = &cur;
+            int jn = j + 1;
+            if (last) {
+                if (!next_item(nxt)) return;
+                n = &nxt;
+                jn = nxt.b.lo;
+                more = nxt.any;
+            }
+            bool have_k = false;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (active(cur, t, j) && !pv(cur, t, j, vs)) return;
+                if (t == 1) mma_commit(&sh.kv_empty[vs]);
+                if (more && active(*n, t, jn)) {
+                    if (!have_k && !take(ks)) return;
+                    have_k = true;
+                    if (!qk(*n, t, jn, ks)) return;
+                }
+            }
+            if (have_k) mma_commit(&sh.kv_empty[ks]);
+        }
+        if (!more) return;
+        cur = nxt;
+    }
+}
+
+// Four warps, a thread a row of tile t: the softmax over the row's blocks.
+template <bool F16>
+__device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, int t) {
+    const int r = threadIdx.x & 127, lane = threadIdx.x & 31;
+    const uint32_t row_addr = sh.tmem + ((uint32_t)(r & ~31) << 16);
+    const uint32_t s_addr = row_addr + t * 128, o_addr = row_addr + kTmemO + t * 128;
+    const int token = r / a.group;
+    const float c = a.scale * kLog2e;
+    uint32_t s_phase = 0, o_phase = 0, ring_phase = 0;
+    int ring = 0;
+    for (;;) {
+        if (!wait_warp(sh, &sh.item_full[ring], ring_phase)) return;
+        const Item it = sh.item[ring];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.item_empty[ring]);
+        if (++ring == kRing) ring = 0, ring_phase ^= 1;
+        if (it.head < 0) return;
+        const Tile tile = tile_of(a, it.e, t);
+        if (tile.hi <= tile.lo) continue;
+        // keys first..pos; a row that is none of the tile's sees none
+        const int pos = token < tile.tokens ? tile.pos + token : -1;
+        const int first = a.window ? max(0, pos - a.window + 1) : 0;
+        // blocks [clear_lo, clear_hi) are seen whole by all of the tile's rows
+        const int clear_hi = (tile.pos + 1) >> 7;
+        const int clear_lo =
+            a.window ? (max(0, tile.pos + tile.tokens - a.window) + 127) >> 7 : 0;
+        float m = -INFINITY, l = 0.f;
+        for (int j = tile.lo; j < tile.hi; ++j) {
+            if (!wait_warp(sh, &sh.s_full[t], s_phase)) return;
+            s_phase ^= 1;
+            tc_fence_after();
+            float s[4][32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tmem_ld32(s_addr + 32 * i, s[i]);
+            tmem_ld_wait();
+            if (j < clear_lo || j >= clear_hi) {
+                const int lo = first - j * 128, hi = pos - j * 128;
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    if (i < lo || i > hi) s[i >> 5][i & 31] = -INFINITY;
+            }
+            float mx[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx[i] = s[i][0];
+#pragma unroll
+            for (int x = 1; x < 31; x += 2)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mx[i] = fmaxf(fmaxf(mx[i], s[i][x]), s[i][x + 1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], s[i][31]);
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            if (j == tile.lo) {
+                m = top;
+            } else {
+                const bool move = (top - m) * c > kLag;
+                if (__any_sync(0xffffffffu, move)) {
+                    // all MMAs before S of this block are done, the last O += P V
+                    // among them
+                    const float f = move ? ex2_approx((m - top) * c) : 1.f;
+                    if (move) m = top;
+                    l *= f;
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {
+                        float o[16];
+                        uint32_t u[16];
+                        tmem_ld16(o_addr + 16 * i, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) u[x] = __float_as_uint(o[x] * f);
+                        tmem_st16u(o_addr + 16 * i, u);
+                    }
+                }
+            }
+            const float shift = (m == -INFINITY ? 0.f : -m * c) + kLift<F16>;
+            const float2 c2 = make_float2(c, c), b2 = make_float2(shift, shift);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t p[32];
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                    float* y = &s[2 * half + (x >> 4)][2 * (x & 15)];
+                    const float2 e = fma2(make_float2(y[0], y[1]), c2, b2);
+                    y[0] = ex2_approx(e.x);
+                    y[1] = ex2_approx(e.y);
+                    p[x] = F16 ? pack_f16x2(y[0], y[1]) : pack_bf16x2(y[0], y[1]);
+                }
+                tmem_st32u(s_addr + 32 * half, p);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[t]);
+            float2 sum[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] = make_float2(s[i][0], s[i][1]);
+#pragma unroll
+            for (int x = 2; x < 32; x += 2)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sum[i] = add2(sum[i], make_float2(s[i][x], s[i][x + 1]));
+            const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+            l += all.x + all.y;
+        }
+        // once the writers have read the last item's
+        if (!wait_warp(sh, &sh.o_empty[t], o_phase ^ 1)) return;
+        o_phase ^= 1;
+        sh.stat[t][r] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.stat_full[t]);
+    }
+}
+
+// Four warps that divide by the sum and write finished tiles.
+template <bool F16>
+__device__ __forceinline__ void write_role(const PrefillArgs& a, Shared& sh) {
+    const int r = threadIdx.x & 127, lane = threadIdx.x & 31;
+    const uint32_t row_addr = sh.tmem + ((uint32_t)(r & ~31) << 16) + kTmemO;
+    const int token = r / a.group, in_group = r - token * a.group;
+    uint32_t phase[2] = {0, 0}, ring_phase = 0;
+    int ring = 0;
+    for (;;) {
+        if (!wait_warp(sh, &sh.item_full[ring], ring_phase)) return;
+        const Item it = sh.item[ring];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.item_empty[ring]);
+        if (++ring == kRing) ring = 0, ring_phase ^= 1;
+        if (it.head < 0) return;
+        const int h = it.head * a.group + in_group;
+#pragma unroll 1
+        for (int t = 0; t < 2; ++t) {
+            const Tile tile = tile_of(a, it.e, t);
+            if (tile.tokens == 0) continue;
+            const bool mine = token < tile.tokens;
+            const long long row = (long long)it.e.row + t * a.tile_tokens + token;
+            uint16_t* dst = a.o + row * a.o_stride + h * D;
+            const bool any = tile.hi > tile.lo;
+            float m = -INFINITY, l = 0.f;
+            if (any) {
+                if (!wait_warp(sh, &sh.stat_full[t], phase[t])) return;
+                const float2 st = sh.stat[t][r];
+                m = st.x;
+                l = st.y;
+                if (!wait_warp(sh, &sh.o_full[t], phase[t])) return;
+                phase[t] ^= 1;
+                tc_fence_after();
+            }
+            const bool empty = l == 0.f;
+            const float inv = empty ? 0.f : 1.f / l;
+            float poison = 0.f;  // NaN once any value is not finite
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+                float o[32];
+                if (any) {
+                    tmem_ld32(row_addr + t * 128 + 32 * i, o);
+                    tmem_ld_wait();
+                }
+                uint32_t u[16];
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const float y0 = empty ? 0.f : o[2 * x] * inv;
+                    const float y1 = empty ? 0.f : o[2 * x + 1] * inv;
+                    poison = fmaf(y0, 0.f, poison);
+                    poison = fmaf(y1, 0.f, poison);
+                    u[x] = narrow2<F16>(y0, y1);
+                }
+                if (mine) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        *reinterpret_cast<uint4*>(dst + 32 * i + 8 * x) =
+                            make_uint4(u[4 * x], u[4 * x + 1], u[4 * x + 2], u[4 * x + 3]);
+                }
+            }
+            if (any) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.o_empty[t]);
+            }
+            if (mine && a.lse)
+                a.lse[row * a.heads + h] =
+                    empty ? -INFINITY : fmaf(m, a.scale, (log2f(l) - kLift<F16>) * kLn2);
+            // a sum that is NaN comes from a key that the row sees
+            unsigned again = __ballot_sync(0xffffffffu, mine && poison != poison && l == l);
+            while (again) {
+                const int who = __ffs(again) - 1;
+                again &= again - 1;
+                attend_row<F16>(a, __shfl_sync(0xffffffffu, row, who), it.e.k0,
+                                __shfl_sync(0xffffffffu, tile.pos + token, who),
+                                __shfl_sync(0xffffffffu, h, who));
+            }
+        }
+    }
 }
 
 template <bool F16>
-__global__ void __launch_bounds__(256) attn_rows_kernel(PrefillArgs a, long long units) {
-    const long long u = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (blockIdx.x == 0 && threadIdx.x < 32 && a.cu_q &&
-        !(warp_offsets_ok(a.cu_q, a.n_seqs, a.t_q) && warp_offsets_ok(a.cu_k, a.n_seqs, a.t_k)) &&
-        threadIdx.x == 0)
-        atomicOr(&g_attn_status, STATUS_BAD_CU_SEQLENS);
-    if (u >= units) return;
-    const long long row = u / a.heads;
-    const int h = (int)(u - row * a.heads);
-    const int n = a.cu_q ? warp_find_last(a.n_seqs, row, [&](int i) { return __ldg(a.cu_q + i); })
-                         : (int)(row / a.t_q);
-    Span s;
-    if (!sequence_span(a, n, s) || row < s.q0 || row >= s.q0 + s.lq) return;
-    attend_row<F16>(a, s, (int)(row - s.q0), h);
+__global__ void __launch_bounds__(kThreads, 1)
+attn_prefill_kernel(PrefillArgs a, const __grid_constant__ CUtensorMap mq,
+                    const __grid_constant__ CUtensorMap mk,
+                    const __grid_constant__ CUtensorMap mv) {
+    extern __shared__ __align__(1024) unsigned char sm[];
+    Shared& sh = *reinterpret_cast<Shared*>(sm + kSharedOff);
+    const int warp = threadIdx.x >> 5;
+    if (smem_u32(sm) & 1023u) {  // the swizzle goes by address bits
+        if (threadIdx.x == 0) atomicOr(&g_attn_status, STATUS_SMEM_ALIGN);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        sh.stop = 0;
+        for (int i = 0; i < kStages; ++i) mbar_init(&sh.kv_full[i], 1), mbar_init(&sh.kv_empty[i], 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&sh.q_full[t], 1);
+            mbar_init(&sh.q_empty[t], 1);
+            mbar_init(&sh.s_full[t], 1);
+            mbar_init(&sh.p_full[t], 4);
+            mbar_init(&sh.o_full[t], 1);
+            mbar_init(&sh.o_empty[t], 4);
+            mbar_init(&sh.stat_full[t], 4);
+        }
+        for (int i = 0; i < kRing; ++i) mbar_init(&sh.item_full[i], 1), mbar_init(&sh.item_empty[i], 13);
+        fence_mbar_init();
+        prefetch_tmap(&mq);
+        prefetch_tmap(&mk);
+        prefetch_tmap(&mv);
+    }
+    if (warp == 12) tmem_alloc(&sh.tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_wait();
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegSoftmax));
+        softmax_role<F16>(a, sh, warp >> 2);
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegWriter));
+        write_role<F16>(a, sh);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegOther));
+        if (warp == 12) {
+            if ((threadIdx.x & 31) == 0) mma_role<F16>(a, sh, sm);
+            __syncwarp();
+        } else if (warp == 13) {
+            load_role(a, sh, sm, &mq, &mk, &mv);
+        } else if (warp == 14 && !a.list && a.cu_q && blockIdx.x == 0) {
+            // with a list, attn_plan_kernel looks at the offsets
+            const bool ok = warp_offsets_ok(a.cu_q, a.n_seqs, a.t_q) &&
+                            warp_offsets_ok(a.cu_k, a.n_seqs, a.t_k);
+            if (!ok && (threadIdx.x & 31) == 0) atomicOr(&g_attn_status, STATUS_BAD_CU_SEQLENS);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 12) tmem_dealloc(sh.tmem, 512);
+}
+
+// Items of a call, at most: slots of all sequences.
+inline long long slot_count(long long rows, int n_seqs, int group) {
+    return rows / (2 * (128 / group)) + n_seqs;
 }
 
 }  // namespace
@@ -128,8 +767,11 @@ using namespace kda;
 
 extern "C" size_t kda_attn_prefill_workspace_size(int64_t rows, int n_seqs, int heads,
                                                   int kv_heads) {
-    if (rows < 0 || n_seqs < 1 || heads < 1 || kv_heads < 1 || heads % kv_heads) return 0;
-    return 256;
+    if (rows < 0 || n_seqs < 1 || heads < 1 || kv_heads < 1 || heads % kv_heads ||
+        heads / kv_heads > 128)
+        return 0;
+    // the ticket counter, then 16 bytes an item
+    return 256 + 16 * (size_t)slot_count(rows, n_seqs, heads / kv_heads);
 }
 
 extern "C" kda_status kda_attn_prefill(const void* q, const void* k, const void* v, void* o,
@@ -168,21 +810,51 @@ extern "C" kda_status kda_attn_prefill(const void* q, const void* k, const void*
     if (st == KDA_OK && rows_k) st = validate_rows(fn, "k", k, k_row_stride, kv_heads);
     if (st == KDA_OK && rows_k) st = validate_rows(fn, "v", v, v_row_stride, kv_heads);
     if (st != KDA_OK) return st;
-    PrefillArgs a = {(const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, (uint16_t*)o,
-                     lse, cu_seqlens_q, cu_seqlens_k, q_row_stride, k_row_stride, v_row_stride,
-                     o_row_stride, t_q, t_k, n_seqs, heads, kv_heads, window, scale};
-    const long long units = rows_q * heads;
-    KDA_REQUIRE((units + 7) / 8 < 0x7fffffffLL, KDA_ERR_INVALID_ARG, "%s: problem too large", fn);
+    const int group = heads / kv_heads, tokens = 128 / group;
+    const long long slots = slot_count(rows_q, n_seqs, group);
+    KDA_REQUIRE(slots < 0x7fffffffLL / kv_heads, KDA_ERR_INVALID_ARG, "%s: problem too large", fn);
     const size_t need = kda_attn_prefill_workspace_size(rows_q, n_seqs, heads, kv_heads);
     KDA_REQUIRE(workspace && workspace_bytes >= need, KDA_ERR_WORKSPACE,
                 "%s: workspace of %zu B, %zu B needed", fn, workspace ? workspace_bytes : 0, need);
     KDA_REQUIRE(aligned16(workspace), KDA_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned",
                 fn);
     KDA_REQUIRE(!fault_injected(), KDA_ERR_CUDA, "%s: injected launch failure", fn);
-    const dim3 grid((unsigned)((units + 7) / 8));
-    if (in_dtype == KDA_F16)
-        attn_rows_kernel<true><<<grid, 256, 0, as_stream(stream)>>>(a, units);
-    else
-        attn_rows_kernel<false><<<grid, 256, 0, as_stream(stream)>>>(a, units);
+    const int sms = sm_count();
+    KDA_REQUIRE(sms > 0, KDA_ERR_CUDA, "%s: no device", fn);
+    const bool f16 = in_dtype == KDA_F16;
+    // without keys nothing is loaded through the K and V maps
+    const void* kb = rows_k ? k : q;
+    const void* vb = rows_k ? v : q;
+    const uint64_t k_rows = rows_k ? (uint64_t)rows_k : 1;
+    CUtensorMap mq, mk, mv;
+    KDA_REQUIRE(
+        tma_map_heads(&mq, q, heads, rows_q, q_row_stride, group, tokens, f16) &&
+            tma_map_heads(&mk, kb, rows_k ? kv_heads : heads, k_rows,
+                          rows_k ? k_row_stride : q_row_stride, 1, 128, f16) &&
+            tma_map_heads(&mv, vb, rows_k ? kv_heads : heads, k_rows,
+                          rows_k ? v_row_stride : q_row_stride, 1, 128, f16),
+        KDA_ERR_CUDA, "%s: cannot describe the inputs to the copy engine", fn);
+    // One CTA per item needs no order and no tickets: the call is one kernel.
+    const long long items = slots * kv_heads;
+    const bool direct = items <= sms;
+    int shift = 0;  // buckets of 2^shift key blocks in the plan's sort
+    while ((t_k / 128 >> shift) >= kPlanThreads) ++shift;
+    unsigned* count = static_cast<unsigned*>(workspace);
+    int4* list = reinterpret_cast<int4*>(static_cast<unsigned char*>(workspace) + 256);
+    PrefillArgs a = {(const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, (uint16_t*)o,
+                     lse, cu_seqlens_q, cu_seqlens_k, q_row_stride, k_row_stride, v_row_stride,
+                     o_row_stride, t_q, t_k, n_seqs, heads, kv_heads, window, group, tokens,
+                     scale, direct ? nullptr : list, count, (int)slots, shift};
+    auto kernel = f16 ? attn_prefill_kernel<true> : attn_prefill_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)kSmemBytes);
+    if (e != cudaSuccess) {
+        set_error("%s: cannot reserve shared memory: %s", fn, cudaGetErrorString(e));
+        return KDA_ERR_CUDA;
+    }
+    cudaStream_t s = as_stream(stream);
+    if (!direct) launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a);
+    launch_pdl(kernel, dim3((unsigned)(direct ? items : sms)), dim3(kThreads), kSmemBytes, s, a,
+               mq, mk, mv);
     return launch_result(fn);
 }

@@ -32,6 +32,14 @@ __device__ __forceinline__ uint64_t make_desc(uint32_t saddr, uint32_t lbo, uint
     return d;                 // base offset 0, relative LBO mode, swizzle none
 }
 
+// Shared-memory matrix descriptor of an operand in the 128-byte swizzle that
+// TMA writes for 64-element (128-byte) box rows.  K-major: SBO = 1024 (8 rows),
+// LBO unused; MN-major: SBO = 1024 (8 K-rows), LBO = the distance between
+// blocks of 64 elements along M or N.
+__device__ __forceinline__ uint64_t make_desc_sw128(uint32_t saddr, uint32_t lbo) {
+    return make_desc(saddr, lbo, 1024) | (uint64_t)2u << 61;
+}
+
 // Instruction descriptor: kind::tf32, FP32 accumulate, A and B K-major.
 __host__ __device__ constexpr uint32_t idesc_tf32(int M, int N) {
     return (1u << 4) | (2u << 7) | (2u << 10) | ((uint32_t)(N >> 3) << 17) |
@@ -42,6 +50,11 @@ __host__ __device__ constexpr uint32_t idesc_tf32(int M, int N) {
 // B K-major.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// The same with A and B both FP16 or both BF16, and B K-major or MN-major.
+__host__ __device__ constexpr uint32_t idesc_16(int M, int N, bool bf16, bool b_mn_major) {
+    return idesc_f16(M, N) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn_major ? 1u << 16 : 0u);
 }
 
 // FP32 -> FP16, round to nearest even (the 16 bits of the result).
@@ -110,6 +123,10 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
         if (done) return true;
     }
     return false;
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // ---------------------------------------------------------------- TMEM

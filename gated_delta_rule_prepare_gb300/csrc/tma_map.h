@@ -62,6 +62,24 @@ inline bool tma_map_bf16_groups8(CUtensorMap* m, const void* base, uint64_t cols
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 16-bit [rows][heads][128] with a row pitch of `pitch_elems` elements, in boxes
+// of 64 channels x box_heads x box_rows: box rows of 128 bytes, written to
+// shared memory in the 128-byte swizzle.  Rows past the end read as zero.
+inline bool tma_map_heads(CUtensorMap* m, const void* base, uint64_t heads, uint64_t rows,
+                          uint64_t pitch_elems, uint32_t box_heads, uint32_t box_rows,
+                          bool f16) {
+    auto fn = tma_encode_fn();
+    if (!fn) return false;
+    cuuint64_t gdim[3] = {128, heads, rows};
+    cuuint64_t gstride[2] = {256, pitch_elems * 2};
+    cuuint32_t box[3] = {64, box_heads, box_rows};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+              const_cast<void*>(base), gdim, gstride, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // FP32 [rows][cols] with a row pitch of `pitch_elems` elements, in boxes of
 // box_cols x box_rows without swizzle (row-major in shared memory).
 inline bool tma_map_f32(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
