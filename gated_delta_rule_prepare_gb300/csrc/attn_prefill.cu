@@ -217,7 +217,7 @@ constexpr int kRing = 4;                   // items between the TMA warp and the
 constexpr uint32_t kTmemO = 256;           // S0, S1, O0, O1: 128 columns each
 // Registers a thread: softmax (2 x 128 threads), writers (128), the rest (128).
 // Together what the launch has: 4 * 128.
-constexpr int kRegSoftmax = 176, kRegWriter = 96, kRegOther = 64;
+constexpr int kRegSoftmax = 176, kRegWriter = 64, kRegOther = 96;
 static_assert(2 * kRegSoftmax + kRegWriter + kRegOther <= 512, "registers of the launch");
 // The running maximum is left behind by up to 2^kLag before O is rescaled: a
 // weight is then at most 2^kLag, the sum and O carry the same factor and the
@@ -236,7 +236,7 @@ struct Item {
 struct Shared {
     uint64_t kv_full[kStages], kv_empty[kStages];
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2], p_full[2];
+    uint64_t s_full[2], p_full[2][2];  // P: keys 0..63 of the block, keys 64..127
     uint64_t o_full[2], o_empty[2], stat_full[2];
     uint64_t item_full[kRing], item_empty[kRing];
     Item item[kRing];
@@ -368,118 +368,137 @@ __device__ __forceinline__ void load_role(const PrefillArgs& a, Shared& sh, unsi
     }
 }
 
-// The thread that issues the MMAs.  Per block and tile: O += P V, then S of the
+// One lane of the warp, always the same one.  The issuing warp runs its code
+// together and only the MMAs and commits are the elected lane's, so that
+// descriptors stay in uniform registers (from a branch of lane 0 alone each was
+// moved there again).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile(
+        "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(yes));
+    return yes != 0;
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// The warp that issues the MMAs.  Per block and tile: O += P V, then S of the
 // next block, which may be the next item's first.  MMAs of one CTA execute in
 // the order of their issue, so S's write over P needs no wait of its own.
 template <bool F16>
 __device__ __forceinline__ void mma_role(const PrefillArgs& a, Shared& sh, unsigned char* sm) {
     constexpr uint32_t kQK = idesc_16(128, 128, !F16, false);
     constexpr uint32_t kPV = idesc_16(128, 128, !F16, true);
-    const uint32_t tmem = sh.tmem;
+    constexpr uint64_t kTile = kTileBytes >> 4;  // in a descriptor's units
+    const bool lane0 = (threadIdx.x & 31) == 0;
+    const uint32_t tmem = uniform(sh.tmem);
+    const uint32_t base = uniform(smem_u32(sm));
+    const uint64_t k_major = make_desc_sw128(base, 16);
+    const uint64_t mn_major = make_desc_sw128(base, kTileBytes / 2);
     int stage = 0;  // of the next K or V to be used
-    uint32_t phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0}, o_phase[2] = {0, 0};
+    uint32_t phase = 0, q_phase = 0, p_phase = 0, o_phase = 0;  // bit t: tile t
     int ring = 0;
     uint32_t ring_phase = 0;
-    struct Work {  // key blocks of the tiles and of both
-        Blocks t[2], b;
-        bool any;
+    struct Work {  // key blocks of the tiles; lo == hi: no more
+        int lo0, hi0, lo1, hi1;
+        __device__ int lo() const { return hi0 <= lo0 ? lo1 : hi1 <= lo1 ? lo0 : min(lo0, lo1); }
+        __device__ int hi() const { return hi0 <= lo0 ? hi1 : hi1 <= lo1 ? hi0 : max(hi0, hi1); }
     };
     // the next item that has key blocks at all
     auto next_item = [&](Work& w) {
         for (;;) {
-            w.any = false;
-            if (!wait(sh, &sh.item_full[ring], ring_phase)) return false;
+            if (!wait_warp(sh, &sh.item_full[ring], ring_phase)) return false;
             const Item it = sh.item[ring];
-            mbar_arrive(&sh.item_empty[ring]);
+            __syncwarp();
+            if (lane0) mbar_arrive(&sh.item_empty[ring]);
             if (++ring == kRing) ring = 0, ring_phase ^= 1;
-            if (it.head < 0) return true;
             const Tile x = tile_of(a, it.e, 0), y = tile_of(a, it.e, 1);
-            w.t[0] = {x.lo, x.hi};
-            w.t[1] = {y.lo, y.hi};
-            w.b = blocks_of(x, y);
-            if (w.b.hi > w.b.lo) {
-                w.any = true;
-                return true;
-            }
+            const bool end = uniform(it.head) < 0;
+            w.lo0 = uniform(x.lo);
+            w.hi0 = end ? w.lo0 : uniform(x.hi);
+            w.lo1 = uniform(y.lo);
+            w.hi1 = end ? w.lo1 : uniform(y.hi);
+            if (end || w.hi() > w.lo()) return true;
         }
     };
-    auto active = [](const Work& w, int t, int j) { return j >= w.t[t].lo && j < w.t[t].hi; };
-    auto qk = [&](const Work& w, int t, int j, int k_stage) {
-        if (j == w.t[t].lo) {
-            if (!wait(sh, &sh.q_full[t], q_phase[t])) return false;
-            q_phase[t] ^= 1;
+    auto qk = [&](int t, bool first, bool last, int k_stage) {
+        if (first) {
+            if (!wait_warp(sh, &sh.q_full[t], q_phase >> t & 1)) return false;
+            q_phase ^= 1u << t;
         }
         tc_fence_after();
-        const uint32_t qa = smem_u32(sm) + t * kTileBytes;
-        const uint32_t kb = smem_u32(sm) + (2 + k_stage) * kTileBytes;
+        const uint64_t qd = k_major + t * kTile, kd = k_major + (2 + k_stage) * kTile;
+        if (elect_one()) {
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
-            const uint32_t off = (s >> 2) * (kTileBytes / 2) + (s & 3) * 32;
-            mma_f16(tmem + t * 128, make_desc_sw128(qa + off, 16), make_desc_sw128(kb + off, 16),
-                    kQK, s > 0);
+            for (int s = 0; s < 8; ++s) {
+                const uint64_t off = (s >> 2) * (kTile / 2) + (s & 3) * 2;
+                mma_f16(tmem + t * 128, qd + off, kd + off, kQK, s > 0);
+            }
+            mma_commit(&sh.s_full[t]);
+            if (last) mma_commit(&sh.q_empty[t]);
         }
-        mma_commit(&sh.s_full[t]);
-        if (j == w.t[t].hi - 1) mma_commit(&sh.q_empty[t]);
+        __syncwarp();
         return true;
     };
-    auto pv = [&](const Work& w, int t, int j, int v_stage) {
-        if (j == w.t[t].lo) {
-            if (!wait(sh, &sh.o_empty[t], o_phase[t] ^ 1)) return false;
-            o_phase[t] ^= 1;
+    auto pv = [&](int t, bool first, bool last, int v_stage) {
+        if (first) {
+            if (!wait_warp(sh, &sh.o_empty[t], (o_phase >> t & 1) ^ 1)) return false;
+            o_phase ^= 1u << t;
         }
-        if (!wait(sh, &sh.p_full[t], p_phase[t])) return false;
-        p_phase[t] ^= 1;
-        tc_fence_after();
-        const uint32_t vb = smem_u32(sm) + (2 + v_stage) * kTileBytes;
+        // the first half of the keys while the softmax finishes the second
+        const uint64_t vd = mn_major + (2 + v_stage) * kTile;
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
-            mma_f16_ta(tmem + kTmemO + t * 128, tmem + t * 128 + 8 * s,
-                       make_desc_sw128(vb + s * 2048, kTileBytes / 2), kPV,
-                       j > w.t[t].lo || s > 0);
-        if (j == w.t[t].hi - 1) mma_commit(&sh.o_full[t]);
+        for (int half = 0; half < 2; ++half) {
+            if (!wait_warp(sh, &sh.p_full[t][half], p_phase >> t & 1)) return false;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int s = 4 * half; s < 4 * half + 4; ++s)
+                    mma_f16_ta(tmem + kTmemO + t * 128, tmem + t * 128 + 8 * s, vd + s * 128, kPV,
+                               !first || s > 0);
+                if (half == 1 && last) mma_commit(&sh.o_full[t]);
+            }
+        }
+        p_phase ^= 1u << t;
+        __syncwarp();
         return true;
     };
     auto take = [&](int& s) {  // the next stage of the ring, once it is filled
         s = stage;
-        if (!wait(sh, &sh.kv_full[stage], phase)) return false;
+        if (!wait_warp(sh, &sh.kv_full[stage], phase)) return false;
         if (++stage == kStages) stage = 0, phase ^= 1;
         return true;
     };
     Work cur, nxt;
-    if (!next_item(cur) || !cur.any) return;
+    if (!next_item(cur) || cur.hi() <= cur.lo()) return;
     int ks, vs;
     if (!take(ks)) return;
-    for (int t = 0; t < 2; ++t)
-        if (active(cur, t, cur.b.lo) && !qk(cur, t, cur.b.lo, ks)) return;
-    mma_commit(&sh.kv_empty[ks]);
+    {
+        const int j = cur.lo();
+        if (j >= cur.lo0 && j < cur.hi0 && !qk(0, true, j == cur.hi0 - 1, ks)) return;
+        if (j >= cur.lo1 && j < cur.hi1 && !qk(1, true, j == cur.hi1 - 1, ks)) return;
+    }
+    if (elect_one()) mma_commit(&sh.kv_empty[ks]);
     for (;;) {
-        bool more = true;
-        for (int j = cur.b.lo; j < cur.b.hi; ++j) {
-            const bool last = j + 1 == cur.b.hi;
+        const int hi = cur.hi();
+        for (int j = cur.lo(); j < hi; ++j) {
             if (!take(vs)) return;
-            const Work* n = &cur;
+            nxt = cur;
             int jn = j + 1;
-            if (last) {
+            if (jn == hi) {
                 if (!next_item(nxt)) return;
-                n = &nxt;
-                jn = nxt.b.lo;
-                more = nxt.any;
+                jn = nxt.lo();
             }
-            bool have_k = false;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (active(cur, t, j) && !pv(cur, t, j, vs)) return;
-                if (t == 1) mma_commit(&sh.kv_empty[vs]);
-                if (more && active(*n, t, jn)) {
-                    if (!have_k && !take(ks)) return;
-                    have_k = true;
-                    if (!qk(*n, t, jn, ks)) return;
-                }
-            }
-            if (have_k) mma_commit(&sh.kv_empty[ks]);
+            const bool k0 = jn >= nxt.lo0 && jn < nxt.hi0, k1 = jn >= nxt.lo1 && jn < nxt.hi1;
+            if (j >= cur.lo0 && j < cur.hi0 && !pv(0, j == cur.lo0, j == cur.hi0 - 1, vs)) return;
+            if ((k0 || k1) && !take(ks)) return;
+            if (k0 && !qk(0, jn == nxt.lo0, jn == nxt.hi0 - 1, ks)) return;
+            if (j >= cur.lo1 && j < cur.hi1 && !pv(1, j == cur.lo1, j == cur.hi1 - 1, vs)) return;
+            if (elect_one()) mma_commit(&sh.kv_empty[vs]);
+            if (k1 && !qk(1, jn == nxt.lo1, jn == nxt.hi1 - 1, ks)) return;
+            if ((k0 || k1) && elect_one()) mma_commit(&sh.kv_empty[ks]);
         }
-        if (!more) return;
         cur = nxt;
+        if (cur.hi() <= cur.lo()) return;
     }
 }
 
@@ -570,11 +589,11 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, i
                     p[x] = F16 ? pack_f16x2(y[0], y[1]) : pack_bf16x2(y[0], y[1]);
                 }
                 tmem_st32u(s_addr + 32 * half, p);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_full[t][half]);
             }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_full[t]);
             float2 sum[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum[i] = make_float2(s[i][0], s[i][1]);
@@ -633,15 +652,15 @@ __device__ __forceinline__ void write_role(const PrefillArgs& a, Shared& sh) {
             const float inv = empty ? 0.f : 1.f / l;
             float poison = 0.f;  // NaN once any value is not finite
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-                float o[32];
+            for (int i = 0; i < 8; ++i) {
+                float o[16];
                 if (any) {
-                    tmem_ld32(row_addr + t * 128 + 32 * i, o);
+                    tmem_ld16(row_addr + t * 128 + 16 * i, o);
                     tmem_ld_wait();
                 }
-                uint32_t u[16];
+                uint32_t u[8];
 #pragma unroll
-                for (int x = 0; x < 16; ++x) {
+                for (int x = 0; x < 8; ++x) {
                     const float y0 = empty ? 0.f : o[2 * x] * inv;
                     const float y1 = empty ? 0.f : o[2 * x + 1] * inv;
                     poison = fmaf(y0, 0.f, poison);
@@ -650,8 +669,8 @@ __device__ __forceinline__ void write_role(const PrefillArgs& a, Shared& sh) {
                 }
                 if (mine) {
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        *reinterpret_cast<uint4*>(dst + 32 * i + 8 * x) =
+                    for (int x = 0; x < 2; ++x)
+                        *reinterpret_cast<uint4*>(dst + 16 * i + 8 * x) =
                             make_uint4(u[4 * x], u[4 * x + 1], u[4 * x + 2], u[4 * x + 3]);
                 }
             }
@@ -695,7 +714,8 @@ attn_prefill_kernel(PrefillArgs a, const __grid_constant__ CUtensorMap mq,
             mbar_init(&sh.q_full[t], 1);
             mbar_init(&sh.q_empty[t], 1);
             mbar_init(&sh.s_full[t], 1);
-            mbar_init(&sh.p_full[t], 4);
+            mbar_init(&sh.p_full[t][0], 4);
+            mbar_init(&sh.p_full[t][1], 4);
             mbar_init(&sh.o_full[t], 1);
             mbar_init(&sh.o_empty[t], 4);
             mbar_init(&sh.stat_full[t], 4);
@@ -720,8 +740,7 @@ attn_prefill_kernel(PrefillArgs a, const __grid_constant__ CUtensorMap mq,
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegOther));
         if (warp == 12) {
-            if ((threadIdx.x & 31) == 0) mma_role<F16>(a, sh, sm);
-            __syncwarp();
+            mma_role<F16>(a, sh, sm);
         } else if (warp == 13) {
             load_role(a, sh, sm, &mq, &mk, &mv);
         } else if (warp == 14 && !a.list && a.cu_q && blockIdx.x == 0) {
