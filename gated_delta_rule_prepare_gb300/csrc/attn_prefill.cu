@@ -36,6 +36,7 @@ using namespace tc;
 
 __device__ unsigned g_attn_status = 0;
 
+struct Redo;
 struct PrefillArgs {
     const uint16_t *q, *k, *v;
     uint16_t* o;
@@ -47,6 +48,7 @@ struct PrefillArgs {
     float scale;
     int4* list;       // sorted entries; null: the slots themselves, one item per CTA
     unsigned* count;  // entries in the list, then the ticket counter
+    Redo* redo;  // [item][tile][warp]
     int slots, bucket_shift;
 };
 
@@ -70,6 +72,15 @@ __device__ __forceinline__ bool sequence_span(const PrefillArgs& a, int n, Span&
 // negative).  Keys of the sequence end at its last query's position.
 struct Entry {
     int row, tokens, k0, pos;
+};
+
+// 32 rows of a tile, some of them (bits of `rows`) to be done again, and the
+// record of the same CTA before it.  One place per item, tile and warp.
+struct Redo {
+    Entry e;
+    int head;
+    unsigned rows;
+    int before;
 };
 
 // Slots number the items of all sequences: sequence n, whose queries start at
@@ -164,7 +175,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(PrefillArgs a) 
 // One row on the CUDA cores by one warp, 4 channels a lane, touching only the
 // keys that the row sees.  The tensor cores multiply a masked key's weight 0
 // with its value, which gives NaN where the value is infinite or NaN; rows that
-// come out so are done again here.  Not a path for ordinary inputs.
+// come out so are done again here (their sums are right: a masked key adds
+// nothing to those).  Not a path for ordinary inputs.
 template <bool F16>
 __device__ __noinline__ void attend_row(const PrefillArgs& a, long long row, long long k0, int p,
                                         int h) {
@@ -205,8 +217,6 @@ __device__ __noinline__ void attend_row(const PrefillArgs& a, long long row, lon
     const float r = l == 0.f ? 0.f : 1.f / l;
     const uint2 out = make_uint2(narrow2<F16>(o.x * r, o.y * r), narrow2<F16>(o.z * r, o.w * r));
     *reinterpret_cast<uint2*>(a.o + row * a.o_stride + h * D + 4 * lane) = out;
-    if (a.lse && lane == 0)
-        a.lse[row * a.heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -217,7 +227,7 @@ constexpr int kRing = 4;                   // items between the TMA warp and the
 constexpr uint32_t kTmemO = 256;           // S0, S1, O0, O1: 128 columns each
 // Registers a thread: softmax (2 x 128 threads), writers (128), the rest (128).
 // Together what the launch has: 4 * 128.
-constexpr int kRegSoftmax = 176, kRegWriter = 64, kRegOther = 96;
+constexpr int kRegSoftmax = 184, kRegWriter = 72, kRegOther = 72;
 static_assert(2 * kRegSoftmax + kRegWriter + kRegOther <= 512, "registers of the launch");
 // The running maximum is left behind by up to 2^kLag before O is rescaled: a
 // weight is then at most 2^kLag, the sum and O carry the same factor and the
@@ -230,19 +240,22 @@ constexpr float kLift = F16 ? 7.f : 0.f;
 
 struct Item {
     Entry e;
-    int head;  // KV head; negative: no more items
+    int head;   // KV head; negative: no more items
+    int index;  // of all the call's items
 };
 
 struct Shared {
     uint64_t kv_full[kStages], kv_empty[kStages];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2][2];  // P: keys 0..63 of the block, keys 64..127
-    uint64_t o_full[2], o_empty[2], stat_full[2];
+    uint64_t turn[2];
+    uint64_t o_full[2], o_empty[2], sum_full[2];
     uint64_t item_full[kRing], item_empty[kRing];
     Item item[kRing];
-    float2 stat[2][128];  // a finished row's reference maximum (raw score) and sum
+    float sum[2][128];   // finished rows' sums of weights
     uint32_t tmem;
     int stop;  // a wait gave up: everybody leaves
+    int redo;  // this CTA's last record of rows to be done again, or -1
 };
 constexpr uint32_t kSharedOff = (2 + kStages) * kTileBytes;
 constexpr uint32_t kSmemBytes = kSharedOff + sizeof(Shared);
@@ -313,11 +326,13 @@ __device__ __forceinline__ void load_role(const PrefillArgs& a, Shared& sh, unsi
                 const int4 v = __ldcg(a.list + e);
                 it.e = {v.x, v.y, v.z, v.w};
                 it.head = (int)(x - e * a.kv_heads);
+                it.index = (int)x;
             }
         } else if (round == 0) {
             const int slot = blockIdx.x / a.kv_heads;
             const int n = warp_find_last(a.n_seqs, slot, [&](int i) { return first_slot(a, i); });
             if (slot_entry(a, n, slot, it.e)) it.head = blockIdx.x - slot * a.kv_heads;
+            it.index = blockIdx.x;
         }
         if (lane == 0) {
             go = wait(sh, &sh.item_empty[ring], ring_phase ^ 1);
@@ -381,124 +396,122 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-// The warp that issues the MMAs.  Per block and tile: O += P V, then S of the
-// next block, which may be the next item's first.  MMAs of one CTA execute in
+// The warp that issues tile t's MMAs: per block S = Q K^T, and O += P V once
+// the softmax has written P.  Each tile has a warp of its own, so that the
+// tensor cores always have the other tile's products while one waits (with one
+// warp for both, what lies between two products stalled them: 1443 against
+// 16xx TFLOP/s at 8192 tokens, 32 heads over 8).  MMAs of one warp execute in
 // the order of their issue, so S's write over P needs no wait of its own.
-template <bool F16>
+template <bool F16, int t>
 __device__ __forceinline__ void mma_role(const PrefillArgs& a, Shared& sh, unsigned char* sm) {
     constexpr uint32_t kQK = idesc_16(128, 128, !F16, false);
     constexpr uint32_t kPV = idesc_16(128, 128, !F16, true);
     constexpr uint64_t kTile = kTileBytes >> 4;  // in a descriptor's units
     const bool lane0 = (threadIdx.x & 31) == 0;
-    const uint32_t tmem = uniform(sh.tmem);
+    const uint32_t s_tmem = uniform(sh.tmem) + t * 128, o_tmem = s_tmem + kTmemO;
     const uint32_t base = uniform(smem_u32(sm));
-    const uint64_t k_major = make_desc_sw128(base, 16);
-    const uint64_t mn_major = make_desc_sw128(base, kTileBytes / 2);
-    int stage = 0;  // of the next K or V to be used
-    uint32_t phase = 0, q_phase = 0, p_phase = 0, o_phase = 0;  // bit t: tile t
-    int ring = 0;
-    uint32_t ring_phase = 0;
-    struct Work {  // key blocks of the tiles; lo == hi: no more
-        int lo0, hi0, lo1, hi1;
-        __device__ int lo() const { return hi0 <= lo0 ? lo1 : hi1 <= lo1 ? lo0 : min(lo0, lo1); }
-        __device__ int hi() const { return hi0 <= lo0 ? hi1 : hi1 <= lo1 ? hi0 : max(hi0, hi1); }
-    };
-    // the next item that has key blocks at all
-    auto next_item = [&](Work& w) {
-        for (;;) {
-            if (!wait_warp(sh, &sh.item_full[ring], ring_phase)) return false;
-            const Item it = sh.item[ring];
-            __syncwarp();
-            if (lane0) mbar_arrive(&sh.item_empty[ring]);
-            if (++ring == kRing) ring = 0, ring_phase ^= 1;
-            const Tile x = tile_of(a, it.e, 0), y = tile_of(a, it.e, 1);
-            const bool end = uniform(it.head) < 0;
-            w.lo0 = uniform(x.lo);
-            w.hi0 = end ? w.lo0 : uniform(x.hi);
-            w.lo1 = uniform(y.lo);
-            w.hi1 = end ? w.lo1 : uniform(y.hi);
-            if (end || w.hi() > w.lo()) return true;
-        }
-    };
-    auto qk = [&](int t, bool first, bool last, int k_stage) {
-        if (first) {
-            if (!wait_warp(sh, &sh.q_full[t], q_phase >> t & 1)) return false;
-            q_phase ^= 1u << t;
-        }
-        tc_fence_after();
-        const uint64_t qd = k_major + t * kTile, kd = k_major + (2 + k_stage) * kTile;
-        if (elect_one()) {
-#pragma unroll
-            for (int s = 0; s < 8; ++s) {
-                const uint64_t off = (s >> 2) * (kTile / 2) + (s & 3) * 2;
-                mma_f16(tmem + t * 128, qd + off, kd + off, kQK, s > 0);
-            }
-            mma_commit(&sh.s_full[t]);
-            if (last) mma_commit(&sh.q_empty[t]);
-        }
-        __syncwarp();
-        return true;
-    };
-    auto pv = [&](int t, bool first, bool last, int v_stage) {
-        if (first) {
-            if (!wait_warp(sh, &sh.o_empty[t], (o_phase >> t & 1) ^ 1)) return false;
-            o_phase ^= 1u << t;
-        }
-        // the first half of the keys while the softmax finishes the second
-        const uint64_t vd = mn_major + (2 + v_stage) * kTile;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (!wait_warp(sh, &sh.p_full[t][half], p_phase >> t & 1)) return false;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-                for (int s = 4 * half; s < 4 * half + 4; ++s)
-                    mma_f16_ta(tmem + kTmemO + t * 128, tmem + t * 128 + 8 * s, vd + s * 128, kPV,
-                               !first || s > 0);
-                if (half == 1 && last) mma_commit(&sh.o_full[t]);
-            }
-        }
-        p_phase ^= 1u << t;
-        __syncwarp();
-        return true;
-    };
-    auto take = [&](int& s) {  // the next stage of the ring, once it is filled
-        s = stage;
-        if (!wait_warp(sh, &sh.kv_full[stage], phase)) return false;
-        if (++stage == kStages) stage = 0, phase ^= 1;
-        return true;
-    };
-    Work cur, nxt;
-    if (!next_item(cur) || cur.hi() <= cur.lo()) return;
-    int ks, vs;
-    if (!take(ks)) return;
-    {
-        const int j = cur.lo();
-        if (j >= cur.lo0 && j < cur.hi0 && !qk(0, true, j == cur.hi0 - 1, ks)) return;
-        if (j >= cur.lo1 && j < cur.hi1 && !qk(1, true, j == cur.hi1 - 1, ks)) return;
-    }
-    if (elect_one()) mma_commit(&sh.kv_empty[ks]);
+    const uint64_t qd = make_desc_sw128(base, 16) + t * kTile;
+    const uint64_t k_major = make_desc_sw128(base, 16) + 2 * kTile;
+    const uint64_t mn_major = make_desc_sw128(base, kTileBytes / 2) + 2 * kTile;
+    int stage = 0, ring = 0;
+    uint32_t phase = 0, ring_phase = 0, q_phase = 0, p_phase = 0, o_phase = 0, turn_phase = t ^ 1;
     for (;;) {
-        const int hi = cur.hi();
-        for (int j = cur.lo(); j < hi; ++j) {
-            if (!take(vs)) return;
-            nxt = cur;
-            int jn = j + 1;
-            if (jn == hi) {
-                if (!next_item(nxt)) return;
-                jn = nxt.lo();
+        if (!wait_warp(sh, &sh.item_full[ring], ring_phase)) return;
+        const Item it = sh.item[ring];
+        __syncwarp();
+        if (lane0) mbar_arrive(&sh.item_empty[ring]);
+        if (++ring == kRing) ring = 0, ring_phase ^= 1;
+        if (uniform(it.head) < 0) return;
+        const Tile x = tile_of(a, it.e, 0), y = tile_of(a, it.e, 1);
+        const Blocks b = blocks_of(x, y);
+        const int b_hi = uniform(b.hi), lo = uniform(t ? y.lo : x.lo), hi = uniform(t ? y.hi : x.hi);
+        const int b_lo = uniform(b.lo);
+        if (b_hi <= b_lo) continue;
+        // S of block j; the stage is filled and it is this tile's turn
+        auto qk = [&](int j) {
+            const bool active = j >= lo && j < hi;
+            tc_fence_after();
+            const uint64_t kd = k_major + stage * kTile;
+            if (active) {
+                if (elect_one()) {
+#pragma unroll
+                    for (int s = 0; s < 8; ++s) {
+                        const uint64_t off = (s >> 2) * (kTile / 2) + (s & 3) * 2;
+                        mma_f16(s_tmem, qd + off, kd + off, kQK, s > 0);
+                    }
+                    mma_commit(&sh.s_full[t]);
+                    mma_commit(&sh.kv_empty[stage]);
+                    if (j == hi - 1) mma_commit(&sh.q_empty[t]);
+                }
+            } else if (lane0) {
+                mbar_arrive(&sh.kv_empty[stage]);
             }
-            const bool k0 = jn >= nxt.lo0 && jn < nxt.hi0, k1 = jn >= nxt.lo1 && jn < nxt.hi1;
-            if (j >= cur.lo0 && j < cur.hi0 && !pv(0, j == cur.lo0, j == cur.hi0 - 1, vs)) return;
-            if ((k0 || k1) && !take(ks)) return;
-            if (k0 && !qk(0, jn == nxt.lo0, jn == nxt.hi0 - 1, ks)) return;
-            if (j >= cur.lo1 && j < cur.hi1 && !pv(1, j == cur.lo1, j == cur.hi1 - 1, vs)) return;
-            if (elect_one()) mma_commit(&sh.kv_empty[vs]);
-            if (k1 && !qk(1, jn == nxt.lo1, jn == nxt.hi1 - 1, ks)) return;
-            if ((k0 || k1) && elect_one()) mma_commit(&sh.kv_empty[ks]);
+            __syncwarp();
+            if (++stage == kStages) stage = 0, phase ^= 1;
+        };
+        auto my_turn = [&] {
+            if (!wait_warp(sh, &sh.turn[t], turn_phase)) return false;
+            turn_phase ^= 1;
+            return true;
+        };
+        auto pass_turn = [&] {
+            __syncwarp();
+            if (lane0) mbar_arrive(&sh.turn[t ^ 1]);
+        };
+        if (!wait_warp(sh, &sh.kv_full[stage], phase)) return;
+        if (b_lo == lo && lo < hi) {
+            if (!wait_warp(sh, &sh.q_full[t], q_phase)) return;
+            q_phase ^= 1;
         }
-        cur = nxt;
-        if (cur.hi() <= cur.lo()) return;
+        if (!my_turn()) return;
+        qk(b_lo);
+        pass_turn();
+        for (int j = b_lo; j < b_hi; ++j) {
+            const bool active = j >= lo && j < hi, more = j + 1 < b_hi;
+            // everything to wait for comes before the turn
+            if (!wait_warp(sh, &sh.kv_full[stage], phase)) return;
+            const int v_stage = stage;
+            if (++stage == kStages) stage = 0, phase ^= 1;
+            if (more && !wait_warp(sh, &sh.kv_full[stage], phase)) return;
+            if (more && j + 1 == lo && lo < hi) {
+                if (!wait_warp(sh, &sh.q_full[t], q_phase)) return;
+                q_phase ^= 1;
+            }
+            if (active) {
+                if (j == lo) {
+                    if (!wait_warp(sh, &sh.o_empty[t], o_phase ^ 1)) return;
+                    o_phase ^= 1;
+                }
+                if (!wait_warp(sh, &sh.p_full[t][0], p_phase)) return;
+            }
+            if (!my_turn()) return;
+            if (active) {
+                const uint64_t vd = mn_major + v_stage * kTile;
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    if (part && !wait_warp(sh, &sh.p_full[t][1], p_phase)) return;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int s = 4 * part + i;
+                            mma_f16_ta(o_tmem, s_tmem + 8 * s, vd + s * 128, kPV,
+                                       j > lo || part || i);
+                        }
+                        if (part) {
+                            mma_commit(&sh.kv_empty[v_stage]);
+                            if (j == hi - 1) mma_commit(&sh.o_full[t]);
+                        }
+                    }
+                    __syncwarp();
+                }
+                p_phase ^= 1;
+            } else if (lane0) {
+                mbar_arrive(&sh.kv_empty[v_stage]);
+            }
+            if (more) qk(j + 1);
+            pass_turn();
+        }
     }
 }
 
@@ -608,9 +621,14 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, i
         // once the writers have read the last item's
         if (!wait_warp(sh, &sh.o_empty[t], o_phase ^ 1)) return;
         o_phase ^= 1;
-        sh.stat[t][r] = make_float2(m, l);
+        sh.sum[t][r] = l;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.stat_full[t]);
+        if (lane == 0) mbar_arrive(&sh.sum_full[t]);
+        if (a.lse && token < tile.tokens) {
+            const long long row = (long long)it.e.row + t * a.tile_tokens + token;
+            a.lse[row * a.heads + it.head * a.group + r - token * a.group] =
+                l == 0.f ? -INFINITY : fmaf(m, a.scale, (log2f(l) - kLift<F16>) * kLn2);
+        }
     }
 }
 
@@ -638,12 +656,10 @@ __device__ __forceinline__ void write_role(const PrefillArgs& a, Shared& sh) {
             const long long row = (long long)it.e.row + t * a.tile_tokens + token;
             uint16_t* dst = a.o + row * a.o_stride + h * D;
             const bool any = tile.hi > tile.lo;
-            float m = -INFINITY, l = 0.f;
+            float l = 0.f;
             if (any) {
-                if (!wait_warp(sh, &sh.stat_full[t], phase[t])) return;
-                const float2 st = sh.stat[t][r];
-                m = st.x;
-                l = st.y;
+                if (!wait_warp(sh, &sh.sum_full[t], phase[t])) return;
+                l = sh.sum[t][r];
                 if (!wait_warp(sh, &sh.o_full[t], phase[t])) return;
                 phase[t] ^= 1;
                 tc_fence_after();
@@ -679,17 +695,12 @@ __device__ __forceinline__ void write_role(const PrefillArgs& a, Shared& sh) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.o_empty[t]);
             }
-            if (mine && a.lse)
-                a.lse[row * a.heads + h] =
-                    empty ? -INFINITY : fmaf(m, a.scale, (log2f(l) - kLift<F16>) * kLn2);
+            if (!any && mine && a.lse) a.lse[row * a.heads + h] = -INFINITY;
             // a sum that is NaN comes from a key that the row sees
-            unsigned again = __ballot_sync(0xffffffffu, mine && poison != poison && l == l);
-            while (again) {
-                const int who = __ffs(again) - 1;
-                again &= again - 1;
-                attend_row<F16>(a, __shfl_sync(0xffffffffu, row, who), it.e.k0,
-                                __shfl_sync(0xffffffffu, tile.pos + token, who),
-                                __shfl_sync(0xffffffffu, h, who));
+            const unsigned again = __ballot_sync(0xffffffffu, mine && poison != poison && l == l);
+            if (again && lane == 0) {
+                const int at = (it.index * 2 + t) * 4 + (r >> 5);
+                a.redo[at] = {it.e, it.head, again, atomicExch(&sh.redo, at)};
             }
         }
     }
@@ -709,18 +720,20 @@ attn_prefill_kernel(PrefillArgs a, const __grid_constant__ CUtensorMap mq,
     }
     if (threadIdx.x == 0) {
         sh.stop = 0;
-        for (int i = 0; i < kStages; ++i) mbar_init(&sh.kv_full[i], 1), mbar_init(&sh.kv_empty[i], 1);
+        sh.redo = -1;
+        for (int i = 0; i < kStages; ++i) mbar_init(&sh.kv_full[i], 1), mbar_init(&sh.kv_empty[i], 2);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sh.q_full[t], 1);
             mbar_init(&sh.q_empty[t], 1);
             mbar_init(&sh.s_full[t], 1);
+            mbar_init(&sh.turn[t], 1);
             mbar_init(&sh.p_full[t][0], 4);
             mbar_init(&sh.p_full[t][1], 4);
             mbar_init(&sh.o_full[t], 1);
             mbar_init(&sh.o_empty[t], 4);
-            mbar_init(&sh.stat_full[t], 4);
+            mbar_init(&sh.sum_full[t], 4);
         }
-        for (int i = 0; i < kRing; ++i) mbar_init(&sh.item_full[i], 1), mbar_init(&sh.item_empty[i], 13);
+        for (int i = 0; i < kRing; ++i) mbar_init(&sh.item_full[i], 1), mbar_init(&sh.item_empty[i], 14);
         fence_mbar_init();
         prefetch_tmap(&mq);
         prefetch_tmap(&mk);
@@ -740,10 +753,12 @@ attn_prefill_kernel(PrefillArgs a, const __grid_constant__ CUtensorMap mq,
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegOther));
         if (warp == 12) {
-            mma_role<F16>(a, sh, sm);
+            mma_role<F16, 0>(a, sh, sm);
         } else if (warp == 13) {
+            mma_role<F16, 1>(a, sh, sm);
+        } else if (warp == 14) {
             load_role(a, sh, sm, &mq, &mk, &mv);
-        } else if (warp == 14 && !a.list && a.cu_q && blockIdx.x == 0) {
+        } else if (!a.list && a.cu_q && blockIdx.x == 0) {
             // with a list, attn_plan_kernel looks at the offsets
             const bool ok = warp_offsets_ok(a.cu_q, a.n_seqs, a.t_q) &&
                             warp_offsets_ok(a.cu_k, a.n_seqs, a.t_k);
@@ -754,6 +769,21 @@ attn_prefill_kernel(PrefillArgs a, const __grid_constant__ CUtensorMap mq,
     __syncthreads();
     tc_fence_after();
     if (warp == 12) tmem_dealloc(sh.tmem, 512);
+    // rows that a masked key's infinity or NaN has reached
+    if (warp < 8) {
+        for (int at = sh.redo; at >= 0;) {
+            const Redo d = a.redo[at];
+            const int t = at >> 2 & 1;
+            for (int i = warp; i < 32; i += 8) {
+                if (!(d.rows >> i & 1)) continue;
+                const int r = (at & 3) * 32 + i, token = r / a.group;
+                attend_row<F16>(a, (long long)d.e.row + t * a.tile_tokens + token, d.e.k0,
+                                d.e.pos + t * a.tile_tokens + token,
+                                d.head * a.group + r - token * a.group);
+            }
+            at = d.before;
+        }
+    }
 }
 
 // Items of a call, at most: slots of all sequences.
@@ -789,8 +819,10 @@ extern "C" size_t kda_attn_prefill_workspace_size(int64_t rows, int n_seqs, int 
     if (rows < 0 || n_seqs < 1 || heads < 1 || kv_heads < 1 || heads % kv_heads ||
         heads / kv_heads > 128)
         return 0;
-    // the ticket counter, then 16 bytes an item
-    return 256 + 16 * (size_t)slot_count(rows, n_seqs, heads / kv_heads);
+    // the ticket counter, 16 bytes an entry, eight records of rows to be done
+    // again per item
+    const size_t slots = (size_t)slot_count(rows, n_seqs, heads / kv_heads);
+    return 256 + 16 * slots + 8 * sizeof(Redo) * slots * kv_heads;
 }
 
 extern "C" kda_status kda_attn_prefill(const void* q, const void* k, const void* v, void* o,
@@ -831,7 +863,7 @@ extern "C" kda_status kda_attn_prefill(const void* q, const void* k, const void*
     if (st != KDA_OK) return st;
     const int group = heads / kv_heads, tokens = 128 / group;
     const long long slots = slot_count(rows_q, n_seqs, group);
-    KDA_REQUIRE(slots < 0x7fffffffLL / kv_heads, KDA_ERR_INVALID_ARG, "%s: problem too large", fn);
+    KDA_REQUIRE(slots < 0x0fffffffLL / kv_heads, KDA_ERR_INVALID_ARG, "%s: problem too large", fn);
     const size_t need = kda_attn_prefill_workspace_size(rows_q, n_seqs, heads, kv_heads);
     KDA_REQUIRE(workspace && workspace_bytes >= need, KDA_ERR_WORKSPACE,
                 "%s: workspace of %zu B, %zu B needed", fn, workspace ? workspace_bytes : 0, need);
@@ -863,7 +895,8 @@ extern "C" kda_status kda_attn_prefill(const void* q, const void* k, const void*
     PrefillArgs a = {(const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, (uint16_t*)o,
                      lse, cu_seqlens_q, cu_seqlens_k, q_row_stride, k_row_stride, v_row_stride,
                      o_row_stride, t_q, t_k, n_seqs, heads, kv_heads, window, group, tokens,
-                     scale, direct ? nullptr : list, count, (int)slots, shift};
+                     scale, direct ? nullptr : list, count, reinterpret_cast<Redo*>(list + slots),
+                     (int)slots, shift};
     auto kernel = f16 ? attn_prefill_kernel<true> : attn_prefill_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)kSmemBytes);
