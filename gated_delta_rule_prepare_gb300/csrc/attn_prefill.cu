@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(PrefillArgs a) 
 // One row on the CUDA cores by one warp, 4 channels a lane, touching only the
 // keys that the row sees.  The tensor cores multiply a masked key's weight 0
 // with its value, which gives NaN where the value is infinite or NaN; rows that
-// come out so are done again here (their sums are right: a masked key adds
-// nothing to those).  Not a path for ordinary inputs.
+// come out so are done again here, and rows whose weights left FP32's range
+// (softmax_role).  Not a path for ordinary inputs.
 template <bool F16>
 __device__ __noinline__ void attend_row(const PrefillArgs& a, long long row, long long k0, int p,
                                         int h) {
@@ -217,6 +217,8 @@ __device__ __noinline__ void attend_row(const PrefillArgs& a, long long row, lon
     const float r = l == 0.f ? 0.f : 1.f / l;
     const uint2 out = make_uint2(narrow2<F16>(o.x * r, o.y * r), narrow2<F16>(o.z * r, o.w * r));
     *reinterpret_cast<uint2*>(a.o + row * a.o_stride + h * D + 4 * lane) = out;
+    if (a.lse && lane == 0)
+        a.lse[row * a.heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -229,12 +231,8 @@ constexpr uint32_t kTmemO = 256;           // S0, S1, O0, O1: 128 columns each
 // Together what the launch has: 4 * 128.
 constexpr int kRegSoftmax = 184, kRegWriter = 72, kRegOther = 72;
 static_assert(2 * kRegSoftmax + kRegWriter + kRegOther <= 512, "registers of the launch");
-// The running maximum is left behind by up to 2^kLag before O is rescaled: a
-// weight is then at most 2^kLag, the sum and O carry the same factor and the
-// final division removes it.  The exponents of FP16 weights start at
-// 2^kLift so that weights down to 2^-31 of the largest one stay above its
-// smallest number.
-constexpr float kLag = 8.f;
+// The softmax's thresholds: see softmax_role.
+constexpr float kLag = 16777216.f;
 template <bool F16>
 constexpr float kLift = F16 ? 7.f : 0.f;
 
@@ -489,7 +487,7 @@ __device__ __forceinline__ void mma_role(const PrefillArgs& a, Shared& sh, unsig
                 const uint64_t vd = mn_major + v_stage * kTile;
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {
-                    if (part && !wait_warp(sh, &sh.p_full[t][1], p_phase)) return;
+                    if (part && !wait_warp(sh, &sh.p_full[t][part], p_phase)) return;
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
@@ -498,7 +496,7 @@ __device__ __forceinline__ void mma_role(const PrefillArgs& a, Shared& sh, unsig
                             mma_f16_ta(o_tmem, s_tmem + 8 * s, vd + s * 128, kPV,
                                        j > lo || part || i);
                         }
-                        if (part) {
+                        if (part == 1) {
                             mma_commit(&sh.kv_empty[v_stage]);
                             if (j == hi - 1) mma_commit(&sh.o_full[t]);
                         }
@@ -515,7 +513,25 @@ __device__ __forceinline__ void mma_role(const PrefillArgs& a, Shared& sh, unsig
     }
 }
 
-// Four warps, a thread a row of tile t: the softmax over the row's blocks.
+__device__ __forceinline__ void store_words(uint32_t addr, const uint32_t (&v)[16]) {
+    tmem_st16u(addr, v);
+}
+__device__ __forceinline__ void store_words(uint32_t addr, const uint32_t (&v)[32]) {
+    tmem_st32u(addr, v);
+}
+
+// Four warps, a thread a row of tile t.  Weights are 2^(c s + shift), c = scale
+// log2 e, and their sum l; the row's shift makes the largest weight of the first
+// block that the row sees 1 (2^kLift for FP16).
+//
+// BF16 weights have FP32's range, so a later block may exceed that: the shift
+// moves, and l and O with it, once l has passed 2^kLag, and no block but the
+// first needs its maximum (64 instructions a block, and the wait for them before
+// the first weight: 1424 against REPLACE TFLOP/s at 8192 tokens).  A row whose
+// scores rise by more than 2^100 within one block comes out infinite and is done
+// again (attend_row).
+// FP16 weights end at 65504: each block's maximum is compared with the shift
+// before, and the shift moves where a weight would pass 2^(kLift + 8).
 template <bool F16>
 __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, int t) {
     const int r = threadIdx.x & 127, lane = threadIdx.x & 31;
@@ -541,82 +557,102 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, i
         const int clear_hi = (tile.pos + 1) >> 7;
         const int clear_lo =
             a.window ? (max(0, tile.pos + tile.tokens - a.window) + 127) >> 7 : 0;
-        float m = -INFINITY, l = 0.f;
+        float shift = 0.f, l = 0.f;
         for (int j = tile.lo; j < tile.hi; ++j) {
             if (!wait_warp(sh, &sh.s_full[t], s_phase)) return;
             s_phase ^= 1;
             tc_fence_after();
-            float s[4][32];
+            const bool edge = j < clear_lo || j >= clear_hi;
+            // scores of keys 32 i .. 32 i + 31 that the row does not see become -inf
+            auto hide = [&](float (&x)[32], int i) {
+                const int from = max(0, min(32, first - j * 128 - 32 * i));
+                const int n = max(0, min(32, pos - j * 128 - 32 * i + 1));
+                const uint32_t see = (uint32_t)(((1ull << n) - 1) >> from << from);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) tmem_ld32(s_addr + 32 * i, s[i]);
-            tmem_ld_wait();
-            if (j < clear_lo || j >= clear_hi) {
-                const int lo = first - j * 128, hi = pos - j * 128;
-#pragma unroll
-                for (int i = 0; i < 128; ++i)
-                    if (i < lo || i > hi) s[i >> 5][i & 31] = -INFINITY;
-            }
-            float mx[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mx[i] = s[i][0];
-#pragma unroll
-            for (int x = 1; x < 31; x += 2)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) mx[i] = fmaxf(fmaxf(mx[i], s[i][x]), s[i][x + 1]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], s[i][31]);
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            if (j == tile.lo) {
-                m = top;
-            } else {
-                const bool move = (top - m) * c > kLag;
-                if (__any_sync(0xffffffffu, move)) {
-                    // all MMAs before S of this block are done, the last O += P V
-                    // among them
-                    const float f = move ? ex2_approx((m - top) * c) : 1.f;
-                    if (move) m = top;
-                    l *= f;
+                for (int k = 0; k < 32; ++k)
+                    if (!(see >> k & 1)) x[k] = -INFINITY;
+            };
+            // The shift moves by `by`.  All MMAs before S of this block are done,
+            // the last O += P V among them.
+            auto move = [&](float by) {
+                const float f = ex2_approx(by);
+                shift += by;
+                l *= f;
 #pragma unroll 1
-                    for (int i = 0; i < 8; ++i) {
-                        float o[16];
-                        uint32_t u[16];
-                        tmem_ld16(o_addr + 16 * i, o);
-                        tmem_ld_wait();
+                for (int i = 0; i < 8; ++i) {
+                    float o[16];
+                    uint32_t u[16];
+                    tmem_ld16(o_addr + 16 * i, o);
+                    tmem_ld_wait();
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) u[x] = __float_as_uint(o[x] * f);
-                        tmem_st16u(o_addr + 16 * i, u);
-                    }
+                    for (int x = 0; x < 16; ++x) u[x] = __float_as_uint(o[x] * f);
+                    tmem_st16u(o_addr + 16 * i, u);
+                }
+            };
+            // rows that had not seen a key before this block, and may now
+            const bool fresh = l == 0.f && pos >= max(first, j * 128);
+            if (F16 || __any_sync(0xffffffffu, fresh)) {
+                float top = -INFINITY;
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    float x[32], mx[4];
+                    tmem_ld32(s_addr + 32 * i, x);
+                    tmem_ld_wait();
+                    if (edge) hide(x, i);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mx[k] = fmaxf(x[k], x[k + 4]);
+#pragma unroll
+                    for (int k = 8; k < 32; k += 8)
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) mx[n] = fmaxf(fmaxf(mx[n], x[k + n]), x[k + n + 4]);
+                    top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                }
+                if (fresh) shift = (top == -INFINITY ? 0.f : -top * c) + kLift<F16>;
+                if (F16) {
+                    const float over = fmaf(top, c, shift) - kLift<F16>;
+                    const float by = over > 8.f ? -over : 0.f;
+                    if (__any_sync(0xffffffffu, by != 0.f)) move(by);
                 }
             }
-            const float shift = (m == -INFINITY ? 0.f : -m * c) + kLift<F16>;
+            if (!F16) {
+                const bool big = l > kLag && l < INFINITY;  // an infinite sum stays one
+                if (__any_sync(0xffffffffu, big)) move(big ? -log2f(l) : 0.f);
+            }
             const float2 c2 = make_float2(c, c), b2 = make_float2(shift, shift);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            // 32 keys to weights, written over S: over keys that are in registers
+            auto weights = [&](float (&x)[32], int i) {
+                if (edge) hide(x, i);
+                uint32_t p[16];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t p[32];
-#pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    float* y = &s[2 * half + (x >> 4)][2 * (x & 15)];
-                    const float2 e = fma2(make_float2(y[0], y[1]), c2, b2);
-                    y[0] = ex2_approx(e.x);
-                    y[1] = ex2_approx(e.y);
-                    p[x] = F16 ? pack_f16x2(y[0], y[1]) : pack_bf16x2(y[0], y[1]);
+                for (int k = 0; k < 16; ++k) {
+                    float2 e = fma2(make_float2(x[2 * k], x[2 * k + 1]), c2, b2);
+                    e.x = ex2_approx(e.x);
+                    e.y = ex2_approx(e.y);
+                    sum[k & 1] = add2(sum[k & 1], e);
+                    p[k] = F16 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
                 }
-                tmem_st32u(s_addr + 32 * half, p);
+                tmem_st16u(s_addr + 16 * i, p);
+            };
+            // (rolled: the code of a block stays short enough for two warps of one
+            // scheduler, which are at different places of it)
+            float x0[32], x1[32];
+            tmem_ld32(s_addr, x0);
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                tmem_ld_wait();
+                tmem_ld32(s_addr + 64 * half + 32, x1);
+                weights(x0, 2 * half);
+                tmem_ld_wait();
+                if (half == 0) tmem_ld32(s_addr + 64, x0);
+                weights(x1, 2 * half + 1);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.p_full[t][half]);
             }
-            float2 sum[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum[i] = make_float2(s[i][0], s[i][1]);
-#pragma unroll
-            for (int x = 2; x < 32; x += 2)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sum[i] = add2(sum[i], make_float2(s[i][x], s[i][x + 1]));
-            const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-            l += all.x + all.y;
+            const float2 both = add2(sum[0], sum[1]);
+            l += both.x + both.y;
         }
         // once the writers have read the last item's
         if (!wait_warp(sh, &sh.o_empty[t], o_phase ^ 1)) return;
@@ -627,7 +663,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, i
         if (a.lse && token < tile.tokens) {
             const long long row = (long long)it.e.row + t * a.tile_tokens + token;
             a.lse[row * a.heads + it.head * a.group + r - token * a.group] =
-                l == 0.f ? -INFINITY : fmaf(m, a.scale, (log2f(l) - kLift<F16>) * kLn2);
+                l == 0.f ? -INFINITY : (log2f(l) - shift) * kLn2;
         }
     }
 }
@@ -727,8 +763,7 @@ attn_prefill_kernel(PrefillArgs a, const __grid_constant__ CUtensorMap mq,
             mbar_init(&sh.q_empty[t], 1);
             mbar_init(&sh.s_full[t], 1);
             mbar_init(&sh.turn[t], 1);
-            mbar_init(&sh.p_full[t][0], 4);
-            mbar_init(&sh.p_full[t][1], 4);
+            for (int i = 0; i < 2; ++i) mbar_init(&sh.p_full[t][i], 4);
             mbar_init(&sh.o_full[t], 1);
             mbar_init(&sh.o_empty[t], 4);
             mbar_init(&sh.sum_full[t], 4);
