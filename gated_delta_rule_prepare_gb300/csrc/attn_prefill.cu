@@ -227,12 +227,8 @@ constexpr int kStages = 5;                 // of 32 KB: a block's K, then its V
 constexpr uint32_t kTileBytes = 128 * 128 * 2;
 constexpr int kRing = 4;                   // items between the TMA warp and the others
 constexpr uint32_t kTmemO = 256;           // S0, S1, O0, O1: 128 columns each
-// Registers a thread: softmax (2 x 128 threads), writers (128), the rest (128).
-// Together what the launch has: 4 * 128.
-constexpr int kRegSoftmax = 184, kRegWriter = 72, kRegOther = 72;
-static_assert(2 * kRegSoftmax + kRegWriter + kRegOther <= 512, "registers of the launch");
 // The softmax's thresholds: see softmax_role.
-constexpr float kLag = 16777216.f;
+constexpr float kLag = 16777216.f;  // 2^24
 template <bool F16>
 constexpr float kLift = F16 ? 7.f : 0.f;
 
@@ -396,10 +392,11 @@ __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, 
 
 // The warp that issues tile t's MMAs: per block S = Q K^T, and O += P V once
 // the softmax has written P.  Each tile has a warp of its own, so that the
-// tensor cores always have the other tile's products while one waits (with one
-// warp for both, what lies between two products stalled them: 1443 against
-// 16xx TFLOP/s at 8192 tokens, 32 heads over 8).  MMAs of one warp execute in
-// the order of their issue, so S's write over P needs no wait of its own.
+// waits of one tile's products run under the other's; they take turns, so that
+// one tile's products run while the other's softmax does (one warp for both:
+// 1366 TFLOP/s at 8192 tokens, 32 heads over 8; two without turns: 1279; with:
+// 1424, before the softmax was shortened).  MMAs of one warp execute in the
+// order of their issue, so S's write over P needs no wait of its own.
 template <bool F16, int t>
 __device__ __forceinline__ void mma_role(const PrefillArgs& a, Shared& sh, unsigned char* sm) {
     constexpr uint32_t kQK = idesc_16(128, 128, !F16, false);
@@ -525,13 +522,13 @@ __device__ __forceinline__ void store_words(uint32_t addr, const uint32_t (&v)[3
 // block that the row sees 1 (2^kLift for FP16).
 //
 // BF16 weights have FP32's range, so a later block may exceed that: the shift
-// moves, and l and O with it, once l has passed 2^kLag, and no block but the
+// moves, and l and O with it, once l has passed 2^24, and no block but the
 // first needs its maximum (64 instructions a block, and the wait for them before
-// the first weight: 1424 against REPLACE TFLOP/s at 8192 tokens).  A row whose
-// scores rise by more than 2^100 within one block comes out infinite and is done
-// again (attend_row).
+// the first weight).  A row whose scores rise by more than 2^100 within one
+// block comes out infinite and is done again (attend_row).
 // FP16 weights end at 65504: each block's maximum is compared with the shift
-// before, and the shift moves where a weight would pass 2^(kLift + 8).
+// before, and the shift moves where a weight would pass 2^(kLift + 8).  kLift
+// keeps weights down to 2^-31 of the largest above FP16's smallest number.
 template <bool F16>
 __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, int t) {
     const int r = threadIdx.x & 127, lane = threadIdx.x & 31;
@@ -620,7 +617,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, i
             }
             const float2 c2 = make_float2(c, c), b2 = make_float2(shift, shift);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            // 32 keys to weights, written over S: over keys that are in registers
+            // 32 keys to weights, written over scores that are no longer needed
             auto weights = [&](float (&x)[32], int i) {
                 if (edge) hide(x, i);
                 uint32_t p[16];
@@ -634,22 +631,23 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, i
                 }
                 tmem_st16u(s_addr + 16 * i, p);
             };
-            // (rolled: the code of a block stays short enough for two warps of one
-            // scheduler, which are at different places of it)
-            float x0[32], x1[32];
-            tmem_ld32(s_addr, x0);
+            // Rolled, 32 keys a step: two warps of a scheduler are at different
+            // places of this code, and what a block takes has to stay in the
+            // instruction cache nearest to it (128 keys unrolled: 1354 TFLOP/s at
+            // 8192 tokens, 64: 1540, 32: 1590).  P goes to the MMA warp in two
+            // parts (in one: 1504).
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
+            for (int i = 0; i < 4; ++i) {
+                float x[32];
+                tmem_ld32(s_addr + 32 * i, x);
                 tmem_ld_wait();
-                tmem_ld32(s_addr + 64 * half + 32, x1);
-                weights(x0, 2 * half);
-                tmem_ld_wait();
-                if (half == 0) tmem_ld32(s_addr + 64, x0);
-                weights(x1, 2 * half + 1);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_full[t][half]);
+                weights(x, i);
+                if (i & 1) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.p_full[t][i >> 1]);
+                }
             }
             const float2 both = add2(sum[0], sum[1]);
             l += both.x + both.y;
@@ -733,7 +731,8 @@ __device__ __forceinline__ void write_role(const PrefillArgs& a, Shared& sh) {
             }
             if (!any && mine && a.lse) a.lse[row * a.heads + h] = -INFINITY;
             // a sum that is NaN comes from a key that the row sees
-            const unsigned again = __ballot_sync(0xffffffffu, mine && poison != poison && l == l);
+            const unsigned again = __ballot_sync(
+                0xffffffffu, mine && ((poison != poison && l == l) || l == INFINITY));
             if (again && lane == 0) {
                 const int at = (it.index * 2 + t) * 4 + (r >> 5);
                 a.redo[at] = {it.e, it.head, again, atomicExch(&sh.redo, at)};
@@ -780,13 +779,10 @@ attn_prefill_kernel(PrefillArgs a, const __grid_constant__ CUtensorMap mq,
     tc_fence_after();
     pdl_wait();
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegSoftmax));
         softmax_role<F16>(a, sh, warp >> 2);
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegWriter));
         write_role<F16>(a, sh);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegOther));
         if (warp == 12) {
             mma_role<F16, 0>(a, sh, sm);
         } else if (warp == 13) {
