@@ -56,6 +56,9 @@ extern "C" {
 /* Bytes one token of one KV head takes in the 4-bit cache, K and V together:
  * for each, 64 bytes of codes and 8 of parameters. */
 #define KDA_KV4_TOKEN_BYTES 144
+/* Pieces into which kda_attn_kv4_decode cuts a batch, at most (its workspace
+ * holds two partial results for each). */
+#define KDA_KV4_PIECES 320
 
 typedef enum {
     KDA_OK = 0,
