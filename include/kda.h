@@ -58,7 +58,7 @@ extern "C" {
 #define KDA_KV4_TOKEN_BYTES 144
 /* Pieces into which kda_attn_kv4_decode cuts a batch, at most (its workspace
  * holds two partial results for each). */
-#define KDA_KV4_PIECES 320
+#define KDA_KV4_PIECES 480
 
 typedef enum {
     KDA_OK = 0,
