@@ -13,6 +13,7 @@
 // memory sees 16-byte accesses on both sides.  Memory-bound: 512 + 144 bytes
 // per (token, head).
 #include "attn_common.h"
+#include "f32x2.h"
 
 namespace kda {
 namespace {
@@ -82,14 +83,19 @@ __device__ __forceinline__ void check_offsets(const RowArgs& a) {
         atomicOr(&g_kv4_status, STATUS_BAD_CU_SEQLENS);
 }
 
-__device__ __forceinline__ float min_nan(float a, float b) {
-    float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+// Minimum and maximum of two elements at a time, NaN if either is.
+template <bool F16>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (F16) asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+template <bool F16>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (F16) asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
@@ -104,11 +110,10 @@ __device__ __forceinline__ uint32_t bf16_up(float x) {
     return (u >> 16) + ((u & 0xffffu) ? 1u : 0u);
 }
 
-// The code of x near a border between two codes, or where 1/s overflows:
-// compares x with the borders m + (c + 0.5) s.  c + 0.5 has 5 bits and s has 8,
-// so (c + 0.5) s is exact; t + e is x - m exactly (the rounded difference and
-// what it lost), and the fused multiply-add gets the comparison's sign right.
-__device__ __noinline__ uint32_t code_at_border(float x, float m, float s) {
+// The code of x by comparison with borders, for groups whose numbers lie too far
+// apart for codes8: t + e is x - m exactly (the rounded difference and what it
+// lost), and the fused multiply-add gets the sign of t - (c + 0.5) s right.
+__device__ __noinline__ uint32_t code_exact(float x, float m, float s) {
     const float t = x - m;
     const float back = x - t;
     const float e = (x - (t + back)) + (back - m);
@@ -123,121 +128,169 @@ __device__ __noinline__ uint32_t code_at_border(float x, float m, float s) {
 }
 
 // Eight channels of one token row: codes packed four bits each, channel x in
-// bits 4x.
+// bits 4x.  With k = floor of the quotient (which may be off by one where the
+// quotient is close to an integer: that moves nothing) the code is k or k + 1, as
+// x lies below or above the border b = m + (k + 0.5) s, and the even one of them
+// on it.  k + 0.5 has 5 bits and s has 8, so b is exact in FP32 unless m and s are
+// more than 2^10 apart: ten operations a value, no case apart for ties
+// (of BF16 rows some 1 in 300 values is one; deciding those in a branch took
+// 640 us for the front end's batch where this takes APPENDUS).
+__device__ __forceinline__ float2 fma2_down(float2 a, float2 b, float2 c) {  // rounded down
+    unsigned long long r;
+    asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pk(a)), "l"(pk(b)), "l"(pk(c)));
+    return upk(r);
+}
+
 template <bool F16>
 __device__ __forceinline__ uint32_t codes8(const uint4& raw, float m, float s, float inv) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     uint32_t out = 0;
-    bool near = !(inv < 1e37f);
+    if (inv != 0.f) {  // m and s are near enough
+        constexpr float kMagic = 8388608.f;  // 2^23: integers above it are their last bits
+        constexpr uint32_t kBits = 0x4b000000u;
+        const float2 inv2 = make_float2(inv, inv), s2 = make_float2(s, s), m2 = make_float2(m, m);
+        const float2 less_m = make_float2(-m, -m), magic = make_float2(kMagic, kMagic);
+        const float2 half = make_float2(0.5f - kMagic, 0.5f - kMagic);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 x = widen2<F16>(w[i]);
-        const float a = (x.x - m) * inv, b = (x.y - m) * inv;
-        const float ra = rintf(a), rb = rintf(b);
-        // the quotient is good to 2^-18: only these can be on the wrong side
-        near |= fabsf(a - ra) > 0.4999f || fabsf(b - rb) > 0.4999f;
-        out |= min((uint32_t)ra, 15u) << (8 * i) | min((uint32_t)rb, 15u) << (8 * i + 4);
-    }
-    if (near) {
-        out = 0;
         for (int i = 0; i < 4; ++i) {
             const float2 x = widen2<F16>(w[i]);
-            out |= code_at_border(x.x, m, s) << (8 * i) |
-                   code_at_border(x.y, m, s) << (8 * i + 4);
+            const float2 k = fma2_down(add2(x, less_m), inv2, magic);
+            const float2 b = fma2(add2(k, half), s2, m2);
+            const float2 d = add2(b, make_float2(-x.x, -x.y));
+            // one more where b - x is negative, or zero and k odd: where its bits,
+            // less k's last one, have the sign bit
+            const uint32_t k0 = __float_as_uint(k.x), k1 = __float_as_uint(k.y);
+            const uint32_t c0 = k0 + ((__float_as_uint(d.x) - (k0 & 1)) >> 31);
+            const uint32_t c1 = k1 + ((__float_as_uint(d.y) - (k1 & 1)) >> 31);
+            // (as multiply-adds: the shifts and ANDs of this loop bound it)
+            asm("mad.lo.u32 %0, %1, %2, %0;" : "+r"(out) : "r"(c0), "r"(1u << (8 * i)));
+            asm("mad.lo.u32 %0, %1, %2, %0;" : "+r"(out) : "r"(c1), "r"(1u << (8 * i + 4)));
         }
+        return out - (kBits + (kBits << 4));
     }
-    return s > 0.f ? out : 0u;
+    if (!(s > 0.f)) return 0u;
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = widen2<F16>(w[i]);
+        out |= code_exact(x.x, m, s) << (8 * i) | code_exact(x.y, m, s) << (8 * i + 4);
+    }
+    return out;
 }
 
-// grid (ceil(slots / 4), kv_heads, 2): z = 0 writes K, z = 1 V.  A half-warp
-// loads a token row of 128 channels, 16 bytes a lane, all sixteen tokens of
-// the group in flight; minimum and maximum over 64 channels are 8-lane
-// shuffles.
+// 16 tokens of one head of K or of V, by one warp.
 template <bool F16>
-__global__ void __launch_bounds__(kWarps * 32) append_kernel(RowArgs a) {
-    __shared__ __align__(16) uint8_t stage[kWarps][kStage];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    check_offsets(a);
-    Slot s;
-    if (!find_slot(a, (long long)blockIdx.x * kWarps + warp, s)) return;  // whole warps
-    const int h = blockIdx.y;
-    const bool is_v = blockIdx.z;
-    uint8_t* block = a.c.block(s.n, s.pos, h);
-    if (!block) {
-        if (lane == 0) atomicOr(&g_kv4_status, STATUS_BAD_PAGES);
-        return;
-    }
-    if (is_v) block += part_bytes(a.c.page());
+__device__ __forceinline__ void append_group(const RowArgs& a, const Slot& s, uint8_t* stage,
+                                             uint8_t* block, int h, bool is_v) {
+    const int lane = threadIdx.x & 31;
     const long long stride = is_v ? a.v_stride : a.k_stride;
     const uint16_t* src = (is_v ? a.v : a.k) + h * D;
     const int hw = lane >> 4, c = lane & 15, b = c >> 1;
     const int t0 = s.pos & 15;  // first token of the group that is written
     uint4 raw[8];
+    src += (s.row - t0 + hw) * stride + 8 * c;
+    if (s.count == 16) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int tok = 2 * j + hw;
-        const bool mine = tok >= t0 && tok < t0 + s.count;
-        raw[j] = mine ? __ldg(reinterpret_cast<const uint4*>(
-                            src + (s.row + tok - t0) * stride + 8 * c))
-                      : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < 8; ++j)
+            raw[j] = __ldg(reinterpret_cast<const uint4*>(src + 2 * j * stride));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int tok = 2 * j + hw;
+            raw[j] = tok >= t0 && tok < t0 + s.count
+                         ? __ldg(reinterpret_cast<const uint4*>(src + 2 * j * stride))
+                         : make_uint4(0, 0, 0, 0);
+        }
     }
     const int in_page = s.pos & (a.c.page() - 1) & ~15;
     uint8_t* par = block + a.c.page() * 64 + (long long)in_page * 8;
+    // Least and greatest of each token's 64 channels, over eight lanes, so that
+    // lane c % 8 = j ends with token j's: 4 + 2 + 1 exchanges for 8 tokens.
+    uint32_t mm[8];  // (least, greatest) of this lane's channels, both 16 bits
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int tok = 2 * j + hw;
-        const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-        float lo, hi;
-        {
-            const float2 x = widen2<F16>(w[0]);
-            lo = min_nan(x.x, x.y);
-            hi = max_nan(x.x, x.y);
-        }
+        const uint32_t lo = min2<F16>(min2<F16>(raw[j].x, raw[j].y), min2<F16>(raw[j].z, raw[j].w));
+        const uint32_t hi = max2<F16>(max2<F16>(raw[j].x, raw[j].y), max2<F16>(raw[j].z, raw[j].w));
+        // (lo.x, -hi.x) and (lo.y, -hi.y): one minimum serves both
+        constexpr uint32_t kMinus = 0x80000000u;
+        mm[j] = min2<F16>(__byte_perm(lo, hi, 0x5410) ^ kMinus, __byte_perm(lo, hi, 0x7632) ^ kMinus);
+    }
 #pragma unroll
-        for (int i = 1; i < 4; ++i) {
-            const float2 x = widen2<F16>(w[i]);
-            lo = min_nan(lo, min_nan(x.x, x.y));
-            hi = max_nan(hi, max_nan(x.x, x.y));
-        }
+    for (int half = 4; half >= 1; half /= 2) {
+        const bool up = c & half;
 #pragma unroll
-        for (int off = 1; off < 8; off <<= 1) {
-            lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-            hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+        for (int j = 0; j < half; ++j) {
+            const uint32_t give = up ? mm[j] : mm[j + half];
+            const uint32_t keep = up ? mm[j + half] : mm[j];
+            mm[j] = min2<F16>(keep, __shfl_xor_sync(0xffffffffu, give, half));
         }
-        uint32_t mb = bf16_down(lo);
-        const float m = __uint_as_float(mb << 16);
-        // both rounded up: at or above the real quotient, and equal to it
-        // where it is a BF16 number
-        const float q = __fdiv_ru(__fsub_ru(hi, m), 15.f);
+    }
+    // token 2 (c % 8) + hw: parameters, and 1 / s, or 0 where m and s lie too far
+    // apart for codes8
+    float my_m, my_s, my_inv;
+    {
+        const float2 x = widen2<F16>(mm[0]);
+        uint32_t mb = bf16_down(x.x);
+        my_m = __uint_as_float(mb << 16);
+        // both rounded up: at or above the real quotient, and equal to it where it
+        // is a BF16 number
+        const float q = __fdiv_ru(__fsub_ru(-x.y, my_m), 15.f);
         uint32_t sb = bf16_up(q);
         // an infinity or a NaN in the group: every value of it reads as NaN
-        const bool bad = !(q < 3e38f) || !(fabsf(m) < INFINITY);
+        const bool bad = !(q < 3e38f) || !(fabsf(my_m) < INFINITY);
         if (bad) mb = sb = 0x7fffu;
-        const float sc = bad ? 0.f : __uint_as_float(sb << 16);
-        const uint32_t own = codes8<F16>(raw[j], bad ? 0.f : m, sc, 1.f / sc);
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
-        // channels 16 b + x (low bits, the even lane's) and 16 b + 8 + x
-        const uint32_t even = lane & 1 ? other : own, odd = lane & 1 ? own : other;
-        const int x0 = (lane & 1) * 4;  // the even lane stores x = 0..3, the odd one 4..7
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int x = x0 + i;
-            const uint32_t byte = (even >> (4 * x) & 15u) | (odd >> (4 * x) & 15u) << 4;
-            const int hi8 = tok >> 3, lo8 = tok & 7;
-            const int at = 512 * (b >> 2) + 4 * (b & 3) +
-                           (is_v ? 16 * (4 * x + (lo8 >> 1)) + 2 * (lo8 & 1) + hi8
-                                 : 16 * (4 * lo8 + (x >> 1)) + 2 * (x & 1) + hi8);
-            stage[warp][staged(at)] = (uint8_t)byte;
-        }
-        if ((c & 7) == 0 && tok >= t0 && tok < t0 + s.count)
+        my_s = bad ? 0.f : __uint_as_float(sb << 16);
+        if (bad) my_m = 0.f;
+        const float size = fabsf(my_m);
+        const bool plain = my_s > 1e-30f && size <= 1024.f * my_s &&
+                           (size == 0.f || my_s <= 1024.f * size);
+        my_inv = plain ? 1.f / my_s : 0.f;
+        const int tok = 2 * (c & 7) + hw;
+        if (tok >= t0 && tok < t0 + s.count)
             *reinterpret_cast<uint32_t*>(par + tok * 8 + (c >> 3) * 4) = sb | mb << 16;
+    }
+    // Codes of tokens tok and tok + 8 at a time: of K, the four bytes of a word.
+    // An even lane holds channels 16 b + x, its odd neighbour 16 b + 8 + x, and
+    // they store x = 0..3 and x = 4..7.
+    const bool odd = lane & 1;
+    __syncwarp();  // the last group's codes have been read
+    uint8_t* const dst = stage + staged(512 * (b >> 2)) + 4 * (b & 3);
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) {
+        uint32_t own[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int from = (lane & ~7) | (jj + 4 * n);
+            own[n] = codes8<F16>(raw[jj + 4 * n], __shfl_sync(0xffffffffu, my_m, from),
+                                 __shfl_sync(0xffffffffu, my_s, from),
+                                 __shfl_sync(0xffffffffu, my_inv, from));
+        }
+        // low halves are x = 0..3; the neighbour gets the half it stores
+        const uint32_t low = __byte_perm(own[0], own[1], 0x5410);
+        const uint32_t high = __byte_perm(own[0], own[1], 0x7632);
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? low : high, 1);
+        const uint32_t nib0 = odd ? got : low, nib1 = odd ? high : got;
+        const uint32_t e = (nib0 & 0x0f0f0f0fu) | (nib1 & 0x0f0f0f0fu) << 4;
+        const uint32_t o = (nib0 >> 4 & 0x0f0f0f0fu) | (nib1 & 0xf0f0f0f0u);
+        const uint32_t w0 = __byte_perm(e, o, 0x6420), w1 = __byte_perm(e, o, 0x7531);
+        if (!is_v) {
+            // token g = 2 jj + hw: words t = 0..3 at 16 (4 g + t)
+            uint32_t* p = reinterpret_cast<uint32_t*>(dst + 64 * (2 * jj + hw) + (odd ? 32 : 0));
+            p[0] = w0;
+            p[4] = w1;
+        } else {
+            // t = jj, e = hw: channel x at 16 (4 x + t) + 2 e
+            uint8_t* p = dst + 16 * jj + 2 * hw + (odd ? 256 : 0);
+            *reinterpret_cast<uint16_t*>(p) = (uint16_t)w0;
+            *reinterpret_cast<uint16_t*>(p + 64) = (uint16_t)(w0 >> 16);
+            *reinterpret_cast<uint16_t*>(p + 128) = (uint16_t)w1;
+            *reinterpret_cast<uint16_t*>(p + 192) = (uint16_t)(w1 >> 16);
+        }
     }
     __syncwarp();
     uint8_t* codes = block + (long long)in_page * 64;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int at = half * 512 + lane * 16;
-        const uint4 v = *reinterpret_cast<const uint4*>(&stage[warp][staged(at)]);
+        const uint4 v = *reinterpret_cast<const uint4*>(&stage[staged(at)]);
         if (s.count == 16) {
             *reinterpret_cast<uint4*>(codes + at) = v;
             continue;
@@ -254,40 +307,56 @@ __global__ void __launch_bounds__(kWarps * 32) append_kernel(RowArgs a) {
     }
 }
 
-// grid as append_kernel.  A lane turns 8 channels of a token into 16 bytes.
+// grid (ceil(slots / 4), kv_heads, 1 or 2): a warp does K and then V of its 16
+// tokens, or with two one of them.  A half-warp
+// loads a token row of 128 channels, 16 bytes a lane, all sixteen tokens of
+// the group in flight.
 template <bool F16>
-__global__ void __launch_bounds__(kWarps * 32) read_kernel(RowArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 8) append_kernel(RowArgs a) {
     __shared__ __align__(16) uint8_t stage[kWarps][kStage];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     check_offsets(a);
     Slot s;
-    if (!find_slot(a, (long long)blockIdx.x * kWarps + warp, s)) return;
+    if (!find_slot(a, (long long)blockIdx.x * kWarps + warp, s)) return;  // whole warps
     const int h = blockIdx.y;
-    const bool is_v = blockIdx.z;
-    const uint8_t* block = a.c.block(s.n, s.pos, h);
-    if (!block && lane == 0) atomicOr(&g_kv4_status, STATUS_BAD_PAGES);
+    uint8_t* block = a.c.block(s.n, s.pos, h);
+    if (!block) {
+        if (lane == 0) atomicOr(&g_kv4_status, STATUS_BAD_PAGES);
+        return;
+    }
+#pragma unroll 1
+    for (int which = blockIdx.z; which < 2; which += gridDim.z)
+        append_group<F16>(a, s, stage[warp], block + which * part_bytes(a.c.page()), h, which);
+}
+
+// The same the other way: a lane turns 8 channels of a token into 16 bytes.
+template <bool F16>
+__device__ __forceinline__ void read_group(const RowArgs& a, const Slot& s, uint8_t* stage,
+                                           const uint8_t* block, int h, bool is_v) {
+    const int lane = threadIdx.x & 31;
     const long long stride = is_v ? a.v_stride : a.k_stride;
-    uint16_t* dst = (is_v ? a.v : a.k) + h * D;
     const int hw = lane >> 4, c = lane & 15, b = c >> 1;
     const int t0 = s.pos & 15;
     const int in_page = s.pos & (a.c.page() - 1) & ~15;
+    uint16_t* dst = (is_v ? a.v : a.k) + h * D + 8 * c + (s.row - t0) * stride;
     const uint8_t* par = nullptr;
+    __syncwarp();  // the last group's codes have been read
     if (block) {
-        if (is_v) block += part_bytes(a.c.page());
         par = block + a.c.page() * 64 + (long long)in_page * 8 + (c >> 3) * 4;
         const uint8_t* codes = block + (long long)in_page * 64;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int at = half * 512 + lane * 16;
-            *reinterpret_cast<uint4*>(&stage[warp][staged(at)]) =
+            *reinterpret_cast<uint4*>(&stage[staged(at)]) =
                 __ldg(reinterpret_cast<const uint4*>(codes + at));
         }
     }
     __syncwarp();
-    const uint8_t* mine = &stage[warp][staged(512 * (b >> 2)) + 4 * (b & 3)];
+    const uint8_t* mine = stage + staged(512 * (b >> 2)) + 4 * (b & 3);
     const int sh = 4 * (lane & 1);
-    // One token: byte_of(x) holds the code of its channel x = 0..7 of this lane.
-    auto put = [&](int tok, auto byte_of) {
+    // One token: code(x) has the code of its channel x = 0..7 of this lane as the
+    // FP32 number 2^23 + code.
+    auto put = [&](int tok, auto code) {
         if (tok < t0 || tok >= t0 + s.count) return;
         // a page that is not there reads as NaN
         const uint32_t p = par ? __ldg(reinterpret_cast<const uint32_t*>(par + tok * 8))
@@ -295,13 +364,13 @@ __global__ void __launch_bounds__(kWarps * 32) read_kernel(RowArgs a) {
         const float sc = __uint_as_float(p << 16), m = __uint_as_float(p & 0xffff0000u);
         uint32_t out[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float lo = (float)(byte_of(2 * i) >> sh & 15u);
-            const float hi = (float)(byte_of(2 * i + 1) >> sh & 15u);
-            out[i] = narrow2<F16>(fmaf(sc, lo, m), fmaf(sc, hi, m));
-        }
-        *reinterpret_cast<uint4*>(dst + (s.row + tok - t0) * stride + 8 * c) =
-            make_uint4(out[0], out[1], out[2], out[3]);
+        for (int i = 0; i < 4; ++i)
+            out[i] = narrow2<F16>(fmaf(sc, code(2 * i) - 8388608.f, m),
+                                  fmaf(sc, code(2 * i + 1) - 8388608.f, m));
+        *reinterpret_cast<uint4*>(dst + tok * stride) = make_uint4(out[0], out[1], out[2], out[3]);
+    };
+    auto number = [](uint32_t w, int byte) {
+        return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7550 + byte));
     };
     if (!is_v) {
 #pragma unroll
@@ -310,10 +379,11 @@ __global__ void __launch_bounds__(kWarps * 32) read_kernel(RowArgs a) {
             uint32_t w[4];
 #pragma unroll
             for (int t = 0; t < 4; ++t)
-                w[t] = *reinterpret_cast<const uint32_t*>(mine + 16 * (4 * g + t));
+                w[t] = *reinterpret_cast<const uint32_t*>(mine + 16 * (4 * g + t)) >> sh &
+                       0x0f0f0f0fu;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                put(g + 8 * i, [&](int x) { return w[x >> 1] >> (16 * (x & 1) + 8 * i); });
+                put(g + 8 * i, [&](int x) { return number(w[x >> 1], 2 * (x & 1) + i); });
         }
     } else {
 #pragma unroll
@@ -322,14 +392,31 @@ __global__ void __launch_bounds__(kWarps * 32) read_kernel(RowArgs a) {
             uint32_t w[8];
 #pragma unroll
             for (int x = 0; x < 8; ++x)
-                w[x] = *reinterpret_cast<const uint32_t*>(mine + 16 * (4 * x + t));
+                w[x] = *reinterpret_cast<const uint32_t*>(mine + 16 * (4 * x + t)) >> sh &
+                       0x0f0f0f0fu;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    put(2 * t + e + 8 * i, [&](int x) { return w[x] >> (16 * e + 8 * i); });
+                    put(2 * t + e + 8 * i, [&](int x) { return number(w[x], 2 * e + i); });
         }
     }
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(kWarps * 32, 12) read_kernel(RowArgs a) {
+    __shared__ __align__(16) uint8_t stage[kWarps][kStage];
+    const int warp = threadIdx.x >> 5;
+    check_offsets(a);
+    Slot s;
+    if (!find_slot(a, (long long)blockIdx.x * kWarps + warp, s)) return;
+    const int h = blockIdx.y;
+    const uint8_t* block = a.c.block(s.n, s.pos, h);
+    if (!block && (threadIdx.x & 31) == 0) atomicOr(&g_kv4_status, STATUS_BAD_PAGES);
+#pragma unroll 1
+    for (int which = blockIdx.z; which < 2; which += gridDim.z)
+        read_group<F16>(a, s, stage[warp],
+                        block ? block + which * part_bytes(a.c.page()) : nullptr, h, which);
 }
 
 kda_status rows_call(const char* fn, bool append, void* k, void* v, int64_t k_stride,
@@ -353,7 +440,10 @@ kda_status rows_call(const char* fn, bool append, void* k, void* v, int64_t k_st
     RowArgs a = {(uint16_t*)k, (uint16_t*)v, k_stride, v_stride, cu, t, n_seqs,
                  {cache, table, lens, n_pages, max_pages, __builtin_ctz((unsigned)page), kv_heads}};
     const long long slots = rows / 16 + 2LL * n_seqs;
-    const dim3 grid((unsigned)((slots + kWarps - 1) / kWarps), (unsigned)kv_heads, 2);
+    // K and V in one warp share the search for its tokens (REPLACEUS at the front
+    // end's batch against two warps' REPLACE2); few tokens are done sooner apart.
+    const unsigned apart = slots * kv_heads < 16LL * 152 ? 2 : 1;
+    const dim3 grid((unsigned)((slots + kWarps - 1) / kWarps), (unsigned)kv_heads, apart);
     const dim3 threads(kWarps * 32);
     cudaStream_t s = as_stream(stream);
     if (append) {
