@@ -441,51 +441,64 @@ def kda_gate(g_raw, dt_bias, a_log, b_raw, g_out, beta_out, gate_lower_bound):
 
 # ---------------------------------------------------------------- full attention
 
+# These calls are short, and a decode step makes them once a layer: arguments are
+# checked with few attribute reads, and a tensor's device by its index (-1: none).
+
 _ATTN_TYPES = {torch.bfloat16: BF16, torch.float16: F16}
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _rows(t, dtype, name):
+def _attn_type(t, name):
+    dt = _ATTN_TYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError("%s must be bfloat16 or float16" % name)
+    dev = t.get_device()
+    if dev < 0:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    return dt, dev
+
+
+def _at(t, dtype, dev, name):
+    """Pointer of a tensor of the given type on device `dev`."""
+    if t.dtype != dtype or t.get_device() != dev:
+        raise TypeError("%s must be a %s tensor on the call's CUDA device" % (name, dtype))
+    return t.data_ptr()
+
+
+def _packed(t, dtype, dev, name):
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return _at(t, dtype, dev, name)
+
+
+def _rows(t, dtype, dev, name):
     """(pointer, token-row stride) of a [..., rows, heads, 128] tensor with its
     heads packed; a leading sequence dimension must be consecutive row blocks."""
-    if not t.is_cuda or t.dtype != dtype:
-        raise TypeError("%s must be a CUDA %s tensor" % (name, dtype))
-    shape, stride = t.shape, t.stride()
-    if (len(shape) not in (3, 4) or shape[-1] != HEAD_DIM or stride[-1] != 1
-            or (stride[-2] != HEAD_DIM and shape[-2] > 1)):
-        raise ValueError("%s must be [rows, heads, 128] with unit channel stride and heads packed"
-                         % name)
-    packed = shape[-2] * HEAD_DIM
-    row = stride[-3] if shape[-3] > 1 else packed
+    ptr, shape = _at(t, dtype, dev, name), t.shape
+    if len(shape) not in (3, 4) or shape[-1] != HEAD_DIM:
+        raise ValueError("%s must be [rows, heads, 128]" % name)
+    if t.is_contiguous():
+        return ptr, shape[-2] * HEAD_DIM
+    stride = t.stride()
+    if stride[-1] != 1 or (stride[-2] != HEAD_DIM and shape[-2] > 1):
+        raise ValueError("%s must have unit channel stride and heads packed" % name)
+    row = stride[-3] if shape[-3] > 1 else shape[-2] * HEAD_DIM
     if len(shape) == 4 and shape[0] > 1:
         if shape[1] == 1:
             row = stride[0]
         elif stride[0] != shape[1] * row:
             raise ValueError("%s: sequences must be consecutive row blocks" % name)
-    return t.data_ptr(), row
+    return ptr, row
 
 
-def _int32(t, n, name):
-    if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous():
-        raise TypeError("%s must be a contiguous CUDA int32 tensor" % name)
-    if n is not None and t.numel() != n:
-        raise ValueError("%s must hold %d values" % (name, n))
-    return t.data_ptr()
-
-
-def _same_device(a, *others):
-    for t in others:
-        if t is not None and t.device != a.device:
-            raise ValueError("all tensors of one call must be on one device")
-
-
-def _scratch(workspace, need, device):
+def _scratch(workspace, need, dev):
     """(tensor, pointer, bytes) of the caller's workspace, or of one allocated
     here (the library itself never allocates)."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    elif workspace.device != device or not workspace.is_contiguous():
+        workspace = torch.empty(need(), dtype=torch.uint8, device="cuda:%d" % dev)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("the workspace must be a contiguous tensor on the call's device")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.nbytes
 
 
 def kda_attn_prefill_workspace(rows, n_seqs, heads, kv_heads, device="cuda"):
@@ -503,46 +516,44 @@ def kda_attn_prefill(q, k, v, out, lse=None, cu_seqlens=None, cu_seqlens_k=None,
     packed sequences; without them, tensors of four dimensions
     [N, T, heads, 128] hold N sequences and of three one.  A sequence's queries
     are its last positions; window > 0 limits each to the last `window` keys."""
-    dt = q.dtype
-    if dt not in _ATTN_TYPES:
-        raise TypeError("kda_attn_prefill: inputs must be bfloat16 or float16")
-    q_ptr, q_row = _rows(q, dt, "q")
-    k_ptr, k_row = _rows(k, dt, "k")
-    v_ptr, v_row = _rows(v, dt, "v")
-    o_ptr, o_row = _rows(out, dt, "out")
-    heads, kv_heads = q.shape[-2], k.shape[-2]
-    if out.shape != q.shape or v.shape != k.shape or q.dim() != k.dim():
+    in_dtype, dev = _attn_type(q, "q")
+    dt, q_shape, k_shape = q.dtype, q.shape, k.shape
+    q_ptr, q_row = _rows(q, dt, dev, "q")
+    k_ptr, k_row = _rows(k, dt, dev, "k")
+    v_ptr, v_row = _rows(v, dt, dev, "v")
+    o_ptr, o_row = _rows(out, dt, dev, "out")
+    heads, kv_heads = q_shape[-2], k_shape[-2]
+    if out.shape != q_shape or v.shape != k_shape or len(q_shape) != len(k_shape):
         raise ValueError("kda_attn_prefill: out must have q's shape, v k's, and k q's dimensions")
-    _same_device(q, k, v, out, lse, cu_seqlens, cu_seqlens_k)
     cu_q = cu_k = None
+    t_q, t_k, n_seqs = q_shape[-3], k_shape[-3], 1
     if cu_seqlens is not None:
-        if q.dim() != 3:
+        if len(q_shape) != 3:
             raise ValueError("kda_attn_prefill: packed rows have three dimensions")
         n_seqs = cu_seqlens.numel() - 1
-        cu_q = _int32(cu_seqlens, None, "cu_seqlens")
-        cu_k = cu_q if cu_seqlens_k is None else _int32(cu_seqlens_k, n_seqs + 1, "cu_seqlens_k")
-        t_q, t_k = q.shape[0], k.shape[0]
+        cu_q = cu_k = _packed(cu_seqlens, torch.int32, dev, "cu_seqlens")
+        if cu_seqlens_k is not None:
+            cu_k = _packed(cu_seqlens_k, torch.int32, dev, "cu_seqlens_k")
+            if cu_seqlens_k.numel() != n_seqs + 1:
+                raise ValueError("kda_attn_prefill: cu_seqlens_k must be as long as cu_seqlens")
     elif cu_seqlens_k is not None:
         raise ValueError("kda_attn_prefill: cu_seqlens_k needs cu_seqlens")
-    else:
-        n_seqs = q.shape[0] if q.dim() == 4 else 1
-        if q.dim() == 4 and k.shape[0] != n_seqs:
+    elif len(q_shape) == 4:
+        n_seqs = q_shape[0]
+        if k_shape[0] != n_seqs:
             raise ValueError("kda_attn_prefill: q and k hold different numbers of sequences")
-        t_q, t_k = q.shape[-3], k.shape[-3]
     lse_ptr = None
     if lse is not None:
-        if lse.shape != q.shape[:-1]:
+        if lse.shape != q_shape[:-1]:
             raise ValueError("kda_attn_prefill: lse must be [rows, heads]")
-        _contig(lse, "lse")
-        lse_ptr = _ptr(lse, torch.float32, "lse")
-    need = 0
-    if workspace is None:
-        rows = t_q if cu_seqlens is not None else t_q * n_seqs
-        need = LIB.kda_attn_prefill_workspace_size(rows, n_seqs, heads, kv_heads)
-    ws, ws_ptr, ws_bytes = _scratch(workspace, need, q.device)
+        lse_ptr = _packed(lse, torch.float32, dev, "lse")
+    rows = t_q if cu_q else t_q * n_seqs
+    workspace, ws_ptr, ws_bytes = _scratch(
+        workspace,
+        lambda: LIB.kda_attn_prefill_workspace_size(rows, n_seqs, heads, kv_heads), dev)
     _check(LIB.kda_attn_prefill(q_ptr, k_ptr, v_ptr, o_ptr, lse_ptr, t_q, t_k, cu_q, cu_k, n_seqs,
-                                heads, kv_heads, HEAD_DIM, _ATTN_TYPES[dt], q_row, k_row, v_row,
-                                o_row, window, scale, ws_ptr, ws_bytes, _stream(q)))
+                                heads, kv_heads, HEAD_DIM, in_dtype, q_row, k_row, v_row, o_row,
+                                window, scale, ws_ptr, ws_bytes, _raw_stream(dev)))
 
 
 def kv4_cache(n_pages, kv_heads, page=64, device="cuda"):
@@ -553,45 +564,40 @@ def kv4_cache(n_pages, kv_heads, page=64, device="cuda"):
                        device=device)
 
 
-def _kv4(cache, page_table, lens):
+def _kv4(cache, page_table, lens, dev):
     """The cache arguments: (pointer, pages, tokens a page, table, width, lens)."""
-    if not cache.is_cuda or cache.dtype != torch.uint8 or cache.dim() != 3:
-        raise TypeError("the cache must be a CUDA uint8 [pages, kv_heads, page * 144] tensor")
-    _contig(cache, "cache")
-    page, rest = divmod(cache.shape[2], KV4_TOKEN_BYTES)
-    if rest or page not in KV4_PAGES:
-        raise ValueError("the cache's last dimension must be page * 144, page one of %s"
+    ptr, shape, table = _packed(cache, torch.uint8, dev, "cache"), cache.shape, page_table.shape
+    if len(shape) != 3 or shape[2] % KV4_TOKEN_BYTES or shape[2] // KV4_TOKEN_BYTES not in KV4_PAGES:
+        raise ValueError("the cache must be [pages, kv_heads, page * 144], page one of %s"
                          % (KV4_PAGES,))
-    if page_table.dim() != 2 or page_table.shape[0] != lens.numel():
+    if len(table) != 2 or table[0] != lens.numel():
         raise ValueError("page_table must be [sequences, pages], lens [sequences]")
-    _same_device(cache, page_table, lens)
-    return (cache.data_ptr(), cache.shape[0], page, _int32(page_table, None, "page_table"),
-            page_table.shape[1], _int32(lens, None, "lens"))
+    return (ptr, shape[0], shape[2] // KV4_TOKEN_BYTES,
+            _packed(page_table, torch.int32, dev, "page_table"), table[1],
+            _packed(lens, torch.int32, dev, "lens"))
 
 
 def _kv4_rows(name, fn, k, v, cache, page_table, lens, cu_seqlens):
-    dt = k.dtype
-    if dt not in _ATTN_TYPES:
-        raise TypeError("%s: rows must be bfloat16 or float16" % name)
-    k_ptr, k_row = _rows(k, dt, "k")
-    v_ptr, v_row = _rows(v, dt, "v")
-    c_ptr, n_pages, page, table, width, lens_ptr = _kv4(cache, page_table, lens)
-    n_seqs, kv_heads = lens.numel(), cache.shape[1]
-    if v.shape != k.shape or k.shape[-2] != kv_heads:
+    in_dtype, dev = _attn_type(k, "k")
+    k_ptr, k_row = _rows(k, k.dtype, dev, "k")
+    v_ptr, v_row = _rows(v, k.dtype, dev, "v")
+    cache_args = _kv4(cache, page_table, lens, dev)
+    shape, n_seqs, kv_heads = k.shape, page_table.shape[0], cache.shape[1]
+    if v.shape != shape or shape[-2] != kv_heads:
         raise ValueError("%s: k and v must be [rows, kv_heads, 128] of the cache's kv_heads" % name)
-    _same_device(cache, k, v, cu_seqlens)
     cu = None
     if cu_seqlens is not None:
-        cu, t = _int32(cu_seqlens, n_seqs + 1, "cu_seqlens"), k.shape[0]
-        if k.dim() != 3:
-            raise ValueError("%s: packed rows have three dimensions" % name)
+        if len(shape) != 3 or cu_seqlens.numel() != n_seqs + 1:
+            raise ValueError("%s: packed rows have three dimensions, and one offset more than "
+                             "sequences" % name)
+        cu, t = _packed(cu_seqlens, torch.int32, dev, "cu_seqlens"), shape[0]
     else:
-        rows = k.shape[0] * (k.shape[1] if k.dim() == 4 else 1)
-        if rows % n_seqs or (k.dim() == 4 and k.shape[0] != n_seqs):
+        rows = shape[0] * (shape[1] if len(shape) == 4 else 1)
+        if rows % n_seqs or (len(shape) == 4 and shape[0] != n_seqs):
             raise ValueError("%s: the rows do not divide over the sequences" % name)
         t = rows // n_seqs
-    _check(fn(k_ptr, v_ptr, k_row, v_row, t, cu, n_seqs, kv_heads, HEAD_DIM, _ATTN_TYPES[dt],
-              c_ptr, n_pages, page, table, width, lens_ptr, _stream(k)))
+    _check(fn(k_ptr, v_ptr, k_row, v_row, t, cu, n_seqs, kv_heads, HEAD_DIM, in_dtype, *cache_args,
+              _raw_stream(dev)))
 
 
 def kda_attn_kv4_append(k, v, cache, page_table, lens, cu_seqlens=None):
@@ -621,33 +627,26 @@ def kda_attn_kv4_decode(q, cache, page_table, lens, out, lse=None, window=0, sca
     """k query rows of each sequence over the 4-bit cache: q, out BF16 or FP16
     [N, k, heads, 128] (or [N, heads, 128]), the last k of lens[n] positions; lse
     FP32 [N, k, heads] or None."""
-    dt = q.dtype
-    if dt not in _ATTN_TYPES:
-        raise TypeError("kda_attn_kv4_decode: q must be bfloat16 or float16")
-    if q.dim() not in (3, 4) or q.shape[-1] != HEAD_DIM or out.shape != q.shape:
+    in_dtype, dev = _attn_type(q, "q")
+    shape = q.shape
+    if len(shape) not in (3, 4) or shape[-1] != HEAD_DIM or out.shape != shape:
         raise ValueError("kda_attn_kv4_decode: q and out must be [N, k, heads, 128]")
-    _contig(q, "q")
-    _contig(out, "out")
-    c_ptr, n_pages, page, table, width, lens_ptr = _kv4(cache, page_table, lens)
-    n_seqs, heads, kv_heads = q.shape[0], q.shape[-2], cache.shape[1]
-    krows = q.shape[1] if q.dim() == 4 else 1
-    if lens.numel() != n_seqs:
-        raise ValueError("kda_attn_kv4_decode: lens must hold one length per sequence")
-    _same_device(cache, q, out, lse)
+    q_ptr, o_ptr = _packed(q, q.dtype, dev, "q"), _packed(out, q.dtype, dev, "out")
+    c_ptr, n_pages, page, table, width, lens_ptr = _kv4(cache, page_table, lens, dev)
+    n_seqs, heads, kv_heads = shape[0], shape[-2], cache.shape[1]
+    krows = shape[1] if len(shape) == 4 else 1
+    if page_table.shape[0] != n_seqs:
+        raise ValueError("kda_attn_kv4_decode: page_table and lens must have q's sequences")
     lse_ptr = None
     if lse is not None:
-        if lse.shape != q.shape[:-1]:
+        if lse.shape != shape[:-1]:
             raise ValueError("kda_attn_kv4_decode: lse must be [N, k, heads]")
-        _contig(lse, "lse")
-        lse_ptr = _ptr(lse, torch.float32, "lse")
-    need = 0
-    if workspace is None:
-        need = LIB.kda_attn_kv4_workspace_size(n_seqs, krows, heads, kv_heads)
-    ws, ws_ptr, ws_bytes = _scratch(workspace, need, q.device)
-    _check(LIB.kda_attn_kv4_decode(_ptr(q, dt, "q"), c_ptr, n_pages, page, table, width, lens_ptr,
-                                   _ptr(out, dt, "out"), lse_ptr, n_seqs, krows, heads, kv_heads,
-                                   HEAD_DIM, _ATTN_TYPES[dt], window, scale, ws_ptr, ws_bytes,
-                                   _stream(q)))
+        lse_ptr = _packed(lse, torch.float32, dev, "lse")
+    workspace, ws_ptr, ws_bytes = _scratch(
+        workspace, lambda: LIB.kda_attn_kv4_workspace_size(n_seqs, krows, heads, kv_heads), dev)
+    _check(LIB.kda_attn_kv4_decode(q_ptr, c_ptr, n_pages, page, table, width, lens_ptr, o_ptr,
+                                   lse_ptr, n_seqs, krows, heads, kv_heads, HEAD_DIM, in_dtype,
+                                   window, scale, ws_ptr, ws_bytes, _raw_stream(dev)))
 
 
 def kda_sync_status(device=None):
