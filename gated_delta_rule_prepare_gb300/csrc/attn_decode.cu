@@ -46,23 +46,26 @@ using tc::mbar_wait;
 
 __device__ unsigned g_decode_status = 0;
 
-// A chunk is 8 groups of 16 tokens; each of a CTA's four warps takes two: with 8
-// query columns together, so that their products and weights run in each other's
-// waits, with 16 one after the other.  Several small CTAs to a multiprocessor,
-// not one large one: while one ends a segment the others go on.  The registers
-// that leaves a thread hold all it has; what spills costs more than anything else
-// here, as the rings leave next to no L1 cache.
+// A chunk is 8 groups of 16 tokens; each of a CTA's four warps takes two.
+// Several small CTAs to a multiprocessor, not one large one: while one ends a
+// segment the others go on (one of 12 warps: 116 us at 64 sequences of 2000 to
+// 8192 tokens, three of 4: 94.5).  A thread's registers hold all it has; what
+// spills costs more than anything else here, as the rings leave next to no L1
+// cache.
 constexpr int kWarps = 4;  // and one that copies
 constexpr int kThreads = (kWarps + 1) * 32;
-template <int NT>
-constexpr int kCtas = NT == 1 ? 3 : 2;
-template <int NT>
-constexpr int kStages = NT == 1 ? 3 : 4;
-template <int NT>
-constexpr int kIlp = NT == 1 ? 2 : 1;
+template <bool WIDE>
+constexpr int kCtas = WIDE ? 2 : 3;  // to a multiprocessor
+template <bool WIDE>
+constexpr int kStages = WIDE ? 4 : 3;
 constexpr int kGroups = 8;
 constexpr int kChunk = kGroups * 16;  // tokens
 constexpr int kStageBytes = kChunk * kTokenBytes;
+// Query rows of a block: where a KV head has up to 8 they are the columns of
+// the products with 16 keys, else 16 of them are the rows of the products with
+// 8 keys.
+template <bool WIDE>
+constexpr int kRows = WIDE ? 16 : 8;
 
 struct DecodeArgs {
     const uint16_t* q;
@@ -72,7 +75,7 @@ struct DecodeArgs {
     int group, rows, blocks;  // heads per KV head; query rows of a KV head; blocks of them
     float scale;
     int pieces;  // CTAs of the main kernel
-    float* part;  // [2 * pieces][8 * NT][128] sums, then [2 * pieces][8 * NT] (shift, l)
+    float* part;  // [2 * pieces][query row][128] sums, then [2 * pieces][query row] (shift, l)
     Cache c;
 };
 
@@ -128,7 +131,7 @@ __device__ __forceinline__ long long scan_lengths(const DecodeArgs& a, Each each
 }
 
 // What a stage of the ring holds.  A segment is what one CTA does of one
-// (sequence, head, block of 8 NT query rows).
+// (sequence, head, block of query rows).
 struct Stage {
     int pos;         // the chunk's first position
     uint32_t flags;  // bit i: tokens 16 i .. 16 i + 15 are in the stage; then:
@@ -139,26 +142,28 @@ struct Stage {
 constexpr uint32_t kStart = 1u << 24, kEnd = 1u << 25, kNoMore = 1u << 26;
 
 constexpr int kPad = 132;  // a query's 128 sums, so that a warp's stores meet all banks
-template <int NT>
+template <bool WIDE>
+constexpr int kBuffers = WIDE ? 1 : 2;
+template <bool WIDE>
 struct Shared {
-    uint64_t full[kStages<NT>], empty[kStages<NT>];
-    Stage stage[kStages<NT>];
-    // the segment's queries as B operands (FP16, scaled by a power of two); by
+    uint64_t full[kStages<WIDE>], empty[kStages<WIDE>];
+    Stage stage[kStages<WIDE>];
+    // the segment's queries as operands (FP16, scaled by a power of two); by
     // query, the factor from a product to a score in log2 units and the sums
     // over 64 channels
-    uint2 q[NT][8][32];
-    float unit[8 * NT];
-    float2 qsum[8 * NT];
+    alignas(16) uint32_t q[8][32][WIDE ? 4 : 2];
+    float unit[kRows<WIDE>];
+    float2 qsum[kRows<WIDE>];
     // its end
-    float2 stat[kWarps][8 * NT];  // a warp's (shift, l) by query
-    float factor[kWarps][8 * NT];
-    float2 joint[8 * NT];
-    float4 sums[2][8 * NT][kPad / 4];  // two warps' outputs at a time
+    float2 stat[kWarps][kRows<WIDE>];  // a warp's (shift, l) by query
+    float factor[kWarps][kRows<WIDE>];
+    float2 joint[kRows<WIDE>];
+    alignas(16) float sums[kBuffers<WIDE>][kRows<WIDE>][kPad];  // some warps' outputs at a time
     int stop;
 };
-template <int NT>
+template <bool WIDE>
 constexpr int smem_bytes() {
-    return kStages<NT> * kStageBytes + (int)sizeof(Shared<NT>);
+    return kStages<WIDE> * kStageBytes + (int)sizeof(Shared<WIDE>);
 }
 
 template <bool B>
@@ -167,8 +172,8 @@ struct Bool {
 };
 
 // Waits end: with the phase, with another role's giving up, or after 2^33 clocks.
-template <int NT>
-__device__ __forceinline__ bool wait_warp(Shared<NT>& sh, uint64_t* bar, uint32_t parity) {
+template <bool WIDE>
+__device__ __forceinline__ bool wait_warp(Shared<WIDE>& sh, uint64_t* bar, uint32_t parity) {
     bool ok = mbar_wait(bar, parity, 1);
     if (!ok) {
         const long long from = clock64();
@@ -191,9 +196,19 @@ __device__ __forceinline__ bool wait_warp(Shared<NT>& sh, uint64_t* bar, uint32_
 // COPYUS, 64 sequences of 2000 to 8192 tokens.)
 __device__ __forceinline__ int piece_tokens(const DecodeArgs& a) { return min(a.c.page(), 128); }
 
+// Where a stage's group of 16 tokens has its codes and parameters of K; those of
+// V are part_bytes(piece_tokens) further.
+__device__ __forceinline__ void group_places(const DecodeArgs& a, int group, int& codes_at,
+                                             int& pars_at) {
+    const int tok = group * 16, piece = piece_tokens(a);
+    const int in = tok & (piece - 1), block = (tok - in) * kTokenBytes;
+    codes_at = block + in * 64;
+    pars_at = block + piece * 64 + in * 8;
+}
+
 // The copying warp: walks this CTA's piece of the line.
-template <int NT>
-__device__ __forceinline__ void copy_role(const DecodeArgs& a, Shared<NT>& sh, uint8_t* sm) {
+template <bool WIDE>
+__device__ __forceinline__ void copy_role(const DecodeArgs& a, Shared<WIDE>& sh, uint8_t* sm) {
     const int lane = threadIdx.x & 31;
     const int heads = a.c.kv_heads, per_seq = heads * a.blocks;
     bool bad_len = false;
@@ -296,7 +311,7 @@ __device__ __forceinline__ void copy_role(const DecodeArgs& a, Shared<NT>& sh, u
                     }
                 }
                 __syncwarp();
-                if (++stage == kStages<NT>) stage = 0, phase ^= 1;
+                if (++stage == kStages<WIDE>) stage = 0, phase ^= 1;
             }
         }
         n_start += (long long)ch.count * per_seq;
@@ -309,7 +324,7 @@ __device__ __forceinline__ void copy_role(const DecodeArgs& a, Shared<NT>& sh, u
             mbar_arrive(&sh.full[stage]);
         } else {
             // copies in flight land before the CTA's memory goes away
-            for (int s = 0; s < kStages<NT>; ++s)
+            for (int s = 0; s < kStages<WIDE>; ++s)
                 mbar_wait(&sh.full[s], s < stage ? phase : phase ^ 1, 1 << 12);
         }
     }
@@ -330,6 +345,15 @@ __device__ __forceinline__ uint32_t sub_h2(uint32_t a, uint32_t b) {
     return r;
 }
 constexpr float kLow = 16777216.f, kHigh = 1048576.f;  // 2^24, 2^20
+// The same of code - 8: a rounding of a weight then meets at most eight steps.
+__device__ __forceinline__ void centred_codes(uint32_t w, uint32_t& lo0, uint32_t& hi0,
+                                              uint32_t& lo1, uint32_t& hi1) {
+    codes(w, lo0, hi0, lo1, hi1);
+    lo0 = sub_h2(lo0, 0x00080008u);  // 8 * 2^-24
+    hi0 = sub_h2(hi0, 0x00800080u);  // 8 * 2^-20
+    lo1 = sub_h2(lo1, 0x00080008u);
+    hi1 = sub_h2(hi1, 0x00800080u);
+}
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -363,39 +387,165 @@ __device__ __forceinline__ float pow2(int e) {  // -126 <= e <= 127
 }
 __device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23 & 255) - 127; }
 
-template <bool F16, int NT>
-__device__ __forceinline__ void attend_role(const DecodeArgs& a, Shared<NT>& sh,
-                                            const uint8_t* sm) {
-    constexpr int Q = 8 * NT;  // query columns
+// The segment's queries into shared memory, a row to a warp at a time, four
+// channels a lane.
+template <bool F16, bool WIDE>
+__device__ __forceinline__ void load_queries(const DecodeArgs& a, Shared<WIDE>& sh,
+                                             const Stage& st) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll 1
+    for (int r = warp; r < kRows<WIDE>; r += kWarps) {
+        const int row = st.block * kRows<WIDE> + r;
+        const int i = row / a.group, hh = row - i * a.group;
+        uint2 raw = make_uint2(0u, 0u);
+        if (row < a.rows)
+            raw = __ldg(reinterpret_cast<const uint2*>(
+                            a.q + (((long long)st.n * a.krows + i) * a.heads +
+                                   st.head * a.group + hh) * D) + lane);
+        float2 x = widen2<F16>(raw.x), y = widen2<F16>(raw.y);
+        float big = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y)));
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1)
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+        // bring the largest to 2^14..2^15: exact, and what is below FP16's
+        // smallest number then is 2^-34 of it
+        const bool plain = big == 0.f || !(big < INFINITY);
+        const int up = plain ? 0 : max(-126, min(126, 14 - exponent(big)));
+        const float f = pow2(up);
+        x.x *= f, x.y *= f, y.x *= f, y.y *= f;
+        float sum = (x.x + x.y) + (y.x + y.y);
+#pragma unroll
+        for (int off = 1; off < 16; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        // channel 16 kb + 8 j + 2 t + e: codes of j = 1 are the high four bits
+        const int kb = lane >> 2, j = lane >> 1 & 1, t0 = 2 * (lane & 1);
+        const float fj = j ? kHigh / kLow : 1.f;
+        const int word = WIDE ? (r >> 3) + 2 * j : j, at = (r & 7) * 4 + t0;
+        sh.q[kb][at][word] = narrow2<true>(x.x * fj, x.y * fj);
+        sh.q[kb][at + 1][word] = narrow2<true>(y.x * fj, y.y * fj);
+        if (lane == 0) {
+            sh.unit[r] = a.scale * kLog2e * kLow * pow2(-up);
+            sh.qsum[r].x = sum * (1.f / kLow);
+        }
+        if (lane == 16) sh.qsum[r].y = sum * (1.f / kLow);
+    }
+    consumer_sync();
+}
+
+// The segment's end: the warps' sums, whose (shift, l) are in sh.stat, become one
+// and go out.  `put` writes a warp's outputs, brought to the common shift, into a
+// buffer.
+template <bool F16, bool WIDE, class Put>
+__device__ __forceinline__ void finish_segment(const DecodeArgs& a, Shared<WIDE>& sh,
+                                               const Stage& st, Put put) {
+    constexpr int Q = kRows<WIDE>, B = kBuffers<WIDE>;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    consumer_sync();
+    if (tid < Q) {
+        // the least shift is that of the largest score
+        float least = INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            if (sh.stat[w][tid].y != 0.f) least = fminf(least, sh.stat[w][tid].x);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float2 x = sh.stat[w][tid];
+            const float f = x.y != 0.f ? ex2_approx(least - x.x) : 0.f;
+            sh.factor[w][tid] = f;
+            if (x.y != 0.f) sum = fmaf(x.y, f, sum);
+        }
+        sh.joint[tid] = make_float2(least, sum);
+    }
+    consumer_sync();
+    constexpr int kQuads = Q * 32 / (kWarps * 32);
+    float4 all[kQuads] = {};  // four channels of a query
+#pragma unroll 1
+    for (int first = 0; first < kWarps; first += B) {
+        if (warp >= first && warp < first + B) put(sh.sums[warp - first], sh.factor[warp]);
+        consumer_sync();
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i)
+#pragma unroll
+            for (int w = 0; w < B; ++w) {
+                const float4 x =
+                    reinterpret_cast<const float4*>(sh.sums[w][warp + kWarps * i])[lane];
+                all[i].x += x.x;
+                all[i].y += x.y;
+                all[i].z += x.z;
+                all[i].w += x.w;
+            }
+        consumer_sync();
+    }
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) {
+        const int c = warp + kWarps * i, row = st.block * Q + c;
+        const float2 joint = sh.joint[c];
+        const float4 x = all[i];
+        if (st.part >= 0) {
+            const long long at = (long long)st.part * Q + c;
+            reinterpret_cast<float4*>(a.part)[at * 32 + lane] = x;
+            if (lane == 0) reinterpret_cast<float2*>(a.part + 2LL * a.pieces * Q * D)[at] = joint;
+        } else if (row < a.rows) {
+            const float inv = joint.y == 0.f ? 0.f : 1.f / joint.y;
+            const int i_row = row / a.group;
+            const long long at = ((long long)st.n * a.krows + i_row) * a.heads +
+                                 st.head * a.group + row - i_row * a.group;
+            reinterpret_cast<uint2*>(a.o + at * D)[lane] =
+                make_uint2(narrow2<F16>(x.x * inv, x.y * inv), narrow2<F16>(x.z * inv, x.w * inv));
+            if (a.lse && lane == 0)
+                a.lse[at] = joint.y == 0.f ? -INFINITY : (log2f(joint.y) - joint.x) * kLn2;
+        }
+    }
+}
+
+// A token's step and minimum of 64 channels.
+__device__ __forceinline__ float step_of(uint32_t par) { return __uint_as_float(par << 16); }
+__device__ __forceinline__ float least_of(uint32_t par) {
+    return __uint_as_float(par & 0xffff0000u);
+}
+
+// What both forms keep of a query: weights are 2^(score + shift), at most 2^7; l
+// sums them, moff weights times m + 8 s, by 64 channels.
+struct Query {
+    float shift, l, moff[2];
+};
+// The power of two that steps enter with, below 2^8 then.
+struct Unit {
+    float v = 1.f;
+    // brings it down (or, `anew`, up as well) for steps that are `most` with it;
+    // returns what that multiplies them by
+    __device__ __forceinline__ float fit(float most, bool anew) {
+        if (!(most > 0.f && most < INFINITY && (anew || most >= 256.f))) return 1.f;
+        const int was = exponent(v), now = max(-126, min(126, was + 6 - exponent(most)));
+        v = pow2(now);
+        return pow2(max(-126, min(126, now - was)));
+    }
+};
+
+// Up to 8 queries, the columns 2 t + c of a lane; keys, and then value channels,
+// are the 16 rows g and g + 8.  Two groups of 16 tokens at a time, so that their
+// products and weights run in each other's waits.
+template <bool F16>
+__device__ __forceinline__ void attend_narrow(const DecodeArgs& a, Shared<false>& sh,
+                                              const uint8_t* sm) {
+    constexpr int I = 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
-    constexpr int I = kIlp<NT>;
+    const int mine = I * warp;
     // where this warp's groups of a stage are: codes, parameters, of K; of V by
     // `to_v` further
-    constexpr int N = kGroups / kWarps;
-    int codes_at[N], pars_at[N];
+    int codes_at[I], pars_at[I];
     const int to_v = part_bytes(piece_tokens(a));
 #pragma unroll
-    for (int u = 0; u < N; ++u) {
-        const int tok = (N * warp + u) * 16, piece = piece_tokens(a);
-        const int in = tok & (piece - 1), block = (tok - in) * kTokenBytes;
-        codes_at[u] = block + in * 64;
-        pars_at[u] = block + piece * 64 + in * 8;
-    }
-    int stage = 0;
+    for (int u = 0; u < I; ++u) group_places(a, mine + u, codes_at[u], pars_at[u]);
+    int stage = 0, len = 0;
     uint32_t phase = 0;
-    // with 8 query columns in registers, with 16 read again for each group
-    uint2 qb[NT == 1 ? 8 : 1];
-    float unit[NT == 1 ? 2 : 1], qsum[NT == 1 ? 2 : 1][2];
-    (void)qb, (void)unit, (void)qsum;
-    int len = 0;
-    float out[NT][8][4];
-    // weights are 2^(score + shift), at most 2^7; l sums them, moff weights times
-    // m + 8 s, by 64 channels; steps enter times v_unit, below 2^8 then
-    float shift[NT][2], l[NT][2], moff[NT][2][2], v_unit = 1.f;
+    uint2 qb[8];
+    float unit[2], qsum[2][2], out[8][4];
+    Query state[2];
+    Unit v_unit;
     bool settled = false;  // every column has a shift that comes from a score
-    auto limit_of = [&](int block, int nt, int c) {  // positions from it on are not seen
-        const int row = block * Q + nt * 8 + 2 * t + c;
+    auto limit_of = [&](int block, int c) {  // positions from it on are not seen
+        const int row = block * 8 + 2 * t + c;
         return row < a.rows ? len - a.krows + row / a.group + 1 : 0;
     };
     for (;;) {
@@ -406,154 +556,76 @@ __device__ __forceinline__ void attend_role(const DecodeArgs& a, Shared<NT>& sh,
             const Stage st = sh.stage[stage];
             len = st.len;
             settled = false;
-#pragma unroll 1
-            for (int r = warp; r < Q; r += kWarps) {  // a query row, four channels a lane
-                const int row = st.block * Q + r;
-                const int i = row / a.group, hh = row - i * a.group;
-                uint2 raw = make_uint2(0u, 0u);
-                if (row < a.rows)
-                    raw = __ldg(reinterpret_cast<const uint2*>(
-                                    a.q + (((long long)st.n * a.krows + i) * a.heads +
-                                           st.head * a.group + hh) * D) + lane);
-                float2 x = widen2<F16>(raw.x), y = widen2<F16>(raw.y);
-                float big = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y)));
+            load_queries<F16>(a, sh, st);
 #pragma unroll
-                for (int off = 1; off < 32; off <<= 1)
-                    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
-                // bring the largest to 2^14..2^15: exact, and what is below FP16's
-                // smallest number then is 2^-34 of it
-                const bool plain = big == 0.f || !(big < INFINITY);
-                const int up = plain ? 0 : max(-126, min(126, 14 - exponent(big)));
-                const float f = pow2(up);
-                x.x *= f, x.y *= f, y.x *= f, y.y *= f;
-                float sum = (x.x + x.y) + (y.x + y.y);
+            for (int k = 0; k < 8; ++k) qb[k] = *reinterpret_cast<const uint2*>(sh.q[k][lane]);
 #pragma unroll
-                for (int off = 1; off < 16; off <<= 1)
-                    sum += __shfl_xor_sync(0xffffffffu, sum, off);
-                // channel 16 kb + 8 j + 2 t + e: codes of j = 1 are the high four bits
-                const int kb = lane >> 2, j = lane >> 1 & 1, t0 = 2 * (lane & 1);
-                const float fj = j ? kHigh / kLow : 1.f;
-                uint32_t* dst = reinterpret_cast<uint32_t*>(&sh.q[r >> 3][kb][(r & 7) * 4 + t0]);
-                dst[j] = narrow2<true>(x.x * fj, x.y * fj);
-                dst[2 + j] = narrow2<true>(y.x * fj, y.y * fj);
-                if (lane == 0) {
-                    sh.unit[r] = a.scale * kLog2e * kLow * pow2(-up);
-                    sh.qsum[r].x = sum * (1.f / kLow);
-                }
-                if (lane == 16) sh.qsum[r].y = sum * (1.f / kLow);
-            }
-            consumer_sync();
-            if constexpr (NT == 1) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) qb[k] = sh.q[0][k][lane];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    unit[c] = sh.unit[2 * t + c];
-                    qsum[c][0] = sh.qsum[2 * t + c].x;
-                    qsum[c][1] = sh.qsum[2 * t + c].y;
-                }
+            for (int c = 0; c < 2; ++c) {
+                unit[c] = sh.unit[2 * t + c];
+                qsum[c][0] = sh.qsum[2 * t + c].x;
+                qsum[c][1] = sh.qsum[2 * t + c].y;
+                state[c] = {};
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
+            for (int cb = 0; cb < 8; ++cb)
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    shift[nt][c] = l[nt][c] = moff[nt][c][0] = moff[nt][c][1] = 0.f;
-#pragma unroll
-                for (int cb = 0; cb < 8; ++cb)
-#pragma unroll
-                    for (int i4 = 0; i4 < 4; ++i4) out[nt][cb][i4] = 0.f;
-            }
+                for (int i = 0; i < 4; ++i) out[cb][i] = 0.f;
         }
-#pragma unroll 1
-        for (int first = 0; first < N; first += I) {
-            const int mine = N * warp + first;
-            // a group that is not there, behind one that is: its tokens are masked
-            if (!(flags >> mine & ((1u << I) - 1))) continue;
-            // (queries are read again for each group, not kept)
-            asm volatile("" ::: "memory");
+        const uint32_t there = flags >> mine & ((1u << I) - 1);
+        if (there) {
             const int pos = sh.stage[stage].pos + 16 * mine;
-            int ca_at[I], pa_at[I];
-#pragma unroll
-            for (int u = 0; u < I; ++u) {
-                ca_at[u] = codes_at[u];
-                pa_at[u] = pars_at[u];
-#pragma unroll
-                for (int x = 1; x < N; ++x)
-                    if (I == 1 && first == x) ca_at[u] = codes_at[x], pa_at[u] = pars_at[x];
-            }
             const uint8_t* base = sm + stage * kStageBytes;
             // scores of tokens g and g + 8 of each group
-            float y[I][NT][4];
+            float y[I][4];
             {
-                float acc[I][NT][2][4] = {};
+                float acc[I][2][4] = {};
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int u = 0; u < I; ++u) {
-                        const uint4 x = reinterpret_cast<const uint4*>(
-                            base + ca_at[u])[lane + 32 * h];
+                        const uint4 x =
+                            reinterpret_cast<const uint4*>(base + codes_at[u])[lane + 32 * h];
                         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             uint32_t ca[4];
                             codes(w[k], ca[0], ca[2], ca[1], ca[3]);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                const uint2 b =
-                                    NT == 1 ? qb[4 * h + k] : sh.q[nt][4 * h + k][lane];
-                                mma_f16(acc[u][nt][h], ca, b.x, b.y);
-                            }
+                            mma_f16(acc[u][h], ca, qb[4 * h + k].x, qb[4 * h + k].y);
                         }
                     }
 #pragma unroll
                 for (int u = 0; u < I; ++u)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint2 par = reinterpret_cast<const uint2*>(
-                            base + pa_at[u])[g + 8 * i];
-                        const float sa = __uint_as_float(par.x << 16);
-                        const float ma = __uint_as_float(par.x & 0xffff0000u);
-                        const float sb = __uint_as_float(par.y << 16);
-                        const float mb = __uint_as_float(par.y & 0xffff0000u);
+                        const uint2 par =
+                            reinterpret_cast<const uint2*>(base + pars_at[u])[g + 8 * i];
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                float un, q0, q1;
-                                if constexpr (NT == 1) {
-                                    un = unit[c], q0 = qsum[c][0], q1 = qsum[c][1];
-                                } else {
-                                    const float2 qs = sh.qsum[8 * nt + 2 * t + c];
-                                    un = sh.unit[8 * nt + 2 * t + c], q0 = qs.x, q1 = qs.y;
-                                }
-                                float d = ma * q0;
-                                d = fmaf(mb, q1, d);
-                                d = fmaf(sa, acc[u][nt][0][2 * i + c], d);
-                                d = fmaf(sb, acc[u][nt][1][2 * i + c], d);
-                                y[u][nt][2 * i + c] = fmaf(d, un, shift[nt][c]);
-                            }
+                        for (int c = 0; c < 2; ++c) {
+                            float d = least_of(par.x) * qsum[c][0];
+                            d = fmaf(least_of(par.y), qsum[c][1], d);
+                            d = fmaf(step_of(par.x), acc[u][0][2 * i + c], d);
+                            d = fmaf(step_of(par.y), acc[u][1][2 * i + c], d);
+                            y[u][2 * i + c] = fmaf(d, unit[c], state[c].shift);
+                        }
                     }
             }
+            // (a group that is not there, behind one that is, is masked whole)
             const bool edge = pos + 16 * I > len - a.krows + 1 ||
-                              (a.window && pos < len - a.window) ||
-                              (flags >> mine & ((1u << I) - 1)) != (1u << I) - 1;
+                              (a.window && pos < len - a.window) || there != (1u << I) - 1;
             if (edge) {
                 const int block = sh.stage[stage].block;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int c = 0; c < 2; ++c) {
+                    const int hi = limit_of(block, c), lo = a.window ? max(0, hi - a.window) : 0;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int hi = limit_of(block, nt, c);
-                        const int lo = a.window ? max(0, hi - a.window) : 0;
+                    for (int u = 0; u < I; ++u)
 #pragma unroll
-                        for (int u = 0; u < I; ++u)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int at = pos + 16 * u + g + 8 * i;
-                                if (at < lo || at >= hi || !(flags >> (mine + u) & 1))
-                                    y[u][nt][2 * i + c] = -INFINITY;
-                            }
-                    }
+                        for (int i = 0; i < 2; ++i) {
+                            const int at = pos + 16 * u + g + 8 * i;
+                            if (at < lo || at >= hi || !(there >> u & 1))
+                                y[u][2 * i + c] = -INFINITY;
+                        }
+                }
             }
             uint2 vpar[I][2];
             float vs[I][2][2], most = 0.f;
@@ -561,106 +633,77 @@ __device__ __forceinline__ void attend_role(const DecodeArgs& a, Shared<NT>& sh,
             for (int u = 0; u < I; ++u)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    vpar[u][i] = reinterpret_cast<const uint2*>(
-                        base + to_v + pa_at[u])[g + 8 * i];
-                    vs[u][i][0] = __uint_as_float(vpar[u][i].x << 16) * v_unit;
-                    vs[u][i][1] = __uint_as_float(vpar[u][i].y << 16) * v_unit;
+                    vpar[u][i] =
+                        reinterpret_cast<const uint2*>(base + to_v + pars_at[u])[g + 8 * i];
+                    vs[u][i][0] = step_of(vpar[u][i].x) * v_unit.v;
+                    vs[u][i][1] = step_of(vpar[u][i].y) * v_unit.v;
                     // whatever the cache holds behind a sequence's end
-                    if (edge && (pos + 16 * u + g + 8 * i >= len || !(flags >> (mine + u) & 1)))
+                    if (edge && (pos + 16 * u + g + 8 * i >= len || !(there >> u & 1)))
                         vs[u][i][0] = vs[u][i][1] = 0.f;
                     most = fmaxf(most, fmaxf(vs[u][i][0], vs[u][i][1]));
                 }
-            bool over = !settled || most >= 256.f;
-            float tops[NT][2];
+            float tops[2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    tops[nt][c] = fmaxf(y[0][nt][c], y[0][nt][2 + c]);
-#pragma unroll
-                    for (int u = 1; u < I; ++u)
-                        tops[nt][c] = fmaxf(fmaxf(tops[nt][c], y[u][nt][c]), y[u][nt][2 + c]);
-                    over |= tops[nt][c] > 7.f;
-                }
-            if (__any_sync(0xffffffffu, over)) {
+            for (int c = 0; c < 2; ++c)
+                tops[c] = fmaxf(fmaxf(y[0][c], y[0][2 + c]), fmaxf(y[1][c], y[1][2 + c]));
+            if (__any_sync(0xffffffffu,
+                           !settled || most >= 256.f || tops[0] > 7.f || tops[1] > 7.f)) {
                 // shifts: from the first scores of a column, and again once a
                 // weight would pass 2^7; the steps' unit likewise
-                most = max_keys(most);
-                float fv = 1.f;
-                if (most > 0.f && most < INFINITY && (!settled || most >= 256.f)) {
-                    const int was = exponent(v_unit);
-                    const int now = max(-126, min(126, was + 6 - exponent(most)));
-                    v_unit = pow2(now);
-                    fv = pow2(max(-126, min(126, now - was)));
+                const float fv = v_unit.fit(max_keys(most), !settled);
 #pragma unroll
-                    for (int u = 0; u < I; ++u)
+                for (int u = 0; u < I; ++u)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            vs[u][i][0] *= fv;
-                            vs[u][i][1] *= fv;
-                        }
-                }
+                    for (int i = 0; i < 2; ++i) vs[u][i][0] *= fv, vs[u][i][1] *= fv;
                 bool all = true;
                 const int block = sh.stage[stage].block;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int c = 0; c < 2; ++c) {
+                    Query& q = state[c];
+                    const float top = max_keys(tops[c]);
+                    const bool fresh = sum_keys(q.l) == 0.f;
+                    const bool move = top > -INFINITY && (fresh || top > 7.f);
+                    const float f = fresh || !move ? 1.f : ex2_approx(-top);
+                    if (move) {
+                        q.shift -= top;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const float top = max_keys(tops[nt][c]);
-                        const bool fresh = sum_keys(l[nt][c]) == 0.f;
-                        const bool move = top > -INFINITY && (fresh || top > 7.f);
-                        const float f = fresh || !move ? 1.f : ex2_approx(-top);
-                        if (move) {
-                            shift[nt][c] -= top;
-#pragma unroll
-                            for (int u = 0; u < I; ++u) {
-                                y[u][nt][c] -= top;
-                                y[u][nt][2 + c] -= top;
-                            }
-                        }
-                        l[nt][c] *= f;
-                        moff[nt][c][0] *= f;
-                        moff[nt][c][1] *= f;
-#pragma unroll
-                        for (int cb = 0; cb < 8; ++cb) {
-                            out[nt][cb][c] *= f * fv;
-                            out[nt][cb][2 + c] *= f * fv;
-                        }
-                        // a column that will see a key later has no shift yet
-                        all &= !fresh || move || limit_of(block, nt, c) <= pos + 16 * I;
+                        for (int u = 0; u < I; ++u) y[u][c] -= top, y[u][2 + c] -= top;
                     }
+                    q.l *= f;
+                    q.moff[0] *= f;
+                    q.moff[1] *= f;
+#pragma unroll
+                    for (int cb = 0; cb < 8; ++cb) out[cb][c] *= f * fv, out[cb][2 + c] *= f * fv;
+                    // a column that will see a key later has no shift yet
+                    all &= !fresh || move || limit_of(block, c) <= pos + 16 * I;
+                }
                 settled = __all_sync(0xffffffffu, all);
             }
             // weights, and with the values' steps the second product's B operand
-            uint32_t pb[I][NT][2][2];  // [64 channels][tokens 0..7, 8..15]
+            uint32_t pb[I][2][2];  // [64 channels][tokens 0..7, 8..15]
             auto weigh = [&](auto masked) {
 #pragma unroll
                 for (int u = 0; u < I; ++u)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint2 par = vpar[u][i];
-                        const float m0 = fmaf(8.f, __uint_as_float(par.x << 16),
-                                              __uint_as_float(par.x & 0xffff0000u));
-                        const float m1 = fmaf(8.f, __uint_as_float(par.y << 16),
-                                              __uint_as_float(par.y & 0xffff0000u));
+                        const float m0 = fmaf(8.f, step_of(par.x), least_of(par.x));
+                        const float m1 = fmaf(8.f, step_of(par.y), least_of(par.y));
+                        float w[2][2];
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            float w[2][2];
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                const float x = y[u][nt][2 * i + c], p = ex2_approx(x);
-                                // what a column does not see has no influence on it,
-                                // a step or minimum that is NaN included
-                                const bool none = decltype(masked)::value && x == -INFINITY;
-                                l[nt][c] += p;
-                                moff[nt][c][0] = fmaf(p, none ? 0.f : m0, moff[nt][c][0]);
-                                moff[nt][c][1] = fmaf(p, none ? 0.f : m1, moff[nt][c][1]);
-                                w[c][0] = p * (none ? 0.f : vs[u][i][0]);
-                                w[c][1] = p * (none ? 0.f : vs[u][i][1]);
-                            }
-                            pb[u][nt][0][i] = transpose8(narrow2<true>(w[0][0], w[1][0]));
-                            pb[u][nt][1][i] = transpose8(narrow2<true>(w[0][1], w[1][1]));
+                        for (int c = 0; c < 2; ++c) {
+                            const float x = y[u][2 * i + c], p = ex2_approx(x);
+                            // what a column does not see has no influence on it, a
+                            // step or minimum that is NaN included
+                            const bool none = decltype(masked)::value && x == -INFINITY;
+                            state[c].l += p;
+                            state[c].moff[0] = fmaf(p, none ? 0.f : m0, state[c].moff[0]);
+                            state[c].moff[1] = fmaf(p, none ? 0.f : m1, state[c].moff[1]);
+                            w[c][0] = p * (none ? 0.f : vs[u][i][0]);
+                            w[c][1] = p * (none ? 0.f : vs[u][i][1]);
                         }
+                        pb[u][0][i] = transpose8(narrow2<true>(w[0][0], w[1][0]));
+                        pb[u][1][i] = transpose8(narrow2<true>(w[0][1], w[1][1]));
                     }
             };
             if (edge) weigh(Bool<true>{});
@@ -669,20 +712,14 @@ __device__ __forceinline__ void attend_role(const DecodeArgs& a, Shared<NT>& sh,
             for (int u = 0; u < I; ++u)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint4 x = reinterpret_cast<const uint4*>(
-                        base + to_v + ca_at[u])[lane + 32 * h];
+                    const uint4 x =
+                        reinterpret_cast<const uint4*>(base + to_v + codes_at[u])[lane + 32 * h];
                     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t ca[4];
-                        codes(w[k], ca[0], ca[1], ca[2], ca[3]);
-                        ca[0] = sub_h2(ca[0], 0x00080008u);  // 8 * 2^-24
-                        ca[1] = sub_h2(ca[1], 0x00800080u);  // 8 * 2^-20
-                        ca[2] = sub_h2(ca[2], 0x00080008u);
-                        ca[3] = sub_h2(ca[3], 0x00800080u);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma_f16(out[nt][4 * h + k], ca, pb[u][nt][h][0], pb[u][nt][h][1]);
+                        centred_codes(w[k], ca[0], ca[1], ca[2], ca[3]);
+                        mma_f16(out[4 * h + k], ca, pb[u][h][0], pb[u][h][1]);
                     }
                 }
         }
@@ -692,112 +729,286 @@ __device__ __forceinline__ void attend_role(const DecodeArgs& a, Shared<NT>& sh,
         if (end) st = sh.stage[stage];
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.empty[stage]);
-        if (++stage == kStages<NT>) stage = 0, phase ^= 1;
+        if (++stage == kStages<false>) stage = 0, phase ^= 1;
         if (!end) continue;
-
-        // The segment's end: the warps' sums become one.  (In short code: what
-        // runs once a segment is fetched anew each time, and unrolled over a
-        // thread's sums it took 7 us, with 16 columns 30.)
-        const int tid = threadIdx.x;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int c = 0; c < 2; ++c) {
+            Query& q = state[c];
+            q.l = sum_keys(q.l);
+            q.moff[0] = sum_keys(q.moff[0]);
+            q.moff[1] = sum_keys(q.moff[1]);
+            if (g == 0) sh.stat[warp][2 * t + c] = make_float2(q.shift, q.l);
+        }
+        finish_segment<F16>(a, sh, st, [&](float (*sums)[kPad], const float* factor) {
+            const float low = kLow / v_unit.v, high = kHigh / v_unit.v;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                l[nt][c] = sum_keys(l[nt][c]);
-                moff[nt][c][0] = sum_keys(moff[nt][c][0]);
-                moff[nt][c][1] = sum_keys(moff[nt][c][1]);
-                if (g == 0) sh.stat[warp][nt * 8 + 2 * t + c] = make_float2(shift[nt][c], l[nt][c]);
-            }
-        consumer_sync();
-        if (tid < Q) {
-            // the least shift is that of the largest score
-            float least = INFINITY, sum = 0.f;
-#pragma unroll 1
-            for (int w = 0; w < kWarps; ++w)
-                if (sh.stat[w][tid].y != 0.f) least = fminf(least, sh.stat[w][tid].x);
-#pragma unroll 1
-            for (int w = 0; w < kWarps; ++w) {
-                const float2 x = sh.stat[w][tid];
-                const float f = x.y != 0.f ? ex2_approx(least - x.x) : 0.f;
-                sh.factor[w][tid] = f;
-                if (x.y != 0.f) sum = fmaf(x.y, f, sum);
-            }
-            sh.joint[tid] = make_float2(least, sum);
-        }
-        consumer_sync();
-        const float low = kLow / v_unit, high = kHigh / v_unit;
-        constexpr int kQuads = (Q * 32 + kWarps * 32 - 1) / (kWarps * 32);
-        float4 all[kQuads] = {};  // four channels of a query
-#pragma unroll 1
-        for (int first = 0; first < kWarps; first += 2) {
-            if (warp >= first && warp < first + 2) {
+                const float f = factor[2 * t + c];
+                float* dst = sums[2 * t + c] + g;
+                const bool some = state[c].l != 0.f;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int col = nt * 8 + 2 * t + c;
-                        const float f = sh.factor[warp][col];
-                        float* dst = reinterpret_cast<float*>(sh.sums[warp - first][col]) + g;
-                        const bool some = l[nt][c] != 0.f;
-#pragma unroll
-                        for (int cb = 0; cb < 8; ++cb) {
-                            const float m = moff[nt][c][cb >> 2];
-                            const float x = fmaf(out[nt][cb][c], low, m) * f;
-                            const float y = fmaf(out[nt][cb][2 + c], high, m) * f;
-                            dst[16 * cb] = some ? x : 0.f;
-                            dst[16 * cb + 8] = some ? y : 0.f;
-                        }
-                    }
-            }
-            consumer_sync();
-#pragma unroll
-            for (int i = 0; i < kQuads; ++i) {
-                const int quad = tid + i * kWarps * 32;
-                if (quad >= Q * 32) break;
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const float4 x = sh.sums[w][quad >> 5][quad & 31];
-                    all[i].x += x.x;
-                    all[i].y += x.y;
-                    all[i].z += x.z;
-                    all[i].w += x.w;
+                for (int cb = 0; cb < 8; ++cb) {
+                    const float m = state[c].moff[cb >> 2];
+                    const float x = fmaf(out[cb][c], low, m) * f;
+                    const float z = fmaf(out[cb][2 + c], high, m) * f;
+                    dst[16 * cb] = some ? x : 0.f;
+                    dst[16 * cb + 8] = some ? z : 0.f;
                 }
             }
-            consumer_sync();
-        }
-#pragma unroll
-        for (int i = 0; i < kQuads; ++i) {
-            const int quad = tid + i * kWarps * 32;
-            if (quad >= Q * 32) break;
-            const int c = quad >> 5, row = st.block * Q + c;
-            const float2 joint = sh.joint[c];
-            const float4 x = all[i];
-            if (st.part >= 0) {
-                const long long at = (long long)st.part * Q + c;
-                reinterpret_cast<float4*>(a.part)[at * 32 + lane] = x;
-                if (lane == 0)
-                    reinterpret_cast<float2*>(a.part + 2LL * a.pieces * Q * D)[at] = joint;
-            } else if (row < a.rows) {
-                const float inv = joint.y == 0.f ? 0.f : 1.f / joint.y;
-                const int i_row = row / a.group;
-                const long long at = ((long long)st.n * a.krows + i_row) * a.heads +
-                                     st.head * a.group + row - i_row * a.group;
-                reinterpret_cast<uint2*>(a.o + at * D)[lane] = make_uint2(
-                    narrow2<F16>(x.x * inv, x.y * inv), narrow2<F16>(x.z * inv, x.w * inv));
-                if (a.lse && lane == 0)
-                    a.lse[at] = joint.y == 0.f ? -INFINITY : (log2f(joint.y) - joint.x) * kLn2;
-            }
-        }
+        });
     }
 }
 
-template <bool F16, int NT>
-__global__ void __launch_bounds__(kThreads, kCtas<NT>) attn_decode_kernel(DecodeArgs a) {
+// Sixteen queries, the rows g and g + 8; keys, and then value channels, are the
+// eight columns of two products: the same words of codes are B operands here,
+// keys 0..7 and 8..15 (or channels) of the low and the high four bits.  A lane's
+// scores are keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9, which as they are make the A
+// operand of the second product.
+template <bool F16>
+__device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& sh,
+                                            const uint8_t* sm) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const int to_v = part_bytes(piece_tokens(a));
+    int stage = 0, len = 0;
+    uint32_t phase = 0;
+    float unit[2], qsum[2][2], out[16][4];  // channels 8 n + 2 t + e
+    Query state[2];
+    Unit v_unit;
+    bool settled = false;
+    auto limit_of = [&](int block, int i) {
+        const int row = block * 16 + g + 8 * i;
+        return row < a.rows ? len - a.krows + row / a.group + 1 : 0;
+    };
+    // over the four lanes that hold the other keys of the same queries
+    auto max4 = [](float x) {
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+    };
+    auto sum4 = [](float x) {
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        return x + __shfl_xor_sync(0xffffffffu, x, 2);
+    };
+    for (;;) {
+        if (!wait_warp(sh, &sh.full[stage], phase)) return;
+        const uint32_t flags = sh.stage[stage].flags;
+        if (flags & kNoMore) return;
+        if (flags & kStart) {
+            const Stage st = sh.stage[stage];
+            len = st.len;
+            settled = false;
+            load_queries<F16>(a, sh, st);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                unit[i] = sh.unit[g + 8 * i];
+                qsum[i][0] = sh.qsum[g + 8 * i].x;
+                qsum[i][1] = sh.qsum[g + 8 * i].y;
+                state[i] = {};
+            }
+#pragma unroll
+            for (int n = 0; n < 16; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) out[n][i] = 0.f;
+        }
+#pragma unroll 1
+        for (int mine = 2 * warp; mine < 2 * warp + 2; ++mine) {
+            if (!(flags >> mine & 1)) continue;
+            // (queries are read again for each group, not kept)
+            asm volatile("" ::: "memory");
+            const int pos = sh.stage[stage].pos + 16 * mine;
+            const uint8_t* base = sm + stage * kStageBytes;
+            int codes_at, pars_at;
+            group_places(a, mine, codes_at, pars_at);
+            float y[2][4];  // [keys 0..7, 8..15][2 i + e]
+            {
+                float acc[2][2][4] = {};  // [keys][64 channels]
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint4 x = reinterpret_cast<const uint4*>(base + codes_at)[lane + 32 * h];
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint4 q4 = *reinterpret_cast<const uint4*>(sh.q[4 * h + k][lane]);
+                        const uint32_t qa[4] = {q4.x, q4.y, q4.z, q4.w};
+                        uint32_t lo0, hi0, lo1, hi1;
+                        codes(w[k], lo0, hi0, lo1, hi1);
+                        mma_f16(acc[0][h], qa, lo0, hi0);
+                        mma_f16(acc[1][h], qa, lo1, hi1);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    // of keys 8 j + 2 t and the next
+                    const uint4 par = *reinterpret_cast<const uint4*>(base + pars_at +
+                                                                      (8 * j + 2 * t) * 8);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t p0 = e ? par.z : par.x, p1 = e ? par.w : par.y;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float d = least_of(p0) * qsum[i][0];
+                            d = fmaf(least_of(p1), qsum[i][1], d);
+                            d = fmaf(step_of(p0), acc[j][0][2 * i + e], d);
+                            d = fmaf(step_of(p1), acc[j][1][2 * i + e], d);
+                            y[j][2 * i + e] = fmaf(d, unit[i], state[i].shift);
+                        }
+                    }
+                }
+            }
+            const bool edge =
+                pos + 16 > len - a.krows + 1 || (a.window && pos < len - a.window);
+            if (edge) {
+                const int block = sh.stage[stage].block;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int hi = limit_of(block, i), lo = a.window ? max(0, hi - a.window) : 0;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int at = pos + 8 * j + 2 * t + e;
+                            if (at < lo || at >= hi) y[j][2 * i + e] = -INFINITY;
+                        }
+                }
+            }
+            uint4 vpar[2];
+            float vs[2][2][2], most = 0.f;  // [keys][e][64 channels]
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                vpar[j] = *reinterpret_cast<const uint4*>(base + to_v + pars_at +
+                                                          (8 * j + 2 * t) * 8);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    vs[j][e][0] = step_of(e ? vpar[j].z : vpar[j].x) * v_unit.v;
+                    vs[j][e][1] = step_of(e ? vpar[j].w : vpar[j].y) * v_unit.v;
+                    if (edge && pos + 8 * j + 2 * t + e >= len) vs[j][e][0] = vs[j][e][1] = 0.f;
+                    most = fmaxf(most, fmaxf(vs[j][e][0], vs[j][e][1]));
+                }
+            }
+            float tops[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                tops[i] = fmaxf(fmaxf(y[0][2 * i], y[0][2 * i + 1]),
+                                fmaxf(y[1][2 * i], y[1][2 * i + 1]));
+            if (__any_sync(0xffffffffu,
+                           !settled || most >= 256.f || tops[0] > 7.f || tops[1] > 7.f)) {
+                // (all lanes agree on the unit: the steps of a group are theirs together)
+                float all_most = max4(most);
+                const float fv = v_unit.fit(all_most, !settled);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) vs[j][e][0] *= fv, vs[j][e][1] *= fv;
+                bool all = true;
+                const int block = sh.stage[stage].block;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    Query& q = state[i];
+                    const float top = max4(tops[i]);
+                    const bool fresh = sum4(q.l) == 0.f;
+                    const bool move = top > -INFINITY && (fresh || top > 7.f);
+                    const float f = fresh || !move ? 1.f : ex2_approx(-top);
+                    if (move) {
+                        q.shift -= top;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) y[j][2 * i] -= top, y[j][2 * i + 1] -= top;
+                    }
+                    q.l *= f;
+                    q.moff[0] *= f;
+                    q.moff[1] *= f;
+#pragma unroll
+                    for (int n = 0; n < 16; ++n)
+                        out[n][2 * i] *= f * fv, out[n][2 * i + 1] *= f * fv;
+                    all &= !fresh || move || limit_of(block, i) <= pos + 16;
+                }
+                settled = __all_sync(0xffffffffu, all);
+            }
+            uint32_t pa[2][4];  // [64 channels]: the A operand
+            auto weigh = [&](auto masked) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float w[2][2][2];  // [i][e][64 channels]
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t p0 = e ? vpar[j].z : vpar[j].x;
+                        const uint32_t p1 = e ? vpar[j].w : vpar[j].y;
+                        const float m0 = fmaf(8.f, step_of(p0), least_of(p0));
+                        const float m1 = fmaf(8.f, step_of(p1), least_of(p1));
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float x = y[j][2 * i + e], p = ex2_approx(x);
+                            const bool none = decltype(masked)::value && x == -INFINITY;
+                            state[i].l += p;
+                            state[i].moff[0] = fmaf(p, none ? 0.f : m0, state[i].moff[0]);
+                            state[i].moff[1] = fmaf(p, none ? 0.f : m1, state[i].moff[1]);
+                            w[i][e][0] = p * (none ? 0.f : vs[j][e][0]);
+                            w[i][e][1] = p * (none ? 0.f : vs[j][e][1]);
+                        }
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            pa[h][2 * j + i] = narrow2<true>(w[i][0][h], w[i][1][h]);
+                }
+            };
+            if (edge) weigh(Bool<true>{});
+            else weigh(Bool<false>{});
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint4 x =
+                    reinterpret_cast<const uint4*>(base + to_v + codes_at)[lane + 32 * h];
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t lo0, hi0, lo1, hi1;
+                    centred_codes(w[k], lo0, hi0, lo1, hi1);
+                    mma_f16(out[8 * h + 2 * k], pa[h], lo0, lo1);
+                    mma_f16(out[8 * h + 2 * k + 1], pa[h], hi0, hi1);
+                }
+            }
+        }
+        const bool end = flags & kEnd;
+        Stage st;
+        if (end) st = sh.stage[stage];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[stage]);
+        if (++stage == kStages<true>) stage = 0, phase ^= 1;
+        if (!end) continue;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            Query& q = state[i];
+            q.l = sum4(q.l);
+            q.moff[0] = sum4(q.moff[0]);
+            q.moff[1] = sum4(q.moff[1]);
+            if (t == 0) sh.stat[warp][g + 8 * i] = make_float2(q.shift, q.l);
+        }
+        finish_segment<F16>(a, sh, st, [&](float (*sums)[kPad], const float* factor) {
+            const float low = kLow / v_unit.v, high = kHigh / v_unit.v;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float f = factor[g + 8 * i];
+                const bool some = state[i].l != 0.f;
+#pragma unroll
+                for (int n = 0; n < 16; ++n) {
+                    const float m = state[i].moff[n >> 3], back = n & 1 ? high : low;
+                    const float x = fmaf(out[n][2 * i], back, m) * f;
+                    const float z = fmaf(out[n][2 * i + 1], back, m) * f;
+                    *reinterpret_cast<float2*>(&sums[g + 8 * i][8 * n + 2 * t]) =
+                        some ? make_float2(x, z) : make_float2(0.f, 0.f);
+                }
+            }
+        });
+    }
+}
+
+template <bool F16, bool WIDE>
+__global__ void __launch_bounds__(kThreads, kCtas<WIDE>) attn_decode_kernel(DecodeArgs a) {
     extern __shared__ __align__(128) uint8_t sm[];
-    Shared<NT>& sh = *reinterpret_cast<Shared<NT>*>(sm + kStages<NT> * kStageBytes);
+    Shared<WIDE>& sh = *reinterpret_cast<Shared<WIDE>*>(sm + kStages<WIDE> * kStageBytes);
     if (threadIdx.x == 0) {
         sh.stop = 0;
-        for (int i = 0; i < kStages<NT>; ++i) {
+        for (int i = 0; i < kStages<WIDE>; ++i) {
             mbar_init(&sh.full[i], 1);
             mbar_init(&sh.empty[i], kWarps);
         }
@@ -806,17 +1017,18 @@ __global__ void __launch_bounds__(kThreads, kCtas<NT>) attn_decode_kernel(Decode
     __syncthreads();
     pdl_wait();
     pdl_release();
-    if (threadIdx.x < kWarps * 32) attend_role<F16, NT>(a, sh, sm);
-    else copy_role<NT>(a, sh, sm);
+    if (threadIdx.x >= kWarps * 32) copy_role(a, sh, sm);
+    else if constexpr (WIDE) attend_wide<F16>(a, sh, sm);
+    else attend_narrow<F16>(a, sh, sm);
 }
 
 // Joins what several CTAs have of one (sequence, head, block), and writes rows
 // that no CTA has anything of.  A warp takes some of the unit's query columns,
 // four channels a lane.
 constexpr int kJoinWarps = 16;
-template <bool F16, int NT>
+template <bool F16, bool WIDE>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(DecodeArgs a) {
-    constexpr int Q = 8 * NT;
+    constexpr int Q = kRows<WIDE>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per_seq = a.c.kv_heads * a.blocks;
     const int n = blockIdx.x / per_seq, unit = blockIdx.x - n * per_seq;
@@ -900,14 +1112,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(DecodeArgs a
 // Query columns of a block: 8 where that is all, else 16.
 inline int columns(int rows) { return rows <= 8 ? 8 : 16; }
 
-template <bool F16, int NT>
+template <bool F16, bool WIDE>
 cudaError_t launch(const DecodeArgs& a, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<F16, NT>,
+    cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<F16, WIDE>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         smem_bytes<NT>());
+                                         smem_bytes<WIDE>());
     if (e != cudaSuccess) return e;
-    launch_pdl(attn_decode_kernel<F16, NT>, dim3(a.pieces), dim3(kThreads), smem_bytes<NT>(), s, a);
-    return launch_pdl(attn_join_kernel<F16, NT>,
+    launch_pdl(attn_decode_kernel<F16, WIDE>, dim3(a.pieces), dim3(kThreads), smem_bytes<WIDE>(), s, a);
+    return launch_pdl(attn_join_kernel<F16, WIDE>,
                       dim3((unsigned)((long long)a.n_seqs * a.c.kv_heads * a.blocks)),
                       dim3(kJoinWarps * 32), 0, s, a);
 }
@@ -969,7 +1181,7 @@ extern "C" kda_status kda_attn_kv4_decode(const void* q, const uint8_t* cache, i
     KDA_REQUIRE(aligned16(workspace), KDA_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned",
                 fn);
     KDA_REQUIRE(!fault_injected(), KDA_ERR_CUDA, "%s: injected launch failure", fn);
-    const int ctas = (cols == 8 ? kCtas<1> : kCtas<2>) * sm_count();
+    const int ctas = (cols == 8 ? kCtas<false> : kCtas<true>) * sm_count();
     const int pieces = ctas < KDA_KV4_PIECES ? ctas : KDA_KV4_PIECES;
     KDA_REQUIRE(pieces > 0, KDA_ERR_CUDA, "%s: no device", fn);
     DecodeArgs a = {(const uint16_t*)q, (uint16_t*)o, lse, n_seqs, krows, heads, window, group,
@@ -979,8 +1191,8 @@ extern "C" kda_status kda_attn_kv4_decode(const void* q, const uint8_t* cache, i
     cudaStream_t s = as_stream(stream);
     const bool f16 = in_dtype == KDA_F16;
     cudaError_t e;
-    if (cols == 8) e = f16 ? launch<true, 1>(a, s) : launch<false, 1>(a, s);
-    else e = f16 ? launch<true, 2>(a, s) : launch<false, 2>(a, s);
+    if (cols == 8) e = f16 ? launch<true, false>(a, s) : launch<false, false>(a, s);
+    else e = f16 ? launch<true, true>(a, s) : launch<false, true>(a, s);
     if (e != cudaSuccess) {
         set_error("%s: launch failed: %s", fn, cudaGetErrorString(e));
         return KDA_ERR_CUDA;
