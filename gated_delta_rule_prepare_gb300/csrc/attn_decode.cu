@@ -90,14 +90,15 @@ __device__ __forceinline__ Chunks chunks_of(const DecodeArgs& a, int len) {
     const int lo = (a.window ? max(0, len - a.krows - a.window + 1) : 0) / kChunk;
     return {lo, len > 0 ? (len - 1) / kChunk + 1 - lo : 0};
 }
-// The line of `total` chunks in pieces, none of them empty: their number, and
-// where piece b starts.
-__device__ __forceinline__ int piece_count(const DecodeArgs& a, long long total) {
-    return (int)min((long long)a.pieces, total);
+// (64-bit divisions are long: most need 32 bits.)
+__device__ __forceinline__ long long divide(long long x, long long y) {
+    if (((x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
+    return x / y;
 }
-__device__ __forceinline__ long long piece_start(const DecodeArgs& a, long long total, int b) {
-    const int pieces = piece_count(a, total);
-    return b >= pieces ? total : total * b / pieces;
+// The line of `total` chunks is cut into pieces of `size`, the last one shorter;
+// piece b is CTA b's.
+__device__ __forceinline__ long long piece_size(const DecodeArgs& a, long long total) {
+    return divide(total + a.pieces - 1, a.pieces);
 }
 
 // All lengths by one warp: the chunks of all sequences of one (head, block),
@@ -144,6 +145,9 @@ constexpr uint32_t kStart = 1u << 24, kEnd = 1u << 25, kNoMore = 1u << 26;
 constexpr int kPad = 132;  // a query's 128 sums, so that a warp's stores meet all banks
 template <bool WIDE>
 constexpr int kBuffers = WIDE ? 1 : 2;
+// A stage of the ring: a chunk and, where a segment starts, its query rows.
+template <bool WIDE>
+constexpr int kSlot = kStageBytes + kRows<WIDE> * D * 2;
 template <bool WIDE>
 struct Shared {
     uint64_t full[kStages<WIDE>], empty[kStages<WIDE>];
@@ -163,7 +167,7 @@ struct Shared {
 };
 template <bool WIDE>
 constexpr int smem_bytes() {
-    return kStages<WIDE> * kStageBytes + (int)sizeof(Shared<WIDE>);
+    return kStages<WIDE> * kSlot<WIDE> + (int)sizeof(Shared<WIDE>);
 }
 
 template <bool B>
@@ -209,13 +213,14 @@ __device__ __forceinline__ void group_places(const DecodeArgs& a, int group, int
 // The copying warp: walks this CTA's piece of the line.
 template <bool WIDE>
 __device__ __forceinline__ void copy_role(const DecodeArgs& a, Shared<WIDE>& sh, uint8_t* sm) {
+    constexpr int Q = kRows<WIDE>;
     const int lane = threadIdx.x & 31;
     const int heads = a.c.kv_heads, per_seq = heads * a.blocks;
     bool bad_len = false;
     const long long one = scan_lengths(a, [](int, long long, int) { return true; });
     const long long total = one * per_seq;
-    const long long from = piece_start(a, total, blockIdx.x);
-    const long long to = piece_start(a, total, blockIdx.x + 1);
+    const long long size = piece_size(a, total);
+    const long long from = min(total, size * blockIdx.x), to = min(total, from + size);
     // the sequence that holds `from`, and where it starts
     int n = 0;
     long long n_start = 0;
@@ -249,7 +254,7 @@ __device__ __forceinline__ void copy_role(const DecodeArgs& a, Shared<WIDE>& sh,
         const Chunks ch = chunks_of(a, len);
         // (n, head, block) units of this sequence, chunk by chunk
         while (go && at < to && at < n_start + (long long)ch.count * per_seq) {
-            const int unit = (int)((at - n_start) / ch.count);
+            const int unit = (int)divide(at - n_start, ch.count);
             const int head = unit / a.blocks, block = unit - head * a.blocks;
             const long long u_start = n_start + (long long)unit * ch.count;
             const long long u_end = u_start + ch.count;
@@ -257,6 +262,7 @@ __device__ __forceinline__ void copy_role(const DecodeArgs& a, Shared<WIDE>& sh,
             const bool whole = at == u_start && seg_end == u_end;
             const int part = whole ? -1 : 2 * (int)blockIdx.x + (at == from ? 0 : 1);
             const long long seg_start = at;
+            const int n_rows = min(Q, a.rows - block * Q);
             const int* table = a.c.table + (long long)n * a.c.max_pages;
             // page numbers, a lane each, some chunks ahead
             int ids = 0, ids_from = -1;
@@ -288,14 +294,22 @@ __device__ __forceinline__ void copy_role(const DecodeArgs& a, Shared<WIDE>& sh,
                     if (at + 1 == seg_end) there |= kEnd;
                     sh.stage[stage] = {pos, there, len, n, head, block, part};
                     mbar_arrive_expect_tx(&sh.full[stage],
-                                          (uint32_t)__popc(ok) * piece * kTokenBytes);
+                                          (uint32_t)__popc(ok) * piece * kTokenBytes +
+                                              (there & kStart ? n_rows * D * 2 : 0));
                 }
                 __syncwarp();
+                if (at == seg_start && lane < n_rows) {
+                    const int row = block * Q + lane, i = row / a.group;
+                    bulk_load(sm + stage * kSlot<WIDE> + kStageBytes + lane * D * 2,
+                              a.q + (((long long)n * a.krows + i) * a.heads + head * a.group +
+                                     row - i * a.group) * D,
+                              D * 2, &sh.full[stage]);
+                }
                 if (valid) {
                     const int in_page = at_tok & (a.c.page() - 1);
                     const uint8_t* src = a.c.data +
                                          ((long long)id * heads + head) * a.c.block_bytes();
-                    uint8_t* dst = sm + stage * kStageBytes + lane * piece * kTokenBytes;
+                    uint8_t* dst = sm + stage * kSlot<WIDE> + lane * piece * kTokenBytes;
                     if (piece == a.c.page()) {
                         bulk_load(dst, src, piece * kTokenBytes, &sh.full[stage]);
                     } else {
@@ -387,21 +401,17 @@ __device__ __forceinline__ float pow2(int e) {  // -126 <= e <= 127
 }
 __device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23 & 255) - 127; }
 
-// The segment's queries into shared memory, a row to a warp at a time, four
-// channels a lane.
+// The segment's queries, as the copying warp brought them, to operands: a row to
+// a warp at a time, four channels a lane.
 template <bool F16, bool WIDE>
 __device__ __forceinline__ void load_queries(const DecodeArgs& a, Shared<WIDE>& sh,
-                                             const Stage& st) {
+                                             const Stage& st, const uint8_t* rows) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll 1
+#pragma unroll 2
     for (int r = warp; r < kRows<WIDE>; r += kWarps) {
-        const int row = st.block * kRows<WIDE> + r;
-        const int i = row / a.group, hh = row - i * a.group;
         uint2 raw = make_uint2(0u, 0u);
-        if (row < a.rows)
-            raw = __ldg(reinterpret_cast<const uint2*>(
-                            a.q + (((long long)st.n * a.krows + i) * a.heads +
-                                   st.head * a.group + hh) * D) + lane);
+        if (st.block * kRows<WIDE> + r < a.rows)
+            raw = reinterpret_cast<const uint2*>(rows + r * D * 2)[lane];
         float2 x = widen2<F16>(raw.x), y = widen2<F16>(raw.y);
         float big = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y)));
 #pragma unroll
@@ -556,7 +566,7 @@ __device__ __forceinline__ void attend_narrow(const DecodeArgs& a, Shared<false>
             const Stage st = sh.stage[stage];
             len = st.len;
             settled = false;
-            load_queries<F16>(a, sh, st);
+            load_queries<F16>(a, sh, st, sm + stage * kSlot<false> + kStageBytes);
 #pragma unroll
             for (int k = 0; k < 8; ++k) qb[k] = *reinterpret_cast<const uint2*>(sh.q[k][lane]);
 #pragma unroll
@@ -574,7 +584,7 @@ __device__ __forceinline__ void attend_narrow(const DecodeArgs& a, Shared<false>
         const uint32_t there = flags >> mine & ((1u << I) - 1);
         if (there) {
             const int pos = sh.stage[stage].pos + 16 * mine;
-            const uint8_t* base = sm + stage * kStageBytes;
+            const uint8_t* base = sm + stage * kSlot<false>;
             // scores of tokens g and g + 8 of each group
             float y[I][4];
             {
@@ -797,7 +807,7 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
             const Stage st = sh.stage[stage];
             len = st.len;
             settled = false;
-            load_queries<F16>(a, sh, st);
+            load_queries<F16>(a, sh, st, sm + stage * kSlot<true> + kStageBytes);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 unit[i] = sh.unit[g + 8 * i];
@@ -816,7 +826,7 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
             // (queries are read again for each group, not kept)
             asm volatile("" ::: "memory");
             const int pos = sh.stage[stage].pos + 16 * mine;
-            const uint8_t* base = sm + stage * kStageBytes;
+            const uint8_t* base = sm + stage * kSlot<true>;
             int codes_at, pars_at;
             group_places(a, mine, codes_at, pars_at);
             float y[2][4];  // [keys 0..7, 8..15][2 i + e]
@@ -1005,7 +1015,7 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
 template <bool F16, bool WIDE>
 __global__ void __launch_bounds__(kThreads, kCtas<WIDE>) attn_decode_kernel(DecodeArgs a) {
     extern __shared__ __align__(128) uint8_t sm[];
-    Shared<WIDE>& sh = *reinterpret_cast<Shared<WIDE>*>(sm + kStages<WIDE> * kStageBytes);
+    Shared<WIDE>& sh = *reinterpret_cast<Shared<WIDE>*>(sm + kStages<WIDE> * kSlot<WIDE>);
     if (threadIdx.x == 0) {
         sh.stop = 0;
         for (int i = 0; i < kStages<WIDE>; ++i) {
@@ -1023,12 +1033,15 @@ __global__ void __launch_bounds__(kThreads, kCtas<WIDE>) attn_decode_kernel(Deco
 }
 
 // Joins what several CTAs have of one (sequence, head, block), and writes rows
-// that no CTA has anything of.  A warp takes some of the unit's query columns,
+// that no CTA has anything of.  CTA (x, y) has unit x and of its queries every
+// gridDim.y-th, `per` of them; each has 16 / per warps, which share the pieces,
 // four channels a lane.
 constexpr int kJoinWarps = 16;
 template <bool F16, bool WIDE>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(DecodeArgs a) {
     constexpr int Q = kRows<WIDE>;
+    __shared__ float4 parts[kJoinWarps][32];
+    __shared__ float part_sum[kJoinWarps], part_least[kJoinWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per_seq = a.c.kv_heads * a.blocks;
     const int n = blockIdx.x / per_seq, unit = blockIdx.x - n * per_seq;
@@ -1043,70 +1056,82 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(DecodeArgs a
         }
         return true;
     });
-    const long long total = one * per_seq;
     int b0 = 0, b1 = -1, slot0 = 0;
     if (count) {
+        const long long size = piece_size(a, one * per_seq);
         const long long start = before * per_seq + (long long)unit * count;
-        auto piece_of = [&](long long at) {
-            const int pieces = piece_count(a, total);
-            int b = (int)(at * pieces / total);
-            while (b + 1 < pieces && piece_start(a, total, b + 1) <= at) ++b;
-            while (piece_start(a, total, b) > at) --b;
-            return b;
-        };
-        b0 = piece_of(start);
-        b1 = piece_of(start + count - 1);
+        b0 = (int)divide(start, size);
+        b1 = (int)divide(start + count - 1, size);
         if (b0 == b1) return;  // one CTA had all of it
-        slot0 = 2 * b0 + (piece_start(a, total, b0) == start ? 0 : 1);
+        slot0 = 2 * b0 + (size * b0 == start ? 0 : 1);
     }
     const float2* stat = reinterpret_cast<const float2*>(a.part + 2LL * a.pieces * Q * D);
-    for (int c = warp; c < Q; c += kJoinWarps) {
-        const int row = block * Q + c;
-        if (row >= a.rows) break;
-        float least = INFINITY;
-        for (int b = b0 + lane; b <= b1; b += 32) {
-            const float2 s = __ldcg(stat + (b == b0 ? slot0 : 2 * b) * Q + c);
-            if (s.y != 0.f) least = fminf(least, s.x);
-        }
+    const int per = Q / gridDim.y, shares = kJoinWarps / per;  // powers of two
+    const int mine = warp / shares, share = warp - mine * shares;
+    const int c = blockIdx.y + mine * gridDim.y, row = block * Q + c;
+    // this warp's pieces: their least shift, then everything brought to it
+    float least = INFINITY, sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int from = b0 + share; from <= b1; from += 32 * shares) {
+        const int b = from + lane * shares;
+        float2 s = make_float2(0.f, 0.f);
+        if (b <= b1) s = __ldcg(stat + (b == b0 ? slot0 : 2 * b) * Q + c);
+        float low = s.y != 0.f ? s.x : INFINITY;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1)
-            least = fminf(least, __shfl_xor_sync(0xffffffffu, least, off));
-        float sum = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int from = b0; from <= b1; from += 32) {
-            // a piece's factor and part of the sum a lane, then its 128 channels
-            const int b = from + lane;
-            float f = 0.f;
-            if (b <= b1) {
-                const float2 s = __ldcg(stat + (b == b0 ? slot0 : 2 * b) * Q + c);
-                if (s.y != 0.f) {
-                    f = ex2_approx(least - s.x);
-                    sum = fmaf(s.y, f, sum);
-                }
-            }
-            const int n_here = min(32, b1 - from + 1);
-#pragma unroll 8
-            for (int i = 0; i < n_here; ++i) {
-                const int slot = from + i == b0 ? slot0 : 2 * (from + i);
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(
-                                            a.part + ((long long)slot * Q + c) * D) + lane);
-                const float fi = __shfl_sync(0xffffffffu, f, i);
-                if (fi == 0.f) continue;
-                o.x = fmaf(x.x, fi, o.x);
-                o.y = fmaf(x.y, fi, o.y);
-                o.z = fmaf(x.z, fi, o.z);
-                o.w = fmaf(x.w, fi, o.w);
-            }
+            low = fminf(low, __shfl_xor_sync(0xffffffffu, low, off));
+        if (low < least) {
+            const float f = least < INFINITY ? ex2_approx(low - least) : 0.f;
+            o.x *= f, o.y *= f, o.z *= f, o.w *= f, sum *= f;
+            least = low;
         }
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const long long at = ((long long)n * a.krows + row / a.group) * a.heads + head * a.group +
-                             row % a.group;
-        *reinterpret_cast<uint2*>(a.o + at * D + 4 * lane) =
-            make_uint2(narrow2<F16>(o.x * inv, o.y * inv), narrow2<F16>(o.z * inv, o.w * inv));
-        if (a.lse && lane == 0) a.lse[at] = sum == 0.f ? -INFINITY : (log2f(sum) - least) * kLn2;
+        const float f = s.y != 0.f ? ex2_approx(least - s.x) : 0.f;
+        sum = s.y != 0.f ? fmaf(s.y, f, sum) : sum;
+        const int here = min(32, (b1 - from) / shares + 1);
+#pragma unroll 8
+        for (int i = 0; i < here; ++i) {
+            const int bi = from + i * shares, slot = bi == b0 ? slot0 : 2 * bi;
+            const float4 x = __ldcg(
+                reinterpret_cast<const float4*>(a.part + ((long long)slot * Q + c) * D) + lane);
+            const float fi = __shfl_sync(0xffffffffu, f, i);
+            if (fi == 0.f) continue;
+            o.x = fmaf(x.x, fi, o.x);
+            o.y = fmaf(x.y, fi, o.y);
+            o.z = fmaf(x.z, fi, o.z);
+            o.w = fmaf(x.w, fi, o.w);
+        }
     }
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (shares > 1) {
+        parts[warp][lane] = o;
+        if (lane == 0) part_sum[warp] = sum, part_least[warp] = least;
+        __syncthreads();
+        if (share) return;
+        float all = INFINITY;
+        for (int w = warp; w < warp + shares; ++w) all = fminf(all, part_least[w]);
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+        sum = 0.f;
+        for (int w = warp; w < warp + shares; ++w) {
+            if (!(part_least[w] < INFINITY)) continue;
+            const float f = ex2_approx(all - part_least[w]);
+            const float4 x = parts[w][lane];
+            o.x = fmaf(x.x, f, o.x);
+            o.y = fmaf(x.y, f, o.y);
+            o.z = fmaf(x.z, f, o.z);
+            o.w = fmaf(x.w, f, o.w);
+            sum = fmaf(part_sum[w], f, sum);
+        }
+        least = all;
+    }
+    if (row >= a.rows) return;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int i_row = row / a.group;
+    const long long at = ((long long)n * a.krows + i_row) * a.heads + head * a.group + row -
+                         i_row * a.group;
+    reinterpret_cast<uint2*>(a.o + at * D)[lane] =
+        make_uint2(narrow2<F16>(o.x * inv, o.y * inv), narrow2<F16>(o.z * inv, o.w * inv));
+    if (a.lse && lane == 0) a.lse[at] = sum == 0.f ? -INFINITY : (log2f(sum) - least) * kLn2;
 }
 
 // Query columns of a block: 8 where that is all, else 16.
@@ -1119,8 +1144,11 @@ cudaError_t launch(const DecodeArgs& a, cudaStream_t s) {
                                          smem_bytes<WIDE>());
     if (e != cudaSuccess) return e;
     launch_pdl(attn_decode_kernel<F16, WIDE>, dim3(a.pieces), dim3(kThreads), smem_bytes<WIDE>(), s, a);
-    return launch_pdl(attn_join_kernel<F16, WIDE>,
-                      dim3((unsigned)((long long)a.n_seqs * a.c.kv_heads * a.blocks)),
+    // few units: their queries to CTAs of their own
+    const long long units = (long long)a.n_seqs * a.c.kv_heads * a.blocks;
+    int apart = 1;
+    while (apart < kRows<WIDE> && 2 * apart * units <= 152) apart *= 2;
+    return launch_pdl(attn_join_kernel<F16, WIDE>, dim3((unsigned)units, apart),
                       dim3(kJoinWarps * 32), 0, s, a);
 }
 
