@@ -55,9 +55,9 @@ __device__ unsigned g_decode_status = 0;
 constexpr int kWarps = 4;  // and one that copies
 constexpr int kThreads = (kWarps + 1) * 32;
 template <bool WIDE>
-constexpr int kCtas = WIDE ? 2 : 3;  // to a multiprocessor
+constexpr int kCtas = 3;  // to a multiprocessor
 template <bool WIDE>
-constexpr int kStages = WIDE ? 4 : 3;
+constexpr int kStages = 3;
 constexpr int kGroups = 8;
 constexpr int kChunk = kGroups * 16;  // tokens
 constexpr int kStageBytes = kChunk * kTokenBytes;
@@ -145,9 +145,6 @@ constexpr uint32_t kStart = 1u << 24, kEnd = 1u << 25, kNoMore = 1u << 26;
 constexpr int kPad = 132;  // a query's 128 sums, so that a warp's stores meet all banks
 template <bool WIDE>
 constexpr int kBuffers = WIDE ? 1 : 2;
-// A stage of the ring: a chunk and, where a segment starts, its query rows.
-template <bool WIDE>
-constexpr int kSlot = kStageBytes + kRows<WIDE> * D * 2;
 template <bool WIDE>
 struct Shared {
     uint64_t full[kStages<WIDE>], empty[kStages<WIDE>];
@@ -158,6 +155,7 @@ struct Shared {
     alignas(16) uint32_t q[8][32][WIDE ? 4 : 2];
     float unit[kRows<WIDE>];
     float2 qsum[kRows<WIDE>];
+    int limit[kRows<WIDE>];  // positions from it on are not seen
     // its end
     float2 stat[kWarps][kRows<WIDE>];  // a warp's (shift, l) by query
     float factor[kWarps][kRows<WIDE>];
@@ -167,7 +165,7 @@ struct Shared {
 };
 template <bool WIDE>
 constexpr int smem_bytes() {
-    return kStages<WIDE> * kSlot<WIDE> + (int)sizeof(Shared<WIDE>);
+    return kStages<WIDE> * kStageBytes + (int)sizeof(Shared<WIDE>);
 }
 
 template <bool B>
@@ -213,7 +211,6 @@ __device__ __forceinline__ void group_places(const DecodeArgs& a, int group, int
 // The copying warp: walks this CTA's piece of the line.
 template <bool WIDE>
 __device__ __forceinline__ void copy_role(const DecodeArgs& a, Shared<WIDE>& sh, uint8_t* sm) {
-    constexpr int Q = kRows<WIDE>;
     const int lane = threadIdx.x & 31;
     const int heads = a.c.kv_heads, per_seq = heads * a.blocks;
     bool bad_len = false;
@@ -262,7 +259,6 @@ __device__ __forceinline__ void copy_role(const DecodeArgs& a, Shared<WIDE>& sh,
             const bool whole = at == u_start && seg_end == u_end;
             const int part = whole ? -1 : 2 * (int)blockIdx.x + (at == from ? 0 : 1);
             const long long seg_start = at;
-            const int n_rows = min(Q, a.rows - block * Q);
             const int* table = a.c.table + (long long)n * a.c.max_pages;
             // page numbers, a lane each, some chunks ahead
             int ids = 0, ids_from = -1;
@@ -294,22 +290,14 @@ __device__ __forceinline__ void copy_role(const DecodeArgs& a, Shared<WIDE>& sh,
                     if (at + 1 == seg_end) there |= kEnd;
                     sh.stage[stage] = {pos, there, len, n, head, block, part};
                     mbar_arrive_expect_tx(&sh.full[stage],
-                                          (uint32_t)__popc(ok) * piece * kTokenBytes +
-                                              (there & kStart ? n_rows * D * 2 : 0));
+                                          (uint32_t)__popc(ok) * piece * kTokenBytes);
                 }
                 __syncwarp();
-                if (at == seg_start && lane < n_rows) {
-                    const int row = block * Q + lane, i = row / a.group;
-                    bulk_load(sm + stage * kSlot<WIDE> + kStageBytes + lane * D * 2,
-                              a.q + (((long long)n * a.krows + i) * a.heads + head * a.group +
-                                     row - i * a.group) * D,
-                              D * 2, &sh.full[stage]);
-                }
                 if (valid) {
                     const int in_page = at_tok & (a.c.page() - 1);
                     const uint8_t* src = a.c.data +
                                          ((long long)id * heads + head) * a.c.block_bytes();
-                    uint8_t* dst = sm + stage * kSlot<WIDE> + lane * piece * kTokenBytes;
+                    uint8_t* dst = sm + stage * kStageBytes + lane * piece * kTokenBytes;
                     if (piece == a.c.page()) {
                         bulk_load(dst, src, piece * kTokenBytes, &sh.full[stage]);
                     } else {
@@ -401,17 +389,26 @@ __device__ __forceinline__ float pow2(int e) {  // -126 <= e <= 127
 }
 __device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23 & 255) - 127; }
 
-// The segment's queries, as the copying warp brought them, to operands: a row to
-// a warp at a time, four channels a lane.
+// The segment's queries to operands: some rows a warp, four channels a lane.
 template <bool F16, bool WIDE>
 __device__ __forceinline__ void load_queries(const DecodeArgs& a, Shared<WIDE>& sh,
-                                             const Stage& st, const uint8_t* rows) {
+                                             const Stage& st) {
+    constexpr int N = kRows<WIDE> / kWarps;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll 2
-    for (int r = warp; r < kRows<WIDE>; r += kWarps) {
-        uint2 raw = make_uint2(0u, 0u);
-        if (st.block * kRows<WIDE> + r < a.rows)
-            raw = reinterpret_cast<const uint2*>(rows + r * D * 2)[lane];
+    uint2 rows[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int row = st.block * kRows<WIDE> + warp + kWarps * k, i = row / a.group;
+        rows[k] = make_uint2(0u, 0u);
+        if (row < a.rows)
+            rows[k] = __ldg(reinterpret_cast<const uint2*>(
+                                a.q + (((long long)st.n * a.krows + i) * a.heads +
+                                       st.head * a.group + row - i * a.group) * D) + lane);
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int r = warp + kWarps * k;
+        const uint2 raw = rows[k];
         float2 x = widen2<F16>(raw.x), y = widen2<F16>(raw.y);
         float big = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y)));
 #pragma unroll
@@ -433,6 +430,8 @@ __device__ __forceinline__ void load_queries(const DecodeArgs& a, Shared<WIDE>& 
         sh.q[kb][at][word] = narrow2<true>(x.x * fj, x.y * fj);
         sh.q[kb][at + 1][word] = narrow2<true>(y.x * fj, y.y * fj);
         if (lane == 0) {
+            const int row = st.block * kRows<WIDE> + r;
+            sh.limit[r] = row < a.rows ? st.len - a.krows + row / a.group + 1 : 0;
             sh.unit[r] = a.scale * kLog2e * kLow * pow2(-up);
             sh.qsum[r].x = sum * (1.f / kLow);
         }
@@ -554,10 +553,7 @@ __device__ __forceinline__ void attend_narrow(const DecodeArgs& a, Shared<false>
     Query state[2];
     Unit v_unit;
     bool settled = false;  // every column has a shift that comes from a score
-    auto limit_of = [&](int block, int c) {  // positions from it on are not seen
-        const int row = block * 8 + 2 * t + c;
-        return row < a.rows ? len - a.krows + row / a.group + 1 : 0;
-    };
+    int limit[2];  // positions from it on are not seen
     for (;;) {
         if (!wait_warp(sh, &sh.full[stage], phase)) return;
         const uint32_t flags = sh.stage[stage].flags;
@@ -566,7 +562,7 @@ __device__ __forceinline__ void attend_narrow(const DecodeArgs& a, Shared<false>
             const Stage st = sh.stage[stage];
             len = st.len;
             settled = false;
-            load_queries<F16>(a, sh, st, sm + stage * kSlot<false> + kStageBytes);
+            load_queries<F16>(a, sh, st);
 #pragma unroll
             for (int k = 0; k < 8; ++k) qb[k] = *reinterpret_cast<const uint2*>(sh.q[k][lane]);
 #pragma unroll
@@ -575,6 +571,7 @@ __device__ __forceinline__ void attend_narrow(const DecodeArgs& a, Shared<false>
                 qsum[c][0] = sh.qsum[2 * t + c].x;
                 qsum[c][1] = sh.qsum[2 * t + c].y;
                 state[c] = {};
+                limit[c] = sh.limit[2 * t + c];
             }
 #pragma unroll
             for (int cb = 0; cb < 8; ++cb)
@@ -584,7 +581,7 @@ __device__ __forceinline__ void attend_narrow(const DecodeArgs& a, Shared<false>
         const uint32_t there = flags >> mine & ((1u << I) - 1);
         if (there) {
             const int pos = sh.stage[stage].pos + 16 * mine;
-            const uint8_t* base = sm + stage * kSlot<false>;
+            const uint8_t* base = sm + stage * kStageBytes;
             // scores of tokens g and g + 8 of each group
             float y[I][4];
             {
@@ -623,10 +620,9 @@ __device__ __forceinline__ void attend_narrow(const DecodeArgs& a, Shared<false>
             const bool edge = pos + 16 * I > len - a.krows + 1 ||
                               (a.window && pos < len - a.window) || there != (1u << I) - 1;
             if (edge) {
-                const int block = sh.stage[stage].block;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const int hi = limit_of(block, c), lo = a.window ? max(0, hi - a.window) : 0;
+                    const int hi = limit[c], lo = a.window ? max(0, hi - a.window) : 0;
 #pragma unroll
                     for (int u = 0; u < I; ++u)
 #pragma unroll
@@ -666,7 +662,6 @@ __device__ __forceinline__ void attend_narrow(const DecodeArgs& a, Shared<false>
 #pragma unroll
                     for (int i = 0; i < 2; ++i) vs[u][i][0] *= fv, vs[u][i][1] *= fv;
                 bool all = true;
-                const int block = sh.stage[stage].block;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     Query& q = state[c];
@@ -685,7 +680,7 @@ __device__ __forceinline__ void attend_narrow(const DecodeArgs& a, Shared<false>
 #pragma unroll
                     for (int cb = 0; cb < 8; ++cb) out[cb][c] *= f * fv, out[cb][2 + c] *= f * fv;
                     // a column that will see a key later has no shift yet
-                    all &= !fresh || move || limit_of(block, c) <= pos + 16 * I;
+                    all &= !fresh || move || limit[c] <= pos + 16 * I;
                 }
                 settled = __all_sync(0xffffffffu, all);
             }
@@ -750,7 +745,7 @@ __device__ __forceinline__ void attend_narrow(const DecodeArgs& a, Shared<false>
             if (g == 0) sh.stat[warp][2 * t + c] = make_float2(q.shift, q.l);
         }
         finish_segment<F16>(a, sh, st, [&](float (*sums)[kPad], const float* factor) {
-            const float low = kLow / v_unit.v, high = kHigh / v_unit.v;
+            const float back = pow2(-exponent(v_unit.v)), low = kLow * back, high = kHigh * back;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const float f = factor[2 * t + c];
@@ -782,14 +777,10 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
     const int to_v = part_bytes(piece_tokens(a));
     int stage = 0, len = 0;
     uint32_t phase = 0;
-    float unit[2], qsum[2][2], out[16][4];  // channels 8 n + 2 t + e
+    float out[16][4];  // channels 8 n + 2 t + e
     Query state[2];
     Unit v_unit;
     bool settled = false;
-    auto limit_of = [&](int block, int i) {
-        const int row = block * 16 + g + 8 * i;
-        return row < a.rows ? len - a.krows + row / a.group + 1 : 0;
-    };
     // over the four lanes that hold the other keys of the same queries
     auto max4 = [](float x) {
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
@@ -807,14 +798,8 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
             const Stage st = sh.stage[stage];
             len = st.len;
             settled = false;
-            load_queries<F16>(a, sh, st, sm + stage * kSlot<true> + kStageBytes);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                unit[i] = sh.unit[g + 8 * i];
-                qsum[i][0] = sh.qsum[g + 8 * i].x;
-                qsum[i][1] = sh.qsum[g + 8 * i].y;
-                state[i] = {};
-            }
+            load_queries<F16>(a, sh, st);
+            state[0] = state[1] = {};
 #pragma unroll
             for (int n = 0; n < 16; ++n)
 #pragma unroll
@@ -826,7 +811,7 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
             // (queries are read again for each group, not kept)
             asm volatile("" ::: "memory");
             const int pos = sh.stage[stage].pos + 16 * mine;
-            const uint8_t* base = sm + stage * kSlot<true>;
+            const uint8_t* base = sm + stage * kStageBytes;
             int codes_at, pars_at;
             group_places(a, mine, codes_at, pars_at);
             float y[2][4];  // [keys 0..7, 8..15][2 i + e]
@@ -834,6 +819,7 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
                 float acc[2][2][4] = {};  // [keys][64 channels]
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
+                    asm volatile("" ::: "memory");  // (nor all of them at once)
                     const uint4 x = reinterpret_cast<const uint4*>(base + codes_at)[lane + 32 * h];
                     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -856,11 +842,12 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
                         const uint32_t p0 = e ? par.z : par.x, p1 = e ? par.w : par.y;
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            float d = least_of(p0) * qsum[i][0];
-                            d = fmaf(least_of(p1), qsum[i][1], d);
+                            const float2 qs = sh.qsum[g + 8 * i];
+                            float d = least_of(p0) * qs.x;
+                            d = fmaf(least_of(p1), qs.y, d);
                             d = fmaf(step_of(p0), acc[j][0][2 * i + e], d);
                             d = fmaf(step_of(p1), acc[j][1][2 * i + e], d);
-                            y[j][2 * i + e] = fmaf(d, unit[i], state[i].shift);
+                            y[j][2 * i + e] = fmaf(d, sh.unit[g + 8 * i], state[i].shift);
                         }
                     }
                 }
@@ -868,10 +855,9 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
             const bool edge =
                 pos + 16 > len - a.krows + 1 || (a.window && pos < len - a.window);
             if (edge) {
-                const int block = sh.stage[stage].block;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int hi = limit_of(block, i), lo = a.window ? max(0, hi - a.window) : 0;
+                    const int hi = sh.limit[g + 8 * i], lo = a.window ? max(0, hi - a.window) : 0;
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -882,19 +868,20 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
                 }
             }
             uint4 vpar[2];
-            float vs[2][2][2], most = 0.f;  // [keys][e][64 channels]
+            float most = 0.f;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 vpar[j] = *reinterpret_cast<const uint4*>(base + to_v + pars_at +
                                                           (8 * j + 2 * t) * 8);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    vs[j][e][0] = step_of(e ? vpar[j].z : vpar[j].x) * v_unit.v;
-                    vs[j][e][1] = step_of(e ? vpar[j].w : vpar[j].y) * v_unit.v;
-                    if (edge && pos + 8 * j + 2 * t + e >= len) vs[j][e][0] = vs[j][e][1] = 0.f;
-                    most = fmaxf(most, fmaxf(vs[j][e][0], vs[j][e][1]));
+                if (edge) {  // whatever the cache holds behind a sequence's end
+                    const int at = pos + 8 * j + 2 * t;
+                    if (at >= len) vpar[j].x = vpar[j].y = 0u;
+                    if (at + 1 >= len) vpar[j].z = vpar[j].w = 0u;
                 }
+                most = fmaxf(most, fmaxf(fmaxf(step_of(vpar[j].x), step_of(vpar[j].y)),
+                                         fmaxf(step_of(vpar[j].z), step_of(vpar[j].w))));
             }
+            most *= v_unit.v;
             float tops[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -903,14 +890,8 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
             if (__any_sync(0xffffffffu,
                            !settled || most >= 256.f || tops[0] > 7.f || tops[1] > 7.f)) {
                 // (all lanes agree on the unit: the steps of a group are theirs together)
-                float all_most = max4(most);
-                const float fv = v_unit.fit(all_most, !settled);
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) vs[j][e][0] *= fv, vs[j][e][1] *= fv;
+                const float fv = v_unit.fit(max4(most), !settled);
                 bool all = true;
-                const int block = sh.stage[stage].block;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     Query& q = state[i];
@@ -926,10 +907,12 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
                     q.l *= f;
                     q.moff[0] *= f;
                     q.moff[1] *= f;
+                    const float both = f * fv;
+                    if (__any_sync(0xffffffffu, both != 1.f))
 #pragma unroll
-                    for (int n = 0; n < 16; ++n)
-                        out[n][2 * i] *= f * fv, out[n][2 * i + 1] *= f * fv;
-                    all &= !fresh || move || limit_of(block, i) <= pos + 16;
+                        for (int n = 0; n < 16; ++n)
+                            out[n][2 * i] *= both, out[n][2 * i + 1] *= both;
+                    all &= !fresh || move || sh.limit[g + 8 * i] <= pos + 16;
                 }
                 settled = __all_sync(0xffffffffu, all);
             }
@@ -944,6 +927,7 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
                         const uint32_t p1 = e ? vpar[j].w : vpar[j].y;
                         const float m0 = fmaf(8.f, step_of(p0), least_of(p0));
                         const float m1 = fmaf(8.f, step_of(p1), least_of(p1));
+                        const float s0 = step_of(p0) * v_unit.v, s1 = step_of(p1) * v_unit.v;
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const float x = y[j][2 * i + e], p = ex2_approx(x);
@@ -951,8 +935,8 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
                             state[i].l += p;
                             state[i].moff[0] = fmaf(p, none ? 0.f : m0, state[i].moff[0]);
                             state[i].moff[1] = fmaf(p, none ? 0.f : m1, state[i].moff[1]);
-                            w[i][e][0] = p * (none ? 0.f : vs[j][e][0]);
-                            w[i][e][1] = p * (none ? 0.f : vs[j][e][1]);
+                            w[i][e][0] = p * (none ? 0.f : s0);
+                            w[i][e][1] = p * (none ? 0.f : s1);
                         }
                     }
 #pragma unroll
@@ -994,16 +978,16 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
             if (t == 0) sh.stat[warp][g + 8 * i] = make_float2(q.shift, q.l);
         }
         finish_segment<F16>(a, sh, st, [&](float (*sums)[kPad], const float* factor) {
-            const float low = kLow / v_unit.v, high = kHigh / v_unit.v;
+            const float back = pow2(-exponent(v_unit.v)), low = kLow * back, high = kHigh * back;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float f = factor[g + 8 * i];
                 const bool some = state[i].l != 0.f;
 #pragma unroll
                 for (int n = 0; n < 16; ++n) {
-                    const float m = state[i].moff[n >> 3], back = n & 1 ? high : low;
-                    const float x = fmaf(out[n][2 * i], back, m) * f;
-                    const float z = fmaf(out[n][2 * i + 1], back, m) * f;
+                    const float m = state[i].moff[n >> 3], unit = n & 1 ? high : low;
+                    const float x = fmaf(out[n][2 * i], unit, m) * f;
+                    const float z = fmaf(out[n][2 * i + 1], unit, m) * f;
                     *reinterpret_cast<float2*>(&sums[g + 8 * i][8 * n + 2 * t]) =
                         some ? make_float2(x, z) : make_float2(0.f, 0.f);
                 }
@@ -1015,7 +999,7 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
 template <bool F16, bool WIDE>
 __global__ void __launch_bounds__(kThreads, kCtas<WIDE>) attn_decode_kernel(DecodeArgs a) {
     extern __shared__ __align__(128) uint8_t sm[];
-    Shared<WIDE>& sh = *reinterpret_cast<Shared<WIDE>*>(sm + kStages<WIDE> * kSlot<WIDE>);
+    Shared<WIDE>& sh = *reinterpret_cast<Shared<WIDE>*>(sm + kStages<WIDE> * kStageBytes);
     if (threadIdx.x == 0) {
         sh.stop = 0;
         for (int i = 0; i < kStages<WIDE>; ++i) {
