@@ -143,24 +143,26 @@ struct Stage {
 constexpr uint32_t kStart = 1u << 24, kEnd = 1u << 25, kNoMore = 1u << 26;
 
 constexpr int kPad = 132;  // a query's 128 sums, so that a warp's stores meet all banks
-template <bool WIDE>
-constexpr int kBuffers = WIDE ? 1 : 2;
+constexpr int kBuffers = 2;
 template <bool WIDE>
 struct Shared {
     uint64_t full[kStages<WIDE>], empty[kStages<WIDE>];
     Stage stage[kStages<WIDE>];
-    // the segment's queries as operands (FP16, scaled by a power of two); by
-    // query, the factor from a product to a score in log2 units and the sums
-    // over 64 channels
-    alignas(16) uint32_t q[8][32][WIDE ? 4 : 2];
+    // by query, the factor from a product to a score in log2 units, the sums over
+    // 64 channels, and the first position that is not seen
     float unit[kRows<WIDE>];
     float2 qsum[kRows<WIDE>];
-    int limit[kRows<WIDE>];  // positions from it on are not seen
-    // its end
+    int limit[kRows<WIDE>];
+    // a segment's end
     float2 stat[kWarps][kRows<WIDE>];  // a warp's (shift, l) by query
     float factor[kWarps][kRows<WIDE>];
     float2 joint[kRows<WIDE>];
-    alignas(16) float sums[kBuffers<WIDE>][kRows<WIDE>][kPad];  // some warps' outputs at a time
+    union {
+        // the segment's queries as operands (FP16, scaled by a power of two)
+        alignas(16) uint32_t q[8][32][WIDE ? 4 : 2];
+        // and at its end two warps' outputs at a time
+        alignas(16) float sums[kBuffers][kRows<WIDE>][kPad];
+    };
     int stop;
 };
 template <bool WIDE>
@@ -446,7 +448,7 @@ __device__ __forceinline__ void load_queries(const DecodeArgs& a, Shared<WIDE>& 
 template <bool F16, bool WIDE, class Put>
 __device__ __forceinline__ void finish_segment(const DecodeArgs& a, Shared<WIDE>& sh,
                                                const Stage& st, Put put) {
-    constexpr int Q = kRows<WIDE>, B = kBuffers<WIDE>;
+    constexpr int Q = kRows<WIDE>, B = kBuffers;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     consumer_sync();
     if (tid < Q) {
@@ -750,14 +752,12 @@ __device__ __forceinline__ void attend_narrow(const DecodeArgs& a, Shared<false>
             for (int c = 0; c < 2; ++c) {
                 const float f = factor[2 * t + c];
                 float* dst = sums[2 * t + c] + g;
-                const bool some = state[c].l != 0.f;
+                const float m[2] = {state[c].moff[0] * f, state[c].moff[1] * f};
+                const bool none = state[c].l == 0.f;
 #pragma unroll
                 for (int cb = 0; cb < 8; ++cb) {
-                    const float m = state[c].moff[cb >> 2];
-                    const float x = fmaf(out[cb][c], low, m) * f;
-                    const float z = fmaf(out[cb][2 + c], high, m) * f;
-                    dst[16 * cb] = some ? x : 0.f;
-                    dst[16 * cb + 8] = some ? z : 0.f;
+                    dst[16 * cb] = none ? 0.f : fmaf(out[cb][c], low * f, m[cb >> 2]);
+                    dst[16 * cb + 8] = none ? 0.f : fmaf(out[cb][2 + c], high * f, m[cb >> 2]);
                 }
             }
         });
@@ -982,14 +982,16 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float f = factor[g + 8 * i];
-                const bool some = state[i].l != 0.f;
+                float* dst = sums[g + 8 * i] + 2 * t;
+                const float m[2] = {state[i].moff[0] * f, state[i].moff[1] * f};
+                const bool none = state[i].l == 0.f;
 #pragma unroll
                 for (int n = 0; n < 16; ++n) {
-                    const float m = state[i].moff[n >> 3], unit = n & 1 ? high : low;
-                    const float x = fmaf(out[n][2 * i], unit, m) * f;
-                    const float z = fmaf(out[n][2 * i + 1], unit, m) * f;
-                    *reinterpret_cast<float2*>(&sums[g + 8 * i][8 * n + 2 * t]) =
-                        some ? make_float2(x, z) : make_float2(0.f, 0.f);
+                    const float unit = (n & 1 ? high : low) * f;
+                    const float x = fmaf(out[n][2 * i], unit, m[n >> 3]);
+                    const float z = fmaf(out[n][2 * i + 1], unit, m[n >> 3]);
+                    *reinterpret_cast<float2*>(dst + 8 * n) =
+                        none ? make_float2(0.f, 0.f) : make_float2(x, z);
                 }
             }
         });
