@@ -19,8 +19,8 @@
 //  - One persistent CTA per SM: a TMA warp, a thread that issues the MMAs, four
 //    softmax warps for each tile, four warps that write finished tiles, so the
 //    next item's first block overlaps the last one's end.
-//  - Items go out longest first, by a list that attn_plan_kernel sorts and a
-//    ticket counter; a call whose items fit one per SM needs neither.
+//  - Items go out by a ticket counter in the order that attn_plan_kernel writes;
+//    a call whose items fit one per SM needs neither.
 #include <cmath>
 
 #include "attn_common.h"
@@ -46,7 +46,9 @@ struct PrefillArgs {
     int t_q, t_k, n_seqs, heads, kv_heads, window;
     int group, tile_tokens;  // heads per KV head; tokens per tile
     float scale;
-    int4* list;       // sorted entries; null: the slots themselves, one item per CTA
+    int4* list;       // ordered entries; null: the slots themselves, one item per CTA
+    int4* group_of;   // of an entry: its sequence's first entry, their number, KV heads at a time
+    int* first_entry; // of a sequence
     unsigned* count;  // entries in the list, then the ticket counter
     Redo* redo;  // [item][tile][warp]
     int slots, bucket_shift;
@@ -110,16 +112,23 @@ __device__ __forceinline__ void key_blocks(const PrefillArgs& a, int pos, int to
     if (hi < lo) hi = lo;
 }
 
-// Writes the entries, most key blocks first (a counting sort), and zeroes the
-// ticket counter.  One CTA: at 16 prompts of 512 to 8192 tokens it sorts about
-// 1100 entries.
+// Writes the entries in the order in which they are worked on, and zeroes the
+// ticket counter: sequences with the most keys first (a counting sort), of each
+// its last tokens first.  Items are a sequence's entries for as many KV heads as
+// have kL2Bytes of keys and values, heads innermost, then for the next ones: what
+// runs at a time reads what the L2 cache holds, and the last items are short.
+// (Entries of all sequences sorted together: 2187 us at the front end's 16
+// prompts, whose keys and values are 360 MB; a head at a time: 1854, but 358
+// instead of 346 for one of 8192 tokens, whose last head then keeps few CTAs.)
+// One CTA; at those prompts it writes about 1400 entries.
+constexpr long long kL2Bytes = 48 << 20;
 constexpr int kPlanThreads = 1024;
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(PrefillArgs a) {
     __shared__ int hist[kPlanThreads];
     __shared__ int warp_sum[32];
     pdl_wait();
     pdl_release();
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, span = 2 * a.tile_tokens;
     hist[tid] = 0;
     if (tid < 32 && a.cu_q) {
         const bool ok = warp_offsets_ok(a.cu_q, a.n_seqs, a.t_q) &&
@@ -127,28 +136,18 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(PrefillArgs a) 
         if (!ok && tid == 0) atomicOr(&g_attn_status, STATUS_BAD_CU_SEQLENS);
     }
     __syncthreads();
-    // bucket 0 holds the longest entries
-    auto entry_of = [&](int slot, Entry& e, int& bucket) {
-        int lo = 0, n = a.n_seqs;
-        while (n > 1) {
-            const int half = n / 2;
-            if (first_slot(a, lo + half) <= slot) {
-                lo += half;
-                n -= half;
-            } else {
-                n = half;
-            }
-        }
-        if (!slot_entry(a, lo, slot, e)) return false;
-        int b0, b1;
-        key_blocks(a, e.pos, e.tokens, b0, b1);
-        bucket = kPlanThreads - 1 - min((b1 - b0) >> a.bucket_shift, kPlanThreads - 1);
-        return true;
+    // bucket 0 holds the longest sequences
+    auto sequence = [&](int n, int& bucket) {
+        Span s;
+        if (!sequence_span(a, n, s)) return 0;
+        bucket = kPlanThreads - 1 - min(s.lk >> (7 + a.bucket_shift), kPlanThreads - 1);
+        return (s.lq + span - 1) / span;
     };
-    Entry e;
-    int bucket;
-    for (int s = tid; s < a.slots; s += kPlanThreads)
-        if (entry_of(s, e, bucket)) atomicAdd(&hist[bucket], 1);
+    int bucket = 0;
+    for (int n = tid; n < a.n_seqs; n += kPlanThreads) {
+        const int entries = sequence(n, bucket);
+        if (entries) atomicAdd(&hist[bucket], entries);
+    }
     __syncthreads();
     const int mine = hist[tid];
     int sum = mine;
@@ -167,9 +166,32 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(PrefillArgs a) 
         a.count[1] = 0;
     }
     __syncthreads();
-    for (int s = tid; s < a.slots; s += kPlanThreads)
-        if (entry_of(s, e, bucket))
-            a.list[atomicAdd(&hist[bucket], 1)] = make_int4(e.row, e.tokens, e.k0, e.pos);
+    for (int n = tid; n < a.n_seqs; n += kPlanThreads) {
+        const int entries = sequence(n, bucket);
+        a.first_entry[n] = entries ? atomicAdd(&hist[bucket], entries) : 0;
+    }
+    __syncthreads();
+    for (int slot = tid; slot < a.slots; slot += kPlanThreads) {
+        int n = 0, left = a.n_seqs;
+        while (left > 1) {
+            const int half = left / 2;
+            if (first_slot(a, n + half) <= slot) {
+                n += half;
+                left -= half;
+            } else {
+                left = half;
+            }
+        }
+        Entry e;
+        if (!slot_entry(a, n, slot, e)) continue;
+        const int base = a.first_entry[n], entries = sequence(n, bucket);
+        const int at = base + entries - 1 - (int)(slot - first_slot(a, n));
+        a.list[at] = make_int4(e.row, e.tokens, e.k0, e.pos);
+        Span whole;
+        sequence_span(a, n, whole);
+        const long long head_bytes = max(1LL, (long long)whole.lk) * (4 * D);
+        a.group_of[at] = make_int4(base, entries, (int)max(1LL, kL2Bytes / head_bytes), 0);
+    }
 }
 
 // One row on the CUDA cores by one warp, 4 channels a lane, touching only the
@@ -315,11 +337,18 @@ __device__ __forceinline__ void load_role(const PrefillArgs& a, Shared& sh, unsi
             unsigned x = 0;
             if (lane == 0) x = atomicAdd(a.count + 1, 1u);
             x = __shfl_sync(0xffffffffu, x, 0);
+            // any entry of the item's sequence, then the item's
             const unsigned e = x / (unsigned)a.kv_heads;
             if (e < (unsigned)n_list) {
-                const int4 v = __ldcg(a.list + e);
+                const int4 seq = __ldcg(a.group_of + e);
+                int i = (int)(x - (unsigned)seq.x * a.kv_heads);
+                const int heads = min(seq.z, a.kv_heads);  // of a full group
+                const int group = i / (seq.y * heads), first = group * heads;
+                i -= group * seq.y * heads;
+                const int here = min(heads, a.kv_heads - first);
+                it.head = first + i % here;
+                const int4 v = __ldcg(a.list + seq.x + i / here);
                 it.e = {v.x, v.y, v.z, v.w};
-                it.head = (int)(x - e * a.kv_heads);
                 it.index = (int)x;
             }
         } else if (round == 0) {
@@ -850,10 +879,11 @@ extern "C" size_t kda_attn_prefill_workspace_size(int64_t rows, int n_seqs, int 
     if (rows < 0 || n_seqs < 1 || heads < 1 || kv_heads < 1 || heads % kv_heads ||
         heads / kv_heads > 128)
         return 0;
-    // the ticket counter, 16 bytes an entry, eight records of rows to be done
-    // again per item
+    // the ticket counter, 32 bytes an entry, 4 a sequence, eight records of rows
+    // to be done again per item
     const size_t slots = (size_t)slot_count(rows, n_seqs, heads / kv_heads);
-    return 256 + 16 * slots + 8 * sizeof(Redo) * slots * kv_heads;
+    return 256 + 32 * slots + 16 * (((size_t)n_seqs + 3) / 4) +
+           8 * sizeof(Redo) * slots * kv_heads;
 }
 
 extern "C" kda_status kda_attn_prefill(const void* q, const void* k, const void* v, void* o,
@@ -923,11 +953,14 @@ extern "C" kda_status kda_attn_prefill(const void* q, const void* k, const void*
     while ((t_k / 128 >> shift) >= kPlanThreads) ++shift;
     unsigned* count = static_cast<unsigned*>(workspace);
     int4* list = reinterpret_cast<int4*>(static_cast<unsigned char*>(workspace) + 256);
+    int4* group_of = list + slots;
+    int* first_entry = reinterpret_cast<int*>(group_of + slots);
+    Redo* redo = reinterpret_cast<Redo*>(first_entry + 4 * ((n_seqs + 3LL) / 4));
     PrefillArgs a = {(const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, (uint16_t*)o,
                      lse, cu_seqlens_q, cu_seqlens_k, q_row_stride, k_row_stride, v_row_stride,
                      o_row_stride, t_q, t_k, n_seqs, heads, kv_heads, window, group, tokens,
-                     scale, direct ? nullptr : list, count, reinterpret_cast<Redo*>(list + slots),
-                     (int)slots, shift};
+                     scale, direct ? nullptr : list, group_of, first_entry, count, redo, (int)slots,
+                     shift};
     auto kernel = f16 ? attn_prefill_kernel<true> : attn_prefill_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)kSmemBytes);
