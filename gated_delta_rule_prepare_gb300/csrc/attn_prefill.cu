@@ -21,6 +21,7 @@
 //    next item's first block overlaps the last one's end.
 //  - Items go out by a ticket counter in the order that attn_plan_kernel writes;
 //    a call whose items fit one per SM needs neither.
+#include <algorithm>
 #include <cmath>
 
 #include "attn_common.h"
@@ -52,6 +53,9 @@ struct PrefillArgs {
     unsigned* count;  // entries in the list, then the ticket counter
     Redo* redo;  // [item][tile][warp]
     int slots, bucket_shift;
+    int splits;          // CTAs that share an item's keys; over 1 without a list only
+    float* part;         // their outputs [item][split][256 rows][128], unscaled
+    float2* part_stat;   // and (shift, sum) of their rows
 };
 
 // Sequence n's query and key rows; false for offsets outside the arrays.
@@ -256,8 +260,9 @@ constexpr float kLift = F16 ? 7.f : 0.f;
 
 struct Item {
     Entry e;
-    int head;   // KV head; negative: no more items
-    int index;  // of all the call's items
+    int head;      // KV head; negative: no more items
+    int index;     // of all the call's items
+    int from, to;  // key blocks of it that this CTA has
 };
 
 struct Shared {
@@ -302,12 +307,14 @@ __device__ __forceinline__ bool wait_warp(Shared& sh, uint64_t* bar, uint32_t pa
 struct Tile {
     int tokens, pos, lo, hi;
 };
-__device__ __forceinline__ Tile tile_of(const PrefillArgs& a, const Entry& e, int t) {
+__device__ __forceinline__ Tile tile_of(const PrefillArgs& a, const Item& it, int t) {
     Tile r;
-    r.tokens = min(a.tile_tokens, e.tokens - t * a.tile_tokens);
+    r.tokens = min(a.tile_tokens, it.e.tokens - t * a.tile_tokens);
     if (r.tokens < 0) r.tokens = 0;
-    r.pos = e.pos + t * a.tile_tokens;
+    r.pos = it.e.pos + t * a.tile_tokens;
     key_blocks(a, r.pos, r.tokens, r.lo, r.hi);
+    r.lo = max(r.lo, it.from);
+    r.hi = max(r.lo, min(r.hi, it.to));
     return r;
 }
 // The union of both tiles' blocks (their ranges overlap or touch).
@@ -333,6 +340,8 @@ __device__ __forceinline__ void load_role(const PrefillArgs& a, Shared& sh, unsi
     for (int round = 0; go; ++round) {
         Item it;
         it.head = -1;
+        it.from = 0;
+        it.to = 0x7fffffff;
         if (a.list) {
             unsigned x = 0;
             if (lane == 0) x = atomicAdd(a.count + 1, 1u);
@@ -352,10 +361,18 @@ __device__ __forceinline__ void load_role(const PrefillArgs& a, Shared& sh, unsi
                 it.index = (int)x;
             }
         } else if (round == 0) {
-            const int slot = blockIdx.x / a.kv_heads;
+            it.index = blockIdx.x / a.splits;
+            const int slot = it.index / a.kv_heads, split = blockIdx.x - it.index * a.splits;
             const int n = warp_find_last(a.n_seqs, slot, [&](int i) { return first_slot(a, i); });
-            if (slot_entry(a, n, slot, it.e)) it.head = blockIdx.x - slot * a.kv_heads;
-            it.index = blockIdx.x;
+            if (slot_entry(a, n, slot, it.e)) {
+                it.head = it.index - slot * a.kv_heads;
+                if (a.splits > 1) {
+                    const Blocks b = blocks_of(tile_of(a, it, 0), tile_of(a, it, 1));
+                    const int each = (b.hi - b.lo + a.splits - 1) / a.splits;
+                    it.from = b.lo + split * each;
+                    it.to = it.from + each;
+                }
+            }
         }
         if (lane == 0) {
             go = wait(sh, &sh.item_empty[ring], ring_phase ^ 1);
@@ -368,7 +385,7 @@ __device__ __forceinline__ void load_role(const PrefillArgs& a, Shared& sh, unsi
         go = __shfl_sync(0xffffffffu, go && it.head >= 0, 0);
         if (!go) break;
         if (lane == 0) {
-            const Tile tile[2] = {tile_of(a, it.e, 0), tile_of(a, it.e, 1)};
+            const Tile tile[2] = {tile_of(a, it, 0), tile_of(a, it, 1)};
             const uint32_t q_bytes = (uint32_t)(a.group * a.tile_tokens) * 256;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -446,7 +463,7 @@ __device__ __forceinline__ void mma_role(const PrefillArgs& a, Shared& sh, unsig
         if (lane0) mbar_arrive(&sh.item_empty[ring]);
         if (++ring == kRing) ring = 0, ring_phase ^= 1;
         if (uniform(it.head) < 0) return;
-        const Tile x = tile_of(a, it.e, 0), y = tile_of(a, it.e, 1);
+        const Tile x = tile_of(a, it, 0), y = tile_of(a, it, 1);
         const Blocks b = blocks_of(x, y);
         const int b_hi = uniform(b.hi), lo = uniform(t ? y.lo : x.lo), hi = uniform(t ? y.hi : x.hi);
         const int b_lo = uniform(b.lo);
@@ -574,7 +591,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, i
         if (lane == 0) mbar_arrive(&sh.item_empty[ring]);
         if (++ring == kRing) ring = 0, ring_phase ^= 1;
         if (it.head < 0) return;
-        const Tile tile = tile_of(a, it.e, t);
+        const Tile tile = tile_of(a, it, t);
         if (tile.hi <= tile.lo) continue;
         // keys first..pos; a row that is none of the tile's sees none
         const int pos = token < tile.tokens ? tile.pos + token : -1;
@@ -687,7 +704,8 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, i
         sh.sum[t][r] = l;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.sum_full[t]);
-        if (a.lse && token < tile.tokens) {
+        if (a.splits > 1) a.part_stat[blockIdx.x * 256LL + t * 128 + r] = make_float2(shift, l);
+        else if (a.lse && token < tile.tokens) {
             const long long row = (long long)it.e.row + t * a.tile_tokens + token;
             a.lse[row * a.heads + it.head * a.group + r - token * a.group] =
                 l == 0.f ? -INFINITY : (log2f(l) - shift) * kLn2;
@@ -713,7 +731,7 @@ __device__ __forceinline__ void write_role(const PrefillArgs& a, Shared& sh) {
         const int h = it.head * a.group + in_group;
 #pragma unroll 1
         for (int t = 0; t < 2; ++t) {
-            const Tile tile = tile_of(a, it.e, t);
+            const Tile tile = tile_of(a, it, t);
             if (tile.tokens == 0) continue;
             const bool mine = token < tile.tokens;
             const long long row = (long long)it.e.row + t * a.tile_tokens + token;
@@ -730,12 +748,26 @@ __device__ __forceinline__ void write_role(const PrefillArgs& a, Shared& sh) {
             const bool empty = l == 0.f;
             const float inv = empty ? 0.f : 1.f / l;
             float poison = 0.f;  // NaN once any value is not finite
+            float* const part = a.splits > 1
+                                    ? a.part + (blockIdx.x * 256LL + t * 128 + r) * D
+                                    : nullptr;
+            if (part && !any) {
+                a.part_stat[blockIdx.x * 256LL + t * 128 + r] = make_float2(0.f, 0.f);
+                continue;
+            }
 #pragma unroll 1
             for (int i = 0; i < 8; ++i) {
                 float o[16];
                 if (any) {
                     tmem_ld16(row_addr + t * 128 + 16 * i, o);
                     tmem_ld_wait();
+                }
+                if (part) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        reinterpret_cast<float4*>(part + 16 * i)[x] =
+                            make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                    continue;
                 }
                 uint32_t u[8];
 #pragma unroll
@@ -758,6 +790,7 @@ __device__ __forceinline__ void write_role(const PrefillArgs& a, Shared& sh) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.o_empty[t]);
             }
+            if (part) continue;
             if (!any && mine && a.lse) a.lse[row * a.heads + h] = -INFINITY;
             // a sum that is NaN comes from a key that the row sees
             const unsigned again = __ballot_sync(
@@ -846,10 +879,84 @@ attn_prefill_kernel(PrefillArgs a, const __grid_constant__ CUtensorMap mq,
     }
 }
 
+// Joins the parts of a call whose items are shared by several CTAs: a row to a
+// warp, four channels a lane.
+constexpr int kJoinWarps = 8;
+template <bool F16>
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_prefill_join_kernel(PrefillArgs a) {
+    const int lane = threadIdx.x & 31;
+    const long long at = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+    pdl_wait();
+    Item it;
+    it.index = (int)(at >> 8);
+    it.from = 0;
+    it.to = 0x7fffffff;
+    const int slot = it.index / a.kv_heads, t = (int)(at >> 7) & 1, r = (int)at & 127;
+    const int n = warp_find_last(a.n_seqs, slot, [&](int i) { return first_slot(a, i); });
+    if (!slot_entry(a, n, slot, it.e)) return;
+    const Tile tile = tile_of(a, it, t);
+    const int token = r / a.group;
+    if (token >= tile.tokens) return;
+    const long long first = ((long long)it.index * a.splits << 8) + t * 128 + r;
+    // up to 152 parts: their factors a lane each, then their channels
+    float least = INFINITY, sum = 0.f;
+    for (int p = lane; p < a.splits; p += 32) {
+        const float2 s = __ldcg(a.part_stat + first + 256LL * p);
+        if (s.y != 0.f) least = fminf(least, s.x);
+    }
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1)
+        least = fminf(least, __shfl_xor_sync(0xffffffffu, least, off));
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = 0; p0 < a.splits; p0 += 32) {
+        float f = 0.f;
+        if (p0 + lane < a.splits) {
+            const float2 s = __ldcg(a.part_stat + first + 256LL * (p0 + lane));
+            if (s.y != 0.f) {
+                f = ex2_approx(least - s.x);
+                sum = fmaf(s.y, f, sum);
+            }
+        }
+        const int here = min(32, a.splits - p0);
+#pragma unroll 4
+        for (int i = 0; i < here; ++i) {
+            const float fi = __shfl_sync(0xffffffffu, f, i);
+            if (fi == 0.f) continue;  // (nothing was written where there was no key)
+            const float4 x = __ldcg(
+                reinterpret_cast<const float4*>(a.part + (first + 256LL * (p0 + i)) * D) + lane);
+            o.x = fmaf(x.x, fi, o.x);
+            o.y = fmaf(x.y, fi, o.y);
+            o.z = fmaf(x.z, fi, o.z);
+            o.w = fmaf(x.w, fi, o.w);
+        }
+    }
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    const int h = (it.index - slot * a.kv_heads) * a.group + r - token * a.group;
+    const long long row = (long long)it.e.row + t * a.tile_tokens + token;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+    const float poison = (o.x + o.y + o.z + o.w) * 0.f;
+    if (__any_sync(0xffffffffu, (poison != poison && sum == sum) || sum == INFINITY)) {
+        attend_row<F16>(a, row, it.e.k0, tile.pos + token, h);
+        return;
+    }
+    *reinterpret_cast<uint2*>(a.o + row * a.o_stride + h * D + 4 * lane) =
+        make_uint2(narrow2<F16>(o.x, o.y), narrow2<F16>(o.z, o.w));
+    if (a.lse && lane == 0)
+        a.lse[row * a.heads + h] =
+            sum == 0.f ? -INFINITY : (log2f(sum) - least) * kLn2;
+}
+
 // Items of a call, at most: slots of all sequences.
 inline long long slot_count(long long rows, int n_seqs, int group) {
     return rows / (2 * (128 / group)) + n_seqs;
 }
+// CTAs that may share an item's keys where items are few, on kSms
+// multiprocessors or more: the workspace is sized for so many.
+constexpr int kSms = 152;
+inline int most_splits(long long items) { return items * 2 <= kSms ? (int)(kSms / items) : 1; }
+constexpr size_t kPartBytes = 256 * (128 + 2) * sizeof(float);
 
 }  // namespace
 
@@ -882,8 +989,10 @@ extern "C" size_t kda_attn_prefill_workspace_size(int64_t rows, int n_seqs, int 
     // the ticket counter, 32 bytes an entry, 4 a sequence, eight records of rows
     // to be done again per item
     const size_t slots = (size_t)slot_count(rows, n_seqs, heads / kv_heads);
-    return 256 + 32 * slots + 16 * (((size_t)n_seqs + 3) / 4) +
-           8 * sizeof(Redo) * slots * kv_heads;
+    const size_t items = slots * kv_heads;
+    const int splits = most_splits((long long)items);
+    return 256 + 32 * slots + 16 * (((size_t)n_seqs + 3) / 4) + 8 * sizeof(Redo) * items +
+           (splits > 1 ? splits * items * kPartBytes : 0);
 }
 
 extern "C" kda_status kda_attn_prefill(const void* q, const void* k, const void* v, void* o,
@@ -949,6 +1058,12 @@ extern "C" kda_status kda_attn_prefill(const void* q, const void* k, const void*
     // One CTA per item needs no order and no tickets: the call is one kernel.
     const long long items = slots * kv_heads;
     const bool direct = items <= sms;
+    // Few items behind many keys: CTAs share an item's keys, at least four blocks
+    // to each, and a second kernel joins them (16 tokens behind 30000, 32 heads
+    // over 8: JOINED us where one CTA an item takes ALONE).
+    const int blocks = (t_k + 127) / 128;
+    int splits = direct ? std::min(most_splits(items), blocks / 4) : 1;
+    if (splits < 1 || sms < kSms) splits = 1;
     int shift = 0;  // buckets of 2^shift key blocks in the plan's sort
     while ((t_k / 128 >> shift) >= kPlanThreads) ++shift;
     unsigned* count = static_cast<unsigned*>(workspace);
@@ -956,11 +1071,13 @@ extern "C" kda_status kda_attn_prefill(const void* q, const void* k, const void*
     int4* group_of = list + slots;
     int* first_entry = reinterpret_cast<int*>(group_of + slots);
     Redo* redo = reinterpret_cast<Redo*>(first_entry + 4 * ((n_seqs + 3LL) / 4));
+    float* part = reinterpret_cast<float*>(redo + 8 * items);
+    float2* part_stat = reinterpret_cast<float2*>(part + 256LL * D * items * splits);
     PrefillArgs a = {(const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, (uint16_t*)o,
                      lse, cu_seqlens_q, cu_seqlens_k, q_row_stride, k_row_stride, v_row_stride,
                      o_row_stride, t_q, t_k, n_seqs, heads, kv_heads, window, group, tokens,
                      scale, direct ? nullptr : list, group_of, first_entry, count, redo, (int)slots,
-                     shift};
+                     shift, splits, part, part_stat};
     auto kernel = f16 ? attn_prefill_kernel<true> : attn_prefill_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)kSmemBytes);
@@ -970,7 +1087,10 @@ extern "C" kda_status kda_attn_prefill(const void* q, const void* k, const void*
     }
     cudaStream_t s = as_stream(stream);
     if (!direct) launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a);
-    launch_pdl(kernel, dim3((unsigned)(direct ? items : sms)), dim3(kThreads), kSmemBytes, s, a,
-               mq, mk, mv);
+    launch_pdl(kernel, dim3((unsigned)(direct ? items * splits : sms)), dim3(kThreads), kSmemBytes,
+               s, a, mq, mk, mv);
+    if (splits > 1)
+        launch_pdl(f16 ? attn_prefill_join_kernel<true> : attn_prefill_join_kernel<false>,
+                   dim3((unsigned)(items * 256 / kJoinWarps)), dim3(kJoinWarps * 32), 0, s, a);
     return launch_result(fn);
 }

@@ -267,3 +267,29 @@ def test_binding_refusals():
         K.kda_attn_prefill(q, k, v, o, window=-1)
     with pytest.raises(K.KdaError):
         K.kda_attn_prefill(q, k, v, o, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("lq,lk,heads,kv,window", [
+    ([1], [4000], 8, 2, 0), ([16, 0, 3], [6000, 900, 2], 5, 1, 0), ([40, 7], [3000, 5000], 4, 4, 700),
+    ([300], [2100], 16, 1, 0)])
+def test_few_queries_behind_many_keys(lq, lk, heads, kv, window, dtype):
+    """So few items that CTAs share an item's keys and a second kernel joins them."""
+    run(lq, lk, heads, kv, dtype, window=window, seed=20)
+
+
+def test_shared_items_and_hidden_bad_values():
+    K = kda()
+    q, k, v = draw(21, [6], [5000], 4, 2, torch.bfloat16)
+    v[4997, 0, 3] = float("nan")      # seen by the last three rows
+    v[100] = float("inf")             # by none, with the window
+    k[101] = float("nan")
+    o, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    K.kda_attn_prefill(q, k, v, o, lse=lse, window=4000)
+    k[101], v[100] = 0, 0
+    ref = attend64(q.double(), k.double(), torch.nan_to_num(v).double(), 4000)
+    seen = torch.zeros_like(o, dtype=torch.bool)
+    seen[3:, :2, 3] = True
+    assert bool(torch.isnan(o[seen]).all())
+    o[seen] = ref[0][seen].to(o.dtype)
+    close(o, lse, ref, torch.bfloat16)
