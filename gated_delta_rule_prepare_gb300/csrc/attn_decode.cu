@@ -12,14 +12,19 @@
 //    low end of an FP16 number are a subnormal, code * 2^-24, the next four
 //    code * 2^-20: one AND makes two operands, and the powers of two go into q
 //    and the output.
-//  - The cache keeps codes in the order of mma.sync's A operand: keys (or value
-//    channels) are the product's 16 rows, queries its 8 columns, so that one
-//    query row in use wastes 7 of 8 columns of an instruction that is not the
-//    bound, and no shared-memory transposition is needed.
-//  - A score's columns are queries, as an output's are: running sums and
-//    rescaling stay within a lane.  p_t s_ta is rounded to FP16 after a common
-//    power of two that keeps it below 2^15 (11 significant bits; weights down to
-//    2^-33 of the largest); scores, sums and outputs are FP32.
+//  - The cache keeps codes in the order of mma.sync's A operand, which is also
+//    that of two B operands: up to 8 queries are the 8 columns of the products
+//    (keys, or value channels, the 16 rows: attend_narrow), more are the 16 rows
+//    (attend_wide).  Codes go from the copied page to registers, nothing is
+//    transposed in shared memory.
+//  - A score's place is its query's in the output too: running sums and rescaling
+//    stay within a lane.  p_t s_ta is rounded to FP16 after a common power of two
+//    that keeps it below 2^15 (11 significant bits; weights down to 2^-33 of the
+//    largest); scores, sums and outputs are FP32.
+// What bounds it then is the issue of instructions and, in short segments, their
+// starts and ends.  64 sequences of 2000 to 8192 tokens, 32 heads over 8: 92.6 us, 4.0
+// TB/s; 128 sequences of 4 rows (16 queries a KV head): 193 us, 2.1 TB/s; one of
+// 131000 tokens and 2 rows: 43 us.
 //
 // All positions of the batch, in chunks of 128 tokens, are one line that the
 // CTAs cut into equal pieces, whatever the lengths: a piece ends where it ends,
@@ -54,9 +59,7 @@ __device__ unsigned g_decode_status = 0;
 // cache.
 constexpr int kWarps = 4;  // and one that copies
 constexpr int kThreads = (kWarps + 1) * 32;
-template <bool WIDE>
 constexpr int kCtas = 3;  // to a multiprocessor
-template <bool WIDE>
 constexpr int kStages = 3;
 constexpr int kGroups = 8;
 constexpr int kChunk = kGroups * 16;  // tokens
@@ -146,8 +149,8 @@ constexpr int kPad = 132;  // a query's 128 sums, so that a warp's stores meet a
 constexpr int kBuffers = 2;
 template <bool WIDE>
 struct Shared {
-    uint64_t full[kStages<WIDE>], empty[kStages<WIDE>];
-    Stage stage[kStages<WIDE>];
+    uint64_t full[kStages], empty[kStages];
+    Stage stage[kStages];
     // by query, the factor from a product to a score in log2 units, the sums over
     // 64 channels, and the first position that is not seen
     float unit[kRows<WIDE>];
@@ -167,7 +170,7 @@ struct Shared {
 };
 template <bool WIDE>
 constexpr int smem_bytes() {
-    return kStages<WIDE> * kStageBytes + (int)sizeof(Shared<WIDE>);
+    return kStages * kStageBytes + (int)sizeof(Shared<WIDE>);
 }
 
 template <bool B>
@@ -196,8 +199,8 @@ __device__ __forceinline__ bool wait_warp(Shared<WIDE>& sh, uint64_t* bar, uint3
 // Tokens that lie together in the cache and in a stage: a stage holds pieces of
 // so many, each laid out as a page of its size, so that a page of up to 128
 // tokens is one copy.  (Small copies cost what large ones do: with four to a
-// page, codes and parameters apart, copying alone took 75 us where it takes
-// COPYUS, 64 sequences of 2000 to 8192 tokens.)
+// page, codes and parameters apart, copying alone took 75 us where it takes 66 to
+// 68, 64 sequences of 2000 to 8192 tokens.)
 __device__ __forceinline__ int piece_tokens(const DecodeArgs& a) { return min(a.c.page(), 128); }
 
 // Where a stage's group of 16 tokens has its codes and parameters of K; those of
@@ -315,7 +318,7 @@ __device__ __forceinline__ void copy_role(const DecodeArgs& a, Shared<WIDE>& sh,
                     }
                 }
                 __syncwarp();
-                if (++stage == kStages<WIDE>) stage = 0, phase ^= 1;
+                if (++stage == kStages) stage = 0, phase ^= 1;
             }
         }
         n_start += (long long)ch.count * per_seq;
@@ -328,7 +331,7 @@ __device__ __forceinline__ void copy_role(const DecodeArgs& a, Shared<WIDE>& sh,
             mbar_arrive(&sh.full[stage]);
         } else {
             // copies in flight land before the CTA's memory goes away
-            for (int s = 0; s < kStages<WIDE>; ++s)
+            for (int s = 0; s < kStages; ++s)
                 mbar_wait(&sh.full[s], s < stage ? phase : phase ^ 1, 1 << 12);
         }
     }
@@ -736,7 +739,7 @@ __device__ __forceinline__ void attend_narrow(const DecodeArgs& a, Shared<false>
         if (end) st = sh.stage[stage];
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.empty[stage]);
-        if (++stage == kStages<false>) stage = 0, phase ^= 1;
+        if (++stage == kStages) stage = 0, phase ^= 1;
         if (!end) continue;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -967,7 +970,7 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
         if (end) st = sh.stage[stage];
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.empty[stage]);
-        if (++stage == kStages<true>) stage = 0, phase ^= 1;
+        if (++stage == kStages) stage = 0, phase ^= 1;
         if (!end) continue;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -999,12 +1002,12 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
 }
 
 template <bool F16, bool WIDE>
-__global__ void __launch_bounds__(kThreads, kCtas<WIDE>) attn_decode_kernel(DecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtas) attn_decode_kernel(DecodeArgs a) {
     extern __shared__ __align__(128) uint8_t sm[];
-    Shared<WIDE>& sh = *reinterpret_cast<Shared<WIDE>*>(sm + kStages<WIDE> * kStageBytes);
+    Shared<WIDE>& sh = *reinterpret_cast<Shared<WIDE>*>(sm + kStages * kStageBytes);
     if (threadIdx.x == 0) {
         sh.stop = 0;
-        for (int i = 0; i < kStages<WIDE>; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             mbar_init(&sh.full[i], 1);
             mbar_init(&sh.empty[i], kWarps);
         }
@@ -1151,8 +1154,8 @@ cudaError_t read_and_clear_status_decode(unsigned* out) {
 
 using namespace kda;
 
-// Two incomplete segments per CTA, 152 SMs' worth of CTAs (more on a device with
-// more: see the call).
+// Two incomplete segments per piece; the call makes no more pieces than
+// KDA_KV4_PIECES (three CTAs on each of 160 multiprocessors).
 extern "C" size_t kda_attn_kv4_workspace_size(int n_seqs, int krows, int heads, int kv_heads) {
     if (n_seqs < 1 || krows < 1 || krows > KDA_MAX_K || heads < 1 || kv_heads < 1 ||
         heads % kv_heads)
@@ -1195,7 +1198,7 @@ extern "C" kda_status kda_attn_kv4_decode(const void* q, const uint8_t* cache, i
     KDA_REQUIRE(aligned16(workspace), KDA_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned",
                 fn);
     KDA_REQUIRE(!fault_injected(), KDA_ERR_CUDA, "%s: injected launch failure", fn);
-    const int ctas = (cols == 8 ? kCtas<false> : kCtas<true>) * sm_count();
+    const int ctas = kCtas * sm_count();
     const int pieces = ctas < KDA_KV4_PIECES ? ctas : KDA_KV4_PIECES;
     KDA_REQUIRE(pieces > 0, KDA_ERR_CUDA, "%s: no device", fn);
     DecodeArgs a = {(const uint16_t*)q, (uint16_t*)o, lse, n_seqs, krows, heads, window, group,

@@ -8,10 +8,12 @@
 // numbers, not of a rounding on the way: the kernel gets them from directed
 // FP32 operations and decides values near a border between two codes apart.
 //
-// Both kernels give one warp 16 tokens of one head of K or of V: one group of
-// the cache, 1024 bytes of codes, staged in shared memory so that global
-// memory sees 16-byte accesses on both sides.  Memory-bound: 512 + 144 bytes
-// per (token, head).
+// Both kernels give one warp 16 tokens of one head: one group of the cache, 1024
+// bytes of codes, staged in shared memory so that global memory sees 16-byte
+// accesses on both sides; of K and then of V, or with few tokens one of them.
+// Memory-bound in principle, 512 + 144 bytes per (token, head); at the front
+// end's batch (88 thousand tokens, 8 heads) read takes 67 us, 5.8 TB/s, and
+// append 110 us, 4.2 TB/s, bound by the issue of its exact rounding's instructions.
 #include "attn_common.h"
 #include "f32x2.h"
 
@@ -134,7 +136,7 @@ __device__ __noinline__ uint32_t code_exact(float x, float m, float s) {
 // on it.  k + 0.5 has 5 bits and s has 8, so b is exact in FP32 unless m and s are
 // more than 2^10 apart: ten operations a value, no case apart for ties
 // (of BF16 rows some 1 in 300 values is one; deciding those in a branch took
-// 640 us for the front end's batch where this takes APPENDUS).
+// 640 us for the front end's batch where this takes 110).
 __device__ __forceinline__ float2 fma2_down(float2 a, float2 b, float2 c) {  // rounded down
     unsigned long long r;
     asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pk(a)), "l"(pk(b)), "l"(pk(c)));
@@ -440,8 +442,9 @@ kda_status rows_call(const char* fn, bool append, void* k, void* v, int64_t k_st
     RowArgs a = {(uint16_t*)k, (uint16_t*)v, k_stride, v_stride, cu, t, n_seqs,
                  {cache, table, lens, n_pages, max_pages, __builtin_ctz((unsigned)page), kv_heads}};
     const long long slots = rows / 16 + 2LL * n_seqs;
-    // K and V in one warp share the search for its tokens (REPLACEUS at the front
-    // end's batch against two warps' REPLACE2); few tokens are done sooner apart.
+    // K and V in one warp share the search for its tokens (append and read of the
+    // front end's batch: 215 us, apart 231, when this was chosen); few tokens are
+    // done sooner apart.
     const unsigned apart = slots * kv_heads < 16LL * 152 ? 2 : 1;
     const dim3 grid((unsigned)((slots + kWarps - 1) / kWarps), (unsigned)kv_heads, apart);
     const dim3 threads(kWarps * 32);

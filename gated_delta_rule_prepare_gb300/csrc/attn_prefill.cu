@@ -13,14 +13,19 @@
 //    little of its last key block is masked.
 //  - A work item is two such tiles, one after the other in the sequence, and
 //    walks their keys in blocks of 128.  S = Q K^T (FP32) sits in TMEM, one
-//    thread owns one row of it, and writes exp2(S - max) over it in 16 bits,
+//    thread owns one row of it, and writes exp2(S - shift) over it in 16 bits,
 //    from where the second product reads it as its A operand.  The tensor
 //    cores work for one tile while the other tile's softmax runs.
-//  - One persistent CTA per SM: a TMA warp, a thread that issues the MMAs, four
-//    softmax warps for each tile, four warps that write finished tiles, so the
-//    next item's first block overlaps the last one's end.
+//  - One persistent CTA per SM: a TMA warp, a warp for each tile that issues its
+//    MMAs, four softmax warps for each tile, four warps that write finished
+//    tiles, so the next item's first block overlaps the last one's end.
 //  - Items go out by a ticket counter in the order that attn_plan_kernel writes;
-//    a call whose items fit one per SM needs neither.
+//    a call whose items fit one per SM needs neither, and one whose items are few
+//    and long shares an item's keys between CTAs.
+// BF16, 32 heads over 8: 1634 TFLOP/s at 8192 tokens, 1713 to 1783 at 32768, 1576
+// at 16 packed prompts of 512 to 8192 (cuBLAS's 8192^3 product: 1940).  What is
+// left is an item's start and end, a part of a round when items do not fill the
+// SMs evenly, and the issue of the softmax.
 #include <algorithm>
 #include <cmath>
 
@@ -1060,7 +1065,7 @@ extern "C" kda_status kda_attn_prefill(const void* q, const void* k, const void*
     const bool direct = items <= sms;
     // Few items behind many keys: CTAs share an item's keys, at least four blocks
     // to each, and a second kernel joins them (16 tokens behind 30000, 32 heads
-    // over 8: JOINED us where one CTA an item takes ALONE).
+    // over 8: 39 us where one CTA an item takes 304).
     const int blocks = (t_k + 127) / 128;
     int splits = direct ? std::min(most_splits(items), blocks / 4) : 1;
     if (splits < 1 || sms < kSms) splits = 1;

@@ -460,7 +460,9 @@ kda_status kda_attn_prefill(const void* q, const void* k, const void* v, void* o
                             size_t workspace_bytes, uint64_t stream);
 
 /* Bytes of workspace kda_attn_prefill needs for `rows` query rows in total.
- * Returns 0 for invalid arguments. */
+ * A few hundred bytes per 256 / heads-per-KV-head rows and KV head; with so few of
+ * these that CTAs may share their keys, up to about 20 MB.  Returns 0 for
+ * invalid arguments. */
 size_t kda_attn_prefill_workspace_size(int64_t rows, int n_seqs, int heads, int kv_heads);
 
 /*
