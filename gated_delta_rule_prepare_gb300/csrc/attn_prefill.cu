@@ -580,12 +580,19 @@ __device__ __forceinline__ void store_words(uint32_t addr, const uint32_t (&v)[3
 // FP16 weights end at 65504: each block's maximum is compared with the shift
 // before, and the shift moves where a weight would pass 2^(kLift + 8).  kLift
 // keeps weights down to 2^-31 of the largest above FP16's smallest number.
+template <bool B>
+struct Bool {
+    static constexpr bool value = B;
+};
+
 template <bool F16>
 __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, int t) {
     const int r = threadIdx.x & 127, lane = threadIdx.x & 31;
     const uint32_t row_addr = sh.tmem + ((uint32_t)(r & ~31) << 16);
     const uint32_t s_addr = row_addr + t * 128, o_addr = row_addr + kTmemO + t * 128;
     const int token = r / a.group;
+    // of the warp's first and last rows
+    const int token_0 = uniform(token), token_1 = __shfl_sync(0xffffffffu, token, 31);
     const float c = a.scale * kLog2e;
     uint32_t s_phase = 0, o_phase = 0, ring_phase = 0;
     int ring = 0;
@@ -598,6 +605,13 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, i
         if (it.head < 0) return;
         const Tile tile = tile_of(a, it, t);
         if (tile.hi <= tile.lo) continue;
+        // The warp's rows see none of the keys before any_lo and from any_hi on, and
+        // all of [all_lo, all_hi): most groups of 32 keys are seen by all of its few
+        // tokens or by none, in the first and last blocks too.
+        const int pos_0 = tile.pos + token_0, pos_1 = tile.pos + min(token_1, tile.tokens - 1);
+        const int any_hi = pos_1 >= pos_0 ? pos_1 + 1 : 0, all_hi = pos_0 + 1;
+        const int any_lo = a.window ? max(0, pos_0 - a.window + 1) : 0;
+        const int all_lo = a.window ? max(0, pos_1 - a.window + 1) : 0;
         // keys first..pos; a row that is none of the tile's sees none
         const int pos = token < tile.tokens ? tile.pos + token : -1;
         const int first = a.window ? max(0, pos - a.window + 1) : 0;
@@ -612,7 +626,13 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, i
             tc_fence_after();
             const bool edge = j < clear_lo || j >= clear_hi;
             // scores of keys 32 i .. 32 i + 31 that the row does not see become -inf
+            auto unseen = [&](int i) {
+                const int at = j * 128 + 32 * i;
+                return at >= any_hi || at + 32 <= any_lo;
+            };
             auto hide = [&](float (&x)[32], int i) {
+                const int at = j * 128 + 32 * i;
+                if (at >= all_lo && at + 32 <= all_hi) return;
                 const int from = max(0, min(32, first - j * 128 - 32 * i));
                 const int n = max(0, min(32, pos - j * 128 - 32 * i + 1));
                 const uint32_t see = (uint32_t)(((1ull << n) - 1) >> from << from);
@@ -641,20 +661,28 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, i
             const bool fresh = l == 0.f && pos >= max(first, j * 128);
             if (F16 || __any_sync(0xffffffffu, fresh)) {
                 float top = -INFINITY;
+                auto most = [&](auto masked) {
 #pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    float x[32], mx[4];
-                    tmem_ld32(s_addr + 32 * i, x);
-                    tmem_ld_wait();
-                    if (edge) hide(x, i);
+                    for (int i = 0; i < 4; ++i) {
+                        if (decltype(masked)::value && unseen(i)) continue;
+                        float x[32], mx[4];
+                        tmem_ld32(s_addr + 32 * i, x);
+                        tmem_ld_wait();
+                        if (decltype(masked)::value) hide(x, i);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mx[k] = fmaxf(x[k], x[k + 4]);
+                        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(x[k], x[k + 4]);
 #pragma unroll
-                    for (int k = 8; k < 32; k += 8)
+                        for (int k = 8; k < 32; k += 8)
 #pragma unroll
-                        for (int n = 0; n < 4; ++n) mx[n] = fmaxf(fmaxf(mx[n], x[k + n]), x[k + n + 4]);
-                    top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-                }
+                            for (int n = 0; n < 4; ++n)
+                                mx[n] = fmaxf(fmaxf(mx[n], x[k + n]), x[k + n + 4]);
+                        top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                        // BF16: any score will do
+                        if (!F16 && !__any_sync(0xffffffffu, fresh && top == -INFINITY)) break;
+                    }
+                };
+                if (edge) most(Bool<true>{});
+                else most(Bool<false>{});
                 if (fresh) shift = (top == -INFINITY ? 0.f : -top * c) + kLift<F16>;
                 if (F16) {
                     const float over = fmaf(top, c, shift) - kLift<F16>;
@@ -669,8 +697,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, i
             const float2 c2 = make_float2(c, c), b2 = make_float2(shift, shift);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             // 32 keys to weights, written over scores that are no longer needed
-            auto weights = [&](float (&x)[32], int i) {
-                if (edge) hide(x, i);
+            auto weights = [&](const float (&x)[32], int i) {
                 uint32_t p[16];
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
@@ -687,19 +714,29 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, i
             // instruction cache nearest to it (128 keys unrolled: 1354 TFLOP/s at
             // 8192 tokens, 64: 1540, 32: 1590).  P goes to the MMA warp in two
             // parts (in one: 1504).
+            auto block = [&](auto masked) {
 #pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-                float x[32];
-                tmem_ld32(s_addr + 32 * i, x);
-                tmem_ld_wait();
-                weights(x, i);
-                if (i & 1) {
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.p_full[t][i >> 1]);
+                for (int i = 0; i < 4; ++i) {
+                    if (decltype(masked)::value && unseen(i)) {
+                        const uint32_t zero[16] = {};
+                        tmem_st16u(s_addr + 16 * i, zero);
+                    } else {
+                        float x[32];
+                        tmem_ld32(s_addr + 32 * i, x);
+                        tmem_ld_wait();
+                        if (decltype(masked)::value) hide(x, i);
+                        weights(x, i);
+                    }
+                    if (i & 1) {
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.p_full[t][i >> 1]);
+                    }
                 }
-            }
+            };
+            if (edge) block(Bool<true>{});
+            else block(Bool<false>{});
             const float2 both = add2(sum[0], sum[1]);
             l += both.x + both.y;
         }
@@ -715,6 +752,19 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, i
             a.lse[row * a.heads + it.head * a.group + r - token * a.group] =
                 l == 0.f ? -INFINITY : (log2f(l) - shift) * kLn2;
         }
+    }
+}
+
+// 32 bytes, a whole sector where the address allows.
+__device__ __forceinline__ void store_32(uint16_t* dst, const uint32_t (&u)[8]) {
+    if (reinterpret_cast<uintptr_t>(dst) & 31) {
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+    } else {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst),
+                     "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]),
+                     "r"(u[7])
+                     : "memory");
     }
 }
 
@@ -783,12 +833,7 @@ __device__ __forceinline__ void write_role(const PrefillArgs& a, Shared& sh) {
                     poison = fmaf(y1, 0.f, poison);
                     u[x] = narrow2<F16>(y0, y1);
                 }
-                if (mine) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        *reinterpret_cast<uint4*>(dst + 16 * i + 8 * x) =
-                            make_uint4(u[4 * x], u[4 * x + 1], u[4 * x + 2], u[4 * x + 3]);
-                }
+                if (mine) store_32(dst + 16 * i, u);
             }
             if (any) {
                 tc_fence_before();
