@@ -22,15 +22,16 @@
 //    that keeps it below 2^15 (11 significant bits; weights down to 2^-33 of the
 //    largest); scores, sums and outputs are FP32.
 // What bounds it then is the issue of instructions and, in short segments, their
-// starts and ends.  64 sequences of 2000 to 8192 tokens, 32 heads over 8: 92.6 us, 4.0
-// TB/s; 128 sequences of 4 rows (16 queries a KV head): 193 us, 2.1 TB/s; one of
-// 131000 tokens and 2 rows: 43 us.
+// starts and ends.  64 sequences of 2000 to 8192 tokens, 32 heads over 8: 91.3 us, 4.0
+// TB/s; 128 sequences of 4 rows (16 queries a KV head): 182 us, 2.3 TB/s; one of
+// 131000 tokens and 2 rows: 41 us.
 //
 // All positions of the batch, in chunks of 128 tokens, are one line that the
 // CTAs cut into equal pieces, whatever the lengths: a piece ends where it ends,
 // and what is left of a (sequence, head) in each is joined by a second kernel
 // (attn_join_kernel), always in the same order.  Per CTA one warp copies chunks
 // into a ring in shared memory and four attend over them.
+#include <algorithm>
 #include <cmath>
 
 #include "attn_common.h"
@@ -79,8 +80,19 @@ struct DecodeArgs {
     float scale;
     int pieces;  // CTAs of the main kernel
     float* part;  // [2 * pieces][query row][128] sums, then [2 * pieces][query row] (shift, l)
+    struct Job* jobs;
     Cache c;
 };
+// What there is to join: the pieces first..last share a (sequence, head, block of
+// query rows), of the first piece in part first_part.  A job for each of these
+// where there are no more than pieces, else for each piece one that starts in it
+// and goes on.
+struct Job {
+    int n, unit, first, last, first_part, unused[3];
+};
+__device__ __forceinline__ bool job_a_unit(const DecodeArgs& a) {
+    return (long long)a.n_seqs * a.c.kv_heads * a.blocks <= a.pieces;
+}
 
 // Chunks that sequence n's queries see: [first, first + count).
 struct Chunks {
@@ -146,7 +158,8 @@ struct Stage {
 constexpr uint32_t kStart = 1u << 24, kEnd = 1u << 25, kNoMore = 1u << 26;
 
 constexpr int kPad = 132;  // a query's 128 sums, so that a warp's stores meet all banks
-constexpr int kBuffers = 2;
+constexpr int kBuffers = 2;  // two warps' each
+static_assert(kWarps == 2 * kBuffers, "");
 template <bool WIDE>
 struct Shared {
     uint64_t full[kStages], empty[kStages];
@@ -158,12 +171,10 @@ struct Shared {
     int limit[kRows<WIDE>];
     // a segment's end
     float2 stat[kWarps][kRows<WIDE>];  // a warp's (shift, l) by query
-    float factor[kWarps][kRows<WIDE>];
-    float2 joint[kRows<WIDE>];
     union {
         // the segment's queries as operands (FP16, scaled by a power of two)
         alignas(16) uint32_t q[8][32][WIDE ? 4 : 2];
-        // and at its end two warps' outputs at a time
+        // and at its end the warps' outputs
         alignas(16) float sums[kBuffers][kRows<WIDE>][kPad];
     };
     int stop;
@@ -213,6 +224,19 @@ __device__ __forceinline__ void group_places(const DecodeArgs& a, int group, int
     pars_at = block + piece * 64 + in * 8;
 }
 
+__device__ __forceinline__ void prefetch_l1(const void* p) {
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(p));
+}
+// What the consumers will want of the segment's queries, 128 bytes a lane.
+template <bool WIDE>
+__device__ __forceinline__ void touch_queries(const DecodeArgs& a, int n, int head, int block) {
+    const int lane = threadIdx.x & 31;
+    const int row = block * kRows<WIDE> + (lane >> 1), i = row / a.group;
+    if ((lane >> 1) < kRows<WIDE> && row < a.rows)
+        prefetch_l1(a.q + (((long long)n * a.krows + i) * a.heads + head * a.group + row -
+                           i * a.group) * D + 64 * (lane & 1));
+}
+
 // The copying warp: walks this CTA's piece of the line.
 template <bool WIDE>
 __device__ __forceinline__ void copy_role(const DecodeArgs& a, Shared<WIDE>& sh, uint8_t* sm) {
@@ -243,6 +267,20 @@ __device__ __forceinline__ void copy_role(const DecodeArgs& a, Shared<WIDE>& sh,
         }
         if (bad_len) atomicOr(&g_decode_status, STATUS_BAD_PAGES);
     }
+    const bool by_unit = job_a_unit(a);
+    if (lane == 0 && !by_unit) a.jobs[blockIdx.x] = {0, 0, 0, -1, 0, {}};
+    // sequences that nothing is seen of
+    for (int i = blockIdx.x; i < a.n_seqs; i += a.pieces) {
+        if (chunks_of(a, good_len(a, __ldg(a.c.lens + i))).count) continue;
+        const long long row = (long long)i * a.krows * a.heads;
+        for (int k = 0; k < a.krows * a.heads; ++k)
+            reinterpret_cast<uint2*>(a.o + (row + k) * D)[lane] = make_uint2(0u, 0u);
+        if (a.lse)
+            for (int k = lane; k < a.krows * a.heads; k += 32) a.lse[row + k] = -INFINITY;
+        if (by_unit)
+            for (int k = lane; k < per_seq; k += 32)
+                a.jobs[i * per_seq + k] = {i, k, 0, -1, 0, {}};
+    }
     int stage = 0;
     uint32_t phase = 0;
     bool go = true;
@@ -264,7 +302,15 @@ __device__ __forceinline__ void copy_role(const DecodeArgs& a, Shared<WIDE>& sh,
             const bool whole = at == u_start && seg_end == u_end;
             const int part = whole ? -1 : 2 * (int)blockIdx.x + (at == from ? 0 : 1);
             const long long seg_start = at;
+            if (lane == 0 && at == u_start && (by_unit || !whole)) {
+                const int first = (int)blockIdx.x;
+                const int last = whole ? -1 : (int)divide(u_end - 1, size);
+                a.jobs[by_unit ? n * per_seq + unit : first] = {
+                    n, unit, first, last, 2 * first + (at == from ? 0 : 1), {}};
+            }
             const int* table = a.c.table + (long long)n * a.c.max_pages;
+            touch_queries<WIDE>(a, n, head, block);
+            if (n + 1 < a.n_seqs && lane == 0) prefetch_l1(table + a.c.max_pages);
             // page numbers, a lane each, some chunks ahead
             int ids = 0, ids_from = -1;
             for (; go && at < seg_end; ++at) {
@@ -447,52 +493,48 @@ __device__ __forceinline__ void load_queries(const DecodeArgs& a, Shared<WIDE>& 
 
 // The segment's end: the warps' sums, whose (shift, l) are in sh.stat, become one
 // and go out.  `put` writes a warp's outputs, brought to the common shift, into a
-// buffer.
+// buffer, or adds them to what is there.
+template <bool WIDE>
+__device__ __forceinline__ float2 joint_stat(const Shared<WIDE>& sh, int c) {
+    // the least shift is that of the largest score
+    float least = INFINITY, sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+        if (sh.stat[w][c].y != 0.f) least = fminf(least, sh.stat[w][c].x);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const float2 x = sh.stat[w][c];
+        if (x.y != 0.f) sum = fmaf(x.y, ex2_approx(least - x.x), sum);
+    }
+    return make_float2(least, sum);
+}
 template <bool F16, bool WIDE, class Put>
 __device__ __forceinline__ void finish_segment(const DecodeArgs& a, Shared<WIDE>& sh,
                                                const Stage& st, Put put) {
     constexpr int Q = kRows<WIDE>, B = kBuffers;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     consumer_sync();
-    if (tid < Q) {
-        // the least shift is that of the largest score
-        float least = INFINITY, sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-            if (sh.stat[w][tid].y != 0.f) least = fminf(least, sh.stat[w][tid].x);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float2 x = sh.stat[w][tid];
-            const float f = x.y != 0.f ? ex2_approx(least - x.x) : 0.f;
-            sh.factor[w][tid] = f;
-            if (x.y != 0.f) sum = fmaf(x.y, f, sum);
-        }
-        sh.joint[tid] = make_float2(least, sum);
-    }
+    if (warp < B) put(sh.sums[warp], Bool<false>{});
+    consumer_sync();
+    if (warp >= B) put(sh.sums[warp - B], Bool<true>{});
     consumer_sync();
     constexpr int kQuads = Q * 32 / (kWarps * 32);
-    float4 all[kQuads] = {};  // four channels of a query
-#pragma unroll 1
-    for (int first = 0; first < kWarps; first += B) {
-        if (warp >= first && warp < first + B) put(sh.sums[warp - first], sh.factor[warp]);
-        consumer_sync();
+    float4 all[kQuads];  // four channels of a query
 #pragma unroll
-        for (int i = 0; i < kQuads; ++i)
-#pragma unroll
-            for (int w = 0; w < B; ++w) {
-                const float4 x =
-                    reinterpret_cast<const float4*>(sh.sums[w][warp + kWarps * i])[lane];
-                all[i].x += x.x;
-                all[i].y += x.y;
-                all[i].z += x.z;
-                all[i].w += x.w;
-            }
-        consumer_sync();
+    for (int i = 0; i < kQuads; ++i) {
+        const float4 x = reinterpret_cast<const float4*>(sh.sums[0][warp + kWarps * i])[lane];
+        const float4 y = reinterpret_cast<const float4*>(sh.sums[1][warp + kWarps * i])[lane];
+        all[i] = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
     }
+    // (now: kept from before, they would spill)
+    float2 stat[kQuads];
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) stat[i] = joint_stat(sh, warp + kWarps * i);
+    consumer_sync();
 #pragma unroll
     for (int i = 0; i < kQuads; ++i) {
         const int c = warp + kWarps * i, row = st.block * Q + c;
-        const float2 joint = sh.joint[c];
+        const float2 joint = stat[i];
         const float4 x = all[i];
         if (st.part >= 0) {
             const long long at = (long long)st.part * Q + c;
@@ -522,6 +564,15 @@ __device__ __forceinline__ float least_of(uint32_t par) {
 struct Query {
     float shift, l, moff[2];
 };
+// What brings a warp's sums of query c to the common shift.
+template <bool WIDE>
+__device__ __forceinline__ float warp_factor(const Shared<WIDE>& sh, int c, const Query& q) {
+    float least = INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+        if (sh.stat[w][c].y != 0.f) least = fminf(least, sh.stat[w][c].x);
+    return q.l != 0.f ? ex2_approx(least - q.shift) : 0.f;
+}
 // The power of two that steps enter with, below 2^8 then.
 struct Unit {
     float v = 1.f;
@@ -557,8 +608,23 @@ __device__ __forceinline__ void attend_narrow(const DecodeArgs& a, Shared<false>
     float unit[2], qsum[2][2], out[8][4];
     Query state[2];
     Unit v_unit;
-    bool settled = false;  // every column has a shift that comes from a score
+    bool settled;  // every column has a shift that comes from a score
     int limit[2];  // positions from it on are not seen
+    // (after a segment's end, not at the next one's start: it leaves the end their
+    // registers)
+    auto reset = [&] {
+        settled = false;
+        state[0] = state[1] = {};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) qb[k] = make_uint2(0u, 0u);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) unit[c] = qsum[c][0] = qsum[c][1] = 0.f, limit[c] = 0;
+#pragma unroll
+        for (int cb = 0; cb < 8; ++cb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[cb][i] = 0.f;
+    };
+    reset();
     for (;;) {
         if (!wait_warp(sh, &sh.full[stage], phase)) return;
         const uint32_t flags = sh.stage[stage].flags;
@@ -566,7 +632,6 @@ __device__ __forceinline__ void attend_narrow(const DecodeArgs& a, Shared<false>
         if (flags & kStart) {
             const Stage st = sh.stage[stage];
             len = st.len;
-            settled = false;
             load_queries<F16>(a, sh, st);
 #pragma unroll
             for (int k = 0; k < 8; ++k) qb[k] = *reinterpret_cast<const uint2*>(sh.q[k][lane]);
@@ -575,13 +640,8 @@ __device__ __forceinline__ void attend_narrow(const DecodeArgs& a, Shared<false>
                 unit[c] = sh.unit[2 * t + c];
                 qsum[c][0] = sh.qsum[2 * t + c].x;
                 qsum[c][1] = sh.qsum[2 * t + c].y;
-                state[c] = {};
                 limit[c] = sh.limit[2 * t + c];
             }
-#pragma unroll
-            for (int cb = 0; cb < 8; ++cb)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) out[cb][i] = 0.f;
         }
         const uint32_t there = flags >> mine & ((1u << I) - 1);
         if (there) {
@@ -749,21 +809,25 @@ __device__ __forceinline__ void attend_narrow(const DecodeArgs& a, Shared<false>
             q.moff[1] = sum_keys(q.moff[1]);
             if (g == 0) sh.stat[warp][2 * t + c] = make_float2(q.shift, q.l);
         }
-        finish_segment<F16>(a, sh, st, [&](float (*sums)[kPad], const float* factor) {
+        finish_segment<F16>(a, sh, st, [&](float (*sums)[kPad], auto add) {
+            constexpr bool kAdd = decltype(add)::value;
             const float back = pow2(-exponent(v_unit.v)), low = kLow * back, high = kHigh * back;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const float f = factor[2 * t + c];
+                const float f = warp_factor(sh, 2 * t + c, state[c]);
                 float* dst = sums[2 * t + c] + g;
                 const float m[2] = {state[c].moff[0] * f, state[c].moff[1] * f};
                 const bool none = state[c].l == 0.f;
 #pragma unroll
                 for (int cb = 0; cb < 8; ++cb) {
-                    dst[16 * cb] = none ? 0.f : fmaf(out[cb][c], low * f, m[cb >> 2]);
-                    dst[16 * cb + 8] = none ? 0.f : fmaf(out[cb][2 + c], high * f, m[cb >> 2]);
+                    const float x = none ? 0.f : fmaf(out[cb][c], low * f, m[cb >> 2]);
+                    const float z = none ? 0.f : fmaf(out[cb][2 + c], high * f, m[cb >> 2]);
+                    dst[16 * cb] = kAdd ? dst[16 * cb] + x : x;
+                    dst[16 * cb + 8] = kAdd ? dst[16 * cb + 8] + z : z;
                 }
             }
         });
+        reset();
     }
 }
 
@@ -783,7 +847,16 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
     float out[16][4];  // channels 8 n + 2 t + e
     Query state[2];
     Unit v_unit;
-    bool settled = false;
+    bool settled;
+    auto reset = [&] {
+        settled = false;
+        state[0] = state[1] = {};
+#pragma unroll
+        for (int n = 0; n < 16; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[n][i] = 0.f;
+    };
+    reset();
     // over the four lanes that hold the other keys of the same queries
     auto max4 = [](float x) {
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
@@ -800,13 +873,7 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
         if (flags & kStart) {
             const Stage st = sh.stage[stage];
             len = st.len;
-            settled = false;
             load_queries<F16>(a, sh, st);
-            state[0] = state[1] = {};
-#pragma unroll
-            for (int n = 0; n < 16; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) out[n][i] = 0.f;
         }
 #pragma unroll 1
         for (int mine = 2 * warp; mine < 2 * warp + 2; ++mine) {
@@ -980,24 +1047,27 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
             q.moff[1] = sum4(q.moff[1]);
             if (t == 0) sh.stat[warp][g + 8 * i] = make_float2(q.shift, q.l);
         }
-        finish_segment<F16>(a, sh, st, [&](float (*sums)[kPad], const float* factor) {
+        finish_segment<F16>(a, sh, st, [&](float (*sums)[kPad], auto add) {
+            constexpr bool kAdd = decltype(add)::value;
             const float back = pow2(-exponent(v_unit.v)), low = kLow * back, high = kHigh * back;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const float f = factor[g + 8 * i];
+                const float f = warp_factor(sh, g + 8 * i, state[i]);
                 float* dst = sums[g + 8 * i] + 2 * t;
                 const float m[2] = {state[i].moff[0] * f, state[i].moff[1] * f};
                 const bool none = state[i].l == 0.f;
 #pragma unroll
                 for (int n = 0; n < 16; ++n) {
                     const float unit = (n & 1 ? high : low) * f;
-                    const float x = fmaf(out[n][2 * i], unit, m[n >> 3]);
-                    const float z = fmaf(out[n][2 * i + 1], unit, m[n >> 3]);
-                    *reinterpret_cast<float2*>(dst + 8 * n) =
-                        none ? make_float2(0.f, 0.f) : make_float2(x, z);
+                    float2 x = make_float2(fmaf(out[n][2 * i], unit, m[n >> 3]),
+                                           fmaf(out[n][2 * i + 1], unit, m[n >> 3]));
+                    if (none) x = make_float2(0.f, 0.f);
+                    float2* at = reinterpret_cast<float2*>(dst + 8 * n);
+                    *at = kAdd ? add2(*at, x) : x;
                 }
             }
         });
+        reset();
     }
 }
 
@@ -1021,10 +1091,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) attn_decode_kernel(DecodeArgs
     else attend_narrow<F16>(a, sh, sm);
 }
 
-// Joins what several CTAs have of one (sequence, head, block), and writes rows
-// that no CTA has anything of.  CTA (x, y) has unit x and of its queries every
-// gridDim.y-th, `per` of them; each has 16 / per warps, which share the pieces,
-// four channels a lane.
+// Joins what several CTAs have of one (sequence, head, block).  CTA (x, y) has
+// job x and of its queries every gridDim.y-th, `per` of them; each has 16 / per
+// warps, which share the pieces, four channels a lane.  What there is to do the
+// main kernel has written down (found here from all lengths, a CTA for every
+// (sequence, head, block), 64 sequences of 2000 to 8192 tokens took 92.9 us where
+// this takes 89.8, one of 777 12.5, and this 11.6).
 constexpr int kJoinWarps = 16;
 template <bool F16, bool WIDE>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(DecodeArgs a) {
@@ -1032,28 +1104,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(DecodeArgs a
     __shared__ float4 parts[kJoinWarps][32];
     __shared__ float part_sum[kJoinWarps], part_least[kJoinWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per_seq = a.c.kv_heads * a.blocks;
-    const int n = blockIdx.x / per_seq, unit = blockIdx.x - n * per_seq;
-    const int head = unit / a.blocks, block = unit - head * a.blocks;
     pdl_wait();
-    long long before = 0;
-    int count = 0;
-    const long long one = scan_lengths(a, [&](int n0, long long b, int mine) {
-        if (n >= n0 && n < n0 + 32) {
-            before = __shfl_sync(0xffffffffu, b, n - n0);
-            count = __shfl_sync(0xffffffffu, mine, n - n0);
-        }
-        return true;
-    });
-    int b0 = 0, b1 = -1, slot0 = 0;
-    if (count) {
-        const long long size = piece_size(a, one * per_seq);
-        const long long start = before * per_seq + (long long)unit * count;
-        b0 = (int)divide(start, size);
-        b1 = (int)divide(start + count - 1, size);
-        if (b0 == b1) return;  // one CTA had all of it
-        slot0 = 2 * b0 + (size * b0 == start ? 0 : 1);
-    }
+    const int4* job = reinterpret_cast<const int4*>(a.jobs + blockIdx.x);
+    const int4 j = __ldcg(job);
+    const int n = j.x, b0 = j.z, b1 = j.w, slot0 = __ldcg(job + 1).x;
+    if (b1 <= b0) return;
+    // (a main kernel that gave up may have left anything)
+    if (b0 < 0 || b1 >= a.pieces || n < 0 || n >= a.n_seqs || j.y < 0 ||
+        j.y >= a.c.kv_heads * a.blocks || (slot0 >> 1) != b0)
+        return;
+    const int head = j.y / a.blocks, block = j.y - head * a.blocks;
     const float2* stat = reinterpret_cast<const float2*>(a.part + 2LL * a.pieces * Q * D);
     const int per = Q / gridDim.y, shares = kJoinWarps / per;  // powers of two
     const int mine = warp / shares, share = warp - mine * shares;
@@ -1137,7 +1197,8 @@ cudaError_t launch(const DecodeArgs& a, cudaStream_t s) {
     const long long units = (long long)a.n_seqs * a.c.kv_heads * a.blocks;
     int apart = 1;
     while (apart < kRows<WIDE> && 2 * apart * units <= 152) apart *= 2;
-    return launch_pdl(attn_join_kernel<F16, WIDE>, dim3((unsigned)units, apart),
+    const unsigned jobs = (unsigned)std::min<long long>(units, a.pieces);
+    return launch_pdl(attn_join_kernel<F16, WIDE>, dim3(jobs, apart),
                       dim3(kJoinWarps * 32), 0, s, a);
 }
 
@@ -1161,7 +1222,7 @@ extern "C" size_t kda_attn_kv4_workspace_size(int n_seqs, int krows, int heads, 
         heads % kv_heads)
         return 0;
     const size_t q = (size_t)columns(krows * (heads / kv_heads));
-    return KDA_KV4_PIECES * 2 * q * (D + 2) * sizeof(float);
+    return KDA_KV4_PIECES * (2 * q * (D + 2) * sizeof(float) + sizeof(Job));
 }
 
 extern "C" kda_status kda_attn_kv4_decode(const void* q, const uint8_t* cache, int64_t n_pages,
@@ -1203,6 +1264,8 @@ extern "C" kda_status kda_attn_kv4_decode(const void* q, const uint8_t* cache, i
     KDA_REQUIRE(pieces > 0, KDA_ERR_CUDA, "%s: no device", fn);
     DecodeArgs a = {(const uint16_t*)q, (uint16_t*)o, lse, n_seqs, krows, heads, window, group,
                     rows, blocks, scale, pieces, static_cast<float*>(workspace),
+                    reinterpret_cast<Job*>(static_cast<float*>(workspace) +
+                                           (size_t)KDA_KV4_PIECES * 2 * cols * (D + 2)),
                     {const_cast<uint8_t*>(cache), page_table, lens, n_pages, max_pages,
                      __builtin_ctz((unsigned)page), kv_heads}};
     cudaStream_t s = as_stream(stream);

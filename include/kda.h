@@ -57,7 +57,7 @@ extern "C" {
  * for each, 64 bytes of codes and 8 of parameters. */
 #define KDA_KV4_TOKEN_BYTES 144
 /* Pieces into which kda_attn_kv4_decode cuts a batch, at most (its workspace
- * holds two partial results for each). */
+ * holds two partial results for each, and a record). */
 #define KDA_KV4_PIECES 480
 
 typedef enum {
