@@ -22,8 +22,8 @@
 //    that keeps it below 2^15 (11 significant bits; weights down to 2^-33 of the
 //    largest); scores, sums and outputs are FP32.
 // What bounds it then is the issue of instructions and, in short segments, their
-// starts and ends.  64 sequences of 2000 to 8192 tokens, 32 heads over 8: 91.3 us, 4.0
-// TB/s; 128 sequences of 4 rows (16 queries a KV head): 182 us, 2.3 TB/s; one of
+// starts and ends.  64 sequences of 2000 to 8192 tokens, 32 heads over 8: 88.1 us, 4.2
+// TB/s; 128 sequences of 4 rows (16 queries a KV head): 142 us, 2.9 TB/s; one of
 // 131000 tokens and 2 rows: 41 us.
 //
 // All positions of the batch, in chunks of 128 tokens, are one line that the
@@ -70,6 +70,11 @@ constexpr int kStageBytes = kChunk * kTokenBytes;
 // 8 keys.
 template <bool WIDE>
 constexpr int kRows = WIDE ? 16 : 8;
+// What a segment's start and end cost, in chunks: pieces are cut with it (128
+// sequences of 4 rows and 100 to 6000 tokens, many of a chunk or two: with 0, 182
+// us; 1, 161; 2, 148; 3, 142; 4, 144; 6, 150.  64 sequences of 2000 to 8192: 91.8,
+// 89.5, 88.1, 88.1, 89.7, 90.9).
+constexpr int kExtra = 3;
 
 struct DecodeArgs {
     const uint16_t* q;
@@ -84,11 +89,11 @@ struct DecodeArgs {
     Cache c;
 };
 // What there is to join: the pieces first..last share a (sequence, head, block of
-// query rows), of the first piece in part first_part.  A job for each of these
-// where there are no more than pieces, else for each piece one that starts in it
-// and goes on.
+// query rows).  Of a piece b, part 2 b is of the one that it starts within, part
+// 2 b + 1 of one that starts in it and goes on.  A job for each (sequence, head,
+// block) where there are no more than pieces, else for what goes on from a piece.
 struct Job {
-    int n, unit, first, last, first_part, unused[3];
+    int n, unit, first, last;
 };
 __device__ __forceinline__ bool job_a_unit(const DecodeArgs& a) {
     return (long long)a.n_seqs * a.c.kv_heads * a.blocks <= a.pieces;
@@ -110,13 +115,18 @@ __device__ __forceinline__ long long divide(long long x, long long y) {
     if (((x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
     return x / y;
 }
-// The line of `total` chunks is cut into pieces of `size`, the last one shorter;
+// What a (head, block) of a sequence is on the line: its chunks, behind kExtra
+// places that stand for the cost of a segment's start and end.
+__device__ __forceinline__ int places(const DecodeArgs& a, const Chunks& ch) {
+    return ch.count ? ch.count + kExtra : 0;
+}
+// The line of `total` places is cut into pieces of `size`, the last one shorter;
 // piece b is CTA b's.
 __device__ __forceinline__ long long piece_size(const DecodeArgs& a, long long total) {
     return divide(total + a.pieces - 1, a.pieces);
 }
 
-// All lengths by one warp: the chunks of all sequences of one (head, block),
+// All lengths by one warp: the places of all sequences of one (head, block),
 // and, through `each`, those before sequences n..n + 31 (lane by lane).
 template <class Each>
 __device__ __forceinline__ long long scan_lengths(const DecodeArgs& a, Each each) {
@@ -132,7 +142,7 @@ __device__ __forceinline__ long long scan_lengths(const DecodeArgs& a, Each each
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (n0 + 32 * i >= a.n_seqs) break;
-            const int mine = chunks_of(a, good_len(a, len[i])).count;
+            const int mine = places(a, chunks_of(a, good_len(a, len[i])));
             int sum = mine;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
@@ -268,7 +278,7 @@ __device__ __forceinline__ void copy_role(const DecodeArgs& a, Shared<WIDE>& sh,
         if (bad_len) atomicOr(&g_decode_status, STATUS_BAD_PAGES);
     }
     const bool by_unit = job_a_unit(a);
-    if (lane == 0 && !by_unit) a.jobs[blockIdx.x] = {0, 0, 0, -1, 0, {}};
+    if (lane == 0 && !by_unit) a.jobs[blockIdx.x] = {0, 0, 0, -1};
     // sequences that nothing is seen of
     for (int i = blockIdx.x; i < a.n_seqs; i += a.pieces) {
         if (chunks_of(a, good_len(a, __ldg(a.c.lens + i))).count) continue;
@@ -279,7 +289,7 @@ __device__ __forceinline__ void copy_role(const DecodeArgs& a, Shared<WIDE>& sh,
             for (int k = lane; k < a.krows * a.heads; k += 32) a.lse[row + k] = -INFINITY;
         if (by_unit)
             for (int k = lane; k < per_seq; k += 32)
-                a.jobs[i * per_seq + k] = {i, k, 0, -1, 0, {}};
+                a.jobs[i * per_seq + k] = {i, k, 0, -1};
     }
     int stage = 0;
     uint32_t phase = 0;
@@ -292,21 +302,23 @@ __device__ __forceinline__ void copy_role(const DecodeArgs& a, Shared<WIDE>& sh,
     while (go && at < to) {
         const int len = good_len(a, __ldg(a.c.lens + n));
         const Chunks ch = chunks_of(a, len);
+        const int length = places(a, ch);
         // (n, head, block) units of this sequence, chunk by chunk
-        while (go && at < to && at < n_start + (long long)ch.count * per_seq) {
-            const int unit = (int)divide(at - n_start, ch.count);
+        while (go && at < to && at < n_start + (long long)length * per_seq) {
+            const int unit = (int)divide(at - n_start, length);
             const int head = unit / a.blocks, block = unit - head * a.blocks;
-            const long long u_start = n_start + (long long)unit * ch.count;
+            const long long u_start = n_start + (long long)unit * length + kExtra;
             const long long u_end = u_start + ch.count;
             const long long seg_end = min(u_end, to);
-            const bool whole = at == u_start && seg_end == u_end;
-            const int part = whole ? -1 : 2 * (int)blockIdx.x + (at == from ? 0 : 1);
+            at = max(at, u_start);
+            if (at >= to) break;
+            const bool starts = at == u_start, whole = starts && seg_end == u_end;
+            const int part = whole ? -1 : 2 * (int)blockIdx.x + (starts ? 1 : 0);
             const long long seg_start = at;
-            if (lane == 0 && at == u_start && (by_unit || !whole)) {
+            if (lane == 0 && starts && (by_unit || !whole)) {
                 const int first = (int)blockIdx.x;
                 const int last = whole ? -1 : (int)divide(u_end - 1, size);
-                a.jobs[by_unit ? n * per_seq + unit : first] = {
-                    n, unit, first, last, 2 * first + (at == from ? 0 : 1), {}};
+                a.jobs[by_unit ? n * per_seq + unit : first] = {n, unit, first, last};
             }
             const int* table = a.c.table + (long long)n * a.c.max_pages;
             touch_queries<WIDE>(a, n, head, block);
@@ -367,7 +379,7 @@ __device__ __forceinline__ void copy_role(const DecodeArgs& a, Shared<WIDE>& sh,
                 if (++stage == kStages) stage = 0, phase ^= 1;
             }
         }
-        n_start += (long long)ch.count * per_seq;
+        n_start += (long long)length * per_seq;
         ++n;
     }
     if (go) go = wait_warp(sh, &sh.empty[stage], phase ^ 1);
@@ -1105,13 +1117,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(DecodeArgs a
     __shared__ float part_sum[kJoinWarps], part_least[kJoinWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
-    const int4* job = reinterpret_cast<const int4*>(a.jobs + blockIdx.x);
-    const int4 j = __ldcg(job);
-    const int n = j.x, b0 = j.z, b1 = j.w, slot0 = __ldcg(job + 1).x;
+    const int4 j = __ldcg(reinterpret_cast<const int4*>(a.jobs + blockIdx.x));
+    const int n = j.x, b0 = j.z, b1 = j.w;
     if (b1 <= b0) return;
     // (a main kernel that gave up may have left anything)
     if (b0 < 0 || b1 >= a.pieces || n < 0 || n >= a.n_seqs || j.y < 0 ||
-        j.y >= a.c.kv_heads * a.blocks || (slot0 >> 1) != b0)
+        j.y >= a.c.kv_heads * a.blocks)
         return;
     const int head = j.y / a.blocks, block = j.y - head * a.blocks;
     const float2* stat = reinterpret_cast<const float2*>(a.part + 2LL * a.pieces * Q * D);
@@ -1124,7 +1135,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(DecodeArgs a
     for (int from = b0 + share; from <= b1; from += 32 * shares) {
         const int b = from + lane * shares;
         float2 s = make_float2(0.f, 0.f);
-        if (b <= b1) s = __ldcg(stat + (b == b0 ? slot0 : 2 * b) * Q + c);
+        if (b <= b1) s = __ldcg(stat + (2 * b + (b == b0)) * Q + c);
         float low = s.y != 0.f ? s.x : INFINITY;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1)
@@ -1139,7 +1150,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(DecodeArgs a
         const int here = min(32, (b1 - from) / shares + 1);
 #pragma unroll 8
         for (int i = 0; i < here; ++i) {
-            const int bi = from + i * shares, slot = bi == b0 ? slot0 : 2 * bi;
+            const int bi = from + i * shares, slot = 2 * bi + (bi == b0);
             const float4 x = __ldcg(
                 reinterpret_cast<const float4*>(a.part + ((long long)slot * Q + c) * D) + lane);
             const float fi = __shfl_sync(0xffffffffu, f, i);
