@@ -22,7 +22,7 @@
 //    that keeps it below 2^15 (11 significant bits; weights down to 2^-33 of the
 //    largest); scores, sums and outputs are FP32.
 // What bounds it then is the issue of instructions and, in short segments, their
-// starts and ends.  64 sequences of 2000 to 8192 tokens, 32 heads over 8: 88.1 us, 4.2
+// starts and ends.  64 sequences of 2000 to 8192 tokens, 32 heads over 8: 84.3 us, 4.4
 // TB/s; 128 sequences of 4 rows (16 queries a KV head): 142 us, 2.9 TB/s; one of
 // 131000 tokens and 2 rows: 41 us.
 //
@@ -200,20 +200,28 @@ struct Bool {
 };
 
 // Waits end: with the phase, with another role's giving up, or after 2^33 clocks.
+__device__ __forceinline__ bool wait_more(uint64_t* bar, uint32_t parity, int* stop) {
+    const long long from = clock64();
+    while (!mbar_wait(bar, parity, 32)) {
+        if (*(volatile int*)stop) return false;
+        if (clock64() - from > 1LL << 33) {
+            atomicOr(&g_decode_status, STATUS_TIMEOUT);
+            *(volatile int*)stop = 1;
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, int* stop) {
+    return wait_more(bar, parity, stop);
+}
+// The long wait is a function of its own, out of the instruction cache's way (64
+// sequences of 2000 to 8192 tokens: 88.1 us with it in the loops, 84.3), but not
+// where that makes registers spill (128 of 4 rows: 142 us, as a function 150).
 template <bool WIDE>
 __device__ __forceinline__ bool wait_warp(Shared<WIDE>& sh, uint64_t* bar, uint32_t parity) {
     bool ok = mbar_wait(bar, parity, 1);
-    if (!ok) {
-        const long long from = clock64();
-        while (!(ok = mbar_wait(bar, parity, 32))) {
-            if (*(volatile int*)&sh.stop) break;
-            if (clock64() - from > 1LL << 33) {
-                atomicOr(&g_decode_status, STATUS_TIMEOUT);
-                *(volatile int*)&sh.stop = 1;
-                break;
-            }
-        }
-    }
+    if (!ok) ok = WIDE ? wait_more(bar, parity, &sh.stop) : wait_long(bar, parity, &sh.stop);
     return __all_sync(0xffffffffu, ok);
 }
 

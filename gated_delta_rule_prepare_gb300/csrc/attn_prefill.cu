@@ -20,10 +20,12 @@
 //    MMAs, four softmax warps for each tile, four warps that write finished
 //    tiles, so the next item's first block overlaps the last one's end.
 //  - Items go out by a ticket counter in the order that attn_plan_kernel writes;
-//    a call whose items fit one per SM needs neither, and one whose items are few
-//    and long shares an item's keys between CTAs.
-// BF16, 32 heads over 8: 1634 TFLOP/s at 8192 tokens, 1713 to 1783 at 32768, 1576
-// at 16 packed prompts of 512 to 8192 (cuBLAS's 8192^3 product: 1940).  What is
+//    a call whose items fit one per SM needs neither.  Where items are few, or a
+//    chunk's do not fill the last round, CTAs share an item's keys.
+//  - The roles' loops are kept short, and what is rare out of them: they meet in
+//    one instruction cache.
+// BF16, 32 heads over 8: 1707 TFLOP/s at 8192 tokens, 1859 at 32768, 1682 at 16
+// packed prompts of 512 to 8192 (cuBLAS's 8192^3 product: 1940).  What is
 // left is an item's start and end, a part of a round when items do not fill the
 // SMs evenly, and the issue of the softmax.
 #include <algorithm>
@@ -58,8 +60,10 @@ struct PrefillArgs {
     unsigned* count;  // entries in the list, then the ticket counter
     Redo* redo;  // [item][tile][warp]
     int slots, bucket_shift;
-    int splits;          // CTAs that share an item's keys; over 1 without a list only
-    float* part;         // their outputs [item][split][256 rows][128], unscaled
+    // Items from `shared` on have their keys cut into `splits` shares, without a list
+    // one CTA each, with one a ticket each.
+    int splits, shared;
+    float* part;         // their outputs [item - shared][share][256 rows][128], unscaled
     float2* part_stat;   // and (shift, sum) of their rows
 };
 
@@ -266,7 +270,7 @@ constexpr float kLift = F16 ? 7.f : 0.f;
 struct Item {
     Entry e;
     int head;      // KV head; negative: no more items
-    int index;     // of all the call's items
+    int index;     // of all the call's items; of a share, -1 less its part's number
     int from, to;  // key blocks of it that this CTA has
 };
 
@@ -289,9 +293,10 @@ static_assert(kSmemBytes <= 232448, "shared memory");
 
 // Waits with an end: a phase that does not come within 2^35 clocks (some 17
 // seconds; rows done again by attend_row may keep others waiting for long), or
-// another role's giving up, ends the kernel with an error status.
-__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity) {
-    if (mbar_wait(bar, parity, 1)) return true;
+// another role's giving up, ends the kernel with an error status.  The long wait
+// is a function of its own: between the roles' loops its code costs room in the
+// instruction cache (8192 tokens, 32 heads over 8: 331 us with it there, 320).
+__device__ __noinline__ bool wait_long(Shared& sh, uint64_t* bar, uint32_t parity) {
     const long long from = clock64();
     while (!mbar_wait(bar, parity, 32)) {
         if (*(volatile int*)&sh.stop) return false;
@@ -302,6 +307,9 @@ __device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity)
         }
     }
     return true;
+}
+__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity) {
+    return mbar_wait(bar, parity, 1) || wait_long(sh, bar, parity);
 }
 // For a whole warp, which leaves together.
 __device__ __forceinline__ bool wait_warp(Shared& sh, uint64_t* bar, uint32_t parity) {
@@ -332,7 +340,30 @@ __device__ __forceinline__ Blocks blocks_of(const Tile& x, const Tile& y) {
     return {min(x.lo, y.lo), max(x.hi, y.hi)};
 }
 
+// Item x of the list's, whole.
+__device__ __forceinline__ void listed_item(const PrefillArgs& a, unsigned x, Item& it) {
+    // any entry of the item's sequence, then the item's
+    const int4 seq = __ldcg(a.group_of + x / (unsigned)a.kv_heads);
+    int i = (int)(x - (unsigned)seq.x * a.kv_heads);
+    const int heads = min(seq.z, a.kv_heads);  // of a full group
+    const int group = i / (seq.y * heads), first = group * heads;
+    i -= group * seq.y * heads;
+    const int here = min(heads, a.kv_heads - first);
+    it.head = first + i % here;
+    const int4 v = __ldcg(a.list + seq.x + i / here);
+    it.e = {v.x, v.y, v.z, v.w};
+    it.index = (int)x;
+}
+__device__ __forceinline__ void take_share(const PrefillArgs& a, Item& it, int share) {
+    const Blocks b = blocks_of(tile_of(a, it, 0), tile_of(a, it, 1));
+    const int each = (b.hi - b.lo + a.splits - 1) / a.splits;
+    it.from = b.lo + share * each;
+    it.to = it.from + each;
+    it.index = -1 - ((it.index - a.shared) * a.splits + share);
+}
+
 // The TMA warp: hands out items and fills the Q tiles and the ring of K and V.
+template <bool CUT>
 __device__ __forceinline__ void load_role(const PrefillArgs& a, Shared& sh, unsigned char* sm,
                                           const CUtensorMap* mq, const CUtensorMap* mk,
                                           const CUtensorMap* mv) {
@@ -351,32 +382,28 @@ __device__ __forceinline__ void load_role(const PrefillArgs& a, Shared& sh, unsi
             unsigned x = 0;
             if (lane == 0) x = atomicAdd(a.count + 1, 1u);
             x = __shfl_sync(0xffffffffu, x, 0);
-            // any entry of the item's sequence, then the item's
-            const unsigned e = x / (unsigned)a.kv_heads;
-            if (e < (unsigned)n_list) {
-                const int4 seq = __ldcg(a.group_of + e);
-                int i = (int)(x - (unsigned)seq.x * a.kv_heads);
-                const int heads = min(seq.z, a.kv_heads);  // of a full group
-                const int group = i / (seq.y * heads), first = group * heads;
-                i -= group * seq.y * heads;
-                const int here = min(heads, a.kv_heads - first);
-                it.head = first + i % here;
-                const int4 v = __ldcg(a.list + seq.x + i / here);
-                it.e = {v.x, v.y, v.z, v.w};
-                it.index = (int)x;
+            // shares of the last items: first of all the first ones, so that keys
+            // in use at a time are few
+            const unsigned n_items = (unsigned)n_list * a.kv_heads;
+            unsigned share = 0;
+            const bool cut = CUT && x >= (unsigned)a.shared;
+            if (cut && n_items > (unsigned)a.shared) {
+                const unsigned n_shared = n_items - a.shared;
+                share = (x - a.shared) / n_shared;
+                x = share < (unsigned)a.splits ? a.shared + (x - a.shared) % n_shared : n_items;
+            }
+            if (x < n_items) {
+                listed_item(a, x, it);
+                if (cut) take_share(a, it, (int)share);
             }
         } else if (round == 0) {
-            it.index = blockIdx.x / a.splits;
-            const int slot = it.index / a.kv_heads, split = blockIdx.x - it.index * a.splits;
+            it.index = CUT ? blockIdx.x / a.splits : blockIdx.x;
+            const int slot = it.index / a.kv_heads;
+            const int split = CUT ? blockIdx.x - it.index * a.splits : 0;
             const int n = warp_find_last(a.n_seqs, slot, [&](int i) { return first_slot(a, i); });
             if (slot_entry(a, n, slot, it.e)) {
                 it.head = it.index - slot * a.kv_heads;
-                if (a.splits > 1) {
-                    const Blocks b = blocks_of(tile_of(a, it, 0), tile_of(a, it, 1));
-                    const int each = (b.hi - b.lo + a.splits - 1) / a.splits;
-                    it.from = b.lo + split * each;
-                    it.to = it.from + each;
-                }
+                if (CUT) take_share(a, it, split);
             }
         }
         if (lane == 0) {
@@ -587,7 +614,7 @@ struct Bool {
     static constexpr bool value = B;
 };
 
-template <bool F16>
+template <bool F16, bool CUT>
 __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, int t) {
     const int r = threadIdx.x & 127, lane = threadIdx.x & 31;
     const uint32_t row_addr = sh.tmem + ((uint32_t)(r & ~31) << 16);
@@ -754,7 +781,8 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, i
         sh.sum[t][r] = l;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.sum_full[t]);
-        if (a.splits > 1) a.part_stat[blockIdx.x * 256LL + t * 128 + r] = make_float2(shift, l);
+        if (CUT && it.index < 0)
+            a.part_stat[(-1 - it.index) * 256LL + t * 128 + r] = make_float2(shift, l);
         else if (a.lse && token < tile.tokens) {
             const long long row = (long long)it.e.row + t * a.tile_tokens + token;
             a.lse[row * a.heads + it.head * a.group + r - token * a.group] =
@@ -777,7 +805,7 @@ __device__ __forceinline__ void store_32(uint16_t* dst, const uint32_t (&u)[8]) 
 }
 
 // Four warps that divide by the sum and write finished tiles.
-template <bool F16>
+template <bool F16, bool CUT>
 __device__ __forceinline__ void write_role(const PrefillArgs& a, Shared& sh) {
     const int r = threadIdx.x & 127, lane = threadIdx.x & 31;
     const uint32_t row_addr = sh.tmem + ((uint32_t)(r & ~31) << 16) + kTmemO;
@@ -811,11 +839,11 @@ __device__ __forceinline__ void write_role(const PrefillArgs& a, Shared& sh) {
             const bool empty = l == 0.f;
             const float inv = empty ? 0.f : 1.f / l;
             float poison = 0.f;  // NaN once any value is not finite
-            float* const part = a.splits > 1
-                                    ? a.part + (blockIdx.x * 256LL + t * 128 + r) * D
+            float* const part =
+                CUT && it.index < 0 ? a.part + ((-1 - it.index) * 256LL + t * 128 + r) * D
                                     : nullptr;
             if (part && !any) {
-                a.part_stat[blockIdx.x * 256LL + t * 128 + r] = make_float2(0.f, 0.f);
+                a.part_stat[(-1 - it.index) * 256LL + t * 128 + r] = make_float2(0.f, 0.f);
                 continue;
             }
 #pragma unroll 1
@@ -861,7 +889,10 @@ __device__ __forceinline__ void write_role(const PrefillArgs& a, Shared& sh) {
     }
 }
 
-template <bool F16>
+// CUT: items may be shared (a kernel of its own: what that adds slows others down).
+// The order of the roles below is that of their code; with the softmax before the
+// TMA warp the same prompts took 2 % longer.
+template <bool F16, bool CUT>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_prefill_kernel(PrefillArgs a, const __grid_constant__ CUtensorMap mq,
                     const __grid_constant__ CUtensorMap mk,
@@ -898,17 +929,17 @@ attn_prefill_kernel(PrefillArgs a, const __grid_constant__ CUtensorMap mq,
     __syncthreads();
     tc_fence_after();
     pdl_wait();
-    if (warp < 8) {
-        softmax_role<F16>(a, sh, warp >> 2);
+    if (warp == 14) {
+        load_role<CUT>(a, sh, sm, &mq, &mk, &mv);
+    } else if (warp < 8) {
+        softmax_role<F16, CUT>(a, sh, warp >> 2);
     } else if (warp < 12) {
-        write_role<F16>(a, sh);
+        write_role<F16, CUT>(a, sh);
     } else {
         if (warp == 12) {
             mma_role<F16, 0>(a, sh, sm);
         } else if (warp == 13) {
             mma_role<F16, 1>(a, sh, sm);
-        } else if (warp == 14) {
-            load_role(a, sh, sm, &mq, &mk, &mv);
         } else if (!a.list && a.cu_q && blockIdx.x == 0) {
             // with a list, attn_plan_kernel looks at the offsets
             const bool ok = warp_offsets_ok(a.cu_q, a.n_seqs, a.t_q) &&
@@ -946,16 +977,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_prefill_join_kernel(Pref
     const long long at = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
     pdl_wait();
     Item it;
-    it.index = (int)(at >> 8);
+    const int index = (int)(at >> 8), t = (int)(at >> 7) & 1, r = (int)at & 127;
     it.from = 0;
     it.to = 0x7fffffff;
-    const int slot = it.index / a.kv_heads, t = (int)(at >> 7) & 1, r = (int)at & 127;
-    const int n = warp_find_last(a.n_seqs, slot, [&](int i) { return first_slot(a, i); });
-    if (!slot_entry(a, n, slot, it.e)) return;
+    if (a.list) {
+        if (a.shared + index >= (int)*a.count * a.kv_heads) return;
+        listed_item(a, a.shared + index, it);
+    } else {
+        const int slot = index / a.kv_heads;
+        const int n = warp_find_last(a.n_seqs, slot, [&](int i) { return first_slot(a, i); });
+        if (!slot_entry(a, n, slot, it.e)) return;
+        it.head = index - slot * a.kv_heads;
+    }
     const Tile tile = tile_of(a, it, t);
     const int token = r / a.group;
     if (token >= tile.tokens) return;
-    const long long first = ((long long)it.index * a.splits << 8) + t * 128 + r;
+    const long long first = ((long long)index * a.splits << 8) + t * 128 + r;
     // up to 152 parts: their factors a lane each, then their channels
     float least = INFINITY, sum = 0.f;
     for (int p = lane; p < a.splits; p += 32) {
@@ -990,7 +1027,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_prefill_join_kernel(Pref
     }
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    const int h = (it.index - slot * a.kv_heads) * a.group + r - token * a.group;
+    const int h = it.head * a.group + r - token * a.group;
     const long long row = (long long)it.e.row + t * a.tile_tokens + token;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
@@ -1015,6 +1052,25 @@ inline long long slot_count(long long rows, int n_seqs, int group) {
 constexpr int kSms = 152;
 inline int most_splits(long long items) { return items * 2 <= kSms ? (int)(kSms / items) : 1; }
 constexpr size_t kPartBytes = 256 * (128 + 2) * sizeof(float);
+// Items of about one length that are more than kSms, but no large multiple of it:
+// those of the last round are cut into shares, so that it ends about everywhere at
+// once.  How many shares, or 1 where that gains little; more cost more to join.
+inline int last_round_splits(long long items, long long& shared) {
+    shared = items / kSms * kSms;
+    const long long rest = items - shared;
+    int best = 1;
+    double least = 1. - 0.02 * (double)(items / kSms);
+    for (int s = 2; s <= 6 && rest; ++s) {
+        const double rounds = (double)((rest * s + kSms - 1) / kSms) / s + 0.01 * s;
+        if (items > kSms && rounds < least) least = rounds, best = s;
+    }
+    return best;
+}
+// Items of the one sequence there is.
+inline long long one_sequence_items(long long rows, int group, int kv_heads) {
+    const int tokens = 2 * (128 / group);
+    return (rows + tokens - 1) / tokens * kv_heads;
+}
 
 }  // namespace
 
@@ -1048,9 +1104,15 @@ extern "C" size_t kda_attn_prefill_workspace_size(int64_t rows, int n_seqs, int 
     // to be done again per item
     const size_t slots = (size_t)slot_count(rows, n_seqs, heads / kv_heads);
     const size_t items = slots * kv_heads;
-    const int splits = most_splits((long long)items);
+    size_t parts = most_splits((long long)items) > 1 ? most_splits((long long)items) * items : 0;
+    if (n_seqs == 1) {
+        const long long exact = one_sequence_items(rows, heads / kv_heads, kv_heads);
+        long long shared;
+        const int splits = last_round_splits(exact, shared);
+        if (splits > 1) parts = std::max(parts, (size_t)(exact - shared) * splits);
+    }
     return 256 + 32 * slots + 16 * (((size_t)n_seqs + 3) / 4) + 8 * sizeof(Redo) * items +
-           (splits > 1 ? splits * items * kPartBytes : 0);
+           parts * kPartBytes;
 }
 
 extern "C" kda_status kda_attn_prefill(const void* q, const void* k, const void* v, void* o,
@@ -1122,6 +1184,16 @@ extern "C" kda_status kda_attn_prefill(const void* q, const void* k, const void*
     const int blocks = (t_k + 127) / 128;
     int splits = direct ? std::min(most_splits(items), blocks / 4) : 1;
     if (splits < 1 || sms < kSms) splits = 1;
+    // A chunk behind a long context: the last round's likewise (32 heads over 8, 2048
+    // tokens behind 30000: 672 us without, 630; 1536: 657, 487; 8192: 2710, 2700).
+    long long shared = 0, joins = splits > 1 ? items : 0;
+    if (!direct && n_seqs == 1 && t_k >= 4LL * t_q) {
+        const long long exact = one_sequence_items(rows_q, group, kv_heads);
+        splits = last_round_splits(exact, shared);
+        const int seen = window ? std::min(t_k, window) : t_k;
+        if (sms < kSms || seen / 128 < 16 * splits) splits = 1;
+        if (splits > 1) joins = exact - shared;
+    }
     int shift = 0;  // buckets of 2^shift key blocks in the plan's sort
     while ((t_k / 128 >> shift) >= kPlanThreads) ++shift;
     unsigned* count = static_cast<unsigned*>(workspace);
@@ -1130,13 +1202,15 @@ extern "C" kda_status kda_attn_prefill(const void* q, const void* k, const void*
     int* first_entry = reinterpret_cast<int*>(group_of + slots);
     Redo* redo = reinterpret_cast<Redo*>(first_entry + 4 * ((n_seqs + 3LL) / 4));
     float* part = reinterpret_cast<float*>(redo + 8 * items);
-    float2* part_stat = reinterpret_cast<float2*>(part + 256LL * D * items * splits);
+    float2* part_stat = reinterpret_cast<float2*>(part + 256LL * D * joins * splits);
     PrefillArgs a = {(const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, (uint16_t*)o,
                      lse, cu_seqlens_q, cu_seqlens_k, q_row_stride, k_row_stride, v_row_stride,
                      o_row_stride, t_q, t_k, n_seqs, heads, kv_heads, window, group, tokens,
                      scale, direct ? nullptr : list, group_of, first_entry, count, redo, (int)slots,
-                     shift, splits, part, part_stat};
-    auto kernel = f16 ? attn_prefill_kernel<true> : attn_prefill_kernel<false>;
+                     shift, splits, (int)shared, part, part_stat};
+    auto kernel = splits > 1 ? attn_prefill_kernel<false, true> : attn_prefill_kernel<false, false>;
+    if (f16)
+        kernel = splits > 1 ? attn_prefill_kernel<true, true> : attn_prefill_kernel<true, false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)kSmemBytes);
     if (e != cudaSuccess) {
@@ -1149,6 +1223,6 @@ extern "C" kda_status kda_attn_prefill(const void* q, const void* k, const void*
                s, a, mq, mk, mv);
     if (splits > 1)
         launch_pdl(f16 ? attn_prefill_join_kernel<true> : attn_prefill_join_kernel<false>,
-                   dim3((unsigned)(items * 256 / kJoinWarps)), dim3(kJoinWarps * 32), 0, s, a);
+                   dim3((unsigned)(joins * 256 / kJoinWarps)), dim3(kJoinWarps * 32), 0, s, a);
     return launch_result(fn);
 }

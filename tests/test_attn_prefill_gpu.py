@@ -293,3 +293,29 @@ def test_shared_items_and_hidden_bad_values():
     assert bool(torch.isnan(o[seen]).all())
     o[seen] = ref[0][seen].to(o.dtype)
     close(o, lse, ref, torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("lq,lk,heads,kv,window", [
+    (2048, 8300, 32, 8, 0), (2500, 10300, 16, 16, 0), (2040, 12500, 20, 4, 9000)])
+def test_chunk_whose_last_items_share_their_keys(lq, lk, heads, kv, window, dtype):
+    """More items than fill whole rounds: the keys of the last ones are cut.  A NaN among the
+    values is seen by the rows from 40 on only."""
+    K = kda()
+    q, k, v = draw(22, [lq], [lk], heads, kv, dtype)
+    v[lk - lq + 40, 0, 5] = float("nan")
+    o, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+    K.kda_attn_prefill(q, k, v, o, lse=lse, window=window)
+    K.kda_sync_status()
+    group = heads // kv
+    assert bool(torch.isfinite(o[:40]).all())
+    assert bool(torch.isnan(o[40:, :group, 5]).all())
+    o[40:, :group, 5] = 0
+    assert bool(torch.isfinite(o).all())
+    plain = torch.nan_to_num(v).double()
+    for i in (0, 1, 39, 40, 63, 64, lq // 2, lq - 70, lq - 1):
+        n = lk - lq + i + 1
+        ref = attend64(q[i:i + 1].double(), k[:n].double(), plain[:n], window)
+        if i >= 40:
+            ref[0][:, :group, 5] = 0
+        close(o[i:i + 1], lse[i:i + 1], ref, dtype)
