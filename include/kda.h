@@ -461,9 +461,8 @@ kda_status kda_attn_prefill(const void* q, const void* k, const void* v, void* o
 
 /* Bytes of workspace kda_attn_prefill needs for `rows` query rows in total.
  * A few hundred bytes per 256 / heads-per-KV-head rows and KV head; with so few of
- * these that CTAs may share their keys, or with one sequence, up to about 60 MB
- * more.  Returns 0 for
- * invalid arguments. */
+ * these that CTAs may share their keys, or with one sequence, up to about 100 MB
+ * more (the shares' sums).  Returns 0 for invalid arguments. */
 size_t kda_attn_prefill_workspace_size(int64_t rows, int n_seqs, int heads, int kv_heads);
 
 /*
