@@ -54,7 +54,8 @@ struct PrefillArgs {
     int t_q, t_k, n_seqs, heads, kv_heads, window;
     int group, tile_tokens;  // heads per KV head; tokens per tile
     float scale;
-    int4* list;       // ordered entries; null: the slots themselves, one item per CTA
+    int4* list;       // ordered entries; null: one sequence's, or one item per CTA
+    bool one;         // sequence: its entries need no list, its items no counter
     int4* group_of;   // of an entry: its sequence's first entry, their number, KV heads at a time
     int* first_entry; // of a sequence
     unsigned* count;  // entries in the list, then the ticket counter
@@ -134,7 +135,10 @@ __device__ __forceinline__ void key_blocks(const PrefillArgs& a, int pos, int to
 // prompts, whose keys and values are 360 MB; a head at a time: 1854, but 358
 // instead of 346 for one of 8192 tokens, whose last head then keeps few CTAs.)
 // One CTA; at those prompts it writes about 1400 entries.
-constexpr long long kL2Bytes = 48 << 20;
+constexpr int kL2Bytes = 48 << 20;
+__device__ __forceinline__ int heads_at_a_time(int lk) {
+    return max(1, kL2Bytes / (4 * D) / max(1, lk));
+}
 constexpr int kPlanThreads = 1024;
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(PrefillArgs a) {
     __shared__ int hist[kPlanThreads];
@@ -202,8 +206,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(PrefillArgs a) 
         a.list[at] = make_int4(e.row, e.tokens, e.k0, e.pos);
         Span whole;
         sequence_span(a, n, whole);
-        const long long head_bytes = max(1LL, (long long)whole.lk) * (4 * D);
-        a.group_of[at] = make_int4(base, entries, (int)max(1LL, kL2Bytes / head_bytes), 0);
+        a.group_of[at] = make_int4(base, entries, heads_at_a_time(whole.lk), 0);
     }
 }
 
@@ -340,18 +343,38 @@ __device__ __forceinline__ Blocks blocks_of(const Tile& x, const Tile& y) {
     return {min(x.lo, y.lo), max(x.hi, y.hi)};
 }
 
-// Item x of the list's, whole.
-__device__ __forceinline__ void listed_item(const PrefillArgs& a, unsigned x, Item& it) {
+// Entries in order.
+__device__ __forceinline__ int one_entries(const PrefillArgs& a) {
+    Span s;
+    if (!sequence_span(a, 0, s)) return 0;
+    return (s.lq + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
+}
+__device__ __forceinline__ int entry_count(const PrefillArgs& a) {
+    return a.list ? (int)__ldcg(a.count) : a.one ? one_entries(a) : 0;
+}
+// Item x in order, whole.
+__device__ __forceinline__ void ordered_item(const PrefillArgs& a, unsigned x, Item& it) {
     // any entry of the item's sequence, then the item's
-    const int4 seq = __ldcg(a.group_of + x / (unsigned)a.kv_heads);
+    int4 seq;
+    if (a.list) {
+        seq = __ldcg(a.group_of + x / (unsigned)a.kv_heads);
+    } else {
+        Span s;
+        sequence_span(a, 0, s);
+        seq = make_int4(0, one_entries(a), heads_at_a_time(s.lk), 0);
+    }
     int i = (int)(x - (unsigned)seq.x * a.kv_heads);
     const int heads = min(seq.z, a.kv_heads);  // of a full group
     const int group = i / (seq.y * heads), first = group * heads;
     i -= group * seq.y * heads;
     const int here = min(heads, a.kv_heads - first);
     it.head = first + i % here;
-    const int4 v = __ldcg(a.list + seq.x + i / here);
-    it.e = {v.x, v.y, v.z, v.w};
+    if (a.list) {
+        const int4 v = __ldcg(a.list + seq.x + i / here);
+        it.e = {v.x, v.y, v.z, v.w};
+    } else {
+        slot_entry(a, 0, first_slot(a, 0) + seq.y - 1 - i / here, it.e);
+    }
     it.index = (int)x;
 }
 __device__ __forceinline__ void take_share(const PrefillArgs& a, Item& it, int share) {
@@ -371,20 +394,24 @@ __device__ __forceinline__ void load_role(const PrefillArgs& a, Shared& sh, unsi
     int stage = 0;
     uint32_t phase = 0, q_phase[2] = {0, 0}, ring_phase = 0;
     int ring = 0;
-    const int n_list = a.list ? (int)*a.count : 0;
+    const unsigned n_items = (unsigned)entry_count(a) * a.kv_heads;
     bool go = true;
     for (int round = 0; go; ++round) {
         Item it;
         it.head = -1;
         it.from = 0;
         it.to = 0x7fffffff;
-        if (a.list) {
-            unsigned x = 0;
-            if (lane == 0) x = atomicAdd(a.count + 1, 1u);
-            x = __shfl_sync(0xffffffffu, x, 0);
+        if (a.list || a.one) {
+            unsigned x;
+            if (a.list) {
+                if (lane == 0) x = atomicAdd(a.count + 1, 1u);
+                x = __shfl_sync(0xffffffffu, x, 0);
+            } else {
+                // there and back, as the items get shorter
+                x = round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            }
             // shares of the last items: first of all the first ones, so that keys
             // in use at a time are few
-            const unsigned n_items = (unsigned)n_list * a.kv_heads;
             unsigned share = 0;
             const bool cut = CUT && x >= (unsigned)a.shared;
             if (cut && n_items > (unsigned)a.shared) {
@@ -393,7 +420,7 @@ __device__ __forceinline__ void load_role(const PrefillArgs& a, Shared& sh, unsi
                 x = share < (unsigned)a.splits ? a.shared + (x - a.shared) % n_shared : n_items;
             }
             if (x < n_items) {
-                listed_item(a, x, it);
+                ordered_item(a, x, it);
                 if (cut) take_share(a, it, (int)share);
             }
         } else if (round == 0) {
@@ -497,8 +524,8 @@ __device__ __forceinline__ void mma_role(const PrefillArgs& a, Shared& sh, unsig
         if (uniform(it.head) < 0) return;
         const Tile x = tile_of(a, it, 0), y = tile_of(a, it, 1);
         const Blocks b = blocks_of(x, y);
-        const int b_hi = uniform(b.hi), lo = uniform(t ? y.lo : x.lo), hi = uniform(t ? y.hi : x.hi);
-        const int b_lo = uniform(b.lo);
+        const int b_lo = uniform(b.lo), b_hi = uniform(b.hi);
+        const int lo = uniform(t ? y.lo : x.lo), hi = uniform(t ? y.hi : x.hi);
         if (b_hi <= b_lo) continue;
         // S of block j; the stage is filled and it is this tile's turn
         auto qk = [&](int j) {
@@ -980,9 +1007,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_prefill_join_kernel(Pref
     const int index = (int)(at >> 8), t = (int)(at >> 7) & 1, r = (int)at & 127;
     it.from = 0;
     it.to = 0x7fffffff;
-    if (a.list) {
-        if (a.shared + index >= (int)*a.count * a.kv_heads) return;
-        listed_item(a, a.shared + index, it);
+    if (a.list || a.one) {
+        if (a.shared + index >= entry_count(a) * a.kv_heads) return;
+        ordered_item(a, a.shared + index, it);
     } else {
         const int slot = index / a.kv_heads;
         const int n = warp_find_last(a.n_seqs, slot, [&](int i) { return first_slot(a, i); });
@@ -1194,6 +1221,11 @@ extern "C" kda_status kda_attn_prefill(const void* q, const void* k, const void*
         if (sms < kSms || seen / 128 < 16 * splits) splits = 1;
         if (splits > 1) joins = exact - shared;
     }
+    // One sequence's items need no plan, and in a few rounds there and back no
+    // counter; in more the counter's evenness is worth more than the plan's time
+    // (4096 tokens, 32 heads over 8: 94.1 us with both, 91.3 without; 8192: 322,
+    // 321; 32768: 4731, 4850).
+    const bool one = !direct && n_seqs == 1 && splits == 1 && items <= 4LL * sms;
     int shift = 0;  // buckets of 2^shift key blocks in the plan's sort
     while ((t_k / 128 >> shift) >= kPlanThreads) ++shift;
     unsigned* count = static_cast<unsigned*>(workspace);
@@ -1206,8 +1238,8 @@ extern "C" kda_status kda_attn_prefill(const void* q, const void* k, const void*
     PrefillArgs a = {(const uint16_t*)q, (const uint16_t*)k, (const uint16_t*)v, (uint16_t*)o,
                      lse, cu_seqlens_q, cu_seqlens_k, q_row_stride, k_row_stride, v_row_stride,
                      o_row_stride, t_q, t_k, n_seqs, heads, kv_heads, window, group, tokens,
-                     scale, direct ? nullptr : list, group_of, first_entry, count, redo, (int)slots,
-                     shift, splits, (int)shared, part, part_stat};
+                     scale, direct || one ? nullptr : list, one, group_of, first_entry, count,
+                     redo, (int)slots, shift, splits, (int)shared, part, part_stat};
     auto kernel = splits > 1 ? attn_prefill_kernel<false, true> : attn_prefill_kernel<false, false>;
     if (f16)
         kernel = splits > 1 ? attn_prefill_kernel<true, true> : attn_prefill_kernel<true, false>;
@@ -1218,7 +1250,7 @@ extern "C" kda_status kda_attn_prefill(const void* q, const void* k, const void*
         return KDA_ERR_CUDA;
     }
     cudaStream_t s = as_stream(stream);
-    if (!direct) launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a);
+    if (!direct && !one) launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a);
     launch_pdl(kernel, dim3((unsigned)(direct ? items * splits : sms)), dim3(kThreads), kSmemBytes,
                s, a, mq, mk, mv);
     if (splits > 1)

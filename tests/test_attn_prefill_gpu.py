@@ -319,3 +319,20 @@ def test_chunk_whose_last_items_share_their_keys(lq, lk, heads, kv, window, dtyp
         if i >= 40:
             ref[0][:, :group, 5] = 0
         close(o[i:i + 1], lse[i:i + 1], ref, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("lq,lk,heads,kv,window", [
+    (2000, 2000, 32, 8, 0), (1100, 1500, 24, 24, 0), (1290, 1290, 32, 32, 300)])
+def test_one_sequence_of_a_few_rounds(lq, lk, heads, kv, window, dtype):
+    """More items than multiprocessors, of one sequence: no list of them is written."""
+    K = kda()
+    q, k, v = draw(23, [lq], [lk], heads, kv, dtype)
+    o, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+    K.kda_attn_prefill(q, k, v, o, lse=lse, window=window)
+    K.kda_sync_status()
+    assert bool(torch.isfinite(o).all()) and not bool((lse == 7.0).any())
+    for i in list(range(0, lq, 97)) + [lq - 1]:
+        n = lk - lq + i + 1
+        ref = attend64(q[i:i + 1].double(), k[:n].double(), v[:n].double(), window)
+        close(o[i:i + 1], lse[i:i + 1], ref, dtype)
