@@ -634,13 +634,8 @@ __device__ __forceinline__ void store_words(uint32_t addr, const uint32_t (&v)[3
 // FP16 weights end at 65504: each block's maximum is compared with the shift
 // before, and the shift moves where a weight would pass 2^(kLift + 8); blocks
 // that are seen whole have their maximum from the load itself (8192 tokens: 386
-// us with 64 comparisons a block, 357; without any maximum 337).  kLift
+// us with 64 comparisons a block, 357; without any maximum 337, at that step).  kLift
 // keeps weights down to 2^-31 of the largest above FP16's smallest number.
-template <bool B>
-struct Bool {
-    static constexpr bool value = B;
-};
-
 template <bool F16, bool CUT>
 __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, int t) {
     const int r = threadIdx.x & 127, lane = threadIdx.x & 31;
@@ -771,34 +766,47 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, i
                 }
                 tmem_st16u(s_addr + 16 * i, p);
             };
-            // Rolled, 32 keys a step: two warps of a scheduler are at different
-            // places of this code, and what a block takes has to stay in the
-            // instruction cache nearest to it (128 keys unrolled: 1354 TFLOP/s at
-            // 8192 tokens, 64: 1540, 32: 1590).  P goes to the MMA warp in two
-            // parts (in one: 1504).
-            auto block = [&](auto masked) {
+            // P goes to the MMA warp in two parts (in one: 1504 TFLOP/s at 8192 tokens
+            // where two gave 1590).
+            auto hand_over = [&](int part) {
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_full[t][part]);
+            };
+            // Rolled: two warps of a scheduler are at different places of this code,
+            // and what a block takes has to stay in the instruction cache nearest to
+            // it (128 keys unrolled: 1354 TFLOP/s at 8192 tokens, 32: 1590; 16: a
+            // tenth less again).  For FP16, whose maxima come before, 64 a step with
+            // both loads in flight (8192 tokens: 340 us, with 32 352; BF16 323, 321).
+            if (!edge) {
+                constexpr int kLoads = F16 ? 2 : 1;
+#pragma unroll 1
+                for (int i = 0; i < 4; i += kLoads) {
+                    float x[kLoads][32];
+#pragma unroll
+                    for (int n = 0; n < kLoads; ++n) tmem_ld32(s_addr + 32 * (i + n), x[n]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int n = 0; n < kLoads; ++n) weights(x[n], i + n);
+                    if (F16 || (i & 1)) hand_over(i >> 1);
+                }
+            } else {
 #pragma unroll 1
                 for (int i = 0; i < 4; ++i) {
-                    if (decltype(masked)::value && unseen(i)) {
+                    if (unseen(i)) {
                         const uint32_t zero[16] = {};
                         tmem_st16u(s_addr + 16 * i, zero);
                     } else {
                         float x[32];
                         tmem_ld32(s_addr + 32 * i, x);
                         tmem_ld_wait();
-                        if (decltype(masked)::value) hide(x, i);
+                        hide(x, i);
                         weights(x, i);
                     }
-                    if (i & 1) {
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.p_full[t][i >> 1]);
-                    }
+                    if (i & 1) hand_over(i >> 1);
                 }
-            };
-            if (edge) block(Bool<true>{});
-            else block(Bool<false>{});
+            }
             const float2 both = add2(sum[0], sum[1]);
             l += both.x + both.y;
         }
