@@ -22,7 +22,7 @@
 //    that keeps it below 2^15 (11 significant bits; weights down to 2^-33 of the
 //    largest); scores, sums and outputs are FP32.
 // What bounds it then is the issue of instructions and, in short segments, their
-// starts and ends.  64 sequences of 2000 to 8192 tokens, 32 heads over 8: 84.3 us, 4.4
+// starts and ends.  64 sequences of 2000 to 8192 tokens, 32 heads over 8: 83.4 us, 4.4
 // TB/s; 128 sequences of 4 rows (16 queries a KV head): 142 us, 2.9 TB/s; one of
 // 131000 tokens and 2 rows: 41 us.
 //
@@ -1112,12 +1112,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) attn_decode_kernel(DecodeArgs
 }
 
 // Joins what several CTAs have of one (sequence, head, block).  CTA (x, y) has
-// job x and of its queries every gridDim.y-th, `per` of them; each has 16 / per
+// job x and of its queries every gridDim.y-th, `per` of them; each has 8 / per
 // warps, which share the pieces, four channels a lane.  What there is to do the
 // main kernel has written down (found here from all lengths, a CTA for every
 // (sequence, head, block), 64 sequences of 2000 to 8192 tokens took 92.9 us where
 // this takes 89.8, one of 777 12.5, and this 11.6).
-constexpr int kJoinWarps = 16;
+constexpr int kJoinWarps = 8;  // (16: 84.5 us where 8 take 83.4, at 64 sequences)
 template <bool F16, bool WIDE>
 __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(DecodeArgs a) {
     constexpr int Q = kRows<WIDE>;
@@ -1214,8 +1214,8 @@ cudaError_t launch(const DecodeArgs& a, cudaStream_t s) {
     launch_pdl(attn_decode_kernel<F16, WIDE>, dim3(a.pieces), dim3(kThreads), smem_bytes<WIDE>(), s, a);
     // few units: their queries to CTAs of their own
     const long long units = (long long)a.n_seqs * a.c.kv_heads * a.blocks;
-    int apart = 1;
-    while (apart < kRows<WIDE> && 2 * apart * units <= 152) apart *= 2;
+    int apart = kRows<WIDE> / kJoinWarps;
+    while (apart < kRows<WIDE> && 2 * apart * units <= 304) apart *= 2;
     const unsigned jobs = (unsigned)std::min<long long>(units, a.pieces);
     return launch_pdl(attn_join_kernel<F16, WIDE>, dim3(jobs, apart),
                       dim3(kJoinWarps * 32), 0, s, a);
