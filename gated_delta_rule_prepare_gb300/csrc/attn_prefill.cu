@@ -742,8 +742,12 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, i
                 }
                 if (fresh) shift = (top == -INFINITY ? 0.f : -top * c) + kLift<F16>;
                 if (F16) {
+                    // Only for rows of the tile that have weights: nothing has waited
+                    // for O in an item's first block (the writers may be reading the
+                    // last item's), and a row that is none of the tile's, which holds
+                    // another sequence's queries, may have any maximum.
                     const float over = fmaf(top, c, shift) - kLift<F16>;
-                    const float by = over > 8.f ? -over : 0.f;
+                    const float by = over > 8.f && pos >= 0 && l > 0.f ? -over : 0.f;
                     if (__any_sync(0xffffffffu, by != 0.f)) move(by);
                 }
             }

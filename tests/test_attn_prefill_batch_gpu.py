@@ -1,0 +1,82 @@
+"""kda_attn_prefill over batches with more items than multiprocessors, against a plain 64-bit form
+of whole sequences: ragged lengths, large scores, masks."""
+
+import itertools
+import math
+
+import pytest
+import torch
+
+from _attn import D, TYPES, close
+from _util import kda
+
+pytestmark = pytest.mark.gpu
+
+# 32 heads over 8, 64 tokens to an item: 12 sequences that make some 500 items, most of them with a
+# last tile that is not full and starts behind position 127.
+RAGGED = [500, 333, 1, 270, 0, 777, 150, 461, 190, 64, 299, 135]
+
+
+def offsets(lens):
+    return torch.tensor([0] + list(itertools.accumulate(lens)), dtype=torch.int32).cuda()
+
+
+def draw(seed, lq, lk, heads, kv, dtype, spread=1.0):
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn((sum(lq), heads, D), generator=g) * spread
+    k = torch.randn((sum(lk), kv, D), generator=g)
+    v = torch.randn((sum(lk), kv, D), generator=g) + 0.5
+    return [x.to(dtype).cuda() for x in (q, k, v)]
+
+
+def whole64(q, k, v, window=0, scale=1 / math.sqrt(D)):
+    """All rows of one sequence at a time: o, lse, sum of weights times |v| (attend64's values)."""
+    R, H = q.shape[:2]
+    L, Hk = k.shape[:2]
+    pos = torch.arange(R, device=q.device)[:, None] + (L - R)
+    key = torch.arange(L, device=q.device)[None]
+    sees = (key <= pos) & ((key > pos - window) if window else (key >= 0))
+    some = sees.any(1)
+    o = torch.zeros((R, H, D), dtype=torch.float64, device=q.device)
+    lse = torch.full((R, H), -math.inf, dtype=torch.float64, device=q.device)
+    mag = torch.zeros_like(o)
+    for h in range(H if bool(some.any()) else 0):
+        hk = h // (H // Hk)
+        s = (q[some, h].double() @ k[:, hk].double().T * scale).masked_fill(~sees[some], -math.inf)
+        lse[some, h] = torch.logsumexp(s, 1)
+        w = torch.exp(s - lse[some, h][:, None])
+        o[some, h] = w @ v[:, hk].double()
+        mag[some, h] = w @ v[:, hk].double().abs()
+    return o, lse, mag
+
+
+def check(q, k, v, o, lse, lq, lk, window=0):
+    a = b = 0
+    for m, n in zip(lq, lk):
+        rows, keys = slice(a, a + m), slice(b, b + n)
+        if m:
+            close(o[rows], lse[rows], whole64(q[rows], k[keys], v[keys], window), q.dtype)
+        a, b = a + m, b + n
+
+
+def call(q, k, v, lq, lk, window=0, ws=None):
+    K = kda()
+    o, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+    K.kda_attn_prefill(q, k, v, o, lse=lse, cu_seqlens=offsets(lq), cu_seqlens_k=offsets(lk),
+                       window=window, workspace=ws)
+    K.kda_sync_status()
+    return o, lse
+
+
+@pytest.mark.parametrize("window", [0, 300])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_large_scores_of_other_sequences_rows(dtype, window):
+    """A last tile that is not full is loaded with the next sequence's queries behind its own,
+    which score far above 10 against this sequence's keys.  They change nothing: rows follow the
+    formula, and repeats give the same bits."""
+    q, k, v = draw(31, RAGGED, RAGGED, 32, 8, dtype, spread=6.0)
+    o, lse = call(q, k, v, RAGGED, RAGGED, window)
+    check(q, k, v, o, lse, RAGGED, RAGGED, window)
+    for _ in range(8):
+        o2, lse2 = call(q, k, v, RAGGED, RAGGED, window)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
