@@ -65,6 +65,17 @@ __device__ __forceinline__ bool warp_offsets_ok(const int* cu, int n_seqs, int t
     return __all_sync(0xffffffffu, ok);
 }
 
+// The part of it that a numbering of the rows rests on: never falls, stays within
+// 0..t.
+__device__ __forceinline__ bool warp_offsets_rise(const int* cu, int n_seqs, int t) {
+    bool ok = true;
+    for (int i = threadIdx.x & 31; i <= n_seqs; i += 32) {
+        const int c = __ldg(cu + i);
+        if (c < 0 || c > t || (i < n_seqs && __ldg(cu + i + 1) < c)) ok = false;
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
 // ---------------------------------------------------------------- 4-bit cache
 // Bytes of one token's K and V, and where the V half of a block of `page`
 // tokens of one KV head starts (K codes, K parameters, V codes, V parameters).

@@ -145,14 +145,25 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(PrefillArgs a) 
     __shared__ int warp_sum[32];
     pdl_wait();
     pdl_release();
+    __shared__ bool overlap;
     const int tid = threadIdx.x, span = 2 * a.tile_tokens;
     hist[tid] = 0;
-    if (tid < 32 && a.cu_q) {
-        const bool ok = warp_offsets_ok(a.cu_q, a.n_seqs, a.t_q) &&
-                        warp_offsets_ok(a.cu_k, a.n_seqs, a.t_k);
-        if (!ok && tid == 0) atomicOr(&g_attn_status, STATUS_BAD_CU_SEQLENS);
+    if (tid < 32) {
+        const bool ok = !a.cu_q || (warp_offsets_ok(a.cu_q, a.n_seqs, a.t_q) &&
+                                    warp_offsets_ok(a.cu_k, a.n_seqs, a.t_k));
+        const bool slots_ok = ok || warp_offsets_rise(a.cu_q, a.n_seqs, a.t_q);
+        if (tid == 0) {
+            overlap = !slots_ok;
+            if (!ok) atomicOr(&g_attn_status, STATUS_BAD_CU_SEQLENS);
+        }
     }
     __syncthreads();
+    // Query offsets that fall or leave the array: sequences may overlap, have more
+    // entries than there are slots, and slots that name others.  Nothing is done.
+    if (overlap) {
+        if (tid < 2) a.count[tid] = 0;
+        return;
+    }
     // bucket 0 holds the longest sequences
     auto sequence = [&](int n, int& bucket) {
         Span s;

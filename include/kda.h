@@ -438,9 +438,11 @@ kda_status kda_prefill_static_ws(float* state, const void* q, const void* k, con
  *   lse : FP32 [rows][heads] (natural logarithm), or NULL
  *   cu_seqlens_q, cu_seqlens_k : DEVICE int32 [n_seqs + 1] row offsets; t_q
  *           and t_k are then the totals.  Both NULL: n_seqs sequences of t_q
- *           query rows and t_k key rows each.  Checked on the device: rows of a
- *           sequence whose offsets lie outside the arrays are not written, and
- *           kda_sync_status reports KDA_ERR_DEVICE.
+ *           query rows and t_k key rows each.  Checked on the device: where the
+ *           offsets are not 0 up to the total, never falling, kda_sync_status
+ *           reports KDA_ERR_DEVICE.  Rows of a sequence whose offsets lie outside
+ *           the arrays are not written then; with query offsets that fall, rows
+ *           of the others may not be either.
  *   heads : a multiple of kv_heads, at most 128 per KV head
  *   in_dtype : KDA_BF16 or KDA_F16
  *   row strides : >= heads*128 (kv_heads*128), multiples of 8 elements; q, k, v

@@ -80,3 +80,37 @@ def test_large_scores_of_other_sequences_rows(dtype, window):
     for _ in range(8):
         o2, lse2 = call(q, k, v, RAGGED, RAGGED, window)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("cu", [[0, 5000, 4000, 10000], [0, 10000] * 4 + [0, 10000],
+                                [0, 7000, 20000, 10000], [0, -50, 6000, 10000]])
+def test_offsets_that_fall_with_many_items(cu):
+    """The plan's list would not hold the items of sequences that overlap: none is taken, the
+    status says so, and nothing outside o is written."""
+    K = kda()
+    T = cu[-1]
+    q, k, v = draw(32, [T], [T], 32, 8, torch.bfloat16)
+    guard = torch.full((T + 600, 32, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T + 600, 32), 7.0, device="cuda")
+    ws = K.kda_attn_prefill_workspace(T, len(cu) - 1, 32, 8)
+    ws.fill_(0x5A)
+    K.kda_attn_prefill(q, k, v, guard[300:300 + T], lse=lse[300:300 + T], workspace=ws,
+                       cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda())
+    with pytest.raises(K.KdaError, match="cu_seqlens"):
+        K.kda_sync_status()
+    assert bool((guard == 7).all()) and bool((lse == 7).all())
+
+
+def test_offsets_short_of_the_total_with_many_items():
+    """Offsets that rise but do not start at 0 and end at the total: reported, and the rows that
+    they name are done."""
+    K = kda()
+    lens = [300, 0, 900]
+    q, k, v = draw(33, [40] + lens + [60], [40] + lens + [60], 32, 8, torch.float16)
+    o, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+    K.kda_attn_prefill(q, k, v, o, lse=lse, cu_seqlens=offsets(lens) + 40)
+    with pytest.raises(K.KdaError, match="cu_seqlens"):
+        K.kda_sync_status()
+    check(*(x[40:1240] for x in (q, k, v, o, lse)), lens, lens)
+    for x in (o, lse):
+        assert bool((x[:40] == 7).all()) and bool((x[1240:] == 7).all())
