@@ -633,6 +633,13 @@ __device__ __forceinline__ void store_words(uint32_t addr, const uint32_t (&v)[3
     tmem_st32u(addr, v);
 }
 
+// 2^x, numbers below 2^-126 included: a sum may be close to 2^128, and what brings
+// it to 1 is one of them (ex2_approx gives 0 there).
+__device__ __forceinline__ float ex2_small(float x) {
+    const float h = ex2_approx(0.5f * x);
+    return h * h;
+}
+
 // Four warps, a thread a row of tile t.  Weights are 2^(c s + shift), c = scale
 // log2 e, and their sum l; the row's shift makes the largest weight of the first
 // block that the row sees 1 (2^kLift for FP16).
@@ -640,8 +647,8 @@ __device__ __forceinline__ void store_words(uint32_t addr, const uint32_t (&v)[3
 // BF16 weights have FP32's range, so a later block may exceed that: the shift
 // moves, and l and O with it, once l has passed 2^24, and no block but the
 // first needs its maximum (a pass over the block, and the wait for it before the
-// first weight).  A row whose scores rise by more than 2^100 within one
-// block comes out infinite and is done again (attend_row).
+// first weight).  A row whose scores rise so far within one block that l or O
+// leaves that range (2^128) comes out infinite and is done again (attend_row).
 // FP16 weights end at 65504: each block's maximum is compared with the shift
 // before, and the shift moves where a weight would pass 2^(kLift + 8); blocks
 // that are seen whole have their maximum from the load itself (8192 tokens: 386
@@ -705,7 +712,7 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, i
             // The shift moves by `by`.  All MMAs before S of this block are done,
             // the last O += P V among them.
             auto move = [&](float by) {
-                const float f = ex2_approx(by);
+                const float f = ex2_small(by);
                 shift += by;
                 l *= f;
 #pragma unroll 1
@@ -1058,8 +1065,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_prefill_join_kernel(Pref
         if (p0 + lane < a.splits) {
             const float2 s = __ldcg(a.part_stat + first + 256LL * (p0 + lane));
             if (s.y != 0.f) {
-                f = ex2_approx(least - s.x);
-                sum = fmaf(s.y, f, sum);
+                f = ex2_small(least - s.x);
+                // (an infinite sum stays one, however small its factor)
+                sum = s.y < INFINITY ? fmaf(s.y, f, sum) : sum + s.y;
             }
         }
         const int here = min(32, a.splits - p0);

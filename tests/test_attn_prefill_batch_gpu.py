@@ -114,3 +114,36 @@ def test_offsets_short_of_the_total_with_many_items():
     check(*(x[40:1240] for x in (q, k, v, o, lse)), lens, lens)
     for x in (o, lse):
         assert bool((x[:40] == 7).all()) and bool((x[1240:] == 7).all())
+
+
+def steep(T, peaks, rows, dtype, heads=2, kv=2):
+    """Scores 0 but for `peaks`, key: score; the last `rows` of T rows are queries."""
+    q = torch.ones((rows, heads, D), dtype=dtype, device="cuda")
+    k = torch.zeros((T, kv, D), dtype=dtype, device="cuda")
+    for at, score in peaks.items():
+        k[at] = score / math.sqrt(D)
+    v = torch.randn((T, kv, D), generator=torch.Generator().manual_seed(34)).clamp(-1.2, 1.2)
+    return q, k, v.to(dtype).cuda()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("score", [60, 70, 86, 87.7, 88.4, 95])
+@pytest.mark.parametrize("T,peaks,rows,window", [
+    (700, [40], 600, 0), (700, [200], 700, 0), (700, [200], 500, 333),  # items whole
+    (3001, [200], 4, 0), (3001, [500], 4, 2800),                        # shares of an item's keys
+    (3001, [500, 512], 4, 0)])                                          # in two shares
+def test_one_key_far_above_the_first(T, peaks, rows, window, score, dtype):
+    """Weights are taken relative to scores seen first: of a key 2^86 to 2^138 above them, and of
+    keys far below it, nothing is lost.  (Values are small enough that their sums stay finite.)"""
+    q, k, v = steep(T, {at: score + 2 * i for i, at in enumerate(peaks)}, rows, dtype)
+    o, lse = call(q, k, v, [rows], [T], window)
+    check(q, k, v, o, lse, [rows], [T], window)
+
+
+@pytest.mark.parametrize("score", [86, 87.7, 88.4])
+def test_one_key_far_above_the_first_in_a_batch(score):
+    lens = [700, 64, 900, 333]
+    parts = [steep(n, {min(200, n // 2): score}, n, torch.bfloat16, 32, 8) for n in lens]
+    q, k, v = (torch.cat(x) for x in zip(*parts))
+    o, lse = call(q, k, v, lens, lens)
+    check(q, k, v, o, lse, lens, lens)
