@@ -81,6 +81,7 @@ struct DecodeArgs {
     uint16_t* o;
     float* lse;
     int n_seqs, krows, heads, window;
+    int reach;  // how many last positions some row may see: 2^31 - 1 without a window
     int group, rows, blocks;  // heads per KV head; query rows of a KV head; blocks of them
     float scale;
     int pieces;  // CTAs of the main kernel
@@ -107,7 +108,7 @@ __device__ __forceinline__ int good_len(const DecodeArgs& a, int len) {
     return len < 0 || (long long)len > ((long long)a.c.max_pages << a.c.page_shift) ? 0 : len;
 }
 __device__ __forceinline__ Chunks chunks_of(const DecodeArgs& a, int len) {
-    const int lo = (a.window ? max(0, len - a.krows - a.window + 1) : 0) / kChunk;
+    const int lo = max(0, len - a.reach) / kChunk;
     return {lo, len > 0 ? (len - 1) / kChunk + 1 - lo : 0};
 }
 // (64-bit divisions are long: most need 32 bits.)
@@ -502,7 +503,7 @@ __device__ __forceinline__ void load_queries(const DecodeArgs& a, Shared<WIDE>& 
         sh.q[kb][at + 1][word] = narrow2<true>(y.x * fj, y.y * fj);
         if (lane == 0) {
             const int row = st.block * kRows<WIDE> + r;
-            sh.limit[r] = row < a.rows ? st.len - a.krows + row / a.group + 1 : 0;
+            sh.limit[r] = row < a.rows ? max(0, st.len - a.krows + row / a.group + 1) : 0;
             sh.unit[r] = a.scale * kLog2e * kLow * pow2(-up);
             sh.qsum[r].x = sum * (1.f / kLow);
         }
@@ -702,7 +703,7 @@ __device__ __forceinline__ void attend_narrow(const DecodeArgs& a, Shared<false>
                     }
             }
             // (a group that is not there, behind one that is, is masked whole)
-            const bool edge = pos + 16 * I > len - a.krows + 1 ||
+            const bool edge = pos > len - a.krows + 1 - 16 * I ||
                               (a.window && pos < len - a.window) || there != (1u << I) - 1;
             if (edge) {
 #pragma unroll
@@ -943,7 +944,7 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
                 }
             }
             const bool edge =
-                pos + 16 > len - a.krows + 1 || (a.window && pos < len - a.window);
+                pos > len - a.krows + 1 - 16 || (a.window && pos < len - a.window);
             if (edge) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -1002,7 +1003,7 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
 #pragma unroll
                         for (int n = 0; n < 16; ++n)
                             out[n][2 * i] *= both, out[n][2 * i + 1] *= both;
-                    all &= !fresh || move || sh.limit[g + 8 * i] <= pos + 16;
+                    all &= !fresh || move || sh.limit[g + 8 * i] - 16 <= pos;
                 }
                 settled = __all_sync(0xffffffffu, all);
             }
@@ -1281,8 +1282,10 @@ extern "C" kda_status kda_attn_kv4_decode(const void* q, const uint8_t* cache, i
     const int ctas = kCtas * sm_count();
     const int pieces = ctas < KDA_KV4_PIECES ? ctas : KDA_KV4_PIECES;
     KDA_REQUIRE(pieces > 0, KDA_ERR_CUDA, "%s: no device", fn);
-    DecodeArgs a = {(const uint16_t*)q, (uint16_t*)o, lse, n_seqs, krows, heads, window, group,
-                    rows, blocks, scale, pieces, static_cast<float*>(workspace),
+    const int reach = (int)(window ? std::min(0x7fffffffLL, (long long)window + krows - 1)
+                                   : 0x7fffffffLL);
+    DecodeArgs a = {(const uint16_t*)q, (uint16_t*)o, lse, n_seqs, krows, heads, window, reach,
+                    group, rows, blocks, scale, pieces, static_cast<float*>(workspace),
                     reinterpret_cast<Job*>(static_cast<float*>(workspace) +
                                            (size_t)KDA_KV4_PIECES * 2 * cols * (D + 2)),
                     {const_cast<uint8_t*>(cache), page_table, lens, n_pages, max_pages,

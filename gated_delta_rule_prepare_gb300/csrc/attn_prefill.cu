@@ -117,11 +117,17 @@ __device__ __forceinline__ bool slot_entry(const PrefillArgs& a, int n, long lon
     return true;
 }
 
+// The first key that a query at position `pos` sees (below 0: it sees none), window
+// 0 for no window; windows up to 2^31 - 1 are taken.
+__device__ __forceinline__ int first_seen(int pos, int window) {
+    return window ? max(0, max(pos, -1) + 1 - window) : 0;
+}
+
 // Key blocks [lo, hi) of 128 that `tokens` tokens from position `pos` see.
 __device__ __forceinline__ void key_blocks(const PrefillArgs& a, int pos, int tokens, int& lo,
                                            int& hi) {
     const int last = pos + tokens - 1;
-    lo = a.window ? max(0, pos - a.window + 1) >> 7 : 0;
+    lo = first_seen(pos, a.window) >> 7;
     hi = tokens > 0 && last >= 0 ? (last >> 7) + 1 : lo;
     if (hi < lo) hi = lo;
 }
@@ -231,7 +237,7 @@ __device__ __noinline__ void attend_row(const PrefillArgs& a, long long row, lon
                                         int h) {
     const int lane = threadIdx.x & 31;
     const int hk = h / a.group;
-    const int first = a.window ? max(0, p - a.window + 1) : 0;
+    const int first = first_seen(p, a.window);
     const uint2 qb = __ldg(reinterpret_cast<const uint2*>(a.q + row * a.q_stride + h * D +
                                                           4 * lane));
     const float c = a.scale * kLog2e;
@@ -679,11 +685,11 @@ __device__ __forceinline__ void softmax_role(const PrefillArgs& a, Shared& sh, i
         // tokens or by none, in the first and last blocks too.
         const int pos_0 = tile.pos + token_0, pos_1 = tile.pos + min(token_1, tile.tokens - 1);
         const int any_hi = pos_1 >= pos_0 ? pos_1 + 1 : 0, all_hi = pos_0 + 1;
-        const int any_lo = a.window ? max(0, pos_0 - a.window + 1) : 0;
-        const int all_lo = a.window ? max(0, pos_1 - a.window + 1) : 0;
+        const int any_lo = first_seen(pos_0, a.window);
+        const int all_lo = first_seen(pos_1, a.window);
         // keys first..pos; a row that is none of the tile's sees none
         const int pos = token < tile.tokens ? tile.pos + token : -1;
-        const int first = a.window ? max(0, pos - a.window + 1) : 0;
+        const int first = first_seen(pos, a.window);
         // blocks [clear_lo, clear_hi) are seen whole by all of the tile's rows
         const int clear_hi = (tile.pos + 1) >> 7;
         const int clear_lo =

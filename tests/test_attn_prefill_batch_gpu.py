@@ -147,3 +147,14 @@ def test_one_key_far_above_the_first_in_a_batch(score):
     q, k, v = (torch.cat(x) for x in zip(*parts))
     o, lse = call(q, k, v, lens, lens)
     check(q, k, v, o, lse, lens, lens)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 3])
+@pytest.mark.parametrize("lq,lk,heads,kv", [
+    ([5, 70, 4], [2, 0, 4], 8, 2), ([700, 400, 900], [3, 399, 130], 16, 8), ([9], [4], 4, 1)])
+def test_the_largest_windows_and_rows_before_the_first_key(lq, lk, heads, kv, window, dtype):
+    """Positions below zero less such a window pass 32 bits."""
+    q, k, v = draw(35, lq, lk, heads, kv, dtype)
+    o, lse = call(q, k, v, lq, lk, window)
+    check(q, k, v, o, lse, lq, lk, window)
