@@ -594,16 +594,17 @@ __device__ __forceinline__ float warp_factor(const Shared<WIDE>& sh, int c, cons
         if (sh.stat[w][c].y != 0.f) least = fminf(least, sh.stat[w][c].x);
     return q.l != 0.f ? ex2_approx(least - q.shift) : 0.f;
 }
-// The power of two that steps enter with, below 2^8 then.
+// The power of two that steps enter with, below 2^8 then.  A segment begins with one
+// so large that the first steps that are not zero bring it down, whichever rows of
+// V have none.
 struct Unit {
-    float v = 1.f;
-    // brings it down (or, `anew`, up as well) for steps that are `most` with it;
-    // returns what that multiplies them by
-    __device__ __forceinline__ float fit(float most, bool anew) {
-        if (!(most > 0.f && most < INFINITY && (anew || most >= 256.f))) return 1.f;
-        const int was = exponent(v), now = max(-126, min(126, was + 6 - exponent(most)));
+    float v = 0x1p120f;
+    // for steps up to `most`; returns what that multiplies them by
+    __device__ __forceinline__ float fit(float most) {
+        const int was = exponent(v), now = max(-126, 6 - exponent(most));
+        if (!(most > 0.f && most < INFINITY) || now + 2 > was) return 1.f;
         v = pow2(now);
-        return pow2(max(-126, min(126, now - was)));
+        return pow2(max(-126, now - was));
     }
 };
 
@@ -635,6 +636,7 @@ __device__ __forceinline__ void attend_narrow(const DecodeArgs& a, Shared<false>
     // registers)
     auto reset = [&] {
         settled = false;
+        v_unit = {};
         state[0] = state[1] = {};
 #pragma unroll
         for (int k = 0; k < 8; ++k) qb[k] = make_uint2(0u, 0u);
@@ -741,12 +743,24 @@ __device__ __forceinline__ void attend_narrow(const DecodeArgs& a, Shared<false>
             if (__any_sync(0xffffffffu,
                            !settled || most >= 256.f || tops[0] > 7.f || tops[1] > 7.f)) {
                 // shifts: from the first scores of a column, and again once a
-                // weight would pass 2^7; the steps' unit likewise
-                const float fv = v_unit.fit(max_keys(most), !settled);
+                // weight would pass 2^7; the steps' unit likewise (with the first one the
+                // steps may have passed FP32's range: they are formed again)
+                most = 0.f;
 #pragma unroll
                 for (int u = 0; u < I; ++u)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) vs[u][i][0] *= fv, vs[u][i][1] *= fv;
+                    for (int i = 0; i < 2; ++i) {
+                        if (vs[u][i][0] != 0.f) most = fmaxf(most, step_of(vpar[u][i].x));
+                        if (vs[u][i][1] != 0.f) most = fmaxf(most, step_of(vpar[u][i].y));
+                    }
+                const float fv = v_unit.fit(max_keys(most));
+#pragma unroll
+                for (int u = 0; u < I; ++u)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (vs[u][i][0] != 0.f) vs[u][i][0] = step_of(vpar[u][i].x) * v_unit.v;
+                        if (vs[u][i][1] != 0.f) vs[u][i][1] = step_of(vpar[u][i].y) * v_unit.v;
+                    }
                 bool all = true;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -871,6 +885,7 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
     bool settled;
     auto reset = [&] {
         settled = false;
+        v_unit = {};
         state[0] = state[1] = {};
 #pragma unroll
         for (int n = 0; n < 16; ++n)
@@ -972,16 +987,15 @@ __device__ __forceinline__ void attend_wide(const DecodeArgs& a, Shared<true>& s
                 most = fmaxf(most, fmaxf(fmaxf(step_of(vpar[j].x), step_of(vpar[j].y)),
                                          fmaxf(step_of(vpar[j].z), step_of(vpar[j].w))));
             }
-            most *= v_unit.v;
             float tops[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 tops[i] = fmaxf(fmaxf(y[0][2 * i], y[0][2 * i + 1]),
                                 fmaxf(y[1][2 * i], y[1][2 * i + 1]));
-            if (__any_sync(0xffffffffu,
-                           !settled || most >= 256.f || tops[0] > 7.f || tops[1] > 7.f)) {
+            if (__any_sync(0xffffffffu, !settled || most * v_unit.v >= 256.f || tops[0] > 7.f ||
+                                            tops[1] > 7.f)) {
                 // (all lanes agree on the unit: the steps of a group are theirs together)
-                const float fv = v_unit.fit(max4(most), !settled);
+                const float fv = v_unit.fit(max4(most));
                 bool all = true;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {

@@ -5,11 +5,17 @@ import numpy as np
 import pytest
 import torch
 
-from _attn import D, Host, attend64, close, random_cache
+from _attn import D, Host, attend64, bf16_bits, close, random_cache
 from _util import kda
 from test_attn_kv4_gpu import dev, pages_for
 
 pytestmark = pytest.mark.gpu
+
+
+def v_parameters(data, page):
+    """uint16 [pages, kv, tokens, 2, (step, minimum)], a view."""
+    v = data[:, :, page * 136:].view(np.uint16)
+    return v.reshape(v.shape[:2] + (page, 2, 2))
 
 
 def decode(q, data, table, lens, window=0):
@@ -44,3 +50,37 @@ def test_the_largest_windows_and_short_sequences(lens, rows, heads, window):
         torch.float16).cuda()
     o, lse = decode(q, data, table, lens, window)
     check(q, o, lse, Host(data), table, lens, 1, range(len(lens)), window)
+
+
+def small_steps(n_seqs, length, page, others, seed):
+    """A cache whose odd sequences have 32 rows of V without a step and then steps of about 1e-6,
+    and whose even ones have steps of about `others`."""
+    rng = np.random.default_rng(seed)
+    lens = [length] * n_seqs
+    table, total = pages_for(rng, lens, page)
+    data = random_cache(rng, total, 1, page)
+    par = v_parameters(data, page)
+    step, least = rng.uniform(0.5, 1.0, (n_seqs, length, 2)), rng.normal(0, 4, (n_seqs, length, 2))
+    pos = np.arange(length)
+    for n in range(n_seqs):
+        unit = np.where(pos < 32, 0.0, 1e-6) if n % 2 else np.full(length, others)
+        bits = np.stack([bf16_bits(step[n] * unit[:, None]),
+                         bf16_bits(least[n] * (1e-6 if n % 2 else others))], -1)
+        par[table[n, pos // page], 0, pos % page] = bits
+    return data, table, lens
+
+
+@pytest.mark.parametrize("heads,rows", [(1, 1), (4, 2), (8, 2), (4, 8)])
+@pytest.mark.parametrize("n_seqs", [2, 701])
+def test_small_steps_behind_rows_without_a_step(n_seqs, heads, rows):
+    """Small values keep their precision, whatever the CTA worked on before."""
+    q = torch.randn((n_seqs, rows, heads, D), generator=torch.Generator().manual_seed(41)).to(
+        torch.bfloat16).cuda()
+    got = []
+    for others in (0.3, 3e4, 3e-9):
+        data, table, lens = small_steps(n_seqs, 150, 16, others, 42)
+        o, lse = decode(q, data, table, lens)
+        check(q, o, lse, Host(data), table, lens, 1, range(1, n_seqs, 1 if n_seqs < 9 else 50))
+        got.append((o[1::2], lse[1::2]))
+    for o, lse in got[1:]:
+        assert torch.equal(o, got[0][0]) and torch.equal(lse, got[0][1])
