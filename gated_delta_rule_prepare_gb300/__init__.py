@@ -491,6 +491,11 @@ def _rows(t, dtype, dev, name):
     return ptr, row
 
 
+def _window(window):
+    """In the C type's range: no position passes its end, and below 0 the call refuses."""
+    return window if 0 <= window <= 0x7fffffff else -1 if window < 0 else 0x7fffffff
+
+
 def _scratch(workspace, need, dev):
     """(tensor, pointer, bytes) of the caller's workspace, or of one allocated
     here (the library itself never allocates)."""
@@ -553,7 +558,7 @@ def kda_attn_prefill(q, k, v, out, lse=None, cu_seqlens=None, cu_seqlens_k=None,
         lambda: LIB.kda_attn_prefill_workspace_size(rows, n_seqs, heads, kv_heads), dev)
     _check(LIB.kda_attn_prefill(q_ptr, k_ptr, v_ptr, o_ptr, lse_ptr, t_q, t_k, cu_q, cu_k, n_seqs,
                                 heads, kv_heads, HEAD_DIM, in_dtype, q_row, k_row, v_row, o_row,
-                                window, scale, ws_ptr, ws_bytes, _raw_stream(dev)))
+                                _window(window), scale, ws_ptr, ws_bytes, _raw_stream(dev)))
 
 
 def kv4_cache(n_pages, kv_heads, page=64, device="cuda"):
@@ -646,7 +651,7 @@ def kda_attn_kv4_decode(q, cache, page_table, lens, out, lse=None, window=0, sca
         workspace, lambda: LIB.kda_attn_kv4_workspace_size(n_seqs, krows, heads, kv_heads), dev)
     _check(LIB.kda_attn_kv4_decode(q_ptr, c_ptr, n_pages, page, table, width, lens_ptr, o_ptr,
                                    lse_ptr, n_seqs, krows, heads, kv_heads, HEAD_DIM, in_dtype,
-                                   window, scale, ws_ptr, ws_bytes, _raw_stream(dev)))
+                                   _window(window), scale, ws_ptr, ws_bytes, _raw_stream(dev)))
 
 
 def kda_sync_status(device=None):

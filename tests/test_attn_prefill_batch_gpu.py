@@ -158,3 +158,26 @@ def test_the_largest_windows_and_rows_before_the_first_key(lq, lk, heads, kv, wi
     q, k, v = draw(35, lq, lk, heads, kv, dtype)
     o, lse = call(q, k, v, lq, lk, window)
     check(q, k, v, o, lse, lq, lk, window)
+
+
+def test_windows_past_the_c_type():
+    """Any window of more positions than there are is none; below zero all are refused."""
+    K = kda()
+    q, k, v = draw(36, [200], [200], 4, 2, torch.bfloat16)
+    o, want = torch.empty_like(q), torch.empty_like(q)
+    K.kda_attn_prefill(q, k, v, want)
+    cache, table = K.kv4_cache(4, 2, 64), torch.arange(4, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([200], dtype=torch.int32).cuda()
+    K.kda_attn_kv4_append(k, v, cache, table, lens)
+    one, one_want = torch.empty_like(q[:1]), torch.empty_like(q[:1])
+    K.kda_attn_kv4_decode(q[-1:].clone(), cache, table, lens, one_want)
+    for window in (2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63 + 1):
+        K.kda_attn_prefill(q, k, v, o, window=window)
+        K.kda_attn_kv4_decode(q[-1:].clone(), cache, table, lens, one, window=window)
+        assert torch.equal(o, want) and torch.equal(one, one_want)
+    for window in (-1, -2 ** 31, -2 ** 32, -2 ** 32 + 5):
+        with pytest.raises(K.KdaError):
+            K.kda_attn_prefill(q, k, v, o, window=window)
+        with pytest.raises(K.KdaError):
+            K.kda_attn_kv4_decode(q[-1:].clone(), cache, table, lens, one, window=window)
+    K.kda_sync_status()
