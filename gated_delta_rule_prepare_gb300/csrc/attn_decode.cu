@@ -1238,11 +1238,8 @@ cudaError_t launch(const DecodeArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t read_and_clear_status_decode(unsigned* out) {
-    const unsigned zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(out, g_decode_status, sizeof(unsigned));
-    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_decode_status, &zero, sizeof(unsigned));
-    return e;
+cudaError_t status_word_decode(unsigned** word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_decode_status);
 }
 
 }  // namespace kda

@@ -461,11 +461,8 @@ kda_status rows_call(const char* fn, bool append, void* k, void* v, int64_t k_st
 
 }  // namespace
 
-cudaError_t read_and_clear_status_kv4(unsigned* out) {
-    const unsigned zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(out, g_kv4_status, sizeof(unsigned));
-    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_kv4_status, &zero, sizeof(unsigned));
-    return e;
+cudaError_t status_word_kv4(unsigned** word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_kv4_status);
 }
 
 kda_status validate_cache(const char* fn, const void* cache, int64_t n_pages, int page,

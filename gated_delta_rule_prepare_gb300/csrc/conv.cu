@@ -542,11 +542,8 @@ kda_status launch(float* conv_state, const uint16_t* x, const uint16_t* w, uint1
 
 }  // namespace
 
-cudaError_t read_and_clear_status_conv(unsigned* out) {
-    unsigned zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(out, g_conv_status, sizeof(unsigned));
-    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_conv_status, &zero, sizeof(unsigned));
-    return e;
+cudaError_t status_word_conv(unsigned** word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_conv_status);
 }
 
 }  // namespace kda

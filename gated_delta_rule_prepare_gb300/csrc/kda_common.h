@@ -44,14 +44,14 @@ enum : unsigned {
     STATUS_BAD_PAGES = 1u << 3,  // lens or page_table does not fit the 4-bit cache
 };
 
-// Each checking unit exposes a reader that returns and clears its word on the
-// current device (synchronous; called from kda_sync_status only).
-cudaError_t read_and_clear_status_prefill(unsigned* out);
-cudaError_t read_and_clear_status_conv(unsigned* out);
-cudaError_t read_and_clear_status_prefill_tc(unsigned* out);
-cudaError_t read_and_clear_status_attn(unsigned* out);
-cudaError_t read_and_clear_status_kv4(unsigned* out);
-cudaError_t read_and_clear_status_decode(unsigned* out);
+// Where each checking unit's word is on the current device (kda_sync_status
+// reads and clears them).
+cudaError_t status_word_prefill(unsigned** word);
+cudaError_t status_word_conv(unsigned** word);
+cudaError_t status_word_prefill_tc(unsigned** word);
+cudaError_t status_word_attn(unsigned** word);
+cudaError_t status_word_kv4(unsigned** word);
+cudaError_t status_word_decode(unsigned** word);
 
 // kda_prefill's argument checks, shared with kda_prefill_static_ws (prefill.cu).
 kda_status validate_prefill(const char* fn, const float* state, const void* q, const void* k,

@@ -263,11 +263,8 @@ kda_status launch(float* state, const void* q, const void* k, const void* v, con
 
 }  // namespace
 
-cudaError_t read_and_clear_status_prefill(unsigned* out) {
-    unsigned zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(out, g_prefill_status, sizeof(unsigned));
-    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_prefill_status, &zero, sizeof(unsigned));
-    return e;
+cudaError_t status_word_prefill(unsigned** word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_prefill_status);
 }
 
 }  // namespace kda

@@ -2034,11 +2034,8 @@ kda_status launch_prefill_tc(float* state, const void* q, const void* k, const v
     return launch_result("kda_prefill (scan)");
 }
 
-cudaError_t read_and_clear_status_prefill_tc(unsigned* out) {
-    unsigned zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(out, g_tc_status, sizeof(unsigned));
-    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_tc_status, &zero, sizeof(unsigned));
-    return e;
+cudaError_t status_word_prefill_tc(unsigned** word) {
+    return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_tc_status);
 }
 
 }  // namespace kda
