@@ -598,9 +598,9 @@ def _kv4_rows(name, fn, k, v, cache, page_table, lens, cu_seqlens):
         cu, t = _packed(cu_seqlens, torch.int32, dev, "cu_seqlens"), shape[0]
     else:
         rows = shape[0] * (shape[1] if len(shape) == 4 else 1)
-        if rows % n_seqs or (len(shape) == 4 and shape[0] != n_seqs):
+        t = rows // n_seqs if n_seqs else 0   # (without sequences the call refuses)
+        if rows != t * n_seqs or (len(shape) == 4 and shape[0] != n_seqs):
             raise ValueError("%s: the rows do not divide over the sequences" % name)
-        t = rows // n_seqs
     _check(fn(k_ptr, v_ptr, k_row, v_row, t, cu, n_seqs, kv_heads, HEAD_DIM, in_dtype, *cache_args,
               _raw_stream(dev)))
 

@@ -84,3 +84,20 @@ def test_small_steps_behind_rows_without_a_step(n_seqs, heads, rows):
         got.append((o[1::2], lse[1::2]))
     for o, lse in got[1:]:
         assert torch.equal(o, got[0][0]) and torch.equal(lse, got[0][1])
+
+
+@pytest.mark.parametrize("name", ["append", "read", "decode"])
+def test_no_sequences_are_refused(name):
+    K = kda()
+    cache = K.kv4_cache(2, 1, 16)
+    table, lens = (torch.zeros(shape, dtype=torch.int32, device="cuda") for shape in ((0, 2), (0,)))
+    x = torch.zeros((0, 1, D), dtype=torch.float16, device="cuda")
+    with pytest.raises(K.KdaError, match="n_seqs"):
+        if name == "decode":
+            K.kda_attn_kv4_decode(x, cache, table, lens, x.clone())
+        else:
+            getattr(K, "kda_attn_kv4_" + name)(x, x, cache, table, lens)
+    if name != "decode":
+        y = torch.zeros((3, 1, D), dtype=torch.float16, device="cuda")
+        with pytest.raises(ValueError, match="divide"):
+            getattr(K, "kda_attn_kv4_" + name)(y, y, cache, table, lens)
