@@ -116,6 +116,7 @@ __device__ __forceinline__ uint32_t bf16_up(float x) {
 // apart for codes8: t + e is x - m exactly (the rounded difference and what it
 // lost), and the fused multiply-add gets the sign of t - (c + 0.5) s right.
 __device__ __noinline__ uint32_t code_exact(float x, float m, float s) {
+    if (s >= 1e37f) x *= 0.25f, m *= 0.25f, s *= 0.25f;  // exact, and x - m finite
     const float t = x - m;
     const float back = x - t;
     const float e = (x - (t + back)) + (back - m);
@@ -233,8 +234,10 @@ __device__ __forceinline__ void append_group(const RowArgs& a, const Slot& s, ui
         uint32_t mb = bf16_down(x.x);
         my_m = __uint_as_float(mb << 16);
         // both rounded up: at or above the real quotient, and equal to it where it
-        // is a BF16 number
-        const float q = __fdiv_ru(__fsub_ru(-x.y, my_m), 15.f);
+        // is a BF16 number (of quarters where the difference may pass FP32's range)
+        const bool huge = fmaxf(fabsf(my_m), fabsf(x.y)) > 1e38f;
+        const float q = huge ? 4.f * __fdiv_ru(__fsub_ru(-0.25f * x.y, 0.25f * my_m), 15.f)
+                             : __fdiv_ru(__fsub_ru(-x.y, my_m), 15.f);
         uint32_t sb = bf16_up(q);
         // an infinity or a NaN in the group: every value of it reads as NaN
         const bool bad = !(q < 3e38f) || !(fabsf(my_m) < INFINITY);
@@ -242,7 +245,7 @@ __device__ __forceinline__ void append_group(const RowArgs& a, const Slot& s, ui
         my_s = bad ? 0.f : __uint_as_float(sb << 16);
         if (bad) my_m = 0.f;
         const float size = fabsf(my_m);
-        const bool plain = my_s > 1e-30f && size <= 1024.f * my_s &&
+        const bool plain = my_s > 1e-30f && my_s < 1e37f && size <= 1024.f * my_s &&
                            (size == 0.f || my_s <= 1024.f * size);
         my_inv = plain ? 1.f / my_s : 0.f;
         const int tok = 2 * (c & 7) + hw;
