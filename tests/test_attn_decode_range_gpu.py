@@ -101,3 +101,19 @@ def test_no_sequences_are_refused(name):
         y = torch.zeros((3, 1, D), dtype=torch.float16, device="cuda")
         with pytest.raises(ValueError, match="divide"):
             getattr(K, "kda_attn_kv4_" + name)(y, y, cache, table, lens)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("page,lens,rows,heads,kv,window", [
+    (64, [1, 64, 65, 200], 1, 8, 2, 0), (32, [300, 15, 16, 17, 257], 8, 4, 2, 0),
+    (16, [400, 70, 3], 3, 4, 2, 64), (64, [150, 90], 8, 16, 1, 0), (256, [700, 2, 513], 5, 12, 2, 100),
+    (128, [5000, 1], 4, 4, 1, 0), (64, [4097, 63], 1, 4, 2, 0)])
+def test_weights_keep_eleven_bits(page, lens, rows, heads, kv, window, dtype):
+    """Weights times steps are rounded to FP16, not to fewer bits."""
+    rng = np.random.default_rng(45)
+    table, total = pages_for(rng, lens, page)
+    data = random_cache(rng, total, kv, page)
+    q = torch.randn((len(lens), rows, heads, D), generator=torch.Generator().manual_seed(46)).to(
+        dtype).cuda()
+    o, lse = decode(q, data, table, lens, window)
+    check(q, o, lse, Host(data), table, lens, kv, range(len(lens)), window)

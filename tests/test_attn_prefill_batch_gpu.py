@@ -181,3 +181,118 @@ def test_windows_past_the_c_type():
         with pytest.raises(K.KdaError):
             K.kda_attn_kv4_decode(q[-1:].clone(), cache, table, lens, one, window=window)
     K.kda_sync_status()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("lq,lk,heads,kv,window", [
+    (RAGGED, RAGGED, 32, 8, 0),
+    (RAGGED, [n + 7 * i for i, n in enumerate(RAGGED)], 20, 4, 250),     # behind contexts
+    (RAGGED, [max(0, n - 40 * (i % 5)) for i, n in enumerate(RAGGED)], 16, 16, 0),  # empty rows
+    ([n % 61 + 1 for n in range(40)], [n % 61 + 1 for n in range(40)], 8, 8, 0),    # short ones
+    ([1] * 200, [9 * n + 1 for n in range(200)], 6, 2, 0),               # single rows
+    ([1, 3000, 2], [1, 4096, 700], 32, 8, 1000),
+    ([2200], [2300], 24, 24, 0)])                                        # one, no list
+def test_batches_with_more_items_than_multiprocessors(lq, lk, heads, kv, window, dtype):
+    """Items by a list and tickets, over several rounds; the same bits again."""
+    q, k, v = draw(37, lq, lk, heads, kv, dtype)
+    o, lse = call(q, k, v, lq, lk, window)
+    check(q, k, v, o, lse, lq, lk, window)
+    ws = kda().kda_attn_prefill_workspace(sum(lq), len(lq), heads, kv)
+    for fill in (0, 0xFF, 0x5A):
+        ws.fill_(fill)
+        o2, lse2 = call(q, k, v, lq, lk, window, ws)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_batch_in_a_graph_with_other_offsets(dtype):
+    """The plan is made anew at each replay, from the offsets that are there then."""
+    K = kda()
+    T, n = sum(RAGGED), len(RAGGED)
+    cu = offsets(RAGGED)
+    q, k, v = draw(38, [T], [T], 32, 8, dtype)
+    ws = K.kda_attn_prefill_workspace(T, n, 32, 8)
+    o, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    K.kda_attn_prefill(q, k, v, o, lse=lse, cu_seqlens=cu, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        K.kda_attn_prefill(q, k, v, o, lse=lse, cu_seqlens=cu, workspace=ws)
+    for lens in (RAGGED[::-1], [T] + [0] * (n - 1), [T // n] * (n - 1) + [T - T // n * (n - 1)]):
+        cu.copy_(offsets(lens))
+        ws.fill_(0xAB)
+        o.fill_(7.0)
+        lse.fill_(7.0)
+        graph.replay()
+        K.kda_sync_status()
+        check(q, k, v, o, lse, lens, lens)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("lens,heads,kv,window", [
+    ([90, 150, 40], 4, 1, 0),                                  # an item to a multiprocessor
+    (RAGGED, 32, 8, 0), (RAGGED, 32, 8, 100)])                 # many more items
+def test_rows_that_do_not_see_a_bad_value_follow_the_formula(lens, heads, kv, window, what, bad,
+                                                             dtype):
+    """Bad values in several sequences, of one head: rows of other heads, rows before them, rows
+    whose window has left them behind and other sequences' rows follow the formula."""
+    q, k, v = draw(39, lens, lens, heads, kv, dtype)
+    sees = torch.zeros(sum(lens), dtype=torch.bool)
+    at = 0
+    for n in lens:
+        if n > 80:
+            x = k if what == "k" else v
+            x[at + 2 * n // 3, kv - 1, 5] = bad
+            last = min(at + n, at + 2 * n // 3 + window) if window else at + n
+            sees[at + 2 * n // 3:last] = True
+        at += n
+    o, lse = call(q, k, v, lens, lens, window)
+    group = heads // kv
+    hit = torch.zeros(q.shape[:2], dtype=torch.bool)
+    hit[sees, heads - group:] = True
+    hit = hit.cuda()
+    if what == "v":
+        got = o[hit][:, 5]
+        assert bool((torch.isnan(got) if bad != bad else got == bad).all())
+    elif bad != bad:
+        assert bool(torch.isnan(o[hit]).all())
+    k, v = (torch.nan_to_num(x, nan=0.0, posinf=0.0, neginf=0.0) for x in (k, v))
+    a = 0
+    for n in lens:
+        rows = slice(a, a + n)
+        if n:
+            ref = whole64(q[rows], k[rows], v[rows], window)
+            clean = ~hit[rows]
+            close(o[rows][clean], lse[rows][clean], [x[clean] for x in ref], dtype)
+        a += n
+
+
+@pytest.mark.parametrize("window", [0, 90])
+@pytest.mark.parametrize("lens", [[333], RAGGED])
+def test_sharp_softmax_fp16(lens, window):
+    """Scores of +-100 and more: the maximum of a row moves in many blocks, weights underflow."""
+    q, k, v = draw(40, lens, lens, 32, 8, torch.float16, spread=30.0)
+    o, lse = call(q, k, v, lens, lens, window)
+    check(q, k, v, o, lse, lens, lens, window)
+
+
+@pytest.mark.parametrize("lens,heads,kv", [([600], 1, 1), ([600, 333, 900], 16, 16)])
+def test_growing_scores_fp16(lens, heads, kv):
+    """Every key beats all before it: the shift moves in every block."""
+    q = torch.ones((sum(lens), heads, D), dtype=torch.float16, device="cuda")
+    k = torch.cat([torch.arange(n, device="cuda") for n in lens])[:, None, None] / 16.0
+    k = (k * torch.ones((1, kv, D), device="cuda")).half()
+    v = torch.randn((sum(lens), kv, D), generator=torch.Generator().manual_seed(41)).half().cuda()
+    o, lse = call(q, k, v, lens, lens)
+    a = 0
+    for n in lens:
+        rows = slice(a, a + n)
+        ro, rl, mag = whole64(q[rows], k[rows], v[rows])
+        # scores reach 6400 (log2: 9200): FP32 holds them, and their products with scale and
+        # log2 e, to 2^-10 together, which a weight's relative size moves by
+        half = torch.finfo(torch.float16).eps / 2
+        err = (o[rows].double() - ro).abs()
+        assert bool((err <= half * ro.abs() + (half + 2.0 ** -9) * mag).all())
+        assert float((lse[rows].double() - rl).abs().max()) <= 2.0 ** -9
+        a += n
