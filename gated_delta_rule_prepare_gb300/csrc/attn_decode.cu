@@ -21,10 +21,12 @@
 //    stay within a lane.  p_t s_ta is rounded to FP16 after a common power of two
 //    that keeps it below 2^15 (11 significant bits; weights down to 2^-33 of the
 //    largest); scores, sums and outputs are FP32.
-// What bounds it then is the issue of instructions and, in short segments, their
-// starts and ends.  64 sequences of 2000 to 8192 tokens, 32 heads over 8: 83.4 us, 4.4
-// TB/s; 128 sequences of 4 rows (16 queries a KV head): 142 us, 2.9 TB/s; one of
-// 131000 tokens and 2 rows: 41 us.
+// What bounds it then: four warps a scheduler (registers and the rings allow no
+// more), in each of which the pages' arrival, unpacking and fixed latencies follow
+// each other, so that issue is busy 54 to 57 % of the time and no stall stands out;
+// in short segments, their starts and ends.  64 sequences of 2000 to 8192 tokens, 32
+// heads over 8: 83.7 us, 4.4 TB/s; 128 sequences of 4 rows (16 queries a KV head):
+// 143 us, 2.9 TB/s; one of 131000 tokens and 2 rows: 41 us.
 //
 // All positions of the batch, in chunks of 128 tokens, are one line that the
 // CTAs cut into equal pieces, whatever the lengths: a piece ends where it ends,

@@ -25,9 +25,10 @@
 //  - The roles' loops are kept short, and what is rare out of them: they meet in
 //    one instruction cache.
 // BF16, 32 heads over 8: 1707 TFLOP/s at 8192 tokens, 1859 at 32768, 1682 at 16
-// packed prompts of 512 to 8192 (cuBLAS's 8192^3 product: 1940).  What is
-// left is an item's start and end, a part of a round when items do not fill the
-// SMs evenly, and the issue of the softmax.
+// packed prompts of 512 to 8192 (cuBLAS's 8192^3 product: 1940), each a burst of a
+// few calls.  Called for seconds, at the power limit, those prompts run at 1510 to
+// 1540 (cuBLAS 1714).  What is left is an item's start and end, a part of a round
+// when items do not fill the SMs evenly, and the issue of the softmax.
 #include <algorithm>
 #include <cmath>
 
@@ -312,8 +313,8 @@ constexpr uint32_t kSmemBytes = kSharedOff + sizeof(Shared);
 static_assert(kSmemBytes <= 232448, "shared memory");
 
 // Waits with an end: a phase that does not come within 2^35 clocks (some 17
-// seconds; rows done again by attend_row may keep others waiting for long), or
-// another role's giving up, ends the kernel with an error status.  The long wait
+// seconds), or another role's giving up, ends the kernel with an error status.
+// (Rows are done again after all waits.)  The long wait
 // is a function of its own: between the roles' loops its code costs room in the
 // instruction cache (8192 tokens, 32 heads over 8: 331 us with it there, 320).
 __device__ __noinline__ bool wait_long(Shared& sh, uint64_t* bar, uint32_t parity) {
@@ -630,13 +631,6 @@ __device__ __forceinline__ void mma_role(const PrefillArgs& a, Shared& sh, unsig
             pass_turn();
         }
     }
-}
-
-__device__ __forceinline__ void store_words(uint32_t addr, const uint32_t (&v)[16]) {
-    tmem_st16u(addr, v);
-}
-__device__ __forceinline__ void store_words(uint32_t addr, const uint32_t (&v)[32]) {
-    tmem_st32u(addr, v);
 }
 
 // 2^x, numbers below 2^-126 included: a sum may be close to 2^128, and what brings
@@ -1247,6 +1241,10 @@ extern "C" kda_status kda_attn_prefill(const void* q, const void* k, const void*
     if (splits < 1 || sms < kSms) splits = 1;
     // A chunk behind a long context: the last round's likewise (32 heads over 8, 2048
     // tokens behind 30000: 672 us without, 630; 1536: 657, 487; 8192: 2710, 2700).
+    // Against shorter contexts shares' sums weigh more (all keys without, with
+    // shares: 2048 tokens, 8192 keys: 160 us, 182; 12288: 247, 258; 20480: 434, 411;
+    // 2500, 10000: 279, 280; 15000: 446, 356; 4096, 16384: 633, 582; under four times
+    // the tokens: 4096, 12288: 434, 417, 2048 and less the same).
     long long shared = 0, joins = splits > 1 ? items : 0;
     if (!direct && n_seqs == 1 && t_k >= 4LL * t_q) {
         const long long exact = one_sequence_items(rows_q, group, kv_heads);

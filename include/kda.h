@@ -487,9 +487,9 @@ size_t kda_attn_prefill_workspace_size(int64_t rows, int n_seqs, int heads, int 
  * lens (DEVICE int32 [n_seqs]) counts each sequence's positions, the rows of
  * the call included: append and read work on the last rows of each sequence,
  * decode's queries are its last krows positions.  Device-side checks (lens
- * outside 0..max_pages * page or below the rows of the call, a page number
- * outside 0..n_pages - 1): nothing outside the cache is touched, and
- * kda_sync_status reports KDA_ERR_DEVICE.
+ * outside 0..max_pages * page, or for append and read below the rows of the
+ * call, a page number outside 0..n_pages - 1): nothing outside the cache is
+ * touched, and kda_sync_status reports KDA_ERR_DEVICE.
  *
  * kda_attn_kv4_append -- writes rows into the cache.  Per row, head and 64
  * channels: m is the largest BF16 <= min x, s the smallest BF16 >=
@@ -527,8 +527,11 @@ kda_status kda_attn_kv4_read(void* k, void* v, int64_t k_row_stride, int64_t v_r
  * KDA_MAX_K for verification) over the cache: kda_attn_prefill's formula with
  * Lq = krows, Lk = lens[n] and the cache's values as k and v.  Row i of
  * sequence n sees positions up to lens[n] - krows + i; a row that sees none
- * gives o = 0 and lse = -inf.  Positions on a page that is not there are left
- * out.
+ * gives o = 0 and lse = -inf (with lens[n] < krows the first rows do).  Positions
+ * on a page that is not there are left out.  Scores, the softmax and the sums are
+ * FP32; a weight times the step of 64 channels enters the product with their
+ * codes rounded to FP16 (11 bits, after a common power of two), whatever in_dtype
+ * is.  For |q|, scale, |q| * scale and |v| up to 2^96.
  *
  *   q, o : in_dtype (KDA_BF16, KDA_F16) [n_seqs][krows][heads][128]
  *   lse : FP32 [n_seqs][krows][heads], or NULL

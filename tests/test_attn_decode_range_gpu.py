@@ -117,3 +117,31 @@ def test_weights_keep_eleven_bits(page, lens, rows, heads, kv, window, dtype):
         dtype).cuda()
     o, lse = decode(q, data, table, lens, window)
     check(q, o, lse, Host(data), table, lens, kv, range(len(lens)), window)
+
+
+@pytest.mark.parametrize("rows,heads", [(1, 4), (4, 8)])
+@pytest.mark.parametrize("q_exp,v_exp", [(95, 0), (-60, 0), (0, 96), (0, -60), (95, 96)])
+def test_queries_and_values_far_from_one(q_exp, v_exp, rows, heads):
+    """The ends of what the header states."""
+    rng = np.random.default_rng(47)
+    lens = [700, 90]
+    table, total = pages_for(rng, lens, 64)
+    data = random_cache(rng, total, 1, 64)
+    par = v_parameters(data, 64)
+    # exponents up: a BF16 number's are bits 7..14 (values here reach 4)
+    par[:] += np.uint16((v_exp - (2 if v_exp > 0 else 0)) % 512 << 7)
+    q = torch.randn((2, rows, heads, D), generator=torch.Generator().manual_seed(48)).clamp(-2, 2)
+    q = (q * 2.0 ** q_exp).to(torch.bfloat16).cuda()
+    K = kda()
+    o, lse = torch.full_like(q, 7.0), torch.full(q.shape[:3], 7.0, device="cuda")
+    scale = 0.09 * 2.0 ** -q_exp
+    K.kda_attn_kv4_decode(q, dev(data), dev(table), torch.tensor(lens, dtype=torch.int32).cuda(),
+                          o, lse=lse, scale=scale)
+    K.kda_sync_status()
+    host = Host(data)
+    for n, length in enumerate(lens):
+        k, v, size = (torch.from_numpy(host.rows(w, table[n], length, 0, big))[:, None]
+                      for w, big in (("k", False), ("v", False), ("v", True)))
+        assert 0 < float(v.abs().max()) <= 2.0 ** max(v_exp, 2)
+        ref = attend64(q[n].double().cpu(), k, v, scale=scale, moved=size)
+        close(o[n].cpu(), lse[n].cpu(), ref, q.dtype, weights=torch.float16)
