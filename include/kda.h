@@ -530,8 +530,10 @@ kda_status kda_attn_kv4_read(void* k, void* v, int64_t k_row_stride, int64_t v_r
  * gives o = 0 and lse = -inf (with lens[n] < krows the first rows do).  Positions
  * on a page that is not there are left out.  Scores, the softmax and the sums are
  * FP32; a weight times the step of 64 channels enters the product with their
- * codes rounded to FP16 (11 bits, after a common power of two), whatever in_dtype
- * is.  For |q|, scale, |q| * scale and |v| up to 2^96.
+ * codes rounded to FP16, whatever in_dtype is, after a power of two that the rows
+ * and tokens of a sequence share: 11 bits down to 2^-21 of the largest weight
+ * times the largest step, fewer below.  For |q|, scale, |q| * scale and |v| up to
+ * 2^96.
  *
  *   q, o : in_dtype (KDA_BF16, KDA_F16) [n_seqs][krows][heads][128]
  *   lse : FP32 [n_seqs][krows][heads], or NULL
