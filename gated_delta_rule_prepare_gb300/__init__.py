@@ -13,6 +13,9 @@ Entry points (same names as the C ABI): ``kda_decode``, ``kda_decode_k``,
 Full attention: ``kda_attn_prefill`` over packed prompts, and the paged 4-bit cache's
 ``kda_attn_kv4_append``, ``kda_attn_kv4_read`` and ``kda_attn_kv4_decode`` (``kv4_cache``
 allocates one).
+Their rows' positions: ``kda_attn_rope``; the cache's pages: ``kda_attn_kv4_resize``,
+``kda_attn_kv4_fork``, ``kda_attn_kv4_compact`` and ``kda_attn_kv4_copy``.
+Linear attention with a decay for each head: ``kda_lin_prefill``, ``kda_lin_decode``.
 ``kda_prefill_static_ws`` is reached through ``LIB`` (its callers hold raw pointers).
 """
 
@@ -31,6 +34,7 @@ MAX_K = 8
 F32, BF16, F16 = 0, 1, 2
 KV4_TOKEN_BYTES = 144
 KV4_PAGES = (16, 32, 64, 128, 256)
+KV4_MAX_CACHES = 128
 
 _c = ctypes
 _vp, _i, _u64, _i64, _f, _sz = _c.c_void_p, _c.c_int, _c.c_uint64, _c.c_int64, _c.c_float, _c.c_size_t
@@ -70,6 +74,16 @@ def _load():
                                + [_f, _vp, _sz, _u64],
     })
     sig["kda_attn_kv4_read"] = sig["kda_attn_kv4_append"]
+    sig.update({
+        "kda_lin_prefill": [_vp] * 7 + [_i, _i, _vp] + [_i] * 5 + [_i64] * 5 + [_f, _vp, _sz, _u64],
+        "kda_lin_decode": [_vp] * 7 + [_i] * 6 + [_i64] * 5 + [_f, _vp, _i, _u64],
+        "kda_attn_rope": [_vp] * 4 + [_i64] + [_i] * 4 + [_i64] * 4
+                         + [_vp, _i, _vp, _i, _vp, _i, _f, _u64],
+        "kda_attn_kv4_resize": [_vp] * 3 + [_i, _i, _i64, _i, _vp, _sz, _u64],
+        "kda_attn_kv4_fork": [_vp] * 10 + [_i, _i, _i64, _i, _vp, _sz, _u64],
+        "kda_attn_kv4_compact": [_vp] * 7 + [_i, _i, _i64, _vp, _sz, _u64],
+        "kda_attn_kv4_copy": [_vp, _i, _i64, _i, _i, _vp, _vp, _vp, _i, _u64],
+    })
     for name, args in sig.items():
         fn = getattr(lib, name)
         fn.argtypes = args
@@ -80,6 +94,10 @@ def _load():
     lib.kda_attn_prefill_workspace_size.restype = _sz
     lib.kda_attn_kv4_workspace_size.argtypes = [_i] * 4
     lib.kda_attn_kv4_workspace_size.restype = _sz
+    lib.kda_lin_prefill_workspace_size.argtypes = [_i64, _i, _i]
+    lib.kda_lin_prefill_workspace_size.restype = _sz
+    lib.kda_attn_kv4_pages_workspace_size.argtypes = [_i64, _i, _i]
+    lib.kda_attn_kv4_pages_workspace_size.restype = _sz
     lib.kda_last_error.argtypes = []
     lib.kda_last_error.restype = _c.c_char_p
     lib.kda_version.argtypes = []
@@ -652,6 +670,277 @@ def kda_attn_kv4_decode(q, cache, page_table, lens, out, lse=None, window=0, sca
     _check(LIB.kda_attn_kv4_decode(q_ptr, c_ptr, n_pages, page, table, width, lens_ptr, o_ptr,
                                    lse_ptr, n_seqs, krows, heads, kv_heads, HEAD_DIM, in_dtype,
                                    _window(window), scale, ws_ptr, ws_bytes, _raw_stream(dev)))
+
+
+# ---------------------------------------------------------------- rotary positions, pages
+
+def _call(dev, fn, *args):
+    """`fn` on device `dev`'s current stream."""
+    if torch.cuda.current_device() == dev:
+        _check(fn(*args, _raw_stream(dev)))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _raw_stream(dev)))
+
+
+def kda_attn_rope(q, k, positions, inv_freq, q_out=None, k_out=None, pair_axis=None,
+                  interleaved=False, factor=1.0):
+    """Rotary positions: BF16 or FP16 q [rows, heads, 128] and k [rows, kv_heads, 128]
+    (or None), which may be strided views, into q_out and k_out (default: in place).
+    positions: device int32 [rows] or [rows, axes]; inv_freq: device FP32 [pairs];
+    pair_axis: the axis of each pair (a sequence of pairs numbers), needed with
+    several axes.  interleaved: a pair is two neighbours, else channels p and
+    p + pairs; channels behind the pairs stay."""
+    in_dtype, dev = _attn_type(q, "q")
+    dt, shape = q.dtype, q.shape
+    q_out = q if q_out is None else q_out
+    q_ptr, q_row = _rows(q, dt, dev, "q")
+    qo_ptr, qo_row = _rows(q_out, dt, dev, "q_out")
+    k_ptr = ko_ptr = None
+    k_row = ko_row = kv_heads = 0
+    if k is not None:
+        k_out = k if k_out is None else k_out
+        k_ptr, k_row = _rows(k, dt, dev, "k")
+        ko_ptr, ko_row = _rows(k_out, dt, dev, "k_out")
+        kv_heads = k.shape[-2]
+        if k_out.shape != k.shape or k.shape[:-2] != shape[:-2]:
+            raise ValueError("kda_attn_rope: k_out must have k's shape, and k q's rows")
+    elif k_out is not None:
+        raise ValueError("kda_attn_rope: k_out without k")
+    if q_out.shape != shape:
+        raise ValueError("kda_attn_rope: q_out must have q's shape")
+    rows = shape[0] if len(shape) == 3 else shape[0] * shape[1]
+    axes = positions.numel() // rows if rows else 1
+    lead = shape[:-2]
+    if positions.shape != lead and positions.shape != lead + (axes,):
+        raise ValueError("kda_attn_rope: positions must be [rows] or [rows, axes]")
+    if inv_freq.dim() != 1:
+        raise ValueError("kda_attn_rope: inv_freq must be [pairs]")
+    pairs = inv_freq.numel()
+    table = None
+    if pair_axis is not None:
+        if len(pair_axis) != pairs or not all(0 <= x < axes for x in pair_axis):
+            raise ValueError("kda_attn_rope: pair_axis must hold an axis below %d for each pair"
+                             % axes)
+        table = bytes(pair_axis)
+    elif axes > 1:
+        raise ValueError("kda_attn_rope: several axes need pair_axis")
+    _call(dev, LIB.kda_attn_rope, q_ptr, k_ptr, qo_ptr, ko_ptr, rows, shape[-2], kv_heads,
+          HEAD_DIM, in_dtype, q_row, k_row, qo_row, ko_row,
+          _packed(positions, torch.int32, dev, "positions"), axes,
+          _packed(inv_freq, torch.float32, dev, "inv_freq"), pairs, table, int(interleaved),
+          float(factor))
+
+
+def _ints(t, dev, name, shape):
+    if t.shape != shape:
+        raise ValueError("%s must be %s" % (name, list(shape)))
+    return _packed(t, torch.int32, dev, name)
+
+
+def kda_attn_kv4_pages_workspace(n_pages, n_seqs, max_pages, device="cuda"):
+    """Workspace for kda_attn_kv4_resize, kda_attn_kv4_fork and kda_attn_kv4_compact."""
+    need = LIB.kda_attn_kv4_pages_workspace_size(int(n_pages), n_seqs, max_pages)
+    return torch.empty(int(need), dtype=torch.uint8, device=device)
+
+
+def _pages(page_table, refs):
+    """(table pointer, refs pointer, sequences, pages each, pages, device)"""
+    dev = page_table.get_device()
+    if dev < 0:
+        raise TypeError("page_table must be a CUDA tensor")
+    if page_table.dim() != 2 or refs.dim() != 1:
+        raise ValueError("page_table must be [sequences, pages], refs [pages of the cache]")
+    n_seqs, width = page_table.shape
+    return (_packed(page_table, torch.int32, dev, "page_table"),
+            _packed(refs, torch.int32, dev, "refs"), n_seqs, width, refs.numel(), dev)
+
+
+def _pages_scratch(workspace, n_pages, n_seqs, width, dev):
+    return _scratch(workspace, lambda: LIB.kda_attn_kv4_pages_workspace_size(
+        n_pages, n_seqs, width), dev)
+
+
+def kda_attn_kv4_resize(page_table, lens, refs, page=64, workspace=None):
+    """Gives and frees pages in place, so that each sequence has those of its lens
+    positions: page_table device int32 [N, max_pages] (-1: none), lens [N], refs
+    [pages of the cache], how often each page is named (0: free)."""
+    table, refs_ptr, n_seqs, width, n_pages, dev = _pages(page_table, refs)
+    lens_ptr = _ints(lens, dev, "lens", (n_seqs,))
+    workspace, ws_ptr, ws_bytes = _pages_scratch(workspace, n_pages, n_seqs, width, dev)
+    _call(dev, LIB.kda_attn_kv4_resize, table, lens_ptr, refs_ptr, n_seqs, width, n_pages, page,
+          ws_ptr, ws_bytes)
+
+
+def kda_attn_kv4_fork(page_table, lens, refs, parent, page_table_out=None, lens_out=None,
+                      refs_out=None, src=None, dst=None, count=None, page=64, workspace=None):
+    """Sequence n goes on from sequence parent[n] (device int32 [N]; -1: it ends).
+    The outputs default to being in place.  Returns (src, dst, count), the pages for
+    kda_attn_kv4_copy: device int32 [N], [N] and [1], allocated where not given."""
+    table, refs_ptr, n_seqs, width, n_pages, dev = _pages(page_table, refs)
+    page_table_out = page_table if page_table_out is None else page_table_out
+    lens_out = lens if lens_out is None else lens_out
+    refs_out = refs if refs_out is None else refs_out
+    src, dst, count = _lists(src, dst, count, n_seqs, dev)
+    args = (_ints(lens, dev, "lens", (n_seqs,)), refs_ptr, _ints(parent, dev, "parent", (n_seqs,)),
+            _ints(page_table_out, dev, "page_table_out", (n_seqs, width)),
+            _ints(lens_out, dev, "lens_out", (n_seqs,)),
+            _ints(refs_out, dev, "refs_out", (n_pages,)), _ints(src, dev, "src", (n_seqs,)),
+            _ints(dst, dev, "dst", (n_seqs,)), _ints(count, dev, "count", (1,)))
+    workspace, ws_ptr, ws_bytes = _pages_scratch(workspace, n_pages, n_seqs, width, dev)
+    _call(dev, LIB.kda_attn_kv4_fork, table, *args, n_seqs, width, n_pages, page, ws_ptr, ws_bytes)
+    return src, dst, count
+
+
+def _lists(src, dst, count, n, dev):
+    def new(t, size):
+        return torch.empty(size, dtype=torch.int32, device="cuda:%d" % dev) if t is None else t
+    return new(src, n), new(dst, n), new(count, 1)
+
+
+def kda_attn_kv4_compact(page_table, refs, page_table_out=None, refs_out=None, src=None, dst=None,
+                         count=None, workspace=None):
+    """Makes the pages in use the lowest-numbered ones.  The outputs default to being
+    in place.  Returns (src, dst, count), the moves for kda_attn_kv4_copy: device
+    int32 [pages // 2] twice and [1], allocated where not given."""
+    table, refs_ptr, n_seqs, width, n_pages, dev = _pages(page_table, refs)
+    page_table_out = page_table if page_table_out is None else page_table_out
+    refs_out = refs if refs_out is None else refs_out
+    half = n_pages // 2
+    src, dst, count = _lists(src, dst, count, half, dev)
+    args = (_ints(page_table_out, dev, "page_table_out", (n_seqs, width)),
+            _ints(refs_out, dev, "refs_out", (n_pages,)), _ints(src, dev, "src", (half,)),
+            _ints(dst, dev, "dst", (half,)), _ints(count, dev, "count", (1,)))
+    workspace, ws_ptr, ws_bytes = _pages_scratch(workspace, n_pages, n_seqs, width, dev)
+    _call(dev, LIB.kda_attn_kv4_compact, table, refs_ptr, *args, n_seqs, width, n_pages, ws_ptr,
+          ws_bytes)
+    return src, dst, count
+
+
+def kda_attn_kv4_copy(caches, src, dst, count):
+    """Copies pages src[i] to dst[i], i < count, in each of `caches` (one 4-bit cache, or a
+    list of them, one for each layer, all of one shape); src and dst device int32
+    [n], count [1]."""
+    caches = [caches] if isinstance(caches, torch.Tensor) else list(caches)
+    if not 1 <= len(caches) <= KV4_MAX_CACHES:
+        raise ValueError("kda_attn_kv4_copy: 1 to %d caches" % KV4_MAX_CACHES)
+    dev, shape = caches[0].get_device(), caches[0].shape
+    if dev < 0:
+        raise TypeError("the caches must be CUDA tensors")
+    if len(shape) != 3 or shape[2] % KV4_TOKEN_BYTES or shape[2] // KV4_TOKEN_BYTES not in KV4_PAGES:
+        raise ValueError("a cache must be [pages, kv_heads, page * 144], page one of %s"
+                         % (KV4_PAGES,))
+    for c in caches:
+        if c.shape != shape:
+            raise ValueError("kda_attn_kv4_copy: the caches must have one shape")
+    most = src.numel()
+    array = (_c.c_void_p * len(caches))(*[_packed(c, torch.uint8, dev, "cache") for c in caches])
+    _call(dev, LIB.kda_attn_kv4_copy, array, len(caches), shape[0], shape[2] // KV4_TOKEN_BYTES,
+          shape[1], _ints(src, dev, "src", (most,)), _ints(dst, dev, "dst", (most,)),
+          _ints(count, dev, "count", (1,)), most)
+
+
+# ---------------------------------------------------------------- linear attention
+
+def _decays(g, lead, heads, dev):
+    """(pointer, token-row stride) of g: [heads], or [.., rows, heads] in rows."""
+    if g.dim() == 1:
+        if g.shape[0] != heads:
+            raise ValueError("g must be [rows, heads] or [heads]")
+        return _packed(g, torch.float32, dev, "g"), 0
+    if g.shape != lead + (heads,):
+        raise ValueError("g must be [rows, heads] or [heads]")
+    ptr = _at(g, torch.float32, dev, "g")
+    if g.is_contiguous():
+        return ptr, heads
+    stride = g.stride()
+    row = stride[-2] if lead[-1] > 1 else heads
+    if stride[-1] != 1 and heads > 1:
+        raise ValueError("g must have unit head stride")
+    if len(lead) == 2 and lead[0] > 1:
+        if lead[1] == 1:
+            row = stride[0]
+        elif stride[0] != lead[1] * row:
+            raise ValueError("g: sequences must be consecutive row blocks")
+    if row < heads:
+        raise ValueError("g: rows must not overlap")
+    return ptr, row
+
+
+def _lin_rows(name, q, k, v, g, out):
+    """What both calls take of their rows: (type, device, pointers, strides, lead, heads)."""
+    in_dtype, dev = _attn_type(q, "q")
+    dt = q.dtype
+    q_ptr, q_row = _rows(q, dt, dev, "q")
+    k_ptr, k_row = _rows(k, dt, dev, "k")
+    v_ptr, v_row = _rows(v, dt, dev, "v")
+    o_ptr, o_row = _rows(out, dt, dev, "out")
+    lead, heads, qk_heads = tuple(q.shape[:-2]), v.shape[-2], q.shape[-2]
+    if k.shape != q.shape or v.shape[:-2] != q.shape[:-2] or out.shape != v.shape:
+        raise ValueError("%s: k must have q's shape, out v's, and v q's rows" % name)
+    g_ptr, g_row = _decays(g, lead, heads, dev)
+    return (in_dtype, dev, (q_ptr, k_ptr, v_ptr, g_ptr, o_ptr),
+            (q_row, k_row, v_row, g_row, o_row), lead, heads, qk_heads)
+
+
+def _lin_state(t, n_seqs, heads, dev, name):
+    if t is None:
+        return None
+    if t.shape != (n_seqs, heads, HEAD_DIM, HEAD_DIM):
+        raise ValueError("%s must be [sequences, heads, 128, 128]" % name)
+    return _packed(t, torch.float32, dev, name)
+
+
+def kda_lin_prefill_workspace(rows, n_seqs, heads, device="cuda"):
+    """Workspace for kda_lin_prefill over `rows` token rows in total."""
+    need = LIB.kda_lin_prefill_workspace_size(int(rows), n_seqs, heads)
+    return torch.empty(int(need), dtype=torch.uint8, device=device)
+
+
+def kda_lin_prefill(q, k, v, g, out, state_in=None, state_out=None, t=None, cu_seqlens=None,
+                    scale=Q_SCALE, workspace=None):
+    """Linear attention with a decay for each head over prompts.  BF16 or FP16 q, k
+    [rows, qk_heads, 128] and v, out [rows, heads, 128], which may be strided views;
+    g FP32 [rows, heads] or [heads]; state_in and state_out FP32 [N, heads, 128, 128],
+    None for states of zero, or states that are not wanted; they may be one.
+    cu_seqlens (device int32 [N+1]) gives packed sequences; without it, four
+    dimensions [N, T, heads, 128] hold N sequences and three one, of t tokens each
+    (default: all) with the rows behind them left alone."""
+    in_dtype, dev, ptrs, strides, lead, heads, qk_heads = _lin_rows("kda_lin_prefill", q, k, v, g,
+                                                                    out)
+    cu = None
+    if cu_seqlens is not None:
+        if len(lead) != 1 or t not in (None, lead[0]):
+            raise ValueError("kda_lin_prefill: packed rows have three dimensions, and t is all "
+                             "of them")
+        cu, n_seqs, t_pad = _packed(cu_seqlens, torch.int32, dev, "cu_seqlens"), \
+            cu_seqlens.numel() - 1, lead[0]
+    else:
+        n_seqs, t_pad = (1, lead[0]) if len(lead) == 1 else lead
+    t = t_pad if t is None else t
+    states = [_lin_state(s, n_seqs, heads, dev, name)
+              for s, name in ((state_in, "state_in"), (state_out, "state_out"))]
+    rows = t_pad if cu else t_pad * n_seqs
+    workspace, ws_ptr, ws_bytes = _scratch(
+        workspace, lambda: LIB.kda_lin_prefill_workspace_size(rows, n_seqs, heads), dev)
+    _call(dev, LIB.kda_lin_prefill, *states, *ptrs, t, t_pad, cu, n_seqs, heads, qk_heads, HEAD_DIM,
+          in_dtype, *strides, float(scale), ws_ptr, ws_bytes)
+
+
+def kda_lin_decode(q, k, v, g, out, state_in=None, state_out=None, snapshots=(), scale=Q_SCALE):
+    """Up to 8 tokens of each sequence: q, k [N, k, qk_heads, 128] and v, out
+    [N, k, heads, 128] (or without k: one token), g FP32 [N, k, heads] or [heads];
+    states as kda_lin_prefill's; snapshots: up to k tensors like the states,
+    snapshots[t] = state after row t."""
+    in_dtype, dev, ptrs, strides, lead, heads, qk_heads = _lin_rows("kda_lin_decode", q, k, v, g,
+                                                                    out)
+    n_seqs, krows = lead if len(lead) == 2 else (lead[0], 1)
+    states = [_lin_state(s, n_seqs, heads, dev, name)
+              for s, name in ((state_in, "state_in"), (state_out, "state_out"))]
+    snaps = [_lin_state(s, n_seqs, heads, dev, "snapshot") for s in snapshots]
+    array = (_c.c_void_p * len(snaps))(*snaps) if snaps else None
+    _call(dev, LIB.kda_lin_decode, *states, *ptrs, n_seqs, krows, heads, qk_heads, HEAD_DIM,
+          in_dtype, *strides, float(scale), array, len(snaps))
 
 
 def kda_sync_status(device=None):

@@ -1,0 +1,217 @@
+// Rotary positions of the rows that the attention calls take (kda_attn_rope).
+// Pair p of a head turns by positions[r][axis of p] * inv_freq[p].
+//
+// Bound by memory, 512 bytes a row and head.  A CTA takes a few rows: their angles
+// first, shared by all heads, then heads in 16-byte pieces.
+//
+// Angles.  A turn is 2^64: F = inv_freq / (2 pi) in that unit (one FP64 product a pair
+// and CTA), and position * F in integers drops whole turns exactly.  F's 53 bits leave
+// an angle exact to 2^-53 |position * inv_freq|, below 2^-20 of a turn for all int32 positions
+// and frequencies up to 4; sincospif takes the rest.
+#include "attn_common.h"
+#include "f32x2.h"
+
+namespace kda {
+namespace {
+
+using namespace attn;
+
+constexpr int kThreads = 256;
+constexpr int kMaxPairs = D / 2;
+
+struct RopeArgs {
+    const uint16_t* in[2];  // q, k
+    uint16_t* out[2];
+    long long in_stride[2], out_stride[2];
+    int heads[2];
+    long long rows;
+    const int* positions;
+    const float* inv_freq;
+    int axes, pairs;
+    uint32_t axis[4];  // of each pair, two bits
+    float factor;
+};
+
+// a, b turned by the pair's angle.
+__device__ __forceinline__ float2 turn(float a, float b, float2 cs) {
+    return make_float2(fmaf(a, cs.x, -b * cs.y), fmaf(b, cs.x, a * cs.y));
+}
+
+// A head's 16-byte piece u (channels 8u..8u+7) with whole pairs next to each other.
+template <bool F16>
+__device__ __forceinline__ uint4 turn_piece(uint4 x, const float2* cs, int u, int pairs) {
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int p = 4 * u + i;
+        if (p < pairs) {
+            const float2 v = widen2<F16>(w[i]), y = turn(v.x, v.y, cs[p]);
+            w[i] = narrow2<F16>(y.x, y.y);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+enum Layout { kInterleaved, kHalves8, kHalves };  // kHalves8: pairs a multiple of 8
+
+template <bool F16, int LAYOUT>
+__global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int tile_rows) {
+    __shared__ float2 cs[8][kMaxPairs];
+    __shared__ unsigned long long unit[kMaxPairs];
+    pdl_wait();
+    pdl_release();
+    const int tid = threadIdx.x;
+    if (tid < a.pairs) {
+        // the fraction of a turn a position adds, in units of 2^-64 turns
+        const double f = (double)__ldg(a.inv_freq + tid) * 0.15915494309189535;
+        const double whole = f - floor(f);
+        unit[tid] = (unsigned long long)(whole * 18446744073709551616.0);
+    }
+    const long long row0 = (long long)blockIdx.x * tile_rows;
+    const int rows = (int)min((long long)tile_rows, a.rows - row0);
+    __syncthreads();
+    for (int i = tid; i < rows * a.pairs; i += kThreads) {
+        const int r = i / a.pairs, p = i - r * a.pairs;
+        const int axis = a.axis[p >> 4] >> (2 * (p & 15)) & 3;
+        const long long pos = __ldg(a.positions + (row0 + r) * a.axes + axis);
+        const unsigned long long at = (unsigned long long)pos * unit[p];
+        float s, c;
+        sincospif((float)((int)(at >> 32)) * 0x1p-31f, &s, &c);
+        cs[r][p] = make_float2(c * a.factor, s * a.factor);
+    }
+    __syncthreads();
+    // pieces of a row: q's heads, then k's, 16 (or fewer) pieces a head
+    const int per_head = LAYOUT == kHalves8 ? 16 - a.pairs / 8 : LAYOUT == kHalves ? 32 : 16;
+    const int heads = a.heads[0] + a.heads[1];
+    const int first = blockIdx.y * kThreads + tid, step = gridDim.y * kThreads;
+    const int per_row = heads * per_head, total = rows * per_row;
+    // (a head's lanes stay together in kHalves: 32 pieces, and step a multiple of 32)
+    for (int i = first; i < total; i += step) {
+        const int r = i / per_row, in_row = i - r * per_row;
+        int h = in_row / per_head;
+        const int u = in_row - h * per_head;
+        const int which = h >= a.heads[0];
+        if (which) h -= a.heads[0];
+        const uint16_t* src = a.in[which] + (row0 + r) * a.in_stride[which] + h * D;
+        uint16_t* dst = a.out[which] + (row0 + r) * a.out_stride[which] + h * D;
+        if constexpr (LAYOUT == kInterleaved) {
+            const uint4 x = reinterpret_cast<const uint4*>(src)[u];
+            reinterpret_cast<uint4*>(dst)[u] = turn_piece<F16>(x, cs[r], u, a.pairs);
+        } else if constexpr (LAYOUT == kHalves8) {
+            const int turned = a.pairs / 8;
+            if (u >= turned) {  // behind the pairs: as it is
+                const int at = u + turned;
+                reinterpret_cast<uint4*>(dst)[at] = reinterpret_cast<const uint4*>(src)[at];
+                continue;
+            }
+            const uint4 x = reinterpret_cast<const uint4*>(src)[u];
+            const uint4 y = reinterpret_cast<const uint4*>(src)[u + turned];
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+            uint32_t xo[4], yo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 p = widen2<F16>(xs[e]), w = widen2<F16>(ys[e]);
+                const float2 lo = turn(p.x, w.x, cs[r][8 * u + 2 * e]);
+                const float2 hi = turn(p.y, w.y, cs[r][8 * u + 2 * e + 1]);
+                xo[e] = narrow2<F16>(lo.x, hi.x);
+                yo[e] = narrow2<F16>(lo.y, hi.y);
+            }
+            reinterpret_cast<uint4*>(dst)[u] = make_uint4(xo[0], xo[1], xo[2], xo[3]);
+            reinterpret_cast<uint4*>(dst)[u + turned] = make_uint4(yo[0], yo[1], yo[2], yo[3]);
+        } else {
+            // four channels a lane, their partners read one by one: all lanes of the
+            // head have read before any writes (the output may be the input)
+            const uint2 own = reinterpret_cast<const uint2*>(src)[u];
+            float x[4], y[4] = {};
+            const float2 lo = widen2<F16>(own.x), hi = widen2<F16>(own.y);
+            x[0] = lo.x, x[1] = lo.y, x[2] = hi.x, x[3] = hi.y;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int c = 4 * u + e;
+                if (c < 2 * a.pairs)
+                    y[e] = widen2<F16>(src[c < a.pairs ? c + a.pairs : c - a.pairs]).x;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int c = 4 * u + e;
+                if (c < a.pairs) x[e] = turn(x[e], y[e], cs[r][c]).x;
+                else if (c < 2 * a.pairs) x[e] = turn(y[e], x[e], cs[r][c - a.pairs]).y;
+            }
+            reinterpret_cast<uint2*>(dst)[u] =
+                make_uint2(narrow2<F16>(x[0], x[1]), narrow2<F16>(x[2], x[3]));
+        }
+    }
+}
+
+}  // namespace
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" kda_status kda_attn_rope(const void* q, const void* k, void* q_out, void* k_out,
+                                    int64_t rows, int heads, int kv_heads, int head_dim,
+                                    int in_dtype, int64_t q_row_stride, int64_t k_row_stride,
+                                    int64_t q_out_row_stride, int64_t k_out_row_stride,
+                                    const int* positions, int axes, const float* inv_freq,
+                                    int pairs, const uint8_t* pair_axis, int interleaved,
+                                    float factor, uint64_t stream) {
+    const char* fn = "kda_attn_rope";
+    KDA_REQUIRE(head_dim == D, KDA_ERR_UNSUPPORTED, "%s: head_dim %d unsupported (only 128)", fn,
+                head_dim);
+    KDA_REQUIRE(in_dtype == KDA_F32 || in_dtype == KDA_BF16 || in_dtype == KDA_F16,
+                KDA_ERR_INVALID_ARG, "%s: in_dtype %d is not a kda_dtype", fn, in_dtype);
+    KDA_REQUIRE(in_dtype != KDA_F32, KDA_ERR_UNSUPPORTED, "%s: FP32 rows are not built", fn);
+    KDA_REQUIRE(rows >= 0 && rows < 0x7fffffffLL && heads >= 1 && kv_heads >= 0 &&
+                    (long long)heads + kv_heads <= 1 << 16,
+                KDA_ERR_INVALID_ARG,
+                "%s: rows (%lld), heads (%d) and kv_heads (%d): 0 to 2^31 - 2 rows, at least one "
+                "head, at most 2^16 heads",
+                fn, (long long)rows, heads, kv_heads);
+    KDA_REQUIRE(axes >= 1 && axes <= 4, KDA_ERR_INVALID_ARG, "%s: axes (%d) must be 1 to 4", fn,
+                axes);
+    KDA_REQUIRE(pairs >= 1 && pairs <= kMaxPairs, KDA_ERR_INVALID_ARG,
+                "%s: pairs (%d) must be 1 to %d", fn, pairs, kMaxPairs);
+    KDA_REQUIRE(isfinite(factor), KDA_ERR_INVALID_ARG, "%s: factor must be finite", fn);
+    RopeArgs a = {};
+    for (int p = 0; pair_axis && p < pairs; ++p) {
+        KDA_REQUIRE(pair_axis[p] < axes, KDA_ERR_INVALID_ARG, "%s: pair %d has axis %d of %d", fn,
+                    p, pair_axis[p], axes);
+        a.axis[p >> 4] |= (uint32_t)pair_axis[p] << (2 * (p & 15));
+    }
+    if (rows == 0) return KDA_OK;
+    kda_status st = validate_rows(fn, "q", q, q_row_stride, heads);
+    if (st == KDA_OK) st = validate_rows(fn, "q_out", q_out, q_out_row_stride, heads);
+    if (st == KDA_OK && kv_heads) st = validate_rows(fn, "k", k, k_row_stride, kv_heads);
+    if (st == KDA_OK && kv_heads)
+        st = validate_rows(fn, "k_out", k_out, k_out_row_stride, kv_heads);
+    if (st != KDA_OK) return st;
+    KDA_REQUIRE((q != q_out || q_row_stride == q_out_row_stride) &&
+                    (!kv_heads || k != k_out || k_row_stride == k_out_row_stride),
+                KDA_ERR_INVALID_ARG, "%s: an output in its input's place has its row stride", fn);
+    KDA_REQUIRE(positions && inv_freq, KDA_ERR_INVALID_ARG, "%s: null pointer argument", fn);
+    KDA_REQUIRE((reinterpret_cast<uintptr_t>(positions) & 3) == 0 &&
+                    (reinterpret_cast<uintptr_t>(inv_freq) & 3) == 0,
+                KDA_ERR_INVALID_ARG, "%s: positions and inv_freq must be 4-byte aligned", fn);
+    KDA_REQUIRE(!fault_injected(), KDA_ERR_CUDA, "%s: injected launch failure", fn);
+    a.in[0] = (const uint16_t*)q;
+    a.in[1] = (const uint16_t*)k;
+    a.out[0] = (uint16_t*)q_out;
+    a.out[1] = (uint16_t*)k_out;
+    a.in_stride[0] = q_row_stride, a.in_stride[1] = k_row_stride;
+    a.out_stride[0] = q_out_row_stride, a.out_stride[1] = k_out_row_stride;
+    a.heads[0] = heads, a.heads[1] = kv_heads;
+    a.rows = rows, a.positions = positions, a.inv_freq = inv_freq;
+    a.axes = axes, a.pairs = pairs, a.factor = factor;
+    // eight rows share the frequencies; with few rows, one each
+    const int tile = rows >= 8 * 152 ? 8 : 1;
+    const dim3 grid((unsigned)((rows + tile - 1) / tile));
+    const bool f16 = in_dtype == KDA_F16;
+    auto kernel = f16 ? rope_kernel<true, kHalves> : rope_kernel<false, kHalves>;
+    if (interleaved)
+        kernel = f16 ? rope_kernel<true, kInterleaved> : rope_kernel<false, kInterleaved>;
+    else if (pairs % 8 == 0)
+        kernel = f16 ? rope_kernel<true, kHalves8> : rope_kernel<false, kHalves8>;
+    launch_pdl(kernel, grid, dim3(kThreads), 0, as_stream(stream), a, tile);
+    return launch_result(fn);
+}

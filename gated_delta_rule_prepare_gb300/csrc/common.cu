@@ -20,9 +20,9 @@ bool fault_injected(const char* what) {
 }
 
 // The units' status words, fetched and cleared together: one copy to the host for
-// all of them (each word read by a copy of its own: 60 us a call for the six,
+// all of them (each word read by a copy of its own: 60 us a call for six,
 // and 82 with another copy to clear it).
-constexpr int kStatusWords = 6;
+constexpr int kStatusWords = 9;
 struct StatusWords {
     unsigned* at[kStatusWords];
 };
@@ -37,7 +37,8 @@ static cudaError_t fetch_status(unsigned (&out)[kStatusWords]) {
     std::lock_guard<std::mutex> hold(one_at_a_time);
     cudaError_t (*const where[kStatusWords])(unsigned**) = {
         status_word_prefill, status_word_conv, status_word_prefill_tc,
-        status_word_attn,    status_word_kv4,  status_word_decode};
+        status_word_attn,    status_word_kv4,  status_word_decode,
+        status_word_pages,   status_word_lin,  status_word_lin_walk};
     StatusWords words;
     for (int i = 0; i < kStatusWords; ++i) {
         const cudaError_t e = where[i](&words.at[i]);
@@ -68,14 +69,16 @@ extern "C" kda_status kda_sync_status(uint64_t stream) {
                        cudaGetErrorString(e));
         return KDA_ERR_CUDA;
     }
-    const unsigned a = w[0] | w[2], b = w[1], d = w[3] | w[4] | w[5], all = a | b | d;
+    const unsigned a = w[0] | w[2], b = w[1], d = w[3] | w[4] | w[5] | w[6];
+    const unsigned l = w[7] | w[8], all = a | b | d | l;
     if (all) {
         kda::set_error("kda_sync_status: device-side check failed (prefill 0x%x, conv 0x%x, "
-                       "attention 0x%x): %s",
-                       a, b, d,
+                       "attention 0x%x, linear attention 0x%x): %s",
+                       a, b, d, l,
                        (all & kda::STATUS_TIMEOUT)      ? "a bounded wait timed out"
                        : (all & kda::STATUS_SMEM_ALIGN) ? "shared memory misaligned"
                        : (all & kda::STATUS_BAD_PAGES)  ? "lens or page_table outside the cache"
+                       : (all & kda::STATUS_NO_PAGES)   ? "no free pages left"
                                                         : "malformed cu_seqlens");
         return KDA_ERR_DEVICE;
     }

@@ -42,6 +42,7 @@ enum : unsigned {
     STATUS_TIMEOUT = 1u << 1,  // a bounded wait on a copy or an MMA gave up
     STATUS_SMEM_ALIGN = 1u << 2,  // dynamic shared memory not 1024-byte aligned
     STATUS_BAD_PAGES = 1u << 3,  // lens or page_table does not fit the 4-bit cache
+    STATUS_NO_PAGES = 1u << 4,  // fewer free pages than a call wanted
 };
 
 // Where each checking unit's word is on the current device (kda_sync_status
@@ -52,6 +53,9 @@ cudaError_t status_word_prefill_tc(unsigned** word);
 cudaError_t status_word_attn(unsigned** word);
 cudaError_t status_word_kv4(unsigned** word);
 cudaError_t status_word_decode(unsigned** word);
+cudaError_t status_word_pages(unsigned** word);
+cudaError_t status_word_lin_walk(unsigned** word);
+cudaError_t status_word_lin(unsigned** word);
 
 // kda_prefill's argument checks, shared with kda_prefill_static_ws (prefill.cu).
 kda_status validate_prefill(const char* fn, const float* state, const void* q, const void* k,

@@ -59,6 +59,8 @@ extern "C" {
 /* Pieces into which kda_attn_kv4_decode cuts a batch, at most (its workspace
  * holds two partial results for each, and a record). */
 #define KDA_KV4_PIECES 480
+/* Caches that one kda_attn_kv4_copy takes, at most. */
+#define KDA_KV4_MAX_CACHES 128
 
 typedef enum {
     KDA_OK = 0,
@@ -69,7 +71,7 @@ typedef enum {
     KDA_ERR_DEVICE = 5       /* device-side check failed (kda_sync_status)     */
 } kda_status;
 
-/* KDA_F16 is taken by the attention calls only. */
+/* KDA_F16 is taken by the kda_attn_ and kda_lin_ calls only. */
 typedef enum { KDA_F32 = 0, KDA_BF16 = 1, KDA_F16 = 2 } kda_dtype;
 
 /*
@@ -417,6 +419,69 @@ kda_status kda_prefill_static_ws(float* state, const void* q, const void* k, con
                                  uint64_t stream);
 
 /*
+ * Linear attention with a decay for each head: the other linear layer of hybrid
+ * decoders, beside the KDA core (no delta term, one decay for all channels of a
+ * head).  The source pages do not describe it; these calls are the library's own.
+ * Per head, an FP32 state S[i][j] in kda_decode's layout (i = key channel, j =
+ * value channel); for each token t
+ *     S[i][j] <- exp(g_t) * S[i][j] + k_t[i] * v_t[j]
+ *     o_t[j]   = scale * sum_i q_t[i] * S[i][j]
+ *
+ *   q, k : in_dtype (KDA_BF16, KDA_F16), qk_heads heads, token row r of head h at
+ *           q + r*q_row_stride + h*128; head h of v, o and the state goes with head
+ *           h / (heads / qk_heads) of q and k
+ *   v, o : in_dtype, heads heads, likewise (o overlaps none of the inputs)
+ *   g    : FP32, token row r of head h at g + r*g_row_stride + h; a stride of 0 is
+ *           one decay for each head, whatever the token.  g <= 0, -inf among it:
+ *           what the state held is gone (decays below e^-100 count as 0).
+ *   state_in : FP32 [n_seqs][heads][128][128], or NULL: states of zero
+ *   state_out : the state after the last token, or NULL: not wanted; may be state_in
+ *   heads : a multiple of qk_heads
+ *   row strides of q, k, v, o : multiples of 8 elements, at least heads*128
+ *           (qk_heads*128); g_row_stride 0 or at least heads.  All pointers but g's
+ *           (4 bytes) 16-byte aligned.
+ *   scale : finite
+ * A token whose q, k, v or g is not finite leaves the tokens before it as they are.
+ *
+ * kda_lin_prefill -- prompts.
+ *   cu_seqlens == NULL: n_seqs sequences of t tokens, rows [n_seqs][t_pad]; rows
+ *           [t, t_pad) are neither read into arithmetic nor written.
+ *   cu_seqlens != NULL: DEVICE int32 [n_seqs + 1] offsets of packed rows, t the
+ *           total and t_pad equal to it.  Checked on the device: a sequence whose
+ *           offsets lie outside 0..t or fall is left out, and kda_sync_status
+ *           reports KDA_ERR_DEVICE.  Sequences may be empty (state_out = state_in).
+ *   workspace : device scratch of at least kda_lin_prefill_workspace_size bytes,
+ *           16-byte aligned; its contents on entry do not matter; calls that share
+ *           one must be ordered on the GPU.
+ */
+kda_status kda_lin_prefill(const float* state_in, float* state_out, const void* q, const void* k,
+                           const void* v, const float* g, void* o, int t, int t_pad,
+                           const int* cu_seqlens, int n_seqs, int heads, int qk_heads,
+                           int head_dim, int in_dtype, int64_t q_row_stride,
+                           int64_t k_row_stride, int64_t v_row_stride, int64_t g_row_stride,
+                           int64_t o_row_stride, float scale, void* workspace,
+                           size_t workspace_bytes, uint64_t stream);
+
+/* Bytes of workspace kda_lin_prefill needs for `rows` token rows in total
+ * (n_seqs * t_pad without offsets).  Returns 0 for invalid arguments. */
+size_t kda_lin_prefill_workspace_size(int64_t rows, int n_seqs, int heads);
+
+/*
+ * kda_lin_decode -- krows tokens (1 for decode, up to KDA_MAX_K for verification)
+ * of each sequence, rows [n_seqs][krows].  The result is that of krows calls of one
+ * row each, bit for bit.
+ *   snapshots : HOST array of n_snap device pointers, as kda_decode_k's:
+ *           snapshots[t] receives the state after row t; none is state_in or
+ *           state_out.
+ */
+kda_status kda_lin_decode(const float* state_in, float* state_out, const void* q, const void* k,
+                          const void* v, const float* g, void* o, int n_seqs, int krows,
+                          int heads, int qk_heads, int head_dim, int in_dtype,
+                          int64_t q_row_stride, int64_t k_row_stride, int64_t v_row_stride,
+                          int64_t g_row_stride, int64_t o_row_stride, float scale,
+                          float* const* snapshots, int n_snap, uint64_t stream);
+
+/*
  * Full attention.  A hybrid decoder puts full-attention layers between its KDA
  * layers; the four calls below are such a layer's core, for the same packed
  * prompts (kda_attn_prefill beside kda_prefill) and the same decode and verify
@@ -551,6 +616,97 @@ kda_status kda_attn_kv4_decode(const void* q, const uint8_t* cache, int64_t n_pa
 /* Bytes of workspace kda_attn_kv4_decode needs.  Returns 0 for invalid
  * arguments. */
 size_t kda_attn_kv4_workspace_size(int n_seqs, int krows, int heads, int kv_heads);
+
+/*
+ * kda_attn_rope -- rotary positions with one or several axes (time, height and
+ * width of video, for one) for the rows that the attention calls take.  Pair p of
+ * each head turns by the angle a = positions[r][axis of p] * inv_freq[p]:
+ *     (x, y) -> factor * (x cos a - y sin a, y cos a + x sin a)
+ * with x, y the channels 2p, 2p + 1 (interleaved) or p, p + pairs; channels from
+ * 2 * pairs on stay as they are.  Angles are exact to 2^-20 of a turn for every
+ * position and frequencies up to 4; the rest is FP32, rounded once.
+ *
+ *   q, k : in_dtype (KDA_BF16, KDA_F16), token row r of head h at
+ *           q + r*q_row_stride + h*128; q_out, k_out likewise, each its input or
+ *           apart from it.  kv_heads 0 with k NULL: q alone.
+ *   positions : DEVICE int32 [rows][axes], 1 <= axes <= 4; negative ones turn back
+ *   inv_freq : DEVICE FP32 [pairs], 1 <= pairs <= 64, finite
+ *   pair_axis : HOST [pairs], the axis of each pair, or NULL: axis 0
+ *   factor : finite (1, or a scaling of long contexts)
+ */
+kda_status kda_attn_rope(const void* q, const void* k, void* q_out, void* k_out, int64_t rows,
+                         int heads, int kv_heads, int head_dim, int in_dtype,
+                         int64_t q_row_stride, int64_t k_row_stride, int64_t q_out_row_stride,
+                         int64_t k_out_row_stride, const int* positions, int axes,
+                         const float* inv_freq, int pairs, const uint8_t* pair_axis,
+                         int interleaved, float factor, uint64_t stream);
+
+/*
+ * Pages of the 4-bit cache.  The three calls below keep page_table (DEVICE int32
+ * [n_seqs][max_pages], -1: no page) and refs (DEVICE int32 [n_pages]: how often a
+ * page is named, by the table or by the caller; 0: free), all on the device, so that
+ * they can be captured.  New pages are the lowest-numbered free ones, in the order
+ * of the rows and their entries: the result is deterministic.  Where there
+ * are not enough, entries stay -1 (what the other calls make of that is said
+ * there), and kda_sync_status reports KDA_ERR_DEVICE; likewise for entries, lens or
+ * parents outside their ranges, which count as -1 (lens: as the nearest in range).
+ * page_table_out may be page_table, lens_out lens and refs_out refs; buffers do not overlap
+ * otherwise.
+ *   workspace : device scratch of at least kda_attn_kv4_pages_workspace_size
+ *           bytes, 16-byte aligned; its contents on entry do not matter; calls that
+ *           share one must be ordered on the GPU.
+ *
+ * kda_attn_kv4_resize -- gives and frees pages, in place: afterwards sequence n
+ * has the pages of lens[n] positions (entries below ceil(lens[n] / page)) and no
+ * others.  Entries that are there stay.  lens[n] = 0 ends a sequence; a smaller
+ * lens[n] takes rejected rows back.
+ */
+kda_status kda_attn_kv4_resize(int* page_table, const int* lens, int* refs, int n_seqs,
+                               int max_pages, int64_t n_pages, int page, void* workspace,
+                               size_t workspace_bytes, uint64_t stream);
+
+/*
+ * kda_attn_kv4_fork -- sequence n goes on from sequence parent[n] (DEVICE int32
+ * [n_seqs]; -1: it ends): lens_out[n] = lens[parent[n]], and its pages are its
+ * parent's, but for a last page that is partly filled: the lowest child keeps it,
+ * every other one gets a page of its own, and (page, page of its own) goes on the
+ * list for kda_attn_kv4_copy.  Pages no longer named become free (they may be
+ * among the new ones); rows hold the pages of lens_out, no others.  A child that
+ * gets no page keeps its parent's full pages, and lens_out[n] counts those alone.
+ *   src, dst : DEVICE int32 [n_seqs], the list, -1 behind its end; count : DEVICE
+ *           int32 [1], its length
+ */
+kda_status kda_attn_kv4_fork(const int* page_table, const int* lens, const int* refs,
+                             const int* parent, int* page_table_out, int* lens_out,
+                             int* refs_out, int* src, int* dst, int* count, int n_seqs,
+                             int max_pages, int64_t n_pages, int page, void* workspace,
+                             size_t workspace_bytes, uint64_t stream);
+
+/*
+ * kda_attn_kv4_compact -- pages in use become the lowest-numbered ones: with u pages in
+ * use, those from u on move, in order, to the free ones below u; page_table_out and
+ * refs_out name them there.
+ *   src, dst : DEVICE int32 [n_pages / 2] (any pointer where that is 0), the moves
+ *           for kda_attn_kv4_copy, -1 behind their end; count : DEVICE int32 [1]
+ */
+kda_status kda_attn_kv4_compact(const int* page_table, const int* refs, int* page_table_out,
+                                int* refs_out, int* src, int* dst, int* count, int n_seqs,
+                                int max_pages, int64_t n_pages, void* workspace,
+                                size_t workspace_bytes, uint64_t stream);
+
+/* Bytes of workspace the three calls need.  Returns 0 for invalid arguments. */
+size_t kda_attn_kv4_pages_workspace_size(int64_t n_pages, int n_seqs, int max_pages);
+
+/*
+ * kda_attn_kv4_copy -- copies page src[i] to page dst[i], i < count[0] (at most
+ * max_count), in each of n_caches caches (HOST array of at most
+ * KDA_KV4_MAX_CACHES device pointers, all of the same sizes: one for each layer).  No
+ * page is both a source and a destination, or twice a destination.  Pairs with a
+ * page outside the cache are left out, and kda_sync_status reports KDA_ERR_DEVICE.
+ */
+kda_status kda_attn_kv4_copy(uint8_t* const* caches, int n_caches, int64_t n_pages, int page,
+                             int kv_heads, const int* src, const int* dst, const int* count,
+                             int max_count, uint64_t stream);
 
 /* Synchronises `stream`, then reads and clears the device status words of the
  * calling thread's current device.  Returns KDA_OK, KDA_ERR_DEVICE (a
