@@ -1,10 +1,1027 @@
-// Linear attention with a decay for each head over prompts (kda_lin_prefill).
+// Linear attention with a decay for each head over prompts (kda_lin_prefill), in
+// chunks of C = 128 tokens on the tensor cores.  With G_t the sum of g over a chunk's
+// tokens up to t, S the state in front of the chunk and a head's Q, K, V [C][128],
+//     P[t][s] = exp(G_t - G_s) (Q K^T)[t][s] for s <= t, else 0
+//     O = scale * (P V + diag(exp(G_t)) Q S)
+//     S <- exp(G_C) S + K^T W,      W[s] = exp(G_C - G_s) V[s]
+//
+// Bound by memory: 1 KB a token and head for five 128^3 products a chunk and head,
+// 83 kFLOP a token against 1 KB.  So all of a chunk's work has to fit under its copy,
+// 2.9 us at a multiprocessor's share of the bandwidth:
+//  - One persistent CTA a multiprocessor, chunks one after the other; chunk c + 1's
+//    Q, K and V are copied by TMA while chunk c is worked on.
+//  - S stays in registers, FP32, added to with one rounding a chunk (256 threads, a row
+//    of 64 columns each); the products' accumulators are TMEM's four quarters: Q K^T (P
+//    is written over it), Q S, P V, K^T W.
+//  - Decays never enter as exp(G_t) exp(-G_s), whose factors leave FP32's range.  Below
+//    the diagonal blocks of 32 tokens the factors are decays up to the end of s's block
+//    and from there to t, on them exp(G_t - G_s) itself.  Sums of g run within blocks, so
+//    that decays near 1 do not come from differences of large sums.
+//  - P and the copy of S that Q is multiplied with are rounded to 16 bits, which
+//    moves O by less than its own rounding does.  W is kept as two 16-bit
+//    numbers, hi + lo, and the product done twice: the state accumulates over thousands of
+//    tokens and is an FP32 output.  hi is written over V and lo over Q once both are
+//    through, so that two stages of inputs fit.
+//  - FP16 operands are scaled by powers of two that the largest entry of S, or of V,
+//    in the chunk gives: FP16's range is narrower than FP32 states are.
+//
+// Pieces.  Chains (heads of sequences) are cut where there are too few of them, or where
+// they are too uneven, for all multiprocessors.  A piece that starts inside a chain
+// needs the state there: lin_prefill_kernel<.., SUM> first adds up what each cut
+// segment contributes (K and V alone), and lin_join_kernel runs through a chain's
+// segments.  See Plan.
+#include <algorithm>
+#include <cmath>
+
+#include "f32x2.h"
 #include "lin_attn.h"
+#include "sm103_tc.h"
+#include "tma_map.h"
 
 namespace kda {
 namespace {
 
+using namespace attn;
+using namespace tc;
+using lin::Args;
+
 __device__ unsigned g_lin_status = 0;
+
+constexpr int C = 128;  // tokens a chunk
+constexpr int kSms = 152;
+constexpr int kLeastPiece = 6;  // chunks
+constexpr int kStateFloats = D * D;
+
+// ---------------------------------------------------------------- pieces
+
+// How the call's chunks go to `pieces` CTAs (at most kSms).
+//  kPadded: each chain starts a piece, pieces of kLeastPiece chunks: few chunks.
+//  kWhole: chains are not cut; sorted by length they are dealt out there and back:
+//      many chains, none of them longer than 0.6 of a CTA's share.
+//  kEven: chains one after the other, cut into equal pieces.
+enum Kind { kPadded, kWhole, kEven };
+struct Plan {
+    Kind kind;
+    int piece;        // chunks of a piece
+    long long total;  // chunks, or (kPadded) pieces
+};
+struct Work {
+    Args a;
+    int pieces;
+    // of a piece whose last segment's chain goes on in the next piece: what the segment
+    // adds to the state, then the state in front of the next piece
+    float* sum;      // [pieces][128 * 128]
+    float* log_sum;  // [pieces] log2 of the segment's decay
+    float* start;    // [pieces] the state in front of a cut chain that starts there
+};
+
+__device__ __forceinline__ int chunks_of(const Args& a, int n) {
+    lin::Rows r;
+    return sequence_rows(a, n, r) ? (r.count + C - 1) / C : 0;
+}
+__device__ __forceinline__ int padded(int chunks) {
+    return (chunks + kLeastPiece - 1) / kLeastPiece;
+}
+
+// One warp; the same for all warps of the call.
+__device__ __forceinline__ Plan make_plan(const Work& w) {
+    const Args& a = w.a;
+    const int lane = threadIdx.x & 31;
+    long long chunks = 0, pads = 0;
+    int longest = 0;
+    if (!a.cu) {
+        longest = (a.t + C - 1) / C;
+        chunks = (long long)longest * a.n_seqs;
+        pads = (long long)padded(longest) * a.n_seqs;
+    } else {
+        for (int n = lane; n < a.n_seqs; n += 32) {
+            const int c = chunks_of(a, n);
+            chunks += c;
+            pads += padded(c);
+            longest = max(longest, c);
+        }
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            chunks += __shfl_xor_sync(0xffffffffu, chunks, off);
+            pads += __shfl_xor_sync(0xffffffffu, pads, off);
+            longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, off));
+        }
+    }
+    chunks *= a.heads;
+    pads *= a.heads;
+    Plan p;
+    if (pads <= w.pieces) {
+        p = {kPadded, kLeastPiece, pads};
+    } else if ((long long)a.n_seqs * a.heads >= 2LL * w.pieces &&
+               10LL * longest * w.pieces <= 6 * chunks) {
+        p = {kWhole, 0, chunks};
+    } else {
+        p = {kEven, (int)max((chunks + w.pieces - 1) / w.pieces, (long long)kLeastPiece), chunks};
+    }
+    return p;
+}
+
+// Part of one chain: chunks [from, to) of the `of` that head h of sequence n has.
+struct Segment {
+    int n, h, from, to, of;
+};
+
+// The chain that unit x falls in (units: chunks, or for kPadded pieces), x below the
+// total; returns x's number within it.  One warp.
+__device__ __forceinline__ int find_chain(const Args& a, bool pads, long long x, int& n, int& h) {
+    if (!a.cu) {
+        const int c = (a.t + C - 1) / C, u = pads ? padded(c) : c;
+        const long long chain = x / u;
+        n = (int)(chain / a.heads);
+        h = (int)(chain - (long long)n * a.heads);
+        return (int)(x - chain * u);
+    }
+    const int lane = threadIdx.x & 31;
+    for (int n0 = 0; n0 < a.n_seqs; n0 += 32) {
+        int u = 0;
+        if (n0 + lane < a.n_seqs) {
+            u = chunks_of(a, n0 + lane);
+            if (pads) u = padded(u);
+        }
+        long long sum = (long long)u * a.heads;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, sum, off);
+            if (lane >= off) sum += up;
+        }
+        const long long all = __shfl_sync(0xffffffffu, sum, 31);
+        if (x >= all) {
+            x -= all;
+            continue;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, sum > x);
+        const int at = __ffs(past) - 1;
+        const long long first = __shfl_sync(0xffffffffu, sum - (long long)u * a.heads, at);
+        const int each = __shfl_sync(0xffffffffu, u, at);
+        n = n0 + at;
+        h = (int)((x - first) / each);
+        return (int)(x - first - (long long)h * each);
+    }
+    n = -1, h = 0;
+    return 0;
+}
+
+// The i-th longest sequence (ties: the first one), for at most 64 sequences; in more
+// they are taken as they come.  One warp.
+__device__ __forceinline__ int sequence_by_length(const Args& a, int i) {
+    if (!a.cu || a.n_seqs > 64) return i;
+    const int lane = threadIdx.x & 31;
+    const int l0 = lane < a.n_seqs ? chunks_of(a, lane) : -1;
+    const int l1 = lane + 32 < a.n_seqs ? chunks_of(a, lane + 32) : -1;
+    int r0 = 0, r1 = 0;  // how many come before
+    for (int m = 0; m < a.n_seqs; ++m) {
+        const int x0 = __shfl_sync(0xffffffffu, l0, m & 31);
+        const int x1 = __shfl_sync(0xffffffffu, l1, m & 31);
+        const int x = m < 32 ? x0 : x1;
+        r0 += x > l0 || (x == l0 && m < lane);
+        r1 += x > l1 || (x == l1 && m < lane + 32);
+    }
+    const unsigned b0 = __ballot_sync(0xffffffffu, r0 == i && lane < a.n_seqs);
+    const unsigned b1 = __ballot_sync(0xffffffffu, r1 == i && lane + 32 < a.n_seqs);
+    return b0 ? __ffs(b0) - 1 : 31 + __ffs(b1);
+}
+
+// Goes through a piece's segments; the whole warp calls it.
+struct Walk {
+    Plan p;
+    long long x, end;  // kEven: chunks still to come; kWhole: x the round; kPadded: 0, 1
+
+    __device__ __forceinline__ void begin(const Plan& plan, int piece) {
+        p = plan;
+        x = p.kind == kEven ? (long long)piece * p.piece : 0;
+        end = p.kind == kEven ? min(p.total, x + p.piece) : 0;
+    }
+    __device__ __forceinline__ bool next(const Work& w, int piece, Segment& s) {
+        const Args& a = w.a;
+        if (p.kind == kPadded) {
+            if (x++ || piece >= p.total) return false;
+            const int part = find_chain(a, true, piece, s.n, s.h);
+            s.of = chunks_of(a, s.n);
+            s.from = part * kLeastPiece;
+            s.to = min(s.of, s.from + kLeastPiece);
+            return true;
+        }
+        if (p.kind == kWhole) {
+            const long long chains = (long long)a.n_seqs * a.heads;
+            while (x * w.pieces < chains) {
+                const long long chain = x * w.pieces + (x & 1 ? w.pieces - 1 - piece : piece);
+                ++x;
+                if (chain >= chains) continue;
+                const int i = (int)(chain / a.heads);
+                s.h = (int)(chain - (long long)i * a.heads);
+                s.n = sequence_by_length(a, i);
+                s.of = s.to = chunks_of(a, s.n);
+                s.from = 0;
+                if (s.of) return true;
+            }
+            return false;
+        }
+        if (x >= end) return false;
+        s.from = find_chain(a, false, x, s.n, s.h);
+        s.of = chunks_of(a, s.n);
+        s.to = (int)min((long long)s.of, s.from + (end - x));
+        x += s.to - s.from;
+        return true;
+    }
+};
+
+// The last segment of piece i, if its chain goes on in the next one.
+__device__ __forceinline__ bool open_segment(const Work& w, const Plan& p, int i, Segment& s) {
+    if (p.kind == kWhole) return false;
+    if (p.kind == kPadded) {
+        if (i >= p.total) return false;
+        const int part = find_chain(w.a, true, i, s.n, s.h);
+        s.of = chunks_of(w.a, s.n);
+        s.from = part * kLeastPiece;
+        s.to = min(s.of, s.from + kLeastPiece);
+        return s.to < s.of;
+    }
+    const long long first = (long long)i * p.piece, end = min(p.total, first + p.piece);
+    if (first >= end) return false;
+    const int last = find_chain(w.a, false, end - 1, s.n, s.h);
+    s.of = chunks_of(w.a, s.n);
+    s.to = last + 1;
+    s.from = (int)max(0LL, last - (end - 1 - first));
+    return s.to < s.of;
+}
+
+// ---------------------------------------------------------------- the kernel
+
+// Warps: 0..3 P and O, 4..11 the state and W, 12 copies, 13 products, 14 the rest.
+constexpr int kThreads = 480;
+constexpr uint32_t kTile = C * D * 2;         // 32 KB
+constexpr uint32_t kStage = 3 * kTile;        // Q, K, V; later lo, K, hi
+constexpr uint32_t kStateTile = 2 * kStage;   // S in 16 bits
+constexpr uint32_t kTmemP = 0, kTmemQS = 128, kTmemPV = 256, kTmemKW = 384;
+constexpr int kRing = 2;
+
+struct Item {
+    long long row;  // of the segment's first token
+    int rows, h, n;
+    int chunks;     // 0: no more segments
+    const float* src;  // the state in front; null: zeros
+    float* dst;        // where the state behind goes; null: nowhere
+};
+
+struct Shared {
+    uint64_t full[2], empty[2];
+    uint64_t p_ready, o_ready, o_read, s16_ready, qk_ready, v_checked;
+    uint64_t w_ready[2], kw_ready[2];  // by chunk parity: SUM's may be a chunk apart
+    uint64_t token_sync, token_clean, half_sync[2], state_sync;
+    uint64_t item_full[kRing], item_empty[kRing];
+    Item item[kRing];
+    uint32_t tmem;
+    int stop;
+    float sum[2][C];    // of g (log2) within blocks of 32 tokens, up to each token
+    float tail[2][C];   // decay from each token to the end of its block
+    float block[3][2][4];  // sums of blocks, for warps 0..3, 4..7, 8..11
+    float largest[2][16];  // FP16: of S and of V, each warp's
+    float s16_unit[2];     // FP16: what one unit of the state's copy stands for
+    // V's infinities and NaN, by chunk parity: each column's first token (255: none)
+    uint32_t bad_first[2][D / 4];
+    int bad[2];
+};
+constexpr uint32_t kSharedOff = kStateTile + kTile;
+constexpr uint32_t kSmemBytes = kSharedOff + sizeof(Shared);
+static_assert(kSmemBytes <= 232448, "shared memory");
+
+// Waits with an end: a phase that does not come within 2^35 clocks (some 17
+// seconds), or another role's giving up, ends the kernel with an error status.
+__device__ __noinline__ bool wait_long(Shared& sh, uint64_t* bar, uint32_t parity) {
+    const long long from = clock64();
+    while (!mbar_wait(bar, parity, 32)) {
+        if (*(volatile int*)&sh.stop) return false;
+        if (clock64() - from > 1LL << 35) {
+            atomicOr(&g_lin_status, STATUS_TIMEOUT);
+            *(volatile int*)&sh.stop = 1;
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool wait_warp(Shared& sh, uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, 1) || wait_long(sh, bar, parity));
+}
+__device__ __forceinline__ void arrive_warp(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile(
+        "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(yes));
+    return yes != 0;
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+// A barrier among some warps, with an end like the other waits (bar.sync has none).
+__device__ __forceinline__ bool sync_warps(Shared& sh, uint64_t* bar, uint32_t& phase) {
+    arrive_warp(bar);
+    const bool ok = wait_warp(sh, bar, phase);
+    phase ^= 1;
+    return ok;
+}
+
+// The roles' view of the ring of segments.
+struct Items {
+    int ring = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ bool next(Shared& sh, Item& it) {
+        if (!wait_warp(sh, &sh.item_full[ring], phase)) return false;
+        it = sh.item[ring];
+        arrive_warp(&sh.item_empty[ring]);
+        if (++ring == kRing) ring = 0, phase ^= 1;
+        return it.chunks > 0;
+    }
+};
+
+// The copying warp: hands out segments and fills the stages.
+template <bool SUM>
+__device__ __forceinline__ void copy_role(const Work& w, Shared& sh, unsigned char* sm,
+                                          const CUtensorMap* mq, const CUtensorMap* mk,
+                                          const CUtensorMap* mv) {
+    const Args& a = w.a;
+    const int lane = threadIdx.x & 31, piece = blockIdx.x;
+    const Plan plan = make_plan(w);
+    Walk walk;
+    walk.begin(plan, piece);
+    Segment cut;
+    const bool open = open_segment(w, plan, piece, cut);
+    bool done = SUM && !open, go = true;
+    int ring = 0, stage = 0;
+    uint32_t ring_phase = 0, phase = 0;
+    while (go) {
+        Item it = {};
+        Segment s = cut;
+        if (!done && (SUM || walk.next(w, piece, s))) {
+            lin::Rows r;
+            sequence_rows(a, s.n, r);
+            it.row = r.first + (long long)s.from * C;
+            it.rows = min(r.count - s.from * C, (s.to - s.from) * C);
+            it.h = s.h;
+            it.n = s.n;
+            it.chunks = s.to - s.from;
+            const size_t chain = ((size_t)s.n * a.heads + s.h) * kStateFloats;
+            if (SUM) {
+                it.dst = w.sum + (size_t)piece * kStateFloats;
+                done = true;
+            } else {
+                if (s.from) it.src = w.sum + (size_t)(piece - 1) * kStateFloats;
+                else if (s.to < s.of) it.src = w.start + (size_t)piece * kStateFloats;
+                else it.src = a.state_in ? a.state_in + chain : nullptr;
+                if (s.to == s.of && a.state_out) it.dst = a.state_out + chain;
+                // a cut chain's state in front: lin_join_kernel's copy, as state_out may
+                // be state_in
+            }
+        }
+        if (lane == 0) {
+            go = mbar_wait(&sh.item_empty[ring], ring_phase ^ 1, 1) ||
+                 wait_long(sh, &sh.item_empty[ring], ring_phase ^ 1);
+            if (go) {
+                sh.item[ring] = it;
+                mbar_arrive(&sh.item_full[ring]);
+            }
+        }
+        if (++ring == kRing) ring = 0, ring_phase ^= 1;
+        go = __shfl_sync(0xffffffffu, go && it.chunks > 0, 0);
+        if (!go) break;
+        if (lane == 0) {
+            const int hq = a.qk_head(it.h);
+            for (int c = 0; go && c < it.chunks; ++c) {
+                go = mbar_wait(&sh.empty[stage], phase ^ 1, 1) ||
+                     wait_long(sh, &sh.empty[stage], phase ^ 1);
+                if (!go) break;
+                mbar_arrive_expect_tx(&sh.full[stage], SUM ? 2 * kTile : 3 * kTile);
+                unsigned char* dst = sm + stage * kStage;
+                const int row = (int)(it.row + (long long)c * C);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (!SUM)
+                        tma_load_3d(dst + half * (kTile / 2), mq, &sh.full[stage], 64 * half, hq,
+                                    row);
+                    tma_load_3d(dst + kTile + half * (kTile / 2), mk, &sh.full[stage], 64 * half,
+                                hq, row);
+                    tma_load_3d(dst + 2 * kTile + half * (kTile / 2), mv, &sh.full[stage],
+                                64 * half, it.h, row);
+                }
+                if (++stage == 2) stage = 0, phase ^= 1;
+            }
+        }
+        go = __shfl_sync(0xffffffffu, go, 0);
+    }
+    // copies in flight must land before the CTA's memory goes away
+    if (lane == 0 && *(volatile int*)&sh.stop)
+        for (int s = 0; s < 2; ++s)
+            mbar_wait(&sh.full[s], s < stage ? phase : phase ^ 1, 1 << 12);
+}
+
+// The warp that issues the products.  Per chunk: Q S and P V, then the next chunk's
+// Q K^T (over P, which P V has read by then: one warp's products run in order), so that
+// its weights are worked out while this chunk's W is; then K^T W.
+template <bool F16, bool SUM>
+__device__ __forceinline__ void product_role(Shared& sh, unsigned char* sm) {
+    constexpr uint32_t kQK = idesc_16(C, C, !F16, false);
+    constexpr uint32_t kNT = idesc_16(C, D, !F16, true);   // B as it lies: [K][N]
+    constexpr uint32_t kTT = kNT | 1u << 15;               // A too: [K][M]
+    constexpr uint64_t kT = kTile >> 4;                    // in a descriptor's units
+    const uint32_t tmem = uniform(sh.tmem);
+    const uint32_t base = uniform(smem_u32(sm));
+    const uint64_t k_major = make_desc_sw128(base, 16);
+    const uint64_t mn_major = make_desc_sw128(base, kTile / 2);
+    const uint64_t state = mn_major + (kStateTile >> 4);
+    auto qk = [&](int stage) {
+        const uint64_t q = k_major + stage * (kStage >> 4), k = q + kT;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const uint64_t off = (s >> 2) * (kT / 2) + (s & 3) * 2;
+                mma_f16(tmem + kTmemP, q + off, k + off, kQK, s > 0);
+            }
+            mma_commit(&sh.qk_ready);
+        }
+        __syncwarp();
+    };
+    Items items;
+    Item it;
+    int n = 0;  // chunks so far
+    bool have = items.next(sh, it);
+    int left = have ? it.chunks : 0;
+    if (!have) return;
+    if (!SUM) {
+        if (!wait_warp(sh, &sh.full[0], 0)) return;
+        qk(0);
+    }
+    while (left > 0) {
+        const int stage = n & 1;
+        const uint32_t odd = n & 1;
+        const uint64_t q = k_major + stage * (kStage >> 4);
+        const uint64_t q_mn = mn_major + stage * (kStage >> 4), k_mn = q_mn + kT, v_mn = k_mn + kT;
+        if (!SUM) {
+            if (!wait_warp(sh, &sh.s16_ready, odd)) return;
+            if (n && !wait_warp(sh, &sh.o_read, odd ^ 1)) return;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    mma_f16(tmem + kTmemQS, q + (s >> 2) * (kT / 2) + (s & 3) * 2,
+                            state + s * 128, kNT, s > 0);
+            }
+            __syncwarp();
+            if (!wait_warp(sh, &sh.v_checked, odd)) return;
+            if (!wait_warp(sh, &sh.p_ready, odd)) return;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    mma_f16_ta(tmem + kTmemPV, tmem + kTmemP + 8 * s, v_mn + s * 128, kNT, s > 0);
+                mma_commit(&sh.o_ready);
+            }
+            __syncwarp();
+        }
+        if (--left == 0) {
+            have = items.next(sh, it);
+            left = have ? it.chunks : 0;
+            if (!have && *(volatile int*)&sh.stop) return;
+        }
+        if (!SUM && left > 0) {
+            if (!wait_warp(sh, &sh.full[stage ^ 1], (n + 1) >> 1 & 1)) return;
+            qk(stage ^ 1);
+        }
+        if (!wait_warp(sh, &sh.w_ready[odd], n >> 1 & 1)) return;
+        tc_fence_after();
+        if (elect_one()) {
+            // (SUM: two accumulators in turn, as W of the next chunk is ready before this
+            // one's product is read)
+            const uint32_t to = tmem + (SUM && odd ? kTmemPV : kTmemKW);
+#pragma unroll
+            for (int s = 0; s < 8; ++s) mma_f16(to, k_mn + s * 128, v_mn + s * 128, kTT, s > 0);
+#pragma unroll
+            for (int s = 0; s < 8; ++s) mma_f16(to, k_mn + s * 128, q_mn + s * 128, kTT, true);
+            mma_commit(&sh.kw_ready[odd]);
+            mma_commit(&sh.empty[stage]);
+        }
+        __syncwarp();
+        ++n;
+    }
+}
+
+// g of a token as log2 of its decay; 0 for tokens that are not there.
+__device__ __forceinline__ float load_decay(const Args& a, const Item& it, int token) {
+    if (token >= it.rows) return 0.f;
+    return lin::clamp_decay(__ldg(a.g + (it.row + token) * a.g_stride + it.h)) * kLog2e;
+}
+
+// 16-byte piece `c` (of 8) of row r of a 128-row half tile in the 128-byte swizzle.
+__device__ __forceinline__ uint4* piece_of(unsigned char* half_tile, int r, int c) {
+    return reinterpret_cast<uint4*>(half_tile + r * 128 + ((c ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ void store_32(uint16_t* dst, const uint32_t (&u)[8]) {
+    if (reinterpret_cast<uintptr_t>(dst) & 31) {
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+    } else {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst),
+                     "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]),
+                     "r"(u[7])
+                     : "memory");
+    }
+}
+
+// Warps 0..3, a thread a token: the weights P, then the rows of O.
+template <bool F16>
+__device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned char* sm) {
+    const Args& a = w.a;
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const uint32_t row = sh.tmem + ((uint32_t)(warp * 32) << 16);
+    Items items;
+    Item it;
+    int n = 0;
+    uint32_t sync_phase = 0, clean_phase = 0;
+    while (items.next(sh, it)) {
+        float g = load_decay(a, it, t);
+#pragma unroll 1
+        for (int c = 0; c < it.chunks; ++c, ++n) {
+            const uint32_t odd = n & 1;
+            const int there = min(C, it.rows - c * C);
+            // sums within the block: up to the token, and behind it
+            float sum = g, tail = g;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const float up = __shfl_up_sync(0xffffffffu, sum, off);
+                const float down = __shfl_down_sync(0xffffffffu, tail, off);
+                if (lane >= off) sum += up;
+                if (lane + off < 32) tail += down;
+            }
+            tail = __shfl_down_sync(0xffffffffu, tail, 1);
+            if (lane == 31) {
+                tail = 0.f;
+                sh.block[0][odd][warp] = sum;
+            }
+            sh.sum[odd][t] = sum;
+            sh.tail[odd][t] = ex2_approx(tail);
+            if (!sync_warps(sh, &sh.token_sync, sync_phase)) return;
+            if (c + 1 < it.chunks) g = load_decay(a, it, (c + 1) * C + t);
+
+            if (!wait_warp(sh, &sh.qk_ready, odd)) return;
+            tc_fence_after();
+            // upwards: the 16 columns that a block's weights take hold scores of blocks
+            // that have been read
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+                uint32_t p[16] = {};
+                if (b <= warp) {
+                    float x[32];
+                    tmem_ld32(row + kTmemP + 32 * b, x);
+                    if (b == warp) {
+                        const float4* other =
+                            reinterpret_cast<const float4*>(sh.sum[odd] + 32 * b);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 s = other[k];
+                            const float y[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int i = 4 * k + e;
+                                x[i] = i <= lane ? x[i] * ex2_approx(sum - y[e]) : 0.f;
+                            }
+                        }
+                    } else {
+                        const float4* other =
+                            reinterpret_cast<const float4*>(sh.tail[odd] + 32 * b);
+                        float from = sum;  // from the end of block b
+                        for (int i = warp - 1; i > b; --i) from += sh.block[0][odd][i];
+                        from = ex2_approx(from);
+                        const float2 f2 = make_float2(from, from);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 s = other[k];
+                            const float2 lo = mul2(make_float2(x[4 * k], x[4 * k + 1]),
+                                                   mul2(make_float2(s.x, s.y), f2));
+                            const float2 hi = mul2(make_float2(x[4 * k + 2], x[4 * k + 3]),
+                                                   mul2(make_float2(s.z, s.w), f2));
+                            x[4 * k] = lo.x, x[4 * k + 1] = lo.y;
+                            x[4 * k + 2] = hi.x, x[4 * k + 3] = hi.y;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        p[i] = F16 ? pack_f16x2(x[2 * i], x[2 * i + 1])
+                                   : pack_bf16x2(x[2 * i], x[2 * i + 1]);
+                }
+                tmem_st16u(row + kTmemP + 16 * b, p);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            // The rows behind the last token hold another sequence's: no weight reaches
+            // their values, but 0 times infinity would.
+            if (t >= there) {
+                unsigned char* k_tile = sm + (n & 1) * kStage + kTile;
+#pragma unroll 1
+                for (int i = 0; i < 32; ++i)  // K's two halves, V's two halves
+                    *piece_of(k_tile + (i >> 3) * (kTile / 2), t, i & 7) = make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+            }
+            float unit = 1.f;
+            if (F16) {  // (waited for before P goes, so that the phase cannot pass by)
+                if (!wait_warp(sh, &sh.s16_ready, odd)) return;
+                unit = sh.s16_unit[odd];
+            }
+            arrive_warp(&sh.p_ready);
+
+            float decay = sum;
+            for (int i = 0; i < warp; ++i) decay += sh.block[0][odd][i];
+            decay = ex2_approx(decay) * a.scale * unit;
+            const float2 d2 = make_float2(decay, decay), s2 = make_float2(a.scale, a.scale);
+            uint16_t* dst = a.o + (it.row + (long long)c * C + t) * a.o_stride + it.h * D;
+            if (!wait_warp(sh, &sh.o_ready, odd)) return;
+            tc_fence_after();
+            const bool bad = *(volatile int*)&sh.bad[odd];
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                float x[16], y[16];
+                tmem_ld16(row + kTmemQS + 16 * i, x);
+                tmem_ld16(row + kTmemPV + 16 * i, y);
+                tmem_ld_wait();
+                uint32_t u[8];
+                if (bad) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if ((int)(sh.bad_first[odd][4 * i + e / 4] >> (e % 4 * 8) & 255u) <= t)
+                            y[e] = NAN;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float2 o = fma2(d2, make_float2(x[2 * e], x[2 * e + 1]),
+                                          mul2(s2, make_float2(y[2 * e], y[2 * e + 1])));
+                    u[e] = narrow2<F16>(o.x, o.y);
+                }
+                if (t < there) store_32(dst + 16 * i, u);
+            }
+            tc_fence_before();
+            if (bad) {  // clean for the chunk after the next one
+                if (!sync_warps(sh, &sh.token_clean, clean_phase)) return;
+                if (t < D / 4) sh.bad_first[odd][t] = 0xffffffffu;
+                if (t == 0) sh.bad[odd] = 0;
+            }
+            arrive_warp(&sh.o_read);
+        }
+    }
+}
+
+// Infinities and NaN of row r of a half tile of V: the product must not see them, as
+// rows before theirs have weight 0 for them.  What they do to the rows from theirs on is
+// noted for token_role.  Not a path for ordinary inputs.
+template <bool F16>
+__device__ __noinline__ void set_aside(Shared& sh, unsigned char* half_tile, int half, int r,
+                                       int odd) {
+    constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
+    for (int i = 0; i < 64; ++i) {
+        uint16_t* at = reinterpret_cast<uint16_t*>(piece_of(half_tile, r, i >> 3)) + (i & 7);
+        if ((*at & kExp) != kExp) continue;
+        *at = 0;
+        const int col = half * 64 + i, shift = (col & 3) * 8;
+        uint32_t* word = &sh.bad_first[odd][col >> 2];
+        uint32_t was = *(volatile uint32_t*)word;
+        while ((was >> shift & 255u) > (uint32_t)r) {
+            const uint32_t now = (was & ~(255u << shift)) | (uint32_t)r << shift;
+            const uint32_t got = atomicCAS(word, was, now);
+            if (got == was) break;
+            was = got;
+        }
+    }
+    *(volatile int*)&sh.bad[odd] = 1;
+}
+
+// The power of two that brings a largest value `x` to [2^13, 2^14) when divided by, and
+// its inverse.
+__device__ __forceinline__ float unit_of(float x, float& inverse) {
+    const int e = min(max((int)(__float_as_uint(x) >> 23) - 13, 1), 241);
+    inverse = __uint_as_float((uint32_t)(254 - e) << 23);
+    return __uint_as_float((uint32_t)e << 23);
+}
+
+// Warps 4..11, a thread a row i of 64 columns of the state, and likewise a token's 64
+// channels of V.
+template <bool F16, bool SUM>
+__device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned char* sm) {
+    const Args& a = w.a;
+    const int r = threadIdx.x & 127, half = (threadIdx.x >> 7) - 1, warp = r >> 5,
+              lane = threadIdx.x & 31, id = (threadIdx.x >> 5) - 4;
+    const uint32_t row = sh.tmem + ((uint32_t)(warp * 32) << 16) + 64 * half;
+    Items items;
+    Item it;
+    int n = 0;
+    uint32_t half_phase = 0, state_phase = 0;
+    while (items.next(sh, it)) {
+        float s[64];
+        {
+            const float4* from = reinterpret_cast<const float4*>(
+                SUM || !it.src ? nullptr : it.src + r * D + half * 64);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float4 x = from ? __ldcg(from + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                s[4 * i] = x.x, s[4 * i + 1] = x.y, s[4 * i + 2] = x.z, s[4 * i + 3] = x.w;
+            }
+        }
+        float decay = 1.f, unit = 1.f, all = 0.f;  // of the last chunk; of the segment
+        // the last chunk's part of the state
+        auto add = [&] {
+            const uint32_t odd = (n - 1) & 1;
+            if (!wait_warp(sh, &sh.kw_ready[odd], (n - 1) >> 1 & 1)) return false;
+            tc_fence_after();
+            const uint32_t at = row + (SUM && odd ? kTmemPV : kTmemKW);
+            const float2 d2 = make_float2(decay, decay), u2 = make_float2(unit, unit);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float x[16];
+                tmem_ld16(at + 16 * i, x);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float2 add = make_float2(x[2 * e], x[2 * e + 1]);
+                    if (F16) add = mul2(add, u2);
+                    const float2 y = fma2(
+                        d2, make_float2(s[16 * i + 2 * e], s[16 * i + 2 * e + 1]), add);
+                    s[16 * i + 2 * e] = y.x, s[16 * i + 2 * e + 1] = y.y;
+                }
+            }
+            tc_fence_before();
+            return true;
+        };
+        float g = load_decay(a, it, r);
+#pragma unroll 1
+        for (int c = 0; c < it.chunks; ++c, ++n) {
+            const uint32_t odd = n & 1;
+            const int there = min(C, it.rows - c * C);
+            unsigned char* q_half = sm + (n & 1) * kStage + half * (kTile / 2);
+            unsigned char* v_half = q_half + 2 * kTile;
+            // from each token to the end of the chunk
+            float tail = g;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const float down = __shfl_down_sync(0xffffffffu, tail, off);
+                if (lane + off < 32) tail += down;
+            }
+            if (lane == 0) sh.block[1 + half][odd][warp] = tail;
+            tail = __shfl_down_sync(0xffffffffu, tail, 1);
+            if (lane == 31) tail = 0.f;
+            if (!sync_warps(sh, &sh.half_sync[half], half_phase)) return;
+            float total = 0.f;
+#pragma unroll
+            for (int b = 3; b >= 0; --b) {
+                const float x = sh.block[1 + half][odd][b];
+                if (b > warp) tail += x;
+                total += x;
+            }
+            float f = ex2_approx(tail);
+            if (c + 1 < it.chunks) g = load_decay(a, it, (c + 1) * C + r);
+
+            if (!wait_warp(sh, &sh.full[n & 1], n >> 1 & 1)) return;
+            uint4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = r < there ? *piece_of(v_half, r, i) : make_uint4(0, 0, 0, 0);
+            constexpr uint32_t kExp = F16 ? 0x7c007c00u : 0x7f807f80u,
+                               kOne = F16 ? 0x04000400u : 0x00800080u;
+            uint32_t odd_one = 0;  // an exponent of ones carries into the sign's place
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                odd_one |= ((v[i].x & kExp) + kOne) | ((v[i].y & kExp) + kOne) |
+                           ((v[i].z & kExp) + kOne) | ((v[i].w & kExp) + kOne);
+            if (!SUM) {
+                if (odd_one & 0x80008000u) {
+                    set_aside<F16>(sh, v_half, half, r, odd);
+                    fence_async_smem();
+                }
+                arrive_warp(&sh.v_checked);
+                if (c && !add()) return;
+            }
+            float v_unit = 1.f, s_inverse = 1.f;
+            if (F16) {
+                float most_s = 0.f;
+                uint32_t most_v = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)  // (magnitudes in order of their bits)
+                        most_v = __vmaxu2(most_v, x[e] & 0x7fff7fffu);
+                }
+                if (!SUM) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) {
+                        const float x = fabsf(s[i]);
+                        most_s = x < INFINITY ? fmaxf(most_s, x) : most_s;
+                    }
+                }
+                // (positive floats are in order of their bits; infinities and NaN of V are
+                // above 65504 and count as that)
+                const uint32_t v16 = min(max(most_v & 0xffffu, most_v >> 16), 0x7bffu);
+                const uint32_t both_s = __reduce_max_sync(0xffffffffu, __float_as_uint(most_s));
+                const uint32_t both_v = __reduce_max_sync(0xffffffffu, v16);
+                if (lane == 0) {
+                    sh.largest[odd][id] = __uint_as_float(both_s);
+                    sh.largest[odd][8 + id] = __half2float(__ushort_as_half((uint16_t)both_v));
+                }
+                if (!sync_warps(sh, &sh.state_sync, state_phase)) return;
+                float ms = 0.f, mv = 0.f, v_inverse;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    ms = fmaxf(ms, sh.largest[odd][i]);
+                    mv = fmaxf(mv, sh.largest[odd][8 + i]);
+                }
+                const float s_unit = unit_of(ms, s_inverse);
+                v_unit = unit_of(mv, v_inverse);
+                f *= v_inverse;
+                if (!SUM && r == 0 && half == 0) sh.s16_unit[odd] = s_unit;
+            }
+            if (!SUM) {
+                unsigned char* state_half = sm + kStateTile + half * (kTile / 2);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t u[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x = s[8 * i + 2 * e], y = s[8 * i + 2 * e + 1];
+                        if (F16) x *= s_inverse, y *= s_inverse;
+                        u[e] = narrow2<F16>(x, y);
+                    }
+                    *piece_of(state_half, r, i) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+                fence_async_smem();
+                arrive_warp(&sh.s16_ready);
+                if (!wait_warp(sh, &sh.o_ready, odd)) return;  // Q and V are through
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 y = mul2(widen2<F16>(x[e]), make_float2(f, f));
+                    hi[e] = narrow2<F16>(y.x, y.y);
+                    const float2 h = widen2<F16>(hi[e]);
+                    lo[e] = narrow2<F16>(y.x - h.x, y.y - h.y);
+                }
+                *piece_of(v_half, r, i) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *piece_of(q_half, r, i) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            if (SUM && r >= there) {  // (token_role does it otherwise)
+#pragma unroll 1
+                for (int i = 0; i < 8; ++i)
+                    *piece_of(q_half + kTile, r, i) = make_uint4(0, 0, 0, 0);
+            }
+            fence_async_smem();
+            arrive_warp(&sh.w_ready[odd]);
+            if (SUM && c && !add()) return;
+            decay = ex2_approx(total);
+            unit = v_unit;
+            all += total;
+        }
+        if (!add()) return;
+        if (it.dst) {
+            float4* to = reinterpret_cast<float4*>(it.dst + r * D + half * 64);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                to[i] = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+        }
+        if (SUM && r == 0 && half == 0) w.log_sum[blockIdx.x] = all;
+    }
+}
+
+template <bool F16, bool SUM>
+__global__ void __launch_bounds__(kThreads, 1)
+lin_prefill_kernel(Work w, const __grid_constant__ CUtensorMap mq,
+                   const __grid_constant__ CUtensorMap mk,
+                   const __grid_constant__ CUtensorMap mv) {
+    extern __shared__ __align__(1024) unsigned char sm[];
+    Shared& sh = *reinterpret_cast<Shared*>(sm + kSharedOff);
+    const int warp = threadIdx.x >> 5;
+    if (smem_u32(sm) & 1023u) {  // the swizzle goes by address bits
+        if (threadIdx.x == 0) atomicOr(&g_lin_status, STATUS_SMEM_ALIGN);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        sh.stop = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], 1);
+            sh.bad[i] = 0;
+        }
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&sh.item_full[i], 1);
+            mbar_init(&sh.item_empty[i], SUM ? 9 : 13);
+        }
+        mbar_init(&sh.qk_ready, 1);
+        mbar_init(&sh.p_ready, 4);
+        mbar_init(&sh.o_ready, 1);
+        mbar_init(&sh.o_read, 4);
+        mbar_init(&sh.s16_ready, 8);
+        mbar_init(&sh.v_checked, 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.w_ready[i], 8);
+            mbar_init(&sh.kw_ready[i], 1);
+            mbar_init(&sh.half_sync[i], 4);
+        }
+        mbar_init(&sh.token_sync, 4);
+        mbar_init(&sh.token_clean, 4);
+        mbar_init(&sh.state_sync, 8);
+        fence_mbar_init();
+        prefetch_tmap(&mq);
+        prefetch_tmap(&mk);
+        prefetch_tmap(&mv);
+    }
+    if (threadIdx.x < 2 * (D / 4)) (&sh.bad_first[0][0])[threadIdx.x] = 0xffffffffu;
+    if (warp == 13) tmem_alloc(&sh.tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_wait();
+    if (warp == 12) {
+        copy_role<SUM>(w, sh, sm, &mq, &mk, &mv);
+    } else if (warp == 13) {
+        product_role<F16, SUM>(sh, sm);
+    } else if (warp >= 4 && warp < 12) {
+        state_role<F16, SUM>(w, sh, sm);
+    } else if (warp < 4) {
+        if (!SUM) token_role<F16>(w, sh, sm);
+    } else if (!SUM && w.a.cu) {
+        const Args& a = w.a;
+        const int lane = threadIdx.x & 31;
+        if (blockIdx.x == 0 && !warp_offsets_ok(a.cu, a.n_seqs, a.t) && lane == 0)
+            atomicOr(&g_lin_status, STATUS_BAD_CU_SEQLENS);
+        // states of sequences without tokens
+        for (int n0 = 0; a.state_out && a.state_out != a.state_in && n0 < a.n_seqs; n0 += 32) {
+            lin::Rows rows;
+            unsigned empty = __ballot_sync(0xffffffffu, n0 + lane < a.n_seqs &&
+                                                            sequence_rows(a, n0 + lane, rows) &&
+                                                            rows.count == 0);
+            for (; empty; empty &= empty - 1) {
+                const long long chain = (long long)(n0 + __ffs(empty) - 1) * a.heads;
+                for (int h = 0; h < a.heads; ++h) {
+                    if ((chain + h) % gridDim.x != blockIdx.x) continue;
+                    const size_t at = (size_t)(chain + h) * kStateFloats;
+                    for (int i = lane; i < kStateFloats / 4; i += 32)
+                        reinterpret_cast<float4*>(a.state_out + at)[i] =
+                            a.state_in ? reinterpret_cast<const float4*>(a.state_in + at)[i]
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 13) tmem_dealloc(sh.tmem, 512);
+}
+
+// States in front of the parts of chains that are cut: from each chain's beginning, S
+// <- 2^log_sum S + sum through its pieces.  Four floats a thread.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) lin_join_kernel(Work w) {
+    const Args& a = w.a;
+    pdl_wait();
+    const Plan p = make_plan(w);
+    const int i = blockIdx.x;
+    Segment s;
+    if (!open_segment(w, p, i, s) || s.from) return;
+    // pieces whose last segment is this chain's and open
+    int last = i + padded(s.of) - 2;
+    if (p.kind == kEven) {
+        const long long chain_end = (long long)(i + 1) * p.piece + (s.of - s.to);
+        last = (int)((chain_end - 1) / p.piece) - 1;
+    }
+    const int at = blockIdx.y * kJoinThreads + threadIdx.x;  // of the state's float4s
+    const size_t chain = ((size_t)s.n * a.heads + s.h) * kStateFloats;
+    float4 x = a.state_in ? __ldcg(reinterpret_cast<const float4*>(a.state_in + chain) + at)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+    reinterpret_cast<float4*>(w.start + (size_t)i * kStateFloats)[at] = x;
+    float4* sums = reinterpret_cast<float4*>(w.sum) + at;
+#pragma unroll 4
+    for (int k = i; k <= last; ++k) {
+        const float4 add = __ldcg(sums + (size_t)k * (kStateFloats / 4));
+        const float d = exp2f(__ldcg(w.log_sum + k));
+        x.x = fmaf(d, x.x, add.x);
+        x.y = fmaf(d, x.y, add.y);
+        x.z = fmaf(d, x.z, add.z);
+        x.w = fmaf(d, x.w, add.w);
+        sums[(size_t)k * (kStateFloats / 4)] = x;
+    }
+}
+
+// Pieces that a call has at most.
+int most_pieces(long long rows, int n_seqs, int heads) {
+    return (int)std::min<long long>(kSms, (rows / C + n_seqs) * heads);
+}
 
 }  // namespace
 
@@ -13,14 +1030,56 @@ cudaError_t status_word_lin(unsigned** word) {
 }
 
 size_t lin_chunked_workspace_bytes(long long rows, int n_seqs, int heads) {
-    (void)rows, (void)n_seqs, (void)heads;
-    return 256;
+    return (size_t)most_pieces(rows, n_seqs, heads) * (2 * kStateFloats + 4) * sizeof(float);
 }
 
-kda_status launch_lin_chunked(const lin::Args& a, bool f16, void* workspace, cudaStream_t s) {
-    (void)workspace;
-    launch_lin_walk(a, f16, LinSnaps{}, s);
-    return launch_result("kda_lin_prefill");
+kda_status launch_lin_chunked(const Args& a, bool f16, void* workspace, cudaStream_t s) {
+    const char* fn = "kda_lin_prefill";
+    const long long rows = a.cu ? a.t : (long long)a.t_pad * a.n_seqs;
+    const int sms = sm_count();
+    KDA_REQUIRE(sms > 0, KDA_ERR_CUDA, "%s: no device", fn);
+    Work w = {a};
+    const int slots = most_pieces(rows, a.n_seqs, a.heads);
+    w.pieces = std::min(slots, sms);
+    w.sum = static_cast<float*>(workspace);
+    w.start = w.sum + (size_t)slots * kStateFloats;
+    w.log_sum = w.start + (size_t)slots * kStateFloats;
+    CUtensorMap mq, mk, mv;
+    KDA_REQUIRE(tma_map_heads(&mq, a.q, a.qk_heads, rows, a.q_stride, 1, C, f16) &&
+                    tma_map_heads(&mk, a.k, a.qk_heads, rows, a.k_stride, 1, C, f16) &&
+                    tma_map_heads(&mv, a.v, a.heads, rows, a.v_stride, 1, C, f16),
+                KDA_ERR_CUDA, "%s: cannot describe the inputs to the copy engine", fn);
+    // Whether chains may be cut: for packed rows the lengths are on the device.
+    const long long chains = (long long)a.n_seqs * a.heads;
+    const long long longest = (a.t + C - 1) / C;
+    const long long pads = (longest + kLeastPiece - 1) / kLeastPiece;
+    bool cut;
+    int grid = w.pieces;
+    if (a.cu) {
+        cut = longest > kLeastPiece || chains > w.pieces;
+    } else if (pads * chains <= w.pieces) {
+        cut = pads > 1;
+        grid = (int)(pads * chains);
+    } else {
+        cut = !(chains >= 2LL * w.pieces && 10 * longest * w.pieces <= 6 * longest * chains);
+    }
+    auto kernel = f16 ? lin_prefill_kernel<true, false> : lin_prefill_kernel<false, false>;
+    auto sums = f16 ? lin_prefill_kernel<true, true> : lin_prefill_kernel<false, true>;
+    for (auto k : {kernel, sums}) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)kSmemBytes);
+        if (e != cudaSuccess) {
+            set_error("%s: cannot reserve shared memory: %s", fn, cudaGetErrorString(e));
+            return KDA_ERR_CUDA;
+        }
+    }
+    if (cut) {
+        launch_pdl(sums, dim3(grid), dim3(kThreads), kSmemBytes, s, w, mq, mk, mv);
+        launch_pdl(lin_join_kernel, dim3(grid, kStateFloats / 4 / kJoinThreads),
+                   dim3(kJoinThreads), 0, s, w);
+    }
+    launch_pdl(kernel, dim3(grid), dim3(kThreads), kSmemBytes, s, w, mq, mk, mv);
+    return launch_result(fn);
 }
 
 }  // namespace kda
