@@ -32,6 +32,7 @@
 // segments.  See Plan.
 #include <algorithm>
 #include <cmath>
+#include <cstddef>
 
 #include "f32x2.h"
 #include "lin_attn.h"
@@ -252,7 +253,7 @@ __device__ __forceinline__ bool open_segment(const Work& w, const Plan& p, int i
 
 // ---------------------------------------------------------------- the kernel
 
-// Warps: 0..3 P and O, 4..11 the state and W, 12 copies, 13 products, 14 the rest.
+// Warps: 0..3 P, 4..11 W, O and the state, 12 copies, 13 products, 14 the rest.
 constexpr int kThreads = 480;
 constexpr uint32_t kTile = C * D * 2;         // 32 KB
 constexpr uint32_t kStage = 3 * kTile;        // Q, K, V; later lo, K, hi
@@ -270,25 +271,31 @@ struct Item {
 
 struct Shared {
     uint64_t full[2], empty[2];
-    uint64_t p_ready, o_ready, o_read, s16_ready, qk_ready, v_checked;
+    uint64_t qk_ready, p_ready, v_checked, pv_ready, s16_ready, qs_ready, o_read;
     uint64_t w_ready[2], kw_ready[2];  // by chunk parity: SUM's may be a chunk apart
-    uint64_t token_sync, token_clean, half_sync[2], state_sync;
+    uint64_t token_sync, half_sync[2], state_sync;
     uint64_t item_full[kRing], item_empty[kRing];
     Item item[kRing];
     uint32_t tmem;
     int stop;
-    float sum[2][C];    // of g (log2) within blocks of 32 tokens, up to each token
-    float tail[2][C];   // decay from each token to the end of its block
-    float block[3][2][4];  // sums of blocks, for warps 0..3, 4..7, 8..11
+    // of g, as log2 of decays, within blocks of 32 tokens: less the sum up to each token,
+    // the sum behind it
+    alignas(16) float sum[C];
+    alignas(16) float tail[2][C];
+    float front[C];        // scale * the decay from the chunk's start to each token
+    float later[2][4];     // of the blocks behind each block
+    float total[2];        // of the chunk
+    float block[2][2][4];  // sums of blocks (SUM: for warps 4..7, 8..11)
     float largest[2][16];  // FP16: of S and of V, each warp's
-    float s16_unit[2];     // FP16: what one unit of the state's copy stands for
     // V's infinities and NaN, by chunk parity: each column's first token (255: none)
     uint32_t bad_first[2][D / 4];
-    int bad[2];
+    int bad[2], bad_seen[2];  // whether there are any; warps that are through with them
 };
 constexpr uint32_t kSharedOff = kStateTile + kTile;
 constexpr uint32_t kSmemBytes = kSharedOff + sizeof(Shared);
 static_assert(kSmemBytes <= 232448, "shared memory");
+static_assert(offsetof(Shared, sum) % 16 == 0 && offsetof(Shared, tail) % 16 == 0 &&
+                  kSharedOff % 16 == 0, "read by 16 bytes");
 
 // Waits with an end: a phase that does not come within 2^35 clocks (some 17
 // seconds), or another role's giving up, ends the kernel with an error status.
@@ -420,9 +427,12 @@ __device__ __forceinline__ void copy_role(const Work& w, Shared& sh, unsigned ch
             mbar_wait(&sh.full[s], s < stage ? phase : phase ^ 1, 1 << 12);
 }
 
-// The warp that issues the products.  Per chunk: Q S and P V, then the next chunk's
-// Q K^T (over P, which P V has read by then: one warp's products run in order), so that
-// its weights are worked out while this chunk's W is; then K^T W.
+// The warp that issues the products: of chunk c Q S and P V, the next chunk's Q K^T, so
+// that its weights are worked out while this chunk's W is, and K^T W.  The products of
+// one warp run in the order of their issue, so Q K^T may follow P V, over whose P it is
+// written.  (In a fixed order: taking whichever has its operands costs more than it
+// gains, as the compiler then moves every descriptor into uniform registers again, 66
+// cycles a product of 16 k against 130 to 170.)
 template <bool F16, bool SUM>
 __device__ __forceinline__ void product_role(Shared& sh, unsigned char* sm) {
     constexpr uint32_t kQK = idesc_16(C, C, !F16, false);
@@ -449,28 +459,28 @@ __device__ __forceinline__ void product_role(Shared& sh, unsigned char* sm) {
     };
     Items items;
     Item it;
-    int n = 0;  // chunks so far
-    bool have = items.next(sh, it);
-    int left = have ? it.chunks : 0;
-    if (!have) return;
+    if (!items.next(sh, it)) return;
+    int left = uniform(it.chunks);
     if (!SUM) {
         if (!wait_warp(sh, &sh.full[0], 0)) return;
         qk(0);
     }
-    while (left > 0) {
+    for (int n = 0; left > 0; ++n) {
         const int stage = n & 1;
-        const uint32_t odd = n & 1;
+        const uint32_t odd = n & 1, pair = n >> 1 & 1;
         const uint64_t q = k_major + stage * (kStage >> 4);
         const uint64_t q_mn = mn_major + stage * (kStage >> 4), k_mn = q_mn + kT, v_mn = k_mn + kT;
         if (!SUM) {
-            if (!wait_warp(sh, &sh.s16_ready, odd)) return;
             if (n && !wait_warp(sh, &sh.o_read, odd ^ 1)) return;
+            if (!wait_warp(sh, &sh.s16_ready, odd)) return;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
-                    mma_f16(tmem + kTmemQS, q + (s >> 2) * (kT / 2) + (s & 3) * 2,
-                            state + s * 128, kNT, s > 0);
+                    mma_f16(tmem + kTmemQS, q + (s >> 2) * (kT / 2) + (s & 3) * 2, state + s * 128,
+                            kNT, s > 0);
+                mma_commit(&sh.qs_ready);
+                mbar_arrive(&sh.qs_ready);  // passes on what s16_ready brought
             }
             __syncwarp();
             if (!wait_warp(sh, &sh.v_checked, odd)) return;
@@ -480,24 +490,25 @@ __device__ __forceinline__ void product_role(Shared& sh, unsigned char* sm) {
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
                     mma_f16_ta(tmem + kTmemPV, tmem + kTmemP + 8 * s, v_mn + s * 128, kNT, s > 0);
-                mma_commit(&sh.o_ready);
+                mma_commit(&sh.pv_ready);
+                mbar_arrive(&sh.pv_ready);  // and p_ready and v_checked
             }
             __syncwarp();
         }
         if (--left == 0) {
-            have = items.next(sh, it);
-            left = have ? it.chunks : 0;
-            if (!have && *(volatile int*)&sh.stop) return;
+            items.next(sh, it);
+            if (*(volatile int*)&sh.stop) return;
+            left = uniform(it.chunks);
         }
         if (!SUM && left > 0) {
             if (!wait_warp(sh, &sh.full[stage ^ 1], (n + 1) >> 1 & 1)) return;
             qk(stage ^ 1);
         }
-        if (!wait_warp(sh, &sh.w_ready[odd], n >> 1 & 1)) return;
+        if (!wait_warp(sh, &sh.w_ready[odd], pair)) return;
         tc_fence_after();
         if (elect_one()) {
             // (SUM: two accumulators in turn, as W of the next chunk is ready before this
-            // one's product is read)
+            // one's product is read; otherwise the last one's was read before S was there)
             const uint32_t to = tmem + (SUM && odd ? kTmemPV : kTmemKW);
 #pragma unroll
             for (int s = 0; s < 8; ++s) mma_f16(to, k_mn + s * 128, v_mn + s * 128, kTT, s > 0);
@@ -507,15 +518,15 @@ __device__ __forceinline__ void product_role(Shared& sh, unsigned char* sm) {
             mma_commit(&sh.empty[stage]);
         }
         __syncwarp();
-        ++n;
     }
 }
 
-// g of a token as log2 of its decay; 0 for tokens that are not there.
-__device__ __forceinline__ float load_decay(const Args& a, const Item& it, int token) {
-    if (token >= it.rows) return 0.f;
-    return lin::clamp_decay(__ldg(a.g + (it.row + token) * a.g_stride + it.h)) * kLog2e;
+// g of a token as it is, 0 for tokens that are not there; and as log2 of the decay.  The
+// load is a chunk ahead of its use, and nothing is done with it before.
+__device__ __forceinline__ float load_g(const Args& a, const Item& it, int token) {
+    return token < it.rows ? __ldg(a.g + (it.row + token) * a.g_stride + it.h) : 0.f;
 }
+__device__ __forceinline__ float log2_decay(float g) { return lin::clamp_decay(g) * kLog2e; }
 
 // 16-byte piece `c` (of 8) of row r of a 128-row half tile in the 128-byte swizzle.
 __device__ __forceinline__ uint4* piece_of(unsigned char* half_tile, int r, int c) {
@@ -534,7 +545,7 @@ __device__ __forceinline__ void store_32(uint16_t* dst, const uint32_t (&u)[8]) 
     }
 }
 
-// Warps 0..3, a thread a token: the weights P, then the rows of O.
+// Warps 0..3, a thread a token: a chunk's weights P, and the decays that state_role takes.
 template <bool F16>
 __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned char* sm) {
     const Args& a = w.a;
@@ -543,13 +554,13 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
     Items items;
     Item it;
     int n = 0;
-    uint32_t sync_phase = 0, clean_phase = 0;
+    uint32_t sync_phase = 0;
     while (items.next(sh, it)) {
-        float g = load_decay(a, it, t);
+        float next_g = load_g(a, it, t);
 #pragma unroll 1
         for (int c = 0; c < it.chunks; ++c, ++n) {
             const uint32_t odd = n & 1;
-            const int there = min(C, it.rows - c * C);
+            const float g = log2_decay(next_g);
             // sums within the block: up to the token, and behind it
             float sum = g, tail = g;
 #pragma unroll
@@ -564,58 +575,53 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
                 tail = 0.f;
                 sh.block[0][odd][warp] = sum;
             }
-            sh.sum[odd][t] = sum;
-            sh.tail[odd][t] = ex2_approx(tail);
+            sh.sum[t] = -sum;
+            sh.tail[odd][t] = tail;
             if (!sync_warps(sh, &sh.token_sync, sync_phase)) return;
-            if (c + 1 < it.chunks) g = load_decay(a, it, (c + 1) * C + t);
+            next_g = load_g(a, it, (c + 1) * C + t);
+            float before = 0.f, behind = 0.f, total = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x = sh.block[0][odd][i];
+                if (i < warp) before += x;
+                if (i > warp) behind += x;
+                total += x;
+            }
+            if (lane == 0) sh.later[odd][warp] = behind;
+            if (t == 0) sh.total[odd] = total;
 
             if (!wait_warp(sh, &sh.qk_ready, odd)) return;
             tc_fence_after();
-            // upwards: the 16 columns that a block's weights take hold scores of blocks
-            // that have been read
+            // A block of 32 columns a step, upwards: the 16 columns that its weights take
+            // hold scores that have been read.  (One rolled loop for blocks on and below
+            // the diagonal: what all roles run has to stay in the instruction cache.)
 #pragma unroll 1
             for (int b = 0; b < 4; ++b) {
                 uint32_t p[16] = {};
                 if (b <= warp) {
                     float x[32];
                     tmem_ld32(row + kTmemP + 32 * b, x);
-                    if (b == warp) {
-                        const float4* other =
-                            reinterpret_cast<const float4*>(sh.sum[odd] + 32 * b);
-                        tmem_ld_wait();
+                    float from = sum;  // from the end of block b; on the diagonal in all
+#pragma unroll 1
+                    for (int k = warp - 1; k > b; --k) from += sh.block[0][odd][k];
+                    const float4* other = reinterpret_cast<const float4*>(
+                        (b == warp ? sh.sum : sh.tail[odd]) + 32 * b);
+                    const int last = b == warp ? lane : 31;
+                    tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float4 s = other[k];
-                            const float y[4] = {s.x, s.y, s.z, s.w};
+                    for (int k = 0; k < 8; ++k) {
+                        const float4 s = other[k];
+                        const float y[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int i = 4 * k + e;
-                                x[i] = i <= lane ? x[i] * ex2_approx(sum - y[e]) : 0.f;
-                            }
-                        }
-                    } else {
-                        const float4* other =
-                            reinterpret_cast<const float4*>(sh.tail[odd] + 32 * b);
-                        float from = sum;  // from the end of block b
-                        for (int i = warp - 1; i > b; --i) from += sh.block[0][odd][i];
-                        from = ex2_approx(from);
-                        const float2 f2 = make_float2(from, from);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float4 s = other[k];
-                            const float2 lo = mul2(make_float2(x[4 * k], x[4 * k + 1]),
-                                                   mul2(make_float2(s.x, s.y), f2));
-                            const float2 hi = mul2(make_float2(x[4 * k + 2], x[4 * k + 3]),
-                                                   mul2(make_float2(s.z, s.w), f2));
-                            x[4 * k] = lo.x, x[4 * k + 1] = lo.y;
-                            x[4 * k + 2] = hi.x, x[4 * k + 3] = hi.y;
+                        for (int e = 0; e < 4; ++e) {
+                            const float d = ex2_approx(from + y[e]);
+                            x[4 * k + e] = 4 * k + e <= last ? x[4 * k + e] * d : 0.f;
                         }
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        p[i] = F16 ? pack_f16x2(x[2 * i], x[2 * i + 1])
-                                   : pack_bf16x2(x[2 * i], x[2 * i + 1]);
+                    for (int k = 0; k < 16; ++k)
+                        p[k] = F16 ? pack_f16x2(x[2 * k], x[2 * k + 1])
+                                   : pack_bf16x2(x[2 * k], x[2 * k + 1]);
                 }
                 tmem_st16u(row + kTmemP + 16 * b, p);
             }
@@ -623,71 +629,45 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
             tc_fence_before();
             // The rows behind the last token hold another sequence's: no weight reaches
             // their values, but 0 times infinity would.
-            if (t >= there) {
+            if (t >= it.rows - c * C) {
                 unsigned char* k_tile = sm + (n & 1) * kStage + kTile;
 #pragma unroll 1
                 for (int i = 0; i < 32; ++i)  // K's two halves, V's two halves
                     *piece_of(k_tile + (i >> 3) * (kTile / 2), t, i & 7) = make_uint4(0, 0, 0, 0);
                 fence_async_smem();
             }
-            float unit = 1.f;
-            if (F16) {  // (waited for before P goes, so that the phase cannot pass by)
-                if (!wait_warp(sh, &sh.s16_ready, odd)) return;
-                unit = sh.s16_unit[odd];
-            }
+            // state_role is through with the last chunk's decays (and P V would wait for
+            // the same)
+            if (n && !wait_warp(sh, &sh.o_read, odd ^ 1)) return;
+            sh.front[t] = ex2_approx(before + sum) * a.scale;
             arrive_warp(&sh.p_ready);
-
-            float decay = sum;
-            for (int i = 0; i < warp; ++i) decay += sh.block[0][odd][i];
-            decay = ex2_approx(decay) * a.scale * unit;
-            const float2 d2 = make_float2(decay, decay), s2 = make_float2(a.scale, a.scale);
-            uint16_t* dst = a.o + (it.row + (long long)c * C + t) * a.o_stride + it.h * D;
-            if (!wait_warp(sh, &sh.o_ready, odd)) return;
-            tc_fence_after();
-            const bool bad = *(volatile int*)&sh.bad[odd];
-#pragma unroll 1
-            for (int i = 0; i < 8; ++i) {
-                float x[16], y[16];
-                tmem_ld16(row + kTmemQS + 16 * i, x);
-                tmem_ld16(row + kTmemPV + 16 * i, y);
-                tmem_ld_wait();
-                uint32_t u[8];
-                if (bad) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if ((int)(sh.bad_first[odd][4 * i + e / 4] >> (e % 4 * 8) & 255u) <= t)
-                            y[e] = NAN;
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float2 o = fma2(d2, make_float2(x[2 * e], x[2 * e + 1]),
-                                          mul2(s2, make_float2(y[2 * e], y[2 * e + 1])));
-                    u[e] = narrow2<F16>(o.x, o.y);
-                }
-                if (t < there) store_32(dst + 16 * i, u);
-            }
-            tc_fence_before();
-            if (bad) {  // clean for the chunk after the next one
-                if (!sync_warps(sh, &sh.token_clean, clean_phase)) return;
-                if (t < D / 4) sh.bad_first[odd][t] = 0xffffffffu;
-                if (t == 0) sh.bad[odd] = 0;
-            }
-            arrive_warp(&sh.o_read);
         }
     }
 }
 
+// NaN in the columns of half a row whose V was not finite at this token or before.
+template <bool F16>
+__device__ __noinline__ void put_nan(uint16_t* o, const uint32_t* bad_first, int half, int t) {
+#pragma unroll 1
+    for (int j = 64 * half; j < 64 * half + 64; ++j)
+        if ((int)(bad_first[j >> 2] >> (j & 3) * 8 & 255u) <= t) o[j] = F16 ? 0x7e00 : 0x7fc0;
+}
+
 // Infinities and NaN of row r of a half tile of V: the product must not see them, as
 // rows before theirs have weight 0 for them.  What they do to the rows from theirs on is
-// noted for token_role.  Not a path for ordinary inputs.
+// noted for the rows of O; put_back_nan brings them into W.  Returns their columns.  Not a
+// path for ordinary inputs.
 template <bool F16>
-__device__ __noinline__ void set_aside(Shared& sh, unsigned char* half_tile, int half, int r,
-                                       int odd) {
+__device__ __noinline__ unsigned long long set_aside(Shared& sh, unsigned char* half_tile,
+                                                     int half, int r, int odd) {
     constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
+    unsigned long long found = 0;
+#pragma unroll 1
     for (int i = 0; i < 64; ++i) {
         uint16_t* at = reinterpret_cast<uint16_t*>(piece_of(half_tile, r, i >> 3)) + (i & 7);
         if ((*at & kExp) != kExp) continue;
         *at = 0;
+        found |= 1ull << i;
         const int col = half * 64 + i, shift = (col & 3) * 8;
         uint32_t* word = &sh.bad_first[odd][col >> 2];
         uint32_t was = *(volatile uint32_t*)word;
@@ -699,6 +679,16 @@ __device__ __noinline__ void set_aside(Shared& sh, unsigned char* half_tile, int
         }
     }
     *(volatile int*)&sh.bad[odd] = 1;
+    return found;
+}
+template <bool F16>
+__device__ __noinline__ void put_back_nan(unsigned char* half_tile, int r,
+                                          unsigned long long found) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (found >> i & 1)
+            reinterpret_cast<uint16_t*>(piece_of(half_tile, r, i >> 3))[i & 7] =
+                F16 ? 0x7e00 : 0x7fc0;
 }
 
 // The power of two that brings a largest value `x` to [2^13, 2^14) when divided by, and
@@ -710,7 +700,7 @@ __device__ __forceinline__ float unit_of(float x, float& inverse) {
 }
 
 // Warps 4..11, a thread a row i of 64 columns of the state, and likewise a token's 64
-// channels of V.
+// channels of V and O.
 template <bool F16, bool SUM>
 __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned char* sm) {
     const Args& a = w.a;
@@ -757,65 +747,73 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
             tc_fence_before();
             return true;
         };
-        float g = load_decay(a, it, r);
+        float next_g = SUM ? load_g(a, it, r) : 0.f;
 #pragma unroll 1
         for (int c = 0; c < it.chunks; ++c, ++n) {
             const uint32_t odd = n & 1;
             const int there = min(C, it.rows - c * C);
             unsigned char* q_half = sm + (n & 1) * kStage + half * (kTile / 2);
             unsigned char* v_half = q_half + 2 * kTile;
-            // from each token to the end of the chunk
-            float tail = g;
+            float f = 0.f, total = 0.f;  // decays from the token on, and of the chunk
+            if (SUM) {
+                float tail = log2_decay(next_g);
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const float down = __shfl_down_sync(0xffffffffu, tail, off);
-                if (lane + off < 32) tail += down;
-            }
-            if (lane == 0) sh.block[1 + half][odd][warp] = tail;
-            tail = __shfl_down_sync(0xffffffffu, tail, 1);
-            if (lane == 31) tail = 0.f;
-            if (!sync_warps(sh, &sh.half_sync[half], half_phase)) return;
-            float total = 0.f;
+                for (int off = 1; off < 32; off <<= 1) {
+                    const float down = __shfl_down_sync(0xffffffffu, tail, off);
+                    if (lane + off < 32) tail += down;
+                }
+                if (lane == 0) sh.block[half][odd][warp] = tail;
+                tail = __shfl_down_sync(0xffffffffu, tail, 1);
+                if (lane == 31) tail = 0.f;
+                if (!sync_warps(sh, &sh.half_sync[half], half_phase)) return;
 #pragma unroll
-            for (int b = 3; b >= 0; --b) {
-                const float x = sh.block[1 + half][odd][b];
-                if (b > warp) tail += x;
-                total += x;
+                for (int b = 3; b >= 0; --b) {
+                    const float x = sh.block[half][odd][b];
+                    if (b > warp) tail += x;
+                    total += x;
+                }
+                f = ex2_approx(tail);
+                next_g = load_g(a, it, (c + 1) * C + r);
             }
-            float f = ex2_approx(tail);
-            if (c + 1 < it.chunks) g = load_decay(a, it, (c + 1) * C + r);
-
             if (!wait_warp(sh, &sh.full[n & 1], n >> 1 & 1)) return;
-            uint4 v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = r < there ? *piece_of(v_half, r, i) : make_uint4(0, 0, 0, 0);
+            if (SUM && r >= there) {  // (token_role does it otherwise)
+#pragma unroll 1
+                for (int i = 0; i < 8; ++i) {
+                    *piece_of(q_half + kTile, r, i) = make_uint4(0, 0, 0, 0);
+                    *piece_of(v_half, r, i) = make_uint4(0, 0, 0, 0);
+                }
+            }
             constexpr uint32_t kExp = F16 ? 0x7c007c00u : 0x7f807f80u,
                                kOne = F16 ? 0x04000400u : 0x00800080u;
-            uint32_t odd_one = 0;  // an exponent of ones carries into the sign's place
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                odd_one |= ((v[i].x & kExp) + kOne) | ((v[i].y & kExp) + kOne) |
-                           ((v[i].z & kExp) + kOne) | ((v[i].w & kExp) + kOne);
+            uint32_t carry = 0;   // an exponent of ones carries into the sign's place
+            uint32_t most_v = 0;  // FP16: magnitudes are in order of their bits
+            if (!SUM || F16) {
+#pragma unroll 4
+                for (int i = 0; i < 8; ++i) {
+                    const uint4 v = *piece_of(v_half, r, i);
+                    carry |= ((v.x & kExp) + kOne) | ((v.y & kExp) + kOne) |
+                             ((v.z & kExp) + kOne) | ((v.w & kExp) + kOne);
+                    if (F16) {
+                        most_v = __vmaxu2(most_v, v.x & 0x7fff7fffu);
+                        most_v = __vmaxu2(most_v, v.y & 0x7fff7fffu);
+                        most_v = __vmaxu2(most_v, v.z & 0x7fff7fffu);
+                        most_v = __vmaxu2(most_v, v.w & 0x7fff7fffu);
+                    }
+                }
+                if (r >= there) most_v = 0;
+            }
+            unsigned long long found = 0;
             if (!SUM) {
-                if (odd_one & 0x80008000u) {
-                    set_aside<F16>(sh, v_half, half, r, odd);
+                if ((carry & 0x80008000u) && r < there) {
+                    found = set_aside<F16>(sh, v_half, half, r, odd);
                     fence_async_smem();
                 }
                 arrive_warp(&sh.v_checked);
                 if (c && !add()) return;
             }
-            float v_unit = 1.f, s_inverse = 1.f;
+            float v_unit = 1.f, v_inverse = 1.f, s_unit = 1.f, s_inverse = 1.f;
             if (F16) {
                 float most_s = 0.f;
-                uint32_t most_v = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)  // (magnitudes in order of their bits)
-                        most_v = __vmaxu2(most_v, x[e] & 0x7fff7fffu);
-                }
                 if (!SUM) {
 #pragma unroll
                     for (int i = 0; i < 64; ++i) {
@@ -833,16 +831,15 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
                     sh.largest[odd][8 + id] = __half2float(__ushort_as_half((uint16_t)both_v));
                 }
                 if (!sync_warps(sh, &sh.state_sync, state_phase)) return;
-                float ms = 0.f, mv = 0.f, v_inverse;
+                float ms = 0.f, mv = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     ms = fmaxf(ms, sh.largest[odd][i]);
                     mv = fmaxf(mv, sh.largest[odd][8 + i]);
                 }
-                const float s_unit = unit_of(ms, s_inverse);
+                s_unit = unit_of(ms, s_inverse);
                 v_unit = unit_of(mv, v_inverse);
-                f *= v_inverse;
-                if (!SUM && r == 0 && half == 0) sh.s16_unit[odd] = s_unit;
+                if (SUM) f *= v_inverse;
             }
             if (!SUM) {
                 unsigned char* state_half = sm + kStateTile + half * (kTile / 2);
@@ -859,11 +856,18 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
                 }
                 fence_async_smem();
                 arrive_warp(&sh.s16_ready);
-                if (!wait_warp(sh, &sh.o_ready, odd)) return;  // Q and V are through
+                // V and Q are through
+                if (!wait_warp(sh, &sh.pv_ready, odd)) return;
+                if (!wait_warp(sh, &sh.qs_ready, odd)) return;
+                total = sh.total[odd];
+                f = ex2_approx(sh.tail[odd][r] + sh.later[odd][warp]);
+                if (F16) f *= v_inverse;
             }
-#pragma unroll
+#pragma unroll 2
             for (int i = 0; i < 8; ++i) {
-                const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                uint4* at = piece_of(v_half, r, i);
+                const uint4 v = *at;
+                const uint32_t x[4] = {v.x, v.y, v.z, v.w};
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -872,17 +876,69 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
                     const float2 h = widen2<F16>(hi[e]);
                     lo[e] = narrow2<F16>(y.x - h.x, y.y - h.y);
                 }
-                *piece_of(v_half, r, i) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *at = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 *piece_of(q_half, r, i) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
-            if (SUM && r >= there) {  // (token_role does it otherwise)
-#pragma unroll 1
-                for (int i = 0; i < 8; ++i)
-                    *piece_of(q_half + kTile, r, i) = make_uint4(0, 0, 0, 0);
-            }
+            if (!SUM && found) put_back_nan<F16>(v_half, r, found);
             fence_async_smem();
             arrive_warp(&sh.w_ready[odd]);
             if (SUM && c && !add()) return;
+            if (!SUM) {
+                // the rows of O, while K^T W is under way
+                tc_fence_after();
+                const float front = sh.front[r] * (F16 ? s_unit : 1.f);
+                const float2 d2 = make_float2(front, front), s2 = make_float2(a.scale, a.scale);
+                uint16_t* to = a.o + (it.row + (long long)c * C + r) * a.o_stride + it.h * D +
+                               64 * half;
+                const long long other_row = lane & 1 ? -a.o_stride : a.o_stride;
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {  // 32 columns a step
+                    uint32_t u[16];
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {
+                        float x[16], y[16];
+                        tmem_ld16(row + kTmemQS + 32 * i + 16 * part, x);
+                        tmem_ld16(row + kTmemPV + 32 * i + 16 * part, y);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float2 o = fma2(d2, make_float2(x[2 * e], x[2 * e + 1]),
+                                                  mul2(s2, make_float2(y[2 * e], y[2 * e + 1])));
+                            u[8 * part + e] = narrow2<F16>(o.x, o.y);
+                        }
+                    }
+                    // Two lanes exchange 32-byte pieces, each then has one of either row: a
+                    // store covers half a line of 16 rows (a lane its own row: 32 lines a
+                    // store, which held up everything else on its way to memory).
+                    uint32_t keep[8], got[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        keep[e] = lane & 1 ? u[8 + e] : u[e];
+                        got[e] = __shfl_xor_sync(0xffffffffu, lane & 1 ? u[e] : u[8 + e], 1);
+                    }
+                    uint16_t* at = to + 32 * i + 16 * (lane & 1);
+                    if (r < there) store_32(at, keep);
+                    if ((r ^ 1) < there) store_32(at + other_row, got);
+                }
+                tc_fence_before();
+                if (*(volatile int*)&sh.bad[odd]) {
+                    __syncwarp();  // the rows' other lanes have stored by now
+                    if (r < there) put_nan<F16>(to - 64 * half, sh.bad_first[odd], half, r);
+                    // the last warp cleans up for the chunk after the next one
+                    __syncwarp();
+                    int seen = 0;
+                    if (lane == 0) {
+                        __threadfence_block();
+                        seen = atomicAdd(&sh.bad_seen[odd], 1);
+                        __threadfence_block();
+                    }
+                    if (__shfl_sync(0xffffffffu, seen, 0) == 7) {
+                        sh.bad_first[odd][lane] = 0xffffffffu;
+                        if (lane == 0) sh.bad[odd] = sh.bad_seen[odd] = 0;
+                    }
+                }
+                arrive_warp(&sh.o_read);
+            }
             decay = ex2_approx(total);
             unit = v_unit;
             all += total;
@@ -915,7 +971,7 @@ lin_prefill_kernel(Work w, const __grid_constant__ CUtensorMap mq,
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.full[i], 1);
             mbar_init(&sh.empty[i], 1);
-            sh.bad[i] = 0;
+            sh.bad[i] = sh.bad_seen[i] = 0;
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sh.item_full[i], 1);
@@ -923,17 +979,17 @@ lin_prefill_kernel(Work w, const __grid_constant__ CUtensorMap mq,
         }
         mbar_init(&sh.qk_ready, 1);
         mbar_init(&sh.p_ready, 4);
-        mbar_init(&sh.o_ready, 1);
-        mbar_init(&sh.o_read, 4);
-        mbar_init(&sh.s16_ready, 8);
         mbar_init(&sh.v_checked, 8);
+        mbar_init(&sh.pv_ready, 2);
+        mbar_init(&sh.s16_ready, 8);
+        mbar_init(&sh.qs_ready, 2);
+        mbar_init(&sh.o_read, 8);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.w_ready[i], 8);
             mbar_init(&sh.kw_ready[i], 1);
             mbar_init(&sh.half_sync[i], 4);
         }
         mbar_init(&sh.token_sync, 4);
-        mbar_init(&sh.token_clean, 4);
         mbar_init(&sh.state_sync, 8);
         fence_mbar_init();
         prefetch_tmap(&mq);
