@@ -253,8 +253,9 @@ __device__ __forceinline__ bool open_segment(const Work& w, const Plan& p, int i
 
 // ---------------------------------------------------------------- the kernel
 
-// Warps: 0..3 P, 4..11 W, O and the state, 12 copies, 13 products, 14 the rest.
-constexpr int kThreads = 480;
+// Warps: 0..3 P, 4..11 W, O and the state, 12 copies, 13 products, 14 and 15 look at
+// V.
+constexpr int kThreads = 512;
 constexpr uint32_t kTile = C * D * 2;         // 32 KB
 constexpr uint32_t kStage = 3 * kTile;        // Q, K, V; later lo, K, hi
 constexpr uint32_t kStateTile = 2 * kStage;   // S in 16 bits
@@ -263,7 +264,7 @@ constexpr int kRing = 2;
 
 struct Item {
     long long row;  // of the segment's first token
-    int rows, h, n;
+    int rows, h;
     int chunks;     // 0: no more segments
     const float* src;  // the state in front; null: zeros
     float* dst;        // where the state behind goes; null: nowhere
@@ -271,22 +272,24 @@ struct Item {
 
 struct Shared {
     uint64_t full[2], empty[2];
-    uint64_t qk_ready, p_ready, v_checked, pv_ready, s16_ready, qs_ready, o_read;
-    uint64_t w_ready[2], kw_ready[2];  // by chunk parity: SUM's may be a chunk apart
+    uint64_t qk_ready, p_ready, pv_ready, s16_ready, qs_ready, o_read;
+    // by chunk parity, where one side may be a chunk ahead of the other's wait
+    uint64_t v_checked[2], w_ready[2], kw_ready[2];
     uint64_t token_sync, half_sync[2], state_sync;
     uint64_t item_full[kRing], item_empty[kRing];
     Item item[kRing];
     uint32_t tmem;
     int stop;
-    // of g, as log2 of decays, within blocks of 32 tokens: less the sum up to each token,
-    // the sum behind it
+    // within blocks of 32 tokens: less the sum of g (log2) up to each token, and the decay
+    // behind it
     alignas(16) float sum[C];
     alignas(16) float tail[2][C];
     float front[C];        // scale * the decay from the chunk's start to each token
-    float later[2][4];     // of the blocks behind each block
-    float total[2];        // of the chunk
+    float later[2][4];     // decay of the blocks behind each block
+    float total[2];        // sum of the chunk
     float block[2][2][4];  // sums of blocks (SUM: for warps 4..7, 8..11)
-    float largest[2][16];  // FP16: of S and of V, each warp's
+    float largest[2][8];   // FP16: of S, each warp's; SUM: of V
+    uint32_t most_v[2][2]; // FP16: the largest magnitude in each half of V
     // V's infinities and NaN, by chunk parity: each column's first token (255: none)
     uint32_t bad_first[2][D / 4];
     int bad[2], bad_seen[2];  // whether there are any; warps that are through with them
@@ -347,7 +350,8 @@ struct Items {
     }
 };
 
-// The copying warp: hands out segments and fills the stages.
+// The copying warp: hands out segments and fills the stages.  (Tiles pulled into L2 one
+// to three chunks ahead of that: no faster.)
 template <bool SUM>
 __device__ __forceinline__ void copy_role(const Work& w, Shared& sh, unsigned char* sm,
                                           const CUtensorMap* mq, const CUtensorMap* mk,
@@ -358,8 +362,7 @@ __device__ __forceinline__ void copy_role(const Work& w, Shared& sh, unsigned ch
     Walk walk;
     walk.begin(plan, piece);
     Segment cut;
-    const bool open = open_segment(w, plan, piece, cut);
-    bool done = SUM && !open, go = true;
+    bool done = SUM && !open_segment(w, plan, piece, cut), go = true;
     int ring = 0, stage = 0;
     uint32_t ring_phase = 0, phase = 0;
     while (go) {
@@ -371,19 +374,17 @@ __device__ __forceinline__ void copy_role(const Work& w, Shared& sh, unsigned ch
             it.row = r.first + (long long)s.from * C;
             it.rows = min(r.count - s.from * C, (s.to - s.from) * C);
             it.h = s.h;
-            it.n = s.n;
             it.chunks = s.to - s.from;
             const size_t chain = ((size_t)s.n * a.heads + s.h) * kStateFloats;
             if (SUM) {
                 it.dst = w.sum + (size_t)piece * kStateFloats;
                 done = true;
             } else {
+                // (of a cut chain lin_join_kernel's copy: state_out may be state_in)
                 if (s.from) it.src = w.sum + (size_t)(piece - 1) * kStateFloats;
                 else if (s.to < s.of) it.src = w.start + (size_t)piece * kStateFloats;
                 else it.src = a.state_in ? a.state_in + chain : nullptr;
                 if (s.to == s.of && a.state_out) it.dst = a.state_out + chain;
-                // a cut chain's state in front: lin_join_kernel's copy, as state_out may
-                // be state_in
             }
         }
         if (lane == 0) {
@@ -427,7 +428,7 @@ __device__ __forceinline__ void copy_role(const Work& w, Shared& sh, unsigned ch
             mbar_wait(&sh.full[s], s < stage ? phase : phase ^ 1, 1 << 12);
 }
 
-// The warp that issues the products: of chunk c Q S and P V, the next chunk's Q K^T, so
+// The warp that issues the products: of chunk c P V and Q S, the next chunk's Q K^T, so
 // that its weights are worked out while this chunk's W is, and K^T W.  The products of
 // one warp run in the order of their issue, so Q K^T may follow P V, over whose P it is
 // written.  (In a fixed order: taking whichever has its operands costs more than it
@@ -472,6 +473,17 @@ __device__ __forceinline__ void product_role(Shared& sh, unsigned char* sm) {
         const uint64_t q_mn = mn_major + stage * (kStage >> 4), k_mn = q_mn + kT, v_mn = k_mn + kT;
         if (!SUM) {
             if (n && !wait_warp(sh, &sh.o_read, odd ^ 1)) return;
+            if (!wait_warp(sh, &sh.v_checked[odd], pair)) return;
+            if (!wait_warp(sh, &sh.p_ready, odd)) return;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    mma_f16_ta(tmem + kTmemPV, tmem + kTmemP + 8 * s, v_mn + s * 128, kNT, s > 0);
+                mma_commit(&sh.pv_ready);
+                mbar_arrive(&sh.pv_ready);  // passes on what p_ready and v_checked brought
+            }
+            __syncwarp();
             if (!wait_warp(sh, &sh.s16_ready, odd)) return;
             tc_fence_after();
             if (elect_one()) {
@@ -480,18 +492,6 @@ __device__ __forceinline__ void product_role(Shared& sh, unsigned char* sm) {
                     mma_f16(tmem + kTmemQS, q + (s >> 2) * (kT / 2) + (s & 3) * 2, state + s * 128,
                             kNT, s > 0);
                 mma_commit(&sh.qs_ready);
-                mbar_arrive(&sh.qs_ready);  // passes on what s16_ready brought
-            }
-            __syncwarp();
-            if (!wait_warp(sh, &sh.v_checked, odd)) return;
-            if (!wait_warp(sh, &sh.p_ready, odd)) return;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    mma_f16_ta(tmem + kTmemPV, tmem + kTmemP + 8 * s, v_mn + s * 128, kNT, s > 0);
-                mma_commit(&sh.pv_ready);
-                mbar_arrive(&sh.pv_ready);  // and p_ready and v_checked
             }
             __syncwarp();
         }
@@ -545,6 +545,34 @@ __device__ __forceinline__ void store_32(uint16_t* dst, const uint32_t (&u)[8]) 
     }
 }
 
+// Eight floats of a row of a state, a whole sector where the address allows.
+__device__ __forceinline__ void load_8(const float* from, float* s) {
+    if (reinterpret_cast<uintptr_t>(from) & 31) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(from) + i);
+            s[4 * i] = x.x, s[4 * i + 1] = x.y, s[4 * i + 2] = x.z, s[4 * i + 3] = x.w;
+        }
+    } else {
+        asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+                     : "=f"(s[0]), "=f"(s[1]), "=f"(s[2]), "=f"(s[3]), "=f"(s[4]), "=f"(s[5]),
+                       "=f"(s[6]), "=f"(s[7])
+                     : "l"(from)
+                     : "memory");
+    }
+}
+__device__ __forceinline__ void store_8(float* to, const float* s) {
+    if (reinterpret_cast<uintptr_t>(to) & 31) {
+        reinterpret_cast<float4*>(to)[0] = make_float4(s[0], s[1], s[2], s[3]);
+        reinterpret_cast<float4*>(to)[1] = make_float4(s[4], s[5], s[6], s[7]);
+    } else {
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(to),
+                     "f"(s[0]), "f"(s[1]), "f"(s[2]), "f"(s[3]), "f"(s[4]), "f"(s[5]), "f"(s[6]),
+                     "f"(s[7])
+                     : "memory");
+    }
+}
+
 // Warps 0..3, a thread a token: a chunk's weights P, and the decays that state_role takes.
 template <bool F16>
 __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned char* sm) {
@@ -576,7 +604,7 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
                 sh.block[0][odd][warp] = sum;
             }
             sh.sum[t] = -sum;
-            sh.tail[odd][t] = tail;
+            sh.tail[odd][t] = ex2_approx(tail);
             if (!sync_warps(sh, &sh.token_sync, sync_phase)) return;
             next_g = load_g(a, it, (c + 1) * C + t);
             float before = 0.f, behind = 0.f, total = 0.f;
@@ -587,35 +615,51 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
                 if (i > warp) behind += x;
                 total += x;
             }
-            if (lane == 0) sh.later[odd][warp] = behind;
+            if (lane == 0) sh.later[odd][warp] = ex2_approx(behind);
             if (t == 0) sh.total[odd] = total;
 
             if (!wait_warp(sh, &sh.qk_ready, odd)) return;
             tc_fence_after();
             // A block of 32 columns a step, upwards: the 16 columns that its weights take
-            // hold scores that have been read.  (One rolled loop for blocks on and below
-            // the diagonal: what all roles run has to stay in the instruction cache.)
+            // hold scores that have been read.  (Rolled: what all roles run has to stay in
+            // the instruction cache.)
 #pragma unroll 1
             for (int b = 0; b < 4; ++b) {
                 uint32_t p[16] = {};
                 if (b <= warp) {
                     float x[32];
                     tmem_ld32(row + kTmemP + 32 * b, x);
-                    float from = sum;  // from the end of block b; on the diagonal in all
+                    if (b == warp) {
+                        const float4* other = reinterpret_cast<const float4*>(sh.sum + 32 * b);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 s = other[k];
+                            const float y[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float d = ex2_approx(sum + y[e]);
+                                x[4 * k + e] = 4 * k + e <= lane ? x[4 * k + e] * d : 0.f;
+                            }
+                        }
+                    } else {
+                        const float4* other =
+                            reinterpret_cast<const float4*>(sh.tail[odd] + 32 * b);
+                        float from = sum;  // from the end of block b
 #pragma unroll 1
-                    for (int k = warp - 1; k > b; --k) from += sh.block[0][odd][k];
-                    const float4* other = reinterpret_cast<const float4*>(
-                        (b == warp ? sh.sum : sh.tail[odd]) + 32 * b);
-                    const int last = b == warp ? lane : 31;
-                    tmem_ld_wait();
+                        for (int k = warp - 1; k > b; --k) from += sh.block[0][odd][k];
+                        from = ex2_approx(from);
+                        const float2 f2 = make_float2(from, from);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float4 s = other[k];
-                        const float y[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float d = ex2_approx(from + y[e]);
-                            x[4 * k + e] = 4 * k + e <= last ? x[4 * k + e] * d : 0.f;
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 s = other[k];
+                            const float2 lo = mul2(make_float2(x[4 * k], x[4 * k + 1]),
+                                                   mul2(make_float2(s.x, s.y), f2));
+                            const float2 hi = mul2(make_float2(x[4 * k + 2], x[4 * k + 3]),
+                                                   mul2(make_float2(s.z, s.w), f2));
+                            x[4 * k] = lo.x, x[4 * k + 1] = lo.y;
+                            x[4 * k + 2] = hi.x, x[4 * k + 3] = hi.y;
                         }
                     }
 #pragma unroll
@@ -653,21 +697,19 @@ __device__ __noinline__ void put_nan(uint16_t* o, const uint32_t* bad_first, int
         if ((int)(bad_first[j >> 2] >> (j & 3) * 8 & 255u) <= t) o[j] = F16 ? 0x7e00 : 0x7fc0;
 }
 
-// Infinities and NaN of row r of a half tile of V: the product must not see them, as
-// rows before theirs have weight 0 for them.  What they do to the rows from theirs on is
-// noted for the rows of O; put_back_nan brings them into W.  Returns their columns.  Not a
-// path for ordinary inputs.
+// Looks V over, a warp for half of its columns: what is not finite the product must not see, as rows
+// before it have weight 0 for it.  It is set aside as zero, and each column's first such
+// row noted: what it does to the rows from there on is put into O and W by state_role.
+// (Not a path for ordinary inputs.)  FP16: finds the largest magnitude too.
 template <bool F16>
-__device__ __noinline__ unsigned long long set_aside(Shared& sh, unsigned char* half_tile,
-                                                     int half, int r, int odd) {
+__device__ __noinline__ void set_aside(Shared& sh, unsigned char* half_tile, int half, int r,
+                                       int odd) {
     constexpr uint32_t kExp = F16 ? 0x7c00u : 0x7f80u;
-    unsigned long long found = 0;
 #pragma unroll 1
     for (int i = 0; i < 64; ++i) {
         uint16_t* at = reinterpret_cast<uint16_t*>(piece_of(half_tile, r, i >> 3)) + (i & 7);
         if ((*at & kExp) != kExp) continue;
         *at = 0;
-        found |= 1ull << i;
         const int col = half * 64 + i, shift = (col & 3) * 8;
         uint32_t* word = &sh.bad_first[odd][col >> 2];
         uint32_t was = *(volatile uint32_t*)word;
@@ -679,16 +721,77 @@ __device__ __noinline__ unsigned long long set_aside(Shared& sh, unsigned char* 
         }
     }
     *(volatile int*)&sh.bad[odd] = 1;
-    return found;
 }
 template <bool F16>
-__device__ __noinline__ void put_back_nan(unsigned char* half_tile, int r,
-                                          unsigned long long found) {
+__device__ __noinline__ void put_back_nan(unsigned char* half_tile, const uint32_t* bad_first,
+                                          int half, int r) {
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-        if (found >> i & 1)
+    for (int i = 0; i < 64; ++i) {
+        const int col = half * 64 + i;
+        if ((int)(bad_first[col >> 2] >> (col & 3) * 8 & 255u) == r)
             reinterpret_cast<uint16_t*>(piece_of(half_tile, r, i >> 3))[i & 7] =
                 F16 ? 0x7e00 : 0x7fc0;
+    }
+}
+// Two FP16 magnitudes: the larger one, at most 65504, as the bits of a float.
+__device__ __forceinline__ uint32_t largest_half(uint32_t two) {
+    const uint32_t x = min(max(two & 0xffffu, two >> 16), 0x7bffu);
+    return __float_as_uint(__half2float(__ushort_as_half((uint16_t)x)));
+}
+template <bool F16>
+__device__ __forceinline__ void check_role(Shared& sh, unsigned char* sm, int half) {
+    constexpr uint32_t kExp = F16 ? 0x7c007c00u : 0x7f807f80u,
+                       kOne = F16 ? 0x04000400u : 0x00800080u;
+    const int lane = threadIdx.x & 31;
+    Items items;
+    Item it;
+    int n = 0;
+    while (items.next(sh, it)) {
+#pragma unroll 1
+        for (int c = 0; c < it.chunks; ++c, ++n) {
+            const uint32_t odd = n & 1;
+            const int there = min(C, it.rows - c * C);
+            unsigned char* half_tile = sm + (n & 1) * kStage + 2 * kTile + half * (kTile / 2);
+            if (!wait_warp(sh, &sh.full[n & 1], n >> 1 & 1)) return;
+            uint32_t most = 0;
+            bool found = false;
+#pragma unroll 1
+            for (int r = lane; r < C; r += 64) {  // two rows a lane
+                uint32_t carry[2] = {0, 0}, largest[2] = {0, 0};
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const uint4 v = *piece_of(half_tile, r + 32 * (i >> 3), i & 7);
+                    // an exponent of ones carries into the sign's place
+                    carry[i >> 3] |= ((v.x & kExp) + kOne) | ((v.y & kExp) + kOne) |
+                                     ((v.z & kExp) + kOne) | ((v.w & kExp) + kOne);
+                    if (F16) {
+                        uint32_t& m = largest[i >> 3];
+                        m = __vmaxu2(__vmaxu2(m, v.x & 0x7fff7fffu),
+                                     __vmaxu2(v.y & 0x7fff7fffu, v.z & 0x7fff7fffu));
+                        m = __vmaxu2(m, v.w & 0x7fff7fffu);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const bool mine = r + 32 * k < there;
+                    if (F16 && mine) most = __vmaxu2(most, largest[k]);
+                    const bool bad = mine && (carry[k] & 0x80008000u);
+                    if (__any_sync(0xffffffffu, bad)) {
+                        // (notes of the last but one chunk are through with by then)
+                        if (n && !wait_warp(sh, &sh.o_read, odd ^ 1)) return;
+                        if (bad) set_aside<F16>(sh, half_tile, half, r + 32 * k, odd);
+                        found = true;
+                    }
+                }
+            }
+            if (F16) {
+                const uint32_t m = __reduce_max_sync(0xffffffffu, largest_half(most));
+                if (lane == 0) sh.most_v[odd][half] = m;
+            }
+            if (found) fence_async_smem();
+            arrive_warp(&sh.v_checked[odd]);
+        }
+    }
 }
 
 // The power of two that brings a largest value `x` to [2^13, 2^14) when divided by, and
@@ -714,12 +817,12 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
     while (items.next(sh, it)) {
         float s[64];
         {
-            const float4* from = reinterpret_cast<const float4*>(
-                SUM || !it.src ? nullptr : it.src + r * D + half * 64);
+            const float* from = SUM || !it.src ? nullptr : it.src + r * D + half * 64;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float4 x = from ? __ldcg(from + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-                s[4 * i] = x.x, s[4 * i + 1] = x.y, s[4 * i + 2] = x.z, s[4 * i + 3] = x.w;
+            for (int i = 0; i < 64; ++i) s[i] = 0.f;
+            if (from) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) load_8(from + 8 * i, s + 8 * i);
             }
         }
         float decay = 1.f, unit = 1.f, all = 0.f;  // of the last chunk; of the segment
@@ -775,7 +878,7 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
                 f = ex2_approx(tail);
                 next_g = load_g(a, it, (c + 1) * C + r);
             }
-            if (!wait_warp(sh, &sh.full[n & 1], n >> 1 & 1)) return;
+            if (SUM && !wait_warp(sh, &sh.full[n & 1], n >> 1 & 1)) return;
             if (SUM && r >= there) {  // (token_role does it otherwise)
 #pragma unroll 1
                 for (int i = 0; i < 8; ++i) {
@@ -783,63 +886,42 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
                     *piece_of(v_half, r, i) = make_uint4(0, 0, 0, 0);
                 }
             }
-            constexpr uint32_t kExp = F16 ? 0x7c007c00u : 0x7f807f80u,
-                               kOne = F16 ? 0x04000400u : 0x00800080u;
-            uint32_t carry = 0;   // an exponent of ones carries into the sign's place
-            uint32_t most_v = 0;  // FP16: magnitudes are in order of their bits
-            if (!SUM || F16) {
-#pragma unroll 4
-                for (int i = 0; i < 8; ++i) {
-                    const uint4 v = *piece_of(v_half, r, i);
-                    carry |= ((v.x & kExp) + kOne) | ((v.y & kExp) + kOne) |
-                             ((v.z & kExp) + kOne) | ((v.w & kExp) + kOne);
-                    if (F16) {
-                        most_v = __vmaxu2(most_v, v.x & 0x7fff7fffu);
-                        most_v = __vmaxu2(most_v, v.y & 0x7fff7fffu);
-                        most_v = __vmaxu2(most_v, v.z & 0x7fff7fffu);
-                        most_v = __vmaxu2(most_v, v.w & 0x7fff7fffu);
-                    }
-                }
-                if (r >= there) most_v = 0;
-            }
-            unsigned long long found = 0;
-            if (!SUM) {
-                if ((carry & 0x80008000u) && r < there) {
-                    found = set_aside<F16>(sh, v_half, half, r, odd);
-                    fence_async_smem();
-                }
-                arrive_warp(&sh.v_checked);
-                if (c && !add()) return;
-            }
+            if (!SUM && c && !add()) return;
             float v_unit = 1.f, v_inverse = 1.f, s_unit = 1.f, s_inverse = 1.f;
             if (F16) {
-                float most_s = 0.f;
-                if (!SUM) {
+                // largest of S (SUM: of V): positive numbers are in order of their bits
+                uint32_t most = 0;
+                if (SUM) {
+                    uint32_t most_v = 0;
+#pragma unroll 4
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 v = *piece_of(v_half, r, i);
+                        most_v = __vmaxu2(__vmaxu2(most_v, v.x & 0x7fff7fffu),
+                                          __vmaxu2(v.y & 0x7fff7fffu, v.z & 0x7fff7fffu));
+                        most_v = __vmaxu2(most_v, v.w & 0x7fff7fffu);
+                    }
+                    most = largest_half(most_v);
+                } else {
+                    float most_s = 0.f;
 #pragma unroll
                     for (int i = 0; i < 64; ++i) {
                         const float x = fabsf(s[i]);
                         most_s = x < INFINITY ? fmaxf(most_s, x) : most_s;
                     }
+                    most = __float_as_uint(most_s);
                 }
-                // (positive floats are in order of their bits; infinities and NaN of V are
-                // above 65504 and count as that)
-                const uint32_t v16 = min(max(most_v & 0xffffu, most_v >> 16), 0x7bffu);
-                const uint32_t both_s = __reduce_max_sync(0xffffffffu, __float_as_uint(most_s));
-                const uint32_t both_v = __reduce_max_sync(0xffffffffu, v16);
-                if (lane == 0) {
-                    sh.largest[odd][id] = __uint_as_float(both_s);
-                    sh.largest[odd][8 + id] = __half2float(__ushort_as_half((uint16_t)both_v));
-                }
+                most = __reduce_max_sync(0xffffffffu, most);
+                if (lane == 0) sh.largest[odd][id] = __uint_as_float(most);
                 if (!sync_warps(sh, &sh.state_sync, state_phase)) return;
-                float ms = 0.f, mv = 0.f;
+                float m = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    ms = fmaxf(ms, sh.largest[odd][i]);
-                    mv = fmaxf(mv, sh.largest[odd][8 + i]);
+                for (int i = 0; i < 8; ++i) m = fmaxf(m, sh.largest[odd][i]);
+                if (SUM) {
+                    v_unit = unit_of(m, v_inverse);
+                    f *= v_inverse;
+                } else {
+                    s_unit = unit_of(m, s_inverse);
                 }
-                s_unit = unit_of(ms, s_inverse);
-                v_unit = unit_of(mv, v_inverse);
-                if (SUM) f *= v_inverse;
             }
             if (!SUM) {
                 unsigned char* state_half = sm + kStateTile + half * (kTile / 2);
@@ -856,30 +938,44 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
                 }
                 fence_async_smem();
                 arrive_warp(&sh.s16_ready);
-                // V and Q are through
-                if (!wait_warp(sh, &sh.pv_ready, odd)) return;
-                if (!wait_warp(sh, &sh.qs_ready, odd)) return;
+                if (!wait_warp(sh, &sh.pv_ready, odd)) return;  // V is through
                 total = sh.total[odd];
-                f = ex2_approx(sh.tail[odd][r] + sh.later[odd][warp]);
-                if (F16) f *= v_inverse;
+                f = sh.tail[odd][r] * sh.later[odd][warp];
+                if (F16) {
+                    v_unit = unit_of(__uint_as_float(max(sh.most_v[odd][0], sh.most_v[odd][1])),
+                                     v_inverse);
+                    f *= v_inverse;
+                }
             }
-#pragma unroll 2
-            for (int i = 0; i < 8; ++i) {
+            // W: hi over V, then lo over Q once that is through
+            auto split = [&](int i, uint4& lo) {
                 uint4* at = piece_of(v_half, r, i);
                 const uint4 v = *at;
                 const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-                uint32_t hi[4], lo[4];
+                uint32_t hi[4], rest[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float2 y = mul2(widen2<F16>(x[e]), make_float2(f, f));
                     hi[e] = narrow2<F16>(y.x, y.y);
                     const float2 h = widen2<F16>(hi[e]);
-                    lo[e] = narrow2<F16>(y.x - h.x, y.y - h.y);
+                    rest[e] = narrow2<F16>(y.x - h.x, y.y - h.y);
                 }
                 *at = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *piece_of(q_half, r, i) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                lo = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+            };
+            if constexpr (SUM) {
+#pragma unroll 2
+                for (int i = 0; i < 8; ++i) split(i, *piece_of(q_half, r, i));
+            } else {
+                uint4 lo[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) split(i, lo[i]);
+                if (*(volatile int*)&sh.bad[odd])
+                    put_back_nan<F16>(v_half, sh.bad_first[odd], half, r);
+                if (!wait_warp(sh, &sh.qs_ready, odd)) return;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) *piece_of(q_half, r, i) = lo[i];
             }
-            if (!SUM && found) put_back_nan<F16>(v_half, r, found);
             fence_async_smem();
             arrive_warp(&sh.w_ready[odd]);
             if (SUM && c && !add()) return;
@@ -945,10 +1041,9 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
         }
         if (!add()) return;
         if (it.dst) {
-            float4* to = reinterpret_cast<float4*>(it.dst + r * D + half * 64);
+            float* to = it.dst + r * D + half * 64;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                to[i] = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+            for (int i = 0; i < 8; ++i) store_8(to + 8 * i, s + 8 * i);
         }
         if (SUM && r == 0 && half == 0) w.log_sum[blockIdx.x] = all;
     }
@@ -975,16 +1070,16 @@ lin_prefill_kernel(Work w, const __grid_constant__ CUtensorMap mq,
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sh.item_full[i], 1);
-            mbar_init(&sh.item_empty[i], SUM ? 9 : 13);
+            mbar_init(&sh.item_empty[i], SUM ? 9 : 15);
         }
         mbar_init(&sh.qk_ready, 1);
         mbar_init(&sh.p_ready, 4);
-        mbar_init(&sh.v_checked, 8);
         mbar_init(&sh.pv_ready, 2);
         mbar_init(&sh.s16_ready, 8);
-        mbar_init(&sh.qs_ready, 2);
+        mbar_init(&sh.qs_ready, 1);
         mbar_init(&sh.o_read, 8);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.v_checked[i], 2);
             mbar_init(&sh.w_ready[i], 8);
             mbar_init(&sh.kw_ready[i], 1);
             mbar_init(&sh.half_sync[i], 4);
@@ -1010,7 +1105,10 @@ lin_prefill_kernel(Work w, const __grid_constant__ CUtensorMap mq,
         state_role<F16, SUM>(w, sh, sm);
     } else if (warp < 4) {
         if (!SUM) token_role<F16>(w, sh, sm);
-    } else if (!SUM && w.a.cu) {
+    } else if (!SUM) {
+        check_role<F16>(sh, sm, warp - 14);
+    }
+    if (!SUM && warp == 15 && w.a.cu) {
         const Args& a = w.a;
         const int lane = threadIdx.x & 31;
         if (blockIdx.x == 0 && !warp_offsets_ok(a.cu, a.n_seqs, a.t) && lane == 0)
@@ -1046,6 +1144,7 @@ constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads) lin_join_kernel(Work w) {
     const Args& a = w.a;
     pdl_wait();
+    pdl_release();
     const Plan p = make_plan(w);
     const int i = blockIdx.x;
     Segment s;
@@ -1062,15 +1161,27 @@ __global__ void __launch_bounds__(kJoinThreads) lin_join_kernel(Work w) {
                           : make_float4(0.f, 0.f, 0.f, 0.f);
     reinterpret_cast<float4*>(w.start + (size_t)i * kStateFloats)[at] = x;
     float4* sums = reinterpret_cast<float4*>(w.sum) + at;
-#pragma unroll 4
-    for (int k = i; k <= last; ++k) {
-        const float4 add = __ldcg(sums + (size_t)k * (kStateFloats / 4));
-        const float d = exp2f(__ldcg(w.log_sum + k));
-        x.x = fmaf(d, x.x, add.x);
-        x.y = fmaf(d, x.y, add.y);
-        x.z = fmaf(d, x.z, add.z);
-        x.w = fmaf(d, x.w, add.w);
-        sums[(size_t)k * (kStateFloats / 4)] = x;
+    // (eight loads in flight: a load may not pass the stores before it by itself)
+    constexpr int kBatch = 8;
+    for (int k0 = i; k0 <= last; k0 += kBatch) {
+        float4 add[kBatch];
+        float d[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (k0 + k > last) break;
+            add[k] = __ldcg(sums + (size_t)(k0 + k) * (kStateFloats / 4));
+            d[k] = __ldcg(w.log_sum + k0 + k);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (k0 + k > last) break;
+            const float by = exp2f(d[k]);
+            x.x = fmaf(by, x.x, add[k].x);
+            x.y = fmaf(by, x.y, add[k].y);
+            x.z = fmaf(by, x.z, add[k].z);
+            x.w = fmaf(by, x.w, add[k].w);
+            sums[(size_t)(k0 + k) * (kStateFloats / 4)] = x;
+        }
     }
 }
 
