@@ -689,12 +689,19 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
     }
 }
 
-// NaN in the columns of half a row whose V was not finite at this token or before.
+// NaN in the columns of half a row of O whose V was not finite at this token or before, in
+// global memory or in the half tile on its way there.
 template <bool F16>
-__device__ __noinline__ void put_nan(uint16_t* o, const uint32_t* bad_first, int half, int t) {
+__device__ __noinline__ void put_nan(uint16_t* o, unsigned char* half_tile,
+                                     const uint32_t* bad_first, int half, int t) {
 #pragma unroll 1
-    for (int j = 64 * half; j < 64 * half + 64; ++j)
-        if ((int)(bad_first[j >> 2] >> (j & 3) * 8 & 255u) <= t) o[j] = F16 ? 0x7e00 : 0x7fc0;
+    for (int i = 0; i < 64; ++i) {
+        const int col = 64 * half + i;
+        if ((int)(bad_first[col >> 2] >> (col & 3) * 8 & 255u) > t) continue;
+        uint16_t* at = o ? o + i
+                         : reinterpret_cast<uint16_t*>(piece_of(half_tile, t, i >> 3)) + (i & 7);
+        *at = F16 ? 0x7e00 : 0x7fc0;
+    }
 }
 
 // Looks V over, a warp for half of its columns: what is not finite the product must not see, as rows
@@ -805,7 +812,8 @@ __device__ __forceinline__ float unit_of(float x, float& inverse) {
 // Warps 4..11, a thread a row i of 64 columns of the state, and likewise a token's 64
 // channels of V and O.
 template <bool F16, bool SUM>
-__device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned char* sm) {
+__device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned char* sm,
+                                           const CUtensorMap* mo) {
     const Args& a = w.a;
     const int r = threadIdx.x & 127, half = (threadIdx.x >> 7) - 1, warp = r >> 5,
               lane = threadIdx.x & 31, id = (threadIdx.x >> 5) - 4;
@@ -857,6 +865,7 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
             const int there = min(C, it.rows - c * C);
             unsigned char* q_half = sm + (n & 1) * kStage + half * (kTile / 2);
             unsigned char* v_half = q_half + 2 * kTile;
+            unsigned char* const state_half = sm + kStateTile + half * (kTile / 2);
             float f = 0.f, total = 0.f;  // decays from the token on, and of the chunk
             if (SUM) {
                 float tail = log2_decay(next_g);
@@ -924,7 +933,9 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
                 }
             }
             if (!SUM) {
-                unsigned char* state_half = sm + kStateTile + half * (kTile / 2);
+                // (rows of O still on their way from there)
+                if (lane == 0) bulk_wait_read_all();
+                __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     uint32_t u[4];
@@ -984,42 +995,39 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
                 tc_fence_after();
                 const float front = sh.front[r] * (F16 ? s_unit : 1.f);
                 const float2 d2 = make_float2(front, front), s2 = make_float2(a.scale, a.scale);
+                // A warp's 32 rows go by way of shared memory, in the place of the state's
+                // copy, which Q S is through with (written by the lanes, 32 bytes of a row
+                // each, the stores held up everything else on its way to memory: 452 us
+                // where this takes 400).  Rows past the last token must not be written:
+                // a warp that has some writes its rows itself.
+                const bool whole = there >= 32 * (warp + 1);
+                const int first = 32 * warp;
                 uint16_t* to = a.o + (it.row + (long long)c * C + r) * a.o_stride + it.h * D +
                                64 * half;
-                const long long other_row = lane & 1 ? -a.o_stride : a.o_stride;
-#pragma unroll 1
-                for (int i = 0; i < 2; ++i) {  // 32 columns a step
-                    uint32_t u[16];
-#pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-                        float x[16], y[16];
-                        tmem_ld16(row + kTmemQS + 32 * i + 16 * part, x);
-                        tmem_ld16(row + kTmemPV + 32 * i + 16 * part, y);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float2 o = fma2(d2, make_float2(x[2 * e], x[2 * e + 1]),
-                                                  mul2(s2, make_float2(y[2 * e], y[2 * e + 1])));
-                            u[8 * part + e] = narrow2<F16>(o.x, o.y);
-                        }
-                    }
-                    // Two lanes exchange 32-byte pieces, each then has one of either row: a
-                    // store covers half a line of 16 rows (a lane its own row: 32 lines a
-                    // store, which held up everything else on its way to memory).
-                    uint32_t keep[8], got[8];
+#pragma unroll 2
+                for (int i = 0; i < 4; ++i) {  // 16 columns a step
+                    float x[16], y[16];
+                    tmem_ld16(row + kTmemQS + 16 * i, x);
+                    tmem_ld16(row + kTmemPV + 16 * i, y);
+                    tmem_ld_wait();
+                    uint32_t u[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        keep[e] = lane & 1 ? u[8 + e] : u[e];
-                        got[e] = __shfl_xor_sync(0xffffffffu, lane & 1 ? u[e] : u[8 + e], 1);
+                        const float2 o = fma2(d2, make_float2(x[2 * e], x[2 * e + 1]),
+                                              mul2(s2, make_float2(y[2 * e], y[2 * e + 1])));
+                        u[e] = narrow2<F16>(o.x, o.y);
                     }
-                    uint16_t* at = to + 32 * i + 16 * (lane & 1);
-                    if (r < there) store_32(at, keep);
-                    if ((r ^ 1) < there) store_32(at + other_row, got);
+                    if (whole) {
+                        *piece_of(state_half, r, 2 * i) = make_uint4(u[0], u[1], u[2], u[3]);
+                        *piece_of(state_half, r, 2 * i + 1) = make_uint4(u[4], u[5], u[6], u[7]);
+                    } else if (r < there) {
+                        store_32(to + 16 * i, u);
+                    }
                 }
                 tc_fence_before();
                 if (*(volatile int*)&sh.bad[odd]) {
-                    __syncwarp();  // the rows' other lanes have stored by now
-                    if (r < there) put_nan<F16>(to - 64 * half, sh.bad_first[odd], half, r);
+                    if (whole) put_nan<F16>(nullptr, state_half, sh.bad_first[odd], half, r);
+                    else if (r < there) put_nan<F16>(to, nullptr, sh.bad_first[odd], half, r);
                     // the last warp cleans up for the chunk after the next one
                     __syncwarp();
                     int seen = 0;
@@ -1033,7 +1041,13 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
                         if (lane == 0) sh.bad[odd] = sh.bad_seen[odd] = 0;
                     }
                 }
+                if (whole) fence_async_smem();
                 arrive_warp(&sh.o_read);
+                if (whole && lane == 0) {
+                    tma_store_3d(mo, state_half + first * 128, 64 * half, it.h,
+                                 (int)(it.row + (long long)c * C + first));
+                    bulk_commit();
+                }
             }
             decay = ex2_approx(total);
             unit = v_unit;
@@ -1053,7 +1067,8 @@ template <bool F16, bool SUM>
 __global__ void __launch_bounds__(kThreads, 1)
 lin_prefill_kernel(Work w, const __grid_constant__ CUtensorMap mq,
                    const __grid_constant__ CUtensorMap mk,
-                   const __grid_constant__ CUtensorMap mv) {
+                   const __grid_constant__ CUtensorMap mv,
+                   const __grid_constant__ CUtensorMap mo) {
     extern __shared__ __align__(1024) unsigned char sm[];
     Shared& sh = *reinterpret_cast<Shared*>(sm + kSharedOff);
     const int warp = threadIdx.x >> 5;
@@ -1090,6 +1105,7 @@ lin_prefill_kernel(Work w, const __grid_constant__ CUtensorMap mq,
         prefetch_tmap(&mq);
         prefetch_tmap(&mk);
         prefetch_tmap(&mv);
+        if (!SUM) prefetch_tmap(&mo);
     }
     if (threadIdx.x < 2 * (D / 4)) (&sh.bad_first[0][0])[threadIdx.x] = 0xffffffffu;
     if (warp == 13) tmem_alloc(&sh.tmem, 512);
@@ -1102,7 +1118,8 @@ lin_prefill_kernel(Work w, const __grid_constant__ CUtensorMap mq,
     } else if (warp == 13) {
         product_role<F16, SUM>(sh, sm);
     } else if (warp >= 4 && warp < 12) {
-        state_role<F16, SUM>(w, sh, sm);
+        state_role<F16, SUM>(w, sh, sm, &mo);
+        if (!SUM) bulk_wait_all();  // rows of O on their way (lane 0's)
     } else if (warp < 4) {
         if (!SUM) token_role<F16>(w, sh, sm);
     } else if (!SUM) {
@@ -1211,11 +1228,12 @@ kda_status launch_lin_chunked(const Args& a, bool f16, void* workspace, cudaStre
     w.sum = static_cast<float*>(workspace);
     w.start = w.sum + (size_t)slots * kStateFloats;
     w.log_sum = w.start + (size_t)slots * kStateFloats;
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mo;
     KDA_REQUIRE(tma_map_heads(&mq, a.q, a.qk_heads, rows, a.q_stride, 1, C, f16) &&
                     tma_map_heads(&mk, a.k, a.qk_heads, rows, a.k_stride, 1, C, f16) &&
-                    tma_map_heads(&mv, a.v, a.heads, rows, a.v_stride, 1, C, f16),
-                KDA_ERR_CUDA, "%s: cannot describe the inputs to the copy engine", fn);
+                    tma_map_heads(&mv, a.v, a.heads, rows, a.v_stride, 1, C, f16) &&
+                    tma_map_heads(&mo, a.o, a.heads, rows, a.o_stride, 1, 32, f16),
+                KDA_ERR_CUDA, "%s: cannot describe the arrays to the copy engine", fn);
     // Whether chains may be cut: for packed rows the lengths are on the device.
     const long long chains = (long long)a.n_seqs * a.heads;
     const long long longest = (a.t + C - 1) / C;
@@ -1241,11 +1259,11 @@ kda_status launch_lin_chunked(const Args& a, bool f16, void* workspace, cudaStre
         }
     }
     if (cut) {
-        launch_pdl(sums, dim3(grid), dim3(kThreads), kSmemBytes, s, w, mq, mk, mv);
+        launch_pdl(sums, dim3(grid), dim3(kThreads), kSmemBytes, s, w, mq, mk, mv, mo);
         launch_pdl(lin_join_kernel, dim3(grid, kStateFloats / 4 / kJoinThreads),
                    dim3(kJoinThreads), 0, s, w);
     }
-    launch_pdl(kernel, dim3(grid), dim3(kThreads), kSmemBytes, s, w, mq, mk, mv);
+    launch_pdl(kernel, dim3(grid), dim3(kThreads), kSmemBytes, s, w, mq, mk, mv, mo);
     return launch_result(fn);
 }
 

@@ -358,6 +358,15 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
         : "memory");
 }
 
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src_smem, int x,
+                                             int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+            reinterpret_cast<uint64_t>(map)),
+        "r"(x), "r"(y), "r"(z), "r"(smem_u32(src_smem))
+        : "memory");
+}
+
 // Contiguous bulk copy global -> shared (bytes a multiple of 16, both ends
 // 16-byte aligned), completing on `bar`.
 __device__ __forceinline__ void bulk_load(void* dst_smem, const void* src, uint32_t bytes,
