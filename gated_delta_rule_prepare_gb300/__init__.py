@@ -674,13 +674,37 @@ def kda_attn_kv4_decode(q, cache, page_table, lens, out, lse=None, window=0, sca
 
 # ---------------------------------------------------------------- rotary positions, pages
 
+_device = torch._C._cuda_getDevice
+_I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
+
+
 def _call(dev, fn, *args):
     """`fn` on device `dev`'s current stream."""
-    if torch.cuda.current_device() == dev:
-        _check(fn(*args, _raw_stream(dev)))
+    if _device() == dev:
+        status = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, _raw_stream(dev)))
+            status = fn(*args, _raw_stream(dev))
+    if status:
+        _check(status)
+
+
+def _array(t, dtype, dev, shape, name):
+    """Pointer of a contiguous array of the given type and shape."""
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    if t.shape != shape:
+        raise ValueError("%s must be %s" % (name, list(shape)))
+    return _packed(t, dtype, dev, name)
+
+
+def _space(workspace, dev, size, *args):
+    """(tensor, pointer, bytes): the caller's workspace, or one of size(*args) bytes."""
+    if workspace is None:
+        workspace = torch.empty(size(*args), dtype=_U8, device="cuda:%d" % dev)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("the workspace must be a contiguous tensor on the call's device")
+    return workspace, workspace.data_ptr(), workspace.nbytes
 
 
 def kda_attn_rope(q, k, positions, inv_freq, q_out=None, k_out=None, pair_axis=None,
@@ -693,49 +717,40 @@ def kda_attn_rope(q, k, positions, inv_freq, q_out=None, k_out=None, pair_axis=N
     p + pairs; channels behind the pairs stay."""
     in_dtype, dev = _attn_type(q, "q")
     dt, shape = q.dtype, q.shape
-    q_out = q if q_out is None else q_out
     q_ptr, q_row = _rows(q, dt, dev, "q")
-    qo_ptr, qo_row = _rows(q_out, dt, dev, "q_out")
+    qo_ptr, qo_row = (q_ptr, q_row) if q_out is None else _rows(q_out, dt, dev, "q_out")
+    if q_out is not None and q_out.shape != shape:
+        raise ValueError("kda_attn_rope: q_out must have q's shape")
     k_ptr = ko_ptr = None
     k_row = ko_row = kv_heads = 0
+    lead = shape[:-2]
     if k is not None:
-        k_out = k if k_out is None else k_out
+        k_shape = k.shape
         k_ptr, k_row = _rows(k, dt, dev, "k")
-        ko_ptr, ko_row = _rows(k_out, dt, dev, "k_out")
-        kv_heads = k.shape[-2]
-        if k_out.shape != k.shape or k.shape[:-2] != shape[:-2]:
+        ko_ptr, ko_row = (k_ptr, k_row) if k_out is None else _rows(k_out, dt, dev, "k_out")
+        kv_heads = k_shape[-2]
+        if k_shape[:-2] != lead or (k_out is not None and k_out.shape != k_shape):
             raise ValueError("kda_attn_rope: k_out must have k's shape, and k q's rows")
     elif k_out is not None:
         raise ValueError("kda_attn_rope: k_out without k")
-    if q_out.shape != shape:
-        raise ValueError("kda_attn_rope: q_out must have q's shape")
-    rows = shape[0] if len(shape) == 3 else shape[0] * shape[1]
-    axes = positions.numel() // rows if rows else 1
-    lead = shape[:-2]
-    if positions.shape != lead and positions.shape != lead + (axes,):
+    rows = lead[0] if len(lead) == 1 else lead[0] * lead[1]
+    pos_shape = positions.shape
+    axes = 1 if pos_shape == lead else pos_shape[-1] if pos_shape[:-1] == lead else 0
+    if not axes:
         raise ValueError("kda_attn_rope: positions must be [rows] or [rows, axes]")
-    if inv_freq.dim() != 1:
-        raise ValueError("kda_attn_rope: inv_freq must be [pairs]")
-    pairs = inv_freq.numel()
+    pairs = inv_freq.shape[0] if inv_freq.dim() == 1 else 0
     table = None
     if pair_axis is not None:
-        if len(pair_axis) != pairs or not all(0 <= x < axes for x in pair_axis):
+        table = bytes(pair_axis)
+        if len(table) != pairs or max(table, default=0) >= axes:
             raise ValueError("kda_attn_rope: pair_axis must hold an axis below %d for each pair"
                              % axes)
-        table = bytes(pair_axis)
     elif axes > 1:
         raise ValueError("kda_attn_rope: several axes need pair_axis")
     _call(dev, LIB.kda_attn_rope, q_ptr, k_ptr, qo_ptr, ko_ptr, rows, shape[-2], kv_heads,
           HEAD_DIM, in_dtype, q_row, k_row, qo_row, ko_row,
-          _packed(positions, torch.int32, dev, "positions"), axes,
-          _packed(inv_freq, torch.float32, dev, "inv_freq"), pairs, table, int(interleaved),
-          float(factor))
-
-
-def _ints(t, dev, name, shape):
-    if t.shape != shape:
-        raise ValueError("%s must be %s" % (name, list(shape)))
-    return _packed(t, torch.int32, dev, name)
+          _array(positions, _I32, dev, pos_shape, "positions"), axes,
+          _array(inv_freq, _F32, dev, (pairs,), "inv_freq"), pairs, table, interleaved, factor)
 
 
 def kda_attn_kv4_pages_workspace(n_pages, n_seqs, max_pages, device="cuda"):
@@ -744,32 +759,31 @@ def kda_attn_kv4_pages_workspace(n_pages, n_seqs, max_pages, device="cuda"):
     return torch.empty(int(need), dtype=torch.uint8, device=device)
 
 
-def _pages(page_table, refs):
-    """(table pointer, refs pointer, sequences, pages each, pages, device)"""
-    dev = page_table.get_device()
+def _pages(page_table, refs, workspace):
+    """(table pointer, its shape, refs pointer, shape, device, workspace, pointer, bytes)"""
+    dev, shape, n = page_table.get_device(), page_table.shape, refs.shape
     if dev < 0:
         raise TypeError("page_table must be a CUDA tensor")
-    if page_table.dim() != 2 or refs.dim() != 1:
+    if len(shape) != 2 or len(n) != 1:
         raise ValueError("page_table must be [sequences, pages], refs [pages of the cache]")
-    n_seqs, width = page_table.shape
-    return (_packed(page_table, torch.int32, dev, "page_table"),
-            _packed(refs, torch.int32, dev, "refs"), n_seqs, width, refs.numel(), dev)
-
-
-def _pages_scratch(workspace, n_pages, n_seqs, width, dev):
-    return _scratch(workspace, lambda: LIB.kda_attn_kv4_pages_workspace_size(
-        n_pages, n_seqs, width), dev)
+    return (_array(page_table, _I32, dev, shape, "page_table"), shape,
+            _array(refs, _I32, dev, n, "refs"), n, dev,
+            *_space(workspace, dev, LIB.kda_attn_kv4_pages_workspace_size, n[0], *shape))
 
 
 def kda_attn_kv4_resize(page_table, lens, refs, page=64, workspace=None):
     """Gives and frees pages in place, so that each sequence has those of its lens
     positions: page_table device int32 [N, max_pages] (-1: none), lens [N], refs
     [pages of the cache], how often each page is named (0: free)."""
-    table, refs_ptr, n_seqs, width, n_pages, dev = _pages(page_table, refs)
-    lens_ptr = _ints(lens, dev, "lens", (n_seqs,))
-    workspace, ws_ptr, ws_bytes = _pages_scratch(workspace, n_pages, n_seqs, width, dev)
-    _call(dev, LIB.kda_attn_kv4_resize, table, lens_ptr, refs_ptr, n_seqs, width, n_pages, page,
-          ws_ptr, ws_bytes)
+    table, shape, refs_ptr, n, dev, workspace, ws, ws_bytes = _pages(page_table, refs, workspace)
+    _call(dev, LIB.kda_attn_kv4_resize, table, _array(lens, _I32, dev, shape[:1], "lens"), refs_ptr,
+          shape[0], shape[1], n[0], page, ws, ws_bytes)
+
+
+def _lists(src, dst, count, n, dev):
+    def new(t, size):
+        return torch.empty(size, dtype=_I32, device="cuda:%d" % dev) if t is None else t
+    return new(src, n), new(dst, n), new(count, 1)
 
 
 def kda_attn_kv4_fork(page_table, lens, refs, parent, page_table_out=None, lens_out=None,
@@ -777,25 +791,19 @@ def kda_attn_kv4_fork(page_table, lens, refs, parent, page_table_out=None, lens_
     """Sequence n goes on from sequence parent[n] (device int32 [N]; -1: it ends).
     The outputs default to being in place.  Returns (src, dst, count), the pages for
     kda_attn_kv4_copy: device int32 [N], [N] and [1], allocated where not given."""
-    table, refs_ptr, n_seqs, width, n_pages, dev = _pages(page_table, refs)
-    page_table_out = page_table if page_table_out is None else page_table_out
-    lens_out = lens if lens_out is None else lens_out
-    refs_out = refs if refs_out is None else refs_out
-    src, dst, count = _lists(src, dst, count, n_seqs, dev)
-    args = (_ints(lens, dev, "lens", (n_seqs,)), refs_ptr, _ints(parent, dev, "parent", (n_seqs,)),
-            _ints(page_table_out, dev, "page_table_out", (n_seqs, width)),
-            _ints(lens_out, dev, "lens_out", (n_seqs,)),
-            _ints(refs_out, dev, "refs_out", (n_pages,)), _ints(src, dev, "src", (n_seqs,)),
-            _ints(dst, dev, "dst", (n_seqs,)), _ints(count, dev, "count", (1,)))
-    workspace, ws_ptr, ws_bytes = _pages_scratch(workspace, n_pages, n_seqs, width, dev)
-    _call(dev, LIB.kda_attn_kv4_fork, table, *args, n_seqs, width, n_pages, page, ws_ptr, ws_bytes)
+    table, shape, refs_ptr, n, dev, workspace, ws, ws_bytes = _pages(page_table, refs, workspace)
+    rows = shape[:1]
+    src, dst, count = _lists(src, dst, count, rows[0], dev)
+    lens_ptr = _array(lens, _I32, dev, rows, "lens")
+    _call(dev, LIB.kda_attn_kv4_fork, table, lens_ptr, refs_ptr,
+          _array(parent, _I32, dev, rows, "parent"),
+          table if page_table_out is None
+          else _array(page_table_out, _I32, dev, shape, "page_table_out"),
+          lens_ptr if lens_out is None else _array(lens_out, _I32, dev, rows, "lens_out"),
+          refs_ptr if refs_out is None else _array(refs_out, _I32, dev, n, "refs_out"),
+          _array(src, _I32, dev, rows, "src"), _array(dst, _I32, dev, rows, "dst"),
+          _array(count, _I32, dev, (1,), "count"), rows[0], shape[1], n[0], page, ws, ws_bytes)
     return src, dst, count
-
-
-def _lists(src, dst, count, n, dev):
-    def new(t, size):
-        return torch.empty(size, dtype=torch.int32, device="cuda:%d" % dev) if t is None else t
-    return new(src, n), new(dst, n), new(count, 1)
 
 
 def kda_attn_kv4_compact(page_table, refs, page_table_out=None, refs_out=None, src=None, dst=None,
@@ -803,17 +811,15 @@ def kda_attn_kv4_compact(page_table, refs, page_table_out=None, refs_out=None, s
     """Makes the pages in use the lowest-numbered ones.  The outputs default to being
     in place.  Returns (src, dst, count), the moves for kda_attn_kv4_copy: device
     int32 [pages // 2] twice and [1], allocated where not given."""
-    table, refs_ptr, n_seqs, width, n_pages, dev = _pages(page_table, refs)
-    page_table_out = page_table if page_table_out is None else page_table_out
-    refs_out = refs if refs_out is None else refs_out
-    half = n_pages // 2
-    src, dst, count = _lists(src, dst, count, half, dev)
-    args = (_ints(page_table_out, dev, "page_table_out", (n_seqs, width)),
-            _ints(refs_out, dev, "refs_out", (n_pages,)), _ints(src, dev, "src", (half,)),
-            _ints(dst, dev, "dst", (half,)), _ints(count, dev, "count", (1,)))
-    workspace, ws_ptr, ws_bytes = _pages_scratch(workspace, n_pages, n_seqs, width, dev)
-    _call(dev, LIB.kda_attn_kv4_compact, table, refs_ptr, *args, n_seqs, width, n_pages, ws_ptr,
-          ws_bytes)
+    table, shape, refs_ptr, n, dev, workspace, ws, ws_bytes = _pages(page_table, refs, workspace)
+    half = (n[0] // 2,)
+    src, dst, count = _lists(src, dst, count, half[0], dev)
+    _call(dev, LIB.kda_attn_kv4_compact, table, refs_ptr,
+          table if page_table_out is None
+          else _array(page_table_out, _I32, dev, shape, "page_table_out"),
+          refs_ptr if refs_out is None else _array(refs_out, _I32, dev, n, "refs_out"),
+          _array(src, _I32, dev, half, "src"), _array(dst, _I32, dev, half, "dst"),
+          _array(count, _I32, dev, (1,), "count"), shape[0], shape[1], n[0], ws, ws_bytes)
     return src, dst, count
 
 
@@ -830,27 +836,25 @@ def kda_attn_kv4_copy(caches, src, dst, count):
     if len(shape) != 3 or shape[2] % KV4_TOKEN_BYTES or shape[2] // KV4_TOKEN_BYTES not in KV4_PAGES:
         raise ValueError("a cache must be [pages, kv_heads, page * 144], page one of %s"
                          % (KV4_PAGES,))
-    for c in caches:
-        if c.shape != shape:
-            raise ValueError("kda_attn_kv4_copy: the caches must have one shape")
-    most = src.numel()
-    array = (_c.c_void_p * len(caches))(*[_packed(c, torch.uint8, dev, "cache") for c in caches])
+    rows = src.shape
+    if len(rows) != 1:
+        raise ValueError("kda_attn_kv4_copy: src must be [n]")
+    array = (_c.c_void_p * len(caches))(*[_array(c, _U8, dev, shape, "cache") for c in caches])
     _call(dev, LIB.kda_attn_kv4_copy, array, len(caches), shape[0], shape[2] // KV4_TOKEN_BYTES,
-          shape[1], _ints(src, dev, "src", (most,)), _ints(dst, dev, "dst", (most,)),
-          _ints(count, dev, "count", (1,)), most)
+          shape[1], _array(src, _I32, dev, rows, "src"), _array(dst, _I32, dev, rows, "dst"),
+          _array(count, _I32, dev, (1,), "count"), rows[0])
 
 
 # ---------------------------------------------------------------- linear attention
 
 def _decays(g, lead, heads, dev):
     """(pointer, token-row stride) of g: [heads], or [.., rows, heads] in rows."""
-    if g.dim() == 1:
-        if g.shape[0] != heads:
-            raise ValueError("g must be [rows, heads] or [heads]")
-        return _packed(g, torch.float32, dev, "g"), 0
-    if g.shape != lead + (heads,):
+    shape = g.shape
+    if len(shape) == 1:
+        return _array(g, _F32, dev, (heads,), "g"), 0
+    if shape[:-1] != lead or shape[-1] != heads:
         raise ValueError("g must be [rows, heads] or [heads]")
-    ptr = _at(g, torch.float32, dev, "g")
+    ptr = _at(g, _F32, dev, "g")
     if g.is_contiguous():
         return ptr, heads
     stride = g.stride()
@@ -870,25 +874,17 @@ def _decays(g, lead, heads, dev):
 def _lin_rows(name, q, k, v, g, out):
     """What both calls take of their rows: (type, device, pointers, strides, lead, heads)."""
     in_dtype, dev = _attn_type(q, "q")
-    dt = q.dtype
+    dt, shape, v_shape = q.dtype, q.shape, v.shape
     q_ptr, q_row = _rows(q, dt, dev, "q")
     k_ptr, k_row = _rows(k, dt, dev, "k")
     v_ptr, v_row = _rows(v, dt, dev, "v")
     o_ptr, o_row = _rows(out, dt, dev, "out")
-    lead, heads, qk_heads = tuple(q.shape[:-2]), v.shape[-2], q.shape[-2]
-    if k.shape != q.shape or v.shape[:-2] != q.shape[:-2] or out.shape != v.shape:
+    lead, heads = shape[:-2], v_shape[-2]
+    if k.shape != shape or v_shape[:-2] != lead or out.shape != v_shape:
         raise ValueError("%s: k must have q's shape, out v's, and v q's rows" % name)
     g_ptr, g_row = _decays(g, lead, heads, dev)
     return (in_dtype, dev, (q_ptr, k_ptr, v_ptr, g_ptr, o_ptr),
-            (q_row, k_row, v_row, g_row, o_row), lead, heads, qk_heads)
-
-
-def _lin_state(t, n_seqs, heads, dev, name):
-    if t is None:
-        return None
-    if t.shape != (n_seqs, heads, HEAD_DIM, HEAD_DIM):
-        raise ValueError("%s must be [sequences, heads, 128, 128]" % name)
-    return _packed(t, torch.float32, dev, name)
+            (q_row, k_row, v_row, g_row, o_row), lead, heads, shape[-2])
 
 
 def kda_lin_prefill_workspace(rows, n_seqs, heads, device="cuda"):
@@ -913,18 +909,19 @@ def kda_lin_prefill(q, k, v, g, out, state_in=None, state_out=None, t=None, cu_s
         if len(lead) != 1 or t not in (None, lead[0]):
             raise ValueError("kda_lin_prefill: packed rows have three dimensions, and t is all "
                              "of them")
-        cu, n_seqs, t_pad = _packed(cu_seqlens, torch.int32, dev, "cu_seqlens"), \
-            cu_seqlens.numel() - 1, lead[0]
+        cu = _packed(cu_seqlens, _I32, dev, "cu_seqlens")
+        n_seqs, t_pad = cu_seqlens.numel() - 1, lead[0]
     else:
         n_seqs, t_pad = (1, lead[0]) if len(lead) == 1 else lead
-    t = t_pad if t is None else t
-    states = [_lin_state(s, n_seqs, heads, dev, name)
-              for s, name in ((state_in, "state_in"), (state_out, "state_out"))]
+    want = (n_seqs, heads, HEAD_DIM, HEAD_DIM)
     rows = t_pad if cu else t_pad * n_seqs
-    workspace, ws_ptr, ws_bytes = _scratch(
-        workspace, lambda: LIB.kda_lin_prefill_workspace_size(rows, n_seqs, heads), dev)
-    _call(dev, LIB.kda_lin_prefill, *states, *ptrs, t, t_pad, cu, n_seqs, heads, qk_heads, HEAD_DIM,
-          in_dtype, *strides, float(scale), ws_ptr, ws_bytes)
+    workspace, ws, ws_bytes = _space(workspace, dev, LIB.kda_lin_prefill_workspace_size, rows,
+                                     n_seqs, heads)
+    _call(dev, LIB.kda_lin_prefill,
+          None if state_in is None else _array(state_in, _F32, dev, want, "state_in"),
+          None if state_out is None else _array(state_out, _F32, dev, want, "state_out"), *ptrs,
+          t_pad if t is None else t, t_pad, cu, n_seqs, heads, qk_heads, HEAD_DIM, in_dtype,
+          *strides, scale, ws, ws_bytes)
 
 
 def kda_lin_decode(q, k, v, g, out, state_in=None, state_out=None, snapshots=(), scale=Q_SCALE):
@@ -935,12 +932,15 @@ def kda_lin_decode(q, k, v, g, out, state_in=None, state_out=None, snapshots=(),
     in_dtype, dev, ptrs, strides, lead, heads, qk_heads = _lin_rows("kda_lin_decode", q, k, v, g,
                                                                     out)
     n_seqs, krows = lead if len(lead) == 2 else (lead[0], 1)
-    states = [_lin_state(s, n_seqs, heads, dev, name)
-              for s, name in ((state_in, "state_in"), (state_out, "state_out"))]
-    snaps = [_lin_state(s, n_seqs, heads, dev, "snapshot") for s in snapshots]
-    array = (_c.c_void_p * len(snaps))(*snaps) if snaps else None
-    _call(dev, LIB.kda_lin_decode, *states, *ptrs, n_seqs, krows, heads, qk_heads, HEAD_DIM,
-          in_dtype, *strides, float(scale), array, len(snaps))
+    want = (n_seqs, heads, HEAD_DIM, HEAD_DIM)
+    array, n_snap = None, len(snapshots)
+    if n_snap:
+        array = (_c.c_void_p * n_snap)(*[_array(s, _F32, dev, want, "snapshot")
+                                         for s in snapshots])
+    _call(dev, LIB.kda_lin_decode,
+          None if state_in is None else _array(state_in, _F32, dev, want, "state_in"),
+          None if state_out is None else _array(state_out, _F32, dev, want, "state_out"), *ptrs,
+          n_seqs, krows, heads, qk_heads, HEAD_DIM, in_dtype, *strides, scale, array, n_snap)
 
 
 def kda_sync_status(device=None):

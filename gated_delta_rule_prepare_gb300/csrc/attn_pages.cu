@@ -3,11 +3,12 @@
 //
 // The three are passes over small integer arrays, each pass needing what the last one
 // counted: latency is what they take.  One cluster of up to eight CTAs runs all
-// passes of a call, with its barrier between them; few entries run in one CTA.
-// An array is cut into one slice for each warp; a warp counts what it looks for in
-// its slice, the counts are summed up in the order of the slices, and on a second
-// pass each thing found knows its number.  So new pages come in order, and no result
-// depends on which warp was first: what is added to a count atomically is integers.
+// passes of a call, two or three of its barriers between them (fork with eight: 23 us
+// for 512 rows); few entries run in one CTA.  Arrays are cut into one slice for each
+// warp; a warp counts what it looks for in its slice, the counts are summed up in the
+// order of the slices, and on a second pass each thing found knows its number.  So new
+// pages come in order, and no result depends on which warp was first: what is added to a
+// count atomically is integers.  What is known of rows (fork) each CTA works out by itself.
 //
 // Arrays that one pass writes and another CTA reads are read through L2 (__ldcg).
 #include <cooperative_groups.h>
@@ -25,38 +26,44 @@ __device__ unsigned g_pages_status = 0;
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMostCtas = 8;
+constexpr int kRowsShared = 12288;  // rows of a fork whose four integers fit shared memory
+constexpr int kMostInts = 0x7ff00000;  // of a table, of pages: a grid's step more is an int
 
 struct PageArgs {
     const int *table, *lens, *refs, *parent;
     int *table_out, *lens_out, *refs_out, *src, *dst, *count;
     int n_seqs, width, n_pages, page_shift;
     // workspace
-    int* got;    // [n_seqs * width at most] new pages, in order (resize: entries, fork: rows)
-    int* first;  // [n_seqs] the lowest child of each row
-    int* staged_table;  // copies of table and lens where the outputs are in their place
-    int* staged_lens;
-    int* place;   // [n_pages] where each page goes, -1 for free ones
-    int* movers;  // [n_pages / 2] pages that move, the last one first
+    int* want;          // [n_seqs * width] entries that want a page, in order (resize)
+    int* rows;          // [kMostCtas][4 * n_seqs] what a CTA knows of the rows, if they are many
+    int* staged_table;  // a copy of the table where the output is in its place
+    int* place;         // [n_pages] where each page goes, -1 for free ones
 
     __device__ __forceinline__ int held(int len) const {
         return (int)(((long long)len + (1 << page_shift) - 1) >> page_shift);
     }
     __device__ __forceinline__ bool names(int v) const { return v >= 0 && v < n_pages; }
+    __device__ __forceinline__ int clamped_len(int len, unsigned& bad) const {
+        const long long most = (long long)width << page_shift;
+        if (len < 0 || len > most) bad |= STATUS_BAD_PAGES;
+        return (int)min(max((long long)len, 0LL), most);
+    }
 };
 
 // One cluster's threads, and sums over its warps.
 struct Team {
     cg::cluster_group cluster = cg::this_cluster();
-    int rank, ctas, warp, lane, id;
-    int* sums;  // [kWarps] of this CTA
-    bool bad = false;
+    int rank, ctas, warp, lane, id, threads, me;
+    int (*sums)[kWarps];  // [2]: of one sum, and of the next one
 
-    __device__ explicit Team(int* shared_sums) : sums(shared_sums) {
+    __device__ explicit Team(int (*shared_sums)[kWarps]) : sums(shared_sums) {
         rank = (int)cluster.block_rank();
         ctas = (int)cluster.num_blocks();
         warp = threadIdx.x >> 5;
         lane = threadIdx.x & 31;
         id = rank * kWarps + warp;
+        threads = ctas * kThreads;
+        me = rank * kThreads + threadIdx.x;
     }
     __device__ void sync() {
         __threadfence();
@@ -64,265 +71,315 @@ struct Team {
     }
     // This warp's part of [0, n), in pieces of 32.
     struct Slice {
-        long long from, to;
+        int from, to;
     };
-    __device__ Slice slice(long long n) const {
-        const long long warps = (long long)ctas * kWarps;
-        const long long each = ((n + 31) / 32 + warps - 1) / warps * 32;
-        const long long from = min(n, each * id);
-        return {from, min(n, from + each)};
+    __device__ Slice slice(int n, int of) const {
+        const int warps = ctas * kWarps;
+        const int each = (int)(((long long)n + 32LL * warps - 1) / (32LL * warps)) * 32;
+        const int from = (int)min((long long)n, (long long)each * of);
+        return {from, (int)min((long long)n, from + (long long)each)};
     }
-    // Sum of `x` (one number a warp) over the warps before this one; `total` over all.
-    // Ends with everybody past its reads.
-    __device__ int before(int x, int& total) {
-        if (lane == 0) sums[warp] = x;
+    __device__ Slice slice(int n) const { return slice(n, id); }
+    // One number a warp (the same in its lanes): the sum over the warps before this one,
+    // and over all.  A barrier of the cluster; `which` alternates between 0 and 1.
+    __device__ int before(int x, int which, int& total) {
+        if (lane == 0) sums[which][warp] = x;
         sync();
         int mine = 0, all = 0;
         for (int r = 0; r < ctas; ++r) {
-            const int* theirs = cluster.map_shared_rank(sums, r);
-            const int y = theirs[lane];
+            const int y = cluster.map_shared_rank(&sums[which][0], r)[lane];
             const int s = __reduce_add_sync(0xffffffffu, y);
             if (r < rank) mine += s;
             if (r == rank) mine += __reduce_add_sync(0xffffffffu, lane < warp ? y : 0);
             all += s;
         }
         total = all;
-        sync();
         return mine;
     }
-    __device__ void report(unsigned bits) {
-        if (bits) atomicOr(&g_pages_status, bits);
+    // Before a CTA ends: others may still read its sums.
+    __device__ void leave(unsigned bad) {
+        if (bad) atomicOr(&g_pages_status, bad);
+        cluster.sync();
     }
 };
 
-// Free pages in order: the i-th of them, i < wanted, goes to got[i] and is counted as
-// named once.  Returns how many there are, at most `wanted`.
-__device__ int take_free(Team& t, const PageArgs& a, int wanted) {
+// How many pages of a warp's slice are free, and each of them with its number.
+constexpr int kAhead = 4;  // steps of 32 pages loaded at a time
+__device__ __forceinline__ int count_free(const Team& t, const PageArgs& a) {
     const Team::Slice s = t.slice(a.n_pages);
     int mine = 0;
-    for (long long i = s.from + t.lane; i < s.to; i += 32) mine += __ldcg(a.refs_out + i) <= 0;
-    mine = __reduce_add_sync(0xffffffffu, mine);
-    int total, at = t.before(mine, total);
-    if (mine) {
-        for (long long i0 = s.from; i0 < s.to && at < wanted; i0 += 32) {
-            const long long i = i0 + t.lane;
-            const bool free = i < s.to && __ldcg(a.refs_out + i) <= 0;
-            const unsigned all = __ballot_sync(0xffffffffu, free);
-            const int n = at + __popc(all & ((1u << t.lane) - 1));
-            if (free && n < wanted) {
-                a.got[n] = (int)i;
-                a.refs_out[i] = 1;
-            }
-            at += __popc(all);
+    for (int i0 = s.from; i0 < s.to; i0 += 32 * kAhead) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + 32 * k + t.lane;
+            mine += i < s.to && __ldcg(a.refs_out + i) <= 0;
         }
     }
-    t.sync();
-    return min(total, wanted);
+    return __reduce_add_sync(0xffffffffu, mine);
 }
-
-__device__ __forceinline__ int clamped_len(const PageArgs& a, int len, unsigned& bad) {
-    const long long most = (long long)a.width << a.page_shift;
-    if (len < 0 || len > most) bad |= STATUS_BAD_PAGES;
-    return (int)min(max((long long)len, 0LL), most);
+template <class Take>
+__device__ __forceinline__ void take_free(const Team& t, const PageArgs& a, int at, int wanted,
+                                          Take take) {
+    const Team::Slice s = t.slice(a.n_pages);
+    for (int i0 = s.from; i0 < s.to && at < wanted; i0 += 32) {
+        const int i = i0 + t.lane;
+        const bool free = i < s.to && __ldcg(a.refs_out + i) <= 0;
+        const unsigned all = __ballot_sync(0xffffffffu, free);
+        const int n = at + __popc(all & ((1u << t.lane) - 1));
+        if (free && n < wanted) {
+            a.refs_out[i] = 1;
+            take(n, i);
+        }
+        at += __popc(all);
+    }
 }
 
 __global__ void __launch_bounds__(kThreads) resize_kernel(PageArgs a) {
-    __shared__ int sums[32];
+    __shared__ int sums[2][kWarps];
     Team t(sums);
     pdl_wait();
     pdl_release();
     unsigned bad = 0;
-    const Team::Slice s = t.slice((long long)a.n_seqs * a.width);
-    // entries past a sequence's length give their pages up; missing ones are counted
+    const Team::Slice s = t.slice(a.n_seqs * a.width);
+    // Entries past a sequence's length give their pages up; missing ones are counted, and
+    // noted by bits, for as many steps as the mask has.
     int mine = 0;
-    for (long long i = s.from + t.lane; i < s.to; i += 32) {
-        const int n = (int)(i / a.width), col = (int)(i - (long long)n * a.width);
-        const int v = a.table_out[i];
-        if (v < -1 || v >= a.n_pages) bad |= STATUS_BAD_PAGES;
-        if (col < a.held(clamped_len(a, __ldcg(a.lens + n), bad))) {
-            mine += !a.names(v);
-        } else if (v != -1) {
-            if (a.names(v)) atomicAdd(a.refs_out + v, -1);
-            a.table_out[i] = -1;
+    auto missing = [&](int i, int v) {
+        unsigned ignore = 0;
+        const int n = i / a.width, col = i - n * a.width;
+        return col < a.held(a.clamped_len(__ldcg(a.lens + n), ignore)) && !a.names(v);
+    };
+    for (int i0 = s.from; i0 < s.to; i0 += 32 * kAhead) {
+        int v[kAhead], len[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + 32 * k + t.lane;
+            if (i < s.to) v[k] = a.table_out[i], len[k] = __ldcg(a.lens + i / a.width);
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + 32 * k + t.lane;
+            if (i >= s.to) continue;
+            if (v[k] < -1 || v[k] >= a.n_pages) bad |= STATUS_BAD_PAGES;
+            if (i % a.width < a.held(a.clamped_len(len[k], bad))) {
+                if (a.names(v[k])) continue;
+                ++mine;
+            } else if (a.names(v[k])) {
+                atomicAdd(a.refs_out + v[k], -1);
+            }
+            if (v[k] != -1) a.table_out[i] = -1;
         }
     }
     mine = __reduce_add_sync(0xffffffffu, mine);
-    int wanted, at = t.before(mine, wanted);
+    int wanted, at = t.before(mine, 0, wanted);
     if (wanted) {
-        const int there = take_free(t, a, wanted);
-        if (there < wanted) bad |= STATUS_NO_PAGES;
-        if (mine) {
-            for (long long i0 = s.from; i0 < s.to; i0 += 32) {
-                const long long i = i0 + t.lane;
-                bool miss = false;
-                if (i < s.to) {
-                    const int n = (int)(i / a.width), col = (int)(i - (long long)n * a.width);
-                    unsigned ignore = 0;
-                    miss = col < a.held(clamped_len(a, __ldcg(a.lens + n), ignore)) &&
-                           !a.names(a.table_out[i]);
-                }
+        if (mine) {  // the entries in order
+            for (int i0 = s.from; i0 < s.to; i0 += 32) {
+                const int i = i0 + t.lane;
+                const bool miss = i < s.to && missing(i, a.table_out[i]);
                 const unsigned all = __ballot_sync(0xffffffffu, miss);
-                const int k = at + __popc(all & ((1u << t.lane) - 1));
-                if (miss) a.table_out[i] = k < there ? __ldcg(a.got + k) : -1;
+                if (miss) a.want[at + __popc(all & ((1u << t.lane) - 1))] = i;
                 at += __popc(all);
             }
         }
+        int there;
+        const int first = t.before(count_free(t, a), 1, there);
+        take_free(t, a, first, wanted,
+                  [&](int n, int page) { a.table_out[__ldcg(a.want + n)] = page; });
+        if (there < wanted) bad |= STATUS_NO_PAGES;
     }
-    t.report(bad);
+    t.leave(bad);
 }
 
+// What a CTA knows of a fork's rows: each one's parent (-1: none) and its length, each
+// parent's lowest child, and the rows that get a page of their own, in order.
+struct ForkRows {
+    int *parent, *len, *first, *copies;
+};
+
 __global__ void __launch_bounds__(kThreads) fork_kernel(PageArgs a) {
-    __shared__ int sums[32];
+    extern __shared__ int row_memory[];
+    __shared__ int sums[2][kWarps], scan[kWarps];
     Team t(sums);
     pdl_wait();
     pdl_release();
     unsigned bad = 0;
-    const int threads = t.ctas * kThreads, me = t.rank * kThreads + threadIdx.x;
-    const long long entries = (long long)a.n_seqs * a.width;
-    const int *table = a.table, *lens = a.lens;
+    const int n_seqs = a.n_seqs, tid = threadIdx.x, entries = n_seqs * a.width;
+    int* const rows = n_seqs <= kRowsShared ? row_memory : a.rows + (size_t)t.rank * 4 * n_seqs;
+    const ForkRows r = {rows, rows + n_seqs, rows + 2 * n_seqs, rows + 3 * n_seqs};
+    const int* table = a.table;
     if (a.table == a.table_out) {
-        for (long long i = me; i < entries; i += threads) a.staged_table[i] = a.table[i];
+        for (int i = t.me; i < entries; i += t.threads) a.staged_table[i] = __ldcg(a.table + i);
         table = a.staged_table;
     }
-    if (a.lens == a.lens_out) lens = a.staged_lens;
     if (a.refs != a.refs_out)
-        for (int i = me; i < a.n_pages; i += threads) a.refs_out[i] = a.refs[i];
-    for (int n = me; n < a.n_seqs; n += threads) {
-        a.first[n] = a.n_seqs;
-        if (a.lens == a.lens_out) a.staged_lens[n] = a.lens[n];
-    }
-    t.sync();
-    auto parent_of = [&](int n) {
+        for (int i = t.me; i < a.n_pages; i += t.threads) a.refs_out[i] = __ldcg(a.refs + i);
+    for (int n = tid; n < n_seqs; n += kThreads) {
         const int p = __ldcg(a.parent + n);
-        if (p < -1 || p >= a.n_seqs) bad |= STATUS_BAD_PAGES;
-        return p >= 0 && p < a.n_seqs ? p : -1;
-    };
-    for (int n = me; n < a.n_seqs; n += threads) {
-        const int p = parent_of(n);
-        if (p >= 0) atomicMin(a.first + p, n);
+        if (p < -1 || p >= n_seqs) bad |= STATUS_BAD_PAGES;
+        const bool live = p >= 0 && p < n_seqs;
+        r.parent[n] = live ? p : -1;
+        r.len[n] = live ? a.clamped_len(__ldcg(a.lens + p), bad) : 0;
+        r.first[n] = n_seqs;
     }
+    // (everybody has read lens, which lens_out may be)
     t.sync();
-    // whether row n has a last page of its own to get; its parent's length
-    auto copied = [&](int n, int p, int& len) {
-        len = p < 0 ? 0 : clamped_len(a, __ldcg(lens + p), bad);
-        return p >= 0 && (len & ((1 << a.page_shift) - 1)) && __ldcg(a.first + p) != n;
+    for (int n = tid; n < n_seqs; n += kThreads)
+        if (r.parent[n] >= 0) atomicMin(r.first + r.parent[n], n);
+    __syncthreads();
+    auto copied = [&](int n) {
+        return r.parent[n] >= 0 && (r.len[n] & ((1 << a.page_shift) - 1)) &&
+               r.first[r.parent[n]] != n;
     };
-    for (long long i = me; i < entries; i += threads) {
-        const int n = (int)(i / a.width), col = (int)(i - (long long)n * a.width);
-        const int p = parent_of(n);
-        int len;
-        const bool copy = copied(n, p, len);
-        const int held = a.held(len), old = __ldcg(table + i);
-        if (old < -1 || old >= a.n_pages) bad |= STATUS_BAD_PAGES;
-        int now = -1;
-        if (col < held - (copy ? 1 : 0)) now = __ldcg(table + (long long)p * a.width + col);
-        if (!a.names(now)) now = -1;
-        if (old != now) {
-            if (a.names(old)) atomicAdd(a.refs_out + old, -1);
-            if (now >= 0) atomicAdd(a.refs_out + now, 1);
+    // the table, less the pages to come, and what that changes in the counts
+    for (int i0 = t.me; i0 < entries; i0 += kAhead * t.threads) {
+        int old[kAhead], now[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + k * t.threads;
+            old[k] = now[k] = -1;
+            if (i >= entries) continue;
+            const int n = i / a.width, col = i - n * a.width;
+            old[k] = __ldcg(table + i);
+            if (col < a.held(r.len[n]) - (copied(n) ? 1 : 0))
+                now[k] = __ldcg(table + r.parent[n] * a.width + col);
         }
-        a.table_out[i] = now;
-    }
-    // pages for the copies, in the order of their rows
-    const Team::Slice s = t.slice(a.n_seqs);
-    int mine = 0;
-    for (long long n = s.from + t.lane; n < s.to; n += 32) {
-        int len;
-        mine += copied((int)n, parent_of((int)n), len);
-    }
-    mine = __reduce_add_sync(0xffffffffu, mine);
-    int wanted, at = t.before(mine, wanted);
-    const int there = wanted ? take_free(t, a, wanted) : 0;
-    if (there < wanted) bad |= STATUS_NO_PAGES;
-    for (long long n0 = s.from; n0 < s.to; n0 += 32) {
-        const long long n = n0 + t.lane;
-        int len = 0, p = -1;
-        bool copy = false;
-        if (n < s.to) copy = copied((int)n, p = parent_of((int)n), len);
-        const unsigned all = __ballot_sync(0xffffffffu, copy);
-        const int k = at + __popc(all & ((1u << t.lane) - 1));
-        at += __popc(all);
-        if (copy) {
-            const int last = a.held(len) - 1;
-            if (k < there) {
-                const int page = __ldcg(a.got + k);
-                a.table_out[n * a.width + last] = page;
-                a.src[k] = __ldcg(table + (long long)p * a.width + last);
-                a.dst[k] = page;
-            } else {
-                len = last << a.page_shift;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + k * t.threads;
+            if (i >= entries) continue;
+            if (old[k] < -1 || old[k] >= a.n_pages) bad |= STATUS_BAD_PAGES;
+            if (!a.names(now[k])) now[k] = -1;
+            if (old[k] != now[k]) {
+                if (a.names(old[k])) atomicAdd(a.refs_out + old[k], -1);
+                if (now[k] >= 0) atomicAdd(a.refs_out + now[k], 1);
             }
-        }
-        if (n < s.to) {
-            a.lens_out[n] = len;
-            if (n >= there) a.src[n] = a.dst[n] = -1;
+            a.table_out[i] = now[k];
         }
     }
-    if (me == 0) a.count[0] = there;
-    t.report(bad);
+    // the rows that get a page, in order
+    int wanted = 0;
+    for (int n0 = 0; n0 < n_seqs; n0 += kThreads) {
+        const int n = n0 + tid;
+        const bool copy = n < n_seqs && copied(n);
+        const unsigned all = __ballot_sync(0xffffffffu, copy);
+        if (t.lane == 0) scan[t.warp] = __popc(all);
+        __syncthreads();
+        const int y = scan[t.lane];
+        const int at = wanted + __reduce_add_sync(0xffffffffu, t.lane < t.warp ? y : 0);
+        wanted += __reduce_add_sync(0xffffffffu, y);
+        if (copy) r.copies[at + __popc(all & ((1u << t.lane) - 1))] = n;
+        __syncthreads();
+    }
+    t.sync();  // the counts are complete
+    int there = 0;
+    if (wanted) {
+        const int first = t.before(count_free(t, a), 0, there);
+        there = min(there, wanted);
+        take_free(t, a, first, wanted, [&](int k, int page) {
+            const int n = r.copies[k], last = a.held(r.len[n]) - 1;
+            a.table_out[n * a.width + last] = page;
+            a.src[k] = __ldcg(table + r.parent[n] * a.width + last);
+            a.dst[k] = page;
+        });
+        if (there < wanted) bad |= STATUS_NO_PAGES;
+    }
+    for (int n = t.me; n < n_seqs; n += t.threads) {
+        if (n >= there) a.src[n] = a.dst[n] = -1;
+        a.lens_out[n] = r.len[n];
+    }
+    __syncthreads();
+    // rows that got no page keep their parents' full ones
+    for (int k = there + tid; k < wanted; k += kThreads) {
+        const int n = r.copies[k];
+        if (n % t.threads / kThreads == t.rank)
+            a.lens_out[n] = r.len[n] >> a.page_shift << a.page_shift;
+    }
+    if (t.me == 0) a.count[0] = there;
+    t.leave(bad);
 }
 
 __global__ void __launch_bounds__(kThreads) compact_kernel(PageArgs a) {
-    __shared__ int sums[32];
+    __shared__ int sums[2][kWarps], high;
     Team t(sums);
     pdl_wait();
     pdl_release();
     unsigned bad = 0;
-    const int threads = t.ctas * kThreads, me = t.rank * kThreads + threadIdx.x;
     const Team::Slice s = t.slice(a.n_pages);
     int mine = 0;
-    for (long long i = s.from + t.lane; i < s.to; i += 32) mine += a.refs[i] > 0;
+    for (int i0 = s.from; i0 < s.to; i0 += 32 * kAhead) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + 32 * k + t.lane;
+            mine += i < s.to && __ldcg(a.refs + i) > 0;
+        }
+    }
     mine = __reduce_add_sync(0xffffffffu, mine);
-    int used, before = t.before(mine, used);
-    // holes, below `used`; pages to move, from there on, counted from the end
-    int at = before;
-    for (long long i0 = s.from; i0 < s.to; i0 += 32) {
-        const long long i = i0 + t.lane;
-        const int count = i < s.to ? a.refs[i] : 0;
+    int used, at = t.before(mine, 0, used);
+    // How many pages move: those in use from `used` on.  Whole slices behind it, and the
+    // rest of its own one (each CTA for itself).
+    if (t.warp == 0) {
+        int count = 0, own = -1;
+        for (int of = t.lane; of < t.ctas * kWarps; of += 32) {
+            const Team::Slice x = t.slice(a.n_pages, of);
+            if (x.from >= used)
+                count += t.cluster.map_shared_rank(&sums[0][0], of / kWarps)[of % kWarps];
+            else if (x.to > used)
+                own = of;
+        }
+        own = __reduce_max_sync(0xffffffffu, own);
+        if (own >= 0) {
+            const Team::Slice x = t.slice(a.n_pages, own);
+            for (int i = used + t.lane; i < x.to; i += 32) count += __ldcg(a.refs + i) > 0;
+        }
+        count = __reduce_add_sync(0xffffffffu, count);
+        if (t.lane == 0) high = count;
+    }
+    __syncthreads();
+    const int moved = high, low = used - moved;  // pages in use that stay
+    for (int i0 = s.from; i0 < s.to; i0 += 32) {
+        const int i = i0 + t.lane;
+        const int count = i < s.to ? __ldcg(a.refs + i) : 0;
         const unsigned all = __ballot_sync(0xffffffffu, count > 0);
         const int below = at + __popc(all & ((1u << t.lane) - 1));  // pages in use before i
         at += __popc(all);
         if (i >= s.to) continue;
-        a.place[i] = count > 0 ? (int)i : -1;
-        if (i < used && count <= 0) a.dst[i - below] = (int)i;
-        if (i >= used && count > 0) a.movers[used - 1 - below] = (int)i;
+        a.place[i] = count > 0 ? i : -1;
+        if (i < used && count <= 0) a.dst[i - below] = i;
+        if (i >= used && count > 0) a.src[below - low] = i;
         if (a.refs != a.refs_out) a.refs_out[i] = count;
     }
+    for (int k = moved + t.me; k < a.n_pages / 2; k += t.threads) a.src[k] = a.dst[k] = -1;
     t.sync();
-    // how many: pages in use from `used` on, one for each hole
-    int high = 0;
-    for (long long i = max(s.from, (long long)used) + t.lane; i < s.to; i += 32)
-        high += __ldcg(a.refs + i) > 0;
-    high = __reduce_add_sync(0xffffffffu, high);
-    int moved;
-    t.before(high, moved);
-    for (int k = me; k < a.n_pages / 2; k += threads) {
-        if (k < moved) {
-            const int from = __ldcg(a.movers + moved - 1 - k), to = __ldcg(a.dst + k);
-            a.src[k] = from;
-            a.refs_out[to] = __ldcg(a.refs + from);
-        } else {
-            a.src[k] = a.dst[k] = -1;
+    for (int k = t.me; k < moved; k += t.threads) {
+        const int from = __ldcg(a.src + k), to = __ldcg(a.dst + k);
+        const int count = __ldcg(a.refs + from);
+        a.refs_out[to] = count;
+        a.refs_out[from] = 0;
+        a.place[from] = to;
+    }
+    t.sync();
+    const int entries = a.n_seqs * a.width;
+    for (int i0 = t.me; i0 < entries; i0 += kAhead * t.threads) {
+        int v[kAhead], now[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + k * t.threads;
+            v[k] = i < entries ? __ldcg(a.table + i) : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) now[k] = a.names(v[k]) ? __ldcg(a.place + v[k]) : -1;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int i = i0 + k * t.threads;
+            if (i >= entries) continue;
+            // (an entry whose page is free by its count names none)
+            if (v[k] != -1 && now[k] < 0) bad |= STATUS_BAD_PAGES;
+            a.table_out[i] = now[k];
         }
     }
-    t.sync();
-    for (int k = me; k < moved; k += threads) {
-        const int from = __ldcg(a.src + k);
-        a.refs_out[from] = 0;
-        a.place[from] = __ldcg(a.dst + k);
-    }
-    t.sync();
-    const long long entries = (long long)a.n_seqs * a.width;
-    for (long long i = me; i < entries; i += threads) {
-        const int v = a.table[i];
-        if (v < -1 || v >= a.n_pages) bad |= STATUS_BAD_PAGES;
-        // (an entry whose page is free by its count names none)
-        const int now = a.names(v) ? __ldcg(a.place + v) : -1;
-        if (a.names(v) && now < 0) bad |= STATUS_BAD_PAGES;
-        a.table_out[i] = now;
-    }
-    if (me == 0) a.count[0] = moved;
-    t.report(bad);
+    if (t.me == 0) a.count[0] = moved;
+    t.leave(bad);
 }
 
 // Pages move in pieces of 16 KB, a CTA each, four 16-byte loads a thread in flight.
@@ -363,18 +420,16 @@ copy_kernel(const __grid_constant__ Caches caches, int n_caches, long long n_pag
 }
 
 struct Layout {
-    size_t got, first, table, lens, place, movers, bytes;
+    size_t want, rows, table, place, bytes;
 };
 Layout workspace_layout(long long n_pages, long long n_seqs, long long width) {
     auto round = [](long long ints) { return (size_t)((ints * 4 + 15) / 16 * 16); };
     Layout l;
-    l.got = 0;
-    l.first = l.got + round(n_pages);
-    l.table = l.first + round(n_seqs);
-    l.lens = l.table + round(n_seqs * width);
-    l.place = l.lens + round(n_seqs);
-    l.movers = l.place + round(n_pages);
-    l.bytes = l.movers + round(n_pages / 2);
+    l.want = 0;  // (a table is staged by fork, its missing entries listed by resize)
+    l.table = 0;
+    l.rows = l.table + round(n_seqs * width);
+    l.place = l.rows + (n_seqs > kRowsShared ? round(kMostCtas * 4 * n_seqs) : 0);
+    l.bytes = l.place + round(n_pages);
     return l;
 }
 
@@ -386,13 +441,13 @@ kda_status pages_call(const char* fn, void (*kernel)(PageArgs), PageArgs a, int6
                 KDA_ERR_UNSUPPORTED, "%s: pages of %d tokens (only 16, 32, 64, 128, 256)", fn,
                 page);
     KDA_REQUIRE(a.n_seqs >= 1 && a.width >= 1 && a.width <= 0x7fffffff / page && n_pages >= 1 &&
-                    n_pages < 0x7fffffff,
+                    n_pages < kMostInts,
                 KDA_ERR_INVALID_ARG,
                 "%s: n_seqs (%d), max_pages (%d) and n_pages (%lld) must be positive, max_pages "
-                "* page and n_pages below 2^31",
+                "* page below 2^31, n_pages below 2^31 - 2^20",
                 fn, a.n_seqs, a.width, (long long)n_pages);
-    KDA_REQUIRE((long long)a.n_seqs * a.width < 0x7fffffffLL, KDA_ERR_INVALID_ARG,
-                "%s: a page table of 2^31 entries or more", fn);
+    KDA_REQUIRE((long long)a.n_seqs * a.width < kMostInts, KDA_ERR_INVALID_ARG,
+                "%s: a page table of 2^31 - 2^20 entries or more", fn);
     const void* all[] = {a.table, a.table_out, a.refs, a.refs_out};
     for (const void* p : all)
         KDA_REQUIRE(p && int_aligned(p), KDA_ERR_INVALID_ARG,
@@ -410,12 +465,10 @@ kda_status pages_call(const char* fn, void (*kernel)(PageArgs), PageArgs a, int6
     a.n_pages = (int)n_pages;
     a.page_shift = __builtin_ctz((unsigned)page);
     char* ws = static_cast<char*>(workspace);
-    a.got = reinterpret_cast<int*>(ws + l.got);
-    a.first = reinterpret_cast<int*>(ws + l.first);
+    a.want = reinterpret_cast<int*>(ws + l.want);
+    a.rows = reinterpret_cast<int*>(ws + l.rows);
     a.staged_table = reinterpret_cast<int*>(ws + l.table);
-    a.staged_lens = reinterpret_cast<int*>(ws + l.lens);
     a.place = reinterpret_cast<int*>(ws + l.place);
-    a.movers = reinterpret_cast<int*>(ws + l.movers);
     // a CTA for every 4096 integers, within a cluster's limit
     const long long ints = n_pages + (long long)a.n_seqs * a.width;
     const int ctas = ints <= 4096 ? 1 : ints <= 8192 ? 2 : ints <= 16384 ? 4 : kMostCtas;
@@ -423,6 +476,16 @@ kda_status pages_call(const char* fn, void (*kernel)(PageArgs), PageArgs a, int6
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = as_stream(stream);
+    if (kernel == fork_kernel && a.n_seqs <= kRowsShared) {
+        cfg.dynamicSmemBytes = 16 * (size_t)a.n_seqs;
+        const cudaError_t e =
+            cfg.dynamicSmemBytes <= 48 * 1024 - 1024
+                ? cudaSuccess
+                : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       16 * kRowsShared);
+        KDA_REQUIRE(e == cudaSuccess, KDA_ERR_CUDA, "%s: cannot reserve shared memory: %s", fn,
+                    cudaGetErrorString(e));
+    }
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -446,8 +509,8 @@ cudaError_t status_word_pages(unsigned** word) {
 using namespace kda;
 
 extern "C" size_t kda_attn_kv4_pages_workspace_size(int64_t n_pages, int n_seqs, int max_pages) {
-    if (n_pages < 1 || n_pages >= 0x7fffffff || n_seqs < 1 || max_pages < 1 ||
-        (long long)n_seqs * max_pages >= 0x7fffffffLL)
+    if (n_pages < 1 || n_pages >= kMostInts || n_seqs < 1 || max_pages < 1 ||
+        (long long)n_seqs * max_pages >= kMostInts)
         return 0;
     return workspace_layout(n_pages, n_seqs, max_pages).bytes;
 }

@@ -54,9 +54,14 @@ __device__ __forceinline__ uint4 turn_piece(uint4 x, const float2* cs, int u, in
 
 enum Layout { kInterleaved, kHalves8, kHalves };  // kHalves8: pairs a multiple of 8
 
-template <bool F16, int LAYOUT>
+// LANES threads a head: each a 16-byte piece of it, or (kHalves8) a piece of the first
+// channels of pairs with the piece of the second ones, then what is behind the pairs;
+// or (kHalves) 8 bytes.  Threads step through a tile's rows and heads, kBatch loads in
+// flight.
+constexpr int kRowsTile = 8;
+template <bool F16, int LAYOUT, int LANES>
 __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int tile_rows) {
-    __shared__ float2 cs[8][kMaxPairs];
+    __shared__ float2 cs[kRowsTile][kMaxPairs];
     __shared__ unsigned long long unit[kMaxPairs];
     pdl_wait();
     pdl_release();
@@ -70,9 +75,12 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int tile_row
     const long long row0 = (long long)blockIdx.x * tile_rows;
     const int rows = (int)min((long long)tile_rows, a.rows - row0);
     __syncthreads();
-    for (int i = tid; i < rows * a.pairs; i += kThreads) {
-        const int r = i / a.pairs, p = i - r * a.pairs;
-        const int axis = a.axis[p >> 4] >> (2 * (p & 15)) & 3;
+    for (int i = tid; i < rows * kMaxPairs; i += kThreads) {
+        const int r = i / kMaxPairs, p = i % kMaxPairs;
+        if (p >= a.pairs) continue;
+        const uint32_t word = p < 32 ? (p < 16 ? a.axis[0] : a.axis[1])
+                                     : (p < 48 ? a.axis[2] : a.axis[3]);
+        const int axis = word >> (2 * (p & 15)) & 3;
         const long long pos = __ldg(a.positions + (row0 + r) * a.axes + axis);
         const unsigned long long at = (unsigned long long)pos * unit[p];
         float s, c;
@@ -80,48 +88,77 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int tile_row
         cs[r][p] = make_float2(c * a.factor, s * a.factor);
     }
     __syncthreads();
-    // pieces of a row: q's heads, then k's, 16 (or fewer) pieces a head
-    const int per_head = LAYOUT == kHalves8 ? 16 - a.pairs / 8 : LAYOUT == kHalves ? 32 : 16;
+    constexpr int kHeads = kThreads / LANES;  // heads at a time
+    constexpr int kBatch = LAYOUT == kHalves ? 1 : 4;
+    const int u = tid % LANES, turned = a.pairs / 8;
+    if (LAYOUT == kHalves8 && u >= 16 - turned) return;
     const int heads = a.heads[0] + a.heads[1];
-    const int first = blockIdx.y * kThreads + tid, step = gridDim.y * kThreads;
-    const int per_row = heads * per_head, total = rows * per_row;
-    // (a head's lanes stay together in kHalves: 32 pieces, and step a multiple of 32)
-    for (int i = first; i < total; i += step) {
-        const int r = i / per_row, in_row = i - r * per_row;
-        int h = in_row / per_head;
-        const int u = in_row - h * per_head;
-        const int which = h >= a.heads[0];
-        if (which) h -= a.heads[0];
-        const uint16_t* src = a.in[which] + (row0 + r) * a.in_stride[which] + h * D;
-        uint16_t* dst = a.out[which] + (row0 + r) * a.out_stride[which] + h * D;
-        if constexpr (LAYOUT == kInterleaved) {
-            const uint4 x = reinterpret_cast<const uint4*>(src)[u];
-            reinterpret_cast<uint4*>(dst)[u] = turn_piece<F16>(x, cs[r], u, a.pairs);
-        } else if constexpr (LAYOUT == kHalves8) {
-            const int turned = a.pairs / 8;
-            if (u >= turned) {  // behind the pairs: as it is
-                const int at = u + turned;
-                reinterpret_cast<uint4*>(dst)[at] = reinterpret_cast<const uint4*>(src)[at];
-                continue;
-            }
-            const uint4 x = reinterpret_cast<const uint4*>(src)[u];
-            const uint4 y = reinterpret_cast<const uint4*>(src)[u + turned];
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-            uint32_t xo[4], yo[4];
+    // slots of a tile: heads innermost
+    const int total = rows * heads;
+    int r = 0, h = tid / LANES;  // of the next slot
+    while (h >= heads && r < rows) h -= heads, ++r;
+    for (int i0 = tid / LANES; i0 < total; i0 += kBatch * kHeads) {
+        const uint16_t* src[kBatch];
+        uint16_t* dst[kBatch];
+        int row[kBatch];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 p = widen2<F16>(xs[e]), w = widen2<F16>(ys[e]);
-                const float2 lo = turn(p.x, w.x, cs[r][8 * u + 2 * e]);
-                const float2 hi = turn(p.y, w.y, cs[r][8 * u + 2 * e + 1]);
-                xo[e] = narrow2<F16>(lo.x, hi.x);
-                yo[e] = narrow2<F16>(lo.y, hi.y);
+        for (int k = 0; k < kBatch; ++k) {
+            row[k] = r < rows ? r : -1;
+            if (r >= rows) continue;
+            const bool key = h >= a.heads[0];
+            const int head = key ? h - a.heads[0] : h;
+            src[k] = (key ? a.in[1] : a.in[0]) +
+                     (row0 + r) * (key ? a.in_stride[1] : a.in_stride[0]) + head * D;
+            dst[k] = (key ? a.out[1] : a.out[0]) +
+                     (row0 + r) * (key ? a.out_stride[1] : a.out_stride[0]) + head * D;
+            for (h += kHeads; h >= heads && r < rows; ++r) h -= heads;
+        }
+        if constexpr (LAYOUT == kInterleaved) {
+            uint4 x[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (row[k] >= 0) x[k] = reinterpret_cast<const uint4*>(src[k])[u];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+                if (row[k] >= 0)
+                    reinterpret_cast<uint4*>(dst[k])[u] =
+                        turn_piece<F16>(x[k], cs[row[k]], u, a.pairs);
+        } else if constexpr (LAYOUT == kHalves8) {
+            const int second = u + turned;
+            uint4 x[kBatch], y[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                if (row[k] < 0) continue;
+                if (u < turned) x[k] = reinterpret_cast<const uint4*>(src[k])[u];
+                y[k] = reinterpret_cast<const uint4*>(src[k])[second];
             }
-            reinterpret_cast<uint4*>(dst)[u] = make_uint4(xo[0], xo[1], xo[2], xo[3]);
-            reinterpret_cast<uint4*>(dst)[u + turned] = make_uint4(yo[0], yo[1], yo[2], yo[3]);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                if (row[k] < 0) continue;
+                if (u < turned) {
+                    const uint32_t xs[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                    const uint32_t ys[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
+                    uint32_t xo[4], yo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 p = widen2<F16>(xs[e]), w = widen2<F16>(ys[e]);
+                        const float2 lo = turn(p.x, w.x, cs[row[k]][8 * u + 2 * e]);
+                        const float2 hi = turn(p.y, w.y, cs[row[k]][8 * u + 2 * e + 1]);
+                        xo[e] = narrow2<F16>(lo.x, hi.x);
+                        yo[e] = narrow2<F16>(lo.y, hi.y);
+                    }
+                    reinterpret_cast<uint4*>(dst[k])[u] = make_uint4(xo[0], xo[1], xo[2], xo[3]);
+                    y[k] = make_uint4(yo[0], yo[1], yo[2], yo[3]);
+                }
+                reinterpret_cast<uint4*>(dst[k])[second] = y[k];
+            }
         } else {
             // four channels a lane, their partners read one by one: all lanes of the
             // head have read before any writes (the output may be the input)
-            const uint2 own = reinterpret_cast<const uint2*>(src)[u];
+            static_assert(LAYOUT != kHalves || (LANES == 32 && kBatch == 1), "a warp a head");
+            if (row[0] < 0) continue;  // (all of the warp)
+            const float2* turns = cs[row[0]];
+            const uint2 own = reinterpret_cast<const uint2*>(src[0])[u];
             float x[4], y[4] = {};
             const float2 lo = widen2<F16>(own.x), hi = widen2<F16>(own.y);
             x[0] = lo.x, x[1] = lo.y, x[2] = hi.x, x[3] = hi.y;
@@ -129,19 +166,29 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int tile_row
             for (int e = 0; e < 4; ++e) {
                 const int c = 4 * u + e;
                 if (c < 2 * a.pairs)
-                    y[e] = widen2<F16>(src[c < a.pairs ? c + a.pairs : c - a.pairs]).x;
+                    y[e] = widen2<F16>(src[0][c < a.pairs ? c + a.pairs : c - a.pairs]).x;
             }
             __syncwarp();
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int c = 4 * u + e;
-                if (c < a.pairs) x[e] = turn(x[e], y[e], cs[r][c]).x;
-                else if (c < 2 * a.pairs) x[e] = turn(y[e], x[e], cs[r][c - a.pairs]).y;
+                if (c < a.pairs) x[e] = turn(x[e], y[e], turns[c]).x;
+                else if (c < 2 * a.pairs) x[e] = turn(y[e], x[e], turns[c - a.pairs]).y;
             }
-            reinterpret_cast<uint2*>(dst)[u] =
+            reinterpret_cast<uint2*>(dst[0])[u] =
                 make_uint2(narrow2<F16>(x[0], x[1]), narrow2<F16>(x[2], x[3]));
         }
     }
+}
+
+template <bool F16>
+void launch_rope(const RopeArgs& a, bool interleaved, dim3 grid, int tile, cudaStream_t s) {
+    // (halves of whole heads: eight threads each have all of it)
+    auto kernel = interleaved        ? rope_kernel<F16, kInterleaved, 16>
+                  : a.pairs == 64    ? rope_kernel<F16, kHalves8, 8>
+                  : a.pairs % 8 == 0 ? rope_kernel<F16, kHalves8, 16>
+                                     : rope_kernel<F16, kHalves, 32>;
+    launch_pdl(kernel, grid, dim3(kThreads), 0, s, a, tile);
 }
 
 }  // namespace
@@ -204,14 +251,9 @@ extern "C" kda_status kda_attn_rope(const void* q, const void* k, void* q_out, v
     a.rows = rows, a.positions = positions, a.inv_freq = inv_freq;
     a.axes = axes, a.pairs = pairs, a.factor = factor;
     // eight rows share the frequencies; with few rows, one each
-    const int tile = rows >= 8 * 152 ? 8 : 1;
+    const int tile = rows >= kRowsTile * 152 ? kRowsTile : 1;
     const dim3 grid((unsigned)((rows + tile - 1) / tile));
-    const bool f16 = in_dtype == KDA_F16;
-    auto kernel = f16 ? rope_kernel<true, kHalves> : rope_kernel<false, kHalves>;
-    if (interleaved)
-        kernel = f16 ? rope_kernel<true, kInterleaved> : rope_kernel<false, kInterleaved>;
-    else if (pairs % 8 == 0)
-        kernel = f16 ? rope_kernel<true, kHalves8> : rope_kernel<false, kHalves8>;
-    launch_pdl(kernel, grid, dim3(kThreads), 0, as_stream(stream), a, tile);
+    if (in_dtype == KDA_F16) launch_rope<true>(a, interleaved, grid, tile, as_stream(stream));
+    else launch_rope<false>(a, interleaved, grid, tile, as_stream(stream));
     return launch_result(fn);
 }
