@@ -61,10 +61,22 @@ constexpr int kStateFloats = D * D;
 //      many chains, none of them longer than 0.6 of a CTA's share.
 //  kEven: chains one after the other, cut into equal pieces.
 enum Kind { kPadded, kWhole, kEven };
+// Part of one chain: chunks [from, to) of the `of` that head h of sequence n has.
+struct Segment {
+    int n, h, from, to, of;
+};
 struct Plan {
     Kind kind;
     int piece;        // chunks of a piece
     long long total;  // chunks, or (kPadded) pieces
+
+    // Pieces of a segment's chain in front of its last one, at most.
+    __device__ __forceinline__ int chain_folds(const Segment& s) const { return s.of / piece + 1; }
+    // The piece in which a chain begins, of whose chunks piece i starts with number `from`.
+    __device__ __forceinline__ int chain_begin(int i, int from) const {
+        return kind == kPadded ? i - from / piece
+                               : (int)(((long long)i * piece - from) / piece);
+    }
 };
 struct Work {
     Args a;
@@ -73,8 +85,13 @@ struct Work {
     // adds to the state, then the state in front of the next piece
     float* sum;      // [pieces][128 * 128]
     float* log_sum;  // [pieces] log2 of the segment's decay
-    float* start;    // [pieces] the state in front of a cut chain that starts there
+    float* start;    // [pieces] the state in front of a cut chain that starts there, where
+                     // state_out is state_in
+    float* folded;   // [pieces] the state in front of a piece
 };
+// A segment's state is summed up where it is wanted from at most so many pieces before it
+// (a microsecond each); of longer chains by lin_join_kernel.
+constexpr int kMostFolds = 9;
 
 __device__ __forceinline__ int chunks_of(const Args& a, int n) {
     lin::Rows r;
@@ -121,11 +138,6 @@ __device__ __forceinline__ Plan make_plan(const Work& w) {
     }
     return p;
 }
-
-// Part of one chain: chunks [from, to) of the `of` that head h of sequence n has.
-struct Segment {
-    int n, h, from, to, of;
-};
 
 // The chain that unit x falls in (units: chunks, or for kPadded pieces), x below the
 // total; returns x's number within it.  One warp.
@@ -257,8 +269,12 @@ __device__ __forceinline__ bool open_segment(const Work& w, const Plan& p, int i
 // V.
 constexpr int kThreads = 512;
 constexpr uint32_t kTile = C * D * 2;         // 32 KB
-constexpr uint32_t kStage = 3 * kTile;        // Q, K, V; later lo, K, hi
-constexpr uint32_t kStateTile = 2 * kStage;   // S in 16 bits
+// Two stages of Q, K, V (later lo, K, hi) and S in 16 bits; SUM: three of K, V (K, hi) and lo.
+constexpr uint32_t kStage = 3 * kTile, kSumStage = 2 * kTile;
+constexpr uint32_t kStateTile = 2 * kStage;
+static_assert(3 * kSumStage == kStateTile, "lo where S is otherwise");
+template <bool SUM>
+constexpr int kStages = SUM ? 3 : 2;
 constexpr uint32_t kTmemP = 0, kTmemQS = 128, kTmemPV = 256, kTmemKW = 384;
 constexpr int kRing = 2;
 
@@ -266,16 +282,17 @@ struct Item {
     long long row;  // of the segment's first token
     int rows, h;
     int chunks;     // 0: no more segments
-    const float* src;  // the state in front; null: zeros
+    const float* src;  // the state in front; null: zeros (SUM: a state to be copied)
+    int fold, folds;   // pieces whose sums go on top: the first one, how many
     float* dst;        // where the state behind goes; null: nowhere
 };
 
 struct Shared {
-    uint64_t full[2], empty[2];
-    uint64_t qk_ready, p_ready, pv_ready, s16_ready, qs_ready, o_read;
+    uint64_t full[3], empty[3];
+    uint64_t qk_ready, pv_ready, s16_ready, qs_ready, o_read;
     // by chunk parity, where one side may be a chunk ahead of the other's wait
-    uint64_t v_checked[2], w_ready[2], kw_ready[2];
-    uint64_t token_sync, half_sync[2], state_sync;
+    uint64_t p_ready[2], v_checked[2], w_ready[2], kw_ready[2];
+    uint64_t token_sync, state_sync;
     uint64_t item_full[kRing], item_empty[kRing];
     Item item[kRing];
     uint32_t tmem;
@@ -287,8 +304,8 @@ struct Shared {
     float front[C];        // scale * the decay from the chunk's start to each token
     float later[2][4];     // decay of the blocks behind each block
     float total[2];        // sum of the chunk
-    float block[2][2][4];  // sums of blocks (SUM: for warps 4..7, 8..11)
-    float largest[2][8];   // FP16: of S, each warp's; SUM: of V
+    float block[2][4];     // sums of blocks
+    float largest[2][8];   // FP16: of S (SUM: of V), each warp's
     uint32_t most_v[2][2]; // FP16: the largest magnitude in each half of V
     // V's infinities and NaN, by chunk parity: each column's first token (255: none)
     uint32_t bad_first[2][D / 4];
@@ -378,12 +395,24 @@ __device__ __forceinline__ void copy_role(const Work& w, Shared& sh, unsigned ch
             const size_t chain = ((size_t)s.n * a.heads + s.h) * kStateFloats;
             if (SUM) {
                 it.dst = w.sum + (size_t)piece * kStateFloats;
+                // the state in front of a chain that is cut is kept where the chain's end
+                // may be written before its beginning is read
+                if (s.from == 0 && a.state_in && a.state_in == a.state_out)
+                    it.src = a.state_in + chain;
                 done = true;
             } else {
-                // (of a cut chain lin_join_kernel's copy: state_out may be state_in)
-                if (s.from) it.src = w.sum + (size_t)(piece - 1) * kStateFloats;
-                else if (s.to < s.of) it.src = w.start + (size_t)piece * kStateFloats;
-                else it.src = a.state_in ? a.state_in + chain : nullptr;
+                // (of a cut chain a copy of it: state_out may be state_in)
+                const int begin = s.from ? plan.chain_begin(piece, s.from) : piece;
+                // (lin_join_kernel's chains: by their last piece)
+                const int folds = piece - begin;
+                const bool joined = s.from && plan.chain_folds(s) > kMostFolds;
+                if (joined)
+                    it.src = w.sum + (size_t)(piece - 1) * kStateFloats;
+                else if (s.to - s.from < s.of && a.state_in && a.state_in == a.state_out)
+                    it.src = w.start + (size_t)begin * kStateFloats;
+                else
+                    it.src = a.state_in ? a.state_in + chain : nullptr;
+                if (s.from && !joined) it.fold = begin, it.folds = folds;
                 if (s.to == s.of && a.state_out) it.dst = a.state_out + chain;
             }
         }
@@ -405,26 +434,24 @@ __device__ __forceinline__ void copy_role(const Work& w, Shared& sh, unsigned ch
                      wait_long(sh, &sh.empty[stage], phase ^ 1);
                 if (!go) break;
                 mbar_arrive_expect_tx(&sh.full[stage], SUM ? 2 * kTile : 3 * kTile);
-                unsigned char* dst = sm + stage * kStage;
+                unsigned char* k_tile = sm + (SUM ? stage * kSumStage : stage * kStage + kTile);
                 const int row = (int)(it.row + (long long)c * C);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
+                    unsigned char* dst = k_tile + half * (kTile / 2);
                     if (!SUM)
-                        tma_load_3d(dst + half * (kTile / 2), mq, &sh.full[stage], 64 * half, hq,
-                                    row);
-                    tma_load_3d(dst + kTile + half * (kTile / 2), mk, &sh.full[stage], 64 * half,
-                                hq, row);
-                    tma_load_3d(dst + 2 * kTile + half * (kTile / 2), mv, &sh.full[stage],
-                                64 * half, it.h, row);
+                        tma_load_3d(dst - kTile, mq, &sh.full[stage], 64 * half, hq, row);
+                    tma_load_3d(dst, mk, &sh.full[stage], 64 * half, hq, row);
+                    tma_load_3d(dst + kTile, mv, &sh.full[stage], 64 * half, it.h, row);
                 }
-                if (++stage == 2) stage = 0, phase ^= 1;
+                if (++stage == kStages<SUM>) stage = 0, phase ^= 1;
             }
         }
         go = __shfl_sync(0xffffffffu, go, 0);
     }
     // copies in flight must land before the CTA's memory goes away
     if (lane == 0 && *(volatile int*)&sh.stop)
-        for (int s = 0; s < 2; ++s)
+        for (int s = 0; s < kStages<SUM>; ++s)
             mbar_wait(&sh.full[s], s < stage ? phase : phase ^ 1, 1 << 12);
 }
 
@@ -466,15 +493,17 @@ __device__ __forceinline__ void product_role(Shared& sh, unsigned char* sm) {
         if (!wait_warp(sh, &sh.full[0], 0)) return;
         qk(0);
     }
+    int stage = 0;
     for (int n = 0; left > 0; ++n) {
-        const int stage = n & 1;
         const uint32_t odd = n & 1, pair = n >> 1 & 1;
         const uint64_t q = k_major + stage * (kStage >> 4);
-        const uint64_t q_mn = mn_major + stage * (kStage >> 4), k_mn = q_mn + kT, v_mn = k_mn + kT;
+        const uint64_t k_mn =
+            mn_major + (SUM ? stage * (kSumStage >> 4) : stage * (kStage >> 4) + kT);
+        const uint64_t v_mn = k_mn + kT, lo_mn = SUM ? state : k_mn - kT;
         if (!SUM) {
             if (n && !wait_warp(sh, &sh.o_read, odd ^ 1)) return;
             if (!wait_warp(sh, &sh.v_checked[odd], pair)) return;
-            if (!wait_warp(sh, &sh.p_ready, odd)) return;
+            if (!wait_warp(sh, &sh.p_ready[odd], pair)) return;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
@@ -513,11 +542,12 @@ __device__ __forceinline__ void product_role(Shared& sh, unsigned char* sm) {
 #pragma unroll
             for (int s = 0; s < 8; ++s) mma_f16(to, k_mn + s * 128, v_mn + s * 128, kTT, s > 0);
 #pragma unroll
-            for (int s = 0; s < 8; ++s) mma_f16(to, k_mn + s * 128, q_mn + s * 128, kTT, true);
+            for (int s = 0; s < 8; ++s) mma_f16(to, k_mn + s * 128, lo_mn + s * 128, kTT, true);
             mma_commit(&sh.kw_ready[odd]);
             mma_commit(&sh.empty[stage]);
         }
         __syncwarp();
+        if (++stage == kStages<SUM>) stage = 0;
     }
 }
 
@@ -573,8 +603,9 @@ __device__ __forceinline__ void store_8(float* to, const float* s) {
     }
 }
 
-// Warps 0..3, a thread a token: a chunk's weights P, and the decays that state_role takes.
-template <bool F16>
+// Warps 0..3, a thread a token: a chunk's weights P, and the decays that state_role takes
+// (SUM: these alone).
+template <bool F16, bool SUM>
 __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned char* sm) {
     const Args& a = w.a;
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -588,6 +619,8 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
 #pragma unroll 1
         for (int c = 0; c < it.chunks; ++c, ++n) {
             const uint32_t odd = n & 1;
+            // (SUM: state_role is through with the last but one chunk's decays)
+            if (SUM && n > 1 && !wait_warp(sh, &sh.w_ready[odd], (n - 2) >> 1 & 1)) return;
             const float g = log2_decay(next_g);
             // sums within the block: up to the token, and behind it
             float sum = g, tail = g;
@@ -601,7 +634,7 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
             tail = __shfl_down_sync(0xffffffffu, tail, 1);
             if (lane == 31) {
                 tail = 0.f;
-                sh.block[0][odd][warp] = sum;
+                sh.block[odd][warp] = sum;
             }
             sh.sum[t] = -sum;
             sh.tail[odd][t] = ex2_approx(tail);
@@ -610,13 +643,17 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
             float before = 0.f, behind = 0.f, total = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float x = sh.block[0][odd][i];
+                const float x = sh.block[odd][i];
                 if (i < warp) before += x;
                 if (i > warp) behind += x;
                 total += x;
             }
             if (lane == 0) sh.later[odd][warp] = ex2_approx(behind);
             if (t == 0) sh.total[odd] = total;
+            if (SUM) {
+                arrive_warp(&sh.p_ready[odd]);
+                continue;
+            }
 
             if (!wait_warp(sh, &sh.qk_ready, odd)) return;
             tc_fence_after();
@@ -647,7 +684,7 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
                             reinterpret_cast<const float4*>(sh.tail[odd] + 32 * b);
                         float from = sum;  // from the end of block b
 #pragma unroll 1
-                        for (int k = warp - 1; k > b; --k) from += sh.block[0][odd][k];
+                        for (int k = warp - 1; k > b; --k) from += sh.block[odd][k];
                         from = ex2_approx(from);
                         const float2 f2 = make_float2(from, from);
                         tmem_ld_wait();
@@ -684,7 +721,7 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
             // the same)
             if (n && !wait_warp(sh, &sh.o_read, odd ^ 1)) return;
             sh.front[t] = ex2_approx(before + sum) * a.scale;
-            arrive_warp(&sh.p_ready);
+            arrive_warp(&sh.p_ready[odd]);
         }
     }
 }
@@ -821,16 +858,57 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
     Items items;
     Item it;
     int n = 0;
-    uint32_t half_phase = 0, state_phase = 0;
+    int stage = 0;
+    uint32_t state_phase = 0, stage_phase = 0;
     while (items.next(sh, it)) {
         float s[64];
         {
-            const float* from = SUM || !it.src ? nullptr : it.src + r * D + half * 64;
+            const float* from = it.src;
+            if (!SUM && it.folds) {
+                // in the order of memory: a row a thread takes three times as long
+                const int at = threadIdx.x - 128;
+                float4 x[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    x[i] = from ? __ldcg(reinterpret_cast<const float4*>(from) + at + 256 * i)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+                for (int k = it.fold; k < it.fold + it.folds; ++k) {
+                    const float d = exp2f(__ldcg(w.log_sum + k));
+                    const float4* add =
+                        reinterpret_cast<const float4*>(w.sum + (size_t)k * kStateFloats) + at;
+#pragma unroll
+                    for (int i = 0; i < 16; i += 8) {
+                        float4 y[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = __ldcg(add + 256 * (i + e));
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            x[i + e].x = fmaf(d, x[i + e].x, y[e].x);
+                            x[i + e].y = fmaf(d, x[i + e].y, y[e].y);
+                            x[i + e].z = fmaf(d, x[i + e].z, y[e].z);
+                            x[i + e].w = fmaf(d, x[i + e].w, y[e].w);
+                        }
+                    }
+                }
+                float* to = w.folded + (size_t)blockIdx.x * kStateFloats;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) reinterpret_cast<float4*>(to)[at + 256 * i] = x[i];
+                if (!sync_warps(sh, &sh.state_sync, state_phase)) return;
+                from = to;
+            }
 #pragma unroll
             for (int i = 0; i < 64; ++i) s[i] = 0.f;
             if (from) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) load_8(from + 8 * i, s + 8 * i);
+                for (int i = 0; i < 8; ++i) load_8(from + r * D + half * 64 + 8 * i, s + 8 * i);
+            }
+            if (SUM && from) {  // only to be copied
+                float* to = w.start + (size_t)blockIdx.x * kStateFloats + r * D + half * 64;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) store_8(to + 8 * i, s + 8 * i);
+#pragma unroll
+                for (int i = 0; i < 64; ++i) s[i] = 0.f;
             }
         }
         float decay = 1.f, unit = 1.f, all = 0.f;  // of the last chunk; of the segment
@@ -858,40 +936,27 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
             tc_fence_before();
             return true;
         };
-        float next_g = SUM ? load_g(a, it, r) : 0.f;
 #pragma unroll 1
         for (int c = 0; c < it.chunks; ++c, ++n) {
             const uint32_t odd = n & 1;
             const int there = min(C, it.rows - c * C);
-            unsigned char* q_half = sm + (n & 1) * kStage + half * (kTile / 2);
-            unsigned char* v_half = q_half + 2 * kTile;
+            unsigned char* const k_half =
+                sm + (SUM ? stage * kSumStage : stage * kStage + kTile) + half * (kTile / 2);
+            unsigned char* const v_half = k_half + kTile;
             unsigned char* const state_half = sm + kStateTile + half * (kTile / 2);
+            unsigned char* const lo_half = SUM ? state_half : k_half - kTile;
             float f = 0.f, total = 0.f;  // decays from the token on, and of the chunk
             if (SUM) {
-                float tail = log2_decay(next_g);
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const float down = __shfl_down_sync(0xffffffffu, tail, off);
-                    if (lane + off < 32) tail += down;
-                }
-                if (lane == 0) sh.block[half][odd][warp] = tail;
-                tail = __shfl_down_sync(0xffffffffu, tail, 1);
-                if (lane == 31) tail = 0.f;
-                if (!sync_warps(sh, &sh.half_sync[half], half_phase)) return;
-#pragma unroll
-                for (int b = 3; b >= 0; --b) {
-                    const float x = sh.block[half][odd][b];
-                    if (b > warp) tail += x;
-                    total += x;
-                }
-                f = ex2_approx(tail);
-                next_g = load_g(a, it, (c + 1) * C + r);
+                if (!wait_warp(sh, &sh.p_ready[odd], n >> 1 & 1)) return;
+                total = sh.total[odd];
+                f = sh.tail[odd][r] * sh.later[odd][warp];
             }
-            if (SUM && !wait_warp(sh, &sh.full[n & 1], n >> 1 & 1)) return;
+            if (SUM && !wait_warp(sh, &sh.full[stage], stage_phase)) return;
+            if (++stage == kStages<SUM>) stage = 0, stage_phase ^= 1;
             if (SUM && r >= there) {  // (token_role does it otherwise)
 #pragma unroll 1
                 for (int i = 0; i < 8; ++i) {
-                    *piece_of(q_half + kTile, r, i) = make_uint4(0, 0, 0, 0);
+                    *piece_of(k_half, r, i) = make_uint4(0, 0, 0, 0);
                     *piece_of(v_half, r, i) = make_uint4(0, 0, 0, 0);
                 }
             }
@@ -958,7 +1023,7 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
                     f *= v_inverse;
                 }
             }
-            // W: hi over V, then lo over Q once that is through
+            // W: hi over V, then lo over Q (SUM: over the last lo) once that is through
             auto split = [&](int i, uint4& lo) {
                 uint4* at = piece_of(v_half, r, i);
                 const uint4 v = *at;
@@ -974,19 +1039,18 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
                 *at = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 lo = make_uint4(rest[0], rest[1], rest[2], rest[3]);
             };
-            if constexpr (SUM) {
-#pragma unroll 2
-                for (int i = 0; i < 8; ++i) split(i, *piece_of(q_half, r, i));
-            } else {
-                uint4 lo[8];
+            uint4 lo[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) split(i, lo[i]);
+            for (int i = 0; i < 8; ++i) split(i, lo[i]);
+            if (!SUM) {
                 if (*(volatile int*)&sh.bad[odd])
                     put_back_nan<F16>(v_half, sh.bad_first[odd], half, r);
                 if (!wait_warp(sh, &sh.qs_ready, odd)) return;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) *piece_of(q_half, r, i) = lo[i];
+            } else if (c) {  // the last chunk's lo
+                if (!wait_warp(sh, &sh.kw_ready[odd ^ 1], (n - 1) >> 1 & 1)) return;
             }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) *piece_of(lo_half, r, i) = lo[i];
             fence_async_smem();
             arrive_warp(&sh.w_ready[odd]);
             if (SUM && c && !add()) return;
@@ -1078,26 +1142,22 @@ lin_prefill_kernel(Work w, const __grid_constant__ CUtensorMap mq,
     }
     if (threadIdx.x == 0) {
         sh.stop = 0;
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], 1);
-            sh.bad[i] = sh.bad_seen[i] = 0;
-        }
+        for (int i = 0; i < 3; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
+        for (int i = 0; i < 2; ++i) sh.bad[i] = sh.bad_seen[i] = 0;
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sh.item_full[i], 1);
-            mbar_init(&sh.item_empty[i], SUM ? 9 : 15);
+            mbar_init(&sh.item_empty[i], SUM ? 13 : 15);
         }
         mbar_init(&sh.qk_ready, 1);
-        mbar_init(&sh.p_ready, 4);
         mbar_init(&sh.pv_ready, 2);
         mbar_init(&sh.s16_ready, 8);
         mbar_init(&sh.qs_ready, 1);
         mbar_init(&sh.o_read, 8);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.p_ready[i], 4);
             mbar_init(&sh.v_checked[i], 2);
             mbar_init(&sh.w_ready[i], 8);
             mbar_init(&sh.kw_ready[i], 1);
-            mbar_init(&sh.half_sync[i], 4);
         }
         mbar_init(&sh.token_sync, 4);
         mbar_init(&sh.state_sync, 8);
@@ -1121,7 +1181,7 @@ lin_prefill_kernel(Work w, const __grid_constant__ CUtensorMap mq,
         state_role<F16, SUM>(w, sh, sm, &mo);
         if (!SUM) bulk_wait_all();  // rows of O on their way (lane 0's)
     } else if (warp < 4) {
-        if (!SUM) token_role<F16>(w, sh, sm);
+        token_role<F16, SUM>(w, sh, sm);
     } else if (!SUM) {
         check_role<F16>(sh, sm, warp - 14);
     }
@@ -1165,7 +1225,7 @@ __global__ void __launch_bounds__(kJoinThreads) lin_join_kernel(Work w) {
     const Plan p = make_plan(w);
     const int i = blockIdx.x;
     Segment s;
-    if (!open_segment(w, p, i, s) || s.from) return;
+    if (!open_segment(w, p, i, s) || s.from || p.chain_folds(s) <= kMostFolds) return;
     // pieces whose last segment is this chain's and open
     int last = i + padded(s.of) - 2;
     if (p.kind == kEven) {
@@ -1176,7 +1236,6 @@ __global__ void __launch_bounds__(kJoinThreads) lin_join_kernel(Work w) {
     const size_t chain = ((size_t)s.n * a.heads + s.h) * kStateFloats;
     float4 x = a.state_in ? __ldcg(reinterpret_cast<const float4*>(a.state_in + chain) + at)
                           : make_float4(0.f, 0.f, 0.f, 0.f);
-    reinterpret_cast<float4*>(w.start + (size_t)i * kStateFloats)[at] = x;
     float4* sums = reinterpret_cast<float4*>(w.sum) + at;
     // (eight loads in flight: a load may not pass the stores before it by itself)
     constexpr int kBatch = 8;
@@ -1214,7 +1273,7 @@ cudaError_t status_word_lin(unsigned** word) {
 }
 
 size_t lin_chunked_workspace_bytes(long long rows, int n_seqs, int heads) {
-    return (size_t)most_pieces(rows, n_seqs, heads) * (2 * kStateFloats + 4) * sizeof(float);
+    return (size_t)most_pieces(rows, n_seqs, heads) * (3 * kStateFloats + 4) * sizeof(float);
 }
 
 kda_status launch_lin_chunked(const Args& a, bool f16, void* workspace, cudaStream_t s) {
@@ -1227,7 +1286,8 @@ kda_status launch_lin_chunked(const Args& a, bool f16, void* workspace, cudaStre
     w.pieces = std::min(slots, sms);
     w.sum = static_cast<float*>(workspace);
     w.start = w.sum + (size_t)slots * kStateFloats;
-    w.log_sum = w.start + (size_t)slots * kStateFloats;
+    w.folded = w.start + (size_t)slots * kStateFloats;
+    w.log_sum = w.folded + (size_t)slots * kStateFloats;
     CUtensorMap mq, mk, mv, mo;
     KDA_REQUIRE(tma_map_heads(&mq, a.q, a.qk_heads, rows, a.q_stride, 1, C, f16) &&
                     tma_map_heads(&mk, a.k, a.qk_heads, rows, a.k_stride, 1, C, f16) &&
@@ -1248,6 +1308,9 @@ kda_status launch_lin_chunked(const Args& a, bool f16, void* workspace, cudaStre
     } else {
         cut = !(chains >= 2LL * w.pieces && 10 * longest * w.pieces <= 6 * longest * chains);
     }
+    // (a piece has at least a share of the longest sequence's chunks)
+    const long long least = std::max<long long>(kLeastPiece, longest * a.heads / w.pieces);
+    const bool join = longest / least + 1 > kMostFolds;
     auto kernel = f16 ? lin_prefill_kernel<true, false> : lin_prefill_kernel<false, false>;
     auto sums = f16 ? lin_prefill_kernel<true, true> : lin_prefill_kernel<false, true>;
     for (auto k : {kernel, sums}) {
@@ -1260,8 +1323,9 @@ kda_status launch_lin_chunked(const Args& a, bool f16, void* workspace, cudaStre
     }
     if (cut) {
         launch_pdl(sums, dim3(grid), dim3(kThreads), kSmemBytes, s, w, mq, mk, mv, mo);
-        launch_pdl(lin_join_kernel, dim3(grid, kStateFloats / 4 / kJoinThreads),
-                   dim3(kJoinThreads), 0, s, w);
+        if (join)
+            launch_pdl(lin_join_kernel, dim3(grid, kStateFloats / 4 / kJoinThreads),
+                       dim3(kJoinThreads), 0, s, w);
     }
     launch_pdl(kernel, dim3(grid), dim3(kThreads), kSmemBytes, s, w, mq, mk, mv, mo);
     return launch_result(fn);
