@@ -22,6 +22,7 @@ Linear attention with a decay for each head: ``kda_lin_prefill``, ``kda_lin_deco
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -678,6 +679,22 @@ _device = torch._C._cuda_getDevice
 _I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
 
 
+def _load_fast():
+    """The calls below in C, for arguments that are as they should be; for others each
+    returns -1 and calls nothing, and the Python code says what is wrong."""
+    spec = importlib.util.spec_from_file_location("fast_calls", _build.FAST)
+    fast = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(fast)
+    names = ("kda_lin_prefill", "kda_lin_decode", "kda_attn_rope", "kda_attn_kv4_resize",
+             "kda_attn_kv4_fork", "kda_attn_kv4_compact", "kda_attn_kv4_copy")
+    fast.setup(tuple(_c.cast(getattr(LIB, name), _vp).value for name in names),
+               (torch.bfloat16, torch.float16, _F32, _I32, _U8), _raw_stream, _device)
+    return fast
+
+
+_fast = _load_fast()
+
+
 def _call(dev, fn, *args):
     """`fn` on device `dev`'s current stream."""
     if _device() == dev:
@@ -715,6 +732,9 @@ def kda_attn_rope(q, k, positions, inv_freq, q_out=None, k_out=None, pair_axis=N
     pair_axis: the axis of each pair (a sequence of pairs numbers), needed with
     several axes.  interleaved: a pair is two neighbours, else channels p and
     p + pairs; channels behind the pairs stay."""
+    status = _fast.rope(q, k, positions, inv_freq, q_out, k_out, pair_axis, interleaved, factor)
+    if status >= 0:
+        return _check(status)
     in_dtype, dev = _attn_type(q, "q")
     dt, shape = q.dtype, q.shape
     q_ptr, q_row = _rows(q, dt, dev, "q")
@@ -775,6 +795,9 @@ def kda_attn_kv4_resize(page_table, lens, refs, page=64, workspace=None):
     """Gives and frees pages in place, so that each sequence has those of its lens
     positions: page_table device int32 [N, max_pages] (-1: none), lens [N], refs
     [pages of the cache], how often each page is named (0: free)."""
+    status = _fast.resize(page_table, lens, refs, page, workspace)
+    if status >= 0:
+        return _check(status)
     table, shape, refs_ptr, n, dev, workspace, ws, ws_bytes = _pages(page_table, refs, workspace)
     _call(dev, LIB.kda_attn_kv4_resize, table, _array(lens, _I32, dev, shape[:1], "lens"), refs_ptr,
           shape[0], shape[1], n[0], page, ws, ws_bytes)
@@ -791,6 +814,11 @@ def kda_attn_kv4_fork(page_table, lens, refs, parent, page_table_out=None, lens_
     """Sequence n goes on from sequence parent[n] (device int32 [N]; -1: it ends).
     The outputs default to being in place.  Returns (src, dst, count), the pages for
     kda_attn_kv4_copy: device int32 [N], [N] and [1], allocated where not given."""
+    status = _fast.fork(page_table, lens, refs, parent, page_table_out, lens_out, refs_out, src, dst,
+                        count, page, workspace)
+    if status >= 0:
+        _check(status)
+        return src, dst, count
     table, shape, refs_ptr, n, dev, workspace, ws, ws_bytes = _pages(page_table, refs, workspace)
     rows = shape[:1]
     src, dst, count = _lists(src, dst, count, rows[0], dev)
@@ -811,6 +839,10 @@ def kda_attn_kv4_compact(page_table, refs, page_table_out=None, refs_out=None, s
     """Makes the pages in use the lowest-numbered ones.  The outputs default to being
     in place.  Returns (src, dst, count), the moves for kda_attn_kv4_copy: device
     int32 [pages // 2] twice and [1], allocated where not given."""
+    status = _fast.compact(page_table, refs, page_table_out, refs_out, src, dst, count, workspace)
+    if status >= 0:
+        _check(status)
+        return src, dst, count
     table, shape, refs_ptr, n, dev, workspace, ws, ws_bytes = _pages(page_table, refs, workspace)
     half = (n[0] // 2,)
     src, dst, count = _lists(src, dst, count, half[0], dev)
@@ -827,6 +859,9 @@ def kda_attn_kv4_copy(caches, src, dst, count):
     """Copies pages src[i] to dst[i], i < count, in each of `caches` (one 4-bit cache, or a
     list of them, one for each layer, all of one shape); src and dst device int32
     [n], count [1]."""
+    status = _fast.copy(caches, src, dst, count)
+    if status >= 0:
+        return _check(status)
     caches = [caches] if isinstance(caches, torch.Tensor) else list(caches)
     if not 1 <= len(caches) <= KV4_MAX_CACHES:
         raise ValueError("kda_attn_kv4_copy: 1 to %d caches" % KV4_MAX_CACHES)
@@ -902,6 +937,9 @@ def kda_lin_prefill(q, k, v, g, out, state_in=None, state_out=None, t=None, cu_s
     cu_seqlens (device int32 [N+1]) gives packed sequences; without it, four
     dimensions [N, T, heads, 128] hold N sequences and three one, of t tokens each
     (default: all) with the rows behind them left alone."""
+    status = _fast.lin_prefill(q, k, v, g, out, state_in, state_out, t, cu_seqlens, scale, workspace)
+    if status >= 0:
+        return _check(status)
     in_dtype, dev, ptrs, strides, lead, heads, qk_heads = _lin_rows("kda_lin_prefill", q, k, v, g,
                                                                     out)
     cu = None
@@ -929,6 +967,9 @@ def kda_lin_decode(q, k, v, g, out, state_in=None, state_out=None, snapshots=(),
     [N, k, heads, 128] (or without k: one token), g FP32 [N, k, heads] or [heads];
     states as kda_lin_prefill's; snapshots: up to k tensors like the states,
     snapshots[t] = state after row t."""
+    status = _fast.lin_decode(q, k, v, g, out, state_in, state_out, snapshots, scale)
+    if status >= 0:
+        return _check(status)
     in_dtype, dev, ptrs, strides, lead, heads, qk_heads = _lin_rows("kda_lin_decode", q, k, v, g,
                                                                     out)
     n_seqs, krows = lead if len(lead) == 2 else (lead[0], 1)

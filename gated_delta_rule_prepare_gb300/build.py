@@ -1,7 +1,9 @@
 """Builds libkda.so in-tree from csrc/*.cu for sm_103a (nvcc, no cmake).
 
 Each translation unit compiles in parallel; the shared library links against
-the shared CUDA runtime so it shares one runtime with the host process.
+the shared CUDA runtime so it shares one runtime with the host process.  The
+binding's short calls (csrc/fast_calls.c) become a Python extension beside it (the host's C
+compiler, no library).
 """
 
 from __future__ import annotations
@@ -11,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libkda.so")
+FAST = os.path.join(OUT_DIR, "fast_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -32,14 +36,15 @@ def _cuda_lib_dir() -> str:
 
 def _inputs():
     return (sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+            + sorted(glob.glob(os.path.join(CSRC, "*.c")))
             + sorted(glob.glob(os.path.join(CSRC, "*.h")))
             + sorted(glob.glob(os.path.join(INCLUDE, "*.h"))))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(FAST):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(FAST))
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
@@ -63,6 +68,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
             raise RuntimeError("nvcc failed on %s:\n%s%s" % (src, r.stdout, r.stderr))
         return obj, r.stderr
 
+    fast = FAST + ".tmp%d" % os.getpid()
+    r = subprocess.run([shutil.which("cc") or "gcc", "-O2", "-fPIC", "-shared", "-I" + INCLUDE,
+                        "-I" + sysconfig.get_paths()["include"],
+                        os.path.join(CSRC, "fast_calls.c"), "-o", fast],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("cc failed on fast_calls.c:\n%s%s" % (r.stdout, r.stderr))
+
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
         results = list(ex.map(compile_one, srcs))
     if verbose:
@@ -75,6 +88,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
+    os.replace(fast, FAST)
     return LIB
 
 
