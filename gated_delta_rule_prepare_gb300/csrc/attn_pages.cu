@@ -142,8 +142,9 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(PageArgs a) {
     unsigned bad = 0;
     const Team::Slice s = t.slice(a.n_seqs * a.width);
     // Entries past a sequence's length give their pages up; missing ones are counted, and
-    // noted by bits, for as many steps as the mask has.
+    // the steps that have some noted (as far as the mask goes).
     int mine = 0;
+    unsigned long long steps = 0;
     auto missing = [&](int i, int v) {
         unsigned ignore = 0;
         const int n = i / a.width, col = i - n * a.width;
@@ -159,22 +160,25 @@ __global__ void __launch_bounds__(kThreads) resize_kernel(PageArgs a) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             const int i = i0 + 32 * k + t.lane;
-            if (i >= s.to) continue;
-            if (v[k] < -1 || v[k] >= a.n_pages) bad |= STATUS_BAD_PAGES;
-            if (i % a.width < a.held(a.clamped_len(len[k], bad))) {
-                if (a.names(v[k])) continue;
-                ++mine;
-            } else if (a.names(v[k])) {
-                atomicAdd(a.refs_out + v[k], -1);
+            bool miss = false;
+            if (i < s.to) {
+                if (v[k] < -1 || v[k] >= a.n_pages) bad |= STATUS_BAD_PAGES;
+                const bool wanted = i % a.width < a.held(a.clamped_len(len[k], bad));
+                const bool there = a.names(v[k]);
+                miss = wanted && !there;
+                if (!wanted && there) atomicAdd(a.refs_out + v[k], -1);
+                if (v[k] != -1 && !(wanted && there)) a.table_out[i] = -1;
             }
-            if (v[k] != -1) a.table_out[i] = -1;
+            const unsigned found = __ballot_sync(0xffffffffu, miss);
+            mine += __popc(found);
+            if (found) steps |= 1ull << min((i0 - s.from) / 32 + k, 63);
         }
     }
-    mine = __reduce_add_sync(0xffffffffu, mine);
     int wanted, at = t.before(mine, 0, wanted);
     if (wanted) {
         if (mine) {  // the entries in order
             for (int i0 = s.from; i0 < s.to; i0 += 32) {
+                if (!(steps >> min((i0 - s.from) / 32, 63) & 1)) continue;
                 const int i = i0 + t.lane;
                 const bool miss = i < s.to && missing(i, a.table_out[i]);
                 const unsigned all = __ballot_sync(0xffffffffu, miss);
