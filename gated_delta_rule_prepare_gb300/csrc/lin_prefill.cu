@@ -25,11 +25,16 @@
 //  - FP16 operands are scaled by powers of two that the largest entry of S, or of V,
 //    in the chunk gives: FP16's range is narrower than FP32 states are.
 //
-// Pieces.  Chains (heads of sequences) are cut where there are too few of them, or where
-// they are too uneven, for all multiprocessors.  A piece that starts inside a chain
-// needs the state there: lin_prefill_kernel<.., SUM> first adds up what each cut
-// segment contributes (K and V alone), and lin_join_kernel runs through a chain's
-// segments.  See Plan.
+// Pieces.  All chains (heads of sequences), one after the other, are cut into equal pieces,
+// one a CTA.  Where no chain is longer than a piece, a CTA works on the beginning of its last
+// chain first of all and hands the state on, and on the end of its first one last.
+// Longer chains, which lie in several pieces, need the state in front of them early:
+// lin_prefill_kernel<.., SUM> first adds up what each cut segment contributes (K and V
+// alone).  See Plan.
+//
+// A chunk takes 3.3 to 3.4 us, a CTA's first 7 us more and a change of chains 5: 16 prompts of
+// 512 to 8192 tokens, 32 heads (2.4 GB): 437 us, 5.5 TB/s.  One prompt of 8192 tokens, 32
+// heads (0.27 GB): 100 us, of these 38 for the sums.
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
@@ -57,18 +62,28 @@ constexpr int kStateFloats = D * D;
 
 // How the call's chunks go to `pieces` CTAs (at most kSms).
 //  kPadded: each chain starts a piece, pieces of kLeastPiece chunks: few chunks.
-//  kWhole: chains are not cut; sorted by length they are dealt out there and back:
-//      many chains, none of them longer than 0.6 of a CTA's share.
-//  kEven: chains one after the other, cut into equal pieces.
-enum Kind { kPadded, kWhole, kEven };
+//  kEven: chains one after the other, cut into equal pieces.  A chain counts kLead chunks
+//      more than it has, in front of its first one: what its states' load and store cost.
+//      (kLead 1: 16 prompts of 512 to 8192 tokens in this order, 32 heads, 462 us, 2: 422.)
+//  kHandOver: the same where no chain is longer than a piece, so that none lies in more
+//      than two, or where pieces as long as the longest chain cost less than sums do.
+//      (Whole chains dealt out by length: the same at many chains, but 114 us for 5 prompts
+//      of 2048 tokens, 32 heads, where this takes 87.)
+enum Kind { kPadded, kEven, kHandOver };
+constexpr int kLead = 2;
+// By the model 3.4 us a chunk and 12 in all, the sums 2 us a chunk and 12: 4 prompts of 2048
+// tokens, 32 heads, 78 us; cut into 152 pieces, with sums, 103.  (2 prompts: 74, and 67.)
+__host__ __device__ __forceinline__ bool hand_over(long long longest, long long piece) {
+    return longest + kLead <= piece + piece / 2 + 3;
+}
 // Part of one chain: chunks [from, to) of the `of` that head h of sequence n has.
 struct Segment {
     int n, h, from, to, of;
 };
 struct Plan {
     Kind kind;
-    int piece;        // chunks of a piece
-    long long total;  // chunks, or (kPadded) pieces
+    int piece;        // units of a piece: chunks, with chains' lead
+    long long total;  // units, or (kPadded) pieces
 
     // Pieces of a segment's chain in front of its last one, at most.
     __device__ __forceinline__ int chain_folds(const Segment& s) const { return s.of / piece + 1; }
@@ -88,6 +103,7 @@ struct Work {
     float* start;    // [pieces] the state in front of a cut chain that starts there, where
                      // state_out is state_in
     float* folded;   // [pieces] the state in front of a piece
+    unsigned* handed;  // [pieces] kHandOver: 1 once `sum` is the state of its last chain
 };
 // A segment's state is summed up where it is wanted from at most so many pieces before it
 // (a microsecond each); of longer chains by lin_join_kernel.
@@ -101,6 +117,10 @@ __device__ __forceinline__ int padded(int chunks) {
     return (chunks + kLeastPiece - 1) / kLeastPiece;
 }
 
+__device__ __forceinline__ int units(int chunks) { return chunks ? chunks + kLead : 0; }
+// The chunk in front of which unit u of a chain begins.
+__device__ __forceinline__ int chunk_at(int u) { return max(0, u - kLead); }
+
 // One warp; the same for all warps of the call.
 __device__ __forceinline__ Plan make_plan(const Work& w) {
     const Args& a = w.a;
@@ -109,12 +129,12 @@ __device__ __forceinline__ Plan make_plan(const Work& w) {
     int longest = 0;
     if (!a.cu) {
         longest = (a.t + C - 1) / C;
-        chunks = (long long)longest * a.n_seqs;
+        chunks = (long long)(longest + kLead) * a.n_seqs;
         pads = (long long)padded(longest) * a.n_seqs;
     } else {
         for (int n = lane; n < a.n_seqs; n += 32) {
             const int c = chunks_of(a, n);
-            chunks += c;
+            chunks += units(c);
             pads += padded(c);
             longest = max(longest, c);
         }
@@ -127,23 +147,21 @@ __device__ __forceinline__ Plan make_plan(const Work& w) {
     }
     chunks *= a.heads;
     pads *= a.heads;
-    Plan p;
-    if (pads <= w.pieces) {
-        p = {kPadded, kLeastPiece, pads};
-    } else if ((long long)a.n_seqs * a.heads >= 2LL * w.pieces &&
-               10LL * longest * w.pieces <= 6 * chunks) {
-        p = {kWhole, 0, chunks};
-    } else {
-        p = {kEven, (int)max((chunks + w.pieces - 1) / w.pieces, (long long)kLeastPiece), chunks};
-    }
-    return p;
+    const bool few = pads <= w.pieces;
+    if (few && (longest <= kLeastPiece || !hand_over(longest, kLeastPiece)))
+        return {kPadded, kLeastPiece, pads};
+    const int piece =
+        few ? kLeastPiece
+            : (int)max((chunks + w.pieces - 1) / w.pieces, (long long)kLeastPiece);
+    if (hand_over(longest, piece)) return {kHandOver, max(piece, units(longest)), chunks};
+    return {kEven, piece, chunks};
 }
 
-// The chain that unit x falls in (units: chunks, or for kPadded pieces), x below the
-// total; returns x's number within it.  One warp.
+// The chain that unit x falls in (for kPadded: that piece x is of), x below the total;
+// returns x's number within it.  One warp.
 __device__ __forceinline__ int find_chain(const Args& a, bool pads, long long x, int& n, int& h) {
     if (!a.cu) {
-        const int c = (a.t + C - 1) / C, u = pads ? padded(c) : c;
+        const int c = (a.t + C - 1) / C, u = pads ? padded(c) : units(c);
         const long long chain = x / u;
         n = (int)(chain / a.heads);
         h = (int)(chain - (long long)n * a.heads);
@@ -154,7 +172,7 @@ __device__ __forceinline__ int find_chain(const Args& a, bool pads, long long x,
         int u = 0;
         if (n0 + lane < a.n_seqs) {
             u = chunks_of(a, n0 + lane);
-            if (pads) u = padded(u);
+            u = pads ? padded(u) : units(u);
         }
         long long sum = (long long)u * a.heads;
 #pragma unroll
@@ -179,38 +197,38 @@ __device__ __forceinline__ int find_chain(const Args& a, bool pads, long long x,
     return 0;
 }
 
-// The i-th longest sequence (ties: the first one), for at most 64 sequences; in more
-// they are taken as they come.  One warp.
-__device__ __forceinline__ int sequence_by_length(const Args& a, int i) {
-    if (!a.cu || a.n_seqs > 64) return i;
-    const int lane = threadIdx.x & 31;
-    const int l0 = lane < a.n_seqs ? chunks_of(a, lane) : -1;
-    const int l1 = lane + 32 < a.n_seqs ? chunks_of(a, lane + 32) : -1;
-    int r0 = 0, r1 = 0;  // how many come before
-    for (int m = 0; m < a.n_seqs; ++m) {
-        const int x0 = __shfl_sync(0xffffffffu, l0, m & 31);
-        const int x1 = __shfl_sync(0xffffffffu, l1, m & 31);
-        const int x = m < 32 ? x0 : x1;
-        r0 += x > l0 || (x == l0 && m < lane);
-        r1 += x > l1 || (x == l1 && m < lane + 32);
-    }
-    const unsigned b0 = __ballot_sync(0xffffffffu, r0 == i && lane < a.n_seqs);
-    const unsigned b1 = __ballot_sync(0xffffffffu, r1 == i && lane + 32 < a.n_seqs);
-    return b0 ? __ffs(b0) - 1 : 31 + __ffs(b1);
-}
-
 // Goes through a piece's segments; the whole warp calls it.
 struct Walk {
     Plan p;
-    long long x, end;  // kEven: chunks still to come; kWhole: x the round; kPadded: 0, 1
+    long long x, end;  // units still to come (kPadded: x is 0, then 1)
+    // kHandOver: the last segment, if its chain goes on in the next piece, comes first, and
+    // the first one, if its chain began in the piece before, last.
+    Segment head, tail;
+    bool has_head = false, has_tail = false;
 
-    __device__ __forceinline__ void begin(const Plan& plan, int piece) {
+    __device__ __forceinline__ void begin(const Args& a, const Plan& plan, int piece) {
         p = plan;
-        x = p.kind == kEven ? (long long)piece * p.piece : 0;
-        end = p.kind == kEven ? min(p.total, x + p.piece) : 0;
+        x = end = 0;
+        if (p.kind == kPadded) return;
+        x = (long long)piece * p.piece;
+        end = min(p.total, x + p.piece);
+        if (p.kind == kEven || x >= end) return;
+        const int at = find_chain(a, false, x, tail.n, tail.h);
+        tail.from = chunk_at(at);
+        tail.of = tail.to = chunks_of(a, tail.n);
+        has_tail = tail.from > 0;
+        if (has_tail) x += units(tail.of) - at;
+        if (x >= end) return;
+        const int last = find_chain(a, false, end - 1, head.n, head.h) + 1;
+        head.from = 0;
+        head.to = chunk_at(last);
+        head.of = chunks_of(a, head.n);
+        if (head.to < head.of) {  // (with no chunk of it here, it begins in the next piece)
+            has_head = head.to > 0;
+            end -= last;
+        }
     }
-    __device__ __forceinline__ bool next(const Work& w, int piece, Segment& s) {
-        const Args& a = w.a;
+    __device__ __forceinline__ bool next(const Args& a, int piece, Segment& s) {
         if (p.kind == kPadded) {
             if (x++ || piece >= p.total) return false;
             const int part = find_chain(a, true, piece, s.n, s.h);
@@ -219,33 +237,31 @@ struct Walk {
             s.to = min(s.of, s.from + kLeastPiece);
             return true;
         }
-        if (p.kind == kWhole) {
-            const long long chains = (long long)a.n_seqs * a.heads;
-            while (x * w.pieces < chains) {
-                const long long chain = x * w.pieces + (x & 1 ? w.pieces - 1 - piece : piece);
-                ++x;
-                if (chain >= chains) continue;
-                const int i = (int)(chain / a.heads);
-                s.h = (int)(chain - (long long)i * a.heads);
-                s.n = sequence_by_length(a, i);
-                s.of = s.to = chunks_of(a, s.n);
-                s.from = 0;
-                if (s.of) return true;
-            }
-            return false;
+        if (has_head) {
+            has_head = false;
+            s = head;
+            return true;
         }
-        if (x >= end) return false;
-        s.from = find_chain(a, false, x, s.n, s.h);
-        s.of = chunks_of(a, s.n);
-        s.to = (int)min((long long)s.of, s.from + (end - x));
-        x += s.to - s.from;
+        while (x < end) {
+            const int at = find_chain(a, false, x, s.n, s.h);
+            s.of = chunks_of(a, s.n);
+            const int to = (int)min((long long)units(s.of), at + (end - x));
+            s.from = chunk_at(at);
+            s.to = chunk_at(to);
+            x += to - at;
+            if (s.from < s.to) return true;
+        }
+        if (!has_tail) return false;
+        has_tail = false;
+        s = tail;
         return true;
     }
 };
 
-// The last segment of piece i, if its chain goes on in the next one.
+// The last segment of piece i, if its chain goes on in the next one and its sum is wanted
+// there.
 __device__ __forceinline__ bool open_segment(const Work& w, const Plan& p, int i, Segment& s) {
-    if (p.kind == kWhole) return false;
+    if (p.kind == kHandOver) return false;
     if (p.kind == kPadded) {
         if (i >= p.total) return false;
         const int part = find_chain(w.a, true, i, s.n, s.h);
@@ -258,9 +274,9 @@ __device__ __forceinline__ bool open_segment(const Work& w, const Plan& p, int i
     if (first >= end) return false;
     const int last = find_chain(w.a, false, end - 1, s.n, s.h);
     s.of = chunks_of(w.a, s.n);
-    s.to = last + 1;
-    s.from = (int)max(0LL, last - (end - 1 - first));
-    return s.to < s.of;
+    s.to = chunk_at(last + 1);
+    s.from = chunk_at((int)max(0LL, last - (end - 1 - first)));
+    return s.from < s.to && s.to < s.of;
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -279,16 +295,18 @@ constexpr uint32_t kTmemP = 0, kTmemQS = 128, kTmemPV = 256, kTmemKW = 384;
 constexpr int kRing = 2;
 
 struct Item {
-    long long row;  // of the segment's first token
-    int rows, h;
+    int row, rows;  // the segment's first token row, and how many
+    int h;
     int chunks;     // 0: no more segments
     const float* src;  // the state in front; null: zeros (SUM: a state to be copied)
     int fold, folds;   // pieces whose sums go on top: the first one, how many
+    const unsigned* wait;  // kHandOver: src is there once this is 1; null: it is there
+    unsigned* hand;        // dst is handed over by this; null: it is not
     float* dst;        // where the state behind goes; null: nowhere
 };
 
 struct Shared {
-    uint64_t full[3], empty[3];
+    uint64_t full[3], v_full[2], empty[3];
     uint64_t qk_ready, pv_ready, s16_ready, qs_ready, o_read;
     // by chunk parity, where one side may be a chunk ahead of the other's wait
     uint64_t p_ready[2], v_checked[2], w_ready[2], kw_ready[2];
@@ -354,16 +372,21 @@ __device__ __forceinline__ bool sync_warps(Shared& sh, uint64_t* bar, uint32_t& 
     return ok;
 }
 
-// The roles' view of the ring of segments.
+// The roles' view of the ring of segments.  A segment is read where it lies, so that it
+// takes no registers, and given back by `done`.
 struct Items {
     int ring = 0;
     uint32_t phase = 0;
-    __device__ __forceinline__ bool next(Shared& sh, Item& it) {
-        if (!wait_warp(sh, &sh.item_full[ring], phase)) return false;
-        it = sh.item[ring];
+    __device__ __forceinline__ const Item* next(Shared& sh) {  // null: no more
+        if (!wait_warp(sh, &sh.item_full[ring], phase)) return nullptr;
+        const Item* it = &sh.item[ring];
+        if (it->chunks > 0) return it;
+        done(sh);
+        return nullptr;
+    }
+    __device__ __forceinline__ void done(Shared& sh) {
         arrive_warp(&sh.item_empty[ring]);
         if (++ring == kRing) ring = 0, phase ^= 1;
-        return it.chunks > 0;
     }
 };
 
@@ -377,7 +400,7 @@ __device__ __forceinline__ void copy_role(const Work& w, Shared& sh, unsigned ch
     const int lane = threadIdx.x & 31, piece = blockIdx.x;
     const Plan plan = make_plan(w);
     Walk walk;
-    walk.begin(plan, piece);
+    walk.begin(a, plan, piece);
     Segment cut;
     bool done = SUM && !open_segment(w, plan, piece, cut), go = true;
     int ring = 0, stage = 0;
@@ -385,10 +408,10 @@ __device__ __forceinline__ void copy_role(const Work& w, Shared& sh, unsigned ch
     while (go) {
         Item it = {};
         Segment s = cut;
-        if (!done && (SUM || walk.next(w, piece, s))) {
+        if (!done && (SUM || walk.next(a, piece, s))) {
             lin::Rows r;
             sequence_rows(a, s.n, r);
-            it.row = r.first + (long long)s.from * C;
+            it.row = (int)r.first + s.from * C;
             it.rows = min(r.count - s.from * C, (s.to - s.from) * C);
             it.h = s.h;
             it.chunks = s.to - s.from;
@@ -401,18 +424,29 @@ __device__ __forceinline__ void copy_role(const Work& w, Shared& sh, unsigned ch
                     it.src = a.state_in + chain;
                 done = true;
             } else {
-                // (of a cut chain a copy of it: state_out may be state_in)
-                const int begin = s.from ? plan.chain_begin(piece, s.from) : piece;
-                // (lin_join_kernel's chains: by their last piece)
-                const int folds = piece - begin;
-                const bool joined = s.from && plan.chain_folds(s) > kMostFolds;
-                if (joined)
-                    it.src = w.sum + (size_t)(piece - 1) * kStateFloats;
-                else if (s.to - s.from < s.of && a.state_in && a.state_in == a.state_out)
-                    it.src = w.start + (size_t)begin * kStateFloats;
-                else
+                if (plan.kind == kHandOver) {
                     it.src = a.state_in ? a.state_in + chain : nullptr;
-                if (s.from && !joined) it.fold = begin, it.folds = folds;
+                    if (s.from) {
+                        it.src = w.sum + (size_t)(piece - 1) * kStateFloats;
+                        it.wait = w.handed + piece - 1;
+                    }
+                    if (s.to < s.of) {
+                        it.dst = w.sum + (size_t)piece * kStateFloats;
+                        it.hand = w.handed + piece;
+                    }
+                } else {
+                    // (of a cut chain a copy of it: state_out may be state_in)
+                    const int begin = s.from ? plan.chain_begin(piece, s.from) : piece;
+                    // (lin_join_kernel's chains: by their last piece)
+                    const bool joined = s.from && plan.chain_folds(s) > kMostFolds;
+                    if (joined)
+                        it.src = w.sum + (size_t)(piece - 1) * kStateFloats;
+                    else if (s.to - s.from < s.of && a.state_in && a.state_in == a.state_out)
+                        it.src = w.start + (size_t)begin * kStateFloats;
+                    else
+                        it.src = a.state_in ? a.state_in + chain : nullptr;
+                    if (s.from && !joined) it.fold = begin, it.folds = piece - begin;
+                }
                 if (s.to == s.of && a.state_out) it.dst = a.state_out + chain;
             }
         }
@@ -433,17 +467,22 @@ __device__ __forceinline__ void copy_role(const Work& w, Shared& sh, unsigned ch
                 go = mbar_wait(&sh.empty[stage], phase ^ 1, 1) ||
                      wait_long(sh, &sh.empty[stage], phase ^ 1);
                 if (!go) break;
-                mbar_arrive_expect_tx(&sh.full[stage], SUM ? 2 * kTile : 3 * kTile);
+                mbar_arrive_expect_tx(&sh.full[stage], 2 * kTile);
+                if (!SUM) mbar_arrive_expect_tx(&sh.v_full[stage], kTile);
                 unsigned char* k_tile = sm + (SUM ? stage * kSumStage : stage * kStage + kTile);
-                const int row = (int)(it.row + (long long)c * C);
+                const int row = it.row + c * C;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     unsigned char* dst = k_tile + half * (kTile / 2);
                     if (!SUM)
                         tma_load_3d(dst - kTile, mq, &sh.full[stage], 64 * half, hq, row);
                     tma_load_3d(dst, mk, &sh.full[stage], 64 * half, hq, row);
-                    tma_load_3d(dst + kTile, mv, &sh.full[stage], 64 * half, it.h, row);
                 }
+#pragma unroll
+                for (int half = 0; half < 2; ++half)  // (behind Q and K, which are wanted first)
+                    tma_load_3d(k_tile + kTile + half * (kTile / 2), mv,
+                                SUM ? &sh.full[stage] : &sh.v_full[stage & 1], 64 * half, it.h,
+                                row);
                 if (++stage == kStages<SUM>) stage = 0, phase ^= 1;
             }
         }
@@ -453,6 +492,9 @@ __device__ __forceinline__ void copy_role(const Work& w, Shared& sh, unsigned ch
     if (lane == 0 && *(volatile int*)&sh.stop)
         for (int s = 0; s < kStages<SUM>; ++s)
             mbar_wait(&sh.full[s], s < stage ? phase : phase ^ 1, 1 << 12);
+    if (!SUM && lane == 0 && *(volatile int*)&sh.stop)
+        for (int s = 0; s < 2; ++s)
+            mbar_wait(&sh.v_full[s], s < stage ? phase : phase ^ 1, 1 << 12);
 }
 
 // The warp that issues the products: of chunk c P V and Q S, the next chunk's Q K^T, so
@@ -486,9 +528,14 @@ __device__ __forceinline__ void product_role(Shared& sh, unsigned char* sm) {
         __syncwarp();
     };
     Items items;
-    Item it;
-    if (!items.next(sh, it)) return;
-    int left = uniform(it.chunks);
+    auto next_chunks = [&] {
+        const Item* it = items.next(sh);
+        const int chunks = it ? it->chunks : 0;
+        if (it) items.done(sh);
+        return uniform(chunks);
+    };
+    int left = next_chunks();
+    if (left == 0) return;
     if (!SUM) {
         if (!wait_warp(sh, &sh.full[0], 0)) return;
         qk(0);
@@ -525,9 +572,8 @@ __device__ __forceinline__ void product_role(Shared& sh, unsigned char* sm) {
             __syncwarp();
         }
         if (--left == 0) {
-            items.next(sh, it);
+            left = next_chunks();
             if (*(volatile int*)&sh.stop) return;
-            left = uniform(it.chunks);
         }
         if (!SUM && left > 0) {
             if (!wait_warp(sh, &sh.full[stage ^ 1], (n + 1) >> 1 & 1)) return;
@@ -554,7 +600,7 @@ __device__ __forceinline__ void product_role(Shared& sh, unsigned char* sm) {
 // g of a token as it is, 0 for tokens that are not there; and as log2 of the decay.  The
 // load is a chunk ahead of its use, and nothing is done with it before.
 __device__ __forceinline__ float load_g(const Args& a, const Item& it, int token) {
-    return token < it.rows ? __ldg(a.g + (it.row + token) * a.g_stride + it.h) : 0.f;
+    return token < it.rows ? __ldg(a.g + ((long long)it.row + token) * a.g_stride + it.h) : 0.f;
 }
 __device__ __forceinline__ float log2_decay(float g) { return lin::clamp_decay(g) * kLog2e; }
 
@@ -611,10 +657,10 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const uint32_t row = sh.tmem + ((uint32_t)(warp * 32) << 16);
     Items items;
-    Item it;
     int n = 0;
     uint32_t sync_phase = 0;
-    while (items.next(sh, it)) {
+    while (const Item* const next = items.next(sh)) {
+        const Item& it = *next;
         float next_g = load_g(a, it, t);
 #pragma unroll 1
         for (int c = 0; c < it.chunks; ++c, ++n) {
@@ -723,6 +769,7 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
             sh.front[t] = ex2_approx(before + sum) * a.scale;
             arrive_warp(&sh.p_ready[odd]);
         }
+        items.done(sh);
     }
 }
 
@@ -741,8 +788,8 @@ __device__ __noinline__ void put_nan(uint16_t* o, unsigned char* half_tile,
     }
 }
 
-// Looks V over, a warp for half of its columns: what is not finite the product must not see, as rows
-// before it have weight 0 for it.  It is set aside as zero, and each column's first such
+// Looks V over, a warp for half of its columns: what is not finite the product must not see, as
+// rows before it have weight 0 for it.  It is set aside as zero, and each column's first such
 // row noted: what it does to the rows from there on is put into O and W by state_role.
 // (Not a path for ordinary inputs.)  FP16: finds the largest magnitude too.
 template <bool F16>
@@ -788,15 +835,15 @@ __device__ __forceinline__ void check_role(Shared& sh, unsigned char* sm, int ha
                        kOne = F16 ? 0x04000400u : 0x00800080u;
     const int lane = threadIdx.x & 31;
     Items items;
-    Item it;
     int n = 0;
-    while (items.next(sh, it)) {
+    while (const Item* const next = items.next(sh)) {
+        const Item& it = *next;
 #pragma unroll 1
         for (int c = 0; c < it.chunks; ++c, ++n) {
             const uint32_t odd = n & 1;
             const int there = min(C, it.rows - c * C);
             unsigned char* half_tile = sm + (n & 1) * kStage + 2 * kTile + half * (kTile / 2);
-            if (!wait_warp(sh, &sh.full[n & 1], n >> 1 & 1)) return;
+            if (!wait_warp(sh, &sh.v_full[n & 1], n >> 1 & 1)) return;
             uint32_t most = 0;
             bool found = false;
 #pragma unroll 1
@@ -835,6 +882,7 @@ __device__ __forceinline__ void check_role(Shared& sh, unsigned char* sm, int ha
             if (found) fence_async_smem();
             arrive_warp(&sh.v_checked[odd]);
         }
+        items.done(sh);
     }
 }
 
@@ -844,6 +892,25 @@ __device__ __forceinline__ float unit_of(float x, float& inverse) {
     const int e = min(max((int)(__float_as_uint(x) >> 23) - 13, 1), 241);
     inverse = __uint_as_float((uint32_t)(254 - e) << 23);
     return __uint_as_float((uint32_t)e << 23);
+}
+
+// For a whole warp: until another CTA of the grid has handed its state over, or for at
+// most 2^35 clocks.
+__device__ __noinline__ bool wait_handed(Shared& sh, const unsigned* flag) {
+    const long long from = clock64();
+    for (;;) {
+        unsigned x;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(x) : "l"(flag) : "memory");
+        if (__all_sync(0xffffffffu, x == 1u)) return true;
+        bool stop = *(volatile int*)&sh.stop;
+        if (!stop && clock64() - from > 1LL << 35) {
+            atomicOr(&g_lin_status, STATUS_TIMEOUT);
+            *(volatile int*)&sh.stop = 1;
+            stop = true;
+        }
+        if (__any_sync(0xffffffffu, stop)) return false;
+        __nanosleep(200);
+    }
 }
 
 // Warps 4..11, a thread a row i of 64 columns of the state, and likewise a token's 64
@@ -856,14 +923,15 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
               lane = threadIdx.x & 31, id = (threadIdx.x >> 5) - 4;
     const uint32_t row = sh.tmem + ((uint32_t)(warp * 32) << 16) + 64 * half;
     Items items;
-    Item it;
     int n = 0;
     int stage = 0;
     uint32_t state_phase = 0, stage_phase = 0;
-    while (items.next(sh, it)) {
+    while (const Item* const next = items.next(sh)) {
+        const Item& it = *next;
         float s[64];
         {
             const float* from = it.src;
+            if (!SUM && it.wait && !wait_handed(sh, it.wait)) return;
             if (!SUM && it.folds) {
                 // in the order of memory: a row a thread takes three times as long
                 const int at = threadIdx.x - 128;
@@ -1061,12 +1129,12 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
                 const float2 d2 = make_float2(front, front), s2 = make_float2(a.scale, a.scale);
                 // A warp's 32 rows go by way of shared memory, in the place of the state's
                 // copy, which Q S is through with (written by the lanes, 32 bytes of a row
-                // each, the stores held up everything else on its way to memory: 452 us
-                // where this takes 400).  Rows past the last token must not be written:
+                // each, the stores held up everything else on its way to memory: 459 us
+                // where this took 447, 16 prompts of 512 to 8192 tokens).  Rows past the last token must not be written:
                 // a warp that has some writes its rows itself.
                 const bool whole = there >= 32 * (warp + 1);
                 const int first = 32 * warp;
-                uint16_t* to = a.o + (it.row + (long long)c * C + r) * a.o_stride + it.h * D +
+                uint16_t* to = a.o + ((long long)it.row + c * C + r) * a.o_stride + it.h * D +
                                64 * half;
 #pragma unroll 2
                 for (int i = 0; i < 4; ++i) {  // 16 columns a step
@@ -1109,7 +1177,7 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
                 arrive_warp(&sh.o_read);
                 if (whole && lane == 0) {
                     tma_store_3d(mo, state_half + first * 128, 64 * half, it.h,
-                                 (int)(it.row + (long long)c * C + first));
+                                 it.row + c * C + first);
                     bulk_commit();
                 }
             }
@@ -1123,7 +1191,16 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
 #pragma unroll
             for (int i = 0; i < 8; ++i) store_8(to + 8 * i, s + 8 * i);
         }
+        if (!SUM && it.hand) {
+            if (!sync_warps(sh, &sh.state_sync, state_phase)) return;
+            if (threadIdx.x == 128) {
+                __threadfence();
+                asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(it.hand), "r"(1u)
+                             : "memory");
+            }
+        }
         if (SUM && r == 0 && half == 0) w.log_sum[blockIdx.x] = all;
+        items.done(sh);
     }
 }
 
@@ -1143,7 +1220,7 @@ lin_prefill_kernel(Work w, const __grid_constant__ CUtensorMap mq,
     if (threadIdx.x == 0) {
         sh.stop = 0;
         for (int i = 0; i < 3; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
-        for (int i = 0; i < 2; ++i) sh.bad[i] = sh.bad_seen[i] = 0;
+        for (int i = 0; i < 2; ++i) mbar_init(&sh.v_full[i], 1), sh.bad[i] = sh.bad_seen[i] = 0;
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sh.item_full[i], 1);
             mbar_init(&sh.item_empty[i], SUM ? 13 : 15);
@@ -1173,6 +1250,7 @@ lin_prefill_kernel(Work w, const __grid_constant__ CUtensorMap mq,
     __syncthreads();
     tc_fence_after();
     pdl_wait();
+    if (SUM && threadIdx.x == 0) w.handed[blockIdx.x] = 0;
     if (warp == 12) {
         copy_role<SUM>(w, sh, sm, &mq, &mk, &mv);
     } else if (warp == 13) {
@@ -1273,7 +1351,7 @@ cudaError_t status_word_lin(unsigned** word) {
 }
 
 size_t lin_chunked_workspace_bytes(long long rows, int n_seqs, int heads) {
-    return (size_t)most_pieces(rows, n_seqs, heads) * (3 * kStateFloats + 4) * sizeof(float);
+    return (size_t)most_pieces(rows, n_seqs, heads) * (3 * kStateFloats + 8) * sizeof(float);
 }
 
 kda_status launch_lin_chunked(const Args& a, bool f16, void* workspace, cudaStream_t s) {
@@ -1288,25 +1366,34 @@ kda_status launch_lin_chunked(const Args& a, bool f16, void* workspace, cudaStre
     w.start = w.sum + (size_t)slots * kStateFloats;
     w.folded = w.start + (size_t)slots * kStateFloats;
     w.log_sum = w.folded + (size_t)slots * kStateFloats;
+    w.handed = reinterpret_cast<unsigned*>(w.log_sum + 4 * (size_t)slots);
     CUtensorMap mq, mk, mv, mo;
     KDA_REQUIRE(tma_map_heads(&mq, a.q, a.qk_heads, rows, a.q_stride, 1, C, f16) &&
                     tma_map_heads(&mk, a.k, a.qk_heads, rows, a.k_stride, 1, C, f16) &&
                     tma_map_heads(&mv, a.v, a.heads, rows, a.v_stride, 1, C, f16) &&
                     tma_map_heads(&mo, a.o, a.heads, rows, a.o_stride, 1, 32, f16),
                 KDA_ERR_CUDA, "%s: cannot describe the arrays to the copy engine", fn);
-    // Whether chains may be cut: for packed rows the lengths are on the device.
+    // Whether sums may be wanted, and whether states may be handed over between CTAs: for
+    // packed rows the lengths are on the device.
     const long long chains = (long long)a.n_seqs * a.heads;
     const long long longest = (a.t + C - 1) / C;
     const long long pads = (longest + kLeastPiece - 1) / kLeastPiece;
-    bool cut;
+    const bool few = pads * chains <= w.pieces;
+    const long long piece =
+        few ? kLeastPiece
+            : std::max<long long>(((longest + kLead) * chains + w.pieces - 1) / w.pieces,
+                                  kLeastPiece);
+    bool cut, hand;
     int grid = w.pieces;
     if (a.cu) {
-        cut = longest > kLeastPiece || chains > w.pieces;
-    } else if (pads * chains <= w.pieces) {
+        cut = hand = longest > kLeastPiece || chains > w.pieces;
+    } else if (few && (pads == 1 || !hand_over(longest, piece))) {
         cut = pads > 1;
+        hand = false;
         grid = (int)(pads * chains);
     } else {
-        cut = !(chains >= 2LL * w.pieces && 10 * longest * w.pieces <= 6 * longest * chains);
+        hand = hand_over(longest, piece);
+        cut = !hand;
     }
     // (a piece has at least a share of the longest sequence's chunks)
     const long long least = std::max<long long>(kLeastPiece, longest * a.heads / w.pieces);
@@ -1326,8 +1413,17 @@ kda_status launch_lin_chunked(const Args& a, bool f16, void* workspace, cudaStre
         if (join)
             launch_pdl(lin_join_kernel, dim3(grid, kStateFloats / 4 / kJoinThreads),
                        dim3(kJoinThreads), 0, s, w);
+    } else if (hand) {
+        cudaMemsetAsync(w.handed, 0, slots * sizeof(unsigned), s);
     }
-    launch_pdl(kernel, dim3(grid), dim3(kThreads), kSmemBytes, s, w, mq, mk, mv, mo);
+    if (!hand) {
+        launch_pdl(kernel, dim3(grid), dim3(kThreads), kSmemBytes, s, w, mq, mk, mv, mo);
+        return launch_result(fn);
+    }
+    // CTAs that may wait for one another run together
+    void* args[] = {&w, &mq, &mk, &mv, &mo};
+    cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kernel), dim3(grid), dim3(kThreads),
+                                args, kSmemBytes, s);
     return launch_result(fn);
 }
 
