@@ -1,14 +1,20 @@
-"""One KDA layer and one full-attention layer served together, as a hybrid decoder stacks them.
+"""A KDA layer, a layer of linear attention with a decay for each head and a full-attention layer
+served together, as hybrid decoders stack them.
 
-The KDA layer keeps a state of fixed size per sequence, the full-attention layer a 4-bit paged
-cache of its keys and values.  Three steps, each over a batch of sequences:
+The linear layers keep a state of fixed size per sequence, the full-attention layer a 4-bit paged
+cache of its keys and values, whose pages kda_attn_kv4_resize gives and frees on the device.  Three
+steps, each over a batch of sequences:
 
 * a first prompt chunk: kda_attn_prefill over the rows at hand, kda_attn_kv4_append to keep them;
 * a later chunk: append first, kda_attn_kv4_read for the context, kda_attn_prefill with more keys
   than queries;
 * rows to be verified (one row: plain decoding): append, kda_attn_kv4_decode.  Rows that the
-  verification rejects are taken back: the KDA layer returns to the snapshot after the last row
-  kept, the full-attention layer counts fewer positions.
+  verification rejects are taken back: the linear layers return to the snapshot after the last
+  row kept, the full-attention layer counts fewer positions.
+
+Between them sequences may go on from others (samples of one prompt, beams): kda_attn_kv4_fork
+shares what pages they can, kda_attn_kv4_copy fills the rest.  kda_attn_kv4_compact gathers the
+pages in use at the cache's beginning.
 
 Weights and inputs are random; projections are plain matrix products.
 
@@ -94,6 +100,41 @@ class KdaLayer:
         self.conv.copy_(self.conv_after[kept - 1, n])
 
 
+class LinearLayer:
+    """Heads that forget at fixed rates, from a token in two to one in 256."""
+
+    def __init__(self, gen, dim, heads, n_seqs, krows):
+        self.heads = heads
+        self.w_in = _weight(gen, dim, 3 * heads * D)
+        self.w_out = _weight(gen, heads * D, dim)
+        self.g = -torch.exp2(torch.linspace(-1, -8, heads)).cuda()
+        self.state = torch.zeros((n_seqs, heads, D, D)).cuda()
+        self.state_after = torch.zeros((krows,) + self.state.shape).cuda()
+
+    def _qkv(self, x, *lead):
+        q, k, v = (x @ self.w_in).view(*lead, 3, self.heads, D).unbind(-3)
+        q, k = (torch.nn.functional.normalize(y.float(), dim=-1).to(BF16) for y in (q, k))
+        return q, k, v, torch.empty_like(q)
+
+    def _out(self, o, rows):
+        o = torch.nn.functional.rms_norm(o, (D,))
+        return o.view(rows, -1) @ self.w_out
+
+    def chunk(self, x, cu):
+        q, k, v, o = self._qkv(x, x.shape[0])
+        K.kda_lin_prefill(q, k, v, self.g, o, self.state, self.state, cu_seqlens=cu)
+        return self._out(o, x.shape[0])
+
+    def rows(self, x, n_seqs, krows):
+        q, k, v, o = self._qkv(x, n_seqs, krows)
+        K.kda_lin_decode(q, k, v, self.g, o, self.state, self.state,
+                         list(self.state_after[:krows]))
+        return self._out(o, x.shape[0])
+
+    def keep(self, kept):
+        self.state.copy_(self.state_after[kept - 1, torch.arange(kept.numel(), device="cuda")])
+
+
 class AttentionLayer:
     """`trace`, a list, receives what the attention calls saw and gave, step by step."""
 
@@ -102,25 +143,43 @@ class AttentionLayer:
         self.w_in = _weight(gen, dim, (heads + 2 * kv_heads) * D)
         self.w_out = _weight(gen, heads * D, dim)
         width = -(-longest // page)
-        self.cache = K.kv4_cache(n_seqs * width, kv_heads, page)
-        order = torch.randperm(n_seqs * width, generator=gen).to(torch.int32)
-        self.table = order.view(n_seqs, width).cuda()
+        self.page, pages = page, n_seqs * width
+        self.cache = K.kv4_cache(pages, kv_heads, page)
+        self.table = torch.full((n_seqs, width), -1, dtype=torch.int32).cuda()
+        self.refs = torch.zeros(pages, dtype=torch.int32).cuda()
         self.workspace = K.kda_attn_kv4_workspace(n_seqs, krows, heads, kv_heads)
+        self.pages_workspace = K.kda_attn_kv4_pages_workspace(pages, n_seqs, width)
+        self.inv_freq = (10000.0 ** (-torch.arange(D // 2) / (D // 2))).cuda()
         self.trace = trace
 
-    def _qkv(self, x):
+    def resize(self, lens):
+        K.kda_attn_kv4_resize(self.table, lens, self.refs, self.page, self.pages_workspace)
+
+    def fork(self, lens, parent):
+        moves = K.kda_attn_kv4_fork(self.table, lens, self.refs, parent, page=self.page,
+                                    workspace=self.pages_workspace)
+        K.kda_attn_kv4_copy([self.cache], *moves)
+
+    def compact(self):
+        moves = K.kda_attn_kv4_compact(self.table, self.refs, workspace=self.pages_workspace)
+        K.kda_attn_kv4_copy([self.cache], *moves)
+
+    def _qkv(self, x, positions):
         heads = (x @ self.w_in).unflatten(1, (-1, D))
-        return heads.split((self.heads, self.kv, self.kv), 1)
+        q, k, v = heads.split((self.heads, self.kv, self.kv), 1)
+        K.kda_attn_rope(q, k, positions, self.inv_freq)
+        return q, k, v
 
     def _out(self, q, k, v, o, lens):
         if self.trace is not None:
             self.trace.append(tuple(y.clone() for y in (q, k, v, o.view(q.shape), lens)))
         return o.view(o.shape[0], -1) @ self.w_out
 
-    def chunk(self, x, cu, lens, context=None):
-        """`lens` counts the chunk's rows; `context`, each sequence's positions with them as a
-        list, unless the chunk is every sequence's first."""
-        q, k, v = self._qkv(x)
+    def chunk(self, x, cu, lens, positions, context=None):
+        """`lens` counts the chunk's rows, whose positions are `positions`; `context`, each
+        sequence's positions with them as a list, unless the chunk is every sequence's first."""
+        q, k, v = self._qkv(x, positions)
+        self.resize(lens)
         o = torch.empty((x.shape[0], self.heads, D), dtype=BF16, device="cuda")
         K.kda_attn_kv4_append(k, v, self.cache, self.table, lens, cu_seqlens=cu)
         if context is None:
@@ -134,7 +193,9 @@ class AttentionLayer:
         return self._out(q, k, v, o, lens)
 
     def rows(self, x, n_seqs, krows, lens):
-        q, k, v = self._qkv(x)
+        rows = torch.arange(-krows, 0, dtype=torch.int32, device="cuda")
+        q, k, v = self._qkv(x, (lens[:, None] + rows).view(-1))
+        self.resize(lens)
         q4 = q.contiguous().view(n_seqs, krows, self.heads, D)
         o = torch.empty_like(q4)
         K.kda_attn_kv4_append(k, v, self.cache, self.table, lens)
@@ -148,6 +209,7 @@ class Model:
         gen = torch.Generator().manual_seed(seed)
         self.n, self.krows = n_seqs, krows
         self.kda = KdaLayer(gen, dim, heads, n_seqs, krows)
+        self.lin = LinearLayer(gen, dim, heads, n_seqs, krows)
         self.attn = AttentionLayer(gen, dim, heads, kv_heads, n_seqs, krows, longest, page, trace)
         self.lens = torch.zeros(n_seqs, dtype=torch.int32).cuda()
         self.positions = [0] * n_seqs      # lens, as the host knows it
@@ -158,11 +220,13 @@ class Model:
     def chunk(self, x, new):
         """x [sum of new, dim], new: rows of each sequence."""
         first = not any(self.positions)
+        at = torch.cat([torch.arange(a, a + b) for a, b in zip(self.positions, new)])
         self.positions = [a + b for a, b in zip(self.positions, new)]
         cu = offsets(new)
         self.lens += cu.diff()
         x = x + self.kda.chunk(self._norm(x), cu)
-        return x + self.attn.chunk(self._norm(x), cu, self.lens,
+        x = x + self.lin.chunk(self._norm(x), cu)
+        return x + self.attn.chunk(self._norm(x), cu, self.lens, at.to(torch.int32).cuda(),
                                    None if first else self.positions)
 
     def rows(self, x):
@@ -171,6 +235,7 @@ class Model:
         krows = x.shape[0] // self.n
         self.lens += krows
         x = x + self.kda.rows(self._norm(x), self.n, krows)
+        x = x + self.lin.rows(self._norm(x), self.n, krows)
         return x + self.attn.rows(self._norm(x), self.n, krows, self.lens)
 
     def keep(self, kept, krows):
@@ -178,7 +243,22 @@ class Model:
         self.positions = [a + b for a, b in zip(self.positions, kept)]
         kept = torch.tensor(kept).cuda()
         self.kda.keep(kept)
+        self.lin.keep(kept)
         self.lens += (kept - krows).to(torch.int32)
+        self.attn.resize(self.lens)
+
+    def fork(self, parent):
+        """Sequence n goes on from sequence parent[n], or (-1) is over."""
+        self.positions = [self.positions[p] if p >= 0 else 0 for p in parent]
+        parent = torch.tensor(parent, dtype=torch.int32).cuda()
+        self.attn.fork(self.lens, parent)      # (and the lengths)
+        live = parent >= 0
+        for state in (self.kda.state, self.kda.conv, self.lin.state):
+            new = state[parent.clamp(min=0)]
+            state.copy_(torch.where(live.view(-1, *[1] * (new.dim() - 1)), new, 0))
+
+    def compact(self):
+        self.attn.compact()
 
 
 def main():
@@ -206,6 +286,14 @@ def main():
     assert torch.isfinite(y).all() and model.lens.tolist() == model.positions
     print("16 sequences of %d to %d positions, 4 rows each: %.3f ms a step" % (
         min(model.positions), max(model.positions), start.elapsed_time(stop) / 20))
+    model.fork([n // 4 for n in range(16)])    # four samples of each of the first four
+    model.compact()
+    graph.replay()
+    model.keep([4] * 16, 4)
+    K.kda_sync_status()
+    assert torch.isfinite(y).all() and model.lens.tolist() == model.positions
+    used = int((model.attn.refs > 0).sum())
+    print("16 sequences over 4 prompts: %d pages of %d in use" % (used, model.attn.refs.numel()))
 
 
 if __name__ == "__main__":

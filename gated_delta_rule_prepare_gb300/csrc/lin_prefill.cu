@@ -55,13 +55,18 @@ __device__ unsigned g_lin_status = 0;
 
 constexpr int C = 128;  // tokens a chunk
 constexpr int kSms = 152;
-constexpr int kLeastPiece = 6;  // chunks
+// A piece's chunks at least (4: 1500 tokens, 32 heads 38 us, 3: 33; 2: some calls are better
+// off by a sixth, others worse).
+constexpr int kLeastPiece = 3;
+// Calls of so few chunks, and of a chain a CTA at most, cut none: one kernel (700 tokens, 24
+// heads: 25.7 us, with cuts 30.2).
+constexpr int kWhole = 6;
 constexpr int kStateFloats = D * D;
 
 // ---------------------------------------------------------------- pieces
 
 // How the call's chunks go to `pieces` CTAs (at most kSms).
-//  kPadded: each chain starts a piece, pieces of kLeastPiece chunks: few chunks.
+//  kPadded: each chain starts a piece, pieces of kLeastPiece (kWhole) chunks: few chunks.
 //  kEven: chains one after the other, cut into equal pieces.  A chain counts kLead chunks
 //      more than it has, in front of its first one: what its states' load and store cost.
 //      (kLead 1: 16 prompts of 512 to 8192 tokens in this order, 32 heads, 462 us, 2: 422.)
@@ -96,6 +101,7 @@ struct Plan {
 struct Work {
     Args a;
     int pieces;
+    int least;  // chunks of a piece: kLeastPiece, or kWhole if no chain is longer
     // of a piece whose last segment's chain goes on in the next piece: what the segment
     // adds to the state, then the state in front of the next piece
     float* sum;      // [pieces][128 * 128]
@@ -106,15 +112,16 @@ struct Work {
     unsigned* handed;  // [pieces] kHandOver: 1 once `sum` is the state of its last chain
 };
 // A segment's state is summed up where it is wanted from at most so many pieces before it
-// (a microsecond each); of longer chains by lin_join_kernel.
-constexpr int kMostFolds = 9;
+// (a microsecond each, what 64 KB from L2 take); of longer chains by lin_join_kernel (7 us: one
+// chain in 17 pieces 37.9 us, folded 40.7).
+constexpr int kMostFolds = 14;
 
 __device__ __forceinline__ int chunks_of(const Args& a, int n) {
     lin::Rows r;
     return sequence_rows(a, n, r) ? (r.count + C - 1) / C : 0;
 }
-__device__ __forceinline__ int padded(int chunks) {
-    return (chunks + kLeastPiece - 1) / kLeastPiece;
+__device__ __forceinline__ int padded(int chunks, int least) {
+    return (chunks + least - 1) / least;
 }
 
 __device__ __forceinline__ int units(int chunks) { return chunks ? chunks + kLead : 0; }
@@ -130,12 +137,12 @@ __device__ __forceinline__ Plan make_plan(const Work& w) {
     if (!a.cu) {
         longest = (a.t + C - 1) / C;
         chunks = (long long)(longest + kLead) * a.n_seqs;
-        pads = (long long)padded(longest) * a.n_seqs;
+        pads = (long long)padded(longest, w.least) * a.n_seqs;
     } else {
         for (int n = lane; n < a.n_seqs; n += 32) {
             const int c = chunks_of(a, n);
             chunks += units(c);
-            pads += padded(c);
+            pads += padded(c, w.least);
             longest = max(longest, c);
         }
 #pragma unroll
@@ -148,20 +155,20 @@ __device__ __forceinline__ Plan make_plan(const Work& w) {
     chunks *= a.heads;
     pads *= a.heads;
     const bool few = pads <= w.pieces;
-    if (few && (longest <= kLeastPiece || !hand_over(longest, kLeastPiece)))
-        return {kPadded, kLeastPiece, pads};
+    if (few && (longest <= w.least || !hand_over(longest, w.least)))
+        return {kPadded, w.least, pads};
     const int piece =
-        few ? kLeastPiece
-            : (int)max((chunks + w.pieces - 1) / w.pieces, (long long)kLeastPiece);
+        few ? w.least : (int)max((chunks + w.pieces - 1) / w.pieces, (long long)w.least);
     if (hand_over(longest, piece)) return {kHandOver, max(piece, units(longest)), chunks};
     return {kEven, piece, chunks};
 }
 
-// The chain that unit x falls in (for kPadded: that piece x is of), x below the total;
+// The chain that unit x falls in (kPadded: that piece x of `pads` chunks is of; otherwise
+// `pads` is 0), x below the total;
 // returns x's number within it.  One warp.
-__device__ __forceinline__ int find_chain(const Args& a, bool pads, long long x, int& n, int& h) {
+__device__ __forceinline__ int find_chain(const Args& a, int pads, long long x, int& n, int& h) {
     if (!a.cu) {
-        const int c = (a.t + C - 1) / C, u = pads ? padded(c) : units(c);
+        const int c = (a.t + C - 1) / C, u = pads ? padded(c, pads) : units(c);
         const long long chain = x / u;
         n = (int)(chain / a.heads);
         h = (int)(chain - (long long)n * a.heads);
@@ -172,7 +179,7 @@ __device__ __forceinline__ int find_chain(const Args& a, bool pads, long long x,
         int u = 0;
         if (n0 + lane < a.n_seqs) {
             u = chunks_of(a, n0 + lane);
-            u = pads ? padded(u) : units(u);
+            u = pads ? padded(u, pads) : units(u);
         }
         long long sum = (long long)u * a.heads;
 #pragma unroll
@@ -213,13 +220,13 @@ struct Walk {
         x = (long long)piece * p.piece;
         end = min(p.total, x + p.piece);
         if (p.kind == kEven || x >= end) return;
-        const int at = find_chain(a, false, x, tail.n, tail.h);
+        const int at = find_chain(a, 0, x, tail.n, tail.h);
         tail.from = chunk_at(at);
         tail.of = tail.to = chunks_of(a, tail.n);
         has_tail = tail.from > 0;
         if (has_tail) x += units(tail.of) - at;
         if (x >= end) return;
-        const int last = find_chain(a, false, end - 1, head.n, head.h) + 1;
+        const int last = find_chain(a, 0, end - 1, head.n, head.h) + 1;
         head.from = 0;
         head.to = chunk_at(last);
         head.of = chunks_of(a, head.n);
@@ -231,10 +238,10 @@ struct Walk {
     __device__ __forceinline__ bool next(const Args& a, int piece, Segment& s) {
         if (p.kind == kPadded) {
             if (x++ || piece >= p.total) return false;
-            const int part = find_chain(a, true, piece, s.n, s.h);
+            const int part = find_chain(a, p.piece, piece, s.n, s.h);
             s.of = chunks_of(a, s.n);
-            s.from = part * kLeastPiece;
-            s.to = min(s.of, s.from + kLeastPiece);
+            s.from = part * p.piece;
+            s.to = min(s.of, s.from + p.piece);
             return true;
         }
         if (has_head) {
@@ -243,7 +250,7 @@ struct Walk {
             return true;
         }
         while (x < end) {
-            const int at = find_chain(a, false, x, s.n, s.h);
+            const int at = find_chain(a, 0, x, s.n, s.h);
             s.of = chunks_of(a, s.n);
             const int to = (int)min((long long)units(s.of), at + (end - x));
             s.from = chunk_at(at);
@@ -264,15 +271,15 @@ __device__ __forceinline__ bool open_segment(const Work& w, const Plan& p, int i
     if (p.kind == kHandOver) return false;
     if (p.kind == kPadded) {
         if (i >= p.total) return false;
-        const int part = find_chain(w.a, true, i, s.n, s.h);
+        const int part = find_chain(w.a, p.piece, i, s.n, s.h);
         s.of = chunks_of(w.a, s.n);
-        s.from = part * kLeastPiece;
-        s.to = min(s.of, s.from + kLeastPiece);
+        s.from = part * p.piece;
+        s.to = min(s.of, s.from + p.piece);
         return s.to < s.of;
     }
     const long long first = (long long)i * p.piece, end = min(p.total, first + p.piece);
     if (first >= end) return false;
-    const int last = find_chain(w.a, false, end - 1, s.n, s.h);
+    const int last = find_chain(w.a, 0, end - 1, s.n, s.h);
     s.of = chunks_of(w.a, s.n);
     s.to = chunk_at(last + 1);
     s.from = chunk_at((int)max(0LL, last - (end - 1 - first)));
@@ -1130,8 +1137,9 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
                 // A warp's 32 rows go by way of shared memory, in the place of the state's
                 // copy, which Q S is through with (written by the lanes, 32 bytes of a row
                 // each, the stores held up everything else on its way to memory: 459 us
-                // where this took 447, 16 prompts of 512 to 8192 tokens).  Rows past the last token must not be written:
-                // a warp that has some writes its rows itself.
+                // where this took 447, 16 prompts of 512 to 8192 tokens).  Rows past the
+                // last token must not be written: a warp that has some writes its rows
+                // itself.
                 const bool whole = there >= 32 * (warp + 1);
                 const int first = 32 * warp;
                 uint16_t* to = a.o + ((long long)it.row + c * C + r) * a.o_stride + it.h * D +
@@ -1305,7 +1313,7 @@ __global__ void __launch_bounds__(kJoinThreads) lin_join_kernel(Work w) {
     Segment s;
     if (!open_segment(w, p, i, s) || s.from || p.chain_folds(s) <= kMostFolds) return;
     // pieces whose last segment is this chain's and open
-    int last = i + padded(s.of) - 2;
+    int last = i + padded(s.of, p.piece) - 2;
     if (p.kind == kEven) {
         const long long chain_end = (long long)(i + 1) * p.piece + (s.of - s.to);
         last = (int)((chain_end - 1) / p.piece) - 1;
@@ -1377,16 +1385,17 @@ kda_status launch_lin_chunked(const Args& a, bool f16, void* workspace, cudaStre
     // packed rows the lengths are on the device.
     const long long chains = (long long)a.n_seqs * a.heads;
     const long long longest = (a.t + C - 1) / C;
-    const long long pads = (longest + kLeastPiece - 1) / kLeastPiece;
+    const bool whole = longest <= kWhole && chains <= w.pieces;
+    w.least = whole ? kWhole : kLeastPiece;
+    const long long pads = (longest + w.least - 1) / w.least;
     const bool few = pads * chains <= w.pieces;
     const long long piece =
-        few ? kLeastPiece
-            : std::max<long long>(((longest + kLead) * chains + w.pieces - 1) / w.pieces,
-                                  kLeastPiece);
+        few ? w.least
+            : std::max<long long>(((longest + kLead) * chains + w.pieces - 1) / w.pieces, w.least);
     bool cut, hand;
     int grid = w.pieces;
     if (a.cu) {
-        cut = hand = longest > kLeastPiece || chains > w.pieces;
+        cut = hand = !whole;
     } else if (few && (pads == 1 || !hand_over(longest, piece))) {
         cut = pads > 1;
         hand = false;
@@ -1396,7 +1405,7 @@ kda_status launch_lin_chunked(const Args& a, bool f16, void* workspace, cudaStre
         cut = !hand;
     }
     // (a piece has at least a share of the longest sequence's chunks)
-    const long long least = std::max<long long>(kLeastPiece, longest * a.heads / w.pieces);
+    const long long least = std::max<long long>(w.least, longest * a.heads / w.pieces);
     const bool join = longest / least + 1 > kMostFolds;
     auto kernel = f16 ? lin_prefill_kernel<true, false> : lin_prefill_kernel<false, false>;
     auto sums = f16 ? lin_prefill_kernel<true, true> : lin_prefill_kernel<false, true>;
