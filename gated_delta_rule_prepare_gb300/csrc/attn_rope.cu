@@ -8,6 +8,9 @@
 // and CTA), and position * F in integers drops whole turns exactly.  F's 53 bits leave
 // an angle exact to 2^-53 |position * inv_freq|, below 2^-20 of a turn for all int32 positions
 // and frequencies up to 4; sincospif takes the rest.
+//
+// 69001 rows of 40 heads, three axes (1.4 GB): 208 us, 6.8 TB/s, what a copy takes (in
+// halves 209 to 223; halves that are no multiple of 8: 350).  64 rows: 2.6 us, as a call 5.3.
 #include "attn_common.h"
 #include "f32x2.h"
 
@@ -51,16 +54,32 @@ __device__ __forceinline__ uint4 turn_piece(uint4 x, const float2* cs, int u, in
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
-
+// Piece u with the first channels of pairs 8u..8u+7, and the piece with their second ones.
+template <bool F16>
+__device__ __forceinline__ void turn_pieces(uint4& x, uint4& y, const float2* cs, int u) {
+    uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 p = widen2<F16>(xs[e]), w = widen2<F16>(ys[e]);
+        const float2 lo = turn(p.x, w.x, cs[8 * u + 2 * e]);
+        const float2 hi = turn(p.y, w.y, cs[8 * u + 2 * e + 1]);
+        xs[e] = narrow2<F16>(lo.x, hi.x);
+        ys[e] = narrow2<F16>(lo.y, hi.y);
+    }
+    x = make_uint4(xs[0], xs[1], xs[2], xs[3]);
+    y = make_uint4(ys[0], ys[1], ys[2], ys[3]);
+}
 enum Layout { kInterleaved, kHalves8, kHalves };  // kHalves8: pairs a multiple of 8
 
-// LANES threads a head: each a 16-byte piece of it, or (kHalves8) a piece of the first
-// channels of pairs with the piece of the second ones, then what is behind the pairs;
-// or (kHalves) 8 bytes.  Threads step through a tile's rows and heads, kBatch loads in
-// flight.
-constexpr int kRowsTile = 8;
-template <bool F16, int LAYOUT, int LANES>
-__global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int tile_rows) {
+// Eight threads a head, two 16-byte pieces each: one of first channels of pairs with that
+// of the second ones, pieces behind the pairs by twos; interleaved, any two.  (Sixteen with a
+// piece each, interleaved, as many loads in flight: 244 us for 69001 rows where this took 211.)
+// Or (kHalves) a warp a head, 8 bytes a lane, whose partners come from shared memory.  Threads step through a
+// tile's rows and heads, kBatch of them in flight (one more or less: up to a tenth longer).
+// An output in its input's place is written behind its reads: a thread's, or a warp's.
+constexpr int kRowsTile = 8;  // at most
+template <bool F16, int LAYOUT>
+__global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int tile) {
     __shared__ float2 cs[kRowsTile][kMaxPairs];
     __shared__ unsigned long long unit[kMaxPairs];
     pdl_wait();
@@ -72,8 +91,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int tile_row
         const double whole = f - floor(f);
         unit[tid] = (unsigned long long)(whole * 18446744073709551616.0);
     }
-    const long long row0 = (long long)blockIdx.x * tile_rows;
-    const int rows = (int)min((long long)tile_rows, a.rows - row0);
+    const long long row0 = (long long)blockIdx.x * tile;
+    const int rows = (int)min((long long)tile, a.rows - row0);
     __syncthreads();
     for (int i = tid; i < rows * kMaxPairs; i += kThreads) {
         const int r = i / kMaxPairs, p = i % kMaxPairs;
@@ -88,10 +107,16 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int tile_row
         cs[r][p] = make_float2(c * a.factor, s * a.factor);
     }
     __syncthreads();
+    constexpr int LANES = LAYOUT == kHalves ? 32 : 8;
     constexpr int kHeads = kThreads / LANES;  // heads at a time
-    constexpr int kBatch = LAYOUT == kHalves ? 1 : 4;
+    constexpr int kBatch = LAYOUT == kHalves ? 2 : 3;
     const int u = tid % LANES, turned = a.pairs / 8;
-    if (LAYOUT == kHalves8 && u >= 16 - turned) return;
+    __shared__ __align__(16) uint16_t head[LAYOUT == kHalves ? kThreads / 32 : 1][kBatch][D];
+    int first = u, second = u + 8;  // of its pieces
+    if (LAYOUT == kHalves8) {
+        second = u + turned;
+        if (u >= turned) first = 2 * u, second = 2 * u + 1;
+    }
     const int heads = a.heads[0] + a.heads[1];
     // slots of a tile: heads innermost
     const int total = rows * heads;
@@ -113,81 +138,71 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int tile_row
                      (row0 + r) * (key ? a.out_stride[1] : a.out_stride[0]) + head * D;
             for (h += kHeads; h >= heads && r < rows; ++r) h -= heads;
         }
-        if constexpr (LAYOUT == kInterleaved) {
-            uint4 x[kBatch];
+        if constexpr (LAYOUT == kHalves) {  // (the same rows and heads for all of a warp)
+            uint2 x[kBatch];
 #pragma unroll
             for (int k = 0; k < kBatch; ++k)
-                if (row[k] >= 0) x[k] = reinterpret_cast<const uint4*>(src[k])[u];
+                if (row[k] >= 0) x[k] = reinterpret_cast<const uint2*>(src[k])[u];
+            __syncwarp();  // the last heads' partners are read
 #pragma unroll
             for (int k = 0; k < kBatch; ++k)
-                if (row[k] >= 0)
-                    reinterpret_cast<uint4*>(dst[k])[u] =
-                        turn_piece<F16>(x[k], cs[row[k]], u, a.pairs);
-        } else if constexpr (LAYOUT == kHalves8) {
-            const int second = u + turned;
+                if (row[k] >= 0) *reinterpret_cast<uint2*>(head[tid >> 5][k] + 4 * u) = x[k];
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                if (row[k] < 0) continue;
+                const float2 lo = widen2<F16>(x[k].x), hi = widen2<F16>(x[k].y);
+                float y[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = 4 * u + e;
+                    if (c >= 2 * a.pairs) continue;
+                    const bool is_first = c < a.pairs;
+                    const int p = is_first ? c : c - a.pairs;
+                    const float2 t = cs[row[k]][p];
+                    const float other =
+                        widen2<F16>(head[tid >> 5][k][is_first ? c + a.pairs : p]).x;
+                    y[e] = turn(y[e], other, make_float2(t.x, is_first ? t.y : -t.y)).x;
+                }
+                reinterpret_cast<uint2*>(dst[k])[u] =
+                    make_uint2(narrow2<F16>(y[0], y[1]), narrow2<F16>(y[2], y[3]));
+            }
+        } else {
             uint4 x[kBatch], y[kBatch];
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 if (row[k] < 0) continue;
-                if (u < turned) x[k] = reinterpret_cast<const uint4*>(src[k])[u];
+                x[k] = reinterpret_cast<const uint4*>(src[k])[first];
                 y[k] = reinterpret_cast<const uint4*>(src[k])[second];
             }
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 if (row[k] < 0) continue;
-                if (u < turned) {
-                    const uint32_t xs[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-                    const uint32_t ys[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
-                    uint32_t xo[4], yo[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 p = widen2<F16>(xs[e]), w = widen2<F16>(ys[e]);
-                        const float2 lo = turn(p.x, w.x, cs[row[k]][8 * u + 2 * e]);
-                        const float2 hi = turn(p.y, w.y, cs[row[k]][8 * u + 2 * e + 1]);
-                        xo[e] = narrow2<F16>(lo.x, hi.x);
-                        yo[e] = narrow2<F16>(lo.y, hi.y);
-                    }
-                    reinterpret_cast<uint4*>(dst[k])[u] = make_uint4(xo[0], xo[1], xo[2], xo[3]);
-                    y[k] = make_uint4(yo[0], yo[1], yo[2], yo[3]);
+                if (LAYOUT == kInterleaved) {
+                    x[k] = turn_piece<F16>(x[k], cs[row[k]], first, a.pairs);
+                    y[k] = turn_piece<F16>(y[k], cs[row[k]], second, a.pairs);
+                } else if (u < turned) {
+                    turn_pieces<F16>(x[k], y[k], cs[row[k]], u);
                 }
+                reinterpret_cast<uint4*>(dst[k])[first] = x[k];
                 reinterpret_cast<uint4*>(dst[k])[second] = y[k];
             }
-        } else {
-            // four channels a lane, their partners read one by one: all lanes of the
-            // head have read before any writes (the output may be the input)
-            static_assert(LAYOUT != kHalves || (LANES == 32 && kBatch == 1), "a warp a head");
-            if (row[0] < 0) continue;  // (all of the warp)
-            const float2* turns = cs[row[0]];
-            const uint2 own = reinterpret_cast<const uint2*>(src[0])[u];
-            float x[4], y[4] = {};
-            const float2 lo = widen2<F16>(own.x), hi = widen2<F16>(own.y);
-            x[0] = lo.x, x[1] = lo.y, x[2] = hi.x, x[3] = hi.y;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c = 4 * u + e;
-                if (c < 2 * a.pairs)
-                    y[e] = widen2<F16>(src[0][c < a.pairs ? c + a.pairs : c - a.pairs]).x;
-            }
-            __syncwarp();
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c = 4 * u + e;
-                if (c < a.pairs) x[e] = turn(x[e], y[e], turns[c]).x;
-                else if (c < 2 * a.pairs) x[e] = turn(y[e], x[e], turns[c - a.pairs]).y;
-            }
-            reinterpret_cast<uint2*>(dst[0])[u] =
-                make_uint2(narrow2<F16>(x[0], x[1]), narrow2<F16>(x[2], x[3]));
         }
     }
 }
 
+// Rows a CTA: one for each multiprocessor while that makes tiles of a few rows (40 heads: 150 rows
+// in tiles of 1 take 2.6 us, of 8 6.5; 1200 rows in tiles of 4 6.4, of 1 8.2), then tiles that
+// share their frequencies (69001 rows in tiles of 8 208 us, of 2 236, of 16 211).
+int tile_rows(long long rows) {
+    return rows <= 152 ? 1 : rows <= 2 * 152 ? 2 : rows <= 8 * 152 ? 4 : kRowsTile;
+}
+
 template <bool F16>
 void launch_rope(const RopeArgs& a, bool interleaved, dim3 grid, int tile, cudaStream_t s) {
-    // (halves of whole heads: eight threads each have all of it)
-    auto kernel = interleaved        ? rope_kernel<F16, kInterleaved, 16>
-                  : a.pairs == 64    ? rope_kernel<F16, kHalves8, 8>
-                  : a.pairs % 8 == 0 ? rope_kernel<F16, kHalves8, 16>
-                                     : rope_kernel<F16, kHalves, 32>;
+    auto kernel = interleaved        ? rope_kernel<F16, kInterleaved>
+                  : a.pairs % 8 == 0 ? rope_kernel<F16, kHalves8>
+                                     : rope_kernel<F16, kHalves>;
     launch_pdl(kernel, grid, dim3(kThreads), 0, s, a, tile);
 }
 
@@ -250,8 +265,7 @@ extern "C" kda_status kda_attn_rope(const void* q, const void* k, void* q_out, v
     a.heads[0] = heads, a.heads[1] = kv_heads;
     a.rows = rows, a.positions = positions, a.inv_freq = inv_freq;
     a.axes = axes, a.pairs = pairs, a.factor = factor;
-    // eight rows share the frequencies; with few rows, one each
-    const int tile = rows >= kRowsTile * 152 ? kRowsTile : 1;
+    const int tile = tile_rows(rows);
     const dim3 grid((unsigned)((rows + tile - 1) / tile));
     if (in_dtype == KDA_F16) launch_rope<true>(a, interleaved, grid, tile, as_stream(stream));
     else launch_rope<false>(a, interleaved, grid, tile, as_stream(stream));
