@@ -443,7 +443,11 @@ kda_status kda_prefill_static_ws(float* state, const void* q, const void* k, con
  *   scale : finite
  * A token whose q, k, v or g is not finite leaves the tokens before it as they are.
  *
- * kda_lin_prefill -- prompts.
+ * kda_lin_prefill -- prompts.  States are FP32, added to once in 128 tokens; products
+ * are of 16-bit numbers, summed in FP32.  v times its decay is taken as two of them (state_out
+ * is good to about 2^-17 of its largest values); weights, and the state that q is multiplied
+ * with, as one, which moves o by less than its own rounding.  FP16: |sum_i q_t[i] k_s[i]|,
+ * s <= t, stays below 65504.
  *   cu_seqlens == NULL: n_seqs sequences of t tokens, rows [n_seqs][t_pad]; rows
  *           [t, t_pad) are neither read into arithmetic nor written.
  *   cu_seqlens != NULL: DEVICE int32 [n_seqs + 1] offsets of packed rows, t the
@@ -468,8 +472,8 @@ size_t kda_lin_prefill_workspace_size(int64_t rows, int n_seqs, int heads);
 
 /*
  * kda_lin_decode -- krows tokens (1 for decode, up to KDA_MAX_K for verification)
- * of each sequence, rows [n_seqs][krows].  The result is that of krows calls of one
- * row each, bit for bit.
+ * of each sequence, rows [n_seqs][krows].  All of it is FP32.  The result is that of
+ * krows calls of one row each, bit for bit.
  *   snapshots : HOST array of n_snap device pointers, as kda_decode_k's:
  *           snapshots[t] receives the state after row t; none is state_in or
  *           state_out.
