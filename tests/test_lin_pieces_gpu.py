@@ -91,3 +91,29 @@ def test_captured_hand_over():
     graph.replay()
     K.kda_sync_status()
     assert torch.equal(o, want) and torch.equal(S1, S2)
+
+
+def test_two_streams_at_once():
+    """Calls in flight on two streams, each with its own workspace, one kind cut and summed up, one
+    handed over: the bits of calls one at a time."""
+    K = kda()
+    runs = []
+    for seed, (lens, heads) in enumerate([([700 + 90 * i for i in range(10)], 40), ([6000], 20)]):
+        d = inputs(seed, sum(lens), heads, heads, torch.bfloat16, n_seqs=len(lens))
+        cu, ws = cu_of(lens), K.kda_lin_prefill_workspace(sum(lens), len(lens), heads)
+        call = (d["q"], d["k"], d["v"], d["g"])
+        want, S = torch.empty_like(d["v"]), torch.empty_like(d["state"])
+        K.kda_lin_prefill(*call, want, d["state"], S, cu_seqlens=cu)
+        outs = [(torch.empty_like(want), torch.empty_like(S)) for _ in range(6)]
+        runs.append((torch.cuda.Stream(), call, d["state"], cu, ws, want, S, outs))
+    torch.cuda.synchronize()
+    for i in range(6):
+        for stream, call, state, cu, ws, _, _, outs in runs:
+            with torch.cuda.stream(stream):
+                K.kda_lin_prefill(*call, outs[i][0], state, outs[i][1], cu_seqlens=cu,
+                                  workspace=ws)
+    torch.cuda.synchronize()
+    K.kda_sync_status()
+    for *_, want, S, outs in runs:
+        for o, So in outs:
+            assert torch.equal(o, want) and torch.equal(So, S)
