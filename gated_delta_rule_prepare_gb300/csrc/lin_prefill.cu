@@ -463,6 +463,12 @@ __device__ __forceinline__ void copy_role(const Work& w, Shared& sh, unsigned ch
             if (go) {
                 sh.item[ring] = it;
                 mbar_arrive(&sh.item_full[ring]);
+                // (on its way while the last chain is worked on: 64 prompts of 64 tokens, 32
+                // heads 123 us, 113)
+                if (!SUM && it.src && !it.wait && !it.folds)
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(it.src),
+                                 "r"(kStateFloats * 4)
+                                 : "memory");
             }
         }
         if (++ring == kRing) ring = 0, ring_phase ^= 1;
