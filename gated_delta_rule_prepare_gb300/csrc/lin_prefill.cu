@@ -200,7 +200,7 @@ __device__ __forceinline__ int find_chain(const Args& a, int pads, long long x, 
         h = (int)((x - first) / each);
         return (int)(x - first - (long long)h * each);
     }
-    n = -1, h = 0;
+    n = h = 0;
     return 0;
 }
 
@@ -208,6 +208,7 @@ __device__ __forceinline__ int find_chain(const Args& a, int pads, long long x, 
 struct Walk {
     Plan p;
     long long x, end;  // units still to come (kPadded: x is 0, then 1)
+    int n, h, of, at;  // the chain that x falls in, its chunks, and x's number within it
     // kHandOver: the last segment, if its chain goes on in the next piece, comes first, and
     // the first one, if its chain began in the piece before, last.
     Segment head, tail;
@@ -219,13 +220,15 @@ struct Walk {
         if (p.kind == kPadded) return;
         x = (long long)piece * p.piece;
         end = min(p.total, x + p.piece);
-        if (p.kind == kEven || x >= end) return;
-        const int at = find_chain(a, 0, x, tail.n, tail.h);
-        tail.from = chunk_at(at);
-        tail.of = tail.to = chunks_of(a, tail.n);
-        has_tail = tail.from > 0;
-        if (has_tail) x += units(tail.of) - at;
         if (x >= end) return;
+        at = find_chain(a, 0, x, n, h);
+        of = chunks_of(a, n);
+        if (p.kind == kEven) return;
+        tail = {n, h, chunk_at(at), of, of};
+        has_tail = tail.from > 0;
+        if (has_tail) x += units(of) - at;
+        if (x >= end) return;
+        if (has_tail) next_chain(a);
         const int last = find_chain(a, 0, end - 1, head.n, head.h) + 1;
         head.from = 0;
         head.to = chunk_at(last);
@@ -233,6 +236,23 @@ struct Walk {
         if (head.to < head.of) {  // (with no chunk of it here, it begins in the next piece)
             has_head = head.to > 0;
             end -= last;
+        }
+    }
+    // (step by step, as finding a chain reads all offsets before it: 4096 prompts of 9 tokens, 2
+    // heads, 2870 us, 603)
+    __device__ __forceinline__ void next_chain(const Args& a) {
+        at = 0;
+        if (++h < a.heads) return;
+        h = 0, ++n;
+        if (!a.cu) return;
+        const int lane = threadIdx.x & 31;
+        for (; n < a.n_seqs; n += 32) {
+            const int c = n + lane < a.n_seqs ? chunks_of(a, n + lane) : 0;
+            const unsigned some = __ballot_sync(0xffffffffu, c > 0);
+            if (!some) continue;
+            of = __shfl_sync(0xffffffffu, c, __ffs(some) - 1);
+            n += __ffs(some) - 1;
+            return;
         }
     }
     __device__ __forceinline__ bool next(const Args& a, int piece, Segment& s) {
@@ -250,12 +270,10 @@ struct Walk {
             return true;
         }
         while (x < end) {
-            const int at = find_chain(a, 0, x, s.n, s.h);
-            s.of = chunks_of(a, s.n);
-            const int to = (int)min((long long)units(s.of), at + (end - x));
-            s.from = chunk_at(at);
-            s.to = chunk_at(to);
+            const int to = (int)min((long long)units(of), at + (end - x));
+            s = {n, h, chunk_at(at), chunk_at(to), of};
             x += to - at;
+            if (x < end) next_chain(a);
             if (s.from < s.to) return true;
         }
         if (!has_tail) return false;

@@ -117,3 +117,32 @@ def test_two_streams_at_once():
     for *_, want, S, outs in runs:
         for o, So in outs:
             assert torch.equal(o, want) and torch.equal(So, S)
+
+
+@pytest.mark.parametrize("n,heads", [(33, 3), (1025, 2), (5000, 1)])
+def test_many_sequences(n, heads):
+    """Ragged ones, a third of them empty, a long one among them."""
+    K = kda()
+    gen = torch.Generator().manual_seed(n)
+    lens = (torch.randint(0, 60, (n,), generator=gen) * (torch.rand(n, generator=gen) > 0.3)).tolist()
+    lens[n // 2] = 2500
+    d = inputs(n, sum(lens), heads, heads, torch.bfloat16, rate=0.3, n_seqs=n)
+    o, S = torch.empty_like(d["v"]), torch.empty_like(d["state"])
+    call = (d["q"], d["k"], d["v"], d["g"])
+    K.kda_lin_prefill(*call, o, d["state"], S, cu_seqlens=cu_of(lens))
+    K.kda_sync_status()
+    starts = [0]
+    for x in lens:
+        starts.append(starts[-1] + x)
+    look = set(range(0, n, max(1, n // 40))) | {n // 2 - 1, n // 2, n // 2 + 1, n - 1}
+    for i in look:
+        one = {x: d[x][:, :1] for x in ("q", "k", "v", "g")}
+        one["state"] = d["state"][:, :1]
+        close(o[:, :1], S[:, :1], one, torch.bfloat16, rows=(starts[i], starts[i + 1]), n=i)
+    empty = torch.tensor([x == 0 for x in lens]).cuda()
+    assert torch.equal(S[empty], d["state"][empty])
+    # each sequence is as it is alone, whichever CTA has it: in place too
+    S2, o2 = d["state"].clone(), torch.empty_like(o)
+    K.kda_lin_prefill(*call, o2, S2, S2, cu_seqlens=cu_of(lens))
+    K.kda_sync_status()
+    assert torch.equal(o, o2) and torch.equal(S, S2)
