@@ -786,8 +786,11 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
             tmem_st_wait();
             tc_fence_before();
             // The rows behind the last token hold another sequence's: no weight reaches
-            // their values, but 0 times infinity would.
-            if (t >= it.rows - c * C) {
+            // their values, but 0 times infinity would.  V has a barrier of its own: until it
+            // has arrived, its copy would write over the zeros.
+            const int there = it.rows - c * C;
+            if (there < 32 * (warp + 1) && !wait_warp(sh, &sh.v_full[odd], n >> 1 & 1)) return;
+            if (t >= there) {
                 unsigned char* k_tile = sm + (n & 1) * kStage + kTile;
 #pragma unroll 1
                 for (int i = 0; i < 32; ++i)  // K's two halves, V's two halves
