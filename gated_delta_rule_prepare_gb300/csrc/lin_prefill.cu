@@ -332,9 +332,9 @@ struct Item {
 
 struct Shared {
     uint64_t full[3], v_full[2], empty[3];
-    uint64_t qk_ready, pv_ready, s16_ready, qs_ready, o_read;
+    uint64_t qk_ready, pv_ready, s16_ready, qs_ready;
     // by chunk parity, where one side may be a chunk ahead of the other's wait
-    uint64_t p_ready[2], v_checked[2], w_ready[2], kw_ready[2];
+    uint64_t p_ready[2], v_checked[2], w_ready[2], kw_ready[2], o_read[2];
     uint64_t token_sync, state_sync;
     uint64_t item_full[kRing], item_empty[kRing];
     Item item[kRing];
@@ -579,7 +579,7 @@ __device__ __forceinline__ void product_role(Shared& sh, unsigned char* sm) {
             mn_major + (SUM ? stage * (kSumStage >> 4) : stage * (kStage >> 4) + kT);
         const uint64_t v_mn = k_mn + kT, lo_mn = SUM ? state : k_mn - kT;
         if (!SUM) {
-            if (n && !wait_warp(sh, &sh.o_read, odd ^ 1)) return;
+            if (n && !wait_warp(sh, &sh.o_read[odd ^ 1], (n - 1) >> 1 & 1)) return;
             if (!wait_warp(sh, &sh.v_checked[odd], pair)) return;
             if (!wait_warp(sh, &sh.p_ready[odd], pair)) return;
             tc_fence_after();
@@ -799,7 +799,7 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
             }
             // state_role is through with the last chunk's decays (and P V would wait for
             // the same)
-            if (n && !wait_warp(sh, &sh.o_read, odd ^ 1)) return;
+            if (n && !wait_warp(sh, &sh.o_read[odd ^ 1], (n - 1) >> 1 & 1)) return;
             sh.front[t] = ex2_approx(before + sum) * a.scale;
             arrive_warp(&sh.p_ready[odd]);
         }
@@ -902,8 +902,9 @@ __device__ __forceinline__ void check_role(Shared& sh, unsigned char* sm, int ha
                     if (F16 && mine) most = __vmaxu2(most, largest[k]);
                     const bool bad = mine && (carry[k] & 0x80008000u);
                     if (__any_sync(0xffffffffu, bad)) {
-                        // (notes of the last but one chunk are through with by then)
-                        if (n && !wait_warp(sh, &sh.o_read, odd ^ 1)) return;
+                        // The last but one chunk's notes are through with once its O is
+                        // written, which may be after its V has made room for this one.
+                        if (n > 1 && !wait_warp(sh, &sh.o_read[odd], (n - 2) >> 1 & 1)) return;
                         if (bad) set_aside<F16>(sh, half_tile, half, r + 32 * k, odd);
                         found = true;
                     }
@@ -1209,7 +1210,7 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
                     }
                 }
                 if (whole) fence_async_smem();
-                arrive_warp(&sh.o_read);
+                arrive_warp(&sh.o_read[odd]);
                 if (whole && lane == 0) {
                     tma_store_3d(mo, state_half + first * 128, 64 * half, it.h,
                                  it.row + c * C + first);
@@ -1264,12 +1265,12 @@ lin_prefill_kernel(Work w, const __grid_constant__ CUtensorMap mq,
         mbar_init(&sh.pv_ready, 2);
         mbar_init(&sh.s16_ready, 8);
         mbar_init(&sh.qs_ready, 1);
-        mbar_init(&sh.o_read, 8);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.p_ready[i], 4);
             mbar_init(&sh.v_checked[i], 2);
             mbar_init(&sh.w_ready[i], 8);
             mbar_init(&sh.kw_ready[i], 1);
+            mbar_init(&sh.o_read[i], 8);
         }
         mbar_init(&sh.token_sync, 4);
         mbar_init(&sh.state_sync, 8);

@@ -73,3 +73,42 @@ def test_sequences_beside_larger_values(most, other, dtype):
             want = o, S
             assert bool(torch.isfinite(o).all()) and bool(torch.isfinite(S).all())
         assert same_bits(o, want[0]) and same_bits(S, want[1])
+
+
+@pytest.mark.parametrize("lens,heads", [([100] * 60, 12), ([1, 128, 60] * 60, 5), ([520] * 40, 9),
+                                        ([1900], 3)])
+def test_values_that_are_not_finite_in_many_chunks(lens, heads):
+    """Chunks with such values behind each other, every other one, and in sequences that one
+    multiprocessor works on in turn: the columns that they are in are NaN from there on, and
+    everything else has the bits that it has with zeros in their place."""
+    K, dtype = kda(), torch.bfloat16
+    d = inputs(heads, sum(lens), heads, heads, dtype, n_seqs=len(lens))
+    gen = torch.Generator().manual_seed(heads)
+    chunks = [(a, min(128, x - a), s) for s, x in zip(cu_of(lens).tolist(), lens)
+              for a in range(0, x, 128)]
+    v = d["v"].clone()
+    first = torch.full((len(lens), heads, D), 1 << 30)         # the first such row of a column
+    starts = cu_of(lens).tolist()
+    for i, (a, count, s) in enumerate(chunks):
+        for h in range(heads):
+            # heads of which no chunk, each, every other one, or some hold one
+            if not (h % 4 == 1 or h % 4 == 2 and i % 2 or
+                    h % 4 == 3 and torch.rand((), generator=gen) < 0.5):
+                continue
+            r = s + a + int(torch.randint(0, count, (), generator=gen))
+            col = int(torch.randint(0, D, (), generator=gen))
+            v[r, h, col] = (float("nan"), float("inf"), -float("inf"))[(i + h) % 3]
+            n = starts.index(s)
+            first[n, h, col] = min(int(first[n, h, col]), r)
+    cu = cu_of(lens)
+    want, S_want = prefill(K, dict(d, v=torch.where(torch.isfinite(v), v, 0)), cu)
+    K.kda_sync_status()
+    row = torch.arange(sum(lens))
+    n_of = torch.repeat_interleave(torch.arange(len(lens)), torch.tensor(lens))
+    bad = (row[:, None, None] >= first[n_of]).cuda()
+    bad_S = (first < 1 << 30).cuda()[:, :, None, :].expand(-1, -1, D, -1)
+    for _ in range(5):
+        o, S = prefill(K, dict(d, v=v), cu)
+        K.kda_sync_status()
+        assert not bool(torch.isfinite(o[bad]).any()) and same_bits(o[~bad], want[~bad])
+        assert not bool(torch.isfinite(S[bad_S]).any()) and same_bits(S[~bad_S], S_want[~bad_S])
