@@ -23,7 +23,8 @@
 //    tokens and is an FP32 output.  hi is written over V and lo over Q once both are
 //    through, so that two stages of inputs fit.
 //  - FP16 operands are scaled by powers of two that the largest entry of S, or of V,
-//    in the chunk gives: FP16's range is narrower than FP32 states are.
+//    in the chunk gives, weights by one that their row's largest product gives: FP16's range
+//    is narrower than FP32 states and products are.
 //
 // Pieces.  All chains (heads of sequences), one after the other, are cut into equal pieces,
 // one a CTA.  Where no chain is longer than a piece, a CTA works on the beginning of its last
@@ -345,6 +346,7 @@ struct Shared {
     alignas(16) float sum[C];
     alignas(16) float tail[2][C];
     float front[C];        // scale * the decay from the chunk's start to each token
+    uint8_t weight_unit[C];  // FP16: what each token's weights are in units of (exponent)
     float later[2][4];     // decay of the blocks behind each block
     float total[2];        // sum of the chunk
     float block[2][4];     // sums of blocks
@@ -680,6 +682,14 @@ __device__ __forceinline__ void store_8(float* to, const float* s) {
     }
 }
 
+// The power of two that brings a largest value `x` to [2^13, 2^14) when divided by, and
+// its inverse.
+__device__ __forceinline__ float unit_of(float x, float& inverse) {
+    const int e = min(max((int)(__float_as_uint(x) >> 23) - 13, 1), 241);
+    inverse = __uint_as_float((uint32_t)(254 - e) << 23);
+    return __uint_as_float((uint32_t)e << 23);
+}
+
 // Warps 0..3, a thread a token: a chunk's weights P, and the decays that state_role takes
 // (SUM: these alone).
 template <bool F16, bool SUM>
@@ -734,6 +744,25 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
 
             if (!wait_warp(sh, &sh.qk_ready, odd)) return;
             tc_fence_after();
+            // FP16: a row's weights in units that bring its largest product to [2^13, 2^14),
+            // or q . k past 65504 would be lost, and so would bits of any below 2^-14.  (Decays
+            // make less of a product: weights below 2^-27 of the largest one keep 2^-38 of it.)
+            float inverse = 1.f;
+            int unit = 0;
+            if (F16) {
+                float most = 0.f;
+#pragma unroll 1
+                for (int b = 0; b <= warp; ++b) {
+                    float x[32];
+                    tmem_ld32(row + kTmemP + 32 * b, x);
+                    const int last = b == warp ? lane : 31;
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        most = fmaxf(most, e <= last ? fabsf(x[e]) : 0.f);
+                }
+                unit = __float_as_uint(unit_of(most, inverse)) >> 23;
+            }
             // A block of 32 columns a step, upwards: the 16 columns that its weights take
             // hold scores that have been read.  (Rolled: what all roles run has to stay in
             // the instruction cache.)
@@ -752,7 +781,8 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
                             const float y[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const float d = ex2_approx(sum + y[e]);
+                                float d = ex2_approx(sum + y[e]);
+                                if (F16) d *= inverse;
                                 x[4 * k + e] = 4 * k + e <= lane ? x[4 * k + e] * d : 0.f;
                             }
                         }
@@ -763,6 +793,7 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
 #pragma unroll 1
                         for (int k = warp - 1; k > b; --k) from += sh.block[odd][k];
                         from = ex2_approx(from);
+                        if (F16) from *= inverse;
                         const float2 f2 = make_float2(from, from);
                         tmem_ld_wait();
 #pragma unroll
@@ -801,6 +832,7 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
             // the same)
             if (n && !wait_warp(sh, &sh.o_read[odd ^ 1], (n - 1) >> 1 & 1)) return;
             sh.front[t] = ex2_approx(before + sum) * a.scale;
+            if (F16) sh.weight_unit[t] = (uint8_t)unit;
             arrive_warp(&sh.p_ready[odd]);
         }
         items.done(sh);
@@ -919,14 +951,6 @@ __device__ __forceinline__ void check_role(Shared& sh, unsigned char* sm, int ha
         }
         items.done(sh);
     }
-}
-
-// The power of two that brings a largest value `x` to [2^13, 2^14) when divided by, and
-// its inverse.
-__device__ __forceinline__ float unit_of(float x, float& inverse) {
-    const int e = min(max((int)(__float_as_uint(x) >> 23) - 13, 1), 241);
-    inverse = __uint_as_float((uint32_t)(254 - e) << 23);
-    return __uint_as_float((uint32_t)e << 23);
 }
 
 // For a whole warp: until another CTA of the grid has handed its state over, or for at
@@ -1161,7 +1185,9 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
                 // the rows of O, while K^T W is under way
                 tc_fence_after();
                 const float front = sh.front[r] * (F16 ? s_unit : 1.f);
-                const float2 d2 = make_float2(front, front), s2 = make_float2(a.scale, a.scale);
+                float scale = a.scale;
+                if (F16) scale *= __uint_as_float((uint32_t)sh.weight_unit[r] << 23);
+                const float2 d2 = make_float2(front, front), s2 = make_float2(scale, scale);
                 // A warp's 32 rows go by way of shared memory, in the place of the state's
                 // copy, which Q S is through with (written by the lanes, 32 bytes of a row
                 // each, the stores held up everything else on its way to memory: 459 us

@@ -446,8 +446,8 @@ kda_status kda_prefill_static_ws(float* state, const void* q, const void* k, con
  * kda_lin_prefill -- prompts.  States are FP32, added to once in 128 tokens; products
  * are of 16-bit numbers, summed in FP32.  v times its decay is taken as two of them (state_out
  * is good to about 2^-17 of its largest values); weights, and the state that q is multiplied
- * with, as one, which moves o by less than its own rounding.  FP16: |sum_i q_t[i] k_s[i]|,
- * s <= t, stays below 65504.
+ * with, as one, which moves o by less than its own rounding.  FP16: a weight below 2^-27 of
+ * the largest |sum_i q_t[i] k_s[i]| of its row and chunk keeps 2^-38 of that.
  *   cu_seqlens == NULL: n_seqs sequences of t tokens, rows [n_seqs][t_pad]; rows
  *           [t, t_pad) are neither read into arithmetic nor written.
  *   cu_seqlens != NULL: DEVICE int32 [n_seqs + 1] offsets of packed rows, t the
