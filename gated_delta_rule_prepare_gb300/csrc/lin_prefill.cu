@@ -746,20 +746,20 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
             tc_fence_after();
             // FP16: a row's weights in units that bring its largest product to [2^13, 2^14),
             // or q . k past 65504 would be lost, and so would bits of any below 2^-14.  (Decays
-            // make less of a product: weights below 2^-27 of the largest one keep 2^-38 of it.)
+            // make less of a product: weights below 2^-27 of the largest one keep 2^-38 of it.  Eight
+            // columns a step, as code here is dear: in steps of 32 16 prompts took 700 us, 663.)
             float inverse = 1.f;
             int unit = 0;
             if (F16) {
                 float most = 0.f;
 #pragma unroll 1
-                for (int b = 0; b <= warp; ++b) {
-                    float x[32];
-                    tmem_ld32(row + kTmemP + 32 * b, x);
-                    const int last = b == warp ? lane : 31;
+                for (int i = 0; i < 4 * (warp + 1); ++i) {
+                    float x[8];
+                    tmem_ld8(row + kTmemP + 8 * i, x);
                     tmem_ld_wait();
+                    const int last = t - 8 * i;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        most = fmaxf(most, e <= last ? fabsf(x[e]) : 0.f);
+                    for (int e = 0; e < 8; ++e) most = fmaxf(most, e <= last ? fabsf(x[e]) : 0.f);
                 }
                 unit = __float_as_uint(unit_of(most, inverse)) >> 23;
             }
