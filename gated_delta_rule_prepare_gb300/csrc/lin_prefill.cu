@@ -15,8 +15,9 @@
 //    is written over it), Q S, P V, K^T W.
 //  - Decays never enter as exp(G_t) exp(-G_s), whose factors leave FP32's range.  Below
 //    the diagonal blocks of 32 tokens the factors are decays up to the end of s's block
-//    and from there to t, on them exp(G_t - G_s) itself.  Sums of g run within blocks, so
-//    that decays near 1 do not come from differences of large sums.
+//    and from there to t, on them exp(G_t - G_s) itself.  Sums of g run within blocks, and
+//    those of blocks with very strong decays in two parts (deep_decays), so that decays near 1
+//    do not come from differences of large sums.
 //  - P and the copy of S that Q is multiplied with are rounded to 16 bits, which
 //    moves O by less than its own rounding does.  W is kept as two 16-bit
 //    numbers, hi + lo, and the product done twice: the state accumulates over thousands of
@@ -690,6 +691,39 @@ __device__ __forceinline__ float unit_of(float x, float& inverse) {
     return __uint_as_float((uint32_t)e << 23);
 }
 
+// A block of 32 tokens whose decays (log2 of them: g) sum up to so little: differences of its sums
+// would lose bits that weights have, 2^-12 of a decay from 4000 on.  Up to here they are good to
+// 2^-14.
+constexpr float kDeepSum = -256.f;
+// Such a block's products on the diagonal, in their place, times the decays: sums of the whole
+// parts of g are exact, those of the rest good to 2^-19.  A row a lane; not a path for ordinary
+// inputs.
+__device__ __noinline__ void deep_decays(uint32_t products, float g) {
+    const int lane = threadIdx.x & 31;
+    float whole = rintf(g), part = g - whole;
+#pragma unroll 1
+    for (int off = 1; off < 32; off <<= 1) {
+        const float w = __shfl_up_sync(0xffffffffu, whole, off);
+        const float p = __shfl_up_sync(0xffffffffu, part, off);
+        if (lane >= off) whole += w, part += p;
+    }
+#pragma unroll 1
+    for (int i = 0; i < 32; i += 8) {
+        float x[8];
+        uint32_t u[8];
+        tmem_ld8(products + i, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float d = (whole - __shfl_sync(0xffffffffu, whole, i + e)) +
+                            (part - __shfl_sync(0xffffffffu, part, i + e));
+            u[e] = __float_as_uint(i + e <= lane ? x[e] * ex2_approx(d) : 0.f);
+        }
+        tmem_st8u(products + i, u);
+    }
+    tmem_st_wait();
+}
+
 // Warps 0..3, a thread a token: a chunk's weights P, and the decays that state_role takes
 // (SUM: these alone).
 template <bool F16, bool SUM>
@@ -747,7 +781,7 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
             // FP16: a row's weights in units that bring its largest product to [2^13, 2^14),
             // or q . k past 65504 would be lost, and so would bits of any below 2^-14.  (Decays
             // make less of a product: weights below 2^-27 of the largest one keep 2^-38 of it.  Eight
-            // columns a step, as code here is dear: in steps of 32 16 prompts took 700 us, 663.)
+            // columns a step, as code here is dear: in steps of 32 16 prompts took 742 us, 692.)
             float inverse = 1.f;
             int unit = 0;
             if (F16) {
@@ -762,6 +796,12 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
                     for (int e = 0; e < 8; ++e) most = fmaxf(most, e <= last ? fabsf(x[e]) : 0.f);
                 }
                 unit = __float_as_uint(unit_of(most, inverse)) >> 23;
+            }
+            float own = sum;  // of the block on the diagonal
+            if (__any_sync(0xffffffffu, sum < kDeepSum)) {
+                deep_decays(row + kTmemP + 32 * warp, g);
+                sh.sum[t] = own = 0.f;
+                __syncwarp();
             }
             // A block of 32 columns a step, upwards: the 16 columns that its weights take
             // hold scores that have been read.  (Rolled: what all roles run has to stay in
@@ -781,7 +821,7 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
                             const float y[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                float d = ex2_approx(sum + y[e]);
+                                float d = ex2_approx(own + y[e]);
                                 if (F16) d *= inverse;
                                 x[4 * k + e] = 4 * k + e <= lane ? x[4 * k + e] * d : 0.f;
                             }
