@@ -164,8 +164,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs a, int tile) {
                         widen2<F16>(head[tid >> 5][k][is_first ? c + a.pairs : p]).x;
                     y[e] = turn(y[e], other, make_float2(t.x, is_first ? t.y : -t.y)).x;
                 }
-                reinterpret_cast<uint2*>(dst[k])[u] =
-                    make_uint2(narrow2<F16>(y[0], y[1]), narrow2<F16>(y[2], y[3]));
+                // (channels behind the pairs as they came: rounding changes NaN)
+                uint2 out = x[k];
+                if (4 * u < 2 * a.pairs) out.x = narrow2<F16>(y[0], y[1]);
+                if (4 * u + 2 < 2 * a.pairs) out.y = narrow2<F16>(y[2], y[3]);
+                reinterpret_cast<uint2*>(dst[k])[u] = out;
             }
         } else {
             uint4 x[kBatch], y[kBatch];
