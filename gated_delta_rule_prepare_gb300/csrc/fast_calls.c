@@ -139,7 +139,16 @@ static PyObject* no(void) { /* nothing called */
     PyErr_Clear();
     return PyLong_FromLong(-1);
 }
-static PyObject* yes(kda_status status) { return PyLong_FromLong(status); }
+/* A function ends with a call of the library, made without the interpreter's lock: a launch may
+ * wait for room in its stream, which may wait for a host function in Python. */
+#define RETURN_CALL(call)                                \
+    do {                                                 \
+        kda_status status;                               \
+        Py_BEGIN_ALLOW_THREADS                           \
+        status = (call);                                 \
+        Py_END_ALLOW_THREADS                             \
+        return PyLong_FromLong(status);                  \
+    } while (0)
 
 static int in_type(const Tensor* t) {
     return t->dtype == bf16 ? KDA_BF16 : t->dtype == f16 ? KDA_F16 : -1;
@@ -222,9 +231,9 @@ static PyObject* lin_prefill(PyObject* self, PyObject* const* a, Py_ssize_t coun
     if (!bytes || !state_of(a[5], dev, n, r.heads, &in) || !state_of(a[6], dev, n, r.heads, &out) ||
         !number(a[9], &scale) || !stream_of(dev, &stream))
         return no();
-    return yes(lin_prefill_(in, out, r.q.at, r.k.at, r.v.at, r.g.at, r.o.at, (int)t, (int)t_pad,
-                            cu.at, (int)n, (int)r.heads, (int)r.qk_heads, D, r.type, r.qs, r.ks,
-                            r.vs, r.gs, r.os, (float)scale, ws.at, bytes, stream));
+    RETURN_CALL(lin_prefill_(in, out, r.q.at, r.k.at, r.v.at, r.g.at, r.o.at, (int)t, (int)t_pad,
+                             cu.at, (int)n, (int)r.heads, (int)r.qk_heads, D, r.type, r.qs, r.ks,
+                             r.vs, r.gs, r.os, (float)scale, ws.at, bytes, stream));
 }
 
 /* q, k, v, g, out, state_in, state_out, snapshots, scale */
@@ -247,10 +256,10 @@ static PyObject* lin_decode(PyObject* self, PyObject* const* a, Py_ssize_t count
     if (!state_of(a[5], dev, n, r.heads, &in) || !state_of(a[6], dev, n, r.heads, &out) ||
         !number(a[8], &scale) || !stream_of(dev, &stream))
         return no();
-    return yes(lin_decode_(in, out, r.q.at, r.k.at, r.v.at, r.g.at, r.o.at, (int)n, (int)krows,
-                           (int)r.heads, (int)r.qk_heads, D, r.type, r.qs, r.ks, r.vs, r.gs, r.os,
-                           (float)scale, n_snap ? (float* const*)snaps : NULL, (int)n_snap,
-                           stream));
+    RETURN_CALL(lin_decode_(in, out, r.q.at, r.k.at, r.v.at, r.g.at, r.o.at, (int)n, (int)krows,
+                            (int)r.heads, (int)r.qk_heads, D, r.type, r.qs, r.ks, r.vs, r.gs, r.os,
+                            (float)scale, n_snap ? (float* const*)snaps : NULL, (int)n_snap,
+                            stream));
 }
 
 /* q, k, positions, inv_freq, q_out, k_out, pair_axis, interleaved, factor */
@@ -304,9 +313,9 @@ static PyObject* rope(PyObject* self, PyObject* const* a, Py_ssize_t count) {
         (has_k && k.shape[n - 2] > 1 << 16) || !stream_of(dev, &stream))
         return no();
     const int64_t rows = n == 3 ? q.shape[0] : q.shape[0] * q.shape[1];
-    return yes(rope_(q.at, has_k ? k.at : NULL, qo.at, has_k ? ko.at : NULL, rows,
-                     (int)q.shape[n - 2], has_k ? (int)k.shape[n - 2] : 0, D, type, qs, ks, qos, kos,
-                     pos.at, (int)axes, freq.at, (int)pairs, table, turn, (float)factor, stream));
+    RETURN_CALL(rope_(q.at, has_k ? k.at : NULL, qo.at, has_k ? ko.at : NULL, rows,
+                      (int)q.shape[n - 2], has_k ? (int)k.shape[n - 2] : 0, D, type, qs, ks, qos, kos,
+                      pos.at, (int)axes, freq.at, (int)pairs, table, turn, (float)factor, stream));
 }
 
 /* A page table, the pages' counts and a workspace. */
@@ -336,8 +345,8 @@ static PyObject* resize(PyObject* self, PyObject* const* a, Py_ssize_t count) {
         !array(a[1], &lens, p.table.device, i32, 1, p.rows, 0) || !whole(a[3], 1, 1 << 20, &page) ||
         !stream_of(p.table.device, &stream))
         return no();
-    return yes(resize_(p.table.at, lens.at, p.refs.at, (int)p.rows, (int)p.width, p.pages,
-                       (int)page, p.ws.at, p.bytes, stream));
+    RETURN_CALL(resize_(p.table.at, lens.at, p.refs.at, (int)p.rows, (int)p.width, p.pages,
+                        (int)page, p.ws.at, p.bytes, stream));
 }
 
 /* page_table, lens, refs, parent, page_table_out, lens_out, refs_out, src, dst, count, page,
@@ -360,9 +369,9 @@ static PyObject* fork_pages(PyObject* self, PyObject* const* a, Py_ssize_t count
         (a[6] != Py_None && !array(a[6], &refs_out, dev, i32, 1, p.pages, 0)) ||
         !stream_of(dev, &stream))
         return no();
-    return yes(fork_(p.table.at, lens.at, p.refs.at, parent.at, table_out.at, lens_out.at,
-                     refs_out.at, src.at, dst.at, n.at, (int)p.rows, (int)p.width, p.pages,
-                     (int)page, p.ws.at, p.bytes, stream));
+    RETURN_CALL(fork_(p.table.at, lens.at, p.refs.at, parent.at, table_out.at, lens_out.at,
+                      refs_out.at, src.at, dst.at, n.at, (int)p.rows, (int)p.width, p.pages,
+                      (int)page, p.ws.at, p.bytes, stream));
 }
 
 /* page_table, refs, page_table_out, refs_out, src, dst, count, workspace */
@@ -380,8 +389,8 @@ static PyObject* compact(PyObject* self, PyObject* const* a, Py_ssize_t count) {
         (a[3] != Py_None && !array(a[3], &refs_out, dev, i32, 1, p.pages, 0)) ||
         !stream_of(dev, &stream))
         return no();
-    return yes(compact_(p.table.at, p.refs.at, table_out.at, refs_out.at, src.at, dst.at, n.at,
-                        (int)p.rows, (int)p.width, p.pages, p.ws.at, p.bytes, stream));
+    RETURN_CALL(compact_(p.table.at, p.refs.at, table_out.at, refs_out.at, src.at, dst.at, n.at,
+                         (int)p.rows, (int)p.width, p.pages, p.ws.at, p.bytes, stream));
 }
 
 /* caches (a list), src, dst, count */
@@ -406,9 +415,9 @@ static PyObject* copy(PyObject* self, PyObject* const* a, Py_ssize_t count) {
         !array(a[2], &dst, dev, i32, 1, src.shape[0], 0) || !array(a[3], &n, dev, i32, 1, 1, 0) ||
         !stream_of(dev, &stream))
         return no();
-    return yes(copy_(at, (int)caches, first.shape[0],
-                     (int)(first.shape[2] / KDA_KV4_TOKEN_BYTES), (int)first.shape[1], src.at,
-                     dst.at, n.at, (int)src.shape[0], stream));
+    RETURN_CALL(copy_(at, (int)caches, first.shape[0],
+                      (int)(first.shape[2] / KDA_KV4_TOKEN_BYTES), (int)first.shape[1], src.at,
+                      dst.at, n.at, (int)src.shape[0], stream));
 }
 
 /* setup(addresses of the seven functions, the types, raw_stream, current_device) */
