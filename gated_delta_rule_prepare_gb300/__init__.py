@@ -679,9 +679,19 @@ _device = torch._C._cuda_getDevice
 _I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
 
 
+class _Slow:
+    """In the extension's place."""
+
+    def __getattr__(self, name):
+        return lambda *args: -1
+
+
 def _load_fast():
     """The calls below in C, for arguments that are as they should be; for others each
-    returns -1 and calls nothing, and the Python code says what is wrong."""
+    returns -1 and calls nothing, and the Python code says what is wrong.  Where the
+    extension is not built, Python does all of it."""
+    if not os.path.exists(_build.FAST):
+        return _Slow()
     spec = importlib.util.spec_from_file_location("fast_calls", _build.FAST)
     fast = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(fast)

@@ -3,7 +3,8 @@
 Each translation unit compiles in parallel; the shared library links against
 the shared CUDA runtime so it shares one runtime with the host process.  The
 binding's short calls (csrc/fast_calls.c) become a Python extension beside it (the host's C
-compiler, no library).
+compiler, no library; named after the interpreter it is for).  Where that cannot be
+built, for lack of Python's headers for one, the calls take their forms in Python.
 """
 
 from __future__ import annotations
@@ -14,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,7 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libkda.so")
-FAST = os.path.join(OUT_DIR, "fast_calls.so")
+FAST = os.path.join(OUT_DIR, "fast_calls" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -34,24 +36,56 @@ def _cuda_lib_dir() -> str:
     return os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "lib64")
 
 
-def _inputs():
-    return (sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-            + sorted(glob.glob(os.path.join(CSRC, "*.c")))
-            + sorted(glob.glob(os.path.join(CSRC, "*.h")))
-            + sorted(glob.glob(os.path.join(INCLUDE, "*.h"))))
+def _newer(path, *patterns) -> bool:
+    """Whether `path` is there and no older than the files that match."""
+    if not os.path.exists(path):
+        return False
+    t = os.path.getmtime(path)
+    return all(os.path.getmtime(p) <= t for x in patterns for p in glob.glob(x))
+
+
+def _headers() -> str:
+    return os.path.join(INCLUDE, "*.h")
+
+
+def _library_up_to_date() -> bool:
+    return _newer(LIB, os.path.join(CSRC, "*.cu"), os.path.join(CSRC, "*.h"), _headers())
+
+
+def _fast_up_to_date() -> bool:
+    return _newer(FAST, os.path.join(CSRC, "fast_calls.c"), _headers())
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(FAST):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(FAST))
-    return all(os.path.getmtime(p) <= t for p in _inputs())
+    return _library_up_to_date() and _fast_up_to_date()
+
+
+def build_fast() -> bool:
+    """Builds the Python extension; False, with a warning, where that fails."""
+    tmp = FAST + ".tmp%d" % os.getpid()
+    try:
+        r = subprocess.run([shutil.which("cc") or "gcc", "-O2", "-fPIC", "-shared",
+                            "-I" + INCLUDE, "-I" + sysconfig.get_paths()["include"],
+                            os.path.join(CSRC, "fast_calls.c"), "-o", tmp],
+                           capture_output=True, text=True)
+        problem = r.stdout + r.stderr if r.returncode else None
+    except OSError as e:
+        problem = str(e)
+    if problem is None:
+        os.replace(tmp, FAST)
+        return True
+    if os.path.exists(FAST):            # (an older one may not fit the library)
+        os.remove(FAST)
+    warnings.warn("fast_calls.c cannot be built; its calls take longer in Python:\n" + problem)
+    return False
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
-    if not force and up_to_date():
-        return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
+    if force or not _fast_up_to_date():
+        build_fast()
+    if not force and _library_up_to_date():
+        return LIB
     nvcc = _nvcc()
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                     "-I" + INCLUDE, "-I" + CSRC, "--expt-relaxed-constexpr"]
@@ -68,14 +102,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
             raise RuntimeError("nvcc failed on %s:\n%s%s" % (src, r.stdout, r.stderr))
         return obj, r.stderr
 
-    fast = FAST + ".tmp%d" % os.getpid()
-    r = subprocess.run([shutil.which("cc") or "gcc", "-O2", "-fPIC", "-shared", "-I" + INCLUDE,
-                        "-I" + sysconfig.get_paths()["include"],
-                        os.path.join(CSRC, "fast_calls.c"), "-o", fast],
-                       capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("cc failed on fast_calls.c:\n%s%s" % (r.stdout, r.stderr))
-
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
         results = list(ex.map(compile_one, srcs))
     if verbose:
@@ -88,7 +114,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
-    os.replace(fast, FAST)
     return LIB
 
 

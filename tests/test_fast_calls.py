@@ -94,3 +94,62 @@ for name, args in calls.items():
 """)
     assert out.split() == [x for name in ("lin_prefill", "lin_decode", "rope", "resize", "fork",
                                           "compact") for x in (name, "True")]
+
+
+def test_the_package_without_the_extension(tmp_path):
+    """A copy of the package that lacks it: imported, and the calls take their forms in Python."""
+    out = run("""
+import shutil
+here, there = os.path.dirname(build.__file__), os.path.join(%r, "gated_delta_rule_prepare_gb300")
+shutil.copytree(here, there, ignore=shutil.ignore_patterns("fast_calls*", "*.o", "__pycache__"))
+sys.path.insert(0, %r)
+import torch
+import gated_delta_rule_prepare_gb300 as K
+assert K.__file__.startswith(there) and not os.path.exists(K._build.FAST)
+x = torch.zeros((3, 2, 128), dtype=torch.bfloat16)
+assert K._fast.rope(x, None, None, None, None, None, None, False, 1.0) == -1
+i = torch.zeros(3, dtype=torch.int32)
+for call in (lambda: K.kda_attn_rope(x, None, i, torch.zeros(64)),
+             lambda: K.kda_lin_prefill(x, x, x, torch.zeros(2), x),
+             lambda: K.kda_lin_decode(x, x, x, torch.zeros(2), x),
+             lambda: K.kda_attn_kv4_resize(i[None], i, i),
+             lambda: K.kda_attn_kv4_fork(i[None], i, i, i),
+             lambda: K.kda_attn_kv4_compact(i[None], i),
+             lambda: K.kda_attn_kv4_copy([x], i, i, i)):
+    try:
+        call()
+    except TypeError as e:
+        assert "CUDA" in str(e), e
+    else:
+        assert False
+print("fine")
+""" % (str(tmp_path), str(tmp_path)))
+    assert out.strip() == "fine"
+
+
+def test_a_build_without_pythons_headers(tmp_path):
+    """The extension is left out, with a warning, and the library is built all the same."""
+    out = run("""
+import shutil, warnings
+there = os.path.join(%r, "package")
+shutil.copytree(os.path.dirname(build.__file__), there,
+                ignore=shutil.ignore_patterns("__pycache__", "*.o"))
+shutil.copytree(build.INCLUDE, os.path.join(%r, "include"))
+spec = importlib.util.spec_from_file_location("there", os.path.join(there, "build.py"))
+copy = importlib.util.module_from_spec(spec)
+spec.loader.exec_module(copy)
+assert copy.FAST.startswith(there) and os.path.exists(copy.FAST)
+os.utime(copy.LIB)
+paths = copy.sysconfig.get_paths
+copy.sysconfig.get_paths = lambda: dict(paths(), include=there)
+os.utime(os.path.join(copy.CSRC, "fast_calls.c"))
+with warnings.catch_warnings(record=True) as seen:
+    warnings.simplefilter("always")
+    assert copy.build() == copy.LIB
+assert len(seen) == 1 and "Python.h" in str(seen[0].message)
+assert not os.path.exists(copy.FAST) and not copy.up_to_date()
+copy.sysconfig.get_paths = paths
+assert copy.build() == copy.LIB and copy.up_to_date()
+print("fine", sys.implementation.cache_tag in copy.FAST)
+""" % (str(tmp_path), str(tmp_path)))
+    assert out.split() == ["fine", "True"]
