@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
+import operator
 import os
 
 import torch
@@ -771,7 +772,7 @@ def kda_attn_rope(q, k, positions, inv_freq, q_out=None, k_out=None, pair_axis=N
     pairs = inv_freq.shape[0] if inv_freq.dim() == 1 else 0
     table = None
     if pair_axis is not None:
-        table = bytes(pair_axis)
+        table = bytes([operator.index(a) for a in pair_axis])
         if len(table) != pairs or max(table, default=0) >= axes:
             raise ValueError("kda_attn_rope: pair_axis must hold an axis below %d for each pair"
                              % axes)
@@ -780,7 +781,8 @@ def kda_attn_rope(q, k, positions, inv_freq, q_out=None, k_out=None, pair_axis=N
     _call(dev, LIB.kda_attn_rope, q_ptr, k_ptr, qo_ptr, ko_ptr, rows, shape[-2], kv_heads,
           HEAD_DIM, in_dtype, q_row, k_row, qo_row, ko_row,
           _array(positions, _I32, dev, pos_shape, "positions"), axes,
-          _array(inv_freq, _F32, dev, (pairs,), "inv_freq"), pairs, table, interleaved, factor)
+          _array(inv_freq, _F32, dev, (pairs,), "inv_freq"), pairs, table, bool(interleaved),
+          factor)
 
 
 def kda_attn_kv4_pages_workspace(n_pages, n_seqs, max_pages, device="cuda"):
