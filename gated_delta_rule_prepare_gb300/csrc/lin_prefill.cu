@@ -5,8 +5,8 @@
 //     O = scale * (P V + diag(exp(G_t)) Q S)
 //     S <- exp(G_C) S + K^T W,      W[s] = exp(G_C - G_s) V[s]
 //
-// Bound by memory: 1 KB a token and head for five 128^3 products a chunk and head,
-// 83 kFLOP a token against 1 KB.  So all of a chunk's work has to fit under its copy,
+// Bound by memory: 1 KB a token and head, 0.15 ns, for five 128^3 products a chunk and head,
+// 164 kFLOP a token and head, 0.09 ns.  So all of a chunk's work has to fit under its copy,
 // 2.9 us at a multiprocessor's share of the bandwidth:
 //  - One persistent CTA a multiprocessor, chunks one after the other; chunk c + 1's
 //    Q, K and V are copied by TMA while chunk c is worked on.
@@ -18,8 +18,9 @@
 //    and from there to t, on them exp(G_t - G_s) itself.  Sums of g run within blocks, and
 //    those of blocks with very strong decays in two parts (deep_decays), so that decays near 1
 //    do not come from differences of large sums.
-//  - P and the copy of S that Q is multiplied with are rounded to 16 bits, which
-//    moves O by less than its own rounding does.  W is kept as two 16-bit
+//  - P and the copy of S that Q is multiplied with are rounded to 16 bits, as tensor cores
+//    take them: O is off by half a 16-bit step of the sums of |P V| and |Q S|, about as much
+//    again as by its own rounding (more where terms cancel).  W is kept as two 16-bit
 //    numbers, hi + lo, and the product done twice: the state accumulates over thousands of
 //    tokens and is an FP32 output.  hi is written over V and lo over Q once both are
 //    through, so that two stages of inputs fit.
@@ -29,14 +30,15 @@
 //
 // Pieces.  All chains (heads of sequences), one after the other, are cut into equal pieces,
 // one a CTA.  Where no chain is longer than a piece, a CTA works on the beginning of its last
-// chain first of all and hands the state on, and on the end of its first one last.
+// chain first of all and hands the state on, and on the end of its first one last.  (For chains
+// up to half as long again pieces are made as long as they are, and some CTAs have none.)
 // Longer chains, which lie in several pieces, need the state in front of them early:
 // lin_prefill_kernel<.., SUM> first adds up what each cut segment contributes (K and V
 // alone).  See Plan.
 //
 // A chunk takes 3.3 to 3.4 us, a CTA's first 7 us more and a change of chains 5: 16 prompts of
-// 512 to 8192 tokens, 32 heads (2.4 GB): 437 us, 5.5 TB/s.  One prompt of 8192 tokens, 32
-// heads (0.27 GB): 100 us, of these 38 for the sums.
+// 512 to 8192 tokens, 32 heads (2.4 GB): 450 us, 5.3 TB/s.  One prompt of 8192 tokens, 32
+// heads (0.27 GB): 101 us, of these 38 for the sums; FP16: 127.
 #include <algorithm>
 #include <cmath>
 #include <cstddef>

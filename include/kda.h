@@ -433,7 +433,8 @@ kda_status kda_prefill_static_ws(float* state, const void* q, const void* k, con
  *   v, o : in_dtype, heads heads, likewise (o overlaps none of the inputs)
  *   g    : FP32, token row r of head h at g + r*g_row_stride + h; a stride of 0 is
  *           one decay for each head, whatever the token.  g <= 0, -inf among it:
- *           what the state held is gone (decays below e^-100 count as 0).
+ *           what the state held is gone, if it was finite (decays below e^-87 may count
+ *           as 0).
  *   state_in : FP32 [n_seqs][heads][128][128], or NULL: states of zero
  *   state_out : the state after the last token, or NULL: not wanted; may be state_in
  *   heads : a multiple of qk_heads
@@ -445,11 +446,15 @@ kda_status kda_prefill_static_ws(float* state, const void* q, const void* k, con
  *
  * kda_lin_prefill -- prompts.  States are FP32, added to once in 128 tokens; products
  * are of 16-bit numbers, summed in FP32.  v times its decay is taken as two of them (state_out
- * is good to about 2^-17 of its largest values); weights, and the state that q is multiplied
- * with, as one, which moves o by less than its own rounding.  FP16: a weight below 2^-27 of
- * the largest |sum_i q_t[i] k_s[i]| of its row and chunk keeps 2^-38 of that.
+ * is good to about 2^-17 of its largest values); weights (q_t . k_s times the decay between
+ * them), and the state S that q is multiplied with, as one: beside its own rounding o is off by
+ * up to half a 16-bit step of scale * (sum_s |weight_s v_s[j]| + sum_i |q_t[i] S[i][j]|), which
+ * is more than a step of o where terms cancel.  FP16: a weight below 2^-27 of the largest
+ * |q_t . k_s| of its row and chunk keeps 2^-38 of that, and so does S of its largest entry.
  *   cu_seqlens == NULL: n_seqs sequences of t tokens, rows [n_seqs][t_pad]; rows
- *           [t, t_pad) are neither read into arithmetic nor written.
+ *           [t, t_pad) are neither read into arithmetic nor written.  Up to KDA_MAX_K
+ *           tokens are walked through one by one, as kda_lin_decode does, in FP32: bits
+ *           are not those of packed rows.
  *   cu_seqlens != NULL: DEVICE int32 [n_seqs + 1] offsets of packed rows, t the
  *           total and t_pad equal to it.  Checked on the device: a sequence whose
  *           offsets lie outside 0..t or fall is left out, and kda_sync_status
@@ -663,7 +668,9 @@ kda_status kda_attn_rope(const void* q, const void* k, void* q_out, void* k_out,
  * kda_attn_kv4_resize -- gives and frees pages, in place: afterwards sequence n
  * has the pages of lens[n] positions (entries below ceil(lens[n] / page)) and no
  * others.  Entries that are there stay.  lens[n] = 0 ends a sequence; a smaller
- * lens[n] takes rejected rows back.
+ * lens[n] takes rejected rows back.  Pages stay shared: where that ends a sequence inside a
+ * page that others name too (rows taken back from before a fork), what it appends next is
+ * written over theirs.
  */
 kda_status kda_attn_kv4_resize(int* page_table, const int* lens, int* refs, int n_seqs,
                                int max_pages, int64_t n_pages, int page, void* workspace,
@@ -677,6 +684,9 @@ kda_status kda_attn_kv4_resize(int* page_table, const int* lens, int* refs, int 
  * list for kda_attn_kv4_copy.  Pages no longer named become free (they may be
  * among the new ones); rows hold the pages of lens_out, no others.  A child that
  * gets no page keeps its parent's full pages, and lens_out[n] counts those alone.
+ * The partly filled page is expected to be its parent's alone.  Where a parent lacks it (an
+ * entry of -1), its other children get a page all the same, listed with a source that the
+ * copy leaves out and reports.
  *   src, dst : DEVICE int32 [n_seqs], the list, -1 behind its end; count : DEVICE
  *           int32 [1], its length
  */
