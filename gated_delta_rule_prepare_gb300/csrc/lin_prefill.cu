@@ -37,8 +37,8 @@
 // alone).  See Plan.
 //
 // A chunk takes 3.3 to 3.4 us, a CTA's first 7 us more and a change of chains 5: 16 prompts of
-// 512 to 8192 tokens, 32 heads (2.4 GB): 450 us, 5.3 TB/s.  One prompt of 8192 tokens, 32
-// heads (0.27 GB): 101 us, of these 38 for the sums; FP16: 127.
+// 512 to 8192 tokens, 32 heads (2.4 GB): 449 us, 5.3 TB/s.  One prompt of 8192 tokens, 32
+// heads (0.27 GB): 101 us, of these 38 for the sums; FP16: 123.
 #include <algorithm>
 #include <cmath>
 #include <cstddef>
@@ -783,7 +783,7 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
             // FP16: a row's weights in units that bring its largest product to [2^13, 2^14),
             // or q . k past 65504 would be lost, and so would bits of any below 2^-14.  (Decays
             // make less of a product: weights below 2^-27 of the largest one keep 2^-38 of it.  Eight
-            // columns a step, as code here is dear: in steps of 32 16 prompts took 742 us, 692.)
+            // columns a step, as code here is dear: in steps of 16 16 prompts took 662 us, 644.)
             float inverse = 1.f;
             int unit = 0;
             if (F16) {
@@ -820,13 +820,17 @@ __device__ __forceinline__ void token_role(const Work& w, Shared& sh, unsigned c
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             const float4 s = other[k];
-                            const float y[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                float d = ex2_approx(own + y[e]);
-                                if (F16) d *= inverse;
-                                x[4 * k + e] = 4 * k + e <= lane ? x[4 * k + e] * d : 0.f;
+                            float d[4] = {ex2_approx(own + s.x), ex2_approx(own + s.y),
+                                          ex2_approx(own + s.z), ex2_approx(own + s.w)};
+                            if (F16) {
+                                const float2 i2 = make_float2(inverse, inverse);
+                                const float2 lo = mul2(make_float2(d[0], d[1]), i2);
+                                const float2 hi = mul2(make_float2(d[2], d[3]), i2);
+                                d[0] = lo.x, d[1] = lo.y, d[2] = hi.x, d[3] = hi.y;
                             }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                x[4 * k + e] = 4 * k + e <= lane ? x[4 * k + e] * d[e] : 0.f;
                         }
                     } else {
                         const float4* other =
@@ -1240,7 +1244,7 @@ __device__ __forceinline__ void state_role(const Work& w, Shared& sh, unsigned c
                 const int first = 32 * warp;
                 uint16_t* to = a.o + ((long long)it.row + c * C + r) * a.o_stride + it.h * D +
                                64 * half;
-#pragma unroll 2
+#pragma unroll (F16 ? 1 : 2)  // (FP16, 2: 690 us where this took 650, by its longer code)
                 for (int i = 0; i < 4; ++i) {  // 16 columns a step
                     float x[16], y[16];
                     tmem_ld16(row + kTmemQS + 16 * i, x);
